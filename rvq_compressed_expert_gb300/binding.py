@@ -1,4 +1,4 @@
-"""ctypes binding of libwaste_moe (include/waste_moe.h): same names, argument marshalling only.
+"""ctypes binding of libwaste_moe (include/waste_moe.h, include/waste_dense.h): same names, argument marshalling only.
 
 Tensors are passed as torch tensors (their data pointers are handed to the
 library) or as raw integer addresses; streams as ``torch.cuda.Stream``, an
@@ -17,7 +17,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libwaste_moe.so")
 
 ABI_VERSION = 1
-ACT_F32, ACT_BF16 = 0, 1
+ACT_F32, ACT_BF16, ACT_F16 = 0, 1, 2  # ACT_F16: the dense operators only
 FLAG_VERIFY_CRC = 1 << 0
 FLAG_FORCE_GEMV = 1 << 2
 FLAG_FORCE_MMA = 1 << 3
@@ -38,6 +38,11 @@ EXPORTED = ["waste_moe_record_layout", "waste_moe_pack_records", "waste_moe_crea
             "waste_bank_create", "waste_bank_destroy", "waste_bank_reset", "waste_bank_stats",
             "waste_moe_set_lookahead",
             "waste_moe_create_banked", "waste_rvq_train", "waste_rvq_encode", "waste_moe_debug_wait"]
+
+# include/waste_dense.h
+EXPORTED_DENSE = ["waste_ffn_workspace", "waste_ffn_forward", "waste_ffn_backward", "waste_mx4_layout",
+                  "waste_mx4_quantize", "waste_mx4_dequantize", "waste_mx4_matmul", "waste_mx4_ffn_workspace",
+                  "waste_mx4_ffn_forward"]
 
 
 class waste_moe_config(ctypes.Structure):
@@ -67,6 +72,17 @@ class waste_moe_stats_t(ctypes.Structure):
 class waste_bank_stats_t(ctypes.Structure):
     _fields_ = [(n, ctypes.c_uint64) for n in (
         "demand_hits", "demand_misses", "prefetch_copies", "prefetch_present", "copied_bytes")]
+
+
+class waste_ffn_config(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_uint32), ("d", ctypes.c_int32), ("f", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+class waste_mx4_ffn_config(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_uint32), ("d", ctypes.c_int32), ("f", ctypes.c_int32)] + [
+        (n, ctypes.c_void_p) for n in ("d_gate_codes", "d_gate_scales", "d_up_codes", "d_up_scales",
+                                       "d_down_codes", "d_down_scales")]
 
 
 class WasteError(RuntimeError):
@@ -120,7 +136,18 @@ def load(path: str = LIB_PATH):
     lib.waste_rvq_train.argtypes = [vp, i32, i32, vp, i32, vp, vp, vp, vp]
     lib.waste_rvq_encode.argtypes = [vp, i32, i32, vp, vp, vp, vp]
     lib.waste_moe_debug_wait.argtypes = [vp, vp, ctypes.c_uint32, ctypes.c_uint64, vp]
-    for name in EXPORTED:
+    i64 = ctypes.c_int64
+    ffn, mx4 = ctypes.POINTER(waste_ffn_config), ctypes.POINTER(waste_mx4_ffn_config)
+    lib.waste_ffn_workspace.argtypes = [ffn, i32, i32, ctypes.POINTER(sz)]
+    lib.waste_ffn_forward.argtypes = [ffn, vp, i32, vp, vp, vp, vp, i32, i32, vp, vp, vp, sz, vp]
+    lib.waste_ffn_backward.argtypes = [ffn, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, vp, sz, vp]
+    lib.waste_mx4_layout.argtypes = [i32, i32, ctypes.POINTER(sz), ctypes.POINTER(sz)]
+    lib.waste_mx4_quantize.argtypes = [vp, i32, i32, i32, i64, vp, vp, vp]
+    lib.waste_mx4_dequantize.argtypes = [vp, vp, i32, i32, vp, i32, i64, vp]
+    lib.waste_mx4_matmul.argtypes = [i32, i32, i32, vp, vp, vp, vp, vp, i32, i32, vp]
+    lib.waste_mx4_ffn_workspace.argtypes = [mx4, i32, ctypes.POINTER(sz)]
+    lib.waste_mx4_ffn_forward.argtypes = [mx4, vp, i32, i32, vp, i32, i32, vp, sz, vp]
+    for name in EXPORTED + EXPORTED_DENSE:
         if name not in ("waste_moe_destroy", "waste_moe_last_error", "waste_bank_destroy"):
             getattr(lib, name).restype = ctypes.c_int
     _lib = lib
@@ -319,3 +346,58 @@ def waste_rvq_encode(w, codebooks, codes, err, stream=None):
     rows, cols = w.shape
     return _check(load().waste_rvq_encode(_ptr(w), rows, cols, _ptr(codebooks), _ptr(codes), _ptr(err),
                                           _stream(stream)))
+
+
+def waste_ffn_workspace(cfg, T, backward=0) -> int:
+    n = ctypes.c_size_t()
+    _check(load().waste_ffn_workspace(ctypes.byref(cfg), T, backward, ctypes.byref(n)))
+    return n.value
+
+
+def waste_ffn_forward(cfg, d_x, T, d_w_gate, d_w_up, d_w_down, d_out, out_dtype, mode, d_g, d_u, workspace,
+                      stream=None):
+    """workspace: a uint8 tensor (its size is passed on)."""
+    return _check(load().waste_ffn_forward(
+        ctypes.byref(cfg), _ptr(d_x), T, _ptr(d_w_gate), _ptr(d_w_up), _ptr(d_w_down), _ptr(d_out), out_dtype, mode,
+        _ptr(d_g), _ptr(d_u), workspace.data_ptr(), workspace.numel(), _stream(stream)))
+
+
+def waste_ffn_backward(cfg, d_dy, T, d_x, d_g, d_u, d_w_gate, d_w_up, d_w_down, d_dx, d_dw_gate, d_dw_up, d_dw_down,
+                       grad_dtype, accumulate, workspace, stream=None):
+    return _check(load().waste_ffn_backward(
+        ctypes.byref(cfg), _ptr(d_dy), T, _ptr(d_x), _ptr(d_g), _ptr(d_u), _ptr(d_w_gate), _ptr(d_w_up),
+        _ptr(d_w_down), _ptr(d_dx), _ptr(d_dw_gate), _ptr(d_dw_up), _ptr(d_dw_down), grad_dtype, accumulate,
+        workspace.data_ptr(), workspace.numel(), _stream(stream)))
+
+
+def waste_mx4_layout(rows, cols):
+    """(bytes of codes, bytes of scales)."""
+    c, s = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(load().waste_mx4_layout(rows, cols, ctypes.byref(c), ctypes.byref(s)))
+    return c.value, s.value
+
+
+def waste_mx4_quantize(d_x, dtype, rows, cols, ld, d_codes, d_scales, stream=None):
+    return _check(load().waste_mx4_quantize(_ptr(d_x), dtype, rows, cols, ld, _ptr(d_codes), _ptr(d_scales),
+                                            _stream(stream)))
+
+
+def waste_mx4_dequantize(d_codes, d_scales, rows, cols, d_out, dtype, ld, stream=None):
+    return _check(load().waste_mx4_dequantize(_ptr(d_codes), _ptr(d_scales), rows, cols, _ptr(d_out), dtype, ld,
+                                              _stream(stream)))
+
+
+def waste_mx4_matmul(M, N, K, d_a_codes, d_a_scales, d_b_codes, d_b_scales, d_out, out_dtype, mode=0, stream=None):
+    return _check(load().waste_mx4_matmul(M, N, K, _ptr(d_a_codes), _ptr(d_a_scales), _ptr(d_b_codes),
+                                          _ptr(d_b_scales), _ptr(d_out), out_dtype, mode, _stream(stream)))
+
+
+def waste_mx4_ffn_workspace(cfg, T) -> int:
+    n = ctypes.c_size_t()
+    _check(load().waste_mx4_ffn_workspace(ctypes.byref(cfg), T, ctypes.byref(n)))
+    return n.value
+
+
+def waste_mx4_ffn_forward(cfg, d_x, x_dtype, T, d_out, out_dtype, mode, workspace, stream=None):
+    return _check(load().waste_mx4_ffn_forward(ctypes.byref(cfg), _ptr(d_x), x_dtype, T, _ptr(d_out), out_dtype, mode,
+                                               workspace.data_ptr(), workspace.numel(), _stream(stream)))

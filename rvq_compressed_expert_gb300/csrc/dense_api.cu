@@ -1,0 +1,283 @@
+// Host side of waste_dense.h: argument checks, workspace layout and the launches of each call.
+#include <cstdarg>
+#include <cstdio>
+
+#include "dense.cuh"
+
+using namespace wm;
+using namespace wm::dense;
+
+namespace {
+
+int fail(int code, const char *fmt, ...) {
+    char buf[256];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    set_last_error(buf);
+    return code;
+}
+int ok() {
+    set_last_error("");
+    return WASTE_OK;
+}
+int done(cudaError_t e, const char *what) {
+    if (e == cudaSuccess) return ok();
+    return fail(WASTE_ECUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
+bool half_type(int t) { return t == WASTE_ACT_BF16 || t == WASTE_ACT_F16; }
+bool any_type(int t) { return t == WASTE_ACT_F32 || half_type(t); }
+
+// NULL or misaligned pointers of a call; names in the order of the pointers.
+int check_ptrs(const void *const *p, const char *const *name, int n) {
+    for (int i = 0; i < n; ++i) {
+        if (!p[i]) return fail(WASTE_EINVAL, "%s is NULL", name[i]);
+        if (!aligned(p[i], 16)) return fail(WASTE_EINVAL, "%s must be 16-byte aligned", name[i]);
+    }
+    return WASTE_OK;
+}
+
+int check_workspace(const void *ws, size_t have, size_t need) {
+    if (need == 0) return WASTE_OK;
+    if (!ws || !aligned(ws, 256)) return fail(WASTE_EINVAL, "workspace is NULL or not 256-byte aligned");
+    if (have < need) return fail(WASTE_EINVAL, "workspace of %zu bytes, %zu needed", have, need);
+    return WASTE_OK;
+}
+
+int check_ffn(const waste_ffn_config *c, int32_t T) {
+    if (!c) return fail(WASTE_EINVAL, "config is NULL");
+    if (c->abi_version != WASTE_MOE_ABI_VERSION)
+        return fail(WASTE_EINVAL, "abi_version %u, library speaks %u", c->abi_version, WASTE_MOE_ABI_VERSION);
+    if (c->d <= 0 || c->d % 8) return fail(WASTE_EINVAL, "d = %d must be a positive multiple of 8", c->d);
+    if (c->f <= 0 || c->f % 8) return fail(WASTE_EINVAL, "f = %d must be a positive multiple of 8", c->f);
+    if (!half_type(c->dtype)) return fail(WASTE_EINVAL, "dtype = %d: bf16 or fp16", c->dtype);
+    if (T < 0) return fail(WASTE_EINVAL, "T = %d", T);
+    return WASTE_OK;
+}
+
+// One [T][f] buffer of the workspace.
+size_t ffn_part(const waste_ffn_config *c, int32_t T) { return round_up((size_t)T * c->f * 2, 256); }
+
+int check_mx4_shape(int32_t rows, int32_t cols) {
+    if (rows < 0) return fail(WASTE_EINVAL, "rows = %d", rows);
+    if (cols <= 0 || cols % kMxBlock) return fail(WASTE_EINVAL, "cols = %d must be a positive multiple of 32", cols);
+    return WASTE_OK;
+}
+
+int check_mx4_x(const void *x, int dtype, int cols, int64_t ld, const char *name) {
+    if (!any_type(dtype)) return fail(WASTE_EINVAL, "dtype = %d: fp32, bf16 or fp16", dtype);
+    if (ld < cols || ld * (int64_t)type_size(dtype) % 16)
+        return fail(WASTE_EINVAL, "row stride %lld: at least cols = %d and a multiple of 16 bytes", (long long)ld, cols);
+    const void *p[] = {x};
+    const char *n[] = {name};
+    return check_ptrs(p, n, 1);
+}
+
+int check_mx4_ffn(const waste_mx4_ffn_config *c, int32_t T) {
+    if (!c) return fail(WASTE_EINVAL, "config is NULL");
+    if (c->abi_version != WASTE_MOE_ABI_VERSION)
+        return fail(WASTE_EINVAL, "abi_version %u, library speaks %u", c->abi_version, WASTE_MOE_ABI_VERSION);
+    if (c->d <= 0 || c->d % kMxBlock) return fail(WASTE_EINVAL, "d = %d must be a positive multiple of 32", c->d);
+    if (c->f <= 0 || c->f % kMxBlock) return fail(WASTE_EINVAL, "f = %d must be a positive multiple of 32", c->f);
+    if (T < 0) return fail(WASTE_EINVAL, "T = %d", T);
+    return WASTE_OK;
+}
+
+struct Mx4FfnParts {
+    size_t xc, xs, ac, as, scratch, total;
+};
+Mx4FfnParts mx4_ffn_parts(const waste_mx4_ffn_config *c, int32_t T) {
+    Mx4FfnParts p;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = at;
+        at += round_up(bytes, 256);
+        return o;
+    };
+    p.xc = take(mx_code_bytes(T, c->d));
+    p.xs = take(mx_scale_bytes(T, c->d));
+    p.ac = take(mx_code_bytes(T, c->f));
+    p.as = take(mx_scale_bytes(T, c->f));
+    p.scratch = take(mx4_gated_scratch(T, c->f));
+    p.total = at;
+    return p;
+}
+
+} // namespace
+
+extern "C" {
+
+int waste_ffn_workspace(const waste_ffn_config *cfg, int32_t T, int32_t backward, size_t *bytes) {
+    const int rc = check_ffn(cfg, T);
+    if (rc) return rc;
+    if (!bytes) return fail(WASTE_EINVAL, "bytes is NULL");
+    *bytes = ffn_part(cfg, T) * (backward ? 3 : 1);
+    return ok();
+}
+
+int waste_ffn_forward(const waste_ffn_config *cfg, const void *d_x, int32_t T, const void *d_w_gate,
+                      const void *d_w_up, const void *d_w_down, void *d_out, int32_t out_dtype, int32_t mode,
+                      void *d_g, void *d_u, void *d_workspace, size_t workspace_bytes, waste_stream_t stream) {
+    const NvtxRange nvtx_range(__func__);
+    int rc = check_ffn(cfg, T);
+    if (rc) return rc;
+    if (out_dtype != cfg->dtype && out_dtype != WASTE_ACT_F32)
+        return fail(WASTE_EINVAL, "out_dtype = %d: the config's dtype or fp32", out_dtype);
+    if (mode != 0 && mode != 1) return fail(WASTE_EINVAL, "mode = %d", mode);
+    if (!d_g != !d_u) return fail(WASTE_EINVAL, "g and u: both or neither");
+    if (T == 0) return ok();
+    const void *p[] = {d_x, d_w_gate, d_w_up, d_w_down, d_out, d_g, d_u};
+    const char *n[] = {"x", "w_gate", "w_up", "w_down", "out", "g", "u"};
+    rc = check_ptrs(p, n, d_g ? 7 : 5);
+    if (!rc) rc = check_workspace(d_workspace, workspace_bytes, ffn_part(cfg, T));
+    if (rc) return rc;
+    FfnFwd P{cfg->d, cfg->f, T, cfg->dtype, out_dtype, mode, d_x, d_w_gate, d_w_up, d_w_down, d_out, d_g, d_u,
+             d_workspace};
+    return done(launch_ffn_forward(P, reinterpret_cast<cudaStream_t>(stream)), "gated feed-forward");
+}
+
+int waste_ffn_backward(const waste_ffn_config *cfg, const void *d_dy, int32_t T, const void *d_x, const void *d_g,
+                       const void *d_u, const void *d_w_gate, const void *d_w_up, const void *d_w_down, void *d_dx,
+                       void *d_dw_gate, void *d_dw_up, void *d_dw_down, int32_t grad_dtype, int32_t accumulate,
+                       void *d_workspace, size_t workspace_bytes, waste_stream_t stream) {
+    const NvtxRange nvtx_range(__func__);
+    int rc = check_ffn(cfg, T);
+    if (rc) return rc;
+    if (grad_dtype != cfg->dtype && grad_dtype != WASTE_ACT_F32)
+        return fail(WASTE_EINVAL, "grad_dtype = %d: the config's dtype or fp32", grad_dtype);
+    if (accumulate != 0 && accumulate != 1) return fail(WASTE_EINVAL, "accumulate = %d", accumulate);
+    const bool dw = d_dw_gate != nullptr;
+    if ((d_dw_up != nullptr) != dw || (d_dw_down != nullptr) != dw)
+        return fail(WASTE_EINVAL, "dw_gate, dw_up and dw_down: all or none");
+    if (!d_dx && !dw) return ok();
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (dw) {
+        const void *p[] = {d_dw_gate, d_dw_up, d_dw_down};
+        const char *n[] = {"dw_gate", "dw_up", "dw_down"};
+        if ((rc = check_ptrs(p, n, 3))) return rc;
+    }
+    if (T == 0) {
+        cudaError_t e = cudaSuccess;
+        const size_t bytes = (size_t)cfg->d * cfg->f * type_size(grad_dtype);
+        if (dw && !accumulate) {
+            void *w[] = {d_dw_gate, d_dw_up, d_dw_down};
+            for (int i = 0; i < 3 && e == cudaSuccess; ++i) e = cudaMemsetAsync(w[i], 0, bytes, s);
+        }
+        return done(e, "clearing the gradients");
+    }
+    const void *p[] = {d_dy, d_x, d_g, d_u, d_w_gate, d_w_up, d_w_down, d_dx};
+    const char *n[] = {"dy", "x", "g", "u", "w_gate", "w_up", "w_down", "dx"};
+    rc = check_ptrs(p, n, d_dx ? 8 : 7);
+    const size_t part = ffn_part(cfg, T);
+    if (!rc) rc = check_workspace(d_workspace, workspace_bytes, 3 * part);
+    if (rc) return rc;
+    char *w = static_cast<char *>(d_workspace);
+    FfnBwd P{cfg->d, cfg->f,  T,      cfg->dtype, grad_dtype, accumulate, d_dy, d_x,      d_g,         d_u, d_w_gate,
+             d_w_up, d_w_down, d_dx, d_dw_gate,  d_dw_up,    d_dw_down,  w,    w + part, w + 2 * part};
+    return done(launch_ffn_backward(P, s), "gated feed-forward gradients");
+}
+
+int waste_mx4_layout(int32_t rows, int32_t cols, size_t *code_bytes, size_t *scale_bytes) {
+    const int rc = check_mx4_shape(rows, cols);
+    if (rc) return rc;
+    if (code_bytes) *code_bytes = mx_code_bytes(rows, cols);
+    if (scale_bytes) *scale_bytes = mx_scale_bytes(rows, cols);
+    return ok();
+}
+
+int waste_mx4_quantize(const void *d_x, int32_t dtype, int32_t rows, int32_t cols, int64_t ld, uint8_t *d_codes,
+                       uint8_t *d_scales, waste_stream_t stream) {
+    const NvtxRange nvtx_range(__func__);
+    int rc = check_mx4_shape(rows, cols);
+    if (rc || rows == 0) return rc ? rc : ok();
+    rc = check_mx4_x(d_x, dtype, cols, ld, "x");
+    const void *p[] = {d_codes, d_scales};
+    const char *n[] = {"codes", "scales"};
+    if (!rc) rc = check_ptrs(p, n, 2);
+    if (rc) return rc;
+    return done(launch_mx4_quantize(d_x, dtype, rows, cols, ld, d_codes, d_scales,
+                                    reinterpret_cast<cudaStream_t>(stream)),
+                "4-bit quantisation");
+}
+
+int waste_mx4_dequantize(const uint8_t *d_codes, const uint8_t *d_scales, int32_t rows, int32_t cols, void *d_out,
+                         int32_t dtype, int64_t ld, waste_stream_t stream) {
+    const NvtxRange nvtx_range(__func__);
+    int rc = check_mx4_shape(rows, cols);
+    if (rc || rows == 0) return rc ? rc : ok();
+    rc = check_mx4_x(d_out, dtype, cols, ld, "out");
+    const void *p[] = {d_codes, d_scales};
+    const char *n[] = {"codes", "scales"};
+    if (!rc) rc = check_ptrs(p, n, 2);
+    if (rc) return rc;
+    return done(launch_mx4_dequantize(Mx4Mat{d_codes, d_scales, rows, cols}, d_out, dtype, ld,
+                                      reinterpret_cast<cudaStream_t>(stream)),
+                "4-bit dequantisation");
+}
+
+int waste_mx4_matmul(int32_t M, int32_t N, int32_t K, const uint8_t *d_a_codes, const uint8_t *d_a_scales,
+                     const uint8_t *d_b_codes, const uint8_t *d_b_scales, void *d_out, int32_t out_dtype,
+                     int32_t mode, waste_stream_t stream) {
+    const NvtxRange nvtx_range(__func__);
+    int rc = check_mx4_shape(M, K);
+    if (rc) return rc;
+    if (N < 1) return fail(WASTE_EINVAL, "N = %d", N);
+    if (!any_type(out_dtype)) return fail(WASTE_EINVAL, "out_dtype = %d: fp32, bf16 or fp16", out_dtype);
+    if (mode != 0 && mode != 1) return fail(WASTE_EINVAL, "mode = %d", mode);
+    if (M == 0) return ok();
+    const void *p[] = {d_a_codes, d_a_scales, d_b_codes, d_b_scales, d_out};
+    const char *n[] = {"a_codes", "a_scales", "b_codes", "b_scales", "out"};
+    rc = check_ptrs(p, n, 5);
+    if (rc) return rc;
+    return done(launch_mx4_matmul(Mx4Mat{d_a_codes, d_a_scales, M, K}, Mx4Mat{d_b_codes, d_b_scales, N, K}, d_out,
+                                  out_dtype, mode, reinterpret_cast<cudaStream_t>(stream)),
+                "4-bit product");
+}
+
+int waste_mx4_ffn_workspace(const waste_mx4_ffn_config *cfg, int32_t T, size_t *bytes) {
+    const int rc = check_mx4_ffn(cfg, T);
+    if (rc) return rc;
+    if (!bytes) return fail(WASTE_EINVAL, "bytes is NULL");
+    *bytes = mx4_ffn_parts(cfg, T).total;
+    return ok();
+}
+
+int waste_mx4_ffn_forward(const waste_mx4_ffn_config *cfg, const void *d_x, int32_t x_dtype, int32_t T, void *d_out,
+                          int32_t out_dtype, int32_t mode, void *d_workspace, size_t workspace_bytes,
+                          waste_stream_t stream) {
+    const NvtxRange nvtx_range(__func__);
+    int rc = check_mx4_ffn(cfg, T);
+    if (rc) return rc;
+    if (!any_type(x_dtype) || !any_type(out_dtype))
+        return fail(WASTE_EINVAL, "x_dtype = %d, out_dtype = %d: fp32, bf16 or fp16", x_dtype, out_dtype);
+    if (mode != 0 && mode != 1) return fail(WASTE_EINVAL, "mode = %d", mode);
+    if (T == 0) return ok();
+    const void *p[] = {d_x,
+                       cfg->d_gate_codes,
+                       cfg->d_gate_scales,
+                       cfg->d_up_codes,
+                       cfg->d_up_scales,
+                       cfg->d_down_codes,
+                       cfg->d_down_scales,
+                       d_out};
+    const char *n[] = {"x", "gate_codes", "gate_scales", "up_codes", "up_scales", "down_codes", "down_scales", "out"};
+    rc = check_ptrs(p, n, 8);
+    const Mx4FfnParts W = mx4_ffn_parts(cfg, T);
+    if (!rc) rc = check_workspace(d_workspace, workspace_bytes, W.total);
+    if (rc) return rc;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    uint8_t *w = static_cast<uint8_t *>(d_workspace);
+    const int d = cfg->d, f = cfg->f;
+    cudaError_t e = launch_mx4_quantize(d_x, x_dtype, T, d, d, w + W.xc, w + W.xs, s);
+    if (e == cudaSuccess)
+        e = launch_mx4_gated(Mx4Mat{w + W.xc, w + W.xs, T, d}, Mx4Mat{cfg->d_gate_codes, cfg->d_gate_scales, f, d},
+                             Mx4Mat{cfg->d_up_codes, cfg->d_up_scales, f, d}, w + W.ac, w + W.as, w + W.scratch, s);
+    if (e == cudaSuccess)
+        e = launch_mx4_matmul(Mx4Mat{w + W.ac, w + W.as, T, f}, Mx4Mat{cfg->d_down_codes, cfg->d_down_scales, d, f},
+                              d_out, out_dtype, mode, s);
+    return done(e, "4-bit gated feed-forward");
+}
+
+} // extern "C"

@@ -1,0 +1,109 @@
+"""A dense expert: the gated feed-forward block of the routed experts on 16-bit weights, forward
+and backward (include/waste_dense.h: waste_ffn_forward, waste_ffn_backward).
+
+Models put such an expert beside the routed ones, applied to every token; an expert is also
+trained in this form before its matrices are encoded (``waste_rvq_train``).  All computation
+is in the library's kernels.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import binding as B
+
+ACT = {torch.float32: B.ACT_F32, torch.bfloat16: B.ACT_BF16, torch.float16: B.ACT_F16}
+
+
+def require(ok: bool, message: str):
+    if not ok:
+        raise B.WasteError(-1, message)
+
+
+def check(t, name: str, shape, dtypes, device):
+    """A contiguous tensor of the given shape, on the given device, of one of the types."""
+    require(isinstance(t, torch.Tensor) and t.shape == shape and t.dtype in dtypes and t.device == device
+            and t.is_contiguous(),
+            f"{name}: a contiguous tensor of shape {tuple(shape)} and type {' or '.join(map(str, dtypes))} "
+            f"on {device} is needed")
+
+
+class DenseExpert:
+    """w_gate, w_up [f, d] and w_down [d, f], bf16 or fp16, contiguous on one GPU (borrowed, not
+    copied).  max_tokens bounds T and sizes the workspace, which belongs to this object: calls
+    of one object must not run at the same time on two streams, and two captured graphs that
+    may replay at the same time need an object each."""
+
+    def __init__(self, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor, max_tokens: int):
+        f, d = w_gate.shape
+        dev, t = w_gate.device, w_gate.dtype
+        require(dev.type == "cuda" and t in (torch.bfloat16, torch.float16),
+                "weights are bf16 or fp16 tensors on a GPU")
+        check(w_gate, "w_gate", (f, d), (t,), dev)
+        check(w_up, "w_up", (f, d), (t,), dev)
+        check(w_down, "w_down", (d, f), (t,), dev)
+        require(max_tokens >= 1, "max_tokens >= 1")
+        self.w_gate, self.w_up, self.w_down = w_gate, w_up, w_down
+        self.d, self.f, self.dtype, self.device, self.max_tokens = d, f, t, dev, int(max_tokens)
+        self.cfg = B.waste_ffn_config(B.ABI_VERSION, d, f, ACT[t])
+        self._ws = {}
+        self._workspace(0)
+
+    def _workspace(self, backward: int) -> torch.Tensor:
+        """One workspace for the forward and one, made by the first call, for the backward; a call
+        that would make it while its stream is being captured is refused (the buffer would
+        belong to the graph)."""
+        ws = self._ws.get(backward)
+        if ws is None:
+            require(not torch.cuda.is_current_stream_capturing(),
+                    "reserve the workspace before the capture (reserve_backward)")
+            n = B.waste_ffn_workspace(self.cfg, self.max_tokens, backward)
+            ws = self._ws[backward] = torch.empty(max(n, 256), dtype=torch.uint8, device=self.device)
+        return ws
+
+    def reserve_backward(self):
+        """Makes the backward's workspace (three [max_tokens, f] buffers) now."""
+        self._workspace(1)
+
+    def _tokens(self, x, name):
+        require(isinstance(x, torch.Tensor) and x.dim() == 2, f"{name}: a [T, d] tensor is needed")
+        T = x.shape[0]
+        require(T <= self.max_tokens, f"T = {T} exceeds max_tokens = {self.max_tokens}")
+        check(x, name, (T, self.d), (self.dtype,), self.device)
+        return T
+
+    def forward(self, x, out=None, mode: int = 0, save_g=None, save_u=None, stream=None):
+        """out [T, d] (fp32 or the weights' type; made if None) = (mode 0) or += (mode 1) the
+        block's output for x [T, d].  save_g, save_u [T, f] receive what backward needs."""
+        T = self._tokens(x, "x")
+        if out is None:
+            require(mode == 0, "mode 1 adds to a given out")
+            out = torch.empty(T, self.d, dtype=self.dtype, device=self.device)
+        check(out, "out", (T, self.d), (self.dtype, torch.float32), self.device)
+        for t, n in ((save_g, "save_g"), (save_u, "save_u")):
+            if t is not None:
+                check(t, n, (T, self.f), (self.dtype,), self.device)
+        with torch.cuda.device(self.device):
+            B.waste_ffn_forward(self.cfg, x, T, self.w_gate, self.w_up, self.w_down, out, ACT[out.dtype], mode,
+                                save_g, save_u, self._ws[0], stream)
+        return out
+
+    def backward(self, dy, x, g, u, dx=None, dw_gate=None, dw_up=None, dw_down=None, accumulate: bool = False,
+                 stream=None):
+        """Gradients for dy [T, d], given forward's x, g and u: into dx [T, d] (None: not computed)
+        and the three weights' gradients (all or none; fp32 or the weights' type), added to
+        what is there with accumulate."""
+        T = self._tokens(dy, "dy")
+        check(x, "x", (T, self.d), (self.dtype,), self.device)
+        check(g, "g", (T, self.f), (self.dtype,), self.device)
+        check(u, "u", (T, self.f), (self.dtype,), self.device)
+        if dx is not None:
+            check(dx, "dx", (T, self.d), (self.dtype,), self.device)
+        gt = self.dtype if dw_gate is None else dw_gate.dtype
+        for t, n, w in ((dw_gate, "dw_gate", self.w_gate), (dw_up, "dw_up", self.w_up),
+                        (dw_down, "dw_down", self.w_down)):
+            if t is not None:
+                require(gt in (self.dtype, torch.float32), f"{n}: fp32 or the weights' type")
+                check(t, n, w.shape, (gt,), self.device)
+        with torch.cuda.device(self.device):
+            B.waste_ffn_backward(self.cfg, dy, T, x, g, u, self.w_gate, self.w_up, self.w_down, dx, dw_gate, dw_up,
+                                 dw_down, ACT[gt], int(accumulate), self._workspace(1), stream)

@@ -1,0 +1,118 @@
+"""Microscaled 4-bit matrices (MXFP4), their product, and a dense expert whose weights are held
+in them (include/waste_dense.h: waste_mx4_*).
+
+Beside the 3-bit codes of the routed experts (``waste_rvq_train``) this is the cheap format: no
+codebooks and no training, a matrix is quantised in one pass, and the tensor core multiplies it
+without decoding.  All computation is in the library's kernels.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import binding as B
+from .dense import ACT, check, require
+
+_FLOATS = (torch.float32, torch.bfloat16, torch.float16)
+
+
+class Mx4Matrix:
+    """codes [rows, cols / 2] uint8 and the scale tiles (uint8, waste_mx4_layout) of a matrix."""
+
+    def __init__(self, rows: int, cols: int, codes: torch.Tensor, scales: torch.Tensor):
+        nc, ns = B.waste_mx4_layout(rows, cols)
+        dev = codes.device
+        require(dev.type == "cuda", "codes and scales are tensors on a GPU")
+        check(codes, "codes", (rows, cols // 2), (torch.uint8,), dev)
+        check(scales, "scales", (ns,), (torch.uint8,), dev)
+        self.rows, self.cols, self.codes, self.scales, self.device = rows, cols, codes, scales, dev
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, device="cuda") -> "Mx4Matrix":
+        _, ns = B.waste_mx4_layout(rows, cols)
+        return cls(rows, cols, torch.empty(rows, cols // 2, dtype=torch.uint8, device=device),
+                   torch.empty(ns, dtype=torch.uint8, device=device))
+
+    @classmethod
+    def from_dense(cls, x: torch.Tensor, stream=None) -> "Mx4Matrix":
+        require(isinstance(x, torch.Tensor) and x.dim() == 2, "x: a [rows, cols] tensor is needed")
+        m = cls.empty(*x.shape, device=x.device)
+        m.quantize(x, stream)
+        return m
+
+    def _plain(self, t, name, dtypes=_FLOATS) -> int:
+        """The row stride of a [rows, cols] tensor whose rows are contiguous."""
+        require(isinstance(t, torch.Tensor) and t.shape == (self.rows, self.cols) and t.dtype in dtypes
+                and t.device == self.device and (self.rows == 0 or t.stride(1) == 1),
+                f"{name}: a [{self.rows}, {self.cols}] tensor with contiguous rows, fp32, bf16 or fp16, on "
+                f"{self.device} is needed")
+        return max(t.stride(0), self.cols) if self.rows < 2 else t.stride(0)
+
+    def quantize(self, x: torch.Tensor, stream=None):
+        """Replace this matrix by the quantised x [rows, cols]."""
+        ld = self._plain(x, "x")
+        with torch.cuda.device(self.device):
+            B.waste_mx4_quantize(x, ACT[x.dtype], self.rows, self.cols, ld, self.codes, self.scales, stream)
+
+    def dequantize(self, out: torch.Tensor | None = None, dtype=torch.float32, stream=None) -> torch.Tensor:
+        """The values the codes stand for, into out [rows, cols] (made with dtype if None)."""
+        if out is None:
+            out = torch.empty(self.rows, self.cols, dtype=dtype, device=self.device)
+        ld = self._plain(out, "out")
+        with torch.cuda.device(self.device):
+            B.waste_mx4_dequantize(self.codes, self.scales, self.rows, self.cols, out, ACT[out.dtype], ld, stream)
+        return out
+
+
+def matmul(a: Mx4Matrix, b: Mx4Matrix, out: torch.Tensor | None = None, mode: int = 0, dtype=torch.float32,
+           stream=None) -> torch.Tensor:
+    """out [a.rows, b.rows] (fp32, bf16 or fp16; made with dtype if None) = (mode 0) or += (mode 1)
+    a b^T, summed in fp32."""
+    require(a.cols == b.cols, f"a has {a.cols} columns, b {b.cols}")
+    require(a.device == b.device, "a and b are on two devices")
+    if out is None:
+        require(mode == 0, "mode 1 adds to a given out")
+        out = torch.empty(a.rows, b.rows, dtype=dtype, device=a.device)
+    check(out, "out", (a.rows, b.rows), _FLOATS, a.device)
+    with torch.cuda.device(a.device):
+        B.waste_mx4_matmul(a.rows, b.rows, a.cols, a.codes, a.scales, b.codes, b.scales, out, ACT[out.dtype], mode,
+                           stream)
+    return out
+
+
+class Mx4Expert:
+    """A dense expert with 4-bit weights: gate, up [f, d] and down [d, f] (kept, not copied).
+    max_tokens bounds T and sizes the workspace, which belongs to this object: calls of one
+    object must not run at the same time on two streams, and two captured graphs that may replay
+    at the same time need an object each."""
+
+    def __init__(self, gate: Mx4Matrix, up: Mx4Matrix, down: Mx4Matrix, max_tokens: int):
+        f, d = gate.rows, gate.cols
+        require((up.rows, up.cols) == (f, d) and (down.rows, down.cols) == (d, f),
+                "gate and up are [f, d], down is [d, f]")
+        require(gate.device == up.device == down.device, "the matrices are on two devices")
+        require(max_tokens >= 1, "max_tokens >= 1")
+        self.gate, self.up, self.down = gate, up, down
+        self.d, self.f, self.device, self.max_tokens = d, f, gate.device, int(max_tokens)
+        self.cfg = B.waste_mx4_ffn_config(B.ABI_VERSION, d, f, *(t.data_ptr() for m in (gate, up, down)
+                                                                 for t in (m.codes, m.scales)))
+        self._ws = torch.empty(max(B.waste_mx4_ffn_workspace(self.cfg, self.max_tokens), 256), dtype=torch.uint8,
+                               device=self.device)
+
+    @classmethod
+    def from_dense(cls, w_gate, w_up, w_down, max_tokens: int) -> "Mx4Expert":
+        return cls(*(Mx4Matrix.from_dense(w) for w in (w_gate, w_up, w_down)), max_tokens=max_tokens)
+
+    def forward(self, x, out=None, mode: int = 0, stream=None):
+        """out [T, d] (fp32, bf16 or fp16; made as x if None) = (mode 0) or += (mode 1) the block's
+        output for x [T, d]."""
+        require(isinstance(x, torch.Tensor) and x.dim() == 2, "x: a [T, d] tensor is needed")
+        T = x.shape[0]
+        require(T <= self.max_tokens, f"T = {T} exceeds max_tokens = {self.max_tokens}")
+        check(x, "x", (T, self.d), _FLOATS, self.device)
+        if out is None:
+            require(mode == 0, "mode 1 adds to a given out")
+            out = torch.empty(T, self.d, dtype=x.dtype, device=self.device)
+        check(out, "out", (T, self.d), _FLOATS, self.device)
+        with torch.cuda.device(self.device):
+            B.waste_mx4_ffn_forward(self.cfg, x, ACT[x.dtype], T, out, ACT[out.dtype], mode, self._ws, stream)
+        return out

@@ -20,17 +20,22 @@ tail and the combine leave free.  x alternates between two buffers so the side
 stream can still read x_L while x_{L+1} is written; layer L+1 routes only after
 its prefetch has finished (an event), which also keeps the next write of x_L's
 buffer behind the read.
+A layer may also have a dense expert that serves every token beside the routed ones
+(``shared``): its output for x_L joins the residual after the routed experts' combine.
 """
 from __future__ import annotations
 
 import torch
 
 from . import binding as B
+from .dense import DenseExpert
 
 
 class DecodeStack:
-    def __init__(self, layers, tokens: int, device="cuda", banked: bool = False):
-        """banked: the layers' records live in a tiered bank (TieredStack); each layer's
+    def __init__(self, layers, tokens: int, device="cuda", banked: bool = False, shared=None):
+        """shared: None, or per layer None, a ``dense.DenseExpert`` or an ``mx4.Mx4Expert`` with
+        max_tokens >= tokens, applied to the layer's input and added to the residual.
+        banked: the layers' records live in a tiered bank (TieredStack); each layer's
         forward is then issued before the lookahead into the next layer, whose copies into
         the HBM cache run beside the forward's expert kernels."""
         self.banked = banked
@@ -42,6 +47,15 @@ class DecodeStack:
         self.x = [torch.empty(tokens, w.d, dtype=torch.float32, device=device) for _ in range(2)]
         self.idx = torch.empty(tokens, w.top_k, dtype=torch.int32, device=device)
         self.gate = torch.empty(tokens, w.top_k, dtype=torch.float32, device=device)
+        self.shared = list(shared) if shared is not None else [None] * len(layers)
+        if len(self.shared) != len(layers):
+            raise ValueError(f"{len(self.shared)} shared experts for {len(layers)} layers")
+        for e in self.shared:
+            if e is not None and (e.d != w.d or e.max_tokens < tokens):
+                raise ValueError("a shared expert has another hidden size or too small a max_tokens")
+        # 16-bit copies of x_L, for the shared experts whose weights are of that type
+        self.x16 = {t: torch.empty(tokens, w.d, dtype=t, device=device)
+                    for t in {e.dtype for e in self.shared if isinstance(e, DenseExpert)}}
 
     def run(self, h0: torch.Tensor, lookahead: int, main: torch.cuda.Stream,
             side: torch.cuda.Stream | None = None, on_layer=None) -> torch.Tensor:
@@ -70,12 +84,23 @@ class DecodeStack:
                 ev.record(side)
             # experts + combine (h += combine)
             self.layers[L].forward(x, T, self.idx, self.gate, self.h, 1, stream=main)
+            self._add_shared(L, x, main)
             if on_layer is not None:
                 on_layer(L, self.idx, self.gate, main)
             pending = ev
         if pending is not None:
             main.wait_event(pending)
         return self.h
+
+    def _add_shared(self, L, x, main):
+        """h += shared expert of layer L applied to x_L, if the layer has one."""
+        e = self.shared[L]
+        if e is None:
+            return
+        if isinstance(e, DenseExpert):
+            with torch.cuda.stream(main):
+                x = self.x16[e.dtype].copy_(x)
+        e.forward(x, self.h, mode=1, stream=main)
 
     def _run_one_token(self, lookahead, main, on_layer):
         """One token: the lookahead runs inside each layer's step (waste_moe_set_lookahead): layer
@@ -90,6 +115,7 @@ class DecodeStack:
             x = self.x[L & 1]
             B.waste_moe_rmsnorm(self.h, x, 1, self.d, main)
             self.layers[L].step(x, 1, self.idx, self.gate, self.h, 1, stream=main)
+            self._add_shared(L, x, main)
             if on_layer is not None:
                 on_layer(L, self.idx, self.gate, main)
         return self.h
@@ -106,6 +132,7 @@ class DecodeStack:
             if pending is not None:
                 main.wait_event(pending)  # layer L's prediction is in place before it routes
             self.layers[L].step(x, T, self.idx, self.gate, self.h, 1, stream=main)
+            self._add_shared(L, x, main)
             if on_layer is not None:
                 on_layer(L, self.idx, self.gate, main)
             pending = None
