@@ -32,6 +32,11 @@ extern "C" {
 
 enum { WASTE_ACT_F16 = 2 }; /* beside WASTE_ACT_F32 and WASTE_ACT_BF16 */
 
+/* Synchronises the device; WASTE_ETIMEOUT if a bounded device wait of one of these operators
+ * gave up on the current device since the last call of this (outputs since then are not to be
+ * used, and the context is to be treated as unusable, as after waste_moe_stats), else WASTE_OK. */
+int waste_dense_status(void);
+
 /* ---- gated feed-forward block ---------------------------------------------------------
  * d % 8 == 0, f % 8 == 0, both positive; dtype WASTE_ACT_BF16 or WASTE_ACT_F16: the type of x,
  * the weights, g, u, dy and dx.  Sums are held in fp32; a, dg and du are rounded once to dtype

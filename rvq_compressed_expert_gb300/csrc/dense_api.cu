@@ -86,7 +86,7 @@ int check_mx4_ffn(const waste_mx4_ffn_config *c, int32_t T) {
 }
 
 struct Mx4FfnParts {
-    size_t xc, xs, ac, as, scratch, total;
+    size_t xc, xs, ac, as, total;
 };
 Mx4FfnParts mx4_ffn_parts(const waste_mx4_ffn_config *c, int32_t T) {
     Mx4FfnParts p;
@@ -100,7 +100,6 @@ Mx4FfnParts mx4_ffn_parts(const waste_mx4_ffn_config *c, int32_t T) {
     p.xs = take(mx_scale_bytes(T, c->d));
     p.ac = take(mx_code_bytes(T, c->f));
     p.as = take(mx_scale_bytes(T, c->f));
-    p.scratch = take(mx4_gated_scratch(T, c->f));
     p.total = at;
     return p;
 }
@@ -108,6 +107,16 @@ Mx4FfnParts mx4_ffn_parts(const waste_mx4_ffn_config *c, int32_t T) {
 } // namespace
 
 extern "C" {
+
+int waste_dense_status(void) {
+    uint32_t timeout = 0;
+    cudaError_t e = cudaDeviceSynchronize();
+    if (e == cudaSuccess) e = ffn_timeout(&timeout);
+    if (e == cudaSuccess) e = mx4_timeout(&timeout);
+    if (e != cudaSuccess) return done(e, "reading the status");
+    if (timeout) return fail(WASTE_ETIMEOUT, "a device wait of a dense operator gave up");
+    return ok();
+}
 
 int waste_ffn_workspace(const waste_ffn_config *cfg, int32_t T, int32_t backward, size_t *bytes) {
     const int rc = check_ffn(cfg, T);
@@ -273,7 +282,7 @@ int waste_mx4_ffn_forward(const waste_mx4_ffn_config *cfg, const void *d_x, int3
     cudaError_t e = launch_mx4_quantize(d_x, x_dtype, T, d, d, w + W.xc, w + W.xs, s);
     if (e == cudaSuccess)
         e = launch_mx4_gated(Mx4Mat{w + W.xc, w + W.xs, T, d}, Mx4Mat{cfg->d_gate_codes, cfg->d_gate_scales, f, d},
-                             Mx4Mat{cfg->d_up_codes, cfg->d_up_scales, f, d}, w + W.ac, w + W.as, w + W.scratch, s);
+                             Mx4Mat{cfg->d_up_codes, cfg->d_up_scales, f, d}, w + W.ac, w + W.as, s);
     if (e == cudaSuccess)
         e = launch_mx4_matmul(Mx4Mat{w + W.ac, w + W.as, T, f}, Mx4Mat{cfg->d_down_codes, cfg->d_down_scales, d, f},
                               d_out, out_dtype, mode, s);

@@ -1,0 +1,138 @@
+// The gated feed-forward block on 16-bit weights, forward and backward, as tensor-core products
+// (dense_gemm.cuh).
+//
+// forward   1. (x Wg^T, x Wu^T) in one launch, both products of a tile side by side, a = silu(g) u
+//              (and g, u if kept) in the epilogue;  2. y = a Wd^T.
+// backward  1. da = dy Wd, a / dg / du in the epilogue from the kept g and u;
+//           2. dx = dg Wg + du Wu, one sum over both products;
+//           3. dWg = dg^T x, dWu = du^T x, dWd = dy^T a, three products of T terms in one launch.
+// Where a product runs over a matrix's rows (Wd, Wg, Wu in 1 and 2, everything in 3) the tiles go
+// to the tensor core MN-major, as they lie in memory: nothing is transposed.
+#include "dense_gemm.cuh"
+
+namespace wm {
+namespace dense {
+
+namespace {
+
+int pieces(int k) { return (k + 63) / 64; }
+
+cudaError_t half_map(CUtensorMap *m, const void *p, int rows, int cols, int box_rows) {
+    return make_map(m, p, 2, rows, (size_t)cols * 2, box_rows);
+}
+
+} // namespace
+
+cudaError_t launch_ffn_forward(const FfnFwd &P, cudaStream_t s) {
+    const int sms = device_sm_count();
+    const bool bf16 = P.dtype == WASTE_ACT_BF16;
+    cudaError_t e;
+    {
+        GemmArgs G = {};
+        G.K = P.d;
+        G.kb = G.kb_seg = pieces(P.d);
+        const Plan L = plan(&P.T, &P.f, 1, G.kb, true, false, sms);
+        G.BN = L.BN;
+        G.S = L.S;
+        G.nacc = 2;
+        set_problems(G, &P.T, &P.f, 1, true);
+        G.idesc = tc::idesc_half(kBM, G.BN, bf16, false, false);
+        if ((e = half_map(&G.ta[0], P.x, P.T, P.d, kBM)) != cudaSuccess) return e;
+        if ((e = half_map(&G.tb[0], P.wg, P.f, P.d, G.BN / 2)) != cudaSuccess) return e;
+        if ((e = half_map(&G.tb[1], P.wu, P.f, P.d, G.BN / 2)) != cudaSuccess) return e;
+        e = launch_gemm<kHalf, kPair, false, false>(G, Gated{P.a, P.g, P.u, P.f, P.dtype}, sms, s);
+        if (e != cudaSuccess) return e;
+    }
+    GemmArgs G = {};
+    G.K = P.f;
+    G.kb = G.kb_seg = pieces(P.f);
+    const Plan L = plan(&P.T, &P.d, 1, G.kb, false, false, sms);
+    G.BN = L.BN;
+    G.S = L.S;
+    G.nacc = 2;
+    set_problems(G, &P.T, &P.d, 1, false);
+    G.idesc = tc::idesc_half(kBM, G.BN, bf16, false, false);
+    if ((e = half_map(&G.ta[0], P.a, P.T, P.f, kBM)) != cudaSuccess) return e;
+    if ((e = half_map(&G.tb[0], P.wd, P.d, P.f, G.BN)) != cudaSuccess) return e;
+    Store st = {};
+    st.out[0] = P.out;
+    st.ld[0] = P.d;
+    st.dtype = P.out_dtype;
+    st.add = P.mode;
+    st.vec = 1; // d % 8 == 0
+    return launch_gemm<kHalf, kOne, false, false>(G, st, sms, s);
+}
+
+cudaError_t launch_ffn_backward(const FfnBwd &P, cudaStream_t s) {
+    const int sms = device_sm_count();
+    const bool bf16 = P.dtype == WASTE_ACT_BF16;
+    cudaError_t e;
+    {
+        GemmArgs G = {};
+        G.K = P.d;
+        G.kb = G.kb_seg = pieces(P.d);
+        const Plan L = plan(&P.T, &P.f, 1, G.kb, false, false, sms);
+        G.BN = L.BN;
+        G.S = L.S;
+        G.nacc = 2;
+        set_problems(G, &P.T, &P.f, 1, false);
+        G.idesc = tc::idesc_half(kBM, G.BN, bf16, false, true);
+        if ((e = half_map(&G.ta[0], P.dy, P.T, P.d, kBM)) != cudaSuccess) return e;
+        if ((e = half_map(&G.tb[0], P.wd, P.d, P.f, 64)) != cudaSuccess) return e;
+        e = launch_gemm<kHalf, kOne, false, true>(G, GatedGrad{P.g, P.u, P.a, P.dg, P.du, P.f, P.dtype}, sms, s);
+        if (e != cudaSuccess) return e;
+    }
+    if (P.dx) {
+        GemmArgs G = {};
+        G.K = P.f;
+        G.kb_seg = pieces(P.f);
+        G.kb = 2 * G.kb_seg;
+        const Plan L = plan(&P.T, &P.d, 1, G.kb, false, false, sms);
+        G.BN = L.BN;
+        G.S = L.S;
+        G.nacc = 2;
+        set_problems(G, &P.T, &P.d, 1, false);
+        G.idesc = tc::idesc_half(kBM, G.BN, bf16, false, true);
+        const void *a[2] = {P.dg, P.du}, *b[2] = {P.wg, P.wu};
+        for (int i = 0; i < 2; ++i) {
+            if ((e = half_map(&G.ta[i], a[i], P.T, P.f, kBM)) != cudaSuccess) return e;
+            if ((e = half_map(&G.tb[i], b[i], P.f, P.d, 64)) != cudaSuccess) return e;
+        }
+        Store st = {};
+        st.out[0] = P.dx;
+        st.ld[0] = P.d;
+        st.dtype = P.dtype;
+        st.vec = 1;
+        e = launch_gemm<kHalf, kSum, false, true>(G, st, sms, s);
+        if (e != cudaSuccess) return e;
+    }
+    if (!P.dwg) return cudaSuccess;
+    const int M[3] = {P.f, P.f, P.d}, N[3] = {P.d, P.d, P.f};
+    GemmArgs G = {};
+    G.K = P.T;
+    G.kb = G.kb_seg = pieces(P.T);
+    const Plan L = plan(M, N, 3, G.kb, false, false, sms);
+    G.BN = L.BN;
+    G.S = L.S;
+    G.nacc = 2;
+    set_problems(G, M, N, 3, false);
+    G.idesc = tc::idesc_half(kBM, G.BN, bf16, true, true);
+    const void *a[3] = {P.dg, P.du, P.dy}, *b[3] = {P.x, P.x, P.a};
+    void *out[3] = {P.dwg, P.dwu, P.dwd};
+    Store st = {};
+    for (int i = 0; i < 3; ++i) {
+        if ((e = half_map(&G.ta[i], a[i], P.T, M[i], 64)) != cudaSuccess) return e;
+        if ((e = half_map(&G.tb[i], b[i], P.T, N[i], 64)) != cudaSuccess) return e;
+        st.out[i] = out[i];
+        st.ld[i] = N[i];
+    }
+    st.dtype = P.grad_dtype;
+    st.add = P.accumulate;
+    st.vec = 1;
+    return launch_gemm<kHalf, kOne, true, true>(G, st, sms, s);
+}
+
+cudaError_t ffn_timeout(uint32_t *out) { return read_and_clear_timeout(out); }
+
+} // namespace dense
+} // namespace wm

@@ -1,0 +1,527 @@
+// The tensor-core product of the dense operators: D[m][n] = sum_k A[m][k] B[n][k] in fp32, on
+// tcgen05.mma, with an epilogue that takes the sums on their way out.
+//
+// A CTA makes 128 x BN tiles (BN <= 256).  One thread moves 128-byte-wide pieces of A and B (64
+// 16-bit or 256 4-bit values of k) into a ring of shared-memory stages by TMA; one thread issues
+// the MMAs on full stages into one of two TMEM accumulators; four warps take the other one out
+// through the epilogue meanwhile.  Rows, columns and k past the matrices' ends arrive as zeros
+// (TMA's fill), so any size works; the epilogue leaves them out.
+//
+// Two launch shapes (plan(), below):
+//   S = 1: a persistent grid, one CTA per SM, each taking every gridDim-th tile.
+//   S > 1: where there are few tiles, a cluster of S CTAs per tile, each with its share of k; the
+//          partial sums meet through distributed shared memory, each CTA adding up its share of
+//          the tile in rank order (the same bits every time) and running the epilogue on it.
+//
+// Waits are bounded: one that gives up (about a second) latches g_dense_timeout, which
+// waste_dense_status reports, and the CTA winds up.
+#pragma once
+
+#include "dense.cuh"
+#include "dense_tc.cuh"
+
+namespace wm {
+namespace dense {
+
+// kOne: up to three independent products of one k in one launch; kPair: two products with the same
+// A in one tile (columns [0, BN/2) by b0, the rest by b1); kSum: two products added.
+enum { kOne, kPair, kSum };
+enum { kHalf, kMx4 };
+
+constexpr int kBM = 128;
+constexpr int kRowBytes = 128; // bytes of one row of a stage
+constexpr int kMaxStages = 8;
+constexpr int kMaxProb = 3;
+constexpr uint32_t kSmemBudget = 225 * 1024;
+constexpr uint32_t kBarBytes = 256;
+constexpr int kThreads = 256;
+constexpr int kTmemCols = 512;
+
+struct Prob {
+    int M, N, tm, tn, begin; // sizes, tiles, first tile
+};
+struct alignas(64) GemmArgs {
+    CUtensorMap ta[kMaxProb], tb[kMaxProb];
+    Prob prob[kMaxProb];
+    int nprob, tiles;
+    int BN, S, stages, nacc;
+    int kb_seg; // k pieces of one product
+    int kb;     // k pieces in all (kSum: twice kb_seg)
+    int K;
+    uint32_t idesc;
+    // scale tiles of 4-bit operands: [row tile][skb] of 512 bytes
+    const uint8_t *sa, *sb[2];
+    int skb, nbt;
+};
+
+__device__ __forceinline__ int stage_scale_bytes(int BN) { return 1024 * (1 + (BN + 127) / 128); }
+
+struct Tile {
+    int p, m0, n0, rows; // n0: first column of b0 (kPair: of both)
+};
+template <int kForm> __device__ __forceinline__ Tile tile_at(const GemmArgs &P, int t) {
+    int p = 0;
+    if (kForm == kOne)
+        while (p + 1 < P.nprob && t >= P.prob[p + 1].begin) ++p;
+    const Prob &Q = P.prob[p];
+    t -= Q.begin;
+    // groups of 16 row tiles, columns moving slowest inside a group: the tiles in flight share
+    // their operands in L2
+    const int per = 16 * Q.tn, g = t / per, first = g * 16, gm = min(16, Q.tm - first), r = t - g * per;
+    Tile o;
+    o.p = p;
+    o.m0 = (first + r % gm) * kBM;
+    o.n0 = (r / gm) * (kForm == kPair ? P.BN / 2 : P.BN);
+    o.rows = min(kBM, Q.M - o.m0);
+    return o;
+}
+
+// One word in each translation unit that has kernels; read_and_clear_timeout reads its own.
+static __device__ uint32_t g_dense_timeout;
+
+static inline cudaError_t read_and_clear_timeout(uint32_t *out) {
+    uint32_t v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_dense_timeout, sizeof v);
+    const uint32_t zero = 0;
+    if (e == cudaSuccess && v) e = cudaMemcpyToSymbol(g_dense_timeout, &zero, sizeof zero);
+    *out |= v;
+    return e;
+}
+
+template <int kKind, int kForm, bool kAmn, bool kBmn, class Epi>
+__global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs P, const Epi epi) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t smem0 = tc::smem_u32(smem_raw);
+    const uint32_t base = (smem0 + kBarBytes + 1023) & ~1023u; // stages
+    const uint32_t bars = smem0;                              // full[8], empty[8], accfull[2], accempty[2]
+    const uint32_t bar_full = bars, bar_empty = bars + 64, bar_accf = bars + 128, bar_acce = bars + 144;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem_raw + 160);
+    volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem_raw + 164);
+    const uint32_t drain = bars + 168;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int BN = P.BN, S = P.S;
+    const uint32_t a_bytes = kBM * kRowBytes, b_bytes = (uint32_t)BN * kRowBytes;
+    const uint32_t s_off = a_bytes + b_bytes;
+    const uint32_t stage_bytes = (s_off + (kKind == kMx4 ? stage_scale_bytes(BN) : 0) + 1023) & ~1023u;
+
+    if (tid == 0) {
+        for (int i = 0; i < P.stages; ++i) {
+            tc::mbar_init(bar_full + 8 * i, 1);
+            tc::mbar_init(bar_empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(bar_accf + 8 * i, 1);
+            tc::mbar_init(bar_acce + 8 * i, 4);
+        }
+        tc::mbar_init(drain, 1);
+        *abort_flag = 0;
+        tc::mbar_init_fence();
+    }
+    if (warp == 2) tc::tmem_alloc(tc::smem_u32(tmem_slot), kTmemCols);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+
+    const int rank = S > 1 ? (int)tc::cluster_rank() : 0;
+    const int kb0 = S > 1 ? (int)((long long)P.kb * rank / S) : 0;
+    const int kb1 = S > 1 ? (int)((long long)P.kb * (rank + 1) / S) : P.kb;
+    const int tile0 = S > 1 ? (int)blockIdx.x / S : (int)blockIdx.x;
+    const int step = S > 1 ? P.tiles : (int)gridDim.x;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---- producer
+            int st = 0, issued = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (int t = tile0; t < P.tiles && ok; t += step) {
+                const Tile T = tile_at<kForm>(P, t);
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!tc::mbar_wait(bar_empty + 8 * st, ph ^ 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t sa = base + st * stage_bytes, sb = sa + a_bytes, full = bar_full + 8 * st;
+                    const bool second = kForm == kSum && kb >= P.kb_seg;
+                    const int k = second ? kb - P.kb_seg : kb;
+                    const CUtensorMap *ta = &P.ta[kForm == kSum ? (second ? 1 : 0) : T.p];
+                    const CUtensorMap *tb = &P.tb[kForm == kSum ? (second ? 1 : 0) : kForm == kPair ? 0 : T.p];
+                    uint32_t bytes = a_bytes + b_bytes;
+                    uint32_t sc = 0;
+                    int rt = 0, nrt = 0;
+                    if (kKind == kMx4) {
+                        sc = (uint32_t)min(2, P.skb - 2 * k) * kMxTileBytes;
+                        rt = T.n0 >> 7;
+                        nrt = kForm == kPair ? 2 : min((BN + 127) >> 7, P.nbt - rt);
+                        bytes += sc * (1 + nrt);
+                    }
+                    tc::mbar_arrive_expect_tx(full, bytes);
+                    const int kx = kKind == kMx4 ? k * kRowBytes : k * 64;
+                    if (kAmn) {
+                        for (int i = 0; i < kBM / 64; ++i) tc::tma_load(sa + i * 8192, ta, T.m0 + 64 * i, kx, full);
+                    } else {
+                        tc::tma_load(sa, ta, kx, T.m0, full);
+                    }
+                    if (kBmn) {
+                        for (int i = 0; i < BN / 64; ++i) tc::tma_load(sb + i * 8192, tb, T.n0 + 64 * i, kx, full);
+                    } else {
+                        tc::tma_load(sb, tb, kx, T.n0, full);
+                        if (kForm == kPair) tc::tma_load(sb + b_bytes / 2, &P.tb[1], kx, T.n0, full);
+                    }
+                    if (kKind == kMx4) {
+                        const uint32_t ss = sa + s_off;
+                        tc::bulk_g2s(ss, P.sa + ((size_t)(T.m0 >> 7) * P.skb + 2 * k) * kMxTileBytes, sc, full);
+                        for (int i = 0; i < nrt; ++i) {
+                            const uint8_t *src = kForm == kPair ? P.sb[i] : P.sb[0];
+                            const int r = kForm == kPair ? rt : rt + i;
+                            tc::bulk_g2s(ss + 1024 * (1 + i), src + ((size_t)r * P.skb + 2 * k) * kMxTileBytes, sc, full);
+                        }
+                    }
+                    ++issued;
+                    if (++st == P.stages) {
+                        st = 0;
+                        ph ^= 1;
+                    }
+                }
+            }
+            if (!ok) {
+                // copies in flight land before the CTA goes: the last rounds' full barriers
+                *abort_flag = 1;
+                const int n = min(issued, P.stages);
+                for (int i = 0; i < n; ++i) {
+                    const int j = issued - n + i;
+                    tc::mbar_wait(bar_full + 8 * (j % P.stages), (j / P.stages) & 1);
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // ---- MMA issuer
+            int st = 0, it = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (int t = tile0; t < P.tiles && ok; t += step, ++it) {
+                const int buf = P.nacc == 2 ? it & 1 : 0;
+                const uint32_t use = P.nacc == 2 ? it >> 1 : it;
+                if (!tc::mbar_wait(bar_acce + 8 * buf, (use & 1) ^ 1)) {
+                    ok = false;
+                    break;
+                }
+                tc::fence_after_sync();
+                const uint32_t d = tmem + buf * (kKind == kMx4 ? BN : 256);
+                uint32_t acc = 0;
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!tc::mbar_wait(bar_full + 8 * st, ph)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after_sync();
+                    const uint32_t sa = base + st * stage_bytes, sb = sa + a_bytes;
+                    if (kKind == kHalf) {
+                        const uint64_t da = tc::desc_sw128(sa, 8192), db = tc::desc_sw128(sb, 8192);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            tc::mma_f16(d, da + (uint64_t)(j * ((kAmn ? 2048 : 32) >> 4)),
+                                        db + (uint64_t)(j * ((kBmn ? 2048 : 32) >> 4)), P.idesc, acc);
+                            acc = 1;
+                        }
+                    } else {
+                        // scales to tensor memory, columns of their own for each stage (the stage
+                        // is full again only after the MMAs that read them are done)
+                        const int nrt = kForm == kPair ? 2 : (BN + 127) >> 7;
+                        const uint32_t sf = tmem + P.nacc * BN + st * (8 + 8 * nrt), ss = sa + s_off;
+                        const int steps = min(4, (P.K - kb * 256 + 63) >> 6);
+                        const int tiles = (steps + 1) >> 1;
+                        for (int h = 0; h < tiles; ++h) {
+                            tc::copy_scales(sf + 4 * h, tc::desc_scales(ss + 512 * h));
+                            for (int i = 0; i < nrt; ++i)
+                                tc::copy_scales(sf + 8 + 4 * (h * nrt + i), tc::desc_scales(ss + 1024 * (1 + i) + 512 * h));
+                        }
+                        const uint64_t da = tc::desc_sw128(sa, 16), db = tc::desc_sw128(sb, 16);
+                        for (int j = 0; j < steps; ++j) {
+                            const uint32_t id = P.idesc | (j & 1 ? (2u << 4) | (2u << 29) : 0u);
+                            tc::mma_mx4(d, da + (uint64_t)(2 * j), db + (uint64_t)(2 * j), id, sf + 4 * (j >> 1),
+                                        sf + 8 + 4 * nrt * (j >> 1), acc);
+                            acc = 1;
+                        }
+                    }
+                    tc::mma_commit(bar_empty + 8 * st);
+                    if (++st == P.stages) {
+                        st = 0;
+                        ph ^= 1;
+                    }
+                }
+                tc::mma_commit(bar_accf + 8 * buf);
+            }
+            if (!ok) {
+                *abort_flag = 1;
+                tc::mma_commit(drain);
+                tc::mbar_wait(drain, 0);
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ---- epilogue: warp q of four takes lanes (rows) 32 q .. 32 q + 31
+        const int q = warp - 4, r = 32 * q + lane;
+        const int cols = kForm == kPair ? BN / 2 : BN;
+        int it = 0;
+        for (int t = tile0; t < P.tiles; t += step, ++it) {
+            const Tile T = tile_at<kForm>(P, t);
+            const int buf = P.nacc == 2 ? it & 1 : 0;
+            const uint32_t use = P.nacc == 2 ? it >> 1 : it;
+            bool ok = true;
+            if (lane == 0) ok = tc::mbar_wait(bar_accf + 8 * buf, use & 1);
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) {
+                *abort_flag = 1;
+                break;
+            }
+            tc::fence_after_sync();
+            const uint32_t src = tmem + buf * (kKind == kMx4 ? BN : 256) + ((uint32_t)(32 * q) << 16);
+            if (32 * q < T.rows) {
+                for (int c = 0; c < cols; c += 32) {
+                    uint32_t v[32], w[32];
+                    tc::tmem_ld32(src + c, v);
+                    if (kForm == kPair) tc::tmem_ld32(src + cols + c, w);
+                    tc::tmem_wait_ld(v);
+                    if (kForm == kPair) tc::tmem_wait_ld(w);
+                    if (S > 1) {
+                        // this CTA's partial sums, rows padded by 16 bytes
+                        if (r < T.rows) {
+                            float4 *p = reinterpret_cast<float4 *>(smem_raw + (base - smem0)) + r * (BN / 4 + 1) + c / 4;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                p[i] = *reinterpret_cast<float4 *>(&v[4 * i]);
+                                if (kForm == kPair) p[cols / 4 + i] = *reinterpret_cast<float4 *>(&w[4 * i]);
+                            }
+                        }
+                    } else if (r < T.rows) {
+                        epi.template row<32>(T.p, T.m0 + r, T.n0 + c, *reinterpret_cast<float(*)[32]>(v),
+                                             *reinterpret_cast<float(*)[32]>(kForm == kPair ? w : v));
+                    }
+                }
+            }
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(bar_acce + 8 * buf);
+        }
+    }
+    if (S > 1) {
+        __syncthreads();
+        tc::cluster_sync();
+        const Tile T = tile_at<kForm>(P, tile0);
+        const int cols = kForm == kPair ? BN / 2 : BN, nc = cols / Epi::kWidth, items = T.rows * nc;
+        constexpr int W = Epi::kWidth;
+        // items of W columns, a contiguous share for each CTA of the cluster
+        const int i1 = (int)((long long)items * (rank + 1) / S);
+        for (int i = (int)((long long)items * rank / S) + tid; i < i1; i += kThreads) {
+            const int rr = i / nc, c = (i - rr * nc) * W;
+            float v[W], w[W];
+#pragma unroll
+            for (int j = 0; j < W; ++j) v[j] = w[j] = 0.f;
+            for (int s = 0; s < S; ++s) {
+                const uint32_t src = tc::map_rank(base + (uint32_t)(rr * (BN + 4) + c) * 4, s);
+#pragma unroll
+                for (int j = 0; j < W / 4; ++j) {
+                    const float4 x = tc::ld_cluster(src + 16 * j);
+                    v[4 * j] += x.x, v[4 * j + 1] += x.y, v[4 * j + 2] += x.z, v[4 * j + 3] += x.w;
+                    if (kForm == kPair) {
+                        const float4 y = tc::ld_cluster(src + 4 * cols + 16 * j);
+                        w[4 * j] += y.x, w[4 * j + 1] += y.y, w[4 * j + 2] += y.z, w[4 * j + 3] += y.w;
+                    }
+                }
+            }
+            epi.template row<W>(T.p, T.m0 + rr, T.n0 + c, v, w);
+        }
+        tc::cluster_sync(); // no CTA leaves while another reads its sums
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (tid == 0 && *abort_flag) atomicOr(&g_dense_timeout, 1u);
+    if (warp == 2) tc::tmem_dealloc(tmem, kTmemCols);
+}
+
+// ---- epilogues -----------------------------------------------------------------------------
+// row<W>(p, m, n, c, c2): W consecutive sums of row m from column n of problem p (n a multiple
+// of W); columns at or past N are left out.
+
+template <class O> __device__ __forceinline__ O round_to(float v);
+template <> __device__ __forceinline__ __nv_bfloat16 round_to<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <> __device__ __forceinline__ __half round_to<__half>(float v) { return __float2half_rn(v); }
+template <> __device__ __forceinline__ float round_to<float>(float v) { return v; }
+
+template <class O> struct Pack {
+    uint4 q;
+    __device__ void set(int i, float v) { reinterpret_cast<O *>(&q)[i] = round_to<O>(v); }
+    __device__ float get(int i) const { return (float)reinterpret_cast<const O *>(&q)[i]; }
+};
+
+// W values to p[0..W) (columns n..): whole 16-byte pieces where the row allows, add: to what is there.
+template <class O, int W>
+__device__ __forceinline__ void put(O *p, int n, int N, bool vec, bool add, const float (&v)[W]) {
+    constexpr int kPer = 16 / sizeof(O);
+    static_assert(W % kPer == 0, "whole pieces");
+#pragma unroll
+    for (int i = 0; i < W; i += kPer) {
+        if (vec && n + i + kPer <= N) {
+            Pack<O> o;
+            if (add) {
+                o.q = *reinterpret_cast<const uint4 *>(p + i);
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) o.set(j, o.get(j) + v[i + j]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) o.set(j, v[i + j]);
+            }
+            *reinterpret_cast<uint4 *>(p + i) = o.q;
+        } else {
+#pragma unroll
+            for (int j = 0; j < kPer; ++j)
+                if (n + i + j < N) p[i + j] = round_to<O>(add ? (float)p[i + j] + v[i + j] : v[i + j]);
+        }
+    }
+}
+template <int W>
+__device__ __forceinline__ void put_as(int dtype, void *out, size_t at, int n, int N, bool vec, bool add,
+                                       const float (&v)[W]) {
+    if (dtype == WASTE_ACT_F32)
+        put(static_cast<float *>(out) + at, n, N, vec, add, v);
+    else if (dtype == WASTE_ACT_BF16)
+        put(static_cast<__nv_bfloat16 *>(out) + at, n, N, vec, add, v);
+    else
+        put(static_cast<__half *>(out) + at, n, N, vec, add, v);
+}
+// 8 values of a 16-bit matrix
+__device__ __forceinline__ void get8(bool bf16, const void *src, size_t at, float (&v)[8]) {
+    if (bf16) {
+        Pack<__nv_bfloat16> p;
+        p.q = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(src) + at);
+        for (int i = 0; i < 8; ++i) v[i] = p.get(i);
+    } else {
+        Pack<__half> p;
+        p.q = *reinterpret_cast<const uint4 *>(static_cast<const __half *>(src) + at);
+        for (int i = 0; i < 8; ++i) v[i] = p.get(i);
+    }
+}
+
+// exp's own error and the division's stay below the bound the operators promise for one element;
+// exp overflowing to infinity gives 0, underflowing 1.
+__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-fmaxf(g, -88.f))); }
+
+struct Store {
+    static constexpr int kWidth = 8;
+    void *out[kMaxProb];
+    int ld[kMaxProb];
+    int dtype, add, vec;
+    template <int W>
+    __device__ __forceinline__ void row(int p, int m, int n, const float (&c)[W], const float (&)[W]) const {
+        put_as(dtype, out[p], (size_t)m * ld[p] + n, n, ld[p], vec, add, c);
+    }
+};
+
+// a = silu(g) u; g and u kept if asked for.  f % 8 == 0, so rows hold whole 16-byte pieces.
+struct Gated {
+    static constexpr int kWidth = 8;
+    void *a, *g, *u;
+    int f, dtype;
+    template <int W>
+    __device__ __forceinline__ void row(int, int m, int n, const float (&cg)[W], const float (&cu)[W]) const {
+        const size_t at = (size_t)m * f + n;
+        float v[W];
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[i] = cg[i] * sigmoid(cg[i]) * cu[i];
+        put_as(dtype, a, at, n, f, true, false, v);
+        if (g) {
+            put_as(dtype, g, at, n, f, true, false, cg);
+            put_as(dtype, u, at, n, f, true, false, cu);
+        }
+    }
+};
+
+// da -> a, dg, du from the kept g and u.
+struct GatedGrad {
+    static constexpr int kWidth = 8;
+    const void *g, *u;
+    void *a, *dg, *du;
+    int f, dtype;
+    template <int W>
+    __device__ __forceinline__ void row(int, int m, int n, const float (&da)[W], const float (&)[W]) const {
+#pragma unroll
+        for (int i = 0; i < W; i += 8) {
+            if (n + i >= f) break;
+            const size_t at = (size_t)m * f + n + i;
+            float gv[8], uv[8], x[8], y[8], z[8];
+            get8(dtype == WASTE_ACT_BF16, g, at, gv);
+            get8(dtype == WASTE_ACT_BF16, u, at, uv);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float s = sigmoid(gv[j]), silu = gv[j] * s;
+                x[j] = silu * uv[j];
+                y[j] = da[i + j] * uv[j] * s * (1.f + gv[j] * (1.f - s));
+                z[j] = da[i + j] * silu;
+            }
+            put_as(dtype, a, at, n + i, f, true, false, x);
+            put_as(dtype, dg, at, n + i, f, true, false, y);
+            put_as(dtype, du, at, n + i, f, true, false, z);
+        }
+    }
+};
+
+// ---- host side -----------------------------------------------------------------------------
+
+// A tensor map over rows x row_bytes bytes (contiguous rows): boxes of box_rows rows x 128 bytes,
+// 128-byte swizzle, zeros past the ends.  unit: bytes of one coordinate step (2 or 1).
+cudaError_t make_map(CUtensorMap *m, const void *p, int unit, int rows, size_t row_bytes, int box_rows);
+
+// Launch shape from the sizes alone: tile width and CTAs per tile for products of sizes (M, N) x
+// n and kb pieces of k.  pair: a tile holds BN / 2 columns of each of two products.  step: BN is a
+// multiple of it.
+struct Plan {
+    int BN, S;
+};
+Plan plan(const int *M, const int *N, int n, int kb, bool pair, bool mx4, int sms);
+
+inline void set_problems(GemmArgs &G, const int *M, const int *N, int n, bool pair) {
+    G.nprob = n;
+    G.tiles = 0;
+    for (int i = 0; i < n; ++i) {
+        const int w = pair ? G.BN / 2 : G.BN;
+        G.prob[i] = Prob{M[i], N[i], (M[i] + kBM - 1) / kBM, (N[i] + w - 1) / w, G.tiles};
+        G.tiles += G.prob[i].tm * G.prob[i].tn;
+    }
+}
+
+template <int kKind, int kForm, bool kAmn, bool kBmn, class Epi>
+cudaError_t launch_gemm(GemmArgs &G, const Epi &epi, int sms, cudaStream_t s) {
+    static SmemAttr attr;
+    const auto kernel = gemm_kernel<kKind, kForm, kAmn, kBmn, Epi>;
+    const uint32_t stage =
+        (uint32_t)round_up((size_t)(kBM + G.BN) * kRowBytes + (kKind == kMx4 ? 1024 * (1 + (G.BN + 127) / 128) : 0), 1024);
+    G.stages = (int)((kSmemBudget - kBarBytes - 1024) / stage);
+    if (G.stages > kMaxStages) G.stages = kMaxStages;
+    const uint32_t smem = kBarBytes + 1024 + G.stages * stage;
+    cudaError_t e = ensure_smem(attr, reinterpret_cast<const void *>(kernel), (int)smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute at[1];
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(G.S > 1 ? G.tiles * G.S : (G.tiles < sms ? G.tiles : sms));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 0;
+    if (G.S > 1) {
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = G.S;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.numAttrs = 1;
+    }
+    return cudaLaunchKernelEx(&cfg, kernel, G, epi);
+}
+
+} // namespace dense
+} // namespace wm

@@ -12,12 +12,6 @@ template <> __device__ __forceinline__ float from_f<float>(float v) { return v; 
 template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <> __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
 
-// Nearest E2M1 magnitude code of x >= 0 (ties to the even code, past 6 to 6): the number of
-// borders passed, a border itself going up where the upper code is even.
-__device__ __forceinline__ uint32_t mx_round(float x) {
-    return (x > 0.25f) + (x >= 0.75f) + (x > 1.25f) + (x >= 1.75f) + (x > 2.5f) + (x >= 3.5f) + (x > 5.f);
-}
-
 // One thread per block of 32 values; scale tiles are written whole, zero past the end.
 template <class T>
 __global__ void __launch_bounds__(256) quantize_kernel(const T *__restrict__ x, int rows, int cols, int64_t ld,
@@ -33,26 +27,10 @@ __global__ void __launch_bounds__(256) quantize_kernel(const T *__restrict__ x, 
         }
         const T *p = x + (size_t)row * ld + (size_t)b * kMxBlock;
         float v[kMxBlock];
-        uint32_t big = 0;
 #pragma unroll
-        for (int j = 0; j < kMxBlock; ++j) {
-            v[j] = to_f(p[j]);
-            big = max(big, __float_as_uint(v[j]) & 0x7fffffffu); // magnitudes order as their bits
-        }
-        // exponent field of the largest magnitude = floor(log2) + 127 (0: zero or subnormal)
-        const uint32_t field = big >> 23;
-        const bool bad = field == 255;
-        const int e = max(-127, (int)field - 127 - 2);
-        *sp = bad ? 255 : (uint8_t)(e + 127);
-        uint32_t w[4] = {0, 0, 0, 0};
-        if (!bad) {
-#pragma unroll
-            for (int j = 0; j < kMxBlock; ++j) {
-                // 2^-e as two factors: one may leave the range of fp32's normal numbers
-                const float m = ldexpf(fabsf(v[j]), -e);
-                w[j >> 3] |= (mx_round(m) | (__float_as_uint(v[j]) >> 31 << 3)) << (4 * (j & 7));
-            }
-        }
+        for (int j = 0; j < kMxBlock; ++j) v[j] = to_f(p[j]);
+        uint32_t w[4];
+        *sp = mx_quantize(v, w);
         *reinterpret_cast<uint4 *>(codes + (size_t)row * (cols / 2) + b * 16) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }

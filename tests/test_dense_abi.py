@@ -35,7 +35,7 @@ class Bytes:
 
 def test_header_matches_binding_and_library(lib):
     text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
-    names = sorted(set(re.findall(r"\b(waste_(?:ffn|mx4)_\w+)\s*\(", text)))
+    names = sorted(set(re.findall(r"\b(waste_(?:dense|ffn|mx4)_\w+)\s*\(", text)))
     assert names == sorted(B.EXPORTED_DENSE)
     out = os.popen(f"nm -D --defined-only {B.LIB_PATH}").read()
     for n in names:
