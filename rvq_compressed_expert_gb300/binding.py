@@ -165,7 +165,8 @@ def _ptr(x):
 
 def _stream(s):
     if s is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the current stream's handle without making a Stream object (3 us of the caller's time)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(s, int):
         return s
     return s.cuda_stream

@@ -57,40 +57,64 @@ cudaError_t ffn_timeout(uint32_t *out);
 cudaError_t mx4_timeout(uint32_t *out);
 
 #ifdef __CUDACC__
-// E2M1 value of a 4-bit code.
-__device__ __forceinline__ float mx_value(uint32_t code) {
-    const uint32_t n = code & 7u;
-    // 0, 0.5 (the only subnormal), then (1 + m / 2) 2^(e - 1)
-    const float v = n < 2 ? 0.5f * (float)n : __uint_as_float((((n >> 1) + 126u) << 23) | ((n & 1u) << 22));
-    return code & 8u ? -v : v;
-}
 // The power of two of a scale byte (2^-127 is a subnormal of fp32); 255 is NaN.
 __device__ __forceinline__ float mx_scale(uint32_t s) {
     return __uint_as_float(s == 255u ? 0x7fc00000u : s == 0u ? 0x00400000u : s << 23);
 }
 
-// Nearest E2M1 magnitude code of x >= 0 (ties to the even code, past 6 to 6): the number of
-// borders passed, a border itself going up where the upper code is even.
-__device__ __forceinline__ uint32_t mx_round(float x) {
-    return (x > 0.25f) + (x >= 0.75f) + (x > 1.25f) + (x >= 1.75f) + (x > 2.5f) + (x >= 3.5f) + (x > 5.f);
+// Exponent of a block whose largest magnitude has the fp32 bits `big`: its exponent field is
+// floor(log2) + 127 (0 for zero and subnormals).  255 in the field: the block holds an infinity
+// or a NaN.
+__device__ __forceinline__ int mx_exponent(uint32_t big) { return max(-127, (int)(big >> 23) - 127 - 2); }
+__device__ __forceinline__ bool mx_bad(uint32_t big) { return big >= 0x7f800000u; }
+// 2^-e: a normal fp32 number for every block exponent (-127 .. 125), so the product with it is
+// exact unless it underflows, far below half the smallest code.
+__device__ __forceinline__ float mx_inverse(int e) { return __uint_as_float((uint32_t)(127 - e) << 23); }
+// Eight E2M1 codes (v[0] in the lowest bits): nearest, ties to the even code, past 6 to 6.
+__device__ __forceinline__ uint32_t mx_codes8(const float (&v)[8]) {
+    uint32_t w;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(w)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return w;
 }
-
-// One block: its 32 codes (four words, lower columns in lower bits) and its scale byte.
+// The values of eight codes.
+__device__ __forceinline__ void mx_values8(uint32_t w, float (&v)[8]) {
+    uint32_t h[4];
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "mov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+    }
+}
+// One block held by one thread: its 32 codes and its scale byte.
 __device__ __forceinline__ uint8_t mx_quantize(const float (&v)[kMxBlock], uint32_t (&w)[4]) {
     uint32_t big = 0;
 #pragma unroll
-    for (int j = 0; j < kMxBlock; ++j) big = max(big, __float_as_uint(v[j]) & 0x7fffffffu); // order of magnitudes
-    // exponent field of the largest magnitude = floor(log2) + 127 (0: zero or subnormal)
-    const int field = (int)(big >> 23);
-    const bool bad = field == 255;
-    const int e = max(-127, field - 127 - 2);
-    w[0] = w[1] = w[2] = w[3] = 0;
-    if (!bad) {
+    for (int j = 0; j < kMxBlock; ++j) big = max(big, __float_as_uint(v[j]) & 0x7fffffffu);
+    const bool bad = mx_bad(big);
+    const int e = mx_exponent(big);
+    const float inv = mx_inverse(e);
 #pragma unroll
-        for (int j = 0; j < kMxBlock; ++j) {
-            const uint32_t c = mx_round(ldexpf(fabsf(v[j]), -e)) | (__float_as_uint(v[j]) >> 31 << 3);
-            w[j >> 3] |= c << (4 * (j & 7));
-        }
+    for (int i = 0; i < 4; ++i) {
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = v[8 * i + j] * inv;
+        w[i] = bad ? 0 : mx_codes8(x);
     }
     return bad ? 255 : (uint8_t)(e + 127);
 }

@@ -1,4 +1,12 @@
 // Microscaled 4-bit matrices: quantisation and its inverse.
+//
+// Both are one pass, bound by memory: a value is read once (2 or 4 bytes), its 4-bit code and its
+// share of a scale byte (1/32) written, or the other way round.  A lane takes 8 consecutive
+// values, so a warp's accesses are whole lines of one row (256 columns) and a block is four
+// neighbouring lanes: its largest magnitude is two shuffles away, and the four scale bytes that
+// stand together in a scale tile are gathered by two more into one word.  The roundings are the
+// hardware's e2m1 conversions.  A warp keeps its 256 columns and walks down the rows, kRows of
+// them in flight at once to cover the memory's latency.
 #include "dense.cuh"
 
 namespace wm {
@@ -6,79 +14,181 @@ namespace dense {
 
 namespace {
 
-template <class T> __device__ __forceinline__ float to_f(T v) { return (float)v; }
-template <class T> __device__ __forceinline__ T from_f(float v);
-template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
-template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-template <> __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kSegment = 256; // columns of a warp
+constexpr int kRows = 4;      // rows of a warp in flight
 
-// One thread per block of 32 values; scale tiles are written whole, zero past the end.
+// 8 consecutive values: one or two 16-byte pieces.
+template <class T> struct Eight {
+    uint4 q[sizeof(T) / 2];
+};
+template <class T> __device__ __forceinline__ Eight<T> load8(const T *p) {
+    Eight<T> r;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.q[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+    return r;
+}
+template <class T> __device__ __forceinline__ void store8(T *p, const Eight<T> &v) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4 *>(p)[i] = v.q[i];
+}
+__device__ __forceinline__ void unpack8(const Eight<float> &a, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = reinterpret_cast<const float *>(a.q)[i];
+}
+__device__ __forceinline__ void unpack8(const Eight<__nv_bfloat16> &a, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(a.q)[i]);
+}
+__device__ __forceinline__ void unpack8(const Eight<__half> &a, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __half2float(reinterpret_cast<const __half *>(a.q)[i]);
+}
+__device__ __forceinline__ void pack8(const float (&v)[8], Eight<float> &a) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) reinterpret_cast<float *>(a.q)[i] = v[i];
+}
+__device__ __forceinline__ void pack8(const float (&v)[8], Eight<__nv_bfloat16> &a) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        reinterpret_cast<__nv_bfloat162 *>(a.q)[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+}
+__device__ __forceinline__ void pack8(const float (&v)[8], Eight<__half> &a) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) reinterpret_cast<__half2 *>(a.q)[i] = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+}
+
+// Where a warp works: its segment, its first row and the distance to its next.
+struct Walk {
+    int col, row, step;
+};
+__device__ __forceinline__ Walk walk(int cols) {
+    const int nseg = (cols + kSegment - 1) / kSegment;
+    const int w = blockIdx.x * kWarps + (threadIdx.x >> 5), all = gridDim.x * kWarps;
+    Walk k;
+    k.col = (w % nseg) * kSegment + (threadIdx.x & 31) * 8;
+    k.row = w / nseg;
+    k.step = all / nseg; // warps past the last whole round have nothing to do
+    if (k.row >= k.step) k.row = 0x7fffffff;
+    return k;
+}
+
 template <class T>
-__global__ void __launch_bounds__(256) quantize_kernel(const T *__restrict__ x, int rows, int cols, int64_t ld,
-                                                       uint8_t *__restrict__ codes, uint8_t *__restrict__ scales) {
-    const int kb = (cols + 127) / 128, nb = cols / kMxBlock;
-    const size_t total = (size_t)((rows + 127) / 128) * 128 * kb * 4;
-    for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (size_t)gridDim.x * blockDim.x) {
-        const int row = (int)(i / (kb * 4)), b = (int)(i % (kb * 4));
-        uint8_t *sp = scales + mx_scale_at(row, b, kb);
-        if (row >= rows || b >= nb) {
-            *sp = 0;
-            continue;
+__global__ void __launch_bounds__(kThreads) quantize_kernel(const T *__restrict__ x, int rows, int cols, int64_t ld,
+                                                            uint8_t *__restrict__ codes, uint8_t *__restrict__ scales) {
+    const int lane = threadIdx.x & 31, kb = (cols + 127) / 128;
+    const Walk K = walk(cols);
+    const bool in = K.col < cols;
+    for (int64_t r0 = K.row; r0 < rows; r0 += (int64_t)kRows * K.step) {
+        Eight<T> a[kRows];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int64_t r = r0 + (int64_t)i * K.step;
+            if (in && r < rows) a[i] = load8(x + r * ld + K.col);
         }
-        const T *p = x + (size_t)row * ld + (size_t)b * kMxBlock;
-        float v[kMxBlock];
 #pragma unroll
-        for (int j = 0; j < kMxBlock; ++j) v[j] = to_f(p[j]);
-        uint32_t w[4];
-        *sp = mx_quantize(v, w);
-        *reinterpret_cast<uint4 *>(codes + (size_t)row * (cols / 2) + b * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int i = 0; i < kRows; ++i) {
+            const int64_t r = r0 + (int64_t)i * K.step;
+            if (r >= rows) break;
+            float v[8];
+            uint32_t big = 0;
+            if (in) {
+                unpack8(a[i], v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) big = max(big, __float_as_uint(v[j]) & 0x7fffffffu);
+            }
+            big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+            big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+            const bool bad = mx_bad(big);
+            const int e = mx_exponent(big);
+            // blocks past the last column have scale 0
+            uint32_t s = in ? (bad ? 255u : (uint32_t)(e + 127)) << (8 * ((lane >> 2) & 3)) : 0u;
+            s |= __shfl_xor_sync(0xffffffffu, s, 4);
+            s |= __shfl_xor_sync(0xffffffffu, s, 8);
+            if ((lane & 15) == 0 && in)
+                *reinterpret_cast<uint32_t *>(scales + mx_scale_at((int)r, K.col / kMxBlock, kb)) = s;
+            if (in) {
+                const float inv = mx_inverse(e);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] *= inv;
+                *reinterpret_cast<uint32_t *>(codes + (size_t)r * (cols / 2) + K.col / 2) = bad ? 0 : mx_codes8(v);
+            }
+        }
     }
+    // the scale words of the last tile's rows past the end
+    const int pad = (128 - (rows & 127)) & 127;
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < (int64_t)pad * kb; i += (int64_t)gridDim.x * kThreads)
+        *reinterpret_cast<uint32_t *>(scales + mx_scale_at(rows + (int)(i / kb), (int)(i % kb) * 4, kb)) = 0;
 }
 
 template <class T>
-__global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t *__restrict__ codes,
-                                                         const uint8_t *__restrict__ scales, int rows, int cols,
-                                                         T *__restrict__ out, int64_t ld) {
-    const int kb = (cols + 127) / 128, nb = cols / kMxBlock;
-    const size_t total = (size_t)rows * nb;
-    for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (size_t)gridDim.x * blockDim.x) {
-        const int row = (int)(i / nb), b = (int)(i % nb);
-        const float s = mx_scale(scales[mx_scale_at(row, b, kb)]);
-        const uint4 c = *reinterpret_cast<const uint4 *>(codes + (size_t)row * (cols / 2) + b * 16);
-        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-        T *p = out + (size_t)row * ld + (size_t)b * kMxBlock;
+__global__ void __launch_bounds__(kThreads) dequantize_kernel(const uint8_t *__restrict__ codes,
+                                                              const uint8_t *__restrict__ scales, int rows, int cols,
+                                                              T *__restrict__ out, int64_t ld) {
+    const int kb = (cols + 127) / 128;
+    const Walk K = walk(cols);
+    if (K.col >= cols) return;
+    for (int64_t r0 = K.row; r0 < rows; r0 += (int64_t)kRows * K.step) {
+        uint32_t w[kRows];
+        uint8_t s[kRows];
 #pragma unroll
-        for (int j = 0; j < kMxBlock; ++j) p[j] = from_f<T>(mx_value(w[j >> 3] >> (4 * (j & 7))) * s);
+        for (int i = 0; i < kRows; ++i) {
+            const int64_t r = r0 + (int64_t)i * K.step;
+            if (r < rows) {
+                w[i] = __ldg(reinterpret_cast<const uint32_t *>(codes + (size_t)r * (cols / 2) + K.col / 2));
+                s[i] = __ldg(scales + mx_scale_at((int)r, K.col / kMxBlock, kb));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int64_t r = r0 + (int64_t)i * K.step;
+            if (r >= rows) break;
+            float v[8];
+            mx_values8(w[i], v);
+            const float p = mx_scale(s[i]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] *= p;
+            Eight<T> a;
+            pack8(v, a);
+            store8(out + r * ld + K.col, a);
+        }
     }
 }
 
-int grid_for(size_t n) {
-    const size_t g = (n + 255) / 256, most = (size_t)device_sm_count() * 16;
-    return (int)(g < most ? g : most);
+// Warps for every (segment, kRows rows), at most four full rounds of the GPU's.
+int grid_for(int rows, int cols) {
+    const int64_t nseg = (cols + kSegment - 1) / kSegment;
+    const int64_t need = nseg * (((int64_t)rows + kRows - 1) / kRows);
+    const int64_t most = (int64_t)device_sm_count() * 32;
+    int64_t g = (need + kWarps - 1) / kWarps;
+    if (g > most) g = most;
+    // at least one whole round over a row
+    const int64_t least = (nseg + kWarps - 1) / kWarps;
+    return (int)(g < least ? least : g);
 }
 
 } // namespace
 
 cudaError_t launch_mx4_quantize(const void *x, int dtype, int rows, int cols, int64_t ld, uint8_t *codes,
                                 uint8_t *scales, cudaStream_t s) {
-    const int g = grid_for((size_t)((rows + 127) / 128) * 128 * ((cols + 127) / 128) * 4);
+    const int g = grid_for(rows, cols);
     if (dtype == WASTE_ACT_F32)
-        quantize_kernel<<<g, 256, 0, s>>>(static_cast<const float *>(x), rows, cols, ld, codes, scales);
+        quantize_kernel<<<g, kThreads, 0, s>>>(static_cast<const float *>(x), rows, cols, ld, codes, scales);
     else if (dtype == WASTE_ACT_BF16)
-        quantize_kernel<<<g, 256, 0, s>>>(static_cast<const __nv_bfloat16 *>(x), rows, cols, ld, codes, scales);
+        quantize_kernel<<<g, kThreads, 0, s>>>(static_cast<const __nv_bfloat16 *>(x), rows, cols, ld, codes, scales);
     else
-        quantize_kernel<<<g, 256, 0, s>>>(static_cast<const __half *>(x), rows, cols, ld, codes, scales);
+        quantize_kernel<<<g, kThreads, 0, s>>>(static_cast<const __half *>(x), rows, cols, ld, codes, scales);
     return cudaGetLastError();
 }
 
 cudaError_t launch_mx4_dequantize(const Mx4Mat &m, void *out, int dtype, int64_t ld, cudaStream_t s) {
-    const int g = grid_for((size_t)m.rows * (m.cols / kMxBlock));
+    const int g = grid_for(m.rows, m.cols);
     if (dtype == WASTE_ACT_F32)
-        dequantize_kernel<<<g, 256, 0, s>>>(m.codes, m.scales, m.rows, m.cols, static_cast<float *>(out), ld);
+        dequantize_kernel<<<g, kThreads, 0, s>>>(m.codes, m.scales, m.rows, m.cols, static_cast<float *>(out), ld);
     else if (dtype == WASTE_ACT_BF16)
-        dequantize_kernel<<<g, 256, 0, s>>>(m.codes, m.scales, m.rows, m.cols, static_cast<__nv_bfloat16 *>(out), ld);
+        dequantize_kernel<<<g, kThreads, 0, s>>>(m.codes, m.scales, m.rows, m.cols, static_cast<__nv_bfloat16 *>(out), ld);
     else
-        dequantize_kernel<<<g, 256, 0, s>>>(m.codes, m.scales, m.rows, m.cols, static_cast<__half *>(out), ld);
+        dequantize_kernel<<<g, kThreads, 0, s>>>(m.codes, m.scales, m.rows, m.cols, static_cast<__half *>(out), ld);
     return cudaGetLastError();
 }
 

@@ -7,6 +7,8 @@ is in the library's kernels.
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import binding as B
@@ -21,10 +23,18 @@ def require(ok: bool, message: str):
 
 def check(t, name: str, shape, dtypes, device):
     """A contiguous tensor of the given shape, on the given device, of one of the types."""
-    require(isinstance(t, torch.Tensor) and t.shape == shape and t.dtype in dtypes and t.device == device
-            and t.is_contiguous(),
-            f"{name}: a contiguous tensor of shape {tuple(shape)} and type {' or '.join(map(str, dtypes))} "
-            f"on {device} is needed")
+    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype in dtypes and t.device == device
+            and t.is_contiguous()):
+        require(False, f"{name}: a contiguous tensor of shape {tuple(shape)} and type "
+                       f"{' or '.join(map(str, dtypes))} on {device} is needed")
+
+
+def on_device(device):
+    """The context in which to call the library for tensors on `device`: none if it is current."""
+    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+_HERE = contextlib.nullcontext()
 
 
 class DenseExpert:
@@ -36,7 +46,7 @@ class DenseExpert:
     def __init__(self, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor, max_tokens: int):
         f, d = w_gate.shape
         dev, t = w_gate.device, w_gate.dtype
-        require(dev.type == "cuda" and t in (torch.bfloat16, torch.float16),
+        require(dev.type == "cuda" and dev.index is not None and t in (torch.bfloat16, torch.float16),
                 "weights are bf16 or fp16 tensors on a GPU")
         check(w_gate, "w_gate", (f, d), (t,), dev)
         check(w_up, "w_up", (f, d), (t,), dev)
@@ -44,6 +54,7 @@ class DenseExpert:
         require(max_tokens >= 1, "max_tokens >= 1")
         self.w_gate, self.w_up, self.w_down = w_gate, w_up, w_down
         self.d, self.f, self.dtype, self.device, self.max_tokens = d, f, t, dev, int(max_tokens)
+        self._own, self._out = (t,), (t, torch.float32)  # types of inputs, and of outputs
         self.cfg = B.waste_ffn_config(B.ABI_VERSION, d, f, ACT[t])
         self._ws = {}
         self._workspace(0)
@@ -65,10 +76,12 @@ class DenseExpert:
         self._workspace(1)
 
     def _tokens(self, x, name):
-        require(isinstance(x, torch.Tensor) and x.dim() == 2, f"{name}: a [T, d] tensor is needed")
+        if not isinstance(x, torch.Tensor) or x.dim() != 2:
+            require(False, f"{name}: a [T, d] tensor is needed")
         T = x.shape[0]
-        require(T <= self.max_tokens, f"T = {T} exceeds max_tokens = {self.max_tokens}")
-        check(x, name, (T, self.d), (self.dtype,), self.device)
+        if T > self.max_tokens:
+            require(False, f"T = {T} exceeds max_tokens = {self.max_tokens}")
+        check(x, name, (T, self.d), self._own, self.device)
         return T
 
     def forward(self, x, out=None, mode: int = 0, save_g=None, save_u=None, stream=None):
@@ -78,11 +91,11 @@ class DenseExpert:
         if out is None:
             require(mode == 0, "mode 1 adds to a given out")
             out = torch.empty(T, self.d, dtype=self.dtype, device=self.device)
-        check(out, "out", (T, self.d), (self.dtype, torch.float32), self.device)
+        check(out, "out", (T, self.d), self._out, self.device)
         for t, n in ((save_g, "save_g"), (save_u, "save_u")):
             if t is not None:
-                check(t, n, (T, self.f), (self.dtype,), self.device)
-        with torch.cuda.device(self.device):
+                check(t, n, (T, self.f), self._own, self.device)
+        with on_device(self.device):
             B.waste_ffn_forward(self.cfg, x, T, self.w_gate, self.w_up, self.w_down, out, ACT[out.dtype], mode,
                                 save_g, save_u, self._ws[0], stream)
         return out
@@ -93,17 +106,16 @@ class DenseExpert:
         and the three weights' gradients (all or none; fp32 or the weights' type), added to
         what is there with accumulate."""
         T = self._tokens(dy, "dy")
-        check(x, "x", (T, self.d), (self.dtype,), self.device)
-        check(g, "g", (T, self.f), (self.dtype,), self.device)
-        check(u, "u", (T, self.f), (self.dtype,), self.device)
+        check(x, "x", (T, self.d), self._own, self.device)
+        check(g, "g", (T, self.f), self._own, self.device)
+        check(u, "u", (T, self.f), self._own, self.device)
         if dx is not None:
-            check(dx, "dx", (T, self.d), (self.dtype,), self.device)
+            check(dx, "dx", (T, self.d), self._own, self.device)
         gt = self.dtype if dw_gate is None else dw_gate.dtype
         for t, n, w in ((dw_gate, "dw_gate", self.w_gate), (dw_up, "dw_up", self.w_up),
                         (dw_down, "dw_down", self.w_down)):
             if t is not None:
-                require(gt in (self.dtype, torch.float32), f"{n}: fp32 or the weights' type")
-                check(t, n, w.shape, (gt,), self.device)
-        with torch.cuda.device(self.device):
+                check(t, n, w.shape, (gt,) if gt in self._out else self._out, self.device)
+        with on_device(self.device):
             B.waste_ffn_backward(self.cfg, dy, T, x, g, u, self.w_gate, self.w_up, self.w_down, dx, dw_gate, dw_up,
                                  dw_down, ACT[gt], int(accumulate), self._workspace(1), stream)

@@ -10,7 +10,7 @@ from __future__ import annotations
 import torch
 
 from . import binding as B
-from .dense import ACT, check, require
+from .dense import ACT, check, on_device, require
 
 _FLOATS = (torch.float32, torch.bfloat16, torch.float16)
 
@@ -41,16 +41,16 @@ class Mx4Matrix:
 
     def _plain(self, t, name, dtypes=_FLOATS) -> int:
         """The row stride of a [rows, cols] tensor whose rows are contiguous."""
-        require(isinstance(t, torch.Tensor) and t.shape == (self.rows, self.cols) and t.dtype in dtypes
-                and t.device == self.device and (self.rows == 0 or t.stride(1) == 1),
-                f"{name}: a [{self.rows}, {self.cols}] tensor with contiguous rows, fp32, bf16 or fp16, on "
-                f"{self.device} is needed")
+        if not (isinstance(t, torch.Tensor) and t.shape == (self.rows, self.cols) and t.dtype in dtypes
+                and t.device == self.device and (self.rows == 0 or t.stride(1) == 1)):
+            require(False, f"{name}: a [{self.rows}, {self.cols}] tensor with contiguous rows, fp32, bf16 or fp16, "
+                           f"on {self.device} is needed")
         return max(t.stride(0), self.cols) if self.rows < 2 else t.stride(0)
 
     def quantize(self, x: torch.Tensor, stream=None):
         """Replace this matrix by the quantised x [rows, cols]."""
         ld = self._plain(x, "x")
-        with torch.cuda.device(self.device):
+        with on_device(self.device):
             B.waste_mx4_quantize(x, ACT[x.dtype], self.rows, self.cols, ld, self.codes, self.scales, stream)
 
     def dequantize(self, out: torch.Tensor | None = None, dtype=torch.float32, stream=None) -> torch.Tensor:
@@ -58,7 +58,7 @@ class Mx4Matrix:
         if out is None:
             out = torch.empty(self.rows, self.cols, dtype=dtype, device=self.device)
         ld = self._plain(out, "out")
-        with torch.cuda.device(self.device):
+        with on_device(self.device):
             B.waste_mx4_dequantize(self.codes, self.scales, self.rows, self.cols, out, ACT[out.dtype], ld, stream)
         return out
 
@@ -67,13 +67,14 @@ def matmul(a: Mx4Matrix, b: Mx4Matrix, out: torch.Tensor | None = None, mode: in
            stream=None) -> torch.Tensor:
     """out [a.rows, b.rows] (fp32, bf16 or fp16; made with dtype if None) = (mode 0) or += (mode 1)
     a b^T, summed in fp32."""
-    require(a.cols == b.cols, f"a has {a.cols} columns, b {b.cols}")
+    if a.cols != b.cols:
+        require(False, f"a has {a.cols} columns, b {b.cols}")
     require(a.device == b.device, "a and b are on two devices")
     if out is None:
         require(mode == 0, "mode 1 adds to a given out")
         out = torch.empty(a.rows, b.rows, dtype=dtype, device=a.device)
     check(out, "out", (a.rows, b.rows), _FLOATS, a.device)
-    with torch.cuda.device(a.device):
+    with on_device(a.device):
         B.waste_mx4_matmul(a.rows, b.rows, a.cols, a.codes, a.scales, b.codes, b.scales, out, ACT[out.dtype], mode,
                            stream)
     return out
@@ -107,12 +108,13 @@ class Mx4Expert:
         output for x [T, d]."""
         require(isinstance(x, torch.Tensor) and x.dim() == 2, "x: a [T, d] tensor is needed")
         T = x.shape[0]
-        require(T <= self.max_tokens, f"T = {T} exceeds max_tokens = {self.max_tokens}")
+        if T > self.max_tokens:
+            require(False, f"T = {T} exceeds max_tokens = {self.max_tokens}")
         check(x, "x", (T, self.d), _FLOATS, self.device)
         if out is None:
             require(mode == 0, "mode 1 adds to a given out")
             out = torch.empty(T, self.d, dtype=x.dtype, device=self.device)
         check(out, "out", (T, self.d), _FLOATS, self.device)
-        with torch.cuda.device(self.device):
+        with on_device(self.device):
             B.waste_mx4_ffn_forward(self.cfg, x, ACT[x.dtype], T, out, ACT[out.dtype], mode, self._ws, stream)
         return out
