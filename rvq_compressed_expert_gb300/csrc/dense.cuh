@@ -47,11 +47,14 @@ cudaError_t launch_ffn_backward(const FfnBwd &P, cudaStream_t s);
 cudaError_t launch_mx4_quantize(const void *x, int dtype, int rows, int cols, int64_t ld, uint8_t *codes,
                                 uint8_t *scales, cudaStream_t s);
 cudaError_t launch_mx4_dequantize(const Mx4Mat &m, void *out, int dtype, int64_t ld, cudaStream_t s);
-cudaError_t launch_mx4_matmul(const Mx4Mat &a, const Mx4Mat &b, void *out, int out_dtype, int mode, cudaStream_t s);
+// after_own: the kernel before this one in the stream is one of these operators' and does not write b.
+cudaError_t launch_mx4_matmul(const Mx4Mat &a, const Mx4Mat &b, void *out, int out_dtype, int mode, bool after_own,
+                              cudaStream_t s);
 // a = silu(x gate^T) * (x up^T), quantised into codes and scales ([x.rows][gate.rows]; the scale
-// bytes of rows past the end are not written).
-cudaError_t launch_mx4_gated(const Mx4Mat &x, const Mx4Mat &gate, const Mx4Mat &up, uint8_t *codes, uint8_t *scales,
-                             cudaStream_t s);
+// bytes of rows past the end are not written).  Behind launch_mx4_quantize of x; next: the codes
+// of the product behind it.
+cudaError_t launch_mx4_gated(const Mx4Mat &x, const Mx4Mat &gate, const Mx4Mat &up, const Mx4Mat &next,
+                             uint8_t *codes, uint8_t *scales, cudaStream_t s);
 // *out |= whether a device wait of these kernels gave up since the last call (cleared).
 cudaError_t ffn_timeout(uint32_t *out);
 cudaError_t mx4_timeout(uint32_t *out);

@@ -241,7 +241,7 @@ int waste_mx4_matmul(int32_t M, int32_t N, int32_t K, const uint8_t *d_a_codes, 
     rc = check_ptrs(p, n, 5);
     if (rc) return rc;
     return done(launch_mx4_matmul(Mx4Mat{d_a_codes, d_a_scales, M, K}, Mx4Mat{d_b_codes, d_b_scales, N, K}, d_out,
-                                  out_dtype, mode, reinterpret_cast<cudaStream_t>(stream)),
+                                  out_dtype, mode, false, reinterpret_cast<cudaStream_t>(stream)),
                 "4-bit product");
 }
 
@@ -279,13 +279,13 @@ int waste_mx4_ffn_forward(const waste_mx4_ffn_config *cfg, const void *d_x, int3
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     uint8_t *w = static_cast<uint8_t *>(d_workspace);
     const int d = cfg->d, f = cfg->f;
+    const Mx4Mat down{cfg->d_down_codes, cfg->d_down_scales, d, f};
     cudaError_t e = launch_mx4_quantize(d_x, x_dtype, T, d, d, w + W.xc, w + W.xs, s);
     if (e == cudaSuccess)
         e = launch_mx4_gated(Mx4Mat{w + W.xc, w + W.xs, T, d}, Mx4Mat{cfg->d_gate_codes, cfg->d_gate_scales, f, d},
-                             Mx4Mat{cfg->d_up_codes, cfg->d_up_scales, f, d}, w + W.ac, w + W.as, s);
+                             Mx4Mat{cfg->d_up_codes, cfg->d_up_scales, f, d}, down, w + W.ac, w + W.as, s);
     if (e == cudaSuccess)
-        e = launch_mx4_matmul(Mx4Mat{w + W.ac, w + W.as, T, f}, Mx4Mat{cfg->d_down_codes, cfg->d_down_scales, d, f},
-                              d_out, out_dtype, mode, s);
+        e = launch_mx4_matmul(Mx4Mat{w + W.ac, w + W.as, T, f}, down, d_out, out_dtype, mode, true, s);
     return done(e, "4-bit gated feed-forward");
 }
 

@@ -40,6 +40,13 @@ cudaError_t launch_ffn_forward(const FfnFwd &P, cudaStream_t s) {
         if ((e = half_map(&G.ta[0], P.x, P.T, P.d, kBM)) != cudaSuccess) return e;
         if ((e = half_map(&G.tb[0], P.wg, P.f, P.d, G.BN / 2)) != cudaSuccess) return e;
         if ((e = half_map(&G.tb[1], P.wu, P.f, P.d, G.BN / 2)) != cudaSuccess) return e;
+        // few tiles: bound by the weights' way from memory, which the next kernel's can follow
+        // at once while this one adds up and ends
+        const size_t wd = (size_t)P.d * P.f * 2;
+        if (G.S > 1 && wd <= kAheadMost) {
+            G.ahead = static_cast<const uint8_t *>(P.wd);
+            G.ahead_bytes = wd;
+        }
         e = launch_gemm<kHalf, kPair, false, false>(G, Gated{P.a, P.g, P.u, P.f, P.dtype}, sms, s);
         if (e != cudaSuccess) return e;
     }
@@ -54,6 +61,7 @@ cudaError_t launch_ffn_forward(const FfnFwd &P, cudaStream_t s) {
     G.idesc = tc::idesc_half(kBM, G.BN, bf16, false, false);
     if ((e = half_map(&G.ta[0], P.a, P.T, P.f, kBM)) != cudaSuccess) return e;
     if ((e = half_map(&G.tb[0], P.wd, P.d, P.f, G.BN)) != cudaSuccess) return e;
+    G.early_b = 1;
     Store st = {};
     st.out[0] = P.out;
     st.ld[0] = P.d;
@@ -98,6 +106,7 @@ cudaError_t launch_ffn_backward(const FfnBwd &P, cudaStream_t s) {
             if ((e = half_map(&G.ta[i], a[i], P.T, P.f, kBM)) != cudaSuccess) return e;
             if ((e = half_map(&G.tb[i], b[i], P.f, P.d, 64)) != cudaSuccess) return e;
         }
+        G.early_b = 1;
         Store st = {};
         st.out[0] = P.dx;
         st.ld[0] = P.d;

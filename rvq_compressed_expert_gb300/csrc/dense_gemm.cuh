@@ -40,7 +40,7 @@ constexpr int kTmemCols = 512;
 struct Prob {
     int M, N, tm, tn, begin; // sizes, tiles, first tile
 };
-struct alignas(64) GemmArgs {
+struct GemmArgs {
     CUtensorMap ta[kMaxProb], tb[kMaxProb];
     Prob prob[kMaxProb];
     int nprob, tiles;
@@ -52,6 +52,12 @@ struct alignas(64) GemmArgs {
     // scale tiles of 4-bit operands: [row tile][skb] of 512 bytes
     const uint8_t *sa, *sb[2];
     int skb, nbt;
+    // early_b: B does not come from the kernel before this one, so its first pieces are asked for
+    // before waiting for that kernel
+    int early_b;
+    // bytes that the next kernel reads and L2 can hold, asked for behind the own loads (or 0)
+    const uint8_t *ahead;
+    size_t ahead_bytes;
 };
 
 __device__ __forceinline__ int stage_scale_bytes(int BN) { return 1024 * (1 + (BN + 127) / 128); }
@@ -86,6 +92,28 @@ static inline cudaError_t read_and_clear_timeout(uint32_t *out) {
     if (e == cudaSuccess && v) e = cudaMemcpyToSymbol(g_dense_timeout, &zero, sizeof zero);
     *out |= v;
     return e;
+}
+
+// v += the W floats at shared address src of each CTA of the cluster, in rank order; the loads of
+// up to eight ranks are in flight at once, 8 floats at a time.
+template <int W> __device__ __forceinline__ void add_ranks(uint32_t src, int S, float (&v)[W]) {
+#pragma unroll
+    for (int j = 0; j < W; j += 8) {
+        float4 x[8][2];
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+            if (s < S) {
+                const uint32_t a = tc::map_rank(src + 4 * j, s);
+                x[s][0] = tc::ld_cluster(a);
+                x[s][1] = tc::ld_cluster(a + 16);
+            }
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+            if (s < S) {
+                v[j] += x[s][0].x, v[j + 1] += x[s][0].y, v[j + 2] += x[s][0].z, v[j + 3] += x[s][0].w;
+                v[j + 4] += x[s][1].x, v[j + 5] += x[s][1].y, v[j + 6] += x[s][1].z, v[j + 7] += x[s][1].w;
+            }
+    }
 }
 
 template <int kKind, int kForm, bool kAmn, bool kBmn, class Epi>
@@ -123,6 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
+    if (warp != 0) tc::grid_wait(); // warp 0's loader may have B's first pieces to ask for before
 
     const int rank = S > 1 ? (int)tc::cluster_rank() : 0;
     const int kb0 = S > 1 ? (int)((long long)P.kb * rank / S) : 0;
@@ -136,54 +165,82 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             int st = 0, issued = 0;
             uint32_t ph = 0;
             bool ok = true;
+            const auto load_a = [&](const Tile &T, int kb, int st) {
+                const uint32_t sa = base + st * stage_bytes, full = bar_full + 8 * st;
+                const bool second = kForm == kSum && kb >= P.kb_seg;
+                const int k = second ? kb - P.kb_seg : kb;
+                const CUtensorMap *ta = &P.ta[kForm == kSum ? (second ? 1 : 0) : T.p];
+                const int kx = kKind == kMx4 ? k * kRowBytes : k * 64;
+                if (kAmn) {
+                    for (int i = 0; i < kBM / 64; ++i) tc::tma_load(sa + i * 8192, ta, T.m0 + 64 * i, kx, full);
+                } else {
+                    tc::tma_load(sa, ta, kx, T.m0, full);
+                }
+                if (kKind == kMx4)
+                    tc::bulk_g2s(sa + s_off, P.sa + ((size_t)(T.m0 >> 7) * P.skb + 2 * k) * kMxTileBytes,
+                                 (uint32_t)min(2, P.skb - 2 * k) * kMxTileBytes, full);
+            };
+            // also announces the bytes of the whole stage
+            const auto load_b = [&](const Tile &T, int kb, int st) {
+                const uint32_t sb = base + st * stage_bytes + a_bytes, full = bar_full + 8 * st;
+                const bool second = kForm == kSum && kb >= P.kb_seg;
+                const int k = second ? kb - P.kb_seg : kb;
+                const CUtensorMap *tb = &P.tb[kForm == kSum ? (second ? 1 : 0) : kForm == kPair ? 0 : T.p];
+                const int kx = kKind == kMx4 ? k * kRowBytes : k * 64;
+                uint32_t bytes = a_bytes + b_bytes, sc = 0;
+                int rt = 0, nrt = 0;
+                if (kKind == kMx4) {
+                    sc = (uint32_t)min(2, P.skb - 2 * k) * kMxTileBytes;
+                    rt = T.n0 >> 7;
+                    nrt = kForm == kPair ? 2 : min((BN + 127) >> 7, P.nbt - rt);
+                    bytes += sc * (1 + nrt);
+                }
+                tc::mbar_arrive_expect_tx(full, bytes);
+                if (kBmn) {
+                    for (int i = 0; i < BN / 64; ++i) tc::tma_load(sb + i * 8192, tb, T.n0 + 64 * i, kx, full);
+                } else {
+                    tc::tma_load(sb, tb, kx, T.n0, full);
+                    if (kForm == kPair) tc::tma_load(sb + b_bytes / 2, &P.tb[1], kx, T.n0, full);
+                }
+                for (int i = 0; i < nrt; ++i) {
+                    const uint8_t *src = kForm == kPair ? P.sb[i] : P.sb[0];
+                    const int r = kForm == kPair ? rt : rt + i;
+                    tc::bulk_g2s(sb - a_bytes + s_off + 1024 * (1 + i), src + ((size_t)r * P.skb + 2 * k) * kMxTileBytes,
+                                 sc, full);
+                }
+            };
+            int early = 0;
+            if (P.early_b && tile0 < P.tiles) {
+                early = min(P.stages, kb1 - kb0);
+                const Tile T = tile_at<kForm>(P, tile0);
+                for (int i = 0; i < early; ++i) load_b(T, kb0 + i, i);
+            }
+            tc::grid_wait();
+            tc::grid_release();
             for (int t = tile0; t < P.tiles && ok; t += step) {
                 const Tile T = tile_at<kForm>(P, t);
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!tc::mbar_wait(bar_empty + 8 * st, ph ^ 1)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t sa = base + st * stage_bytes, sb = sa + a_bytes, full = bar_full + 8 * st;
-                    const bool second = kForm == kSum && kb >= P.kb_seg;
-                    const int k = second ? kb - P.kb_seg : kb;
-                    const CUtensorMap *ta = &P.ta[kForm == kSum ? (second ? 1 : 0) : T.p];
-                    const CUtensorMap *tb = &P.tb[kForm == kSum ? (second ? 1 : 0) : kForm == kPair ? 0 : T.p];
-                    uint32_t bytes = a_bytes + b_bytes;
-                    uint32_t sc = 0;
-                    int rt = 0, nrt = 0;
-                    if (kKind == kMx4) {
-                        sc = (uint32_t)min(2, P.skb - 2 * k) * kMxTileBytes;
-                        rt = T.n0 >> 7;
-                        nrt = kForm == kPair ? 2 : min((BN + 127) >> 7, P.nbt - rt);
-                        bytes += sc * (1 + nrt);
-                    }
-                    tc::mbar_arrive_expect_tx(full, bytes);
-                    const int kx = kKind == kMx4 ? k * kRowBytes : k * 64;
-                    if (kAmn) {
-                        for (int i = 0; i < kBM / 64; ++i) tc::tma_load(sa + i * 8192, ta, T.m0 + 64 * i, kx, full);
-                    } else {
-                        tc::tma_load(sa, ta, kx, T.m0, full);
-                    }
-                    if (kBmn) {
-                        for (int i = 0; i < BN / 64; ++i) tc::tma_load(sb + i * 8192, tb, T.n0 + 64 * i, kx, full);
-                    } else {
-                        tc::tma_load(sb, tb, kx, T.n0, full);
-                        if (kForm == kPair) tc::tma_load(sb + b_bytes / 2, &P.tb[1], kx, T.n0, full);
-                    }
-                    if (kKind == kMx4) {
-                        const uint32_t ss = sa + s_off;
-                        tc::bulk_g2s(ss, P.sa + ((size_t)(T.m0 >> 7) * P.skb + 2 * k) * kMxTileBytes, sc, full);
-                        for (int i = 0; i < nrt; ++i) {
-                            const uint8_t *src = kForm == kPair ? P.sb[i] : P.sb[0];
-                            const int r = kForm == kPair ? rt : rt + i;
-                            tc::bulk_g2s(ss + 1024 * (1 + i), src + ((size_t)r * P.skb + 2 * k) * kMxTileBytes, sc, full);
+                    if (issued >= early) {
+                        if (!tc::mbar_wait(bar_empty + 8 * st, ph ^ 1)) {
+                            ok = false;
+                            break;
                         }
+                        load_b(T, kb, st);
                     }
+                    load_a(T, kb, st);
                     ++issued;
                     if (++st == P.stages) {
                         st = 0;
                         ph ^= 1;
                     }
+                }
+            }
+            if (P.ahead_bytes) {
+                // this CTA's share, in pieces of 16 KiB
+                const size_t n = (P.ahead_bytes + 16383) >> 14;
+                for (size_t i = blockIdx.x; i < n; i += gridDim.x) {
+                    const size_t left = P.ahead_bytes - (i << 14);
+                    tc::prefetch_l2(P.ahead + (i << 14), left < 16384 ? (uint32_t)left : 16384u);
                 }
             }
             if (!ok) {
@@ -322,18 +379,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             float v[W], w[W];
 #pragma unroll
             for (int j = 0; j < W; ++j) v[j] = w[j] = 0.f;
-            for (int s = 0; s < S; ++s) {
-                const uint32_t src = tc::map_rank(base + (uint32_t)(rr * (BN + 4) + c) * 4, s);
-#pragma unroll
-                for (int j = 0; j < W / 4; ++j) {
-                    const float4 x = tc::ld_cluster(src + 16 * j);
-                    v[4 * j] += x.x, v[4 * j + 1] += x.y, v[4 * j + 2] += x.z, v[4 * j + 3] += x.w;
-                    if (kForm == kPair) {
-                        const float4 y = tc::ld_cluster(src + 4 * cols + 16 * j);
-                        w[4 * j] += y.x, w[4 * j + 1] += y.y, w[4 * j + 2] += y.z, w[4 * j + 3] += y.w;
-                    }
-                }
-            }
+            const uint32_t src = base + (uint32_t)(rr * (BN + 4) + c) * 4;
+            add_ranks<W>(src, S, v);
+            if (kForm == kPair) add_ranks<W>(src + 4 * cols, S, w);
             epi.template row<W>(T.p, T.m0 + rr, T.n0 + c, v, w);
         }
         tc::cluster_sync(); // no CTA leaves while another reads its sums
@@ -473,6 +521,9 @@ struct GatedGrad {
 
 // ---- host side -----------------------------------------------------------------------------
 
+// L2 holds this much of the next kernel's weights beside what is in flight.
+constexpr size_t kAheadMost = 48u << 20;
+
 // A tensor map over rows x row_bytes bytes (contiguous rows): boxes of box_rows rows x 128 bytes,
 // 128-byte swizzle, zeros past the ends.  unit: bytes of one coordinate step (2 or 1).
 cudaError_t make_map(CUtensorMap *m, const void *p, int unit, int rows, size_t row_bytes, int box_rows);
@@ -506,19 +557,23 @@ cudaError_t launch_gemm(GemmArgs &G, const Epi &epi, int sms, cudaStream_t s) {
     const uint32_t smem = kBarBytes + 1024 + G.stages * stage;
     cudaError_t e = ensure_smem(attr, reinterpret_cast<const void *>(kernel), (int)smem);
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute at[1];
+    // The launch may begin while the kernel before it in the stream ends (grid_wait holds back
+    // everything that touches memory): its setup hides behind that kernel's tail.
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(G.S > 1 ? G.tiles * G.S : (G.tiles < sms ? G.tiles : sms));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = at;
-    cfg.numAttrs = 0;
+    cfg.numAttrs = 1;
     if (G.S > 1) {
-        at[0].id = cudaLaunchAttributeClusterDimension;
-        at[0].val.clusterDim.x = G.S;
-        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-        cfg.numAttrs = 1;
+        at[1].id = cudaLaunchAttributeClusterDimension;
+        at[1].val.clusterDim.x = G.S;
+        at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
     }
     return cudaLaunchKernelEx(&cfg, kernel, G, epi);
 }

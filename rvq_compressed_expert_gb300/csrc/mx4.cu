@@ -8,6 +8,7 @@
 // hardware's e2m1 conversions.  A warp keeps its 256 columns and walks down the rows, kRows of
 // them in flight at once to cover the memory's latency.
 #include "dense.cuh"
+#include "dense_tc.cuh"
 
 namespace wm {
 namespace dense {
@@ -79,6 +80,8 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const T *__restrict_
     const int lane = threadIdx.x & 31, kb = (cols + 127) / 128;
     const Walk K = walk(cols);
     const bool in = K.col < cols;
+    tc::grid_wait();
+    tc::grid_release();
     for (int64_t r0 = K.row; r0 < rows; r0 += (int64_t)kRows * K.step) {
         Eight<T> a[kRows];
 #pragma unroll
@@ -127,6 +130,8 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const uint8_t *__r
                                                               T *__restrict__ out, int64_t ld) {
     const int kb = (cols + 127) / 128;
     const Walk K = walk(cols);
+    tc::grid_wait();
+    tc::grid_release();
     if (K.col >= cols) return;
     for (int64_t r0 = K.row; r0 < rows; r0 += (int64_t)kRows * K.step) {
         uint32_t w[kRows];
@@ -167,29 +172,42 @@ int grid_for(int rows, int cols) {
     return (int)(g < least ? least : g);
 }
 
+// A launch that may begin while the kernel before it ends (the kernels wait for it themselves).
+template <class... P, class... A> cudaError_t launch(void (*kernel)(P...), int grid, cudaStream_t s, A... args) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
+template <class T>
+cudaError_t quantize(const void *x, int rows, int cols, int64_t ld, uint8_t *codes, uint8_t *scales, cudaStream_t s) {
+    return launch(quantize_kernel<T>, grid_for(rows, cols), s, static_cast<const T *>(x), rows, cols, ld, codes, scales);
+}
+template <class T> cudaError_t dequantize(const Mx4Mat &m, void *out, int64_t ld, cudaStream_t s) {
+    return launch(dequantize_kernel<T>, grid_for(m.rows, m.cols), s, m.codes, m.scales, m.rows, m.cols,
+                  static_cast<T *>(out), ld);
+}
+
 } // namespace
 
 cudaError_t launch_mx4_quantize(const void *x, int dtype, int rows, int cols, int64_t ld, uint8_t *codes,
                                 uint8_t *scales, cudaStream_t s) {
-    const int g = grid_for(rows, cols);
-    if (dtype == WASTE_ACT_F32)
-        quantize_kernel<<<g, kThreads, 0, s>>>(static_cast<const float *>(x), rows, cols, ld, codes, scales);
-    else if (dtype == WASTE_ACT_BF16)
-        quantize_kernel<<<g, kThreads, 0, s>>>(static_cast<const __nv_bfloat16 *>(x), rows, cols, ld, codes, scales);
-    else
-        quantize_kernel<<<g, kThreads, 0, s>>>(static_cast<const __half *>(x), rows, cols, ld, codes, scales);
-    return cudaGetLastError();
+    return dtype == WASTE_ACT_F32    ? quantize<float>(x, rows, cols, ld, codes, scales, s)
+           : dtype == WASTE_ACT_BF16 ? quantize<__nv_bfloat16>(x, rows, cols, ld, codes, scales, s)
+                                     : quantize<__half>(x, rows, cols, ld, codes, scales, s);
 }
 
 cudaError_t launch_mx4_dequantize(const Mx4Mat &m, void *out, int dtype, int64_t ld, cudaStream_t s) {
-    const int g = grid_for(m.rows, m.cols);
-    if (dtype == WASTE_ACT_F32)
-        dequantize_kernel<<<g, kThreads, 0, s>>>(m.codes, m.scales, m.rows, m.cols, static_cast<float *>(out), ld);
-    else if (dtype == WASTE_ACT_BF16)
-        dequantize_kernel<<<g, kThreads, 0, s>>>(m.codes, m.scales, m.rows, m.cols, static_cast<__nv_bfloat16 *>(out), ld);
-    else
-        dequantize_kernel<<<g, kThreads, 0, s>>>(m.codes, m.scales, m.rows, m.cols, static_cast<__half *>(out), ld);
-    return cudaGetLastError();
+    return dtype == WASTE_ACT_F32    ? dequantize<float>(m, out, ld, s)
+           : dtype == WASTE_ACT_BF16 ? dequantize<__nv_bfloat16>(m, out, ld, s)
+                                     : dequantize<__half>(m, out, ld, s);
 }
 
 } // namespace dense

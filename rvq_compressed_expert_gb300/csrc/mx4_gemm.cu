@@ -53,9 +53,11 @@ GemmArgs common(const Mx4Mat &a, const Mx4Mat &b, bool pair, int sms) {
 
 } // namespace
 
-cudaError_t launch_mx4_matmul(const Mx4Mat &a, const Mx4Mat &b, void *out, int out_dtype, int mode, cudaStream_t s) {
+cudaError_t launch_mx4_matmul(const Mx4Mat &a, const Mx4Mat &b, void *out, int out_dtype, int mode, bool after_own,
+                              cudaStream_t s) {
     const int sms = device_sm_count();
     GemmArgs G = common(a, b, false, sms);
+    G.early_b = after_own;
     cudaError_t e = mx_map(&G.ta[0], a, kBM);
     if (e == cudaSuccess) e = mx_map(&G.tb[0], b, G.BN);
     if (e != cudaSuccess) return e;
@@ -68,11 +70,17 @@ cudaError_t launch_mx4_matmul(const Mx4Mat &a, const Mx4Mat &b, void *out, int o
     return launch_gemm<kMx4, kOne, false, false>(G, st, sms, s);
 }
 
-cudaError_t launch_mx4_gated(const Mx4Mat &x, const Mx4Mat &gate, const Mx4Mat &up, uint8_t *codes, uint8_t *scales,
-                             cudaStream_t s) {
+cudaError_t launch_mx4_gated(const Mx4Mat &x, const Mx4Mat &gate, const Mx4Mat &up, const Mx4Mat &next,
+                             uint8_t *codes, uint8_t *scales, cudaStream_t s) {
     const int sms = device_sm_count();
     GemmArgs G = common(x, gate, true, sms);
     G.sb[1] = up.scales;
+    G.early_b = 1;
+    const size_t bytes = mx_code_bytes(next.rows, next.cols);
+    if (G.S > 1 && bytes <= kAheadMost) {
+        G.ahead = next.codes;
+        G.ahead_bytes = bytes;
+    }
     cudaError_t e = mx_map(&G.ta[0], x, kBM);
     if (e == cudaSuccess) e = mx_map(&G.tb[0], gate, G.BN / 2);
     if (e == cudaSuccess) e = mx_map(&G.tb[1], up, G.BN / 2);
