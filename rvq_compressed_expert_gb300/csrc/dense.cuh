@@ -42,7 +42,18 @@ struct Mx4Mat {
     int rows, cols;
 };
 
+// Calls of at most so many tokens take the kernels that read the weights straight into registers
+// (dense_gemv.cu); their a is fp32 in the workspace.
+constexpr int kGemvTokens = 2;
+constexpr int kMxGemvTokens = 2;
+// Shared memory in which those of 4-bit weights stage nt rows of n quantised values.
+__host__ __device__ inline size_t mx_gemv_smem(int n, int nt) { return (size_t)nt * (n * 2 + (n / 32 + 15) / 16 * 16); }
+constexpr size_t kMxGemvSmem = 48 << 10; // what a kernel may take without asking
+
 cudaError_t launch_ffn_forward(const FfnFwd &P, cudaStream_t s);
+cudaError_t launch_ffn_gemv(const FfnFwd &P, cudaStream_t s);
+cudaError_t launch_mx4_ffn_gemv(const void *x, int x_dtype, int T, const Mx4Mat &gate, const Mx4Mat &up,
+                                const Mx4Mat &down, float *a, void *out, int out_dtype, int mode, cudaStream_t s);
 cudaError_t launch_ffn_backward(const FfnBwd &P, cudaStream_t s);
 cudaError_t launch_mx4_quantize(const void *x, int dtype, int rows, int cols, int64_t ld, uint8_t *codes,
                                 uint8_t *scales, cudaStream_t s);
@@ -86,9 +97,8 @@ __device__ __forceinline__ uint32_t mx_codes8(const float (&v)[8]) {
         : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
     return w;
 }
-// The values of eight codes.
-__device__ __forceinline__ void mx_values8(uint32_t w, float (&v)[8]) {
-    uint32_t h[4];
+// Eight codes as halves (exact).
+__device__ __forceinline__ void mx_halves8(uint32_t w, uint32_t (&h)[4]) {
     asm("{\n\t.reg .b8 a, b, c, d;\n\t"
         "mov.b32 {a, b, c, d}, %4;\n\t"
         "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
@@ -97,6 +107,11 @@ __device__ __forceinline__ void mx_values8(uint32_t w, float (&v)[8]) {
         "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
         : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
         : "r"(w));
+}
+// The values of eight codes.
+__device__ __forceinline__ void mx_values8(uint32_t w, float (&v)[8]) {
+    uint32_t h[4];
+    mx_halves8(w, h);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));

@@ -57,8 +57,12 @@ int check_ffn(const waste_ffn_config *c, int32_t T) {
     return WASTE_OK;
 }
 
-// One [T][f] buffer of the workspace.
-size_t ffn_part(const waste_ffn_config *c, int32_t T) { return round_up((size_t)T * c->f * 2, 256); }
+// One [T][f] buffer of the workspace; a forward call of few tokens keeps fp32 in it, so the size
+// for T tokens also covers every smaller call.
+size_t ffn_part(const waste_ffn_config *c, int32_t T) {
+    const size_t few = T < kGemvTokens ? T : kGemvTokens, half = (size_t)T * c->f * 2, full = few * c->f * 4;
+    return round_up(half > full ? half : full, 256);
+}
 
 int check_mx4_shape(int32_t rows, int32_t cols) {
     if (rows < 0) return fail(WASTE_EINVAL, "rows = %d", rows);
@@ -86,7 +90,7 @@ int check_mx4_ffn(const waste_mx4_ffn_config *c, int32_t T) {
 }
 
 struct Mx4FfnParts {
-    size_t xc, xs, ac, as, total;
+    size_t xc, xs, ac, as, af, total;
 };
 Mx4FfnParts mx4_ffn_parts(const waste_mx4_ffn_config *c, int32_t T) {
     Mx4FfnParts p;
@@ -100,6 +104,8 @@ Mx4FfnParts mx4_ffn_parts(const waste_mx4_ffn_config *c, int32_t T) {
     p.xs = take(mx_scale_bytes(T, c->d));
     p.ac = take(mx_code_bytes(T, c->f));
     p.as = take(mx_scale_bytes(T, c->f));
+    // calls of few tokens keep a in fp32 instead
+    p.af = take((size_t)(T < kMxGemvTokens ? T : kMxGemvTokens) * c->f * 4);
     p.total = at;
     return p;
 }
@@ -279,11 +285,15 @@ int waste_mx4_ffn_forward(const waste_mx4_ffn_config *cfg, const void *d_x, int3
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     uint8_t *w = static_cast<uint8_t *>(d_workspace);
     const int d = cfg->d, f = cfg->f;
-    const Mx4Mat down{cfg->d_down_codes, cfg->d_down_scales, d, f};
+    const Mx4Mat gate{cfg->d_gate_codes, cfg->d_gate_scales, f, d}, up{cfg->d_up_codes, cfg->d_up_scales, f, d},
+        down{cfg->d_down_codes, cfg->d_down_scales, d, f};
+    if (T <= kMxGemvTokens && mx_gemv_smem(d, T) <= kMxGemvSmem && mx_gemv_smem(f, T) <= kMxGemvSmem)
+        return done(launch_mx4_ffn_gemv(d_x, x_dtype, T, gate, up, down, reinterpret_cast<float *>(w + W.af), d_out,
+                                        out_dtype, mode, s),
+                    "4-bit gated feed-forward");
     cudaError_t e = launch_mx4_quantize(d_x, x_dtype, T, d, d, w + W.xc, w + W.xs, s);
     if (e == cudaSuccess)
-        e = launch_mx4_gated(Mx4Mat{w + W.xc, w + W.xs, T, d}, Mx4Mat{cfg->d_gate_codes, cfg->d_gate_scales, f, d},
-                             Mx4Mat{cfg->d_up_codes, cfg->d_up_scales, f, d}, down, w + W.ac, w + W.as, s);
+        e = launch_mx4_gated(Mx4Mat{w + W.xc, w + W.xs, T, d}, gate, up, down, w + W.ac, w + W.as, s);
     if (e == cudaSuccess)
         e = launch_mx4_matmul(Mx4Mat{w + W.ac, w + W.as, T, f}, down, d_out, out_dtype, mode, true, s);
     return done(e, "4-bit gated feed-forward");

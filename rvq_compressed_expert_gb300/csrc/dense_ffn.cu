@@ -24,6 +24,7 @@ cudaError_t half_map(CUtensorMap *m, const void *p, int rows, int cols, int box_
 } // namespace
 
 cudaError_t launch_ffn_forward(const FfnFwd &P, cudaStream_t s) {
+    if (P.T <= kGemvTokens) return launch_ffn_gemv(P, s);
     const int sms = device_sm_count();
     const bool bf16 = P.dtype == WASTE_ACT_BF16;
     cudaError_t e;

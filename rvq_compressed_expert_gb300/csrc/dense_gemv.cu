@@ -1,0 +1,421 @@
+// The gated feed-forward block for a few tokens (decode): the weights are read once, straight
+// into registers, and that reading is all that takes time.
+//
+// Two launches.  gate_up: a warp takes one column f of the block, streams its gate and up rows
+// (16 bytes a lane, several pieces in flight) against the tokens' x, adds across the lanes and
+// writes a = silu(g) u in fp32.  down: a warp takes a few rows of Wd against a.  No shared memory
+// ring, no tensor memory and no sums across CTAs: what bounds both is memory latency times
+// bandwidth, so every SM holds as many loads in flight as its registers allow.  down does not
+// depend on gate_up for its weights: it is launched while gate_up runs and asks for its first rows
+// before it waits for a.  a never leaves fp32, so only the output is rounded.
+//
+// Against the tensor-core path (dense_gemm.cuh), d 7168, f 1536, bf16, weights from memory: one
+// token 19.3 us here and 33.5 there (its launches set up TMA and TMEM and add up over clusters),
+// two 25.7, four 44.0 here and 32.3 there: the multiplications grow with the tokens, so past
+// kGemvTokens the tensor cores take over.  4-bit weights: one 12.4 here and 22.1 there, two 15.0,
+// three 20.6, four 22.8.
+#include "dense.cuh"
+#include "dense_tc.cuh"
+
+namespace wm {
+namespace dense {
+
+namespace {
+
+constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kDownRows = 2;
+
+// streamed once: no place in L1, which keeps x (or a)
+__device__ __forceinline__ uint4 load_stream(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+__device__ __forceinline__ void widen(uint32_t w, float &lo, float &hi, __nv_bfloat16) {
+    lo = __uint_as_float(w << 16);
+    hi = __uint_as_float(w & 0xffff0000u);
+}
+__device__ __forceinline__ void widen(uint32_t w, float &lo, float &hi, __half) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    lo = f.x;
+    hi = f.y;
+}
+template <class T> __device__ __forceinline__ void widen8(const uint4 &q, float (&v)[8]) {
+    widen(q.x, v[0], v[1], T());
+    widen(q.y, v[2], v[3], T());
+    widen(q.z, v[4], v[5], T());
+    widen(q.w, v[6], v[7], T());
+}
+__device__ __forceinline__ float add_lanes(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.f + __expf(-fmaxf(g, -80.f))); }
+
+template <class T> __device__ __forceinline__ T narrow(float v);
+template <> __device__ __forceinline__ float narrow<float>(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <> __device__ __forceinline__ __half narrow<__half>(float v) { return __float2half_rn(v); }
+
+template <class O> __device__ __forceinline__ void put(void *out, size_t at, float v, int add) {
+    O &o = static_cast<O *>(out)[at];
+    o = narrow<O>(add ? (float)o + v : v);
+}
+__device__ __forceinline__ void put_as(int dtype, void *out, size_t at, float v, int add) {
+    if (dtype == WASTE_ACT_F32)
+        put<float>(out, at, v, add);
+    else if (dtype == WASTE_ACT_BF16)
+        put<__nv_bfloat16>(out, at, v, add);
+    else
+        put<__half>(out, at, v, add);
+}
+
+// ---- 16-bit weights --------------------------------------------------------------------------
+
+template <class T, int NT>
+__global__ void __launch_bounds__(kThreads) gate_up_kernel(const T *__restrict__ x, const T *__restrict__ wg,
+                                                           const T *__restrict__ wu, float *__restrict__ a,
+                                                           T *__restrict__ g, T *__restrict__ u, int T_, int d, int f) {
+    constexpr int U = 4; // pieces of each row in flight
+    const int lane = threadIdx.x & 31, col = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    tc::grid_wait();
+    tc::grid_release();
+    if (col >= f) return;
+    const T *pg = wg + (size_t)col * d, *pu = wu + (size_t)col * d;
+    float sg[NT] = {}, su[NT] = {};
+    for (int k0 = lane * 8; k0 < d; k0 += 256 * U) {
+        uint4 qg[U], qu[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int k = k0 + 256 * i;
+            qg[i] = k < d ? load_stream(pg + k) : make_uint4(0, 0, 0, 0);
+            qu[i] = k < d ? load_stream(pu + k) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int k = k0 + 256 * i;
+            if (k >= d) break;
+            float vg[8], vu[8];
+            widen8<T>(qg[i], vg);
+            widen8<T>(qu[i], vu);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                if (t >= T_) break;
+                float vx[8];
+                widen8<T>(__ldg(reinterpret_cast<const uint4 *>(x + (size_t)t * d + k)), vx);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    sg[t] = fmaf(vg[j], vx[j], sg[t]);
+                    su[t] = fmaf(vu[j], vx[j], su[t]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const float cg = add_lanes(sg[t]), cu = add_lanes(su[t]);
+        if (lane == t && t < T_) {
+            const size_t at = (size_t)t * f + col;
+            a[at] = silu(cg) * cu;
+            if (g) {
+                g[at] = narrow<T>(cg);
+                u[at] = narrow<T>(cu);
+            }
+        }
+    }
+}
+
+template <class T, int NT>
+__global__ void __launch_bounds__(kThreads) down_kernel(const float *__restrict__ a, const T *__restrict__ wd, void *out,
+                                                        int out_dtype, int add, int T_, int d, int f) {
+    constexpr int U = 6;
+    const int lane = threadIdx.x & 31, row = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * kDownRows;
+    float s[kDownRows][NT] = {};
+    uint4 q[kDownRows][U];
+    const auto fetch = [&](int k0) {
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+#pragma unroll
+            for (int r = 0; r < kDownRows; ++r) {
+                const int k = k0 + 256 * i;
+                q[r][i] = k < f && row + r < d ? load_stream(wd + (size_t)(row + r) * f + k) : make_uint4(0, 0, 0, 0);
+            }
+    };
+    fetch(lane * 8);
+    tc::grid_wait();
+    tc::grid_release();
+    for (int k0 = lane * 8; k0 < f;) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int k = k0 + 256 * i;
+            if (k >= f) break;
+            float w[kDownRows][8];
+#pragma unroll
+            for (int r = 0; r < kDownRows; ++r) widen8<T>(q[r][i], w[r]);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                if (t >= T_) break;
+                const float4 *p = reinterpret_cast<const float4 *>(a + (size_t)t * f + k);
+                const float4 y = p[0], z = p[1];
+                const float v[8] = {y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
+#pragma unroll
+                for (int r = 0; r < kDownRows; ++r)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) s[r][t] = fmaf(w[r][j], v[j], s[r][t]);
+            }
+        }
+        k0 += 256 * U;
+        if (k0 - lane * 8 < f) fetch(k0);
+    }
+#pragma unroll
+    for (int r = 0; r < kDownRows; ++r)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const float y = add_lanes(s[r][t]);
+            if (lane == r * NT + t && t < T_ && row + r < d) put_as(out_dtype, out, (size_t)t * d + row + r, y, add);
+        }
+}
+static_assert(kDownRows * kGemvTokens <= 32, "a lane for each sum");
+
+template <class... P, class... A> cudaError_t launch(void (*kernel)(P...), int grid, int smem, cudaStream_t s, A... args) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
+template <class T, int NT> cudaError_t forward(const FfnFwd &P, cudaStream_t s) {
+    const cudaError_t e = launch(gate_up_kernel<T, NT>, (P.f + kWarps - 1) / kWarps, 0, s, static_cast<const T *>(P.x),
+                                 static_cast<const T *>(P.wg), static_cast<const T *>(P.wu), static_cast<float *>(P.a),
+                                 static_cast<T *>(P.g), static_cast<T *>(P.u), P.T, P.d, P.f);
+    if (e != cudaSuccess) return e;
+    constexpr int kPer = kWarps * kDownRows;
+    return launch(down_kernel<T, NT>, (P.d + kPer - 1) / kPer, 0, s, static_cast<const float *>(P.a),
+                  static_cast<const T *>(P.wd), P.out, P.out_dtype, P.mode, P.T, P.d, P.f);
+}
+template <class T> cudaError_t forward_any(const FfnFwd &P, cudaStream_t s) {
+    return P.T == 1 ? forward<T, 1>(P, s) : forward<T, 2>(P, s);
+}
+
+// ---- microscaled 4-bit weights ---------------------------------------------------------------
+// The same two launches.  x (then a) is quantised by every CTA for itself into shared memory --
+// a few thousand values, less than one launch's latency -- as the halves its codes stand for and
+// the blocks' exponents.  A lane takes whole blocks of 32: the products of two E2M1 values are
+// multiples of 1/4 up to 36, so eight of them add up exactly in an fp16 lane; a block's sum is
+// exact and meets its two powers of two in fp32.
+
+constexpr int kMxDownRows = 4;
+
+// A staged row: 16-byte piece j of block b at (j * nb + b), then the scale bytes (mx_gemv_smem).
+
+template <class T> __device__ __forceinline__ void block_of(const T *p, float (&v)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32 * (int)sizeof(T) / 16; ++i) {
+        const uint4 q = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+        if constexpr (sizeof(T) == 4) {
+            v[4 * i] = __uint_as_float(q.x), v[4 * i + 1] = __uint_as_float(q.y);
+            v[4 * i + 2] = __uint_as_float(q.z), v[4 * i + 3] = __uint_as_float(q.w);
+        } else {
+            widen(q.x, v[8 * i], v[8 * i + 1], T());
+            widen(q.y, v[8 * i + 2], v[8 * i + 3], T());
+            widen(q.z, v[8 * i + 4], v[8 * i + 5], T());
+            widen(q.w, v[8 * i + 6], v[8 * i + 7], T());
+        }
+    }
+}
+template <class T> __device__ __forceinline__ void stage(const T *x, int T_, int n, uint8_t *smem) {
+    const int nb = n / 32;
+    for (int i = threadIdx.x; i < T_ * nb; i += kThreads) {
+        const int t = i / nb, b = i - t * nb;
+        uint8_t *base = smem + t * mx_gemv_smem(n, 1);
+        float v[32];
+        block_of(x + (size_t)t * n + b * 32, v);
+        uint32_t w[4];
+        base[n * 2 + b] = mx_quantize(v, w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t h[4];
+            mx_halves8(w[j], h);
+            reinterpret_cast<uint4 *>(base)[j * nb + b] = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+    }
+    __syncthreads();
+}
+// Sum of the 32 products of a weight block and a staged block, exact.
+__device__ __forceinline__ float dot32(const uint4 &codes, const uint8_t *base, int nb, int b) {
+    float s = 0.f;
+    const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        __half2 acc = __float2half2_rn(0.f);
+#pragma unroll
+        for (int j = 2 * p; j < 2 * p + 2; ++j) {
+            uint32_t h[4];
+            mx_halves8(w[j], h);
+            const uint4 q = reinterpret_cast<const uint4 *>(base)[j * nb + b];
+            const uint32_t y[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                acc = __hfma2(*reinterpret_cast<const __half2 *>(&h[i]), *reinterpret_cast<const __half2 *>(&y[i]), acc);
+        }
+        const float2 f = __half22float2(acc);
+        s += f.x + f.y;
+    }
+    return s;
+}
+// v 2^(a + b - 254) for two scale bytes, in two steps that stay in range; NaN for byte 255.
+__device__ __forceinline__ float scaled(float v, uint32_t a, uint32_t b) {
+    const int e = (int)(a + b) - 254, h = e >> 1;
+    const float p = __uint_as_float((uint32_t)max(h + 127, 1) << 23);
+    const float q = __uint_as_float((uint32_t)max(e - h + 127, 1) << 23);
+    v = v * p * q;
+    return a == 255u || b == 255u ? __uint_as_float(0x7fc00000u) : v;
+}
+
+template <class T, int NT>
+__global__ void __launch_bounds__(kThreads) mx_gate_up_kernel(const T *__restrict__ x, Mx4Mat wg, Mx4Mat wu,
+                                                              float *__restrict__ a, int T_) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    constexpr int U = 4;
+    const int d = wg.cols, f = wg.rows, nb = d / 32, kb = (d + 127) / 128;
+    const int lane = threadIdx.x & 31, col = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    tc::grid_wait();
+    tc::grid_release();
+    uint4 q[2][U];
+    uint32_t sc[2][U];
+    const auto fetch = [&](int b0) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int b = b0 + 32 * i;
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const Mx4Mat &W = m ? wu : wg;
+                const bool in = b < nb && col < f;
+                q[m][i] = in ? load_stream(W.codes + (size_t)col * (d / 2) + b * 16) : make_uint4(0, 0, 0, 0);
+                sc[m][i] = in ? __ldg(W.scales + mx_scale_at(col, b, kb)) : 0;
+            }
+        }
+    };
+    fetch(lane); // the first rows are on their way while x is quantised
+    stage(x, T_, d, smem);
+    if (col >= f) return;
+    float sg[NT] = {}, su[NT] = {};
+    for (int b0 = lane; b0 < nb;) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int b = b0 + 32 * i;
+            if (b >= nb) break;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                if (t >= T_) break;
+                const uint8_t *base = smem + t * mx_gemv_smem(d, 1);
+                const uint32_t sx = base[d * 2 + b];
+                sg[t] += scaled(dot32(q[0][i], base, nb, b), sx, sc[0][i]);
+                su[t] += scaled(dot32(q[1][i], base, nb, b), sx, sc[1][i]);
+            }
+        }
+        b0 += 32 * U;
+        if (b0 - lane < nb) fetch(b0);
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const float cg = add_lanes(sg[t]), cu = add_lanes(su[t]);
+        if (lane == t && t < T_) a[(size_t)t * f + col] = silu(cg) * cu;
+    }
+}
+
+template <int NT>
+__global__ void __launch_bounds__(kThreads) mx_down_kernel(const float *__restrict__ a, Mx4Mat wd, void *out,
+                                                           int out_dtype, int add, int T_) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    constexpr int U = 2;
+    const int f = wd.cols, d = wd.rows, nb = f / 32, kb = (f + 127) / 128;
+    const int lane = threadIdx.x & 31, row = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * kMxDownRows;
+    uint4 q[kMxDownRows][U];
+    uint32_t sc[kMxDownRows][U];
+    const auto fetch = [&](int b0) {
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+#pragma unroll
+            for (int r = 0; r < kMxDownRows; ++r) {
+                const int b = b0 + 32 * i;
+                const bool in = b < nb && row + r < d;
+                q[r][i] = in ? load_stream(wd.codes + (size_t)(row + r) * (f / 2) + b * 16) : make_uint4(0, 0, 0, 0);
+                sc[r][i] = in ? __ldg(wd.scales + mx_scale_at(row + r, b, kb)) : 0;
+            }
+    };
+    fetch(lane);
+    tc::grid_wait();
+    tc::grid_release();
+    stage(a, T_, f, smem);
+    float s[kMxDownRows][NT] = {};
+    for (int b0 = lane; b0 < nb;) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int b = b0 + 32 * i;
+            if (b >= nb) break;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                if (t >= T_) break;
+                const uint8_t *base = smem + t * mx_gemv_smem(f, 1);
+                const uint32_t sx = base[f * 2 + b];
+#pragma unroll
+                for (int r = 0; r < kMxDownRows; ++r) s[r][t] += scaled(dot32(q[r][i], base, nb, b), sx, sc[r][i]);
+            }
+        }
+        b0 += 32 * U;
+        if (b0 - lane < nb) fetch(b0);
+    }
+#pragma unroll
+    for (int r = 0; r < kMxDownRows; ++r)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const float y = add_lanes(s[r][t]);
+            if (lane == r * NT + t && t < T_ && row + r < d) put_as(out_dtype, out, (size_t)t * d + row + r, y, add);
+        }
+}
+static_assert(kMxDownRows * kMxGemvTokens <= 32, "a lane for each sum");
+
+template <class T, int NT>
+cudaError_t mx_forward(const T *x, int T_, const Mx4Mat &gate, const Mx4Mat &up, const Mx4Mat &down, float *a, void *out,
+                       int out_dtype, int mode, cudaStream_t s) {
+    cudaError_t e = launch(mx_gate_up_kernel<T, NT>, (gate.rows + kWarps - 1) / kWarps, (int)mx_gemv_smem(gate.cols, T_), s,
+                           x, gate, up, a, T_);
+    if (e != cudaSuccess) return e;
+    constexpr int kPer = kWarps * kMxDownRows;
+    return launch(mx_down_kernel<NT>, (down.rows + kPer - 1) / kPer, (int)mx_gemv_smem(down.cols, T_), s,
+                  static_cast<const float *>(a), down, out, out_dtype, mode, T_);
+}
+template <class T>
+cudaError_t mx_forward_any(const void *x, int T_, const Mx4Mat &gate, const Mx4Mat &up, const Mx4Mat &down, float *a,
+                           void *out, int out_dtype, int mode, cudaStream_t s) {
+    const T *p = static_cast<const T *>(x);
+    return T_ == 1 ? mx_forward<T, 1>(p, T_, gate, up, down, a, out, out_dtype, mode, s)
+                   : mx_forward<T, 2>(p, T_, gate, up, down, a, out, out_dtype, mode, s);
+}
+
+} // namespace
+
+cudaError_t launch_ffn_gemv(const FfnFwd &P, cudaStream_t s) {
+    return P.dtype == WASTE_ACT_BF16 ? forward_any<__nv_bfloat16>(P, s) : forward_any<__half>(P, s);
+}
+
+cudaError_t launch_mx4_ffn_gemv(const void *x, int x_dtype, int T, const Mx4Mat &gate, const Mx4Mat &up,
+                                const Mx4Mat &down, float *a, void *out, int out_dtype, int mode, cudaStream_t s) {
+    return x_dtype == WASTE_ACT_F32    ? mx_forward_any<float>(x, T, gate, up, down, a, out, out_dtype, mode, s)
+           : x_dtype == WASTE_ACT_BF16 ? mx_forward_any<__nv_bfloat16>(x, T, gate, up, down, a, out, out_dtype, mode, s)
+                                       : mx_forward_any<__half>(x, T, gate, up, down, a, out, out_dtype, mode, s);
+}
+
+} // namespace dense
+} // namespace wm

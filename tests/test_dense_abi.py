@@ -54,8 +54,12 @@ def cfg(d=64, f=32, dtype=B.ACT_BF16, abi=B.ABI_VERSION):
 
 def test_workspace_sizes():
     assert B.waste_ffn_workspace(cfg(64, 32), 0) == 0
-    assert B.waste_ffn_workspace(cfg(64, 32), 4) == 256
-    assert B.waste_ffn_workspace(cfg(64, 32), 5, 1) == 3 * 512
+    assert B.waste_ffn_workspace(cfg(64, 32), 1) == 256
+    # a call of T tokens may be followed by one of fewer in the same workspace
+    for f in (8, 32, 1536):
+        for back in (0, 1):
+            n = [B.waste_ffn_workspace(cfg(64, f), T, back) for T in range(1, 40)]
+            assert n == sorted(n) and all(v >= T * f * 2 * (3 if back else 1) and v % 256 == 0 for T, v in enumerate(n, 1))
     # past 32 bits
     assert B.waste_ffn_workspace(cfg(8, 1 << 20), 1 << 16) == 1 << 37
     assert B.waste_mx4_layout(0, 32) == (0, 0)

@@ -51,7 +51,7 @@ def guarded(*shape, dtype, fill=7.0):
 
 
 # d and f of one core matrix, below and past a tile, of no round number, and of the workloads
-SHAPES = [(1, 8, 8), (2, 64, 24), (3, 256, 128), (33, 136, 264), (127, 1032, 136), (128, 512, 520), (129, 72, 1544),
+SHAPES = [(1, 8, 8), (1, 1032, 1544), (2, 64, 24), (3, 256, 128), (5, 264, 1800), (8, 2056, 136), (9, 520, 136), (33, 136, 264), (127, 1032, 136), (128, 512, 520), (129, 72, 1544),
           (200, 1032, 264), (257, 264, 1032), (511, 648, 392)]
 
 
@@ -397,7 +397,7 @@ def mx4_block(x, W, t_out):
 
 
 @pytest.mark.parametrize("tx,to", [(FP, FP), (BF, BF), (HF, FP)])
-@pytest.mark.parametrize("T,d,f", [(1, 32, 32), (1, 1056, 160), (5, 256, 128), (130, 288, 416), (260, 512, 352)])
+@pytest.mark.parametrize("T,d,f", [(1, 32, 32), (1, 4128, 160), (2, 160, 2080), (3, 288, 96), (4, 1056, 160), (5, 256, 128), (8, 6176, 1056), (130, 288, 416), (260, 512, 352)])
 def test_mx4_expert(T, d, f, tx, to):
     g = gen(T + d + f)
     W = weights(g, d, f, BF)
