@@ -33,14 +33,11 @@ cudaError_t launch_ffn_forward(const FfnFwd &P, cudaStream_t s) {
         G.K = P.d;
         G.kb = G.kb_seg = pieces(P.d);
         const Plan L = plan(&P.T, &P.f, 1, G.kb, true, false, sms);
-        G.BN = L.BN;
-        G.S = L.S;
-        G.nacc = 2;
-        set_problems(G, &P.T, &P.f, 1, true);
-        G.idesc = tc::idesc_half(kBM, G.BN, bf16, false, false);
+        set_shape(G, L, &P.T, &P.f, 1, true);
+        G.idesc = tc::idesc_half(kBM * L.cg, G.BN, bf16, false, false);
         if ((e = half_map(&G.ta[0], P.x, P.T, P.d, kBM)) != cudaSuccess) return e;
-        if ((e = half_map(&G.tb[0], P.wg, P.f, P.d, G.BN / 2)) != cudaSuccess) return e;
-        if ((e = half_map(&G.tb[1], P.wu, P.f, P.d, G.BN / 2)) != cudaSuccess) return e;
+        if ((e = half_map(&G.tb[0], P.wg, P.f, P.d, box_rows_b(L, true))) != cudaSuccess) return e;
+        if ((e = half_map(&G.tb[1], P.wu, P.f, P.d, box_rows_b(L, true))) != cudaSuccess) return e;
         // few tiles: bound by the weights' way from memory, which the next kernel's can follow
         // at once while this one adds up and ends
         const size_t wd = (size_t)P.d * P.f * 2;
@@ -48,20 +45,17 @@ cudaError_t launch_ffn_forward(const FfnFwd &P, cudaStream_t s) {
             G.ahead = static_cast<const uint8_t *>(P.wd);
             G.ahead_bytes = wd;
         }
-        e = launch_gemm<kHalf, kPair, false, false>(G, Gated{P.a, P.g, P.u, P.f, P.dtype}, sms, s);
+        e = launch_gemm<kHalf, kPair, false, false>(G, L, Gated{P.a, P.g, P.u, P.f, P.dtype}, sms, s);
         if (e != cudaSuccess) return e;
     }
     GemmArgs G = {};
     G.K = P.f;
     G.kb = G.kb_seg = pieces(P.f);
     const Plan L = plan(&P.T, &P.d, 1, G.kb, false, false, sms);
-    G.BN = L.BN;
-    G.S = L.S;
-    G.nacc = 2;
-    set_problems(G, &P.T, &P.d, 1, false);
-    G.idesc = tc::idesc_half(kBM, G.BN, bf16, false, false);
+    set_shape(G, L, &P.T, &P.d, 1, false);
+    G.idesc = tc::idesc_half(kBM * L.cg, G.BN, bf16, false, false);
     if ((e = half_map(&G.ta[0], P.a, P.T, P.f, kBM)) != cudaSuccess) return e;
-    if ((e = half_map(&G.tb[0], P.wd, P.d, P.f, G.BN)) != cudaSuccess) return e;
+    if ((e = half_map(&G.tb[0], P.wd, P.d, P.f, box_rows_b(L, false))) != cudaSuccess) return e;
     G.early_b = 1;
     Store st = {};
     st.out[0] = P.out;
@@ -69,7 +63,7 @@ cudaError_t launch_ffn_forward(const FfnFwd &P, cudaStream_t s) {
     st.dtype = P.out_dtype;
     st.add = P.mode;
     st.vec = 1; // d % 8 == 0
-    return launch_gemm<kHalf, kOne, false, false>(G, st, sms, s);
+    return launch_gemm<kHalf, kOne, false, false>(G, L, st, sms, s);
 }
 
 cudaError_t launch_ffn_backward(const FfnBwd &P, cudaStream_t s) {
@@ -81,14 +75,11 @@ cudaError_t launch_ffn_backward(const FfnBwd &P, cudaStream_t s) {
         G.K = P.d;
         G.kb = G.kb_seg = pieces(P.d);
         const Plan L = plan(&P.T, &P.f, 1, G.kb, false, false, sms);
-        G.BN = L.BN;
-        G.S = L.S;
-        G.nacc = 2;
-        set_problems(G, &P.T, &P.f, 1, false);
-        G.idesc = tc::idesc_half(kBM, G.BN, bf16, false, true);
+        set_shape(G, L, &P.T, &P.f, 1, false);
+        G.idesc = tc::idesc_half(kBM * L.cg, G.BN, bf16, false, true);
         if ((e = half_map(&G.ta[0], P.dy, P.T, P.d, kBM)) != cudaSuccess) return e;
         if ((e = half_map(&G.tb[0], P.wd, P.d, P.f, 64)) != cudaSuccess) return e;
-        e = launch_gemm<kHalf, kOne, false, true>(G, GatedGrad{P.g, P.u, P.a, P.dg, P.du, P.f, P.dtype}, sms, s);
+        e = launch_gemm<kHalf, kOne, false, true>(G, L, GatedGrad{P.g, P.u, P.a, P.dg, P.du, P.f, P.dtype}, sms, s);
         if (e != cudaSuccess) return e;
     }
     if (P.dx) {
@@ -97,11 +88,8 @@ cudaError_t launch_ffn_backward(const FfnBwd &P, cudaStream_t s) {
         G.kb_seg = pieces(P.f);
         G.kb = 2 * G.kb_seg;
         const Plan L = plan(&P.T, &P.d, 1, G.kb, false, false, sms);
-        G.BN = L.BN;
-        G.S = L.S;
-        G.nacc = 2;
-        set_problems(G, &P.T, &P.d, 1, false);
-        G.idesc = tc::idesc_half(kBM, G.BN, bf16, false, true);
+        set_shape(G, L, &P.T, &P.d, 1, false);
+        G.idesc = tc::idesc_half(kBM * L.cg, G.BN, bf16, false, true);
         const void *a[2] = {P.dg, P.du}, *b[2] = {P.wg, P.wu};
         for (int i = 0; i < 2; ++i) {
             if ((e = half_map(&G.ta[i], a[i], P.T, P.f, kBM)) != cudaSuccess) return e;
@@ -113,7 +101,7 @@ cudaError_t launch_ffn_backward(const FfnBwd &P, cudaStream_t s) {
         st.ld[0] = P.d;
         st.dtype = P.dtype;
         st.vec = 1;
-        e = launch_gemm<kHalf, kSum, false, true>(G, st, sms, s);
+        e = launch_gemm<kHalf, kSum, false, true>(G, L, st, sms, s);
         if (e != cudaSuccess) return e;
     }
     if (!P.dwg) return cudaSuccess;
@@ -122,11 +110,8 @@ cudaError_t launch_ffn_backward(const FfnBwd &P, cudaStream_t s) {
     G.K = P.T;
     G.kb = G.kb_seg = pieces(P.T);
     const Plan L = plan(M, N, 3, G.kb, false, false, sms);
-    G.BN = L.BN;
-    G.S = L.S;
-    G.nacc = 2;
-    set_problems(G, M, N, 3, false);
-    G.idesc = tc::idesc_half(kBM, G.BN, bf16, true, true);
+    set_shape(G, L, M, N, 3, false);
+    G.idesc = tc::idesc_half(kBM * L.cg, G.BN, bf16, true, true);
     const void *a[3] = {P.dg, P.du, P.dy}, *b[3] = {P.x, P.x, P.a};
     void *out[3] = {P.dwg, P.dwu, P.dwd};
     Store st = {};
@@ -139,7 +124,7 @@ cudaError_t launch_ffn_backward(const FfnBwd &P, cudaStream_t s) {
     st.dtype = P.grad_dtype;
     st.add = P.accumulate;
     st.vec = 1;
-    return launch_gemm<kHalf, kOne, true, true>(G, st, sms, s);
+    return launch_gemm<kHalf, kOne, true, true>(G, L, st, sms, s);
 }
 
 cudaError_t ffn_timeout(uint32_t *out) { return read_and_clear_timeout(out); }

@@ -1,14 +1,16 @@
 // The tensor-core product of the dense operators: D[m][n] = sum_k A[m][k] B[n][k] in fp32, on
 // tcgen05.mma, with an epilogue that takes the sums on their way out.
 //
-// A CTA makes 128 x BN tiles (BN <= 256).  One thread moves 128-byte-wide pieces of A and B (64
+// A CTA makes 128 x BN tiles (BN <= 256), or two CTAs together 256 x BN ones (cg = 2: each loads 128
+// rows of A and half of B, and the tensor cores of both read both halves, so a tile needs two
+// thirds of the bytes at BN = 256).  One thread moves 128-byte-wide pieces of A and B (64
 // 16-bit or 256 4-bit values of k) into a ring of shared-memory stages by TMA; one thread issues
 // the MMAs on full stages into one of two TMEM accumulators; four warps take the other one out
 // through the epilogue meanwhile.  Rows, columns and k past the matrices' ends arrive as zeros
 // (TMA's fill), so any size works; the epilogue leaves them out.
 //
 // Two launch shapes (plan(), below):
-//   S = 1: a persistent grid, one CTA per SM, each taking every gridDim-th tile.
+//   S = 1: a persistent grid, one CTA per SM, each (or each pair) taking every so-manieth tile.
 //   S > 1: where there are few tiles, a cluster of S CTAs per tile, each with its share of k; the
 //          partial sums meet through distributed shared memory, each CTA adding up its share of
 //          the tile in rank order (the same bits every time) and running the epilogue on it.
@@ -42,16 +44,14 @@ struct Prob {
 };
 struct GemmArgs {
     CUtensorMap ta[kMaxProb], tb[kMaxProb];
+    CUtensorMap sa, sb[2]; // 4-bit operands: their scale tiles, [row tile * skb + tile of blocks]
     Prob prob[kMaxProb];
     int nprob, tiles;
     int BN, S, stages, nacc;
     int kb_seg; // k pieces of one product
     int kb;     // k pieces in all (kSum: twice kb_seg)
-    int K;
+    int K, skb;
     uint32_t idesc;
-    // scale tiles of 4-bit operands: [row tile][skb] of 512 bytes
-    const uint8_t *sa, *sb[2];
-    int skb, nbt;
     // early_b: B does not come from the kernel before this one, so its first pieces are asked for
     // before waiting for that kernel
     int early_b;
@@ -60,12 +60,20 @@ struct GemmArgs {
     size_t ahead_bytes;
 };
 
-__device__ __forceinline__ int stage_scale_bytes(int BN) { return 1024 * (1 + (BN + 127) / 128); }
+// Bytes of a stage in one CTA: 128 rows of A, its rows of B, the scale tiles of both.
+__host__ __device__ inline uint32_t stage_b_bytes(int BN, int cg, bool b_mn) {
+    const int rows = BN / cg;
+    return (uint32_t)(b_mn ? (rows + 63) / 64 * 64 : rows) * kRowBytes;
+}
+__host__ __device__ inline uint32_t stage_size(int BN, int cg, bool b_mn, bool mx4) {
+    const uint32_t n = kBM * kRowBytes + stage_b_bytes(BN, cg, b_mn) + (mx4 ? 1024u * (1 + (BN + 127) / 128) : 0u);
+    return (n + 1023) & ~1023u;
+}
 
 struct Tile {
     int p, m0, n0, rows; // n0: first column of b0 (kPair: of both)
 };
-template <int kForm> __device__ __forceinline__ Tile tile_at(const GemmArgs &P, int t) {
+template <int kForm, int kCG> __device__ __forceinline__ Tile tile_at(const GemmArgs &P, int t, int rank) {
     int p = 0;
     if (kForm == kOne)
         while (p + 1 < P.nprob && t >= P.prob[p + 1].begin) ++p;
@@ -73,12 +81,13 @@ template <int kForm> __device__ __forceinline__ Tile tile_at(const GemmArgs &P, 
     t -= Q.begin;
     // groups of 16 row tiles, columns moving slowest inside a group: the tiles in flight share
     // their operands in L2
-    const int per = 16 * Q.tn, g = t / per, first = g * 16, gm = min(16, Q.tm - first), r = t - g * per;
+    constexpr int kGroup = 16 / kCG;
+    const int per = kGroup * Q.tn, g = t / per, first = g * kGroup, gm = min(kGroup, Q.tm - first), r = t - g * per;
     Tile o;
     o.p = p;
-    o.m0 = (first + r % gm) * kBM;
+    o.m0 = (first + r % gm) * kBM * kCG + (kCG == 2 ? rank * kBM : 0);
     o.n0 = (r / gm) * (kForm == kPair ? P.BN / 2 : P.BN);
-    o.rows = min(kBM, Q.M - o.m0);
+    o.rows = min(kBM, Q.M - o.m0); // none (or fewer) in a pair's second CTA
     return o;
 }
 
@@ -116,7 +125,33 @@ template <int W> __device__ __forceinline__ void add_ranks(uint32_t src, int S, 
     }
 }
 
-template <int kKind, int kForm, bool kAmn, bool kBmn, class Epi>
+// W columns of a row from tensor memory through the epilogue (or, split: to the partial sums).
+template <int W, int kForm, class Epi>
+__device__ __forceinline__ void take(const Epi &epi, const Tile &T, uint32_t src, int cols, int r, int c, float4 *part) {
+    uint32_t v[W], w[W];
+    if constexpr (W == 32) {
+        tc::tmem_ld32(src + c, v);
+        if (kForm == kPair) tc::tmem_ld32(src + cols + c, w);
+    } else {
+        tc::tmem_ld16n(src + c, v);
+        if (kForm == kPair) tc::tmem_ld16n(src + cols + c, w);
+    }
+    tc::tmem_wait_ld(v);
+    if (kForm == kPair) tc::tmem_wait_ld(w);
+    if (r >= T.rows) return;
+    if (part) {
+#pragma unroll
+        for (int i = 0; i < W / 4; ++i) {
+            part[c / 4 + i] = *reinterpret_cast<float4 *>(&v[4 * i]);
+            if (kForm == kPair) part[(cols + c) / 4 + i] = *reinterpret_cast<float4 *>(&w[4 * i]);
+        }
+    } else {
+        epi.template row<W>(T.p, T.m0 + r, T.n0 + c, *reinterpret_cast<float(*)[W]>(v),
+                            *reinterpret_cast<float(*)[W]>(kForm == kPair ? w : v));
+    }
+}
+
+template <int kCG, int kKind, int kForm, bool kAmn, bool kBmn, class Epi>
 __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs P, const Epi epi) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t smem0 = tc::smem_u32(smem_raw);
@@ -128,10 +163,12 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     const uint32_t drain = bars + 168;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int BN = P.BN, S = P.S;
-    const uint32_t a_bytes = kBM * kRowBytes, b_bytes = (uint32_t)BN * kRowBytes;
-    const uint32_t s_off = a_bytes + b_bytes;
-    const uint32_t stage_bytes = (s_off + (kKind == kMx4 ? stage_scale_bytes(BN) : 0) + 1023) & ~1023u;
+    const int BN = P.BN, S = kCG == 2 ? 1 : P.S;
+    const uint32_t a_bytes = kBM * kRowBytes, b_bytes = stage_b_bytes(BN, kCG, kBmn);
+    const uint32_t s_off = a_bytes + b_bytes, stage_bytes = stage_size(BN, kCG, kBmn, kKind == kMx4);
+    const int nrt = (BN + 127) >> 7; // scale tiles of B
+    const int rank = kCG == 2 || S > 1 ? (int)tc::cluster_rank() : 0;
+    const bool leads = kCG == 1 || rank == 0; // issues the MMAs
 
     if (tid == 0) {
         for (int i = 0; i < P.stages; ++i) {
@@ -140,85 +177,91 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(bar_accf + 8 * i, 1);
-            tc::mbar_init(bar_acce + 8 * i, 4);
+            tc::mbar_init(bar_acce + 8 * i, 4 * kCG);
         }
         tc::mbar_init(drain, 1);
         *abort_flag = 0;
         tc::mbar_init_fence();
     }
-    if (warp == 2) tc::tmem_alloc(tc::smem_u32(tmem_slot), kTmemCols);
+    if (warp == 2) {
+        if (kCG == 2)
+            tc::tmem_alloc_pair(tc::smem_u32(tmem_slot), kTmemCols);
+        else
+            tc::tmem_alloc(tc::smem_u32(tmem_slot), kTmemCols);
+    }
     tc::fence_before_sync();
     __syncthreads();
+    if (kCG == 2) tc::cluster_sync(); // the other CTA's barriers are up
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     if (warp != 0) tc::grid_wait(); // warp 0's loader may have B's first pieces to ask for before
 
-    const int rank = S > 1 ? (int)tc::cluster_rank() : 0;
     const int kb0 = S > 1 ? (int)((long long)P.kb * rank / S) : 0;
     const int kb1 = S > 1 ? (int)((long long)P.kb * (rank + 1) / S) : P.kb;
-    const int tile0 = S > 1 ? (int)blockIdx.x / S : (int)blockIdx.x;
-    const int step = S > 1 ? P.tiles : (int)gridDim.x;
+    const int tile0 = S > 1 ? (int)blockIdx.x / S : (int)blockIdx.x / kCG;
+    const int step = S > 1 ? P.tiles : (int)gridDim.x / kCG;
+    const auto acc_at = [&](int buf) { return tmem + buf * (kKind == kMx4 ? BN : 256); };
 
     if (warp == 0) {
         if (lane == 0) {
-            // ---- producer
+            // ---- loader.  A pair's CTAs load their own rows of A and their half of B; the bytes
+            // of both count on the first one's barrier, which announces them.
             int st = 0, issued = 0;
             uint32_t ph = 0;
             bool ok = true;
+            const uint32_t full0 = kCG == 2 ? tc::map_rank(bar_full, 0) : bar_full;
+            const auto load = [](uint32_t dst, const CUtensorMap *m, int x, int y, uint32_t bar) {
+                if (kCG == 2)
+                    tc::tma_load_pair(dst, m, x, y, bar);
+                else
+                    tc::tma_load(dst, m, x, y, bar);
+            };
             const auto load_a = [&](const Tile &T, int kb, int st) {
-                const uint32_t sa = base + st * stage_bytes, full = bar_full + 8 * st;
+                const uint32_t sa = base + st * stage_bytes, full = full0 + 8 * st;
                 const bool second = kForm == kSum && kb >= P.kb_seg;
                 const int k = second ? kb - P.kb_seg : kb;
                 const CUtensorMap *ta = &P.ta[kForm == kSum ? (second ? 1 : 0) : T.p];
                 const int kx = kKind == kMx4 ? k * kRowBytes : k * 64;
                 if (kAmn) {
-                    for (int i = 0; i < kBM / 64; ++i) tc::tma_load(sa + i * 8192, ta, T.m0 + 64 * i, kx, full);
+                    for (int i = 0; i < kBM / 64; ++i) load(sa + i * 8192, ta, T.m0 + 64 * i, kx, full);
                 } else {
-                    tc::tma_load(sa, ta, kx, T.m0, full);
+                    load(sa, ta, kx, T.m0, full);
                 }
-                if (kKind == kMx4)
-                    tc::bulk_g2s(sa + s_off, P.sa + ((size_t)(T.m0 >> 7) * P.skb + 2 * k) * kMxTileBytes,
-                                 (uint32_t)min(2, P.skb - 2 * k) * kMxTileBytes, full);
+                if (kKind == kMx4) load(sa + s_off, &P.sa, 0, (T.m0 >> 7) * P.skb + 2 * k, full);
             };
             // also announces the bytes of the whole stage
             const auto load_b = [&](const Tile &T, int kb, int st) {
-                const uint32_t sb = base + st * stage_bytes + a_bytes, full = bar_full + 8 * st;
+                const uint32_t sb = base + st * stage_bytes + a_bytes, full = full0 + 8 * st;
                 const bool second = kForm == kSum && kb >= P.kb_seg;
                 const int k = second ? kb - P.kb_seg : kb;
-                const CUtensorMap *tb = &P.tb[kForm == kSum ? (second ? 1 : 0) : kForm == kPair ? 0 : T.p];
+                const CUtensorMap *tb =
+                    &P.tb[kForm == kSum ? (second ? 1 : 0) : kForm == kPair ? (kCG == 2 ? rank : 0) : T.p];
                 const int kx = kKind == kMx4 ? k * kRowBytes : k * 64;
-                uint32_t bytes = a_bytes + b_bytes, sc = 0;
-                int rt = 0, nrt = 0;
-                if (kKind == kMx4) {
-                    sc = (uint32_t)min(2, P.skb - 2 * k) * kMxTileBytes;
-                    rt = T.n0 >> 7;
-                    nrt = kForm == kPair ? 2 : min((BN + 127) >> 7, P.nbt - rt);
-                    bytes += sc * (1 + nrt);
-                }
-                tc::mbar_arrive_expect_tx(full, bytes);
+                const int n0 = T.n0 + (kCG == 2 && kForm != kPair ? rank * (BN / 2) : 0);
+                if (leads)
+                    tc::mbar_arrive_expect_tx(bar_full + 8 * st,
+                                              kCG * (a_bytes + b_bytes + (kKind == kMx4 ? 1024u * (1 + nrt) : 0u)));
                 if (kBmn) {
-                    for (int i = 0; i < BN / 64; ++i) tc::tma_load(sb + i * 8192, tb, T.n0 + 64 * i, kx, full);
+                    for (uint32_t i = 0; i * 8192 < b_bytes; ++i) load(sb + i * 8192, tb, n0 + 64 * i, kx, full);
                 } else {
-                    tc::tma_load(sb, tb, kx, T.n0, full);
-                    if (kForm == kPair) tc::tma_load(sb + b_bytes / 2, &P.tb[1], kx, T.n0, full);
+                    load(sb, tb, kx, n0, full);
+                    if (kForm == kPair && kCG == 1) load(sb + b_bytes / 2, &P.tb[1], kx, n0, full);
                 }
-                for (int i = 0; i < nrt; ++i) {
-                    const uint8_t *src = kForm == kPair ? P.sb[i] : P.sb[0];
-                    const int r = kForm == kPair ? rt : rt + i;
-                    tc::bulk_g2s(sb - a_bytes + s_off + 1024 * (1 + i), src + ((size_t)r * P.skb + 2 * k) * kMxTileBytes,
-                                 sc, full);
-                }
+                if (kKind == kMx4)
+                    for (int i = 0; i < nrt; ++i)
+                        load(sb + b_bytes + 1024 * (1 + i), &P.sb[kForm == kPair ? i : 0], 0,
+                             ((T.n0 >> 7) + (kForm == kPair ? 0 : i)) * P.skb + 2 * k, full);
             };
             int early = 0;
             if (P.early_b && tile0 < P.tiles) {
                 early = min(P.stages, kb1 - kb0);
-                const Tile T = tile_at<kForm>(P, tile0);
+                const Tile T = tile_at<kForm, kCG>(P, tile0, rank);
                 for (int i = 0; i < early; ++i) load_b(T, kb0 + i, i);
             }
             tc::grid_wait();
             tc::grid_release();
             for (int t = tile0; t < P.tiles && ok; t += step) {
-                const Tile T = tile_at<kForm>(P, t);
+                const Tile T = tile_at<kForm, kCG>(P, t, rank);
                 for (int kb = kb0; kb < kb1; ++kb) {
                     if (issued >= early) {
                         if (!tc::mbar_wait(bar_empty + 8 * st, ph ^ 1)) {
@@ -247,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 // copies in flight land before the CTA goes: the last rounds' full barriers
                 *abort_flag = 1;
                 const int n = min(issued, P.stages);
-                for (int i = 0; i < n; ++i) {
+                for (int i = 0; i < n && leads; ++i) {
                     const int j = issued - n + i;
                     tc::mbar_wait(bar_full + 8 * (j % P.stages), (j / P.stages) & 1);
                 }
@@ -255,8 +298,14 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (lane == 0 && leads) {
             // ---- MMA issuer
+            const auto commit = [](uint32_t bar) {
+                if (kCG == 2)
+                    tc::mma_commit_pair(bar);
+                else
+                    tc::mma_commit(bar);
+            };
             int st = 0, it = 0;
             uint32_t ph = 0;
             bool ok = true;
@@ -268,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                     break;
                 }
                 tc::fence_after_sync();
-                const uint32_t d = tmem + buf * (kKind == kMx4 ? BN : 256);
+                const uint32_t d = acc_at(buf);
                 uint32_t acc = 0;
                 for (int kb = kb0; kb < kb1; ++kb) {
                     if (!tc::mbar_wait(bar_full + 8 * st, ph)) {
@@ -281,41 +330,51 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                         const uint64_t da = tc::desc_sw128(sa, 8192), db = tc::desc_sw128(sb, 8192);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            tc::mma_f16(d, da + (uint64_t)(j * ((kAmn ? 2048 : 32) >> 4)),
-                                        db + (uint64_t)(j * ((kBmn ? 2048 : 32) >> 4)), P.idesc, acc);
+                            const uint64_t dj = da + (uint64_t)(j * ((kAmn ? 2048 : 32) >> 4));
+                            const uint64_t ej = db + (uint64_t)(j * ((kBmn ? 2048 : 32) >> 4));
+                            if (kCG == 2)
+                                tc::mma_f16_pair(d, dj, ej, P.idesc, acc);
+                            else
+                                tc::mma_f16(d, dj, ej, P.idesc, acc);
                             acc = 1;
                         }
                     } else {
-                        // scales to tensor memory, columns of their own for each stage (the stage
-                        // is full again only after the MMAs that read them are done)
-                        const int nrt = kForm == kPair ? 2 : (BN + 127) >> 7;
+                        // scales to tensor memory (a pair: each CTA's A rows, and all of B's, in
+                        // both), columns of their own for each stage (the stage is full again only
+                        // after the MMAs that read them are done)
                         const uint32_t sf = tmem + P.nacc * BN + st * (8 + 8 * nrt), ss = sa + s_off;
                         const int steps = min(4, (P.K - kb * 256 + 63) >> 6);
-                        const int tiles = (steps + 1) >> 1;
-                        for (int h = 0; h < tiles; ++h) {
-                            tc::copy_scales(sf + 4 * h, tc::desc_scales(ss + 512 * h));
-                            for (int i = 0; i < nrt; ++i)
-                                tc::copy_scales(sf + 8 + 4 * (h * nrt + i), tc::desc_scales(ss + 1024 * (1 + i) + 512 * h));
-                        }
+                        for (int h = 0; h < (steps + 1) >> 1; ++h)
+                            for (int i = 0; i <= nrt; ++i) {
+                                const uint32_t to = i ? sf + 8 + 4 * (h * nrt + i - 1) : sf + 4 * h;
+                                const uint64_t from = tc::desc_scales(ss + 1024 * i + 512 * h);
+                                if (kCG == 2)
+                                    tc::copy_scales_pair(to, from);
+                                else
+                                    tc::copy_scales(to, from);
+                            }
                         const uint64_t da = tc::desc_sw128(sa, 16), db = tc::desc_sw128(sb, 16);
                         for (int j = 0; j < steps; ++j) {
                             const uint32_t id = P.idesc | (j & 1 ? (2u << 4) | (2u << 29) : 0u);
-                            tc::mma_mx4(d, da + (uint64_t)(2 * j), db + (uint64_t)(2 * j), id, sf + 4 * (j >> 1),
-                                        sf + 8 + 4 * nrt * (j >> 1), acc);
+                            const uint32_t fa = sf + 4 * (j >> 1), fb = sf + 8 + 4 * nrt * (j >> 1);
+                            if (kCG == 2)
+                                tc::mma_mx4_pair(d, da + (uint64_t)(2 * j), db + (uint64_t)(2 * j), id, fa, fb, acc);
+                            else
+                                tc::mma_mx4(d, da + (uint64_t)(2 * j), db + (uint64_t)(2 * j), id, fa, fb, acc);
                             acc = 1;
                         }
                     }
-                    tc::mma_commit(bar_empty + 8 * st);
+                    commit(bar_empty + 8 * st);
                     if (++st == P.stages) {
                         st = 0;
                         ph ^= 1;
                     }
                 }
-                tc::mma_commit(bar_accf + 8 * buf);
+                commit(bar_accf + 8 * buf);
             }
             if (!ok) {
                 *abort_flag = 1;
-                tc::mma_commit(drain);
+                commit(drain);
                 tc::mbar_wait(drain, 0);
             }
         }
@@ -324,9 +383,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         // ---- epilogue: warp q of four takes lanes (rows) 32 q .. 32 q + 31
         const int q = warp - 4, r = 32 * q + lane;
         const int cols = kForm == kPair ? BN / 2 : BN;
+        // split k: this CTA's partial sums go to shared memory, rows padded by 16 bytes
+        float4 *part = S > 1 ? reinterpret_cast<float4 *>(smem_raw + (base - smem0)) + r * (BN / 4 + 1) : nullptr;
         int it = 0;
         for (int t = tile0; t < P.tiles; t += step, ++it) {
-            const Tile T = tile_at<kForm>(P, t);
+            const Tile T = tile_at<kForm, kCG>(P, t, rank);
             const int buf = P.nacc == 2 ? it & 1 : 0;
             const uint32_t use = P.nacc == 2 ? it >> 1 : it;
             bool ok = true;
@@ -337,39 +398,27 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 break;
             }
             tc::fence_after_sync();
-            const uint32_t src = tmem + buf * (kKind == kMx4 ? BN : 256) + ((uint32_t)(32 * q) << 16);
+            const uint32_t src = acc_at(buf) + ((uint32_t)(32 * q) << 16);
             if (32 * q < T.rows) {
-                for (int c = 0; c < cols; c += 32) {
-                    uint32_t v[32], w[32];
-                    tc::tmem_ld32(src + c, v);
-                    if (kForm == kPair) tc::tmem_ld32(src + cols + c, w);
-                    tc::tmem_wait_ld(v);
-                    if (kForm == kPair) tc::tmem_wait_ld(w);
-                    if (S > 1) {
-                        // this CTA's partial sums, rows padded by 16 bytes
-                        if (r < T.rows) {
-                            float4 *p = reinterpret_cast<float4 *>(smem_raw + (base - smem0)) + r * (BN / 4 + 1) + c / 4;
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                p[i] = *reinterpret_cast<float4 *>(&v[4 * i]);
-                                if (kForm == kPair) p[cols / 4 + i] = *reinterpret_cast<float4 *>(&w[4 * i]);
-                            }
-                        }
-                    } else if (r < T.rows) {
-                        epi.template row<32>(T.p, T.m0 + r, T.n0 + c, *reinterpret_cast<float(*)[32]>(v),
-                                             *reinterpret_cast<float(*)[32]>(kForm == kPair ? w : v));
-                    }
-                }
+                int c = 0;
+                for (; c + 32 <= cols; c += 32) take<32, kForm>(epi, T, src, cols, r, c, part);
+                if constexpr (Epi::kWidth <= 16)
+                    if (c < cols) take<16, kForm>(epi, T, src, cols, r, c, part);
             }
             tc::fence_before_sync();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(bar_acce + 8 * buf);
+            if (lane == 0) {
+                if (leads)
+                    tc::mbar_arrive(bar_acce + 8 * buf);
+                else
+                    tc::mbar_arrive_cluster(tc::map_rank(bar_acce + 8 * buf, 0));
+            }
         }
     }
     if (S > 1) {
         __syncthreads();
         tc::cluster_sync();
-        const Tile T = tile_at<kForm>(P, tile0);
+        const Tile T = tile_at<kForm, kCG>(P, tile0, rank);
         const int cols = kForm == kPair ? BN / 2 : BN, nc = cols / Epi::kWidth, items = T.rows * nc;
         constexpr int W = Epi::kWidth;
         // items of W columns, a contiguous share for each CTA of the cluster
@@ -388,9 +437,15 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     }
     tc::fence_before_sync();
     __syncthreads();
+    if (kCG == 2) tc::cluster_sync(); // nor while its memory takes part in the other's MMAs or barriers
     tc::fence_after_sync();
     if (tid == 0 && *abort_flag) atomicOr(&g_dense_timeout, 1u);
-    if (warp == 2) tc::tmem_dealloc(tmem, kTmemCols);
+    if (warp == 2) {
+        if (kCG == 2)
+            tc::tmem_dealloc_pair(tmem, kTmemCols);
+        else
+            tc::tmem_dealloc(tmem, kTmemCols);
+    }
 }
 
 // ---- epilogues -----------------------------------------------------------------------------
@@ -528,32 +583,44 @@ constexpr size_t kAheadMost = 48u << 20;
 // 128-byte swizzle, zeros past the ends.  unit: bytes of one coordinate step (2 or 1).
 cudaError_t make_map(CUtensorMap *m, const void *p, int unit, int rows, size_t row_bytes, int box_rows);
 
-// Launch shape from the sizes alone: tile width and CTAs per tile for products of sizes (M, N) x
-// n and kb pieces of k.  pair: a tile holds BN / 2 columns of each of two products.  step: BN is a
-// multiple of it.
+// A tensor map over scale tiles (512 bytes each): boxes of two tiles.
+cudaError_t make_scale_map(CUtensorMap *m, const void *p, size_t tiles);
+
+// Launch shape from the sizes alone: tile width, CTAs per tile that split k, and CTAs (1 or 2)
+// that make one tile together, for n products of sizes (M, N) and kb pieces of k.  pair: a tile
+// holds BN / 2 columns of each of two products.
 struct Plan {
-    int BN, S;
+    int BN, S, cg;
 };
 Plan plan(const int *M, const int *N, int n, int kb, bool pair, bool mx4, int sms);
 
-inline void set_problems(GemmArgs &G, const int *M, const int *N, int n, bool pair) {
+// Fills in the plan and the tiles.
+inline void set_shape(GemmArgs &G, const Plan &L, const int *M, const int *N, int n, bool pair) {
+    G.BN = L.BN;
+    G.S = L.S;
     G.nprob = n;
     G.tiles = 0;
+    const int h = kBM * L.cg, w = pair ? L.BN / 2 : L.BN;
     for (int i = 0; i < n; ++i) {
-        const int w = pair ? G.BN / 2 : G.BN;
-        G.prob[i] = Prob{M[i], N[i], (M[i] + kBM - 1) / kBM, (N[i] + w - 1) / w, G.tiles};
+        G.prob[i] = Prob{M[i], N[i], (M[i] + h - 1) / h, (N[i] + w - 1) / w, G.tiles};
         G.tiles += G.prob[i].tm * G.prob[i].tn;
     }
 }
+// Rows of B's boxes (K-major).
+inline int box_rows_b(const Plan &L, bool pair) { return pair || L.cg == 2 ? L.BN / 2 : L.BN; }
 
-template <int kKind, int kForm, bool kAmn, bool kBmn, class Epi>
-cudaError_t launch_gemm(GemmArgs &G, const Epi &epi, int sms, cudaStream_t s) {
+template <int kCG, int kKind, int kForm, bool kAmn, bool kBmn, class Epi>
+cudaError_t launch_gemm_as(GemmArgs &G, const Epi &epi, int sms, cudaStream_t s) {
     static SmemAttr attr;
-    const auto kernel = gemm_kernel<kKind, kForm, kAmn, kBmn, Epi>;
-    const uint32_t stage =
-        (uint32_t)round_up((size_t)(kBM + G.BN) * kRowBytes + (kKind == kMx4 ? 1024 * (1 + (G.BN + 127) / 128) : 0), 1024);
+    const auto kernel = gemm_kernel<kCG, kKind, kForm, kAmn, kBmn, Epi>;
+    const uint32_t stage = stage_size(G.BN, kCG, kBmn, kKind == kMx4);
     G.stages = (int)((kSmemBudget - kBarBytes - 1024) / stage);
     if (G.stages > kMaxStages) G.stages = kMaxStages;
+    G.nacc = 2;
+    if (kKind == kMx4) { // the stages' scales take tensor memory too
+        const int per = 8 + 8 * ((G.BN + 127) / 128);
+        if (2 * G.BN + G.stages * per > kTmemCols) G.nacc = 1;
+    }
     const uint32_t smem = kBarBytes + 1024 + G.stages * stage;
     cudaError_t e = ensure_smem(attr, reinterpret_cast<const void *>(kernel), (int)smem);
     if (e != cudaSuccess) return e;
@@ -563,19 +630,25 @@ cudaError_t launch_gemm(GemmArgs &G, const Epi &epi, int sms, cudaStream_t s) {
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(G.S > 1 ? G.tiles * G.S : (G.tiles < sms ? G.tiles : sms));
+    const int most = sms / kCG, ctas = kCG == 2 ? 2 : G.S;
+    cfg.gridDim = dim3(G.S > 1 ? G.tiles * G.S : (G.tiles < most ? G.tiles : most) * kCG);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (G.S > 1) {
+    if (ctas > 1) {
         at[1].id = cudaLaunchAttributeClusterDimension;
-        at[1].val.clusterDim.x = G.S;
+        at[1].val.clusterDim.x = ctas;
         at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
         cfg.numAttrs = 2;
     }
     return cudaLaunchKernelEx(&cfg, kernel, G, epi);
+}
+template <int kKind, int kForm, bool kAmn, bool kBmn, class Epi>
+cudaError_t launch_gemm(GemmArgs &G, const Plan &L, const Epi &epi, int sms, cudaStream_t s) {
+    return L.cg == 2 ? launch_gemm_as<2, kKind, kForm, kAmn, kBmn>(G, epi, sms, s)
+                     : launch_gemm_as<1, kKind, kForm, kAmn, kBmn>(G, epi, sms, s);
 }
 
 } // namespace dense

@@ -30,25 +30,22 @@ struct GatedMx4 {
     }
 };
 
-cudaError_t mx_map(CUtensorMap *m, const Mx4Mat &x, int box_rows) {
-    return make_map(m, x.codes, 1, x.rows, (size_t)x.cols / 2, box_rows);
+// Maps of an operand's codes and scales.
+cudaError_t maps(CUtensorMap *codes, CUtensorMap *scales, const Mx4Mat &x, int box_rows) {
+    const cudaError_t e = make_map(codes, x.codes, 1, x.rows, (size_t)x.cols / 2, box_rows);
+    if (e != cudaSuccess) return e;
+    return make_scale_map(scales, x.scales, mx_scale_bytes(x.rows, x.cols) / kMxTileBytes);
 }
 
-GemmArgs common(const Mx4Mat &a, const Mx4Mat &b, bool pair, int sms) {
-    GemmArgs G = {};
+// Everything but B's maps.
+cudaError_t common(GemmArgs &G, Plan &L, const Mx4Mat &a, const Mx4Mat &b, bool pair, int sms) {
     G.K = a.cols;
     G.kb = G.kb_seg = (a.cols + 255) / 256;
-    const Plan L = plan(&a.rows, &b.rows, 1, G.kb, pair, true, sms);
-    G.BN = L.BN;
-    G.S = L.S;
-    G.nacc = G.BN <= 128 ? 2 : 1; // the scales of the stages take tensor memory too
-    set_problems(G, &a.rows, &b.rows, 1, pair);
-    G.idesc = tc::idesc_mx4(kBM, G.BN, 0);
-    G.sa = a.scales;
-    G.sb[0] = b.scales;
     G.skb = (a.cols + 127) / 128;
-    G.nbt = (b.rows + kMxTileRows - 1) / kMxTileRows;
-    return G;
+    L = plan(&a.rows, &b.rows, 1, G.kb, pair, true, sms);
+    set_shape(G, L, &a.rows, &b.rows, 1, pair);
+    G.idesc = tc::idesc_mx4(kBM * L.cg, G.BN, 0);
+    return maps(&G.ta[0], &G.sa, a, kBM);
 }
 
 } // namespace
@@ -56,37 +53,38 @@ GemmArgs common(const Mx4Mat &a, const Mx4Mat &b, bool pair, int sms) {
 cudaError_t launch_mx4_matmul(const Mx4Mat &a, const Mx4Mat &b, void *out, int out_dtype, int mode, bool after_own,
                               cudaStream_t s) {
     const int sms = device_sm_count();
-    GemmArgs G = common(a, b, false, sms);
-    G.early_b = after_own;
-    cudaError_t e = mx_map(&G.ta[0], a, kBM);
-    if (e == cudaSuccess) e = mx_map(&G.tb[0], b, G.BN);
+    GemmArgs G = {};
+    Plan L;
+    cudaError_t e = common(G, L, a, b, false, sms);
+    if (e == cudaSuccess) e = maps(&G.tb[0], &G.sb[0], b, box_rows_b(L, false));
     if (e != cudaSuccess) return e;
+    G.early_b = after_own;
     Store st = {};
     st.out[0] = out;
     st.ld[0] = b.rows;
     st.dtype = out_dtype;
     st.add = mode;
     st.vec = (size_t)b.rows * type_size(out_dtype) % 16 == 0;
-    return launch_gemm<kMx4, kOne, false, false>(G, st, sms, s);
+    return launch_gemm<kMx4, kOne, false, false>(G, L, st, sms, s);
 }
 
 cudaError_t launch_mx4_gated(const Mx4Mat &x, const Mx4Mat &gate, const Mx4Mat &up, const Mx4Mat &next,
                              uint8_t *codes, uint8_t *scales, cudaStream_t s) {
     const int sms = device_sm_count();
-    GemmArgs G = common(x, gate, true, sms);
-    G.sb[1] = up.scales;
+    GemmArgs G = {};
+    Plan L;
+    cudaError_t e = common(G, L, x, gate, true, sms);
+    if (e == cudaSuccess) e = maps(&G.tb[0], &G.sb[0], gate, box_rows_b(L, true));
+    if (e == cudaSuccess) e = maps(&G.tb[1], &G.sb[1], up, box_rows_b(L, true));
+    if (e != cudaSuccess) return e;
     G.early_b = 1;
     const size_t bytes = mx_code_bytes(next.rows, next.cols);
     if (G.S > 1 && bytes <= kAheadMost) {
         G.ahead = next.codes;
         G.ahead_bytes = bytes;
     }
-    cudaError_t e = mx_map(&G.ta[0], x, kBM);
-    if (e == cudaSuccess) e = mx_map(&G.tb[0], gate, G.BN / 2);
-    if (e == cudaSuccess) e = mx_map(&G.tb[1], up, G.BN / 2);
-    if (e != cudaSuccess) return e;
     const int f = gate.rows;
-    return launch_gemm<kMx4, kPair, false, false>(G, GatedMx4{codes, scales, f, (f + 127) / 128}, sms, s);
+    return launch_gemm<kMx4, kPair, false, false>(G, L, GatedMx4{codes, scales, f, (f + 127) / 128}, sms, s);
 }
 
 cudaError_t mx4_timeout(uint32_t *out) { return read_and_clear_timeout(out); }

@@ -52,7 +52,7 @@ def guarded(*shape, dtype, fill=7.0):
 
 # d and f of one core matrix, below and past a tile, of no round number, and of the workloads
 SHAPES = [(1, 8, 8), (1, 1032, 1544), (2, 64, 24), (3, 256, 128), (5, 264, 1800), (8, 2056, 136), (9, 520, 136), (33, 136, 264), (127, 1032, 136), (128, 512, 520), (129, 72, 1544),
-          (200, 1032, 264), (257, 264, 1032), (511, 648, 392)]
+          (200, 1032, 264), (257, 264, 1032), (511, 648, 392), (1000, 1544, 776), (2049, 2056, 1032)]
 
 
 @pytest.mark.parametrize("t", [BF, HF])
@@ -333,7 +333,7 @@ def test_quantize_strided_rows():
 
 
 MATMULS = [(1, 1, 32), (1, 130, 7168), (2, 17, 96), (16, 64, 160), (100, 129, 128), (128, 256, 256), (129, 257, 288),
-           (300, 200, 1056), (257, 1000, 512), (640, 513, 2048)]
+           (300, 200, 1056), (257, 1000, 512), (640, 513, 2048), (1000, 1100, 544), (2500, 2100, 1056)]
 
 
 @pytest.mark.parametrize("M,N,K", MATMULS)
@@ -397,7 +397,7 @@ def mx4_block(x, W, t_out):
 
 
 @pytest.mark.parametrize("tx,to", [(FP, FP), (BF, BF), (HF, FP)])
-@pytest.mark.parametrize("T,d,f", [(1, 32, 32), (1, 4128, 160), (2, 160, 2080), (3, 288, 96), (4, 1056, 160), (5, 256, 128), (8, 6176, 1056), (130, 288, 416), (260, 512, 352)])
+@pytest.mark.parametrize("T,d,f", [(1, 32, 32), (1, 4128, 160), (2, 160, 2080), (3, 288, 96), (4, 1056, 160), (5, 256, 128), (8, 6176, 1056), (130, 288, 416), (260, 512, 352), (1000, 1184, 800)])
 def test_mx4_expert(T, d, f, tx, to):
     g = gen(T + d + f)
     W = weights(g, d, f, BF)
