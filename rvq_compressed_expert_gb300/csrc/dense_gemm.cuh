@@ -298,8 +298,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && leads) {
-            // ---- MMA issuer
+        if (leads) {
+            // ---- MMA issuer.  The whole warp walks the loop and one elected lane issues, so that
+            // addresses and descriptors stay in the warp's uniform registers, where the tensor
+            // core takes them from: a loop inside "if (lane == 0)" moves each operand there anew.
             const auto commit = [](uint32_t bar) {
                 if (kCG == 2)
                     tc::mma_commit_pair(bar);
@@ -309,6 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             int st = 0, it = 0;
             uint32_t ph = 0;
             bool ok = true;
+            const uint64_t desc0 = tc::desc_sw128(base, kKind == kHalf ? 8192 : 16);
             for (int t = tile0; t < P.tiles && ok; t += step, ++it) {
                 const int buf = P.nacc == 2 ? it & 1 : 0;
                 const uint32_t use = P.nacc == 2 ? it >> 1 : it;
@@ -318,63 +321,70 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 }
                 tc::fence_after_sync();
                 const uint32_t d = acc_at(buf);
-                uint32_t acc = 0;
                 for (int kb = kb0; kb < kb1; ++kb) {
                     if (!tc::mbar_wait(bar_full + 8 * st, ph)) {
                         ok = false;
                         break;
                     }
                     tc::fence_after_sync();
-                    const uint32_t sa = base + st * stage_bytes, sb = sa + a_bytes;
-                    if (kKind == kHalf) {
-                        const uint64_t da = tc::desc_sw128(sa, 8192), db = tc::desc_sw128(sb, 8192);
+                    const uint64_t da = desc0 + (uint64_t)((st * stage_bytes) >> 4), db = da + (uint64_t)(a_bytes >> 4);
+                    if (tc::elect_one()) {
+                        if (kKind == kHalf) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint64_t dj = da + (uint64_t)(j * ((kAmn ? 2048 : 32) >> 4));
-                            const uint64_t ej = db + (uint64_t)(j * ((kBmn ? 2048 : 32) >> 4));
-                            if (kCG == 2)
-                                tc::mma_f16_pair(d, dj, ej, P.idesc, acc);
-                            else
-                                tc::mma_f16(d, dj, ej, P.idesc, acc);
-                            acc = 1;
-                        }
-                    } else {
-                        // scales to tensor memory (a pair: each CTA's A rows, and all of B's, in
-                        // both), columns of their own for each stage (the stage is full again only
-                        // after the MMAs that read them are done)
-                        const uint32_t sf = tmem + P.nacc * BN + st * (8 + 8 * nrt), ss = sa + s_off;
-                        const int steps = min(4, (P.K - kb * 256 + 63) >> 6);
-                        for (int h = 0; h < (steps + 1) >> 1; ++h)
-                            for (int i = 0; i <= nrt; ++i) {
-                                const uint32_t to = i ? sf + 8 + 4 * (h * nrt + i - 1) : sf + 4 * h;
-                                const uint64_t from = tc::desc_scales(ss + 1024 * i + 512 * h);
+                            for (int j = 0; j < 4; ++j) {
+                                const uint64_t dj = da + (uint64_t)(j * ((kAmn ? 2048 : 32) >> 4));
+                                const uint64_t ej = db + (uint64_t)(j * ((kBmn ? 2048 : 32) >> 4));
+                                const uint32_t acc = j > 0 || kb > kb0;
                                 if (kCG == 2)
-                                    tc::copy_scales_pair(to, from);
+                                    tc::mma_f16_pair(d, dj, ej, P.idesc, acc);
                                 else
-                                    tc::copy_scales(to, from);
+                                    tc::mma_f16(d, dj, ej, P.idesc, acc);
                             }
-                        const uint64_t da = tc::desc_sw128(sa, 16), db = tc::desc_sw128(sb, 16);
-                        for (int j = 0; j < steps; ++j) {
-                            const uint32_t id = P.idesc | (j & 1 ? (2u << 4) | (2u << 29) : 0u);
-                            const uint32_t fa = sf + 4 * (j >> 1), fb = sf + 8 + 4 * nrt * (j >> 1);
-                            if (kCG == 2)
-                                tc::mma_mx4_pair(d, da + (uint64_t)(2 * j), db + (uint64_t)(2 * j), id, fa, fb, acc);
-                            else
-                                tc::mma_mx4(d, da + (uint64_t)(2 * j), db + (uint64_t)(2 * j), id, fa, fb, acc);
-                            acc = 1;
+                        } else {
+                            // scales to tensor memory (a pair: each CTA's A rows, and all of B's, in
+                            // both), columns of their own for each stage (the stage is full again
+                            // only after the MMAs that read them are done)
+                            const uint32_t sf = tmem + P.nacc * BN + st * (8 + 8 * nrt);
+                            const uint64_t ds = tc::desc_scales(base + st * stage_bytes + s_off);
+                            const int steps = P.K - kb * 256;
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                if (128 * h >= steps) break;
+                                const uint32_t fa = sf + 4 * h, fb = sf + 8 + 4 * nrt * h;
+                                for (int i = 0; i <= nrt; ++i) {
+                                    const uint32_t to = i ? fb + 4 * (i - 1) : fa;
+                                    const uint64_t from = ds + (uint64_t)((1024 * i + 512 * h) >> 4);
+                                    if (kCG == 2)
+                                        tc::copy_scales_pair(to, from);
+                                    else
+                                        tc::copy_scales(to, from);
+                                }
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) {
+                                    if (128 * h + 64 * j >= steps) break;
+                                    const uint32_t id = P.idesc | (j ? (2u << 4) | (2u << 29) : 0u);
+                                    const uint64_t off = (uint64_t)(2 * (2 * h + j));
+                                    const uint32_t acc = h > 0 || j > 0 || kb > kb0;
+                                    if (kCG == 2)
+                                        tc::mma_mx4_pair(d, da + off, db + off, id, fa, fb, acc);
+                                    else
+                                        tc::mma_mx4(d, da + off, db + off, id, fa, fb, acc);
+                                }
+                            }
                         }
+                        commit(bar_empty + 8 * st);
+                        if (kb + 1 == kb1) commit(bar_accf + 8 * buf);
                     }
-                    commit(bar_empty + 8 * st);
+                    __syncwarp();
                     if (++st == P.stages) {
                         st = 0;
                         ph ^= 1;
                     }
                 }
-                commit(bar_accf + 8 * buf);
             }
             if (!ok) {
-                *abort_flag = 1;
-                commit(drain);
+                if (lane == 0) *abort_flag = 1;
+                if (tc::elect_one()) commit(drain);
                 tc::mbar_wait(drain, 0);
             }
         }
