@@ -36,7 +36,7 @@ constexpr int kMaxStages = 8;
 constexpr int kMaxProb = 3;
 constexpr uint32_t kSmemBudget = 225 * 1024;
 constexpr uint32_t kBarBytes = 256;
-constexpr int kThreads = 256;
+constexpr int kThreads = 352; // loader, issuer, allocator, eight epilogue warps
 constexpr int kTmemCols = 512;
 
 struct Prob {
@@ -125,31 +125,39 @@ template <int W> __device__ __forceinline__ void add_ranks(uint32_t src, int S, 
     }
 }
 
-// W columns of a row from tensor memory through the epilogue (or, split: to the partial sums).
-template <int W, int kForm, class Epi>
-__device__ __forceinline__ void take(const Epi &epi, const Tile &T, uint32_t src, int cols, int r, int c, float4 *part) {
-    uint32_t v[W], w[W];
-    if constexpr (W == 32) {
-        tc::tmem_ld32(src + c, v);
-        if (kForm == kPair) tc::tmem_ld32(src + cols + c, w);
-    } else {
-        tc::tmem_ld16n(src + c, v);
-        if (kForm == kPair) tc::tmem_ld16n(src + cols + c, w);
+// W columns of a row (kPair: of both products) from tensor memory to registers; complete after
+// taken().
+template <int W, int kForm> struct Sums {
+    uint32_t v[W], w[kForm == kPair ? W : 1];
+    __device__ __forceinline__ void take(uint32_t src, int cols) {
+        if constexpr (W == 32) {
+            tc::tmem_ld32(src, v);
+            if constexpr (kForm == kPair) tc::tmem_ld32(src + cols, w);
+        } else {
+            tc::tmem_ld16n(src, v);
+            if constexpr (kForm == kPair) tc::tmem_ld16n(src + cols, w);
+        }
     }
-    tc::tmem_wait_ld(v);
-    if (kForm == kPair) tc::tmem_wait_ld(w);
-    if (r >= T.rows) return;
-    if (part) {
+    __device__ __forceinline__ void taken() {
+        tc::tmem_wait_ld(v);
+        if constexpr (kForm == kPair) tc::tmem_wait_ld(w);
+    }
+    // to the partial sums' row
+    __device__ __forceinline__ void keep(float4 *part, int cols, int c) const {
 #pragma unroll
         for (int i = 0; i < W / 4; ++i) {
-            part[c / 4 + i] = *reinterpret_cast<float4 *>(&v[4 * i]);
-            if (kForm == kPair) part[(cols + c) / 4 + i] = *reinterpret_cast<float4 *>(&w[4 * i]);
+            part[c / 4 + i] = *reinterpret_cast<const float4 *>(&v[4 * i]);
+            if constexpr (kForm == kPair) part[(cols + c) / 4 + i] = *reinterpret_cast<const float4 *>(&w[4 * i]);
         }
-    } else {
-        epi.template row<W>(T.p, T.m0 + r, T.n0 + c, *reinterpret_cast<float(*)[W]>(v),
-                            *reinterpret_cast<float(*)[W]>(kForm == kPair ? w : v));
     }
-}
+    template <class Epi> __device__ __forceinline__ void give(const Epi &epi, const Tile &T, int r, int c) const {
+        const auto &x = *reinterpret_cast<const float(*)[W]>(v);
+        if constexpr (kForm == kPair)
+            epi.template row<W>(T.p, T.m0 + r, T.n0 + c, x, *reinterpret_cast<const float(*)[W]>(w));
+        else
+            epi.template row<W>(T.p, T.m0 + r, T.n0 + c, x, x);
+    }
+};
 
 template <int kCG, int kKind, int kForm, bool kAmn, bool kBmn, class Epi>
 __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs P, const Epi epi) {
@@ -177,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(bar_accf + 8 * i, 1);
-            tc::mbar_init(bar_acce + 8 * i, 4 * kCG);
+            tc::mbar_init(bar_acce + 8 * i, 8 * kCG);
         }
         tc::mbar_init(drain, 1);
         *abort_flag = 0;
@@ -203,97 +211,100 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     const auto acc_at = [&](int buf) { return tmem + buf * (kKind == kMx4 ? BN : 256); };
 
     if (warp == 0) {
-        if (lane == 0) {
-            // ---- loader.  A pair's CTAs load their own rows of A and their half of B; the bytes
-            // of both count on the first one's barrier, which announces them.
-            int st = 0, issued = 0;
-            uint32_t ph = 0;
-            bool ok = true;
-            const uint32_t full0 = kCG == 2 ? tc::map_rank(bar_full, 0) : bar_full;
-            const auto load = [](uint32_t dst, const CUtensorMap *m, int x, int y, uint32_t bar) {
-                if (kCG == 2)
-                    tc::tma_load_pair(dst, m, x, y, bar);
-                else
-                    tc::tma_load(dst, m, x, y, bar);
-            };
-            const auto load_a = [&](const Tile &T, int kb, int st) {
-                const uint32_t sa = base + st * stage_bytes, full = full0 + 8 * st;
-                const bool second = kForm == kSum && kb >= P.kb_seg;
-                const int k = second ? kb - P.kb_seg : kb;
-                const CUtensorMap *ta = &P.ta[kForm == kSum ? (second ? 1 : 0) : T.p];
-                const int kx = kKind == kMx4 ? k * kRowBytes : k * 64;
-                if (kAmn) {
-                    for (int i = 0; i < kBM / 64; ++i) load(sa + i * 8192, ta, T.m0 + 64 * i, kx, full);
-                } else {
-                    load(sa, ta, kx, T.m0, full);
-                }
-                if (kKind == kMx4) load(sa + s_off, &P.sa, 0, (T.m0 >> 7) * P.skb + 2 * k, full);
-            };
-            // also announces the bytes of the whole stage
-            const auto load_b = [&](const Tile &T, int kb, int st) {
-                const uint32_t sb = base + st * stage_bytes + a_bytes, full = full0 + 8 * st;
-                const bool second = kForm == kSum && kb >= P.kb_seg;
-                const int k = second ? kb - P.kb_seg : kb;
-                const CUtensorMap *tb =
-                    &P.tb[kForm == kSum ? (second ? 1 : 0) : kForm == kPair ? (kCG == 2 ? rank : 0) : T.p];
-                const int kx = kKind == kMx4 ? k * kRowBytes : k * 64;
-                const int n0 = T.n0 + (kCG == 2 && kForm != kPair ? rank * (BN / 2) : 0);
-                if (leads)
-                    tc::mbar_arrive_expect_tx(bar_full + 8 * st,
-                                              kCG * (a_bytes + b_bytes + (kKind == kMx4 ? 1024u * (1 + nrt) : 0u)));
-                if (kBmn) {
-                    for (uint32_t i = 0; i * 8192 < b_bytes; ++i) load(sb + i * 8192, tb, n0 + 64 * i, kx, full);
-                } else {
-                    load(sb, tb, kx, n0, full);
-                    if (kForm == kPair && kCG == 1) load(sb + b_bytes / 2, &P.tb[1], kx, n0, full);
-                }
-                if (kKind == kMx4)
-                    for (int i = 0; i < nrt; ++i)
-                        load(sb + b_bytes + 1024 * (1 + i), &P.sb[kForm == kPair ? i : 0], 0,
-                             ((T.n0 >> 7) + (kForm == kPair ? 0 : i)) * P.skb + 2 * k, full);
-            };
-            int early = 0;
-            if (P.early_b && tile0 < P.tiles) {
-                early = min(P.stages, kb1 - kb0);
-                const Tile T = tile_at<kForm, kCG>(P, tile0, rank);
+        // ---- loader (the warp walks the loop, an elected lane issues).  A pair's CTAs load their own rows of A and their half of B; the bytes
+        // of both count on the first one's barrier, which announces them.
+        int st = 0, issued = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        const uint32_t full0 = kCG == 2 ? tc::map_rank(bar_full, 0) : bar_full;
+        const auto load = [](uint32_t dst, const CUtensorMap *m, int x, int y, uint32_t bar) {
+            if (kCG == 2)
+                tc::tma_load_pair(dst, m, x, y, bar);
+            else
+                tc::tma_load(dst, m, x, y, bar);
+        };
+        const auto load_a = [&](const Tile &T, int kb, int st) {
+            const uint32_t sa = base + st * stage_bytes, full = full0 + 8 * st;
+            const bool second = kForm == kSum && kb >= P.kb_seg;
+            const int k = second ? kb - P.kb_seg : kb;
+            const CUtensorMap *ta = &P.ta[kForm == kSum ? (second ? 1 : 0) : T.p];
+            const int kx = kKind == kMx4 ? k * kRowBytes : k * 64;
+            if (kAmn) {
+                for (int i = 0; i < kBM / 64; ++i) load(sa + i * 8192, ta, T.m0 + 64 * i, kx, full);
+            } else {
+                load(sa, ta, kx, T.m0, full);
+            }
+            if (kKind == kMx4) load(sa + s_off, &P.sa, 0, (T.m0 >> 7) * P.skb + 2 * k, full);
+        };
+        // also announces the bytes of the whole stage
+        const auto load_b = [&](const Tile &T, int kb, int st) {
+            const uint32_t sb = base + st * stage_bytes + a_bytes, full = full0 + 8 * st;
+            const bool second = kForm == kSum && kb >= P.kb_seg;
+            const int k = second ? kb - P.kb_seg : kb;
+            const CUtensorMap *tb =
+                &P.tb[kForm == kSum ? (second ? 1 : 0) : kForm == kPair ? (kCG == 2 ? rank : 0) : T.p];
+            const int kx = kKind == kMx4 ? k * kRowBytes : k * 64;
+            const int n0 = T.n0 + (kCG == 2 && kForm != kPair ? rank * (BN / 2) : 0);
+            if (leads)
+                tc::mbar_arrive_expect_tx(bar_full + 8 * st,
+                                          kCG * (a_bytes + b_bytes + (kKind == kMx4 ? 1024u * (1 + nrt) : 0u)));
+            if (kBmn) {
+                for (uint32_t i = 0; i * 8192 < b_bytes; ++i) load(sb + i * 8192, tb, n0 + 64 * i, kx, full);
+            } else {
+                load(sb, tb, kx, n0, full);
+                if (kForm == kPair && kCG == 1) load(sb + b_bytes / 2, &P.tb[1], kx, n0, full);
+            }
+            if (kKind == kMx4)
+                for (int i = 0; i < nrt; ++i)
+                    load(sb + b_bytes + 1024 * (1 + i), &P.sb[kForm == kPair ? i : 0], 0,
+                         ((T.n0 >> 7) + (kForm == kPair ? 0 : i)) * P.skb + 2 * k, full);
+        };
+        int early = 0;
+        if (P.early_b && tile0 < P.tiles) {
+            early = min(P.stages, kb1 - kb0);
+            const Tile T = tile_at<kForm, kCG>(P, tile0, rank);
+            if (tc::elect_one())
                 for (int i = 0; i < early; ++i) load_b(T, kb0 + i, i);
-            }
-            tc::grid_wait();
-            tc::grid_release();
-            for (int t = tile0; t < P.tiles && ok; t += step) {
-                const Tile T = tile_at<kForm, kCG>(P, t, rank);
-                for (int kb = kb0; kb < kb1; ++kb) {
-                    if (issued >= early) {
-                        if (!tc::mbar_wait(bar_empty + 8 * st, ph ^ 1)) {
-                            ok = false;
-                            break;
-                        }
-                        load_b(T, kb, st);
+            __syncwarp();
+        }
+        tc::grid_wait();
+        tc::grid_release();
+        for (int t = tile0; t < P.tiles && ok; t += step) {
+            const Tile T = tile_at<kForm, kCG>(P, t, rank);
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (issued >= early) {
+                    if (!tc::mbar_wait(bar_empty + 8 * st, ph ^ 1)) {
+                        ok = false;
+                        break;
                     }
+                }
+                if (tc::elect_one()) {
+                    if (issued >= early) load_b(T, kb, st);
                     load_a(T, kb, st);
-                    ++issued;
-                    if (++st == P.stages) {
-                        st = 0;
-                        ph ^= 1;
-                    }
+                }
+                __syncwarp();
+                ++issued;
+                if (++st == P.stages) {
+                    st = 0;
+                    ph ^= 1;
                 }
             }
-            if (P.ahead_bytes) {
-                // this CTA's share, in pieces of 16 KiB
-                const size_t n = (P.ahead_bytes + 16383) >> 14;
-                for (size_t i = blockIdx.x; i < n; i += gridDim.x) {
-                    const size_t left = P.ahead_bytes - (i << 14);
-                    tc::prefetch_l2(P.ahead + (i << 14), left < 16384 ? (uint32_t)left : 16384u);
-                }
+        }
+        if (P.ahead_bytes && lane == 0) {
+            // this CTA's share, in pieces of 16 KiB
+            const size_t n = (P.ahead_bytes + 16383) >> 14;
+            for (size_t i = blockIdx.x; i < n; i += gridDim.x) {
+                const size_t left = P.ahead_bytes - (i << 14);
+                tc::prefetch_l2(P.ahead + (i << 14), left < 16384 ? (uint32_t)left : 16384u);
             }
-            if (!ok) {
-                // copies in flight land before the CTA goes: the last rounds' full barriers
-                *abort_flag = 1;
-                const int n = min(issued, P.stages);
-                for (int i = 0; i < n && leads; ++i) {
-                    const int j = issued - n + i;
-                    tc::mbar_wait(bar_full + 8 * (j % P.stages), (j / P.stages) & 1);
-                }
+        }
+        if (!ok) {
+            // copies in flight land before the CTA goes: the last rounds' full barriers
+            if (lane == 0) *abort_flag = 1;
+            const int n = min(issued, P.stages);
+            for (int i = 0; i < n && leads; ++i) {
+                const int j = issued - n + i;
+                tc::mbar_wait(bar_full + 8 * (j % P.stages), (j / P.stages) & 1);
             }
         }
         __syncwarp();
@@ -389,9 +400,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             }
         }
         __syncwarp();
-    } else if (warp >= 4) {
-        // ---- epilogue: warp q of four takes lanes (rows) 32 q .. 32 q + 31
-        const int q = warp - 4, r = 32 * q + lane;
+    } else if (warp >= 3) {
+        // ---- epilogue: two warps for each quarter of the lanes (rows); they take its pieces of 32
+        // columns in turn
+        const int q = warp & 3, half = (warp - 3) >> 2, r = 32 * q + lane;
         const int cols = kForm == kPair ? BN / 2 : BN;
         // split k: this CTA's partial sums go to shared memory, rows padded by 16 bytes
         float4 *part = S > 1 ? reinterpret_cast<float4 *>(smem_raw + (base - smem0)) + r * (BN / 4 + 1) : nullptr;
@@ -409,19 +421,59 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             }
             tc::fence_after_sync();
             const uint32_t src = acc_at(buf) + ((uint32_t)(32 * q) << 16);
-            if (32 * q < T.rows) {
-                int c = 0;
-                for (; c + 32 <= cols; c += 32) take<32, kForm>(epi, T, src, cols, r, c, part);
-                if constexpr (Epi::kWidth <= 16)
-                    if (c < cols) take<16, kForm>(epi, T, src, cols, r, c, part);
-            }
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) {
-                if (leads)
-                    tc::mbar_arrive(bar_acce + 8 * buf);
-                else
-                    tc::mbar_arrive_cluster(tc::map_rank(bar_acce + 8 * buf, 0));
+            const auto free_acc = [&] {
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    if (leads)
+                        tc::mbar_arrive(bar_acce + 8 * buf);
+                    else
+                        tc::mbar_arrive_cluster(tc::map_rank(bar_acce + 8 * buf, 0));
+                }
+            };
+            const bool any = 32 * q < T.rows;
+            if constexpr (kKind == kMx4) {
+                // one accumulator (the other's place holds scales): all of it to registers first,
+                // so that the next tile's MMAs wait for the reading alone
+                constexpr int kHeld = kForm == kPair ? 2 : 4;
+                Sums<32, kForm> x[kHeld];
+                if (any) {
+#pragma unroll
+                    for (int i = 0; i < kHeld; ++i)
+                        if (64 * i + 32 * half < cols) x[i].take(src + 64 * i + 32 * half, cols);
+#pragma unroll
+                    for (int i = 0; i < kHeld; ++i)
+                        if (64 * i + 32 * half < cols) x[i].taken();
+                }
+                free_acc();
+                if (any && r < T.rows) {
+#pragma unroll
+                    for (int i = 0; i < kHeld; ++i) {
+                        const int c = 64 * i + 32 * half;
+                        if (c >= cols) break;
+                        if (part)
+                            x[i].keep(part, cols, c);
+                        else
+                            x[i].give(epi, T, r, c);
+                    }
+                }
+            } else {
+                if (any) {
+                    for (int c = 32 * half; c < cols; c += 64) {
+                        if (c + 32 <= cols) {
+                            Sums<32, kForm> x;
+                            x.take(src + c, cols);
+                            x.taken();
+                            if (r < T.rows) part ? x.keep(part, cols, c) : x.give(epi, T, r, c);
+                        } else {
+                            Sums<16, kForm> x;
+                            x.take(src + c, cols);
+                            x.taken();
+                            if (r < T.rows) part ? x.keep(part, cols, c) : x.give(epi, T, r, c);
+                        }
+                    }
+                }
+                free_acc();
             }
         }
     }
