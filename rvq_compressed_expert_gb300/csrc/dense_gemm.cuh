@@ -91,6 +91,9 @@ template <int kForm, int kCG> __device__ __forceinline__ Tile tile_at(const Gemm
     return o;
 }
 
+// A warp's common answer, which the compiler knows to be common.
+__device__ __forceinline__ bool all(bool v) { return __all_sync(0xffffffffu, v); }
+
 // One word in each translation unit that has kernels; read_and_clear_timeout reads its own.
 static __device__ uint32_t g_dense_timeout;
 
@@ -170,12 +173,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem_raw + 164);
     const uint32_t drain = bars + 168;
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // one value a warp, and known to be: the loops' addresses stay in uniform registers
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int BN = P.BN, S = kCG == 2 ? 1 : P.S;
     const uint32_t a_bytes = kBM * kRowBytes, b_bytes = stage_b_bytes(BN, kCG, kBmn);
     const uint32_t s_off = a_bytes + b_bytes, stage_bytes = stage_size(BN, kCG, kBmn, kKind == kMx4);
     const int nrt = (BN + 127) >> 7; // scale tiles of B
-    const int rank = kCG == 2 || S > 1 ? (int)tc::cluster_rank() : 0;
+    const int rank = kCG == 2 ? (int)(blockIdx.x & 1) : S > 1 ? (int)(blockIdx.x % S) : 0; // in the cluster
     const bool leads = kCG == 1 || rank == 0; // issues the MMAs
 
     if (tid == 0) {
@@ -201,7 +205,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     __syncthreads();
     if (kCG == 2) tc::cluster_sync(); // the other CTA's barriers are up
     tc::fence_after_sync();
-    const uint32_t tmem = *tmem_slot;
+    constexpr uint32_t tmem = 0; // all columns are this CTA's, so they start at the first
+    if (*tmem_slot != tmem && tid == 0) *abort_flag = 1;
     if (warp != 0) tc::grid_wait(); // warp 0's loader may have B's first pieces to ask for before
 
     const int kb0 = S > 1 ? (int)((long long)P.kb * rank / S) : 0;
@@ -273,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             const Tile T = tile_at<kForm, kCG>(P, t, rank);
             for (int kb = kb0; kb < kb1; ++kb) {
                 if (issued >= early) {
-                    if (!tc::mbar_wait(bar_empty + 8 * st, ph ^ 1)) {
+                    if (!all(tc::mbar_wait(bar_empty + 8 * st, ph ^ 1))) {
                         ok = false;
                         break;
                     }
@@ -326,14 +331,14 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             for (int t = tile0; t < P.tiles && ok; t += step, ++it) {
                 const int buf = P.nacc == 2 ? it & 1 : 0;
                 const uint32_t use = P.nacc == 2 ? it >> 1 : it;
-                if (!tc::mbar_wait(bar_acce + 8 * buf, (use & 1) ^ 1)) {
+                if (!all(tc::mbar_wait(bar_acce + 8 * buf, (use & 1) ^ 1))) {
                     ok = false;
                     break;
                 }
                 tc::fence_after_sync();
                 const uint32_t d = acc_at(buf);
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!tc::mbar_wait(bar_full + 8 * st, ph)) {
+                    if (!all(tc::mbar_wait(bar_full + 8 * st, ph))) {
                         ok = false;
                         break;
                     }
