@@ -106,6 +106,39 @@ static inline cudaError_t read_and_clear_timeout(uint32_t *out) {
     return e;
 }
 
+// One stage of 4-bit operands: its scale tiles to tensor memory (a pair: each CTA's A rows, and all
+// of B's, in both), and its MMAs, two to a half.  The scales have columns of their own for each
+// stage (the stage is full again only after the MMAs that read them are done).  left: k from here on.
+template <int kCG, int kNrt>
+__device__ __forceinline__ void issue_mx4(uint32_t d, uint64_t da, uint64_t db, uint32_t sf, uint64_t ds, uint32_t idesc,
+                                          int left, uint32_t acc) {
+    const uint32_t id1 = idesc | (2u << 4) | (2u << 29); // the upper byte pair of the scale words
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (h && left <= 128) return;
+        const uint32_t fa = sf + 4 * h, fb = sf + 8 + 4 * kNrt * h;
+#pragma unroll
+        for (int i = 0; i <= kNrt; ++i) {
+            const uint32_t to = i ? fb + 4 * (i - 1) : fa;
+            const uint64_t from = ds + (uint64_t)((1024 * i + 512 * h) >> 4);
+            if (kCG == 2)
+                tc::copy_scales_pair(to, from);
+            else
+                tc::copy_scales(to, from);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (j && left <= 128 * h + 64) return;
+            const uint64_t off = (uint64_t)(2 * (2 * h + j));
+            if (kCG == 2)
+                tc::mma_mx4_pair(d, da + off, db + off, j ? id1 : idesc, fa, fb, acc);
+            else
+                tc::mma_mx4(d, da + off, db + off, j ? id1 : idesc, fa, fb, acc);
+            acc = 1;
+        }
+    }
+}
+
 // v += the W floats at shared address src of each CTA of the cluster, in rank order; the loads of
 // up to eight ranks are in flight at once, 8 floats at a time.
 template <int W> __device__ __forceinline__ void add_ranks(uint32_t src, int S, float (&v)[W]) {
@@ -327,6 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             int st = 0, it = 0;
             uint32_t ph = 0;
             bool ok = true;
+            const uint64_t scales0 = tc::desc_scales(base + s_off);
             const uint64_t desc0 = tc::desc_sw128(base, kKind == kHalf ? 8192 : 16);
             for (int t = tile0; t < P.tiles && ok; t += step, ++it) {
                 const int buf = P.nacc == 2 ? it & 1 : 0;
@@ -357,36 +391,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                                     tc::mma_f16(d, dj, ej, P.idesc, acc);
                             }
                         } else {
-                            // scales to tensor memory (a pair: each CTA's A rows, and all of B's, in
-                            // both), columns of their own for each stage (the stage is full again
-                            // only after the MMAs that read them are done)
                             const uint32_t sf = tmem + P.nacc * BN + st * (8 + 8 * nrt);
-                            const uint64_t ds = tc::desc_scales(base + st * stage_bytes + s_off);
-                            const int steps = P.K - kb * 256;
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                if (128 * h >= steps) break;
-                                const uint32_t fa = sf + 4 * h, fb = sf + 8 + 4 * nrt * h;
-                                for (int i = 0; i <= nrt; ++i) {
-                                    const uint32_t to = i ? fb + 4 * (i - 1) : fa;
-                                    const uint64_t from = ds + (uint64_t)((1024 * i + 512 * h) >> 4);
-                                    if (kCG == 2)
-                                        tc::copy_scales_pair(to, from);
-                                    else
-                                        tc::copy_scales(to, from);
-                                }
-#pragma unroll
-                                for (int j = 0; j < 2; ++j) {
-                                    if (128 * h + 64 * j >= steps) break;
-                                    const uint32_t id = P.idesc | (j ? (2u << 4) | (2u << 29) : 0u);
-                                    const uint64_t off = (uint64_t)(2 * (2 * h + j));
-                                    const uint32_t acc = h > 0 || j > 0 || kb > kb0;
-                                    if (kCG == 2)
-                                        tc::mma_mx4_pair(d, da + off, db + off, id, fa, fb, acc);
-                                    else
-                                        tc::mma_mx4(d, da + off, db + off, id, fa, fb, acc);
-                                }
-                            }
+                            const uint64_t ds = scales0 + (uint64_t)((st * stage_bytes) >> 4);
+                            const int left = P.K - kb * 256;
+                            if (nrt == 2)
+                                issue_mx4<kCG, 2>(d, da, db, sf, ds, P.idesc, left, kb > kb0);
+                            else
+                                issue_mx4<kCG, 1>(d, da, db, sf, ds, P.idesc, left, kb > kb0);
                         }
                         commit(bar_empty + 8 * st);
                         if (kb + 1 == kb1) commit(bar_accf + 8 * buf);
