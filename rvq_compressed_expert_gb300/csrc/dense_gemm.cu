@@ -1,5 +1,6 @@
 // Host side of the dense operators' products: tensor maps, launch shapes, the timeout word.
 #include <algorithm>
+#include <atomic>
 
 #include "dense_gemm.cuh"
 
@@ -51,8 +52,48 @@ cudaError_t make_scale_map(CUtensorMap *m, const void *p, size_t tiles) {
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// The estimate: pieces of k one after another, each as long as its MMAs or as its bytes need into
-// one SM (about 100 B/ns), whole waves of tiles; splitting k costs the exchange of the sums.
+namespace {
+
+// Takes as much of an SM as the products' CTAs do, to ask how many clusters of them fit.
+__global__ void __launch_bounds__(kThreads, 1) cluster_probe_kernel() {}
+
+// Clusters of S CTAs (2..8) that run at once on the current device: SMs come in groups that a
+// cluster does not cross, so fewer than SMs / S (on one GB300: 76, 46, 36, 28, 23, 15, 15).
+int clusters_at_once(int S, int sms) {
+    static std::atomic<int> cache[kMaxDevices][9];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return sms / S / 2;
+    int n = cache[dev][S].load(std::memory_order_relaxed);
+    if (n == 0) {
+        static SmemAttr attr;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = S;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(S);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = kSmemBudget;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        if (ensure_smem(attr, reinterpret_cast<const void *>(cluster_probe_kernel), kSmemBudget) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, cluster_probe_kernel, &cfg) != cudaSuccess || n < 1) {
+            cudaGetLastError();
+            n = sms / S / 2;
+        }
+        cache[dev][S].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+} // namespace
+
+// The estimate, in ns: pieces of k one after another, each as long as its MMAs or as its bytes
+// need into one SM, for whole waves of tiles; the last tile's way out; for split k the exchange of
+// the sums, and only one wave (a second one waits for whole clusters to end: twice the time).  Its
+// constants are fitted to 1,308 measured launches (3 to 2048 rows, 256 to 7168 columns and k, both
+// kinds, every shape below): over these it picks a launch 2 % slower than the best one, in the
+// geometric mean.
 Plan plan(const int *M, const int *N, int n, int kb, bool pair, bool mx4, int sms) {
     Plan best{256, 1, 1};
     double best_t = 1e30;
@@ -62,21 +103,23 @@ Plan plan(const int *M, const int *N, int n, int kb, bool pair, bool mx4, int sm
         const int w = pair ? BN / 2 : BN, h = kBM * cg;
         long long tiles = 0;
         for (int i = 0; i < n; ++i) tiles += (long long)((M[i] + h - 1) / h) * ((N[i] + w - 1) / w);
-        const double mma = mx4 ? BN * 0.75 : BN * 1.08, feed = (rows + BN / cg) * 128.0 / 100.0;
-        const double piece = std::max(mma, feed);
-        const double out = 500.0 + rows * BN * 0.05; // the last tile's way out; the others' is hidden
-        const double waves = (double)((tiles * S * cg + sms - 1) / sms);
-        const double t = S == 1 ? waves * kb * piece + out
-                                : waves * (((kb + S - 1) / S) * piece + out + 1500.0 + rows * BN * 0.02);
-        if (t < best_t * 0.98) {
+        const int slots = S > 1 ? clusters_at_once(S, sms) : sms / cg;
+        const long long waves = (tiles + slots - 1) / slots;
+        if (S > 1 && waves > 1) return;
+        const double mma = BN * (mx4 ? 0.54 : 1.38), feed = (kBM + BN / cg) * kRowBytes / 109.0;
+        double t = (cg == 2 ? 1190.0 : 0.0) + (double)waves * ((kb + S - 1) / S) * std::max(std::max(mma, feed), 60.0) +
+                   rows * BN * 0.066;
+        if (S > 1) t += 1880.0 + rows * BN * 0.256;
+        if (t < best_t) {
             best_t = t;
             best = Plan{BN, S, cg};
         }
     };
     // 4-bit: whole scale tiles (128 rows) of each product; 16-bit: any multiple of 32
-    for (int BN = 256; BN >= (mx4 && pair ? 256 : 128); BN -= mx4 ? 128 : 32)
+    const int least = mx4 ? (pair ? 256 : 128) : 64;
+    for (int BN = 256; BN >= least; BN -= mx4 ? 128 : 32)
         if (rows == kBM) consider(BN, 2, 1);
-    for (int BN = 256; BN >= (mx4 && pair ? 256 : 128); BN -= 128)
+    for (int BN = 256; BN >= least; BN /= 2)
         for (int S = 1; S <= 8 && S <= kb; ++S) consider(BN, 1, S);
     return best;
 }
