@@ -88,12 +88,12 @@ int clusters_at_once(int S, int sms) {
 
 } // namespace
 
-// The estimate, in ns: pieces of k one after another, each as long as its MMAs or as its bytes
-// need into one SM, for whole waves of tiles; the last tile's way out; for split k the exchange of
-// the sums, and only one wave (a second one waits for whole clusters to end: twice the time).  Its
-// constants are fitted to 1,308 measured launches (3 to 2048 rows, 256 to 7168 columns and k, both
-// kinds, every shape below): over these it picks a launch 2 % slower than the best one, in the
-// geometric mean.
+// The estimate, in ns: whole waves of tiles, each as long as its bytes need into one SM (its MMAs
+// are shorter, or as long); the last tile's way out; for split k the exchange of the sums, and only
+// one wave (a second one waits for whole clusters to end: twice the time).  Its constants are
+// fitted to 1,713 measured launches (3 to 8192 rows, 256 to 7168 columns and k, both kinds, every
+// shape below): over these it picks a launch 1.6 % slower than the best one, in the geometric
+// mean.
 Plan plan(const int *M, const int *N, int n, int kb, bool pair, bool mx4, int sms) {
     Plan best{256, 1, 1};
     double best_t = 1e30;
@@ -106,10 +106,9 @@ Plan plan(const int *M, const int *N, int n, int kb, bool pair, bool mx4, int sm
         const int slots = S > 1 ? clusters_at_once(S, sms) : sms / cg;
         const long long waves = (tiles + slots - 1) / slots;
         if (S > 1 && waves > 1) return;
-        const double mma = BN * (mx4 ? 0.54 : 1.38), feed = (kBM + BN / cg) * kRowBytes / 109.0;
-        double t = (cg == 2 ? 1190.0 : 0.0) + (double)waves * ((kb + S - 1) / S) * std::max(std::max(mma, feed), 60.0) +
-                   rows * BN * 0.066;
-        if (S > 1) t += 1880.0 + rows * BN * 0.256;
+        const double piece = (kBM + BN / cg) * kRowBytes / 88.8;
+        double t = (cg == 2 ? 1370.0 : 0.0) + (double)waves * ((kb + S - 1) / S) * piece + rows * BN * 0.123;
+        if (S > 1) t += 2240.0 + rows * BN * 0.285;
         if (t < best_t) {
             best_t = t;
             best = Plan{BN, S, cg};

@@ -428,6 +428,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             const Tile T = tile_at<kForm, kCG>(P, t, rank);
             const int buf = P.nacc == 2 ? it & 1 : 0;
             const uint32_t use = P.nacc == 2 ? it >> 1 : it;
+            if constexpr (Epi::kAhead)
+                if (S == 1 && r < T.rows && half == 0) epi.ahead(T.m0 + r, T.n0, cols);
             bool ok = true;
             if (lane == 0) ok = tc::mbar_wait(bar_accf + 8 * buf, use & 1);
             ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -527,6 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
 }
 
 // ---- epilogues -----------------------------------------------------------------------------
+// ahead(m, n, cols) (kAhead): row m of a tile will be taken from column n on.
 // row<W>(p, m, n, c, c2): W consecutive sums of row m from column n of problem p (n a multiple
 // of W); columns at or past N are left out.
 
@@ -576,15 +579,15 @@ __device__ __forceinline__ void put_as(int dtype, void *out, size_t at, int n, i
     else
         put(static_cast<__half *>(out) + at, n, N, vec, add, v);
 }
-// 8 values of a 16-bit matrix
-__device__ __forceinline__ void get8(bool bf16, const void *src, size_t at, float (&v)[8]) {
+// 8 values of a 16-bit type
+__device__ __forceinline__ void widen8(bool bf16, const uint4 &q, float (&v)[8]) {
     if (bf16) {
-        Pack<__nv_bfloat16> p;
-        p.q = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(src) + at);
+        const Pack<__nv_bfloat16> p{q};
+#pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = p.get(i);
     } else {
-        Pack<__half> p;
-        p.q = *reinterpret_cast<const uint4 *>(static_cast<const __half *>(src) + at);
+        const Pack<__half> p{q};
+#pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = p.get(i);
     }
 }
@@ -595,6 +598,7 @@ __device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f +
 
 struct Store {
     static constexpr int kWidth = 8;
+    static constexpr bool kAhead = false;
     void *out[kMaxProb];
     int ld[kMaxProb];
     int dtype, add, vec;
@@ -607,6 +611,7 @@ struct Store {
 // a = silu(g) u; g and u kept if asked for.  f % 8 == 0, so rows hold whole 16-byte pieces.
 struct Gated {
     static constexpr int kWidth = 8;
+    static constexpr bool kAhead = false;
     void *a, *g, *u;
     int f, dtype;
     template <int W>
@@ -623,31 +628,48 @@ struct Gated {
     }
 };
 
-// da -> a, dg, du from the kept g and u.
+// da -> a, dg, du from the kept g and u, which are asked of L2 while the tile's product runs.
 struct GatedGrad {
     static constexpr int kWidth = 8;
+    static constexpr bool kAhead = true;
     const void *g, *u;
     void *a, *dg, *du;
     int f, dtype;
+    __device__ __forceinline__ void ahead(int m, int n, int cols) const {
+        const char *pg = static_cast<const char *>(g) + ((size_t)m * f + n) * 2;
+        const char *pu = static_cast<const char *>(u) + ((size_t)m * f + n) * 2;
+        const int bytes = min(cols, f - n) * 2;
+        for (int i = 0; i < bytes; i += 128) {
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(pg + i));
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(pu + i));
+        }
+    }
     template <int W>
     __device__ __forceinline__ void row(int, int m, int n, const float (&da)[W], const float (&)[W]) const {
+        const size_t at = (size_t)m * f + n;
+        const bool bf16 = dtype == WASTE_ACT_BF16;
+        uint4 qg[W / 8], qu[W / 8];
 #pragma unroll
-        for (int i = 0; i < W; i += 8) {
-            if (n + i >= f) break;
-            const size_t at = (size_t)m * f + n + i;
+        for (int i = 0; i < W / 8; ++i) {
+            const bool in = n + 8 * i < f; // f % 8 == 0
+            qg[i] = in ? *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(g) + at + 8 * i) : uint4{};
+            qu[i] = in ? *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(u) + at + 8 * i) : uint4{};
+        }
+#pragma unroll
+        for (int i = 0; i < W / 8; ++i) {
             float gv[8], uv[8], x[8], y[8], z[8];
-            get8(dtype == WASTE_ACT_BF16, g, at, gv);
-            get8(dtype == WASTE_ACT_BF16, u, at, uv);
+            widen8(bf16, qg[i], gv);
+            widen8(bf16, qu[i], uv);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float s = sigmoid(gv[j]), silu = gv[j] * s;
+                const float s = sigmoid(gv[j]), silu = gv[j] * s, da_ = da[8 * i + j];
                 x[j] = silu * uv[j];
-                y[j] = da[i + j] * uv[j] * s * (1.f + gv[j] * (1.f - s));
-                z[j] = da[i + j] * silu;
+                y[j] = da_ * uv[j] * s * (1.f + gv[j] * (1.f - s));
+                z[j] = da_ * silu;
             }
-            put_as(dtype, a, at, n + i, f, true, false, x);
-            put_as(dtype, dg, at, n + i, f, true, false, y);
-            put_as(dtype, du, at, n + i, f, true, false, z);
+            put_as(dtype, a, at + 8 * i, n + 8 * i, f, true, false, x);
+            put_as(dtype, dg, at + 8 * i, n + 8 * i, f, true, false, y);
+            put_as(dtype, du, at + 8 * i, n + 8 * i, f, true, false, z);
         }
     }
 };

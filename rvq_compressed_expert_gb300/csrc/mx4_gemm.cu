@@ -12,6 +12,7 @@ namespace {
 // that reads them multiplies them with zero codes.
 struct GatedMx4 {
     static constexpr int kWidth = 32;
+    static constexpr bool kAhead = false;
     uint8_t *codes, *scales;
     int f, kb;
     template <int W>
