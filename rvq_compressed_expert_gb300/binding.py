@@ -156,11 +156,7 @@ def load(path: str = LIB_PATH):
 
 
 def _ptr(x):
-    if x is None:
-        return None
-    if isinstance(x, int):
-        return x
-    return x.data_ptr()
+    return x if x is None or type(x) is int else x.data_ptr()
 
 
 def _stream(s):
@@ -364,17 +360,19 @@ def waste_ffn_workspace(cfg, T, backward=0) -> int:
 def waste_ffn_forward(cfg, d_x, T, d_w_gate, d_w_up, d_w_down, d_out, out_dtype, mode, d_g, d_u, workspace,
                       stream=None):
     """workspace: a uint8 tensor (its size is passed on)."""
-    return _check(load().waste_ffn_forward(
+    rc = (_lib or load()).waste_ffn_forward(
         ctypes.byref(cfg), _ptr(d_x), T, _ptr(d_w_gate), _ptr(d_w_up), _ptr(d_w_down), _ptr(d_out), out_dtype, mode,
-        _ptr(d_g), _ptr(d_u), workspace.data_ptr(), workspace.numel(), _stream(stream)))
+        _ptr(d_g), _ptr(d_u), workspace.data_ptr(), workspace.numel(), _stream(stream))
+    return rc and _check(rc)
 
 
 def waste_ffn_backward(cfg, d_dy, T, d_x, d_g, d_u, d_w_gate, d_w_up, d_w_down, d_dx, d_dw_gate, d_dw_up, d_dw_down,
                        grad_dtype, accumulate, workspace, stream=None):
-    return _check(load().waste_ffn_backward(
+    rc = (_lib or load()).waste_ffn_backward(
         ctypes.byref(cfg), _ptr(d_dy), T, _ptr(d_x), _ptr(d_g), _ptr(d_u), _ptr(d_w_gate), _ptr(d_w_up),
         _ptr(d_w_down), _ptr(d_dx), _ptr(d_dw_gate), _ptr(d_dw_up), _ptr(d_dw_down), grad_dtype, accumulate,
-        workspace.data_ptr(), workspace.numel(), _stream(stream)))
+        workspace.data_ptr(), workspace.numel(), _stream(stream))
+    return rc and _check(rc)
 
 
 def waste_mx4_layout(rows, cols):
@@ -385,18 +383,21 @@ def waste_mx4_layout(rows, cols):
 
 
 def waste_mx4_quantize(d_x, dtype, rows, cols, ld, d_codes, d_scales, stream=None):
-    return _check(load().waste_mx4_quantize(_ptr(d_x), dtype, rows, cols, ld, _ptr(d_codes), _ptr(d_scales),
-                                            _stream(stream)))
+    rc = (_lib or load()).waste_mx4_quantize(_ptr(d_x), dtype, rows, cols, ld, _ptr(d_codes), _ptr(d_scales),
+                                             _stream(stream))
+    return rc and _check(rc)
 
 
 def waste_mx4_dequantize(d_codes, d_scales, rows, cols, d_out, dtype, ld, stream=None):
-    return _check(load().waste_mx4_dequantize(_ptr(d_codes), _ptr(d_scales), rows, cols, _ptr(d_out), dtype, ld,
-                                              _stream(stream)))
+    rc = (_lib or load()).waste_mx4_dequantize(_ptr(d_codes), _ptr(d_scales), rows, cols, _ptr(d_out), dtype, ld,
+                                               _stream(stream))
+    return rc and _check(rc)
 
 
 def waste_mx4_matmul(M, N, K, d_a_codes, d_a_scales, d_b_codes, d_b_scales, d_out, out_dtype, mode=0, stream=None):
-    return _check(load().waste_mx4_matmul(M, N, K, _ptr(d_a_codes), _ptr(d_a_scales), _ptr(d_b_codes),
-                                          _ptr(d_b_scales), _ptr(d_out), out_dtype, mode, _stream(stream)))
+    rc = (_lib or load()).waste_mx4_matmul(M, N, K, _ptr(d_a_codes), _ptr(d_a_scales), _ptr(d_b_codes),
+                                           _ptr(d_b_scales), _ptr(d_out), out_dtype, mode, _stream(stream))
+    return rc and _check(rc)
 
 
 def waste_mx4_ffn_workspace(cfg, T) -> int:
@@ -406,5 +407,6 @@ def waste_mx4_ffn_workspace(cfg, T) -> int:
 
 
 def waste_mx4_ffn_forward(cfg, d_x, x_dtype, T, d_out, out_dtype, mode, workspace, stream=None):
-    return _check(load().waste_mx4_ffn_forward(ctypes.byref(cfg), _ptr(d_x), x_dtype, T, _ptr(d_out), out_dtype, mode,
-                                               workspace.data_ptr(), workspace.numel(), _stream(stream)))
+    rc = (_lib or load()).waste_mx4_ffn_forward(ctypes.byref(cfg), _ptr(d_x), x_dtype, T, _ptr(d_out), out_dtype, mode,
+                                                workspace.data_ptr(), workspace.numel(), _stream(stream))
+    return rc and _check(rc)
