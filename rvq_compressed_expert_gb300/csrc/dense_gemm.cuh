@@ -34,7 +34,8 @@ constexpr int kBM = 128;
 constexpr int kRowBytes = 128; // bytes of one row of a stage
 constexpr int kMaxStages = 8;
 constexpr int kMaxProb = 3;
-constexpr uint32_t kSmemBudget = 225 * 1024;
+constexpr uint32_t kSmemBudget = 227 * 1024;
+constexpr uint32_t kPieceBytes = 4096; // an epilogue warp's 32 rows x 128 bytes on their way out
 constexpr uint32_t kBarBytes = 256;
 constexpr int kThreads = 352; // loader, issuer, allocator, eight epilogue warps
 constexpr int kTmemCols = 512;
@@ -161,6 +162,13 @@ template <int W> __device__ __forceinline__ void add_ranks(uint32_t src, int S, 
     }
 }
 
+// An epilogue warp's 32 rows: the first, how many of them there are, and shared memory to turn
+// pieces of them round in.
+struct Out32 {
+    uint4 *turn;
+    int m, rows, lane;
+};
+
 // W columns of a row (kPair: of both products) from tensor memory to registers; complete after
 // taken().
 template <int W, int kForm> struct Sums {
@@ -186,17 +194,19 @@ template <int W, int kForm> struct Sums {
             if constexpr (kForm == kPair) part[(cols + c) / 4 + i] = *reinterpret_cast<const float4 *>(&w[4 * i]);
         }
     }
-    template <class Epi> __device__ __forceinline__ void give(const Epi &epi, const Tile &T, int r, int c) const {
+    // 32 rows (the warp's) from row m on, `rows` of them valid
+    template <class Epi>
+    __device__ __forceinline__ void give(const Epi &epi, const Tile &T, const Out32 &o, int c) const {
         const auto &x = *reinterpret_cast<const float(*)[W]>(v);
         if constexpr (kForm == kPair)
-            epi.template row<W>(T.p, T.m0 + r, T.n0 + c, x, *reinterpret_cast<const float(*)[W]>(w));
+            epi.template tile<W>(o, T.p, T.n0 + c, x, *reinterpret_cast<const float(*)[W]>(w));
         else
-            epi.template row<W>(T.p, T.m0 + r, T.n0 + c, x, x);
+            epi.template tile<W>(o, T.p, T.n0 + c, x, x);
     }
 };
 
 template <int kCG, int kKind, int kForm, bool kAmn, bool kBmn, class Epi>
-__global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs P, const Epi epi) {
+__global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs P, const __grid_constant__ Epi epi) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t smem0 = tc::smem_u32(smem_raw);
     const uint32_t base = (smem0 + kBarBytes + 1023) & ~1023u; // stages
@@ -450,6 +460,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 }
             };
             const bool any = 32 * q < T.rows;
+            const Out32 out{reinterpret_cast<uint4 *>(smem_raw + (base - smem0) + P.stages * stage_bytes) +
+                                (warp - 3) * (kPieceBytes / 16),
+                            T.m0 + 32 * q, T.rows - 32 * q, lane};
             if constexpr (kKind == kMx4) {
                 // one accumulator (the other's place holds scales): all of it to registers first,
                 // so that the next tile's MMAs wait for the reading alone
@@ -464,15 +477,15 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                         if (64 * i + 32 * half < cols) x[i].taken();
                 }
                 free_acc();
-                if (any && r < T.rows) {
+                if (any) {
 #pragma unroll
                     for (int i = 0; i < kHeld; ++i) {
                         const int c = 64 * i + 32 * half;
                         if (c >= cols) break;
-                        if (part)
+                        if (!part)
+                            x[i].give(epi, T, out, c);
+                        else if (r < T.rows)
                             x[i].keep(part, cols, c);
-                        else
-                            x[i].give(epi, T, r, c);
                     }
                 }
             } else {
@@ -482,12 +495,18 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                             Sums<32, kForm> x;
                             x.take(src + c, cols);
                             x.taken();
-                            if (r < T.rows) part ? x.keep(part, cols, c) : x.give(epi, T, r, c);
+                            if (!part)
+                                x.give(epi, T, out, c);
+                            else if (r < T.rows)
+                                x.keep(part, cols, c);
                         } else {
                             Sums<16, kForm> x;
                             x.take(src + c, cols);
                             x.taken();
-                            if (r < T.rows) part ? x.keep(part, cols, c) : x.give(epi, T, r, c);
+                            if (!part)
+                                x.give(epi, T, out, c);
+                            else if (r < T.rows)
+                                x.keep(part, cols, c);
                         }
                     }
                 }
@@ -529,9 +548,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
 }
 
 // ---- epilogues -----------------------------------------------------------------------------
-// ahead(m, n, cols) (kAhead): row m of a tile will be taken from column n on.
+// kTurns: tile() needs the shared memory of Out32.  ahead(m, n, cols) (kAhead): row m of a tile will be taken from column n on.
 // row<W>(p, m, n, c, c2): W consecutive sums of row m from column n of problem p (n a multiple
-// of W); columns at or past N are left out.
+// of W); columns at or past N are left out.  tile<W>(o, p, n, c, c2): the same for the 32 rows of
+// a warp, lane = row, all lanes together.
 
 template <class O> __device__ __forceinline__ O round_to(float v);
 template <> __device__ __forceinline__ __nv_bfloat16 round_to<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
@@ -544,6 +564,22 @@ template <class O> struct Pack {
     __device__ float get(int i) const { return (float)reinterpret_cast<const O *>(&q)[i]; }
 };
 
+// A 16-byte piece of rounded values, two at a time where the type allows.
+__device__ __forceinline__ uint4 piece_of(const float *v, float) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+}
+__device__ __forceinline__ uint32_t two(float a, float b, __nv_bfloat16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t two(float a, float b, __half) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+template <class O> __device__ __forceinline__ uint4 piece_of(const float *v, O t) {
+    return make_uint4(two(v[0], v[1], t), two(v[2], v[3], t), two(v[4], v[5], t), two(v[6], v[7], t));
+}
+
 // W values to p[0..W) (columns n..): whole 16-byte pieces where the row allows, add: to what is there.
 template <class O, int W>
 __device__ __forceinline__ void put(O *p, int n, int N, bool vec, bool add, const float (&v)[W]) {
@@ -552,16 +588,12 @@ __device__ __forceinline__ void put(O *p, int n, int N, bool vec, bool add, cons
 #pragma unroll
     for (int i = 0; i < W; i += kPer) {
         if (vec && n + i + kPer <= N) {
+            float w[kPer];
             Pack<O> o;
-            if (add) {
-                o.q = *reinterpret_cast<const uint4 *>(p + i);
+            if (add) o.q = *reinterpret_cast<const uint4 *>(p + i);
 #pragma unroll
-                for (int j = 0; j < kPer; ++j) o.set(j, o.get(j) + v[i + j]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < kPer; ++j) o.set(j, v[i + j]);
-            }
-            *reinterpret_cast<uint4 *>(p + i) = o.q;
+            for (int j = 0; j < kPer; ++j) w[j] = add ? o.get(j) + v[i + j] : v[i + j];
+            *reinterpret_cast<uint4 *>(p + i) = piece_of(w, O());
         } else {
 #pragma unroll
             for (int j = 0; j < kPer; ++j)
@@ -579,6 +611,76 @@ __device__ __forceinline__ void put_as(int dtype, void *out, size_t at, int n, i
     else
         put(static_cast<__half *>(out) + at, n, N, vec, add, v);
 }
+// The same for the 32 rows of a warp, lane = row: the values cross through shared memory so that
+// consecutive lanes store consecutive 16-byte pieces of a row (64 or 128 bytes of each row at
+// once; a lane storing its own row touches 32 rows with every instruction).
+__device__ __forceinline__ int turned(int row, int piece, int pieces) {
+    // pieces is 2, 4 or 8; permuted so that neither the writes (lane = row) nor the reads (lane =
+    // piece) meet in a bank
+    return row * pieces + (piece ^ ((row * pieces >> 3) & (pieces - 1)));
+}
+template <class O, int W>
+__device__ __forceinline__ void put32(const Out32 &o, O *out, size_t ld, int n, int N, bool vec, bool add,
+                                      const float (&v)[W]) {
+    constexpr int kPer = 16 / (int)sizeof(O), kPieces = W / kPer;
+    if (sizeof(O) == 2 && add) { // the sum is rounded once: each lane its own row
+        if (o.lane < o.rows) put(out + (size_t)(o.m + o.lane) * ld + n, n, N, vec, true, v);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) o.turn[turned(o.lane, i, kPieces)] = piece_of(v + kPer * i, O());
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+        const int at = 32 * i + o.lane, row = at / kPieces, piece = at % kPieces, c = n + kPer * piece;
+        Pack<O> x;
+        x.q = o.turn[turned(row, piece, kPieces)];
+        O *p = out + (size_t)(o.m + row) * ld + c;
+        if (row >= o.rows) continue;
+        if (vec && c + kPer <= N) {
+            if (add) {
+                Pack<O> y;
+                y.q = *reinterpret_cast<const uint4 *>(p);
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) x.set(j, y.get(j) + x.get(j));
+            }
+            *reinterpret_cast<uint4 *>(p) = x.q;
+        } else {
+#pragma unroll
+            for (int j = 0; j < kPer; ++j)
+                if (c + j < N) p[j] = round_to<O>(add ? (float)p[j] + x.get(j) : x.get(j));
+        }
+    }
+    __syncwarp();
+}
+template <int W>
+__device__ __forceinline__ void put32_as(int dtype, const Out32 &o, void *out, size_t ld, int n, int N, bool vec, bool add,
+                                         const float (&v)[W]) {
+    if (dtype == WASTE_ACT_F32)
+        put32(o, static_cast<float *>(out), ld, n, N, vec, add, v);
+    else if (dtype == WASTE_ACT_BF16)
+        put32(o, static_cast<__nv_bfloat16 *>(out), ld, n, N, vec, add, v);
+    else
+        put32(o, static_cast<__half *>(out), ld, n, N, vec, add, v);
+}
+// W columns of a 16-bit matrix for the 32 rows of a warp, lane = row (rows of N % 8 == 0 columns;
+// zeros past the ends).
+template <int W>
+__device__ __forceinline__ void get32(const Out32 &o, const void *src, size_t ld, int n, int N, uint4 (&q)[W / 8]) {
+    constexpr int kPieces = W / 8;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+        const int at = 32 * i + o.lane, row = at / kPieces, piece = at % kPieces, c = n + 8 * piece;
+        const bool in = row < o.rows && c < N;
+        const uint16_t *p = static_cast<const uint16_t *>(src) + (size_t)(o.m + row) * ld + c;
+        o.turn[turned(row, piece, kPieces)] = in ? *reinterpret_cast<const uint4 *>(p) : uint4{};
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) q[i] = o.turn[turned(o.lane, i, kPieces)];
+    __syncwarp();
+}
+
 // 8 values of a 16-bit type
 __device__ __forceinline__ void widen8(bool bf16, const uint4 &q, float (&v)[8]) {
     if (bf16) {
@@ -598,19 +700,31 @@ __device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f +
 
 struct Store {
     static constexpr int kWidth = 8;
+    static constexpr bool kTurns = true;
     static constexpr bool kAhead = false;
     void *out[kMaxProb];
     int ld[kMaxProb];
     int dtype, add, vec;
+    // selected, not indexed: an index would put a copy of the whole in local memory, whose loads
+    // miss the little L1 that the stages leave
+    __device__ __forceinline__ void *to(int p) const { return p == 0 ? out[0] : p == 1 ? out[1] : out[2]; }
+    __device__ __forceinline__ int row_of(int p) const { return p == 0 ? ld[0] : p == 1 ? ld[1] : ld[2]; }
     template <int W>
     __device__ __forceinline__ void row(int p, int m, int n, const float (&c)[W], const float (&)[W]) const {
-        put_as(dtype, out[p], (size_t)m * ld[p] + n, n, ld[p], vec, add, c);
+        const int w = row_of(p);
+        put_as(dtype, to(p), (size_t)m * w + n, n, w, vec, add, c);
+    }
+    template <int W>
+    __device__ __forceinline__ void tile(const Out32 &o, int p, int n, const float (&c)[W], const float (&)[W]) const {
+        const int w = row_of(p);
+        put32_as(dtype, o, to(p), w, n, w, vec, add, c);
     }
 };
 
 // a = silu(g) u; g and u kept if asked for.  f % 8 == 0, so rows hold whole 16-byte pieces.
 struct Gated {
     static constexpr int kWidth = 8;
+    static constexpr bool kTurns = true;
     static constexpr bool kAhead = false;
     void *a, *g, *u;
     int f, dtype;
@@ -626,11 +740,23 @@ struct Gated {
             put_as(dtype, u, at, n, f, true, false, cu);
         }
     }
+    template <int W>
+    __device__ __forceinline__ void tile(const Out32 &o, int, int n, const float (&cg)[W], const float (&cu)[W]) const {
+        float v[W];
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[i] = cg[i] * sigmoid(cg[i]) * cu[i];
+        put32_as(dtype, o, a, f, n, f, true, false, v);
+        if (g) {
+            put32_as(dtype, o, g, f, n, f, true, false, cg);
+            put32_as(dtype, o, u, f, n, f, true, false, cu);
+        }
+    }
 };
 
 // da -> a, dg, du from the kept g and u, which are asked of L2 while the tile's product runs.
 struct GatedGrad {
     static constexpr int kWidth = 8;
+    static constexpr bool kTurns = true;
     static constexpr bool kAhead = true;
     const void *g, *u;
     void *a, *dg, *du;
@@ -644,33 +770,43 @@ struct GatedGrad {
             asm volatile("prefetch.global.L2 [%0];" ::"l"(pu + i));
         }
     }
+    // one piece of 8 columns: a, dg and du
+    __device__ __forceinline__ void grads(const uint4 &qg, const uint4 &qu, const float *da, float *x, float *y,
+                                          float *z) const {
+        float gv[8], uv[8];
+        widen8(dtype == WASTE_ACT_BF16, qg, gv);
+        widen8(dtype == WASTE_ACT_BF16, qu, uv);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float s = sigmoid(gv[j]), silu = gv[j] * s;
+            x[j] = silu * uv[j];
+            y[j] = da[j] * uv[j] * s * (1.f + gv[j] * (1.f - s));
+            z[j] = da[j] * silu;
+        }
+    }
     template <int W>
     __device__ __forceinline__ void row(int, int m, int n, const float (&da)[W], const float (&)[W]) const {
+        static_assert(W == 8, "one piece");
+        if (n >= f) return; // f % 8 == 0
         const size_t at = (size_t)m * f + n;
-        const bool bf16 = dtype == WASTE_ACT_BF16;
+        float x[8], y[8], z[8];
+        grads(*reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(g) + at),
+              *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(u) + at), da, x, y, z);
+        put_as(dtype, a, at, n, f, true, false, x);
+        put_as(dtype, dg, at, n, f, true, false, y);
+        put_as(dtype, du, at, n, f, true, false, z);
+    }
+    template <int W>
+    __device__ __forceinline__ void tile(const Out32 &o, int, int n, const float (&da)[W], const float (&)[W]) const {
         uint4 qg[W / 8], qu[W / 8];
+        get32<W>(o, g, f, n, f, qg);
+        get32<W>(o, u, f, n, f, qu);
+        float x[W], y[W], z[W];
 #pragma unroll
-        for (int i = 0; i < W / 8; ++i) {
-            const bool in = n + 8 * i < f; // f % 8 == 0
-            qg[i] = in ? *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(g) + at + 8 * i) : uint4{};
-            qu[i] = in ? *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(u) + at + 8 * i) : uint4{};
-        }
-#pragma unroll
-        for (int i = 0; i < W / 8; ++i) {
-            float gv[8], uv[8], x[8], y[8], z[8];
-            widen8(bf16, qg[i], gv);
-            widen8(bf16, qu[i], uv);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float s = sigmoid(gv[j]), silu = gv[j] * s, da_ = da[8 * i + j];
-                x[j] = silu * uv[j];
-                y[j] = da_ * uv[j] * s * (1.f + gv[j] * (1.f - s));
-                z[j] = da_ * silu;
-            }
-            put_as(dtype, a, at + 8 * i, n + 8 * i, f, true, false, x);
-            put_as(dtype, dg, at + 8 * i, n + 8 * i, f, true, false, y);
-            put_as(dtype, du, at + 8 * i, n + 8 * i, f, true, false, z);
-        }
+        for (int i = 0; i < W / 8; ++i) grads(qg[i], qu[i], da + 8 * i, x + 8 * i, y + 8 * i, z + 8 * i);
+        put32_as(dtype, o, a, f, n, f, true, false, x);
+        put32_as(dtype, o, dg, f, n, f, true, false, y);
+        put32_as(dtype, o, du, f, n, f, true, false, z);
     }
 };
 
@@ -714,14 +850,15 @@ cudaError_t launch_gemm_as(GemmArgs &G, const Epi &epi, int sms, cudaStream_t s)
     static SmemAttr attr;
     const auto kernel = gemm_kernel<kCG, kKind, kForm, kAmn, kBmn, Epi>;
     const uint32_t stage = stage_size(G.BN, kCG, kBmn, kKind == kMx4);
-    G.stages = (int)((kSmemBudget - kBarBytes - 1024) / stage);
+    const uint32_t turn = Epi::kTurns ? 8 * kPieceBytes : 0;
+    G.stages = (int)((kSmemBudget - kBarBytes - 1024 - turn) / stage);
     if (G.stages > kMaxStages) G.stages = kMaxStages;
     G.nacc = 2;
     if (kKind == kMx4) { // the stages' scales take tensor memory too
         const int per = 8 + 8 * ((G.BN + 127) / 128);
         if (2 * G.BN + G.stages * per > kTmemCols) G.nacc = 1;
     }
-    const uint32_t smem = kBarBytes + 1024 + G.stages * stage;
+    const uint32_t smem = kBarBytes + 1024 + G.stages * stage + turn;
     cudaError_t e = ensure_smem(attr, reinterpret_cast<const void *>(kernel), (int)smem);
     if (e != cudaSuccess) return e;
     // The launch may begin while the kernel before it in the stream ends (grid_wait holds back

@@ -12,7 +12,7 @@ namespace {
 // that reads them multiplies them with zero codes.
 struct GatedMx4 {
     static constexpr int kWidth = 32;
-    static constexpr bool kAhead = false;
+    static constexpr bool kTurns = false, kAhead = false;
     uint8_t *codes, *scales;
     int f, kb;
     template <int W>
@@ -28,6 +28,10 @@ struct GatedMx4 {
         *reinterpret_cast<uint4 *>(codes + (size_t)m * (f / 2) + n / 2) = make_uint4(w[0], w[1], w[2], w[3]);
         if (n + W == f)
             for (int b = n / kMxBlock + 1, j = 1; b & 3; ++b, ++j) sp[j] = 0;
+    }
+    template <int W>
+    __device__ __forceinline__ void tile(const Out32 &o, int p, int n, const float (&g)[W], const float (&u)[W]) const {
+        if (o.lane < o.rows) row<W>(p, o.m + o.lane, n, g, u);
     }
 };
 
