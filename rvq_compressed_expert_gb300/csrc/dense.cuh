@@ -44,8 +44,11 @@ struct Mx4Mat {
 
 // Calls of at most so many tokens take the kernels that read the weights straight into registers
 // (dense_gemv.cu); their a is fp32 in the workspace.
-constexpr int kGemvTokens = 2;
+constexpr int kGemvTokens = 1;
 constexpr int kMxGemvTokens = 2;
+// Calls of at most so many tokens keep what rounding a to 16 bits leaves too (twice the columns of
+// a product that the weights' way from memory bounds).
+constexpr int kSplitTokens = 32;
 // Shared memory in which those of 4-bit weights stage nt rows of n quantised values.
 __host__ __device__ inline size_t mx_gemv_smem(int n, int nt) { return (size_t)nt * (n * 2 + (n / 32 + 15) / 16 * 16); }
 constexpr size_t kMxGemvSmem = 48 << 10; // what a kernel may take without asking

@@ -57,10 +57,11 @@ int check_ffn(const waste_ffn_config *c, int32_t T) {
     return WASTE_OK;
 }
 
-// One [T][f] buffer of the workspace; a forward call of few tokens keeps fp32 in it, so the size
-// for T tokens also covers every smaller call.
+// One [T][f] buffer of the workspace; a forward call of few tokens keeps 32 bits of each value in
+// it, so the size for T tokens also covers every smaller call.
+static_assert(kGemvTokens <= kSplitTokens, "32 bits of a");
 size_t ffn_part(const waste_ffn_config *c, int32_t T) {
-    const size_t few = T < kGemvTokens ? T : kGemvTokens, half = (size_t)T * c->f * 2, full = few * c->f * 4;
+    const size_t few = T < kSplitTokens ? T : kSplitTokens, half = (size_t)T * c->f * 2, full = few * c->f * 4;
     return round_up(half > full ? half : full, 256);
 }
 

@@ -8,7 +8,7 @@
 //           3. dWg = dg^T x, dWu = du^T x, dWd = dy^T a, three products of T terms in one launch.
 // Where a product runs over a matrix's rows (Wd, Wg, Wu in 1 and 2, everything in 3) the tiles go
 // to the tensor core MN-major, as they lie in memory: nothing is transposed.
-#include "dense_gemm.cuh"
+#include "dense_skinny.cuh"
 
 namespace wm {
 namespace dense {
@@ -21,10 +21,78 @@ cudaError_t half_map(CUtensorMap *m, const void *p, int rows, int cols, int box_
     return make_map(m, p, 2, rows, (size_t)cols * 2, box_rows);
 }
 
+// a in two 16-bit parts: its rounding and what that left, one above the other.
+struct GatedSplit {
+    static constexpr int kWidth = 8;
+    void *hi, *lo, *g, *u;
+    int f, dtype;
+    template <int W>
+    __device__ __forceinline__ void row(int, int m, int n, const float (&cg)[W], const float (&cu)[W]) const {
+        const size_t at = (size_t)m * f + n;
+        float v[W], r[W];
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            v[i] = cg[i] * sigmoid(cg[i]) * cu[i];
+            r[i] = v[i] - (dtype == WASTE_ACT_BF16 ? (float)__float2bfloat16_rn(v[i]) : (float)__float2half_rn(v[i]));
+        }
+        put_as(dtype, hi, at, n, f, true, false, v);
+        if (lo) put_as(dtype, lo, at, n, f, true, false, r);
+        if (g) {
+            put_as(dtype, g, at, n, f, true, false, cg);
+            put_as(dtype, u, at, n, f, true, false, cu);
+        }
+    }
+};
+
+SkinnyArgs skinny(int T, int N, int K) {
+    SkinnyArgs G = {};
+    G.T = T;
+    G.N = N;
+    G.npad = (T + 15) / 16 * 16;
+    G.kb = G.kb_seg = pieces(K);
+    return G;
+}
+
+cudaError_t forward_skinny(const FfnFwd &P, cudaStream_t s) {
+    const int sms = device_sm_count();
+    const bool bf16 = P.dtype == WASTE_ACT_BF16, split = P.T <= kSplitTokens;
+    void *lo = split ? static_cast<uint16_t *>(P.a) + (size_t)P.T * P.f : nullptr;
+    cudaError_t e;
+    {
+        SkinnyArgs G = skinny(P.T, P.f, P.d);
+        if ((e = half_map(&G.ta[0], P.wg, P.f, P.d, kBM)) != cudaSuccess) return e;
+        if ((e = half_map(&G.ta[1], P.wu, P.f, P.d, kBM)) != cudaSuccess) return e;
+        if ((e = half_map(&G.tb[0], P.x, P.T, P.d, G.npad)) != cudaSuccess) return e;
+        // bound by the weights' way from memory, which the next kernel's can follow at once while
+        // this one adds up and ends
+        const size_t wd = (size_t)P.d * P.f * 2;
+        if (wd <= kAheadMost) {
+            G.ahead = static_cast<const uint8_t *>(P.wd);
+            G.ahead_bytes = wd;
+        }
+        e = launch_skinny<kPair, false>(G, bf16, GatedSplit{P.a, lo, P.g, P.u, P.f, P.dtype}, sms, s);
+        if (e != cudaSuccess) return e;
+    }
+    SkinnyArgs G = skinny(P.T, P.d, P.f);
+    G.early_w = 1;
+    G.lo = split;
+    if ((e = half_map(&G.ta[0], P.wd, P.d, P.f, kBM)) != cudaSuccess) return e;
+    if ((e = half_map(&G.tb[0], P.a, P.T, P.f, G.npad)) != cudaSuccess) return e;
+    if (split && (e = half_map(&G.tb[1], lo, P.T, P.f, G.npad)) != cudaSuccess) return e;
+    Store st = {};
+    st.out[0] = P.out;
+    st.ld[0] = P.d;
+    st.dtype = P.out_dtype;
+    st.add = P.mode;
+    st.vec = 1; // d % 8 == 0
+    return launch_skinny<kOne, false>(G, bf16, st, sms, s);
+}
+
 } // namespace
 
 cudaError_t launch_ffn_forward(const FfnFwd &P, cudaStream_t s) {
     if (P.T <= kGemvTokens) return launch_ffn_gemv(P, s);
+    if (P.T <= kSkinnyTokens) return forward_skinny(P, s);
     const int sms = device_sm_count();
     const bool bf16 = P.dtype == WASTE_ACT_BF16;
     cudaError_t e;
@@ -68,9 +136,16 @@ cudaError_t launch_ffn_forward(const FfnFwd &P, cudaStream_t s) {
 
 cudaError_t launch_ffn_backward(const FfnBwd &P, cudaStream_t s) {
     const int sms = device_sm_count();
-    const bool bf16 = P.dtype == WASTE_ACT_BF16;
+    const bool bf16 = P.dtype == WASTE_ACT_BF16, few = P.T <= kSkinnyTokens;
+    const GatedGrad grad{P.g, P.u, P.a, P.dg, P.du, P.f, P.dtype};
     cudaError_t e;
-    {
+    if (few) {
+        SkinnyArgs G = skinny(P.T, P.f, P.d);
+        if ((e = half_map(&G.ta[0], P.wd, P.d, P.f, 64)) != cudaSuccess) return e;
+        if ((e = half_map(&G.tb[0], P.dy, P.T, P.d, G.npad)) != cudaSuccess) return e;
+        e = launch_skinny<kOne, true>(G, bf16, grad, sms, s);
+        if (e != cudaSuccess) return e;
+    } else {
         GemmArgs G = {};
         G.K = P.d;
         G.kb = G.kb_seg = pieces(P.d);
@@ -79,10 +154,26 @@ cudaError_t launch_ffn_backward(const FfnBwd &P, cudaStream_t s) {
         G.idesc = tc::idesc_half(kBM * L.cg, G.BN, bf16, false, true);
         if ((e = half_map(&G.ta[0], P.dy, P.T, P.d, kBM)) != cudaSuccess) return e;
         if ((e = half_map(&G.tb[0], P.wd, P.d, P.f, 64)) != cudaSuccess) return e;
-        e = launch_gemm<kHalf, kOne, false, true>(G, L, GatedGrad{P.g, P.u, P.a, P.dg, P.du, P.f, P.dtype}, sms, s);
+        e = launch_gemm<kHalf, kOne, false, true>(G, L, grad, sms, s);
         if (e != cudaSuccess) return e;
     }
-    if (P.dx) {
+    if (P.dx && few) {
+        SkinnyArgs G = skinny(P.T, P.d, P.f);
+        G.kb = 2 * G.kb_seg;
+        G.early_w = 1;
+        const void *w[2] = {P.wg, P.wu}, *t[2] = {P.dg, P.du};
+        for (int i = 0; i < 2; ++i) {
+            if ((e = half_map(&G.ta[i], w[i], P.f, P.d, 64)) != cudaSuccess) return e;
+            if ((e = half_map(&G.tb[i], t[i], P.T, P.f, G.npad)) != cudaSuccess) return e;
+        }
+        Store st = {};
+        st.out[0] = P.dx;
+        st.ld[0] = P.d;
+        st.dtype = P.dtype;
+        st.vec = 1;
+        e = launch_skinny<kSum, true>(G, bf16, st, sms, s);
+        if (e != cudaSuccess) return e;
+    } else if (P.dx) {
         GemmArgs G = {};
         G.K = P.f;
         G.kb_seg = pieces(P.f);

@@ -53,9 +53,9 @@ cudaError_t make_scale_map(CUtensorMap *m, const void *p, size_t tiles) {
 }
 
 namespace {
-
 // Takes as much of an SM as the products' CTAs do, to ask how many clusters of them fit.
 __global__ void __launch_bounds__(kThreads, 1) cluster_probe_kernel() {}
+} // namespace
 
 // Clusters of S CTAs (2..8) that run at once on the current device: SMs come in groups that a
 // cluster does not cross, so fewer than SMs / S (on one GB300: 76, 46, 36, 28, 23, 15, 15).
@@ -85,8 +85,6 @@ int clusters_at_once(int S, int sms) {
     }
     return n;
 }
-
-} // namespace
 
 // The estimate, in ns: whole waves of tiles, each as long as its bytes need into one SM (its MMAs
 // are shorter, or as long); the last tile's way out; for split k the exchange of the sums, and only

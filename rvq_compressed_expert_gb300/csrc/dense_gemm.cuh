@@ -828,6 +828,7 @@ cudaError_t make_scale_map(CUtensorMap *m, const void *p, size_t tiles);
 struct Plan {
     int BN, S, cg;
 };
+int clusters_at_once(int S, int sms); // clusters of S CTAs that run at once
 Plan plan(const int *M, const int *N, int n, int kb, bool pair, bool mx4, int sms);
 
 // Fills in the plan and the tiles.

@@ -73,71 +73,79 @@ __device__ __forceinline__ void put_as(int dtype, void *out, size_t at, float v,
         put<__half>(out, at, v, add);
 }
 
-// ---- 16-bit weights --------------------------------------------------------------------------
+// ---- 16-bit weights, one token ---------------------------------------------------------------
 
-template <class T, int NT>
-__global__ void __launch_bounds__(kThreads) gate_up_kernel(const T *__restrict__ x, const T *__restrict__ wg,
-                                                           const T *__restrict__ wu, float *__restrict__ a,
-                                                           T *__restrict__ g, T *__restrict__ u, int T_, int d, int f) {
-    constexpr int U = 4; // pieces of each row in flight
-    const int lane = threadIdx.x & 31, col = blockIdx.x * kWarps + (threadIdx.x >> 5);
+constexpr int kQuarters = 4; // warps that share a column's k in gate_up
+constexpr int kPieces = 7;   // pieces of 256 k of each row in flight in a warp (gate_up)
+constexpr int kRowPieces = 6; // the same of each row in down
+
+// A warp takes a quarter of one column's k; the quarters meet in shared memory.  With a column a
+// warp the two rows of 28 pieces were four loads deep: 18.5 us for the 44 MB of d 7168, f 1536.
+template <class T>
+__global__ void __launch_bounds__(2 * kQuarters * 32) gate_up_kernel(const T *__restrict__ x, const T *__restrict__ wg,
+                                                                     const T *__restrict__ wu, float *__restrict__ a,
+                                                                     T *__restrict__ g, T *__restrict__ u, int d, int f) {
+    __shared__ float2 sums[2][kQuarters];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quarter = warp % kQuarters, which = warp / kQuarters;
+    const int col = blockIdx.x * 2 + which;
     tc::grid_wait();
     tc::grid_release();
-    if (col >= f) return;
-    const T *pg = wg + (size_t)col * d, *pu = wu + (size_t)col * d;
-    float sg[NT] = {}, su[NT] = {};
-    for (int k0 = lane * 8; k0 < d; k0 += 256 * U) {
-        uint4 qg[U], qu[U];
+    const int all = (d + 255) / 256, first = all * quarter / kQuarters, last = all * (quarter + 1) / kQuarters;
+    float sg = 0.f, su = 0.f;
+    if (col < f) {
+        const T *pg = wg + (size_t)col * d, *pu = wu + (size_t)col * d;
+        for (int p0 = first; p0 < last; p0 += kPieces) {
+            uint4 qg[kPieces], qu[kPieces];
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int k = k0 + 256 * i;
-            qg[i] = k < d ? load_stream(pg + k) : make_uint4(0, 0, 0, 0);
-            qu[i] = k < d ? load_stream(pu + k) : make_uint4(0, 0, 0, 0);
-        }
+            for (int i = 0; i < kPieces; ++i) {
+                const int k = (p0 + i) * 256 + lane * 8;
+                const bool in = p0 + i < last && k < d;
+                qg[i] = in ? load_stream(pg + k) : make_uint4(0, 0, 0, 0);
+                qu[i] = in ? load_stream(pu + k) : make_uint4(0, 0, 0, 0);
+            }
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int k = k0 + 256 * i;
-            if (k >= d) break;
-            float vg[8], vu[8];
-            widen8<T>(qg[i], vg);
-            widen8<T>(qu[i], vu);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                if (t >= T_) break;
-                float vx[8];
-                widen8<T>(__ldg(reinterpret_cast<const uint4 *>(x + (size_t)t * d + k)), vx);
+            for (int i = 0; i < kPieces; ++i) {
+                const int k = (p0 + i) * 256 + lane * 8;
+                if (p0 + i >= last || k >= d) break;
+                float vg[8], vu[8], vx[8];
+                widen8<T>(qg[i], vg);
+                widen8<T>(qu[i], vu);
+                widen8<T>(__ldg(reinterpret_cast<const uint4 *>(x + k)), vx);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    sg[t] = fmaf(vg[j], vx[j], sg[t]);
-                    su[t] = fmaf(vu[j], vx[j], su[t]);
+                    sg = fmaf(vg[j], vx[j], sg);
+                    su = fmaf(vu[j], vx[j], su);
                 }
             }
         }
     }
+    sg = add_lanes(sg);
+    su = add_lanes(su);
+    if (lane == 0) sums[which][quarter] = make_float2(sg, su);
+    __syncthreads();
+    if (quarter || lane || col >= f) return;
+    float cg = 0.f, cu = 0.f;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const float cg = add_lanes(sg[t]), cu = add_lanes(su[t]);
-        if (lane == t && t < T_) {
-            const size_t at = (size_t)t * f + col;
-            a[at] = silu(cg) * cu;
-            if (g) {
-                g[at] = narrow<T>(cg);
-                u[at] = narrow<T>(cu);
-            }
-        }
+    for (int i = 0; i < kQuarters; ++i) {
+        cg += sums[which][i].x;
+        cu += sums[which][i].y;
+    }
+    a[col] = silu(cg) * cu;
+    if (g) {
+        g[col] = narrow<T>(cg);
+        u[col] = narrow<T>(cu);
     }
 }
 
-template <class T, int NT>
+template <class T>
 __global__ void __launch_bounds__(kThreads) down_kernel(const float *__restrict__ a, const T *__restrict__ wd, void *out,
-                                                        int out_dtype, int add, int T_, int d, int f) {
-    constexpr int U = 6;
+                                                        int out_dtype, int add, int d, int f) {
     const int lane = threadIdx.x & 31, row = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * kDownRows;
-    float s[kDownRows][NT] = {};
-    uint4 q[kDownRows][U];
+    float s[kDownRows] = {};
+    uint4 q[kDownRows][kRowPieces];
     const auto fetch = [&](int k0) {
 #pragma unroll
-        for (int i = 0; i < U; ++i)
+        for (int i = 0; i < kRowPieces; ++i)
 #pragma unroll
             for (int r = 0; r < kDownRows; ++r) {
                 const int k = k0 + 256 * i;
@@ -147,46 +155,40 @@ __global__ void __launch_bounds__(kThreads) down_kernel(const float *__restrict_
     fetch(lane * 8);
     tc::grid_wait();
     tc::grid_release();
-    for (int k0 = lane * 8; k0 < f;) {
+    for (int k0 = lane * 8; k0 - lane * 8 < f;) {
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
+        for (int i = 0; i < kRowPieces; ++i) {
             const int k = k0 + 256 * i;
             if (k >= f) break;
-            float w[kDownRows][8];
+            const float4 *p = reinterpret_cast<const float4 *>(a + k);
+            const float4 y = p[0], z = p[1];
+            const float v[8] = {y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
 #pragma unroll
-            for (int r = 0; r < kDownRows; ++r) widen8<T>(q[r][i], w[r]);
+            for (int r = 0; r < kDownRows; ++r) {
+                float w[8];
+                widen8<T>(q[r][i], w);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                if (t >= T_) break;
-                const float4 *p = reinterpret_cast<const float4 *>(a + (size_t)t * f + k);
-                const float4 y = p[0], z = p[1];
-                const float v[8] = {y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
-#pragma unroll
-                for (int r = 0; r < kDownRows; ++r)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) s[r][t] = fmaf(w[r][j], v[j], s[r][t]);
+                for (int j = 0; j < 8; ++j) s[r] = fmaf(w[j], v[j], s[r]);
             }
         }
-        k0 += 256 * U;
+        k0 += 256 * kRowPieces;
         if (k0 - lane * 8 < f) fetch(k0);
     }
 #pragma unroll
-    for (int r = 0; r < kDownRows; ++r)
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const float y = add_lanes(s[r][t]);
-            if (lane == r * NT + t && t < T_ && row + r < d) put_as(out_dtype, out, (size_t)t * d + row + r, y, add);
-        }
+    for (int r = 0; r < kDownRows; ++r) {
+        const float y = add_lanes(s[r]);
+        if (lane == r && row + r < d) put_as(out_dtype, out, row + r, y, add);
+    }
 }
-static_assert(kDownRows * kGemvTokens <= 32, "a lane for each sum");
 
-template <class... P, class... A> cudaError_t launch(void (*kernel)(P...), int grid, int smem, cudaStream_t s, A... args) {
+template <class... P, class... A>
+cudaError_t launch(void (*kernel)(P...), int grid, int threads, int smem, cudaStream_t s, A... args) {
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = at;
@@ -194,17 +196,15 @@ template <class... P, class... A> cudaError_t launch(void (*kernel)(P...), int g
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
-template <class T, int NT> cudaError_t forward(const FfnFwd &P, cudaStream_t s) {
-    const cudaError_t e = launch(gate_up_kernel<T, NT>, (P.f + kWarps - 1) / kWarps, 0, s, static_cast<const T *>(P.x),
-                                 static_cast<const T *>(P.wg), static_cast<const T *>(P.wu), static_cast<float *>(P.a),
-                                 static_cast<T *>(P.g), static_cast<T *>(P.u), P.T, P.d, P.f);
+template <class T> cudaError_t forward(const FfnFwd &P, cudaStream_t s) {
+    const cudaError_t e =
+        launch(gate_up_kernel<T>, (P.f + 1) / 2, 2 * kQuarters * 32, 0, s, static_cast<const T *>(P.x),
+               static_cast<const T *>(P.wg), static_cast<const T *>(P.wu), static_cast<float *>(P.a),
+               static_cast<T *>(P.g), static_cast<T *>(P.u), P.d, P.f);
     if (e != cudaSuccess) return e;
     constexpr int kPer = kWarps * kDownRows;
-    return launch(down_kernel<T, NT>, (P.d + kPer - 1) / kPer, 0, s, static_cast<const float *>(P.a),
-                  static_cast<const T *>(P.wd), P.out, P.out_dtype, P.mode, P.T, P.d, P.f);
-}
-template <class T> cudaError_t forward_any(const FfnFwd &P, cudaStream_t s) {
-    return P.T == 1 ? forward<T, 1>(P, s) : forward<T, 2>(P, s);
+    return launch(down_kernel<T>, (P.d + kPer - 1) / kPer, kThreads, 0, s, static_cast<const float *>(P.a),
+                  static_cast<const T *>(P.wd), P.out, P.out_dtype, P.mode, P.d, P.f);
 }
 
 // ---- microscaled 4-bit weights ---------------------------------------------------------------
@@ -389,11 +389,11 @@ static_assert(kMxDownRows * kMxGemvTokens <= 32, "a lane for each sum");
 template <class T, int NT>
 cudaError_t mx_forward(const T *x, int T_, const Mx4Mat &gate, const Mx4Mat &up, const Mx4Mat &down, float *a, void *out,
                        int out_dtype, int mode, cudaStream_t s) {
-    cudaError_t e = launch(mx_gate_up_kernel<T, NT>, (gate.rows + kWarps - 1) / kWarps, (int)mx_gemv_smem(gate.cols, T_), s,
+    cudaError_t e = launch(mx_gate_up_kernel<T, NT>, (gate.rows + kWarps - 1) / kWarps, kThreads, (int)mx_gemv_smem(gate.cols, T_), s,
                            x, gate, up, a, T_);
     if (e != cudaSuccess) return e;
     constexpr int kPer = kWarps * kMxDownRows;
-    return launch(mx_down_kernel<NT>, (down.rows + kPer - 1) / kPer, (int)mx_gemv_smem(down.cols, T_), s,
+    return launch(mx_down_kernel<NT>, (down.rows + kPer - 1) / kPer, kThreads, (int)mx_gemv_smem(down.cols, T_), s,
                   static_cast<const float *>(a), down, out, out_dtype, mode, T_);
 }
 template <class T>
@@ -407,7 +407,7 @@ cudaError_t mx_forward_any(const void *x, int T_, const Mx4Mat &gate, const Mx4M
 } // namespace
 
 cudaError_t launch_ffn_gemv(const FfnFwd &P, cudaStream_t s) {
-    return P.dtype == WASTE_ACT_BF16 ? forward_any<__nv_bfloat16>(P, s) : forward_any<__half>(P, s);
+    return P.dtype == WASTE_ACT_BF16 ? forward<__nv_bfloat16>(P, s) : forward<__half>(P, s);
 }
 
 cudaError_t launch_mx4_ffn_gemv(const void *x, int x_dtype, int T, const Mx4Mat &gate, const Mx4Mat &up,
