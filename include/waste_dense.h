@@ -16,7 +16,7 @@
  * captured into a CUDA graph; arguments are checked on the host before anything is launched;
  * the return value is WASTE_OK or a negative waste_status whose message is
  * waste_moe_last_error().  Matrices are row-major without padding unless a row stride is an
- * argument.  Pointers are 16-byte aligned, workspaces 256-byte aligned.  A workspace holds
+ * argument, and no size is past 2^30.  Pointers are 16-byte aligned, workspaces 256-byte aligned.  A workspace holds
  * nothing between calls; two calls that may run at the same time (two streams, two captured
  * graphs) need one each.  Inputs and outputs do not overlap, unless a call says so.  The same
  * inputs give the same bits: no sum depends on the order in which blocks run.

@@ -26,6 +26,7 @@ int done(cudaError_t e, const char *what) {
     if (e == cudaSuccess) return ok();
     return fail(WASTE_ECUDA, "%s: %s", what, cudaGetErrorString(e));
 }
+constexpr int32_t kMostRows = 1 << 30; // rows and columns of anything: their tiles' indices fit 32 bits
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 bool half_type(int t) { return t == WASTE_ACT_BF16 || t == WASTE_ACT_F16; }
 bool any_type(int t) { return t == WASTE_ACT_F32 || half_type(t); }
@@ -53,7 +54,8 @@ int check_ffn(const waste_ffn_config *c, int32_t T) {
     if (c->d <= 0 || c->d % 8) return fail(WASTE_EINVAL, "d = %d must be a positive multiple of 8", c->d);
     if (c->f <= 0 || c->f % 8) return fail(WASTE_EINVAL, "f = %d must be a positive multiple of 8", c->f);
     if (!half_type(c->dtype)) return fail(WASTE_EINVAL, "dtype = %d: bf16 or fp16", c->dtype);
-    if (T < 0) return fail(WASTE_EINVAL, "T = %d", T);
+    if (c->d > kMostRows || c->f > kMostRows) return fail(WASTE_EINVAL, "d = %d, f = %d: at most 2^30", c->d, c->f);
+    if (T < 0 || T > kMostRows) return fail(WASTE_EINVAL, "T = %d outside [0, 2^30]", T);
     return WASTE_OK;
 }
 
@@ -66,8 +68,9 @@ size_t ffn_part(const waste_ffn_config *c, int32_t T) {
 }
 
 int check_mx4_shape(int32_t rows, int32_t cols) {
-    if (rows < 0) return fail(WASTE_EINVAL, "rows = %d", rows);
-    if (cols <= 0 || cols % kMxBlock) return fail(WASTE_EINVAL, "cols = %d must be a positive multiple of 32", cols);
+    if (rows < 0 || rows > kMostRows) return fail(WASTE_EINVAL, "rows = %d outside [0, 2^30]", rows);
+    if (cols <= 0 || cols % kMxBlock || cols > kMostRows)
+        return fail(WASTE_EINVAL, "cols = %d must be a positive multiple of 32, at most 2^30", cols);
     return WASTE_OK;
 }
 
@@ -86,7 +89,8 @@ int check_mx4_ffn(const waste_mx4_ffn_config *c, int32_t T) {
         return fail(WASTE_EINVAL, "abi_version %u, library speaks %u", c->abi_version, WASTE_MOE_ABI_VERSION);
     if (c->d <= 0 || c->d % kMxBlock) return fail(WASTE_EINVAL, "d = %d must be a positive multiple of 32", c->d);
     if (c->f <= 0 || c->f % kMxBlock) return fail(WASTE_EINVAL, "f = %d must be a positive multiple of 32", c->f);
-    if (T < 0) return fail(WASTE_EINVAL, "T = %d", T);
+    if (c->d > kMostRows || c->f > kMostRows) return fail(WASTE_EINVAL, "d = %d, f = %d: at most 2^30", c->d, c->f);
+    if (T < 0 || T > kMostRows) return fail(WASTE_EINVAL, "T = %d outside [0, 2^30]", T);
     return WASTE_OK;
 }
 
@@ -239,7 +243,7 @@ int waste_mx4_matmul(int32_t M, int32_t N, int32_t K, const uint8_t *d_a_codes, 
     const NvtxRange nvtx_range(__func__);
     int rc = check_mx4_shape(M, K);
     if (rc) return rc;
-    if (N < 1) return fail(WASTE_EINVAL, "N = %d", N);
+    if (N < 1 || N > kMostRows) return fail(WASTE_EINVAL, "N = %d outside [1, 2^30]", N);
     if (!any_type(out_dtype)) return fail(WASTE_EINVAL, "out_dtype = %d: fp32, bf16 or fp16", out_dtype);
     if (mode != 0 && mode != 1) return fail(WASTE_EINVAL, "mode = %d", mode);
     if (M == 0) return ok();

@@ -1,19 +1,17 @@
 // The gated feed-forward block for a few tokens (decode): the weights are read once, straight
 // into registers, and that reading is all that takes time.
 //
-// Two launches.  gate_up: a warp takes one column f of the block, streams its gate and up rows
-// (16 bytes a lane, several pieces in flight) against the tokens' x, adds across the lanes and
-// writes a = silu(g) u in fp32.  down: a warp takes a few rows of Wd against a.  No shared memory
+// Two launches.  gate_up: one column f of the block, its gate and up rows streamed (16 bytes a lane,
+// several pieces in flight) against the tokens' x, added across the lanes, a = silu(g) u written
+// in fp32.  down: a warp takes a few rows of Wd against a.  No shared memory
 // ring, no tensor memory and no sums across CTAs: what bounds both is memory latency times
 // bandwidth, so every SM holds as many loads in flight as its registers allow.  down does not
 // depend on gate_up for its weights: it is launched while gate_up runs and asks for its first rows
 // before it waits for a.  a never leaves fp32, so only the output is rounded.
 //
-// Against the tensor-core path (dense_gemm.cuh), d 7168, f 1536, bf16, weights from memory: one
-// token 19.3 us here and 33.5 there (its launches set up TMA and TMEM and add up over clusters),
-// two 25.7, four 44.0 here and 32.3 there: the multiplications grow with the tokens, so past
-// kGemvTokens the tensor cores take over.  4-bit weights: one 12.4 here and 22.1 there, two 15.0,
-// three 20.6, four 22.8.
+// Against the tensor cores, d 7168, f 1536, weights from memory: one token of 16 bits 15.3 us here and
+// 21.0 there (dense_skinny.cuh), two 25.7 here and 21.0 there; 4-bit weights, one token 10.3 us here
+// and 22.1 there, two 16.0, three 20.6, four 22.8: the multiplications grow with the tokens.
 #include "dense.cuh"
 #include "dense_tc.cuh"
 
@@ -75,60 +73,59 @@ __device__ __forceinline__ void put_as(int dtype, void *out, size_t at, float v,
 
 // ---- 16-bit weights, one token ---------------------------------------------------------------
 
-constexpr int kQuarters = 4; // warps that share a column's k in gate_up
-constexpr int kPieces = 7;   // pieces of 256 k of each row in flight in a warp (gate_up)
+constexpr int kPieces = 4;    // pieces of 256 k of each row in flight in a warp (gate_up)
 constexpr int kRowPieces = 6; // the same of each row in down
 
-// A warp takes a quarter of one column's k; the quarters meet in shared memory.  With a column a
-// warp the two rows of 28 pieces were four loads deep: 18.5 us for the 44 MB of d 7168, f 1536.
-template <class T>
-__global__ void __launch_bounds__(2 * kQuarters * 32) gate_up_kernel(const T *__restrict__ x, const T *__restrict__ wg,
+// A CTA takes one column, its Q warps share the k and meet in shared memory.  Q so that a warp's
+// pieces are on the way at once (8 past k = 4096, else 4); small CTAs, so that the SMs stay full
+// to the end.  Block of one token, d 7168, f 1536: a column a warp 19.2 us, two columns a CTA with 4
+// warps and 7 pieces each 17.1, one column with 4 warps of 7 16.0, 8 warps of 4 15.3; d 2048, f 768:
+// 8 warps 5.6, 4 warps 4.9.
+template <class T, int Q>
+__global__ void __launch_bounds__(Q * 32) gate_up_kernel(const T *__restrict__ x, const T *__restrict__ wg,
                                                                      const T *__restrict__ wu, float *__restrict__ a,
                                                                      T *__restrict__ g, T *__restrict__ u, int d, int f) {
-    __shared__ float2 sums[2][kQuarters];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quarter = warp % kQuarters, which = warp / kQuarters;
-    const int col = blockIdx.x * 2 + which;
+    __shared__ float2 sums[Q];
+    const int lane = threadIdx.x & 31, part = threadIdx.x >> 5, col = blockIdx.x;
     tc::grid_wait();
     tc::grid_release();
-    const int all = (d + 255) / 256, first = all * quarter / kQuarters, last = all * (quarter + 1) / kQuarters;
+    const int all = (d + 255) / 256, first = all * part / Q, last = all * (part + 1) / Q;
     float sg = 0.f, su = 0.f;
-    if (col < f) {
-        const T *pg = wg + (size_t)col * d, *pu = wu + (size_t)col * d;
-        for (int p0 = first; p0 < last; p0 += kPieces) {
-            uint4 qg[kPieces], qu[kPieces];
+    const T *pg = wg + (size_t)col * d, *pu = wu + (size_t)col * d;
+    for (int p0 = first; p0 < last; p0 += kPieces) {
+        uint4 qg[kPieces], qu[kPieces];
 #pragma unroll
-            for (int i = 0; i < kPieces; ++i) {
-                const int k = (p0 + i) * 256 + lane * 8;
-                const bool in = p0 + i < last && k < d;
-                qg[i] = in ? load_stream(pg + k) : make_uint4(0, 0, 0, 0);
-                qu[i] = in ? load_stream(pu + k) : make_uint4(0, 0, 0, 0);
-            }
+        for (int i = 0; i < kPieces; ++i) {
+            const int k = (p0 + i) * 256 + lane * 8;
+            const bool in = p0 + i < last && k < d;
+            qg[i] = in ? load_stream(pg + k) : make_uint4(0, 0, 0, 0);
+            qu[i] = in ? load_stream(pu + k) : make_uint4(0, 0, 0, 0);
+        }
 #pragma unroll
-            for (int i = 0; i < kPieces; ++i) {
-                const int k = (p0 + i) * 256 + lane * 8;
-                if (p0 + i >= last || k >= d) break;
-                float vg[8], vu[8], vx[8];
-                widen8<T>(qg[i], vg);
-                widen8<T>(qu[i], vu);
-                widen8<T>(__ldg(reinterpret_cast<const uint4 *>(x + k)), vx);
+        for (int i = 0; i < kPieces; ++i) {
+            const int k = (p0 + i) * 256 + lane * 8;
+            if (p0 + i >= last || k >= d) break;
+            float vg[8], vu[8], vx[8];
+            widen8<T>(qg[i], vg);
+            widen8<T>(qu[i], vu);
+            widen8<T>(__ldg(reinterpret_cast<const uint4 *>(x + k)), vx);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    sg = fmaf(vg[j], vx[j], sg);
-                    su = fmaf(vu[j], vx[j], su);
-                }
+            for (int j = 0; j < 8; ++j) {
+                sg = fmaf(vg[j], vx[j], sg);
+                su = fmaf(vu[j], vx[j], su);
             }
         }
     }
     sg = add_lanes(sg);
     su = add_lanes(su);
-    if (lane == 0) sums[which][quarter] = make_float2(sg, su);
+    if (lane == 0) sums[part] = make_float2(sg, su);
     __syncthreads();
-    if (quarter || lane || col >= f) return;
+    if (threadIdx.x) return;
     float cg = 0.f, cu = 0.f;
 #pragma unroll
-    for (int i = 0; i < kQuarters; ++i) {
-        cg += sums[which][i].x;
-        cu += sums[which][i].y;
+    for (int i = 0; i < Q; ++i) {
+        cg += sums[i].x;
+        cu += sums[i].y;
     }
     a[col] = silu(cg) * cu;
     if (g) {
@@ -197,10 +194,11 @@ cudaError_t launch(void (*kernel)(P...), int grid, int threads, int smem, cudaSt
 }
 
 template <class T> cudaError_t forward(const FfnFwd &P, cudaStream_t s) {
+    const bool far = P.d > 4096;
     const cudaError_t e =
-        launch(gate_up_kernel<T>, (P.f + 1) / 2, 2 * kQuarters * 32, 0, s, static_cast<const T *>(P.x),
-               static_cast<const T *>(P.wg), static_cast<const T *>(P.wu), static_cast<float *>(P.a),
-               static_cast<T *>(P.g), static_cast<T *>(P.u), P.d, P.f);
+        launch(far ? gate_up_kernel<T, 8> : gate_up_kernel<T, 4>, P.f, far ? 256 : 128, 0, s,
+               static_cast<const T *>(P.x), static_cast<const T *>(P.wg), static_cast<const T *>(P.wu),
+               static_cast<float *>(P.a), static_cast<T *>(P.g), static_cast<T *>(P.u), P.d, P.f);
     if (e != cudaSuccess) return e;
     constexpr int kPer = kWarps * kDownRows;
     return launch(down_kernel<T>, (P.d + kPer - 1) / kPer, kThreads, 0, s, static_cast<const float *>(P.a),
@@ -215,6 +213,7 @@ template <class T> cudaError_t forward(const FfnFwd &P, cudaStream_t s) {
 // exact and meets its two powers of two in fp32.
 
 constexpr int kMxDownRows = 4;
+constexpr int kMxWarps = 8, kMxThreads = kMxWarps * 32;
 
 // A staged row: 16-byte piece j of block b at (j * nb + b), then the scale bytes (mx_gemv_smem).
 
@@ -235,7 +234,7 @@ template <class T> __device__ __forceinline__ void block_of(const T *p, float (&
 }
 template <class T> __device__ __forceinline__ void stage(const T *x, int T_, int n, uint8_t *smem) {
     const int nb = n / 32;
-    for (int i = threadIdx.x; i < T_ * nb; i += kThreads) {
+    for (int i = threadIdx.x; i < T_ * nb; i += kMxThreads) {
         const int t = i / nb, b = i - t * nb;
         uint8_t *base = smem + t * mx_gemv_smem(n, 1);
         float v[32];
@@ -283,12 +282,12 @@ __device__ __forceinline__ float scaled(float v, uint32_t a, uint32_t b) {
 }
 
 template <class T, int NT>
-__global__ void __launch_bounds__(kThreads) mx_gate_up_kernel(const T *__restrict__ x, Mx4Mat wg, Mx4Mat wu,
+__global__ void __launch_bounds__(kMxThreads) mx_gate_up_kernel(const T *__restrict__ x, Mx4Mat wg, Mx4Mat wu,
                                                               float *__restrict__ a, int T_) {
     extern __shared__ __align__(16) uint8_t smem[];
     constexpr int U = 4;
     const int d = wg.cols, f = wg.rows, nb = d / 32, kb = (d + 127) / 128;
-    const int lane = threadIdx.x & 31, col = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, col = blockIdx.x * kMxWarps + (threadIdx.x >> 5);
     tc::grid_wait();
     tc::grid_release();
     uint4 q[2][U];
@@ -335,12 +334,12 @@ __global__ void __launch_bounds__(kThreads) mx_gate_up_kernel(const T *__restric
 }
 
 template <int NT>
-__global__ void __launch_bounds__(kThreads) mx_down_kernel(const float *__restrict__ a, Mx4Mat wd, void *out,
+__global__ void __launch_bounds__(kMxThreads) mx_down_kernel(const float *__restrict__ a, Mx4Mat wd, void *out,
                                                            int out_dtype, int add, int T_) {
     extern __shared__ __align__(16) uint8_t smem[];
     constexpr int U = 2;
     const int f = wd.cols, d = wd.rows, nb = f / 32, kb = (f + 127) / 128;
-    const int lane = threadIdx.x & 31, row = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * kMxDownRows;
+    const int lane = threadIdx.x & 31, row = (blockIdx.x * kMxWarps + (threadIdx.x >> 5)) * kMxDownRows;
     uint4 q[kMxDownRows][U];
     uint32_t sc[kMxDownRows][U];
     const auto fetch = [&](int b0) {
@@ -389,11 +388,11 @@ static_assert(kMxDownRows * kMxGemvTokens <= 32, "a lane for each sum");
 template <class T, int NT>
 cudaError_t mx_forward(const T *x, int T_, const Mx4Mat &gate, const Mx4Mat &up, const Mx4Mat &down, float *a, void *out,
                        int out_dtype, int mode, cudaStream_t s) {
-    cudaError_t e = launch(mx_gate_up_kernel<T, NT>, (gate.rows + kWarps - 1) / kWarps, kThreads, (int)mx_gemv_smem(gate.cols, T_), s,
+    cudaError_t e = launch(mx_gate_up_kernel<T, NT>, (gate.rows + kMxWarps - 1) / kMxWarps, kMxThreads, (int)mx_gemv_smem(gate.cols, T_), s,
                            x, gate, up, a, T_);
     if (e != cudaSuccess) return e;
-    constexpr int kPer = kWarps * kMxDownRows;
-    return launch(mx_down_kernel<NT>, (down.rows + kPer - 1) / kPer, kThreads, (int)mx_gemv_smem(down.cols, T_), s,
+    constexpr int kPer = kMxWarps * kMxDownRows;
+    return launch(mx_down_kernel<NT>, (down.rows + kPer - 1) / kPer, kMxThreads, (int)mx_gemv_smem(down.cols, T_), s,
                   static_cast<const float *>(a), down, out, out_dtype, mode, T_);
 }
 template <class T>

@@ -37,11 +37,38 @@ def on_device(device):
 _HERE = contextlib.nullcontext()
 
 
+def make(shape, dtype, device, stream) -> torch.Tensor:
+    """An output made for a call on `stream` (None or an integer handle: made on the current one)."""
+    with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else None):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+class Workspace:
+    """A buffer made on one stream and lent to calls on any: the allocator is told of the others, so
+    that its memory is not given away while a call there still runs."""
+
+    def __init__(self, nbytes: int, device):
+        self.bytes = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+        with on_device(device):
+            self.home = B._stream(None)
+
+    def lend(self, stream) -> torch.Tensor:
+        if stream is None:
+            if B._stream(None) != self.home:
+                self.bytes.record_stream(torch.cuda.current_stream())
+        elif isinstance(stream, torch.cuda.Stream) and stream.cuda_stream != self.home:
+            self.bytes.record_stream(stream)
+        return self.bytes
+
+
 class DenseExpert:
     """w_gate, w_up [f, d] and w_down [d, f], bf16 or fp16, contiguous on one GPU (borrowed, not
     copied).  max_tokens bounds T and sizes the workspace, which belongs to this object: calls
-    of one object must not run at the same time on two streams, and two captured graphs that
-    may replay at the same time need an object each."""
+    of one object must not run at the same time on two streams, two captured graphs that may
+    replay at the same time need an object each, and an object outlives the graphs that hold its
+    calls.  stream: a torch.cuda.Stream, an integer handle (then the object must outlive the
+    call) or None for the current stream; ordering the tensors' use between streams is the
+    caller's."""
 
     def __init__(self, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor, max_tokens: int):
         f, d = w_gate.shape
@@ -59,7 +86,7 @@ class DenseExpert:
         self._ws = {}
         self._workspace(0)
 
-    def _workspace(self, backward: int) -> torch.Tensor:
+    def _workspace(self, backward: int) -> Workspace:
         """One workspace for the forward and one, made by the first call, for the backward; a call
         that would make it while its stream is being captured is refused (the buffer would
         belong to the graph)."""
@@ -67,8 +94,7 @@ class DenseExpert:
         if ws is None:
             require(not torch.cuda.is_current_stream_capturing(),
                     "reserve the workspace before the capture (reserve_backward)")
-            n = B.waste_ffn_workspace(self.cfg, self.max_tokens, backward)
-            ws = self._ws[backward] = torch.empty(max(n, 256), dtype=torch.uint8, device=self.device)
+            ws = self._ws[backward] = Workspace(B.waste_ffn_workspace(self.cfg, self.max_tokens, backward), self.device)
         return ws
 
     def reserve_backward(self):
@@ -90,14 +116,14 @@ class DenseExpert:
         T = self._tokens(x, "x")
         if out is None:
             require(mode == 0, "mode 1 adds to a given out")
-            out = torch.empty(T, self.d, dtype=self.dtype, device=self.device)
+            out = make((T, self.d), self.dtype, self.device, stream)
         check(out, "out", (T, self.d), self._out, self.device)
         for t, n in ((save_g, "save_g"), (save_u, "save_u")):
             if t is not None:
                 check(t, n, (T, self.f), self._own, self.device)
         with on_device(self.device):
             B.waste_ffn_forward(self.cfg, x, T, self.w_gate, self.w_up, self.w_down, out, ACT[out.dtype], mode,
-                                save_g, save_u, self._ws[0], stream)
+                                save_g, save_u, self._ws[0].lend(stream), stream)
         return out
 
     def backward(self, dy, x, g, u, dx=None, dw_gate=None, dw_up=None, dw_down=None, accumulate: bool = False,
@@ -118,4 +144,4 @@ class DenseExpert:
                 check(t, n, w.shape, (gt,) if gt in self._out else self._out, self.device)
         with on_device(self.device):
             B.waste_ffn_backward(self.cfg, dy, T, x, g, u, self.w_gate, self.w_up, self.w_down, dx, dw_gate, dw_up,
-                                 dw_down, ACT[gt], int(accumulate), self._workspace(1), stream)
+                                 dw_down, ACT[gt], int(accumulate), self._workspace(1).lend(stream), stream)

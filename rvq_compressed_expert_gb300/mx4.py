@@ -10,7 +10,7 @@ from __future__ import annotations
 import torch
 
 from . import binding as B
-from .dense import ACT, check, on_device, require
+from .dense import ACT, Workspace, check, make, on_device, require
 
 _FLOATS = (torch.float32, torch.bfloat16, torch.float16)
 
@@ -35,7 +35,8 @@ class Mx4Matrix:
     @classmethod
     def from_dense(cls, x: torch.Tensor, stream=None) -> "Mx4Matrix":
         require(isinstance(x, torch.Tensor) and x.dim() == 2, "x: a [rows, cols] tensor is needed")
-        m = cls.empty(*x.shape, device=x.device)
+        with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else None):
+            m = cls.empty(*x.shape, device=x.device)
         m.quantize(x, stream)
         return m
 
@@ -56,7 +57,7 @@ class Mx4Matrix:
     def dequantize(self, out: torch.Tensor | None = None, dtype=torch.float32, stream=None) -> torch.Tensor:
         """The values the codes stand for, into out [rows, cols] (made with dtype if None)."""
         if out is None:
-            out = torch.empty(self.rows, self.cols, dtype=dtype, device=self.device)
+            out = make((self.rows, self.cols), dtype, self.device, stream)
         ld = self._plain(out, "out")
         with on_device(self.device):
             B.waste_mx4_dequantize(self.codes, self.scales, self.rows, self.cols, out, ACT[out.dtype], ld, stream)
@@ -72,7 +73,7 @@ def matmul(a: Mx4Matrix, b: Mx4Matrix, out: torch.Tensor | None = None, mode: in
     require(a.device == b.device, "a and b are on two devices")
     if out is None:
         require(mode == 0, "mode 1 adds to a given out")
-        out = torch.empty(a.rows, b.rows, dtype=dtype, device=a.device)
+        out = make((a.rows, b.rows), dtype, a.device, stream)
     check(out, "out", (a.rows, b.rows), _FLOATS, a.device)
     with on_device(a.device):
         B.waste_mx4_matmul(a.rows, b.rows, a.cols, a.codes, a.scales, b.codes, b.scales, out, ACT[out.dtype], mode,
@@ -83,8 +84,9 @@ def matmul(a: Mx4Matrix, b: Mx4Matrix, out: torch.Tensor | None = None, mode: in
 class Mx4Expert:
     """A dense expert with 4-bit weights: gate, up [f, d] and down [d, f] (kept, not copied).
     max_tokens bounds T and sizes the workspace, which belongs to this object: calls of one
-    object must not run at the same time on two streams, and two captured graphs that may replay
-    at the same time need an object each."""
+    object must not run at the same time on two streams, two captured graphs that may replay at the
+    same time need an object each, and an object outlives the graphs that hold its calls.  stream
+    as for ``dense.DenseExpert``."""
 
     def __init__(self, gate: Mx4Matrix, up: Mx4Matrix, down: Mx4Matrix, max_tokens: int):
         f, d = gate.rows, gate.cols
@@ -96,8 +98,7 @@ class Mx4Expert:
         self.d, self.f, self.device, self.max_tokens = d, f, gate.device, int(max_tokens)
         self.cfg = B.waste_mx4_ffn_config(B.ABI_VERSION, d, f, *(t.data_ptr() for m in (gate, up, down)
                                                                  for t in (m.codes, m.scales)))
-        self._ws = torch.empty(max(B.waste_mx4_ffn_workspace(self.cfg, self.max_tokens), 256), dtype=torch.uint8,
-                               device=self.device)
+        self._ws = Workspace(B.waste_mx4_ffn_workspace(self.cfg, self.max_tokens), self.device)
 
     @classmethod
     def from_dense(cls, w_gate, w_up, w_down, max_tokens: int) -> "Mx4Expert":
@@ -113,8 +114,9 @@ class Mx4Expert:
         check(x, "x", (T, self.d), _FLOATS, self.device)
         if out is None:
             require(mode == 0, "mode 1 adds to a given out")
-            out = torch.empty(T, self.d, dtype=x.dtype, device=self.device)
+            out = make((T, self.d), x.dtype, self.device, stream)
         check(out, "out", (T, self.d), _FLOATS, self.device)
         with on_device(self.device):
-            B.waste_mx4_ffn_forward(self.cfg, x, ACT[x.dtype], T, out, ACT[out.dtype], mode, self._ws, stream)
+            B.waste_mx4_ffn_forward(self.cfg, x, ACT[x.dtype], T, out, ACT[out.dtype], mode, self._ws.lend(stream),
+                                    stream)
         return out

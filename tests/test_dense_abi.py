@@ -120,6 +120,17 @@ def test_mx4_bad_shapes(shape):
     refused(B.waste_mx4_matmul, shape[0], 1, shape[1], P, P, P, P, P, B.ACT_F32, stream=0)
 
 
+def test_sizes_past_the_limit():
+    """Sizes past 2^30 are refused before any arithmetic on them."""
+    big = (1 << 30) + 32
+    refused(B.waste_ffn_workspace, cfg(), big)
+    refused(B.waste_ffn_workspace, cfg(d=big), 1)
+    refused(B.waste_mx4_layout, big, 32)
+    refused(B.waste_mx4_layout, 1, big)
+    refused(B.waste_mx4_matmul, 1, big, 32, P, P, P, P, P, B.ACT_F32, 0, stream=0)
+    refused(B.waste_mx4_ffn_workspace, B.waste_mx4_ffn_config(B.ABI_VERSION, 32, big, P, P, P, P, P, P), 1)
+
+
 def test_mx4_refusals():
     for a in ((None, B.ACT_F32, 1, 32, 32, P, P), (P + 4, B.ACT_F32, 1, 32, 32, P, P), (P, 3, 1, 32, 32, P, P),
               (P, B.ACT_F32, 1, 64, 32, P, P), (P, B.ACT_BF16, 2, 32, 36, P, P), (P, B.ACT_F32, 1, 32, 32, None, P),

@@ -51,7 +51,7 @@ def guarded(*shape, dtype, fill=7.0):
 
 
 # d and f of one core matrix, below and past a tile, of no round number, and of the workloads
-SHAPES = [(1, 8, 8), (1, 1032, 1544), (2, 64, 24), (3, 256, 128), (5, 264, 1800), (8, 2056, 136), (9, 520, 136), (33, 136, 264), (127, 1032, 136), (128, 512, 520), (129, 72, 1544),
+SHAPES = [(1, 8, 8), (1, 1032, 1544), (2, 64, 24), (3, 256, 128), (5, 264, 1800), (8, 2056, 136), (9, 520, 136), (24, 2056, 1032), (32, 136, 4104), (33, 136, 264), (127, 1032, 136), (128, 512, 520), (129, 72, 1544),
           (200, 1032, 264), (257, 264, 1032), (511, 648, 392), (1000, 1544, 776), (2049, 2056, 1032)]
 
 
@@ -194,6 +194,31 @@ def test_fewer_tokens_than_reserved_leave_the_rest():
     e.backward(dy[:37], x, sg[:37], su[:37], None, *dw)
     DenseExpert(*W, max_tokens=37).backward(dy[:37], x, sg[:37], su[:37], None, *dw2)
     assert all(torch.equal(a, b) and torch.isfinite(a).all() for a, b in zip(dw, dw2))
+
+
+def test_past_32_bits():
+    """More than 2^31 elements of x and out, and of a matrix to quantise: sampled rows from both ends
+    and around the border against the same rows alone."""
+    T, d, f, t = 300_000, 7168, 8, BF
+    g = gen(77)
+    W = weights(g, d, f, t)
+    x = torch.empty(T, d, dtype=t, device="cuda")
+    for i in range(0, T, 50_000):
+        x[i:i + 50_000] = randn(g, 50_000, d, t=t)
+    rows = torch.tensor([0, 1, 127, 128, 299_592, 299_593, 299_594, 299_595, T - 129, T - 2, T - 1], device="cuda")
+    out = torch.empty_like(x)
+    DenseExpert(*W, max_tokens=T).forward(x, out)
+    ref = R.forward(x[rows], *W, t)
+    y, ey = ref["y"]
+    R.close(out[rows], y, ey + R.rnd(y.abs() + ey, t), "y")
+    m = Mx4Matrix.from_dense(x)
+    code, scale = R.mx_codes(x[rows])
+    codes = (code[:, 0::2] + 16 * code[:, 1::2]).to(torch.uint8)
+    assert torch.equal(m.codes[rows], codes)
+    m.dequantize(out)
+    assert torch.equal(out[rows].double(), R.mx_values(code, scale))
+    del out, m, x
+    torch.cuda.empty_cache()
 
 
 def test_infinities_and_nans_stay_in_their_rows():
@@ -433,7 +458,7 @@ def test_mx4_refusals():
             call()
         assert ei.value.status == -1
     e.forward(x)
-    torch.cuda.synchronize()
+    B.waste_dense_status()  # waits; no device wait gave up
 
 
 # ---------------------------------------------------------------- as they are used together
@@ -523,6 +548,50 @@ def test_streams_and_graphs():
         gr.replay()
         torch.cuda.synchronize()
         assert torch.equal(o[0], want[i][0]) and torch.equal(o[1], want[i][1])
+
+
+@pytest.mark.parametrize("T", [1, 7, 40, 300])
+def test_backward_captured(T):
+    """A captured backward, replayed on other inputs, gives the bits of a plain one; called through a
+    current stream that is not the one the expert was made on."""
+    t, d, f = HF, 392, 264
+    g = gen(50 + T)
+    W = weights(g, d, f, t)
+    e = DenseExpert(*W, max_tokens=T)
+    e.reserve_backward()
+    sets = [[randn(g, T, n, t=t) for n in (d, d, f, f)] for _ in range(2)]
+    want = []
+    for s in sets:
+        dx, dw = torch.empty(T, d, dtype=t, device="cuda"), [torch.empty_like(w) for w in W]
+        e.backward(*s, dx, *dw)
+        want.append([dx, *dw])
+    buf = [v.clone() for v in sets[0]]
+    got = [torch.empty_like(v) for v in want[0]]
+    gr = run_captured(lambda: e.backward(*buf, *got))
+    for i in (1, 0):
+        for a, b in zip(buf, sets[i]):
+            a.copy_(b)
+        gr.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want[i]))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for v in got:
+            v.zero_()
+        e.backward(*sets[1], *got)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want[1]))
+    fresh = DenseExpert(*W, max_tokens=T)
+    gr2 = torch.cuda.CUDAGraph()
+    refusal = None
+    with torch.cuda.graph(gr2):
+        try:
+            fresh.backward(*buf, *got)  # would make its workspace inside the capture
+        except B.WasteError as err:
+            refusal = err
+        got[0].zero_()
+    assert refusal is not None and refusal.status == -1
 
 
 @pytest.mark.parametrize("tokens", [1, 3])
