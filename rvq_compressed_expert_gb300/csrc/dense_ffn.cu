@@ -48,55 +48,31 @@ SkinnyArgs skinny(int T, int N, int K) {
     SkinnyArgs G = {};
     G.T = T;
     G.N = N;
-    G.npad = (T + 15) / 16 * 16;
+    G.npad = pad_tokens(T);
     G.kb = G.kb_seg = pieces(K);
     return G;
-}
-
-cudaError_t forward_skinny(const FfnFwd &P, cudaStream_t s) {
-    const int sms = device_sm_count();
-    const bool bf16 = P.dtype == WASTE_ACT_BF16, split = P.T <= kSplitTokens;
-    void *lo = split ? static_cast<uint16_t *>(P.a) + (size_t)P.T * P.f : nullptr;
-    cudaError_t e;
-    {
-        SkinnyArgs G = skinny(P.T, P.f, P.d);
-        if ((e = half_map(&G.ta[0], P.wg, P.f, P.d, kBM)) != cudaSuccess) return e;
-        if ((e = half_map(&G.ta[1], P.wu, P.f, P.d, kBM)) != cudaSuccess) return e;
-        if ((e = half_map(&G.tb[0], P.x, P.T, P.d, G.npad)) != cudaSuccess) return e;
-        // bound by the weights' way from memory, which the next kernel's can follow at once while
-        // this one adds up and ends
-        const size_t wd = (size_t)P.d * P.f * 2;
-        if (wd <= kAheadMost) {
-            G.ahead = static_cast<const uint8_t *>(P.wd);
-            G.ahead_bytes = wd;
-        }
-        e = launch_skinny<kPair, false>(G, bf16, GatedSplit{P.a, lo, P.g, P.u, P.f, P.dtype}, sms, s);
-        if (e != cudaSuccess) return e;
-    }
-    SkinnyArgs G = skinny(P.T, P.d, P.f);
-    G.early_w = 1;
-    G.lo = split;
-    if ((e = half_map(&G.ta[0], P.wd, P.d, P.f, kBM)) != cudaSuccess) return e;
-    if ((e = half_map(&G.tb[0], P.a, P.T, P.f, G.npad)) != cudaSuccess) return e;
-    if (split && (e = half_map(&G.tb[1], lo, P.T, P.f, G.npad)) != cudaSuccess) return e;
-    Store st = {};
-    st.out[0] = P.out;
-    st.ld[0] = P.d;
-    st.dtype = P.out_dtype;
-    st.add = P.mode;
-    st.vec = 1; // d % 8 == 0
-    return launch_skinny<kOne, false>(G, bf16, st, sms, s);
 }
 
 } // namespace
 
 cudaError_t launch_ffn_forward(const FfnFwd &P, cudaStream_t s) {
     if (P.T <= kGemvTokens) return launch_ffn_gemv(P, s);
-    if (P.T <= kSkinnyTokens) return forward_skinny(P, s);
     const int sms = device_sm_count();
-    const bool bf16 = P.dtype == WASTE_ACT_BF16;
+    const bool bf16 = P.dtype == WASTE_ACT_BF16, split = P.T <= kSplitTokens;
+    void *lo = split ? static_cast<uint16_t *>(P.a) + (size_t)P.T * P.f : nullptr;
     cudaError_t e;
-    {
+    // few tiles: bound by the weights' way from memory, which the next kernel's can follow at once
+    // while this one adds up and ends
+    const size_t wd = (size_t)P.d * P.f * 2, ahead = wd <= kAheadMost ? wd : 0;
+    if (skinny_wins(P.T, P.f, pieces(P.d), true, sms)) {
+        SkinnyArgs G = skinny(P.T, P.f, P.d);
+        if ((e = half_map(&G.ta[0], P.wg, P.f, P.d, kBM / 2)) != cudaSuccess) return e;
+        if ((e = half_map(&G.ta[1], P.wu, P.f, P.d, kBM / 2)) != cudaSuccess) return e;
+        if ((e = half_map(&G.tb[0], P.x, P.T, P.d, G.npad)) != cudaSuccess) return e;
+        G.ahead = static_cast<const uint8_t *>(P.wd);
+        G.ahead_bytes = ahead;
+        e = launch_skinny<kPair, false>(G, bf16, GatedSplit{P.a, lo, P.g, P.u, P.f, P.dtype}, sms, s);
+    } else {
         GemmArgs G = {};
         G.K = P.d;
         G.kb = G.kb_seg = pieces(P.d);
@@ -106,15 +82,27 @@ cudaError_t launch_ffn_forward(const FfnFwd &P, cudaStream_t s) {
         if ((e = half_map(&G.ta[0], P.x, P.T, P.d, kBM)) != cudaSuccess) return e;
         if ((e = half_map(&G.tb[0], P.wg, P.f, P.d, box_rows_b(L, true))) != cudaSuccess) return e;
         if ((e = half_map(&G.tb[1], P.wu, P.f, P.d, box_rows_b(L, true))) != cudaSuccess) return e;
-        // few tiles: bound by the weights' way from memory, which the next kernel's can follow
-        // at once while this one adds up and ends
-        const size_t wd = (size_t)P.d * P.f * 2;
-        if (G.S > 1 && wd <= kAheadMost) {
+        if (G.S > 1) {
             G.ahead = static_cast<const uint8_t *>(P.wd);
-            G.ahead_bytes = wd;
+            G.ahead_bytes = ahead;
         }
         e = launch_gemm<kHalf, kPair, false, false>(G, L, Gated{P.a, P.g, P.u, P.f, P.dtype}, sms, s);
-        if (e != cudaSuccess) return e;
+    }
+    if (e != cudaSuccess) return e;
+    Store st = {};
+    st.out[0] = P.out;
+    st.ld[0] = P.d;
+    st.dtype = P.out_dtype;
+    st.add = P.mode;
+    st.vec = 1; // d % 8 == 0
+    if (skinny_wins(P.T, P.d, pieces(P.f), false, sms)) {
+        SkinnyArgs G = skinny(P.T, P.d, P.f);
+        G.early_w = 1;
+        G.lo = split;
+        if ((e = half_map(&G.ta[0], P.wd, P.d, P.f, kBM)) != cudaSuccess) return e;
+        if ((e = half_map(&G.tb[0], P.a, P.T, P.f, G.npad)) != cudaSuccess) return e;
+        if (split && (e = half_map(&G.tb[1], lo, P.T, P.f, G.npad)) != cudaSuccess) return e;
+        return launch_skinny<kOne, false>(G, bf16, st, sms, s);
     }
     GemmArgs G = {};
     G.K = P.f;
@@ -125,21 +113,15 @@ cudaError_t launch_ffn_forward(const FfnFwd &P, cudaStream_t s) {
     if ((e = half_map(&G.ta[0], P.a, P.T, P.f, kBM)) != cudaSuccess) return e;
     if ((e = half_map(&G.tb[0], P.wd, P.d, P.f, box_rows_b(L, false))) != cudaSuccess) return e;
     G.early_b = 1;
-    Store st = {};
-    st.out[0] = P.out;
-    st.ld[0] = P.d;
-    st.dtype = P.out_dtype;
-    st.add = P.mode;
-    st.vec = 1; // d % 8 == 0
     return launch_gemm<kHalf, kOne, false, false>(G, L, st, sms, s);
 }
 
 cudaError_t launch_ffn_backward(const FfnBwd &P, cudaStream_t s) {
     const int sms = device_sm_count();
-    const bool bf16 = P.dtype == WASTE_ACT_BF16, few = P.T <= kSkinnyTokens;
+    const bool bf16 = P.dtype == WASTE_ACT_BF16;
     const GatedGrad grad{P.g, P.u, P.a, P.dg, P.du, P.f, P.dtype};
     cudaError_t e;
-    if (few) {
+    if (skinny_wins(P.T, P.f, pieces(P.d), false, sms)) {
         SkinnyArgs G = skinny(P.T, P.f, P.d);
         if ((e = half_map(&G.ta[0], P.wd, P.d, P.f, 64)) != cudaSuccess) return e;
         if ((e = half_map(&G.tb[0], P.dy, P.T, P.d, G.npad)) != cudaSuccess) return e;
@@ -157,7 +139,7 @@ cudaError_t launch_ffn_backward(const FfnBwd &P, cudaStream_t s) {
         e = launch_gemm<kHalf, kOne, false, true>(G, L, grad, sms, s);
         if (e != cudaSuccess) return e;
     }
-    if (P.dx && few) {
+    if (P.dx && skinny_wins(P.T, P.d, 2 * pieces(P.f), false, sms)) {
         SkinnyArgs G = skinny(P.T, P.d, P.f);
         G.kb = 2 * G.kb_seg;
         G.early_w = 1;

@@ -93,8 +93,7 @@ int clusters_at_once(int S, int sms) {
 // shape below): over these it picks a launch 1.6 % slower than the best one, in the geometric
 // mean.
 Plan plan(const int *M, const int *N, int n, int kb, bool pair, bool mx4, int sms) {
-    Plan best{256, 1, 1};
-    double best_t = 1e30;
+    Plan best{256, 1, 1, 1e30};
     int rows = 0;
     for (int i = 0; i < n; ++i) rows = std::max(rows, std::min(M[i], kBM));
     const auto consider = [&](int BN, int cg, int S) {
@@ -107,10 +106,7 @@ Plan plan(const int *M, const int *N, int n, int kb, bool pair, bool mx4, int sm
         const double piece = (kBM + BN / cg) * kRowBytes / 88.8;
         double t = (cg == 2 ? 1370.0 : 0.0) + (double)waves * ((kb + S - 1) / S) * piece + rows * BN * 0.123;
         if (S > 1) t += 2240.0 + rows * BN * 0.285;
-        if (t < best_t) {
-            best_t = t;
-            best = Plan{BN, S, cg};
-        }
+        if (t < best.ns) best = Plan{BN, S, cg, t};
     };
     // 4-bit: whole scale tiles (128 rows) of each product; 16-bit: any multiple of 32
     const int least = mx4 ? (pair ? 256 : 128) : 64;

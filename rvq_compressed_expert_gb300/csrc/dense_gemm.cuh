@@ -827,6 +827,7 @@ cudaError_t make_scale_map(CUtensorMap *m, const void *p, size_t tiles);
 // holds BN / 2 columns of each of two products.
 struct Plan {
     int BN, S, cg;
+    double ns; // estimated
 };
 int clusters_at_once(int S, int sms); // clusters of S CTAs that run at once
 Plan plan(const int *M, const int *N, int n, int kb, bool pair, bool mx4, int sms);

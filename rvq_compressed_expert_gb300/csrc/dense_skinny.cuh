@@ -22,10 +22,8 @@
 namespace wm {
 namespace dense {
 
-// The exchange of the sums grows with the tokens (T x 256 fp32 a CTA): d 7168, f 1536, bf16, weights
-// from memory, both products: 3 tokens 21.0 us here and 27.5 us in 128-row tiles of tokens, 16 22.0
-// and 27.7, 64 29.4 and 26.5, 131 35.9 and 31.4.
-constexpr int kSkinnyTokens = 32;
+// Past these the sums of a CTA's tokens and the ring do not pay any more (an estimate decides below).
+constexpr int kSkinnyTokens = 192;
 
 struct SkinnyArgs {
     CUtensorMap ta[2], tb[2]; // weights (kPair: both products'; kSum: both segments'); tokens (kSum,
@@ -39,16 +37,14 @@ struct SkinnyArgs {
     size_t ahead_bytes;
 };
 
-__host__ __device__ inline uint32_t skinny_stage(int nt, bool pair) {
-    return (pair ? 2u : 1u) * kBM * kRowBytes + (uint32_t)nt * kRowBytes;
-}
+__host__ __device__ inline uint32_t skinny_stage(int nt) { return (uint32_t)(kBM + nt) * kRowBytes; }
 
 template <int kForm, bool kAmn, class Epi>
 __global__ void __launch_bounds__(kThreads, 1) skinny_kernel(const __grid_constant__ SkinnyArgs P,
                                                              const __grid_constant__ Epi epi) {
     extern __shared__ uint8_t smem_raw[];
-    constexpr int kAcc = kForm == kPair ? 2 : 1;
-    constexpr uint32_t kTile = kBM * kRowBytes; // one weight tile
+    constexpr int kCols = kForm == kPair ? kBM / 2 : kBM; // columns of the result in a tile
+    constexpr int kRow = kBM + 4;                         // floats of a token's row of sums
     const uint32_t smem0 = tc::smem_u32(smem_raw);
     const uint32_t base = (smem0 + kBarBytes + 1023) & ~1023u;
     const uint32_t bar_full = smem0, bar_empty = smem0 + 64, bar_acc = smem0 + 128, drain = smem0 + 136;
@@ -57,9 +53,9 @@ __global__ void __launch_bounds__(kThreads, 1) skinny_kernel(const __grid_consta
 
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int S = P.S, nt = P.npad * (1 + P.lo);
-    const uint32_t b_at = kAcc * kTile, stage_bytes = skinny_stage(nt, kForm == kPair);
+    const uint32_t b_at = kBM * kRowBytes, stage_bytes = skinny_stage(nt);
     const int rank = S > 1 ? (int)(blockIdx.x % S) : 0, tile = (int)blockIdx.x / S;
-    const int n0 = tile * kBM;
+    const int n0 = tile * kCols;
     const int kb0 = (int)((long long)P.kb * rank / S), kb1 = (int)((long long)P.kb * (rank + 1) / S);
 
     if (tid == 0) {
@@ -90,15 +86,14 @@ __global__ void __launch_bounds__(kThreads, 1) skinny_kernel(const __grid_consta
             const bool second = kForm == kSum && kb >= P.kb_seg;
             const int kx = (second ? kb - P.kb_seg : kb) * 64;
             tc::mbar_arrive_expect_tx(full, stage_bytes);
-#pragma unroll
-            for (int i = 0; i < kAcc; ++i) {
-                const CUtensorMap *m = &P.ta[kForm == kPair ? i : second ? 1 : 0];
-                if (kAmn) {
-                    tc::tma_load(at + i * kTile, m, n0, kx, full);
-                    tc::tma_load(at + i * kTile + 8192, m, n0 + 64, kx, full);
-                } else {
-                    tc::tma_load(at + i * kTile, m, kx, n0, full);
-                }
+            if (kForm == kPair) { // 64 rows of each
+                tc::tma_load(at, &P.ta[0], kx, n0, full);
+                tc::tma_load(at + b_at / 2, &P.ta[1], kx, n0, full);
+            } else if (kAmn) {
+                tc::tma_load(at, &P.ta[second ? 1 : 0], n0, kx, full);
+                tc::tma_load(at + 8192, &P.ta[second ? 1 : 0], n0 + 64, kx, full);
+            } else {
+                tc::tma_load(at, &P.ta[second ? 1 : 0], kx, n0, full);
             }
         };
         const auto load_t = [&](int kb, int st) {
@@ -163,10 +158,8 @@ __global__ void __launch_bounds__(kThreads, 1) skinny_kernel(const __grid_consta
             if (tc::elect_one()) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int i = 0; i < kAcc; ++i)
-                        tc::mma_f16(tmem + i * nt, da + (uint64_t)((i * kTile + j * (kAmn ? 2048 : 32)) >> 4),
-                                    db + (uint64_t)(2 * j), P.idesc, j > 0 || kb > kb0);
+                    tc::mma_f16(tmem, da + (uint64_t)(j * ((kAmn ? 2048 : 32) >> 4)), db + (uint64_t)(2 * j), P.idesc,
+                                j > 0 || kb > kb0);
                 tc::mma_commit(bar_empty + 8 * st);
                 if (kb + 1 == kb1) tc::mma_commit(bar_acc);
             }
@@ -183,8 +176,8 @@ __global__ void __launch_bounds__(kThreads, 1) skinny_kernel(const __grid_consta
         }
         __syncwarp();
     } else if (warp >= 3) {
-        // ---- sums to shared memory, a row of kAcc x 128 per token (padded by 16 bytes); two warps
-        // for each quarter of the lanes, 16 tokens at a time in turn
+        // ---- sums to shared memory, a row of 128 per token (padded by 16 bytes); two warps for
+        // each quarter of the lanes, 16 tokens at a time in turn
         const int q = warp & 3, half = (warp - 3) >> 2;
         bool ok = true;
         if (lane == 0) ok = tc::mbar_wait(bar_acc, 0);
@@ -195,16 +188,11 @@ __global__ void __launch_bounds__(kThreads, 1) skinny_kernel(const __grid_consta
             const uint32_t src = tmem + ((uint32_t)(32 * q) << 16);
             float *part = reinterpret_cast<float *>(smem_raw + (base - smem0)) + 32 * q + lane;
             for (int c = 16 * half; c < nt; c += 32) {
-                uint32_t v[kAcc][16];
+                uint32_t v[16];
+                tc::tmem_ld16n(src + c, v);
+                tc::tmem_wait_ld(v);
 #pragma unroll
-                for (int i = 0; i < kAcc; ++i) tc::tmem_ld16n(src + i * nt + c, v[i]);
-#pragma unroll
-                for (int i = 0; i < kAcc; ++i) tc::tmem_wait_ld(v[i]);
-#pragma unroll
-                for (int i = 0; i < kAcc; ++i)
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        part[(c + j) * (kAcc * kBM + 4) + i * kBM] = __uint_as_float(v[i][j]);
+                for (int j = 0; j < 16; ++j) part[(c + j) * kRow] = __uint_as_float(v[j]);
             }
             tc::fence_before_sync();
         }
@@ -212,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1) skinny_kernel(const __grid_consta
     __syncthreads();
     if (S > 1) tc::cluster_sync();
     {
-        constexpr int W = Epi::kWidth, kPerRow = kBM / W;
+        constexpr int W = Epi::kWidth, kPerRow = kCols / W;
         const int items = P.T * kPerRow;
         const int i1 = (int)((long long)items * (rank + 1) / S);
         for (int i = (int)((long long)items * rank / S) + tid; i < i1; i += kThreads) {
@@ -221,11 +209,11 @@ __global__ void __launch_bounds__(kThreads, 1) skinny_kernel(const __grid_consta
             float v[W], w[W];
 #pragma unroll
             for (int j = 0; j < W; ++j) v[j] = w[j] = 0.f;
-            const uint32_t src = base + (uint32_t)(t * (kAcc * kBM + 4) + c) * 4;
+            const uint32_t src = base + (uint32_t)(t * kRow + c) * 4;
             add_ranks<W>(src, S, v);
-            if (kForm == kPair) add_ranks<W>(src + 4 * kBM, S, w);
+            if (kForm == kPair) add_ranks<W>(src + 4 * kCols, S, w);
             if (kForm != kPair && P.lo) {
-                add_ranks<W>(src + (uint32_t)(P.npad * (kAcc * kBM + 4)) * 4, S, w);
+                add_ranks<W>(src + (uint32_t)(P.npad * kRow) * 4, S, w);
 #pragma unroll
                 for (int j = 0; j < W; ++j) v[j] += w[j];
             }
@@ -240,20 +228,35 @@ __global__ void __launch_bounds__(kThreads, 1) skinny_kernel(const __grid_consta
     if (warp == 2) tc::tmem_dealloc(tmem, P.cols);
 }
 
-// How many CTAs split a tile's k: as many as shorten it and still run at once.
-inline int skinny_split(int tiles, int kb, uint32_t stage, int sms) {
-    int best = 1;
-    double best_t = 1e30;
+// How many CTAs split a tile's k -- as many as shorten it and still run at once -- and the estimated
+// time in ns, on the scale of plan().  The sums' exchange is slow (about 13 B/ns into an SM, by loads
+// or by bulk copies of the other CTAs' shared memory) and grows with the tokens.
+struct SkinnyPlan {
+    int S;
+    double ns;
+};
+inline SkinnyPlan skinny_plan(int T, int N, int kb, bool pair, int nt, int sms) {
+    const int cols = pair ? kBM / 2 : kBM, tiles = (N + cols - 1) / cols;
+    SkinnyPlan best{1, 1e30};
     for (int S = 1; S <= 8 && S <= kb; ++S) {
         if (S > 1 && tiles > clusters_at_once(S, sms)) continue;
         const int waves = S > 1 ? 1 : (tiles + sms - 1) / sms;
-        const double t = (double)waves * ((kb + S - 1) / S) * stage / 100.0 + (S > 1 ? 1500.0 : 0.0);
-        if (t < best_t) {
-            best_t = t;
-            best = S;
-        }
+        const double t = 3000.0 + (double)waves * ((kb + S - 1) / S) * skinny_stage(nt) / 100.0 +
+                         (S > 1 ? 1500.0 + T * (kBM * 4 / 13.0) : 0.0);
+        if (t < best.ns) best = SkinnyPlan{S, t};
     }
     return best;
+}
+inline int pad_tokens(int T) { return (T + 15) / 16 * 16; }
+// Whether a product of T tokens takes this kernel rather than 128-row tiles of tokens.  Measured for
+// d 7168, f 1536, bf16, weights from memory, both products: 3 tokens 21.0 us here and 27.5 us there,
+// 33 22.0 and 28.3, 64 24.2 and 26.0, 131 29.1 and 31.5, 200 34.4 and 31.4; for d 2048, f 768 64 tokens
+// 13.9 and 13.4, 131 20.4 and 13.6.  The two estimates' difference is
+// not trusted for the fewest.
+static_assert(kSplitTokens <= 48, "a in two parts is read by this kernel alone");
+inline bool skinny_wins(int T, int N, int kb, bool pair, int sms) {
+    if (T > kSkinnyTokens) return false;
+    return T <= 48 || skinny_plan(T, N, kb, pair, pad_tokens(T), sms).ns < plan(&T, &N, 1, kb, pair, false, sms).ns;
 }
 
 // G: maps, T, N, lo, kb, kb_seg, early_w set; the rest is filled in here.
@@ -261,22 +264,22 @@ template <int kForm, bool kAmn, class Epi>
 cudaError_t launch_skinny(SkinnyArgs &G, bool bf16, const Epi &epi, int sms, cudaStream_t s) {
     static SmemAttr attr;
     const auto kernel = skinny_kernel<kForm, kAmn, Epi>;
-    constexpr bool kTwo = kForm == kPair;
+    constexpr int kCols = kForm == kPair ? kBM / 2 : kBM;
     const int nt = G.npad * (1 + G.lo);
-    const uint32_t stage = skinny_stage(nt, kTwo);
-    G.tiles = (G.N + kBM - 1) / kBM;
-    G.S = skinny_split(G.tiles, G.kb, stage, sms);
+    const uint32_t stage = skinny_stage(nt);
+    G.tiles = (G.N + kCols - 1) / kCols;
+    G.S = skinny_plan(G.T, G.N, G.kb, kForm == kPair, nt, sms).S;
     G.idesc = tc::idesc_half(kBM, nt, bf16, kAmn, false);
     // what one CTA will use, at least the room of the exchange
     const uint32_t most = (kSmemBudget - kBarBytes - 1024) / stage, need = (uint32_t)(G.kb + G.S - 1) / G.S;
-    const uint32_t sums = (uint32_t)nt * ((kTwo ? 2 : 1) * kBM + 4) * 4;
+    const uint32_t sums = (uint32_t)nt * (kBM + 4) * 4;
     G.stages = (int)(need < most ? need : most);
     if (G.stages > kMaxStages) G.stages = kMaxStages;
     if (G.stages < 1) return cudaErrorInvalidValue;
     uint32_t ring = G.stages * stage;
     if (ring < sums) ring = sums;
     G.cols = 32;
-    while (G.cols < (kTwo ? 2 : 1) * nt) G.cols *= 2;
+    while (G.cols < nt) G.cols *= 2;
     const uint32_t smem = kBarBytes + 1024 + ring;
     if (G.cols > kTmemCols || smem > kSmemBudget) return cudaErrorInvalidValue;
     cudaError_t e = ensure_smem(attr, reinterpret_cast<const void *>(kernel), (int)smem);
