@@ -24,6 +24,7 @@ int ok() {
 }
 int done(cudaError_t e, const char *what) {
     if (e == cudaSuccess) return ok();
+    cudaGetLastError(); // not left for the next call to find
     return fail(WASTE_ECUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 constexpr int32_t kMostRows = 1 << 30; // rows and columns of anything: their tiles' indices fit 32 bits

@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1) skinny_kernel(const __grid_consta
         // each quarter of the lanes, 16 tokens at a time in turn
         const int q = warp & 3, half = (warp - 3) >> 2;
         bool ok = true;
-        if (lane == 0) ok = tc::mbar_wait(bar_acc, 0);
+        if (lane == 0) ok = wait_tile(bar_acc, 0, kb1 - kb0);
         if (!__shfl_sync(0xffffffffu, ok, 0)) {
             *abort_flag = 1;
         } else {

@@ -46,7 +46,7 @@ class Mx4Matrix:
                 and t.device == self.device and (self.rows == 0 or t.stride(1) == 1)):
             require(False, f"{name}: a [{self.rows}, {self.cols}] tensor with contiguous rows, fp32, bf16 or fp16, "
                            f"on {self.device} is needed")
-        return max(t.stride(0), self.cols) if self.rows < 2 else t.stride(0)
+        return self.cols if self.rows < 2 else t.stride(0)
 
     def quantize(self, x: torch.Tensor, stream=None):
         """Replace this matrix by the quantised x [rows, cols]."""
