@@ -5,7 +5,8 @@
 //              (and g, u if kept) in the epilogue;  2. y = a Wd^T.
 // backward  1. da = dy Wd, a / dg / du in the epilogue from the kept g and u;
 //           2. dx = dg Wg + du Wu, one sum over both products;
-//           3. dWg = dg^T x, dWu = du^T x, dWd = dy^T a, three products of T terms in one launch.
+//           3. dWg = dg^T x, dWu = du^T x, dWd = dy^T a, three products of T terms in one launch, which
+//              runs beside 2.
 // Where a product runs over a matrix's rows (Wd, Wg, Wu in 1 and 2, everything in 3) the tiles go
 // to the tensor core MN-major, as they lie in memory: nothing is transposed.
 #include "dense_skinny.cuh"
@@ -131,7 +132,7 @@ cudaError_t launch_ffn_backward(const FfnBwd &P, cudaStream_t s) {
         GemmArgs G = {};
         G.K = P.d;
         G.kb = G.kb_seg = pieces(P.d);
-        const Plan L = plan(&P.T, &P.f, 1, G.kb, false, false, sms);
+        const Plan L = plan(&P.T, &P.f, 1, G.kb, false, false, sms, true);
         set_shape(G, L, &P.T, &P.f, 1, false);
         G.idesc = tc::idesc_half(kBM * L.cg, G.BN, bf16, false, true);
         if ((e = half_map(&G.ta[0], P.dy, P.T, P.d, kBM)) != cudaSuccess) return e;
@@ -180,6 +181,7 @@ cudaError_t launch_ffn_backward(const FfnBwd &P, cudaStream_t s) {
     if (!P.dwg) return cudaSuccess;
     const int M[3] = {P.f, P.f, P.d}, N[3] = {P.d, P.d, P.f};
     GemmArgs G = {};
+    G.late_wait = P.dx != nullptr; // needs what the first launch made, and the second waited for that
     G.K = P.T;
     G.kb = G.kb_seg = pieces(P.T);
     const Plan L = plan(M, N, 3, G.kb, false, false, sms);

@@ -91,8 +91,9 @@ int clusters_at_once(int S, int sms) {
 // one wave (a second one waits for whole clusters to end: twice the time).  Its constants are
 // fitted to 1,713 measured launches (3 to 8192 rows, 256 to 7168 columns and k, both kinds, every
 // shape below): over these it picks a launch 1.6 % slower than the best one, in the geometric
-// mean.
-Plan plan(const int *M, const int *N, int n, int kb, bool pair, bool mx4, int sms) {
+// mean.  heavy: an epilogue that reads and writes several matrices (the gradients': for 333 tokens, d
+// 1032, f 264 four CTAs a tile make the backward 22.7 -> 19.2 us).
+Plan plan(const int *M, const int *N, int n, int kb, bool pair, bool mx4, int sms, bool heavy) {
     Plan best{256, 1, 1, 1e30};
     int rows = 0;
     for (int i = 0; i < n; ++i) rows = std::max(rows, std::min(M[i], kBM));
@@ -106,6 +107,7 @@ Plan plan(const int *M, const int *N, int n, int kb, bool pair, bool mx4, int sm
         const double piece = (kBM + BN / cg) * kRowBytes / 88.8;
         double t = (cg == 2 ? 1370.0 : 0.0) + (double)waves * ((kb + S - 1) / S) * piece + rows * BN * 0.123;
         if (S > 1) t += 2240.0 + rows * BN * 0.285;
+        if (heavy) t += rows * BN * 0.3 / S; // split k splits the way out too
         if (t < best.ns) best = Plan{BN, S, cg, t};
     };
     // 4-bit: whole scale tiles (128 rows) of each product; 16-bit: any multiple of 32
