@@ -7,8 +7,6 @@ is in the library's kernels.
 """
 from __future__ import annotations
 
-import contextlib
-
 import torch
 
 from . import binding as B
@@ -29,14 +27,6 @@ def check(t, name: str, shape, dtypes, device):
                        f"{' or '.join(map(str, dtypes))} on {device} is needed")
 
 
-def on_device(device):
-    """The context in which to call the library for tensors on `device`: none if it is current."""
-    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-
-
-_HERE = contextlib.nullcontext()
-
-
 def make(shape, dtype, device, stream) -> torch.Tensor:
     """An output made for a call on `stream` (None or an integer handle: made on the current one)."""
     with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else None):
@@ -49,15 +39,12 @@ class Workspace:
 
     def __init__(self, nbytes: int, device):
         self.bytes = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-        with on_device(device):
-            self.home = B._stream(None)
+        self.home = B.stream_on(device.index, None)
 
-    def lend(self, stream) -> torch.Tensor:
-        if stream is None:
-            if B._stream(None) != self.home:
-                self.bytes.record_stream(torch.cuda.current_stream())
-        elif isinstance(stream, torch.cuda.Stream) and stream.cuda_stream != self.home:
-            self.bytes.record_stream(stream)
+    def lend(self, stream, handle: int) -> torch.Tensor:
+        """For a call on `stream`, whose handle is given."""
+        if handle != self.home and not isinstance(stream, int):
+            self.bytes.record_stream(torch.cuda.current_stream(self.bytes.device) if stream is None else stream)
         return self.bytes
 
 
@@ -113,6 +100,10 @@ class DenseExpert:
     def forward(self, x, out=None, mode: int = 0, save_g=None, save_u=None, stream=None):
         """out [T, d] (fp32 or the weights' type; made if None) = (mode 0) or += (mode 1) the
         block's output for x [T, d].  save_g, save_u [T, f] receive what backward needs."""
+        index = self.device.index
+        if torch.cuda.current_device() != index:
+            with torch.cuda.device(index):
+                return self.forward(x, out, mode, save_g, save_u, stream)
         T = self._tokens(x, "x")
         if out is None:
             require(mode == 0, "mode 1 adds to a given out")
@@ -121,9 +112,9 @@ class DenseExpert:
         for t, n in ((save_g, "save_g"), (save_u, "save_u")):
             if t is not None:
                 check(t, n, (T, self.f), self._own, self.device)
-        with on_device(self.device):
-            B.waste_ffn_forward(self.cfg, x, T, self.w_gate, self.w_up, self.w_down, out, ACT[out.dtype], mode,
-                                save_g, save_u, self._ws[0].lend(stream), stream)
+        h = B.stream_on(index, stream)
+        B.waste_ffn_forward(self.cfg, x, T, self.w_gate, self.w_up, self.w_down, out, ACT[out.dtype], mode, save_g,
+                            save_u, self._ws[0].lend(stream, h), h)
         return out
 
     def backward(self, dy, x, g, u, dx=None, dw_gate=None, dw_up=None, dw_down=None, accumulate: bool = False,
@@ -131,6 +122,10 @@ class DenseExpert:
         """Gradients for dy [T, d], given forward's x, g and u: into dx [T, d] (None: not computed)
         and the three weights' gradients (all or none; fp32 or the weights' type), added to
         what is there with accumulate."""
+        index = self.device.index
+        if torch.cuda.current_device() != index:
+            with torch.cuda.device(index):
+                return self.backward(dy, x, g, u, dx, dw_gate, dw_up, dw_down, accumulate, stream)
         T = self._tokens(dy, "dy")
         check(x, "x", (T, self.d), self._own, self.device)
         check(g, "g", (T, self.f), self._own, self.device)
@@ -142,6 +137,6 @@ class DenseExpert:
                         (dw_down, "dw_down", self.w_down)):
             if t is not None:
                 check(t, n, w.shape, (gt,) if gt in self._out else self._out, self.device)
-        with on_device(self.device):
-            B.waste_ffn_backward(self.cfg, dy, T, x, g, u, self.w_gate, self.w_up, self.w_down, dx, dw_gate, dw_up,
-                                 dw_down, ACT[gt], int(accumulate), self._workspace(1).lend(stream), stream)
+        h = B.stream_on(index, stream)
+        B.waste_ffn_backward(self.cfg, dy, T, x, g, u, self.w_gate, self.w_up, self.w_down, dx, dw_gate, dw_up, dw_down,
+                             ACT[gt], int(accumulate), self._workspace(1).lend(stream, h), h)

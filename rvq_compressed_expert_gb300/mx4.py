@@ -10,7 +10,7 @@ from __future__ import annotations
 import torch
 
 from . import binding as B
-from .dense import ACT, Workspace, check, make, on_device, require
+from .dense import ACT, Workspace, check, make, require
 
 _FLOATS = (torch.float32, torch.bfloat16, torch.float16)
 
@@ -50,17 +50,25 @@ class Mx4Matrix:
 
     def quantize(self, x: torch.Tensor, stream=None):
         """Replace this matrix by the quantised x [rows, cols]."""
+        index = self.device.index
+        if torch.cuda.current_device() != index:
+            with torch.cuda.device(index):
+                return self.quantize(x, stream)
         ld = self._plain(x, "x")
-        with on_device(self.device):
-            B.waste_mx4_quantize(x, ACT[x.dtype], self.rows, self.cols, ld, self.codes, self.scales, stream)
+        B.waste_mx4_quantize(x, ACT[x.dtype], self.rows, self.cols, ld, self.codes, self.scales,
+                             B.stream_on(index, stream))
 
     def dequantize(self, out: torch.Tensor | None = None, dtype=torch.float32, stream=None) -> torch.Tensor:
         """The values the codes stand for, into out [rows, cols] (made with dtype if None)."""
+        index = self.device.index
+        if torch.cuda.current_device() != index:
+            with torch.cuda.device(index):
+                return self.dequantize(out, dtype, stream)
         if out is None:
             out = make((self.rows, self.cols), dtype, self.device, stream)
         ld = self._plain(out, "out")
-        with on_device(self.device):
-            B.waste_mx4_dequantize(self.codes, self.scales, self.rows, self.cols, out, ACT[out.dtype], ld, stream)
+        B.waste_mx4_dequantize(self.codes, self.scales, self.rows, self.cols, out, ACT[out.dtype], ld,
+                               B.stream_on(index, stream))
         return out
 
 
@@ -70,14 +78,18 @@ def matmul(a: Mx4Matrix, b: Mx4Matrix, out: torch.Tensor | None = None, mode: in
     a b^T, summed in fp32."""
     if a.cols != b.cols:
         require(False, f"a has {a.cols} columns, b {b.cols}")
-    require(a.device == b.device, "a and b are on two devices")
+    if a.device != b.device:
+        require(False, "a and b are on two devices")
+    index = a.device.index
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return matmul(a, b, out, mode, dtype, stream)
     if out is None:
         require(mode == 0, "mode 1 adds to a given out")
         out = make((a.rows, b.rows), dtype, a.device, stream)
     check(out, "out", (a.rows, b.rows), _FLOATS, a.device)
-    with on_device(a.device):
-        B.waste_mx4_matmul(a.rows, b.rows, a.cols, a.codes, a.scales, b.codes, b.scales, out, ACT[out.dtype], mode,
-                           stream)
+    B.waste_mx4_matmul(a.rows, b.rows, a.cols, a.codes, a.scales, b.codes, b.scales, out, ACT[out.dtype], mode,
+                       B.stream_on(index, stream))
     return out
 
 
@@ -107,6 +119,10 @@ class Mx4Expert:
     def forward(self, x, out=None, mode: int = 0, stream=None):
         """out [T, d] (fp32, bf16 or fp16; made as x if None) = (mode 0) or += (mode 1) the block's
         output for x [T, d]."""
+        index = self.device.index
+        if torch.cuda.current_device() != index:
+            with torch.cuda.device(index):
+                return self.forward(x, out, mode, stream)
         require(isinstance(x, torch.Tensor) and x.dim() == 2, "x: a [T, d] tensor is needed")
         T = x.shape[0]
         if T > self.max_tokens:
@@ -116,7 +132,6 @@ class Mx4Expert:
             require(mode == 0, "mode 1 adds to a given out")
             out = make((T, self.d), x.dtype, self.device, stream)
         check(out, "out", (T, self.d), _FLOATS, self.device)
-        with on_device(self.device):
-            B.waste_mx4_ffn_forward(self.cfg, x, ACT[x.dtype], T, out, ACT[out.dtype], mode, self._ws.lend(stream),
-                                    stream)
+        h = B.stream_on(index, stream)
+        B.waste_mx4_ffn_forward(self.cfg, x, ACT[x.dtype], T, out, ACT[out.dtype], mode, self._ws.lend(stream, h), h)
         return out
