@@ -41,7 +41,7 @@ constexpr int kRowBytes = 128; // bytes of one row of a stage
 constexpr int kMaxStages = 8;
 constexpr int kMaxProb = 3;
 constexpr uint32_t kSmemBudget = 227 * 1024;
-constexpr uint32_t kPieceBytes = 4096; // an epilogue warp's 32 rows x 128 bytes on their way out
+constexpr uint32_t kPieceBytes = 2048; // an epilogue warp's 32 rows x 64 bytes on their way out
 constexpr uint32_t kBarBytes = 256;
 constexpr int kThreads = 352; // loader, issuer, allocator, eight epilogue warps
 constexpr int kTmemCols = 512;
@@ -58,7 +58,7 @@ struct GemmArgs {
     int kb_seg; // k pieces of one product
     int kb;     // k pieces in all (kSum: twice kb_seg)
     int K, skb;
-    uint32_t idesc;
+    uint32_t idesc, smem;
     // early_b: B does not come from the kernel before this one, so its first pieces are asked for
     // before waiting for that kernel
     int early_b;
@@ -225,13 +225,13 @@ template <int W, int kForm> struct Sums {
 
 template <int kCG, int kKind, int kForm, bool kAmn, bool kBmn, class Epi>
 __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs P, const __grid_constant__ Epi epi) {
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t smem0 = tc::smem_u32(smem_raw);
-    const uint32_t base = (smem0 + kBarBytes + 1023) & ~1023u; // stages
-    const uint32_t bars = smem0;                              // full[8], empty[8], accfull[2], accempty[2]
+    extern __shared__ __align__(1024) uint8_t smem_raw[]; // stages, pieces on their way out, barriers
+    const uint32_t smem0 = tc::smem_u32(smem_raw), base = smem0;
+    const uint32_t bars_at = P.smem - kBarBytes;
+    const uint32_t bars = smem0 + bars_at; // full[8], empty[8], accfull[2], accempty[2]
     const uint32_t bar_full = bars, bar_empty = bars + 64, bar_accf = bars + 128, bar_acce = bars + 144;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem_raw + 160);
-    volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem_raw + 164);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem_raw + bars_at + 160);
+    volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem_raw + bars_at + 164);
     const uint32_t drain = bars + 168;
 
     // one value a warp, and known to be: the loops' addresses stay in uniform registers
@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         const int q = warp & 3, half = (warp - 3) >> 2, r = 32 * q + lane;
         const int cols = kForm == kPair ? BN / 2 : BN;
         // split k: this CTA's partial sums go to shared memory, rows padded by 16 bytes
-        float4 *part = S > 1 ? reinterpret_cast<float4 *>(smem_raw + (base - smem0)) + r * (BN / 4 + 1) : nullptr;
+        float4 *part = S > 1 ? reinterpret_cast<float4 *>(smem_raw) + r * (BN / 4 + 1) : nullptr;
         int it = 0;
         for (int t = tile0; t < P.tiles; t += step, ++it) {
             const Tile T = tile_at<kForm, kCG>(P, t, rank);
@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 }
             };
             const bool any = 32 * q < T.rows;
-            const Out32 out{reinterpret_cast<uint4 *>(smem_raw + (base - smem0) + P.stages * stage_bytes) +
+            const Out32 out{reinterpret_cast<uint4 *>(smem_raw + P.stages * stage_bytes) +
                                 (warp - 3) * (kPieceBytes / 16),
                             T.m0 + 32 * q, T.rows - 32 * q, lane};
             if constexpr (kKind == kMx4) {
@@ -632,8 +632,8 @@ __device__ __forceinline__ void put_as(int dtype, void *out, size_t at, int n, i
         put(static_cast<__half *>(out) + at, n, N, vec, add, v);
 }
 // The same for the 32 rows of a warp, lane = row: the values cross through shared memory so that
-// consecutive lanes store consecutive 16-byte pieces of a row (64 or 128 bytes of each row at
-// once; a lane storing its own row touches 32 rows with every instruction).
+// consecutive lanes store consecutive 16-byte pieces of a row (64 bytes of each row at once; a
+// lane storing its own row touches 32 rows with every instruction).
 __device__ __forceinline__ int turned(int row, int piece, int pieces) {
     // pieces is 2, 4 or 8; permuted so that neither the writes (lane = row) nor the reads (lane =
     // piece) meet in a bank
@@ -642,6 +642,11 @@ __device__ __forceinline__ int turned(int row, int piece, int pieces) {
 template <class O, int W>
 __device__ __forceinline__ void put32(const Out32 &o, O *out, size_t ld, int n, int N, bool vec, bool add,
                                       const float (&v)[W]) {
+    if constexpr (W * sizeof(O) > 64) { // in two halves
+        put32(o, out, ld, n, N, vec, add, *reinterpret_cast<const float(*)[W / 2]>(v));
+        put32(o, out, ld, n + W / 2, N, vec, add, *reinterpret_cast<const float(*)[W / 2]>(v + W / 2));
+        return;
+    }
     constexpr int kPer = 16 / (int)sizeof(O), kPieces = W / kPer;
     if (sizeof(O) == 2 && add) { // the sum is rounded once: each lane its own row
         if (o.lane < o.rows) put(out + (size_t)(o.m + o.lane) * ld + n, n, N, vec, true, v);
@@ -875,15 +880,17 @@ cudaError_t launch_gemm_as(GemmArgs &G, const Epi &epi, int sms, cudaStream_t s)
     const auto kernel = gemm_kernel<kCG, kKind, kForm, kAmn, kBmn, Epi>;
     const uint32_t stage = stage_size(G.BN, kCG, kBmn, kKind == kMx4);
     const uint32_t turn = Epi::kTurns ? 8 * kPieceBytes : 0;
-    G.stages = (int)((kSmemBudget - kBarBytes - 1024 - turn) / stage);
-    if (G.stages > kMaxStages) G.stages = kMaxStages;
+    G.stages = (int)((kSmemBudget - kBarBytes - turn) / stage);
+    // 4-bit: a sixth stage makes it slower (the prompt of 2048 tokens 59.9 -> 61.3 us)
+    const int most_stages = kKind == kMx4 && G.BN == 256 ? 5 : kMaxStages;
+    if (G.stages > most_stages) G.stages = most_stages;
     G.nacc = 2;
     if (kKind == kMx4) { // the stages' scales take tensor memory too
         const int per = 8 + 8 * ((G.BN + 127) / 128);
         if (2 * G.BN + G.stages * per > kTmemCols) G.nacc = 1;
     }
-    const uint32_t smem = kBarBytes + 1024 + G.stages * stage + turn;
-    cudaError_t e = ensure_smem(attr, reinterpret_cast<const void *>(kernel), (int)smem);
+    const uint32_t smem = G.smem = G.stages * stage + turn + kBarBytes;
+    const cudaError_t e = ensure_smem(attr, reinterpret_cast<const void *>(kernel), (int)smem);
     if (e != cudaSuccess) return e;
     // The launch may begin while the kernel before it in the stream ends (grid_wait holds back
     // everything that touches memory): its setup hides behind that kernel's tail.
