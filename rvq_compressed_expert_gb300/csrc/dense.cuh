@@ -46,8 +46,9 @@ struct Mx4Mat {
 // (dense_gemv.cu); their a is fp32 in the workspace.
 constexpr int kGemvTokens = 1;
 constexpr int kMxGemvTokens = 2;
-// Calls of at most so many tokens keep what rounding a to 16 bits leaves too (twice the columns of
-// a product that the weights' way from memory bounds).
+// Calls of at most so many tokens keep what rounding a (dg, du) to 16 bits leaves too, and multiply
+// both parts: with few tokens the error of a few large values is not averaged out, and the products
+// are bound by the weights' way from memory or the gradients' to it.
 constexpr int kSplitTokens = 32;
 // Shared memory in which those of 4-bit weights stage nt rows of n quantised values.
 __host__ __device__ inline size_t mx_gemv_smem(int n, int nt) { return (size_t)nt * (n * 2 + (n / 32 + 15) / 16 * 16); }

@@ -30,14 +30,11 @@ struct GatedSplit {
     template <int W>
     __device__ __forceinline__ void row(int, int m, int n, const float (&cg)[W], const float (&cu)[W]) const {
         const size_t at = (size_t)m * f + n;
-        float v[W], r[W];
+        float v[W];
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-            v[i] = cg[i] * sigmoid(cg[i]) * cu[i];
-            r[i] = v[i] - (dtype == WASTE_ACT_BF16 ? (float)__float2bfloat16_rn(v[i]) : (float)__float2half_rn(v[i]));
-        }
+        for (int i = 0; i < W; ++i) v[i] = cg[i] * sigmoid(cg[i]) * cu[i];
         put_as(dtype, hi, at, n, f, true, false, v);
-        if (lo) put_as(dtype, lo, at, n, f, true, false, r);
+        if (lo) put_rest(dtype, lo, at, n, f, v);
         if (g) {
             put_as(dtype, g, at, n, f, true, false, cg);
             put_as(dtype, u, at, n, f, true, false, cu);
@@ -102,7 +99,7 @@ cudaError_t launch_ffn_forward(const FfnFwd &P, cudaStream_t s) {
         G.lo = split;
         if ((e = half_map(&G.ta[0], P.wd, P.d, P.f, kBM)) != cudaSuccess) return e;
         if ((e = half_map(&G.tb[0], P.a, P.T, P.f, G.npad)) != cudaSuccess) return e;
-        if (split && (e = half_map(&G.tb[1], lo, P.T, P.f, G.npad)) != cudaSuccess) return e;
+        if (split && (e = half_map(&G.tl[0], lo, P.T, P.f, G.npad)) != cudaSuccess) return e;
         return launch_skinny<kOne, false>(G, bf16, st, sms, s);
     }
     GemmArgs G = {};
@@ -120,7 +117,11 @@ cudaError_t launch_ffn_forward(const FfnFwd &P, cudaStream_t s) {
 cudaError_t launch_ffn_backward(const FfnBwd &P, cudaStream_t s) {
     const int sms = device_sm_count();
     const bool bf16 = P.dtype == WASTE_ACT_BF16;
-    const GatedGrad grad{P.g, P.u, P.a, P.dg, P.du, P.f, P.dtype};
+    // few tokens: a, dg and du in two parts
+    const bool split = P.T <= kSplitTokens;
+    const auto rest = [&](void *p) { return split ? static_cast<uint16_t *>(p) + (size_t)P.T * P.f : nullptr; };
+    void *a_lo = rest(P.a), *dg_lo = rest(P.dg), *du_lo = rest(P.du);
+    const GatedGrad grad{P.g, P.u, P.a, P.dg, P.du, P.f, P.dtype, a_lo, dg_lo, du_lo};
     cudaError_t e;
     if (skinny_wins(P.T, P.f, pieces(P.d), false, sms)) {
         SkinnyArgs G = skinny(P.T, P.f, P.d);
@@ -144,8 +145,10 @@ cudaError_t launch_ffn_backward(const FfnBwd &P, cudaStream_t s) {
         SkinnyArgs G = skinny(P.T, P.d, P.f);
         G.kb = 2 * G.kb_seg;
         G.early_w = 1;
-        const void *w[2] = {P.wg, P.wu}, *t[2] = {P.dg, P.du};
+        G.lo = split;
+        const void *w[2] = {P.wg, P.wu}, *t[2] = {P.dg, P.du}, *l[2] = {dg_lo, du_lo};
         for (int i = 0; i < 2; ++i) {
+            if (split && (e = half_map(&G.tl[i], l[i], P.T, P.f, G.npad)) != cudaSuccess) return e;
             if ((e = half_map(&G.ta[i], w[i], P.f, P.d, 64)) != cudaSuccess) return e;
             if ((e = half_map(&G.tb[i], t[i], P.T, P.f, G.npad)) != cudaSuccess) return e;
         }
@@ -164,11 +167,10 @@ cudaError_t launch_ffn_backward(const FfnBwd &P, cudaStream_t s) {
         const Plan L = plan(&P.T, &P.d, 1, G.kb, false, false, sms);
         set_shape(G, L, &P.T, &P.d, 1, false);
         G.idesc = tc::idesc_half(kBM * L.cg, G.BN, bf16, false, true);
-        const void *a[2] = {P.dg, P.du}, *b[2] = {P.wg, P.wu};
-        for (int i = 0; i < 2; ++i) {
-            if ((e = half_map(&G.ta[i], a[i], P.T, P.f, kBM)) != cudaSuccess) return e;
-            if ((e = half_map(&G.tb[i], b[i], P.f, P.d, 64)) != cudaSuccess) return e;
-        }
+        if ((e = half_map(&G.ta[0], P.dg, P.T, P.f, kBM)) != cudaSuccess) return e;
+        if ((e = half_map(&G.tb[0], P.wg, P.f, P.d, 64)) != cudaSuccess) return e;
+        if ((e = half_map(&G.ta2[0], P.du, P.T, P.f, kBM)) != cudaSuccess) return e;
+        if ((e = half_map(&G.tb2[0], P.wu, P.f, P.d, 64)) != cudaSuccess) return e;
         G.early_b = 1;
         Store st = {};
         st.out[0] = P.dx;
@@ -183,23 +185,28 @@ cudaError_t launch_ffn_backward(const FfnBwd &P, cudaStream_t s) {
     GemmArgs G = {};
     G.late_wait = P.dx != nullptr; // needs what the first launch made, and the second waited for that
     G.K = P.T;
-    G.kb = G.kb_seg = pieces(P.T);
+    G.kb_seg = pieces(P.T);
+    G.kb = split ? 2 * G.kb_seg : G.kb_seg; // the low parts' products behind the others'
     const Plan L = plan(M, N, 3, G.kb, false, false, sms);
     set_shape(G, L, M, N, 3, false);
     G.idesc = tc::idesc_half(kBM * L.cg, G.BN, bf16, true, true);
     const void *a[3] = {P.dg, P.du, P.dy}, *b[3] = {P.x, P.x, P.a};
+    const void *a2[3] = {dg_lo, du_lo, P.dy}, *b2[3] = {P.x, P.x, a_lo};
     void *out[3] = {P.dwg, P.dwu, P.dwd};
     Store st = {};
     for (int i = 0; i < 3; ++i) {
         if ((e = half_map(&G.ta[i], a[i], P.T, M[i], 64)) != cudaSuccess) return e;
         if ((e = half_map(&G.tb[i], b[i], P.T, N[i], 64)) != cudaSuccess) return e;
+        if (split && (e = half_map(&G.ta2[i], a2[i], P.T, M[i], 64)) != cudaSuccess) return e;
+        if (split && (e = half_map(&G.tb2[i], b2[i], P.T, N[i], 64)) != cudaSuccess) return e;
         st.out[i] = out[i];
         st.ld[i] = N[i];
     }
     st.dtype = P.grad_dtype;
     st.add = P.accumulate;
     st.vec = 1;
-    return launch_gemm<kHalf, kOne, true, true>(G, L, st, sms, s);
+    return split ? launch_gemm<kHalf, kSum, true, true>(G, L, st, sms, s)
+                 : launch_gemm<kHalf, kOne, true, true>(G, L, st, sms, s);
 }
 
 cudaError_t ffn_timeout(uint32_t *out) { return read_and_clear_timeout(out); }

@@ -31,8 +31,8 @@
 namespace wm {
 namespace dense {
 
-// kOne: up to three independent products of one k in one launch; kPair: two products with the same
-// A in one tile (columns [0, BN/2) by b0, the rest by b1); kSum: two products added.
+// kOne: up to three independent products of one k in one launch; kSum: the same, each the sum of two;
+// kPair: two products with the same A in one tile (columns [0, BN/2) by b0, the rest by b1).
 enum { kOne, kPair, kSum };
 enum { kHalf, kMx4 };
 
@@ -50,13 +50,14 @@ struct Prob {
     int M, N, tm, tn, begin; // sizes, tiles, first tile
 };
 struct GemmArgs {
-    CUtensorMap ta[kMaxProb], tb[kMaxProb];
+    CUtensorMap ta[kMaxProb], tb[kMaxProb];   // kPair: tb[0], tb[1] are the two products'
+    CUtensorMap ta2[kMaxProb], tb2[kMaxProb]; // kSum: where pieces of k past kb_seg come from
     CUtensorMap sa, sb[2]; // 4-bit operands: their scale tiles, [row tile * skb + tile of blocks]
     Prob prob[kMaxProb];
     int nprob, tiles;
     int BN, S, stages, nacc;
-    int kb_seg; // k pieces of one product
-    int kb;     // k pieces in all (kSum: twice kb_seg)
+    int kb_seg; // k pieces of the first part of a sum
+    int kb;     // k pieces in all (kSum: twice as many)
     int K, skb;
     uint32_t idesc, smem;
     // early_b: B does not come from the kernel before this one, so its first pieces are asked for
@@ -86,7 +87,7 @@ struct Tile {
 };
 template <int kForm, int kCG> __device__ __forceinline__ Tile tile_at(const GemmArgs &P, int t, int rank) {
     int p = 0;
-    if (kForm == kOne)
+    if (kForm != kPair)
         while (p + 1 < P.nprob && t >= P.prob[p + 1].begin) ++p;
     const Prob &Q = P.prob[p];
     t -= Q.begin;
@@ -294,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             const uint32_t sa = base + st * stage_bytes, full = full0 + 8 * st;
             const bool second = kForm == kSum && kb >= P.kb_seg;
             const int k = second ? kb - P.kb_seg : kb;
-            const CUtensorMap *ta = &P.ta[kForm == kSum ? (second ? 1 : 0) : T.p];
+            const CUtensorMap *ta = second ? &P.ta2[T.p] : &P.ta[T.p];
             const int kx = kKind == kMx4 ? k * kRowBytes : k * 64;
             if (kAmn) {
                 for (int i = 0; i < kBM / 64; ++i) load(sa + i * 8192, ta, T.m0 + 64 * i, kx, full);
@@ -308,8 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             const uint32_t sb = base + st * stage_bytes + a_bytes, full = full0 + 8 * st;
             const bool second = kForm == kSum && kb >= P.kb_seg;
             const int k = second ? kb - P.kb_seg : kb;
-            const CUtensorMap *tb =
-                &P.tb[kForm == kSum ? (second ? 1 : 0) : kForm == kPair ? (kCG == 2 ? rank : 0) : T.p];
+            const CUtensorMap *tb = second ? &P.tb2[T.p] : &P.tb[kForm == kPair ? (kCG == 2 ? rank : 0) : T.p];
             const int kx = kKind == kMx4 ? k * kRowBytes : k * 64;
             const int n0 = T.n0 + (kCG == 2 && kForm != kPair ? rank * (BN / 2) : 0);
             if (leads)
@@ -631,6 +631,16 @@ __device__ __forceinline__ void put_as(int dtype, void *out, size_t at, int n, i
     else
         put(static_cast<__half *>(out) + at, n, N, vec, add, v);
 }
+// What rounding v to the 16-bit type leaves, rounded to it.
+template <int W>
+__device__ __forceinline__ void put_rest(int dtype, void *out, size_t at, int n, int N, const float (&v)[W]) {
+    float r[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+        r[i] = v[i] - (dtype == WASTE_ACT_BF16 ? (float)__float2bfloat16_rn(v[i]) : (float)__float2half_rn(v[i]));
+    put_as(dtype, out, at, n, N, true, false, r);
+}
+
 // The same for the 32 rows of a warp, lane = row: the values cross through shared memory so that
 // consecutive lanes store consecutive 16-byte pieces of a row (64 bytes of each row at once; a
 // lane storing its own row touches 32 rows with every instruction).
@@ -788,6 +798,7 @@ struct GatedGrad {
     const void *g, *u;
     void *a, *dg, *du;
     int f, dtype;
+    void *a_lo, *dg_lo, *du_lo; // what rounding them left, or null (row() alone)
     __device__ __forceinline__ void ahead(int m, int n, int cols) const {
         const char *pg = static_cast<const char *>(g) + ((size_t)m * f + n) * 2;
         const char *pu = static_cast<const char *>(u) + ((size_t)m * f + n) * 2;
@@ -822,6 +833,11 @@ struct GatedGrad {
         put_as(dtype, a, at, n, f, true, false, x);
         put_as(dtype, dg, at, n, f, true, false, y);
         put_as(dtype, du, at, n, f, true, false, z);
+        if (a_lo) {
+            put_rest(dtype, a_lo, at, n, f, x);
+            put_rest(dtype, dg_lo, at, n, f, y);
+            put_rest(dtype, du_lo, at, n, f, z);
+        }
     }
     template <int W>
     __device__ __forceinline__ void tile(const Out32 &o, int, int n, const float (&da)[W], const float (&)[W]) const {

@@ -26,8 +26,9 @@ namespace dense {
 constexpr int kSkinnyTokens = 192;
 
 struct SkinnyArgs {
-    CUtensorMap ta[2], tb[2]; // weights (kPair: both products'; kSum: both segments'); tokens (kSum,
-                              // or the low part)
+    CUtensorMap ta[2]; // weights (kPair: both products'; else the two parts of a sum)
+    CUtensorMap tb[2]; // tokens (the two parts of a sum)
+    CUtensorMap tl[2]; // their low parts
     int T, N, npad, lo;       // tokens, columns of the result, tokens padded to 16, low part too
     int tiles, S, stages, cols;
     int kb, kb_seg;
@@ -101,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, 1) skinny_kernel(const __grid_consta
             const bool second = kForm == kSum && kb >= P.kb_seg;
             const int kx = (second ? kb - P.kb_seg : kb) * 64;
             tc::tma_load(at, &P.tb[second ? 1 : 0], kx, 0, full);
-            if (kForm != kSum && P.lo) tc::tma_load(at + P.npad * kRowBytes, &P.tb[1], kx, 0, full);
+            if (P.lo) tc::tma_load(at + P.npad * kRowBytes, &P.tl[second ? 1 : 0], kx, 0, full);
         };
         const int early = P.early_w ? min(P.stages, kb1 - kb0) : 0;
         if (tc::elect_one())

@@ -19,6 +19,15 @@ def tiny(t):
     return torch.finfo(t).smallest_normal * torch.finfo(t).eps / 2
 
 
+SPLIT = 32  # calls of at most so many tokens keep intermediate values in two parts of type t
+
+
+def kept(v, e, t, tokens):
+    """Bound on a value of magnitude v, off by e, on its way into the next product: rounded to t, or
+    to t and the rest to t again."""
+    return e + (rnd(v + e, t) if tokens > SPLIT else 2 * half(t) ** 2 * (v + e) + tiny(t))
+
+
 def rnd(v, t):
     """Bound on rounding values of magnitude at most v to type t."""
     return half(t) * v + tiny(t)
@@ -41,7 +50,7 @@ def forward(x, wg, wu, wd, t):
     a = g * s * u
     # |silu'| <= 1.1
     ea = 1.1 * eg * (u.abs() + eu) + (g * s).abs() * eu + FUN * a.abs()
-    ea = ea + rnd(a.abs() + ea, t)
+    ea = kept(a.abs(), ea, t, x.shape[0])
     y = a @ wd.T
     ey = ea @ wd.abs().T + ((a.abs() + ea) @ wd.abs().T) * (wd.shape[1] * SUM)
     return {"g": (g, eg), "u": (u, eu), "a": (a, ea), "y": (y, ey)}
@@ -55,13 +64,12 @@ def backward(dy, x, g, u, wg, wu, wd, t):
     eda = (dy.abs() @ wd.abs()) * (dy.shape[1] * SUM)
     a, du, dg = g * s * u, da * g * s, da * u * slope
 
-    def kept(v, e):  # a value with error e, rounded to t
-        e = e + FUN * v.abs()
-        return e + rnd(v.abs() + e, t)
+    def into(v, e):
+        return kept(v.abs(), e + FUN * v.abs(), t, x.shape[0])
 
     # the slope is a sum with cancellation: its own error is up to FUN of its terms
-    ea, edu = kept(a, torch.zeros_like(a)), kept(du, eda * (g * s).abs())
-    edg = kept(dg, eda * (u * slope).abs() + FUN * (da * u).abs() * s * (1 + g.abs() * (1 - s)))
+    ea, edu = into(a, torch.zeros_like(a)), into(du, eda * (g * s).abs())
+    edg = into(dg, eda * (u * slope).abs() + FUN * (da * u).abs() * s * (1 + g.abs() * (1 - s)))
 
     def prod(p, ep, q, n):  # p^T q with p off by ep
         v = p.T @ q
