@@ -41,7 +41,8 @@ int waste_dense_status(void);
  * d % 8 == 0, f % 8 == 0, both positive; dtype WASTE_ACT_BF16 or WASTE_ACT_F16: the type of x,
  * the weights, g, u, dy and dx.  Sums are held in fp32; a, dg and du are rounded once to dtype
  * on their way into the next product (calls of at most 32 tokens keep what that rounding leaves as
- * well, to about 2^-16 of the value in bf16 and 2^-22 in fp16). */
+ * well, to about 2^-16 of the value in bf16 and 2^-22 in fp16; an infinite weight or dy may then give NaN
+ * where one product would give an infinity). */
 typedef struct {
     uint32_t abi_version; /* must equal WASTE_MOE_ABI_VERSION */
     int32_t d;            /* hidden size */

@@ -631,13 +631,15 @@ __device__ __forceinline__ void put_as(int dtype, void *out, size_t at, int n, i
     else
         put(static_cast<__half *>(out) + at, n, N, vec, add, v);
 }
-// What rounding v to the 16-bit type leaves, rounded to it.
+// What rounding v to the 16-bit type leaves, rounded to it; nothing where it leaves the type's range.
 template <int W>
 __device__ __forceinline__ void put_rest(int dtype, void *out, size_t at, int n, int N, const float (&v)[W]) {
     float r[W];
 #pragma unroll
-    for (int i = 0; i < W; ++i)
-        r[i] = v[i] - (dtype == WASTE_ACT_BF16 ? (float)__float2bfloat16_rn(v[i]) : (float)__float2half_rn(v[i]));
+    for (int i = 0; i < W; ++i) {
+        const float h = dtype == WASTE_ACT_BF16 ? (float)__float2bfloat16_rn(v[i]) : (float)__float2half_rn(v[i]);
+        r[i] = isinf(h) ? 0.f : v[i] - h;
+    }
     put_as(dtype, out, at, n, N, true, false, r);
 }
 

@@ -257,6 +257,27 @@ def test_large_gates():
     assert (dw[0][:8, 0] == 8 * T).all() and (dw[0][8:] == 0).all() and (dw[2][:, 8:] == 0).all()
 
 
+@pytest.mark.parametrize("T", [2, 8, 32, 40])
+def test_past_fp16_is_infinite(T):
+    """a, du and dg past fp16's range in one column: infinities in what they enter (all other factors are
+    positive), and nowhere else."""
+    t, d, f = HF, 64, 64
+    x = torch.ones(T, d, dtype=t, device="cuda")
+    w = torch.full((f, d), 2.0 ** -6, dtype=t, device="cuda")
+    w[0] = 8.0
+    wd = torch.full((d, f), 0.5, dtype=t, device="cuda")
+    e = DenseExpert(w, w, wd, max_tokens=T)
+    sg, su = (torch.empty(T, f, dtype=t, device="cuda") for _ in range(2))
+    y = e.forward(x, torch.empty(T, d, device="cuda"), save_g=sg, save_u=su)
+    assert torch.isposinf(y).all()
+    assert (sg[:, 0] == 512).all() and (su[:, 1:] == 1).all()
+    dx, dwg, dwu, dwd = (torch.empty_like(v) for v in (x, w, w, wd))
+    e.backward(torch.full_like(x, 8.0), x, sg, su, dx, dwg, dwu, dwd)
+    assert torch.isposinf(dx).all()
+    for v in (dwg, dwu, dwd.T):
+        assert torch.isposinf(v[0]).all() and torch.isfinite(v[1:]).all()
+
+
 def test_expert_refusals():
     g = gen(2)
     W = weights(g, 64, 32, BF)
