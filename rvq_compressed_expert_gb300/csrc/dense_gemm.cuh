@@ -731,12 +731,6 @@ __device__ __forceinline__ void widen8(bool bf16, const uint4 &q, float (&v)[8])
     }
 }
 
-// The approximate exponential and quotient: relative errors of 2^-22 and of the argument's rounding,
-// |g| 2^-23, far below what the 16-bit or 4-bit rounding behind it leaves.  -88 keeps the quotient's
-// divisor where it is exact to the last bits (e^88 < 2^127); there and below the value is 0 to any
-// type written.  A NaN stays one: it is multiplied in again.
-__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-fmaxf(g, -88.f))); }
-
 struct Store {
     static constexpr int kWidth = 8;
     static constexpr bool kTurns = true;
@@ -820,7 +814,7 @@ struct GatedGrad {
         for (int j = 0; j < 8; ++j) {
             const float s = sigmoid(gv[j]), silu = gv[j] * s;
             x[j] = silu * uv[j];
-            y[j] = da[j] * uv[j] * s * (1.f + gv[j] * (1.f - s));
+            y[j] = da[j] * (uv[j] * (s * (1.f + gv[j] * (1.f - s)))); // no factor past the result's range
             z[j] = da[j] * silu;
         }
     }

@@ -51,7 +51,7 @@ __device__ __forceinline__ float add_lanes(float v) {
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
-__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.f + __expf(-fmaxf(g, -80.f))); }
+__device__ __forceinline__ float silu(float g) { return g * sigmoid(g); }
 
 template <class T> __device__ __forceinline__ T narrow(float v);
 template <> __device__ __forceinline__ float narrow<float>(float v) { return v; }

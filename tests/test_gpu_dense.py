@@ -257,6 +257,25 @@ def test_large_gates():
     assert (dw[0][:8, 0] == 8 * T).all() and (dw[0][8:] == 0).all() and (dw[2][:, 8:] == 0).all()
 
 
+@pytest.mark.parametrize("T", [1, 2, 4, 40])
+def test_far_gates_leave_nothing(T):
+    """Gates of -1000 beside values of 1e30: silu and its slope are 0 in fp32, and so is everything made
+    with them, on the way there too (da u alone is past fp32)."""
+    t, d, f = BF, 32, 32
+    x = torch.zeros(T, d, dtype=t, device="cuda")
+    x[:, 0] = 1.0
+    wg, wu = (torch.zeros(f, d, dtype=t, device="cuda") for _ in range(2))
+    wg[:, 0], wu[:, 0] = -1000.0, 1e30
+    wd = torch.ones(d, f, dtype=t, device="cuda")
+    e = DenseExpert(wg, wu, wd, max_tokens=T)
+    sg, su = (torch.empty(T, f, dtype=t, device="cuda") for _ in range(2))
+    assert (e.forward(x, save_g=sg, save_u=su) == 0).all()
+    out = [torch.full_like(v, 7.0) for v in (x, wg, wu, wd)]
+    e.backward(torch.full_like(x, 1e9), x, sg, su, *out)
+    assert all((v == 0).all() for v in out)
+    assert (Mx4Expert.from_dense(wg, wu, wd, max_tokens=T).forward(x) == 0).all()
+
+
 @pytest.mark.parametrize("T", [2, 8, 32, 40])
 def test_past_fp16_is_infinite(T):
     """a, du and dg past fp16's range in one column: infinities in what they enter (all other factors are
