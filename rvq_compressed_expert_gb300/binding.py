@@ -156,7 +156,7 @@ def load(path: str = LIB_PATH):
 
 
 def _ptr(x):
-    return x if x is None or type(x) is int else x.data_ptr()
+    return x if x is None or isinstance(x, int) else x.data_ptr()
 
 
 def stream_on(index: int, s) -> int:

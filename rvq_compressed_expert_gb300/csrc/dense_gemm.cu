@@ -58,11 +58,11 @@ __global__ void __launch_bounds__(kThreads, 1) cluster_probe_kernel() {}
 } // namespace
 
 // Clusters of S CTAs (2..8) that run at once on the current device: SMs come in groups that a
-// cluster does not cross, so fewer than SMs / S (on one GB300: 76, 46, 36, 28, 23, 15, 15).
-int clusters_at_once(int S, int sms) {
+// cluster does not cross, so fewer than SMs / S (on one GB300: 76, 46, 36, 28, 23, 15, 15).  0: none.
+int clusters_at_once(int S) {
     static std::atomic<int> cache[kMaxDevices][9];
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return sms / S / 2;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
     int n = cache[dev][S].load(std::memory_order_relaxed);
     if (n == 0) {
         static SmemAttr attr;
@@ -79,7 +79,7 @@ int clusters_at_once(int S, int sms) {
         if (ensure_smem(attr, reinterpret_cast<const void *>(cluster_probe_kernel), kSmemBudget) != cudaSuccess ||
             cudaOccupancyMaxActiveClusters(&n, cluster_probe_kernel, &cfg) != cudaSuccess || n < 1) {
             cudaGetLastError();
-            n = sms / S / 2;
+            return 0;
         }
         cache[dev][S].store(n, std::memory_order_relaxed);
     }
@@ -101,7 +101,8 @@ Plan plan(const int *M, const int *N, int n, int kb, bool pair, bool mx4, int sm
         const int w = pair ? BN / 2 : BN, h = kBM * cg;
         long long tiles = 0;
         for (int i = 0; i < n; ++i) tiles += (long long)((M[i] + h - 1) / h) * ((N[i] + w - 1) / w);
-        const int slots = S > 1 ? clusters_at_once(S, sms) : sms / cg;
+        const int slots = S > 1 ? clusters_at_once(S) : sms / cg;
+        if (slots < 1) return;
         const long long waves = (tiles + slots - 1) / slots;
         if (S > 1 && waves > 1) return;
         const double piece = (kBM + BN / cg) * kRowBytes / 88.8;

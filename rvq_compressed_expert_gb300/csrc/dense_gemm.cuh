@@ -868,7 +868,7 @@ struct Plan {
     int BN, S, cg;
     double ns; // estimated
 };
-int clusters_at_once(int S, int sms); // clusters of S CTAs that run at once
+int clusters_at_once(int S); // clusters of S CTAs that run at once
 Plan plan(const int *M, const int *N, int n, int kb, bool pair, bool mx4, int sms, bool heavy = false);
 
 // Fills in the plan and the tiles.

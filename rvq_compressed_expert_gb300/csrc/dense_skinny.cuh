@@ -240,7 +240,7 @@ inline SkinnyPlan skinny_plan(int T, int N, int kb, bool pair, int nt, int sms) 
     const int cols = pair ? kBM / 2 : kBM, tiles = (N + cols - 1) / cols;
     SkinnyPlan best{1, 1e30};
     for (int S = 1; S <= 8 && S <= kb; ++S) {
-        if (S > 1 && tiles > clusters_at_once(S, sms)) continue;
+        if (S > 1 && tiles > clusters_at_once(S)) continue;
         const int waves = S > 1 ? 1 : (tiles + sms - 1) / sms;
         const double t = 3000.0 + (double)waves * ((kb + S - 1) / S) * skinny_stage(nt) / 100.0 +
                          (S > 1 ? 1500.0 + T * (kBM * 4 / 13.0) : 0.0);
