@@ -84,7 +84,7 @@ cudaError_t launch_ffn_forward(const FfnFwd &P, cudaStream_t s) {
             G.ahead = static_cast<const uint8_t *>(P.wd);
             G.ahead_bytes = ahead;
         }
-        e = launch_gemm<kHalf, kPair, false, false>(G, L, Gated{P.a, P.g, P.u, P.f, P.dtype}, sms, s);
+        e = launch_gemm<kHalf, kPair, false, false>(G, L, Gated{{}, P.a, P.g, P.u, P.f, P.dtype}, sms, s);
     }
     if (e != cudaSuccess) return e;
     Store st = {};
@@ -121,7 +121,7 @@ cudaError_t launch_ffn_backward(const FfnBwd &P, cudaStream_t s) {
     const bool split = P.T <= kSplitTokens;
     const auto rest = [&](void *p) { return split ? static_cast<uint16_t *>(p) + (size_t)P.T * P.f : nullptr; };
     void *a_lo = rest(P.a), *dg_lo = rest(P.dg), *du_lo = rest(P.du);
-    const GatedGrad grad{P.g, P.u, P.a, P.dg, P.du, P.f, P.dtype, a_lo, dg_lo, du_lo};
+    const GatedGrad grad{{}, P.g, P.u, P.a, P.dg, P.du, P.f, P.dtype, a_lo, dg_lo, du_lo};
     cudaError_t e;
     if (skinny_wins(P.T, P.f, pieces(P.d), false, sms)) {
         SkinnyArgs G = skinny(P.T, P.f, P.d);

@@ -39,6 +39,19 @@ cudaError_t make_map(CUtensorMap *m, const void *p, int unit, int rows, size_t r
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+cudaError_t store_map(CUtensorMap *m, void *p, int bytes, int rows, int cols) {
+    const EncodeFn fn = encoder();
+    if (!fn) return cudaErrorNotSupported;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)cols * bytes};
+    const cuuint32_t box[2] = {(cuuint32_t)(64 / bytes), 32};
+    const cuuint32_t one[2] = {1, 1};
+    const CUresult r = fn(m, bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, p, dims, strides,
+                          box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                          CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 cudaError_t make_scale_map(CUtensorMap *m, const void *p, size_t tiles) {
     const EncodeFn fn = encoder();
     if (!fn) return cudaErrorNotSupported;

@@ -39,6 +39,20 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap *m
                  : "memory");
 }
 
+// A box from shared memory to global memory, with the map's swizzle; parts past the matrix's ends are left
+// out.  Copies gather in groups of the issuing thread: close_stores ends one, stores_read<N> waits
+// until all but the last N have read their shared memory, stores_done until everything is written.
+__device__ __forceinline__ void tma_store(const CUtensorMap *m, int x, int y, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(m), "r"(src),
+                 "r"(x), "r"(y)
+                 : "memory");
+}
+__device__ __forceinline__ void close_stores() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void stores_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 // ---- CTA pairs: one thread of the pair's first CTA issues for both ------------------------
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t slot_addr, uint32_t n_cols) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot_addr), "r"(n_cols)
