@@ -58,6 +58,9 @@ cudaError_t launch_ffn_forward(const FfnFwd &P, cudaStream_t s);
 cudaError_t launch_ffn_gemv(const FfnFwd &P, cudaStream_t s);
 cudaError_t launch_mx4_ffn_gemv(const void *x, int x_dtype, int T, const Mx4Mat &gate, const Mx4Mat &up,
                                 const Mx4Mat &down, float *a, void *out, int out_dtype, int mode, cudaStream_t s);
+// out = x w^T of one or two rows x, and whether this is the quicker way.
+bool mx4_gemv_wins(const Mx4Mat &x, const Mx4Mat &w);
+cudaError_t launch_mx4_gemv(const Mx4Mat &x, const Mx4Mat &w, void *out, int out_dtype, int mode, cudaStream_t s);
 cudaError_t launch_ffn_backward(const FfnBwd &P, cudaStream_t s);
 cudaError_t launch_mx4_quantize(const void *x, int dtype, int rows, int cols, int64_t ld, uint8_t *codes,
                                 uint8_t *scales, cudaStream_t s);

@@ -1,5 +1,5 @@
-// The gated feed-forward block for a few tokens (decode): the weights are read once, straight
-// into registers, and that reading is all that takes time.
+// The gated feed-forward block for a few tokens (decode), and the 4-bit product of as many rows: the
+// weights are read once, straight into registers, and that reading is all that takes time.
 //
 // Two launches.  gate_up: one column f of the block, its gate and up rows streamed (16 bytes a lane,
 // several pieces in flight) against the tokens' x, added across the lanes, a = silu(g) u written
@@ -250,6 +250,24 @@ template <class T> __device__ __forceinline__ void stage(const T *x, int T_, int
     }
     __syncthreads();
 }
+// The same of rows that are 4-bit already.
+__device__ __forceinline__ void stage_codes(const Mx4Mat &x, uint8_t *smem) {
+    const int nb = x.cols / 32, kb = (x.cols + 127) / 128;
+    for (int i = threadIdx.x; i < x.rows * nb; i += kMxThreads) {
+        const int t = i / nb, b = i - t * nb;
+        uint8_t *base = smem + t * mx_gemv_smem(x.cols, 1);
+        const uint4 q = __ldg(reinterpret_cast<const uint4 *>(x.codes + (size_t)t * (x.cols / 2)) + b);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        base[x.cols * 2 + b] = __ldg(x.scales + mx_scale_at(t, b, kb));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t h[4];
+            mx_halves8(w[j], h);
+            reinterpret_cast<uint4 *>(base)[j * nb + b] = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+    }
+    __syncthreads();
+}
 // Sum of the 32 products of a weight block and a staged block, exact.
 __device__ __forceinline__ float dot32(const uint4 &codes, const uint8_t *base, int nb, int b) {
     float s = 0.f;
@@ -333,31 +351,38 @@ __global__ void __launch_bounds__(kMxThreads) mx_gate_up_kernel(const T *__restr
     }
 }
 
-template <int NT>
-__global__ void __launch_bounds__(kMxThreads) mx_down_kernel(const float *__restrict__ a, Mx4Mat wd, void *out,
-                                                           int out_dtype, int add, int T_) {
+// out = x W^T for one or two rows x: fp32 (down: a, quantised here), or 4-bit already.  R rows of W a
+// warp, U blocks of each on the way at once in a lane.
+template <int NT, int R, int U, bool kQuantised>
+__global__ void __launch_bounds__(kMxThreads) mx_rows_kernel(const float *__restrict__ a, Mx4Mat x, Mx4Mat w, void *out,
+                                                             int out_dtype, int add, int T_) {
+    static_assert(R * NT <= 32, "a lane for each sum");
     extern __shared__ __align__(16) uint8_t smem[];
-    constexpr int U = 2;
-    const int f = wd.cols, d = wd.rows, nb = f / 32, kb = (f + 127) / 128;
-    const int lane = threadIdx.x & 31, row = (blockIdx.x * kMxWarps + (threadIdx.x >> 5)) * kMxDownRows;
-    uint4 q[kMxDownRows][U];
-    uint32_t sc[kMxDownRows][U];
+    const int n = w.cols, rows = w.rows, nb = n / 32, kb = (n + 127) / 128;
+    const int lane = threadIdx.x & 31, row = (blockIdx.x * kMxWarps + (threadIdx.x >> 5)) * R;
+    uint4 q[R][U];
+    uint32_t sc[R][U];
     const auto fetch = [&](int b0) {
 #pragma unroll
         for (int i = 0; i < U; ++i)
 #pragma unroll
-            for (int r = 0; r < kMxDownRows; ++r) {
+            for (int r = 0; r < R; ++r) {
                 const int b = b0 + 32 * i;
-                const bool in = b < nb && row + r < d;
-                q[r][i] = in ? load_stream(wd.codes + (size_t)(row + r) * (f / 2) + b * 16) : make_uint4(0, 0, 0, 0);
-                sc[r][i] = in ? __ldg(wd.scales + mx_scale_at(row + r, b, kb)) : 0;
+                const bool in = b < nb && row + r < rows;
+                q[r][i] = in ? load_stream(w.codes + (size_t)(row + r) * (n / 2) + b * 16) : make_uint4(0, 0, 0, 0);
+                sc[r][i] = in ? __ldg(w.scales + mx_scale_at(row + r, b, kb)) : 0;
             }
     };
-    fetch(lane);
+    if constexpr (!kQuantised) fetch(lane); // the kernel before this one made a, not W
     tc::grid_wait();
     tc::grid_release();
-    stage(a, T_, f, smem);
-    float s[kMxDownRows][NT] = {};
+    if constexpr (kQuantised) {
+        fetch(lane);
+        stage_codes(x, smem);
+    } else {
+        stage(a, T_, n, smem);
+    }
+    float s[R][NT] = {};
     for (int b0 = lane; b0 < nb;) {
 #pragma unroll
         for (int i = 0; i < U; ++i) {
@@ -366,24 +391,24 @@ __global__ void __launch_bounds__(kMxThreads) mx_down_kernel(const float *__rest
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 if (t >= T_) break;
-                const uint8_t *base = smem + t * mx_gemv_smem(f, 1);
-                const uint32_t sx = base[f * 2 + b];
+                const uint8_t *base = smem + t * mx_gemv_smem(n, 1);
+                const uint32_t sx = base[n * 2 + b];
 #pragma unroll
-                for (int r = 0; r < kMxDownRows; ++r) s[r][t] += scaled(dot32(q[r][i], base, nb, b), sx, sc[r][i]);
+                for (int r = 0; r < R; ++r) s[r][t] += scaled(dot32(q[r][i], base, nb, b), sx, sc[r][i]);
             }
         }
         b0 += 32 * U;
         if (b0 - lane < nb) fetch(b0);
     }
 #pragma unroll
-    for (int r = 0; r < kMxDownRows; ++r)
+    for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             const float y = add_lanes(s[r][t]);
-            if (lane == r * NT + t && t < T_ && row + r < d) put_as(out_dtype, out, (size_t)t * d + row + r, y, add);
+            if (lane == r * NT + t && t < T_ && row + r < rows)
+                put_as(out_dtype, out, (size_t)t * rows + row + r, y, add);
         }
 }
-static_assert(kMxDownRows * kMxGemvTokens <= 32, "a lane for each sum");
 
 template <class T, int NT>
 cudaError_t mx_forward(const T *x, int T_, const Mx4Mat &gate, const Mx4Mat &up, const Mx4Mat &down, float *a, void *out,
@@ -392,8 +417,8 @@ cudaError_t mx_forward(const T *x, int T_, const Mx4Mat &gate, const Mx4Mat &up,
                            x, gate, up, a, T_);
     if (e != cudaSuccess) return e;
     constexpr int kPer = kMxWarps * kMxDownRows;
-    return launch(mx_down_kernel<NT>, (down.rows + kPer - 1) / kPer, kMxThreads, (int)mx_gemv_smem(down.cols, T_), s,
-                  static_cast<const float *>(a), down, out, out_dtype, mode, T_);
+    return launch(mx_rows_kernel<NT, kMxDownRows, 2, false>, (down.rows + kPer - 1) / kPer, kMxThreads,
+                  (int)mx_gemv_smem(down.cols, T_), s, static_cast<const float *>(a), Mx4Mat{}, down, out, out_dtype, mode, T_);
 }
 template <class T>
 cudaError_t mx_forward_any(const void *x, int T_, const Mx4Mat &gate, const Mx4Mat &up, const Mx4Mat &down, float *a,
@@ -403,7 +428,32 @@ cudaError_t mx_forward_any(const void *x, int T_, const Mx4Mat &gate, const Mx4M
                    : mx_forward<T, 2>(p, T_, gate, up, down, a, out, out_dtype, mode, s);
 }
 
+template <int NT, int R, int U>
+cudaError_t mx_product(const Mx4Mat &x, const Mx4Mat &w, void *out, int out_dtype, int mode, cudaStream_t s) {
+    constexpr int kPer = kMxWarps * R;
+    return launch(mx_rows_kernel<NT, R, U, true>, (w.rows + kPer - 1) / kPer, kMxThreads, (int)mx_gemv_smem(w.cols, x.rows), s,
+                  static_cast<const float *>(nullptr), x, w, out, out_dtype, mode, x.rows);
+}
+// Rows of W from which on four of them a warp still give every SM a CTA.
+int many_rows() { return kMxWarps * kMxDownRows * device_sm_count(); }
+
 } // namespace
+
+// Products of one or two rows that the multiplications here do not hold up more than the tensor-core
+// kernel's setup and exchange would.  Here and there, us (rows x columns x k): 1 x 1536 x 7168 3.7 and
+// 7.2, 1 x 7168 x 1536 3.8 and 5.5, 1 x 7168 x 7168 9.7 and 11.4, 1 x 100000 x 2048 30.3 and 28.3; 2 x 1536 x
+// 7168 5.2 and 7.2, 2 x 2048 x 2048 2.8 and 5.8, 2 x 7168 x 1536 6.1 and 5.6, 2 x 7168 x 7168 17.8 and 11.1.
+bool mx4_gemv_wins(const Mx4Mat &x, const Mx4Mat &w) {
+    if (x.rows > kMxGemvTokens || mx_gemv_smem(x.cols, x.rows) > kMxGemvSmem) return false;
+    const int64_t values = (int64_t)w.rows * w.cols;
+    return x.rows == 1 ? values <= 1 << 27 : values <= 1 << 24 && w.rows < many_rows();
+}
+
+cudaError_t launch_mx4_gemv(const Mx4Mat &x, const Mx4Mat &w, void *out, int out_dtype, int mode, cudaStream_t s) {
+    return x.rows == 2                 ? mx_product<2, 1, 8>(x, w, out, out_dtype, mode, s)
+           : w.rows >= many_rows() ? mx_product<1, kMxDownRows, 2>(x, w, out, out_dtype, mode, s)
+                                       : mx_product<1, 1, 8>(x, w, out, out_dtype, mode, s);
+}
 
 cudaError_t launch_ffn_gemv(const FfnFwd &P, cudaStream_t s) {
     return P.dtype == WASTE_ACT_BF16 ? forward<__nv_bfloat16>(P, s) : forward<__half>(P, s);

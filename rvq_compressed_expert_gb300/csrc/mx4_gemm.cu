@@ -57,6 +57,7 @@ cudaError_t common(GemmArgs &G, Plan &L, const Mx4Mat &a, const Mx4Mat &b, bool 
 
 cudaError_t launch_mx4_matmul(const Mx4Mat &a, const Mx4Mat &b, void *out, int out_dtype, int mode, bool after_own,
                               cudaStream_t s) {
+    if (mx4_gemv_wins(a, b)) return launch_mx4_gemv(a, b, out, out_dtype, mode, s);
     const int sms = device_sm_count();
     GemmArgs G = {};
     Plan L;

@@ -397,7 +397,7 @@ def test_quantize_strided_rows():
     assert torch.equal(m1.dequantize().double(), R.mx_round(one))
 
 
-MATMULS = [(1, 1, 32), (1, 130, 7168), (2, 17, 96), (16, 64, 160), (100, 129, 128), (128, 256, 256), (129, 257, 288),
+MATMULS = [(1, 1, 32), (1, 130, 7168), (1, 5001, 1056), (1, 7, 24064), (1, 19000, 7168), (2, 17, 96), (2, 130, 12064), (2, 5001, 1056), (2, 999, 416), (3, 130, 7168), (16, 64, 160), (100, 129, 128), (128, 256, 256), (129, 257, 288),
            (300, 200, 1056), (257, 1000, 512), (640, 513, 2048), (1000, 1100, 544), (2500, 2100, 1056)]
 
 
