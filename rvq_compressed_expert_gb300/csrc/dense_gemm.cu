@@ -100,12 +100,14 @@ int clusters_at_once(int S) {
 }
 
 // The estimate, in ns: whole waves of tiles, each as long as its bytes need into one SM (its MMAs
-// are shorter, or as long); the last tile's way out; for split k the exchange of the sums, and only
-// one wave (a second one waits for whole clusters to end: twice the time).  Its constants are
-// fitted to 1,713 measured launches (3 to 8192 rows, 256 to 7168 columns and k, both kinds, every
-// shape below): over these it picks a launch 1.6 % slower than the best one, in the geometric
-// mean.  heavy: an epilogue that reads and writes several matrices (the gradients': for 333 tokens, d
-// 1032, f 264 four CTAs a tile make the backward 22.7 -> 19.2 us).
+// are shorter, or as long, and the way out of all but the last is behind the next one's loads); what a pair
+// costs more than a CTA alone, and with 4-bit operands, whose scales both CTAs copy, much more; for
+// split k the exchange of the sums, and only one wave (a second one waits for whole clusters to end:
+// twice the time).  Its constants are fitted to 1,365 measured launches (16 to 3000 rows, 256 to 7168
+// columns and k, both kinds, every shape below): over these it picks a launch 0.7 % slower than the best
+// one, in the geometric mean (with the same for 4 bits 1.6 %: 509 x 7168 x 1536 in pairs 8.1 us, without 7.0).
+// heavy: an epilogue that reads and writes several matrices (the gradients': for 333 tokens, d 1032, f
+// 264 four CTAs a tile make the backward 22.7 -> 19.2 us).
 Plan plan(const int *M, const int *N, int n, int kb, bool pair, bool mx4, int sms, bool heavy) {
     Plan best{256, 1, 1, 1e30};
     int rows = 0;
@@ -118,10 +120,10 @@ Plan plan(const int *M, const int *N, int n, int kb, bool pair, bool mx4, int sm
         if (slots < 1) return;
         const long long waves = (tiles + slots - 1) / slots;
         if (S > 1 && waves > 1) return;
-        const double piece = (kBM + BN / cg) * kRowBytes / 88.8;
-        double t = (cg == 2 ? 1370.0 : 0.0) + (double)waves * ((kb + S - 1) / S) * piece + rows * BN * 0.123;
-        if (S > 1) t += 2240.0 + rows * BN * 0.285;
-        if (heavy) t += rows * BN * 0.3 / S; // split k splits the way out too
+        const double piece = (kBM + BN / cg) * kRowBytes / 80.0;
+        double t = (cg == 1 ? 0.0 : mx4 ? 4000.0 : 1570.0) + (double)waves * ((kb + S - 1) / S) * piece;
+        if (S > 1) t += 3400.0 + rows * BN * 0.43;
+        if (heavy) t += rows * BN * 0.6 / S; // split k splits the way out too
         if (t < best.ns) best = Plan{BN, S, cg, t};
     };
     // 4-bit: whole scale tiles (128 rows) of each product; 16-bit: any multiple of 32

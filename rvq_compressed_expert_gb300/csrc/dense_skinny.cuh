@@ -23,7 +23,7 @@ namespace wm {
 namespace dense {
 
 // Past these the sums of a CTA's tokens and the ring do not pay any more (an estimate decides below).
-constexpr int kSkinnyTokens = 192;
+constexpr int kSkinnyTokens = 144;
 
 struct SkinnyArgs {
     CUtensorMap ta[2]; // weights (kPair: both products'; else the two parts of a sum)
@@ -249,11 +249,11 @@ inline SkinnyPlan skinny_plan(int T, int N, int kb, bool pair, int nt, int sms) 
     return best;
 }
 inline int pad_tokens(int T) { return (T + 15) / 16 * 16; }
-// Whether a product of T tokens takes this kernel rather than 128-row tiles of tokens.  Measured for
-// d 7168, f 1536, bf16, weights from memory, both products: 3 tokens 21.0 us here and 27.5 us there,
-// 33 22.0 and 28.3, 64 24.2 and 26.0, 131 29.1 and 31.5, 200 34.4 and 31.4; for d 2048, f 768 64 tokens
-// 13.9 and 13.4, 131 20.4 and 13.6.  The two estimates' difference is
-// not trusted for the fewest.
+// Whether a product of T tokens takes this kernel rather than 128-row tiles of tokens.  Measured here and
+// there, forward, bf16, weights from memory, both products, us: d 7168, f 1536, 3 tokens 20.8 and 27.5, 64
+// 24.1 and 25.2, 131 27.5 and 29.7, 192 30.5 and 30.1; d 4096, f 1024, 64 15.2 and 16.4, 131 19.2 and 19.5,
+// 192 22.8 and 19.8; d 2048, f 768, 64 12.8 and 13.0, 131 13.4 and 13.3.  The two estimates' difference
+// is not trusted for the fewest.
 static_assert(kSplitTokens <= 48, "a in two parts is read by this kernel alone");
 inline bool skinny_wins(int T, int N, int kb, bool pair, int sms) {
     if (T > kSkinnyTokens) return false;
