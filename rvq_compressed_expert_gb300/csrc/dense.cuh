@@ -30,12 +30,14 @@ struct FfnFwd {
     const void *x, *wg, *wu, *wd;
     void *out, *g, *u; // g, u may be null
     void *a;           // workspace [T][f]
+    float *sums;       // and skinny_bytes(T)
 };
 struct FfnBwd {
     int d, f, T, dtype, grad_dtype, accumulate;
     const void *dy, *x, *g, *u, *wg, *wu, *wd;
     void *dx, *dwg, *dwu, *dwd; // dx or the three dw may be null
     void *a, *dg, *du;          // workspace [T][f] each
+    float *sums;                // and skinny_bytes(T)
 };
 struct Mx4Mat {
     const uint8_t *codes, *scales;
@@ -50,6 +52,17 @@ constexpr int kMxGemvTokens = 2;
 // both parts: with few tokens the error of a few large values is not averaged out, and the products
 // are bound by the weights' way from memory or the gradients' to it.
 constexpr int kSplitTokens = 32;
+// Calls of at most so many tokens may take the kernel with the weights on the MMA's row side
+// (dense_skinny.cuh; an estimate decides there), which splits k over at most so many CTAs; their partial
+// sums stand in the workspace.
+constexpr int kSkinnyTokens = 144, kSkinnyCtas = 160;
+inline int pad_tokens(int T) { return (T + 15) / 16 * 16; }
+// Bytes of partial sums for T tokens or fewer.
+inline size_t skinny_bytes(int T) {
+    const int few = T < kSplitTokens ? T : kSplitTokens, all = T < kSkinnyTokens ? T : kSkinnyTokens;
+    const int n = 2 * pad_tokens(few) > pad_tokens(all) ? 2 * pad_tokens(few) : pad_tokens(all);
+    return (size_t)kSkinnyCtas * n * 128 * 4;
+}
 // Shared memory in which those of 4-bit weights stage nt rows of n quantised values.
 __host__ __device__ inline size_t mx_gemv_smem(int n, int nt) { return (size_t)nt * (n * 2 + (n / 32 + 15) / 16 * 16); }
 constexpr size_t kMxGemvSmem = 48 << 10; // what a kernel may take without asking

@@ -68,6 +68,15 @@ size_t ffn_part(const waste_ffn_config *c, int32_t T) {
     return round_up(half > full ? half : full, 256);
 }
 
+// And for a call of few tokens its partial sums (a forward of kGemvTokens has none).
+size_t ffn_bytes(const waste_ffn_config *c, int32_t T, bool backward) {
+    const int parts = backward ? 3 : 1, few = T < kSkinnyTokens ? T : kSkinnyTokens;
+    const size_t all = parts * ffn_part(c, T);
+    if (few <= (backward ? 0 : kGemvTokens)) return all;
+    const size_t with_sums = parts * ffn_part(c, few) + skinny_bytes(few);
+    return all > with_sums ? all : with_sums;
+}
+
 int check_mx4_shape(int32_t rows, int32_t cols) {
     if (rows < 0 || rows > kMostRows) return fail(WASTE_EINVAL, "rows = %d outside [0, 2^30]", rows);
     if (cols <= 0 || cols % kMxBlock || cols > kMostRows)
@@ -134,7 +143,7 @@ int waste_ffn_workspace(const waste_ffn_config *cfg, int32_t T, int32_t backward
     const int rc = check_ffn(cfg, T);
     if (rc) return rc;
     if (!bytes) return fail(WASTE_EINVAL, "bytes is NULL");
-    *bytes = ffn_part(cfg, T) * (backward ? 3 : 1);
+    *bytes = ffn_bytes(cfg, T, backward);
     return ok();
 }
 
@@ -152,10 +161,10 @@ int waste_ffn_forward(const waste_ffn_config *cfg, const void *d_x, int32_t T, c
     const void *p[] = {d_x, d_w_gate, d_w_up, d_w_down, d_out, d_g, d_u};
     const char *n[] = {"x", "w_gate", "w_up", "w_down", "out", "g", "u"};
     rc = check_ptrs(p, n, d_g ? 7 : 5);
-    if (!rc) rc = check_workspace(d_workspace, workspace_bytes, ffn_part(cfg, T));
+    if (!rc) rc = check_workspace(d_workspace, workspace_bytes, ffn_bytes(cfg, T, false));
     if (rc) return rc;
     FfnFwd P{cfg->d, cfg->f, T, cfg->dtype, out_dtype, mode, d_x, d_w_gate, d_w_up, d_w_down, d_out, d_g, d_u,
-             d_workspace};
+             d_workspace, reinterpret_cast<float *>(static_cast<char *>(d_workspace) + ffn_part(cfg, T))};
     return done(launch_ffn_forward(P, reinterpret_cast<cudaStream_t>(stream)), "gated feed-forward");
 }
 
@@ -192,11 +201,12 @@ int waste_ffn_backward(const waste_ffn_config *cfg, const void *d_dy, int32_t T,
     const char *n[] = {"dy", "x", "g", "u", "w_gate", "w_up", "w_down", "dx"};
     rc = check_ptrs(p, n, d_dx ? 8 : 7);
     const size_t part = ffn_part(cfg, T);
-    if (!rc) rc = check_workspace(d_workspace, workspace_bytes, 3 * part);
+    if (!rc) rc = check_workspace(d_workspace, workspace_bytes, ffn_bytes(cfg, T, true));
     if (rc) return rc;
     char *w = static_cast<char *>(d_workspace);
     FfnBwd P{cfg->d, cfg->f,  T,      cfg->dtype, grad_dtype, accumulate, d_dy, d_x,      d_g,         d_u, d_w_gate,
-             d_w_up, d_w_down, d_dx, d_dw_gate,  d_dw_up,    d_dw_down,  w,    w + part, w + 2 * part};
+             d_w_up, d_w_down, d_dx, d_dw_gate,  d_dw_up,    d_dw_down,  w,    w + part, w + 2 * part,
+             reinterpret_cast<float *>(w + 3 * part)};
     return done(launch_ffn_backward(P, s), "gated feed-forward gradients");
 }
 

@@ -42,12 +42,13 @@ struct GatedSplit {
     }
 };
 
-SkinnyArgs skinny(int T, int N, int K) {
+SkinnyArgs skinny(int T, int N, int K, float *sums) {
     SkinnyArgs G = {};
     G.T = T;
     G.N = N;
     G.npad = pad_tokens(T);
     G.kb = G.kb_seg = pieces(K);
+    G.sums = sums;
     return G;
 }
 
@@ -63,7 +64,7 @@ cudaError_t launch_ffn_forward(const FfnFwd &P, cudaStream_t s) {
     // while this one adds up and ends
     const size_t wd = (size_t)P.d * P.f * 2, ahead = wd <= kAheadMost ? wd : 0;
     if (skinny_wins(P.T, P.f, pieces(P.d), true, sms)) {
-        SkinnyArgs G = skinny(P.T, P.f, P.d);
+        SkinnyArgs G = skinny(P.T, P.f, P.d, P.sums);
         if ((e = half_map(&G.ta[0], P.wg, P.f, P.d, kBM / 2)) != cudaSuccess) return e;
         if ((e = half_map(&G.ta[1], P.wu, P.f, P.d, kBM / 2)) != cudaSuccess) return e;
         if ((e = half_map(&G.tb[0], P.x, P.T, P.d, G.npad)) != cudaSuccess) return e;
@@ -94,7 +95,7 @@ cudaError_t launch_ffn_forward(const FfnFwd &P, cudaStream_t s) {
     st.add = P.mode;
     st.vec = 1; // d % 8 == 0
     if (skinny_wins(P.T, P.d, pieces(P.f), false, sms)) {
-        SkinnyArgs G = skinny(P.T, P.d, P.f);
+        SkinnyArgs G = skinny(P.T, P.d, P.f, P.sums);
         G.early_w = 1;
         G.lo = split;
         if ((e = half_map(&G.ta[0], P.wd, P.d, P.f, kBM)) != cudaSuccess) return e;
@@ -124,7 +125,7 @@ cudaError_t launch_ffn_backward(const FfnBwd &P, cudaStream_t s) {
     const GatedGrad grad{{}, P.g, P.u, P.a, P.dg, P.du, P.f, P.dtype, a_lo, dg_lo, du_lo};
     cudaError_t e;
     if (skinny_wins(P.T, P.f, pieces(P.d), false, sms)) {
-        SkinnyArgs G = skinny(P.T, P.f, P.d);
+        SkinnyArgs G = skinny(P.T, P.f, P.d, P.sums);
         if ((e = half_map(&G.ta[0], P.wd, P.d, P.f, 64)) != cudaSuccess) return e;
         if ((e = half_map(&G.tb[0], P.dy, P.T, P.d, G.npad)) != cudaSuccess) return e;
         e = launch_skinny<kOne, true>(G, bf16, grad, sms, s);
@@ -142,7 +143,7 @@ cudaError_t launch_ffn_backward(const FfnBwd &P, cudaStream_t s) {
         if (e != cudaSuccess) return e;
     }
     if (P.dx && skinny_wins(P.T, P.d, 2 * pieces(P.f), false, sms)) {
-        SkinnyArgs G = skinny(P.T, P.d, P.f);
+        SkinnyArgs G = skinny(P.T, P.d, P.f, P.sums);
         G.kb = 2 * G.kb_seg;
         G.early_w = 1;
         G.lo = split;

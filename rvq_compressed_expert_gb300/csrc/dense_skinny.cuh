@@ -8,9 +8,10 @@
 // matrix and only as many columns as there are tokens, so nearly all of it is weights that are read
 // once.  Every tile is split over k by a cluster, so that all SMs take part.
 //
-// The sums leave tensor memory transposed (a lane is a weight row) into shared memory rows per
-// token, meet there through distributed shared memory as in dense_gemm.cuh (each CTA adds up its
-// share in rank order), and go through the same epilogues.  One tile per CTA.
+// The sums leave tensor memory transposed (a lane is a weight row) into rows per token, each CTA of a
+// cluster adds up its share of them in rank order, and they go through the same epilogues as
+// dense_gemm.cuh's.  They meet in L2, in a part of the workspace: an SM reads another's shared memory
+// at about 13 B/ns, L2 at 100 (block of 131 tokens, d 7168, f 1536: 27.0 us and 24.8).  One tile per CTA.
 //
 // A token operand may come in two parts (lo: what rounding it to 16 bits left): their columns stand
 // side by side in one MMA and are added with the ranks.  The weights are on the way before the
@@ -21,9 +22,6 @@
 
 namespace wm {
 namespace dense {
-
-// Past these the sums of a CTA's tokens and the ring do not pay any more (an estimate decides below).
-constexpr int kSkinnyTokens = 144;
 
 struct SkinnyArgs {
     CUtensorMap ta[2]; // weights (kPair: both products'; else the two parts of a sum)
@@ -36,9 +34,28 @@ struct SkinnyArgs {
     int early_w;
     const uint8_t *ahead;
     size_t ahead_bytes;
+    float *sums; // S > 1: [CTA][token][128], kSkinnyCtas of them at most
 };
 
 __host__ __device__ inline uint32_t skinny_stage(int nt) { return (uint32_t)(kBM + nt) * kRowBytes; }
+
+// v += the W floats at p + s * step for each s < S, in that order; from L2 (another SM wrote them).
+template <int W> __device__ __forceinline__ void add_parts(const float *p, size_t step, int S, float (&v)[W]) {
+    static_assert(W == 8, "two pieces");
+    float4 x[8][2];
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+        if (s < S) {
+            x[s][0] = __ldcg(reinterpret_cast<const float4 *>(p + s * step));
+            x[s][1] = __ldcg(reinterpret_cast<const float4 *>(p + s * step) + 1);
+        }
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+        if (s < S) {
+            v[0] += x[s][0].x, v[1] += x[s][0].y, v[2] += x[s][0].z, v[3] += x[s][0].w;
+            v[4] += x[s][1].x, v[5] += x[s][1].y, v[6] += x[s][1].z, v[7] += x[s][1].w;
+        }
+}
 
 template <int kForm, bool kAmn, class Epi>
 __global__ void __launch_bounds__(kThreads, 1) skinny_kernel(const __grid_constant__ SkinnyArgs P,
@@ -188,12 +205,20 @@ __global__ void __launch_bounds__(kThreads, 1) skinny_kernel(const __grid_consta
             tc::fence_after_sync();
             const uint32_t src = tmem + ((uint32_t)(32 * q) << 16);
             float *part = reinterpret_cast<float *>(smem_raw + (base - smem0)) + 32 * q + lane;
+            float *out = P.sums + (size_t)blockIdx.x * nt * kBM + 32 * q + lane;
             for (int c = 16 * half; c < nt; c += 32) {
                 uint32_t v[16];
                 tc::tmem_ld16n(src + c, v);
                 tc::tmem_wait_ld(v);
+                if (S == 1) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) part[(c + j) * kRow] = __uint_as_float(v[j]);
+                    for (int j = 0; j < 16; ++j) part[(c + j) * kRow] = __uint_as_float(v[j]);
+                } else {
+                    const int left = P.T - (c < P.npad ? c : c - P.npad); // tokens from here on
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (j < left) __stcg(out + (size_t)(c + j) * kBM, __uint_as_float(v[j]));
+                }
             }
             tc::fence_before_sync();
         }
@@ -210,18 +235,27 @@ __global__ void __launch_bounds__(kThreads, 1) skinny_kernel(const __grid_consta
             float v[W], w[W];
 #pragma unroll
             for (int j = 0; j < W; ++j) v[j] = w[j] = 0.f;
-            const uint32_t src = base + (uint32_t)(t * kRow + c) * 4;
-            add_ranks<W>(src, S, v);
-            if (kForm == kPair) add_ranks<W>(src + 4 * kCols, S, w);
+            const int row = S > 1 ? kBM : kRow;
+            const float *src = S > 1 ? P.sums + (size_t)tile * S * nt * kBM : reinterpret_cast<float *>(smem_raw + (base - smem0));
+            src += (size_t)t * row + c;
+            const auto add = [&](const float *p, float(&x)[W]) {
+                if (S > 1) {
+                    add_parts<W>(p, (size_t)nt * kBM, S, x);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < W; ++j) x[j] += p[j];
+                }
+            };
+            add(src, v);
+            if (kForm == kPair) add(src + kCols, w);
             if (kForm != kPair && P.lo) {
-                add_ranks<W>(src + (uint32_t)(P.npad * kRow) * 4, S, w);
+                add(src + P.npad * row, w);
 #pragma unroll
                 for (int j = 0; j < W; ++j) v[j] += w[j];
             }
             epi.template row<W>(0, t, n0 + c, v, w);
         }
     }
-    if (S > 1) tc::cluster_sync(); // no CTA leaves while another reads its sums
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -230,8 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1) skinny_kernel(const __grid_consta
 }
 
 // How many CTAs split a tile's k -- as many as shorten it and still run at once -- and the estimated
-// time in ns, on the scale of plan().  The sums' exchange is slow (about 13 B/ns into an SM, by loads
-// or by bulk copies of the other CTAs' shared memory) and grows with the tokens.
+// time in ns, on the scale of plan().  The sums' exchange grows with the tokens.
 struct SkinnyPlan {
     int S;
     double ns;
@@ -240,15 +273,14 @@ inline SkinnyPlan skinny_plan(int T, int N, int kb, bool pair, int nt, int sms) 
     const int cols = pair ? kBM / 2 : kBM, tiles = (N + cols - 1) / cols;
     SkinnyPlan best{1, 1e30};
     for (int S = 1; S <= 8 && S <= kb; ++S) {
-        if (S > 1 && tiles > clusters_at_once(S)) continue;
+        if (S > 1 && (tiles > clusters_at_once(S) || tiles * S > kSkinnyCtas)) continue;
         const int waves = S > 1 ? 1 : (tiles + sms - 1) / sms;
         const double t = 3000.0 + (double)waves * ((kb + S - 1) / S) * skinny_stage(nt) / 100.0 +
-                         (S > 1 ? 1500.0 + T * (kBM * 4 / 13.0) : 0.0);
+                         (S > 1 ? 1500.0 + T * (kBM * 4 / 27.0) : 0.0);
         if (t < best.ns) best = SkinnyPlan{S, t};
     }
     return best;
 }
-inline int pad_tokens(int T) { return (T + 15) / 16 * 16; }
 // Whether a product of T tokens takes this kernel rather than 128-row tiles of tokens.  Measured here and
 // there, forward, bf16, weights from memory, both products, us: d 7168, f 1536, 3 tokens 20.8 and 27.5, 64
 // 24.1 and 25.2, 131 27.5 and 29.7, 192 30.5 and 30.1; d 4096, f 1024, 64 15.2 and 16.4, 131 19.2 and 19.5,
@@ -271,14 +303,14 @@ cudaError_t launch_skinny(SkinnyArgs &G, bool bf16, const Epi &epi, int sms, cud
     G.tiles = (G.N + kCols - 1) / kCols;
     G.S = skinny_plan(G.T, G.N, G.kb, kForm == kPair, nt, sms).S;
     G.idesc = tc::idesc_half(kBM, nt, bf16, kAmn, false);
-    // what one CTA will use, at least the room of the exchange
+    // what one CTA will use, at least the room of its sums if they stay there
     const uint32_t most = (kSmemBudget - kBarBytes - 1024) / stage, need = (uint32_t)(G.kb + G.S - 1) / G.S;
     const uint32_t sums = (uint32_t)nt * (kBM + 4) * 4;
     G.stages = (int)(need < most ? need : most);
     if (G.stages > kMaxStages) G.stages = kMaxStages;
     if (G.stages < 1) return cudaErrorInvalidValue;
     uint32_t ring = G.stages * stage;
-    if (ring < sums) ring = sums;
+    if (G.S == 1 && ring < sums) ring = sums;
     G.cols = 32;
     while (G.cols < nt) G.cols *= 2;
     const uint32_t smem = kBarBytes + 1024 + ring;
