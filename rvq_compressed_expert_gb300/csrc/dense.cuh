@@ -55,7 +55,7 @@ constexpr int kSplitTokens = 32;
 // Calls of at most so many tokens may take the kernel with the weights on the MMA's row side
 // (dense_skinny.cuh; an estimate decides there), which splits k over at most so many CTAs; their partial
 // sums stand in the workspace.
-constexpr int kSkinnyTokens = 144, kSkinnyCtas = 160;
+constexpr int kSkinnyTokens = 208, kSkinnyCtas = 160;
 inline int pad_tokens(int T) { return (T + 15) / 16 * 16; }
 // Bytes of partial sums for T tokens or fewer.
 inline size_t skinny_bytes(int T) {

@@ -276,16 +276,16 @@ inline SkinnyPlan skinny_plan(int T, int N, int kb, bool pair, int nt, int sms) 
         if (S > 1 && (tiles > clusters_at_once(S) || tiles * S > kSkinnyCtas)) continue;
         const int waves = S > 1 ? 1 : (tiles + sms - 1) / sms;
         const double t = 3000.0 + (double)waves * ((kb + S - 1) / S) * skinny_stage(nt) / 100.0 +
-                         (S > 1 ? 1500.0 + T * (kBM * 4 / 27.0) : 0.0);
+                         (S > 1 ? 500.0 + T * (kBM * 4 / 40.0) : 0.0);
         if (t < best.ns) best = SkinnyPlan{S, t};
     }
     return best;
 }
 // Whether a product of T tokens takes this kernel rather than 128-row tiles of tokens.  Measured here and
-// there, forward, bf16, weights from memory, both products, us: d 7168, f 1536, 3 tokens 20.8 and 27.5, 64
-// 24.1 and 25.2, 131 27.5 and 29.7, 192 30.5 and 30.1; d 4096, f 1024, 64 15.2 and 16.4, 131 19.2 and 19.5,
-// 192 22.8 and 19.8; d 2048, f 768, 64 12.8 and 13.0, 131 13.4 and 13.3.  The two estimates' difference
-// is not trusted for the fewest.
+// there, forward, bf16, weights from memory, both products, us: d 7168, f 1536, 3 tokens 20.6 and 27.5, 64
+// 22.7 and 25.2, 131 24.8 and 29.7, 192 26.4 and 29.5, 256 30.1 and 30.1; d 4096, f 1024, 64 13.7 and 16.4,
+// 131 16.4 and 19.5, 192 18.1 and 19.3, 256 20.7 and 19.8; d 2048, f 768, 131 12.4 and 13.3, 256 14.4 and
+// 13.1.  The two estimates' difference is not trusted for the fewest.
 static_assert(kSplitTokens <= 48, "a in two parts is read by this kernel alone");
 inline bool skinny_wins(int T, int N, int kb, bool pair, int sms) {
     if (T > kSkinnyTokens) return false;

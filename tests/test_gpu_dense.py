@@ -52,7 +52,7 @@ def guarded(*shape, dtype, fill=7.0):
 
 # d and f of one core matrix, below and past a tile, of no round number, and of the workloads
 SHAPES = [(1, 8, 8), (1, 1032, 1544), (2, 64, 24), (3, 256, 128), (5, 264, 1800), (8, 2056, 136), (9, 520, 136), (24, 2056, 1032), (32, 136, 4104), (33, 136, 264), (127, 1032, 136), (128, 512, 520), (129, 72, 1544),
-          (200, 1032, 264), (257, 264, 1032), (511, 648, 392), (1000, 1544, 776), (2049, 2056, 1032)]
+          (150, 2056, 1032), (200, 1032, 264), (208, 4104, 136), (257, 264, 1032), (511, 648, 392), (1000, 1544, 776), (2049, 2056, 1032)]
 
 
 @pytest.mark.parametrize("t", [BF, HF])
