@@ -19,7 +19,7 @@
 // in about 100 B/ns, so loads and MMAs are near balance, and long 16-bit products run at the power
 // limit.  Measured: block of 4096 tokens (d 7168, f 1536, bf16, g and u kept) 168 us = 1.61 PFLOP/s,
 // its gradients 347 us = 1.56 PFLOP/s (cuBLAS sustains 1.71 on a square product); 4-bit
-// 4096 x 7168 x 7168 70.7 us = 5.95 PFLOP/s, tensor pipe 62 % active.
+// 4096 x 7168 x 7168 68 us = 6.2 PFLOP/s, tensor pipe 63 % active.
 //
 // Waits are bounded: one that gives up (about a second) latches g_dense_timeout, which
 // waste_dense_status reports, and the CTA winds up.
