@@ -85,7 +85,7 @@ class DenseExpert:
         return ws
 
     def reserve_backward(self):
-        """Makes the backward's workspace (three [max_tokens, f] buffers) now."""
+        """Makes the backward's workspace (three [max_tokens, f] buffers, and partial sums of few tokens) now."""
         self._workspace(1)
 
     def _tokens(self, x, name):
