@@ -557,11 +557,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         __syncthreads();
         tc::cluster_sync();
         const Tile T = tile_at<kForm, kCG>(P, tile0, rank);
-        const int cols = kForm == kPair ? BN / 2 : BN, nc = cols / Epi::kWidth, items = T.rows * nc;
-        constexpr int W = Epi::kWidth;
-        // items of W columns, a contiguous share for each CTA of the cluster
-        const int i1 = (int)((long long)items * (rank + 1) / S);
-        for (int i = (int)((long long)items * rank / S) + tid; i < i1; i += kThreads) {
+        constexpr int W = Epi::kWidth, kLanes = Epi::kLanes;
+        const int cols = kForm == kPair ? BN / 2 : BN, nc = cols / W, items = T.rows * nc / kLanes;
+        // items of W columns for kLanes lanes each, a contiguous share for each CTA of the cluster
+        const int i1 = (int)((long long)items * (rank + 1) / S) * kLanes;
+        for (int i = (int)((long long)items * rank / S) * kLanes + tid; i < i1; i += kThreads) {
             const int rr = i / nc, c = (i - rr * nc) * W;
             float v[W], w[W];
 #pragma unroll
@@ -603,7 +603,7 @@ cudaError_t store_map(CUtensorMap *m, void *p, int bytes, int rows, int cols);
 // ---- epilogues -----------------------------------------------------------------------------
 // kTurns: tile() needs the shared memory of Out32, and maps() makes tensor maps of the outputs for it.
 // ahead(m, n, cols) (kAhead): row m of a tile will be taken from column n on.  row<W>(p, m, n, c, c2): W consecutive sums of row m from column n of problem p (n a multiple
-// of W); columns at or past N are left out.  tile<W>(o, p, n, c, c2): the same for the 32 rows of
+// of W; kLanes neighbouring lanes take neighbouring pieces at once); columns at or past N are left out.  tile<W>(o, p, n, c, c2): the same for the 32 rows of
 // a warp, lane = row, all lanes together.
 
 template <class O> __device__ __forceinline__ O round_to(float v);
@@ -786,7 +786,7 @@ __device__ __forceinline__ void widen8(bool bf16, const uint4 &q, float (&v)[8])
 }
 
 struct Store {
-    static constexpr int kWidth = 8;
+    static constexpr int kWidth = 8, kLanes = 1;
     static constexpr bool kTurns = true;
     static constexpr bool kAhead = false;
     CUtensorMap map[kMaxProb];
@@ -819,7 +819,7 @@ struct Store {
 
 // a = silu(g) u; g and u kept if asked for.  f % 8 == 0, so rows hold whole 16-byte pieces.
 struct Gated {
-    static constexpr int kWidth = 8;
+    static constexpr int kWidth = 8, kLanes = 1;
     static constexpr bool kTurns = true;
     static constexpr bool kAhead = false;
     CUtensorMap map[3];
@@ -858,7 +858,7 @@ struct Gated {
 
 // da -> a, dg, du from the kept g and u, which are asked of L2 while the tile's product runs.
 struct GatedGrad {
-    static constexpr int kWidth = 8;
+    static constexpr int kWidth = 8, kLanes = 1;
     static constexpr bool kTurns = true;
     static constexpr bool kAhead = true;
     CUtensorMap map[3];
