@@ -590,6 +590,32 @@ def test_streams_and_graphs():
         assert torch.equal(o[0], want[i][0]) and torch.equal(o[1], want[i][1])
 
 
+@pytest.mark.parametrize("T,d,f", [(3, 2048, 768), (20, 1920, 608), (131, 4096, 1024), (300, 1024, 288)])
+def test_repeats_give_the_same_bits(T, d, f):
+    """Calls one behind another, with another stream's work beside some of them: every output's bits are the
+    first call's (split sums meet in one order, whoever is first)."""
+    g = gen(T + d)
+    t = BF
+    W = weights(g, d, f, t)
+    e, q = DenseExpert(*W, max_tokens=T), Mx4Expert.from_dense(*W, max_tokens=T)
+    x, dy = randn(g, T, d, t=t), randn(g, T, d, t=t)
+    side, other = torch.cuda.Stream(), torch.zeros(1 << 26, device="cuda")
+    want, differ = None, torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(60):
+        if i % 3 == 0:
+            with torch.cuda.stream(side):
+                other.add_(1)
+        got = [torch.full_like(v, float("nan")) for v in (x, x, x, *W)]
+        sg, su = (torch.full((T, f), float("nan"), dtype=t, device="cuda") for _ in range(2))
+        e.forward(x, got[0], save_g=sg, save_u=su)
+        q.forward(x, got[1])
+        e.backward(dy, x, sg, su, *got[2:])
+        want = want or got
+        differ += ~torch.stack([(a == b).all() for a, b in zip(got, want)]).all()
+    assert int(differ) == 0
+    side.synchronize()
+
+
 @pytest.mark.parametrize("T", [1, 7, 40, 300])
 def test_backward_captured(T):
     """A captured backward, replayed on other inputs, gives the bits of a plain one; called through a
