@@ -613,7 +613,6 @@ template <> __device__ __forceinline__ float round_to<float>(float v) { return v
 
 template <class O> struct Pack {
     uint4 q;
-    __device__ void set(int i, float v) { reinterpret_cast<O *>(&q)[i] = round_to<O>(v); }
     __device__ float get(int i) const { return (float)reinterpret_cast<const O *>(&q)[i]; }
 };
 

@@ -20,9 +20,6 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
 // ---- TMA: one two-dimensional box, x the contiguous coordinate ----------------------------
-__device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *m) {
-    asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
-}
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *m, int x, int y, uint32_t mbar) {
     asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
                  "[%2];" ::"r"(dst),
