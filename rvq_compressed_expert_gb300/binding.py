@@ -167,6 +167,11 @@ def stream_on(index: int, s) -> int:
     return s if isinstance(s, int) else s.cuda_stream
 
 
+def device_now() -> int:
+    """The current device's index (CUDA is up: a tensor is on it)."""
+    return torch._C._cuda_getDevice()
+
+
 def _stream(s):
     return s if isinstance(s, int) else stream_on(torch.cuda.current_device() if s is None else 0, s)
 

@@ -67,7 +67,7 @@ class DenseExpert:
         check(w_down, "w_down", (d, f), (t,), dev)
         require(max_tokens >= 1, "max_tokens >= 1")
         self.w_gate, self.w_up, self.w_down = w_gate, w_up, w_down
-        self.d, self.f, self.dtype, self.device, self.max_tokens = d, f, t, dev, int(max_tokens)
+        self.d, self.f, self.dtype, self.device, self.index, self.max_tokens = d, f, t, dev, dev.index, int(max_tokens)
         self._own, self._out = (t,), (t, torch.float32)  # types of inputs, and of outputs
         self.cfg = B.waste_ffn_config(B.ABI_VERSION, d, f, ACT[t])
         self._ws = {}
@@ -100,8 +100,8 @@ class DenseExpert:
     def forward(self, x, out=None, mode: int = 0, save_g=None, save_u=None, stream=None):
         """out [T, d] (fp32 or the weights' type; made if None) = (mode 0) or += (mode 1) the
         block's output for x [T, d].  save_g, save_u [T, f] receive what backward needs."""
-        index = self.device.index
-        if torch.cuda.current_device() != index:
+        index = self.index
+        if B.device_now() != index:
             with torch.cuda.device(index):
                 return self.forward(x, out, mode, save_g, save_u, stream)
         T = self._tokens(x, "x")
@@ -122,8 +122,8 @@ class DenseExpert:
         """Gradients for dy [T, d], given forward's x, g and u: into dx [T, d] (None: not computed)
         and the three weights' gradients (all or none; fp32 or the weights' type), added to
         what is there with accumulate."""
-        index = self.device.index
-        if torch.cuda.current_device() != index:
+        index = self.index
+        if B.device_now() != index:
             with torch.cuda.device(index):
                 return self.backward(dy, x, g, u, dx, dw_gate, dw_up, dw_down, accumulate, stream)
         T = self._tokens(dy, "dy")

@@ -24,7 +24,8 @@ class Mx4Matrix:
         require(dev.type == "cuda", "codes and scales are tensors on a GPU")
         check(codes, "codes", (rows, cols // 2), (torch.uint8,), dev)
         check(scales, "scales", (ns,), (torch.uint8,), dev)
-        self.rows, self.cols, self.codes, self.scales, self.device = rows, cols, codes, scales, dev
+        self.rows, self.cols, self.codes, self.scales = rows, cols, codes, scales
+        self.device, self.index = dev, dev.index
 
     @classmethod
     def empty(cls, rows: int, cols: int, device="cuda") -> "Mx4Matrix":
@@ -50,8 +51,8 @@ class Mx4Matrix:
 
     def quantize(self, x: torch.Tensor, stream=None):
         """Replace this matrix by the quantised x [rows, cols]."""
-        index = self.device.index
-        if torch.cuda.current_device() != index:
+        index = self.index
+        if B.device_now() != index:
             with torch.cuda.device(index):
                 return self.quantize(x, stream)
         ld = self._plain(x, "x")
@@ -60,8 +61,8 @@ class Mx4Matrix:
 
     def dequantize(self, out: torch.Tensor | None = None, dtype=torch.float32, stream=None) -> torch.Tensor:
         """The values the codes stand for, into out [rows, cols] (made with dtype if None)."""
-        index = self.device.index
-        if torch.cuda.current_device() != index:
+        index = self.index
+        if B.device_now() != index:
             with torch.cuda.device(index):
                 return self.dequantize(out, dtype, stream)
         if out is None:
@@ -78,10 +79,10 @@ def matmul(a: Mx4Matrix, b: Mx4Matrix, out: torch.Tensor | None = None, mode: in
     a b^T, summed in fp32."""
     if a.cols != b.cols:
         require(False, f"a has {a.cols} columns, b {b.cols}")
-    if a.device != b.device:
+    index = a.index
+    if b.index != index:
         require(False, "a and b are on two devices")
-    index = a.device.index
-    if torch.cuda.current_device() != index:
+    if B.device_now() != index:
         with torch.cuda.device(index):
             return matmul(a, b, out, mode, dtype, stream)
     if out is None:
@@ -107,7 +108,7 @@ class Mx4Expert:
         require(gate.device == up.device == down.device, "the matrices are on two devices")
         require(max_tokens >= 1, "max_tokens >= 1")
         self.gate, self.up, self.down = gate, up, down
-        self.d, self.f, self.device, self.max_tokens = d, f, gate.device, int(max_tokens)
+        self.d, self.f, self.device, self.index, self.max_tokens = d, f, gate.device, gate.index, int(max_tokens)
         self.cfg = B.waste_mx4_ffn_config(B.ABI_VERSION, d, f, *(t.data_ptr() for m in (gate, up, down)
                                                                  for t in (m.codes, m.scales)))
         self._ws = Workspace(B.waste_mx4_ffn_workspace(self.cfg, self.max_tokens), self.device)
@@ -119,8 +120,8 @@ class Mx4Expert:
     def forward(self, x, out=None, mode: int = 0, stream=None):
         """out [T, d] (fp32, bf16 or fp16; made as x if None) = (mode 0) or += (mode 1) the block's
         output for x [T, d]."""
-        index = self.device.index
-        if torch.cuda.current_device() != index:
+        index = self.index
+        if B.device_now() != index:
             with torch.cuda.device(index):
                 return self.forward(x, out, mode, stream)
         require(isinstance(x, torch.Tensor) and x.dim() == 2, "x: a [T, d] tensor is needed")
