@@ -37,6 +37,12 @@ enum { WASTE_ACT_F16 = 2 }; /* beside WASTE_ACT_F32 and WASTE_ACT_BF16 */
  * used, and the context is to be treated as unusable, as after waste_moe_stats), else WASTE_OK. */
 int waste_dense_status(void);
 
+/* Test aid for that report: one CTA on `stream` waits, by the operators' own wait, on a barrier that
+ * nobody else arrives at, and latches the timeout if the wait gives up.  polls: 1 .. 2^18 polls of up to 4 us
+ * before it does, or 0: the operators' limit (2^18: 1.1 s).  arrive 1: the wait is over when it begins, and
+ * nothing is latched.  The context stays usable; the library never calls it. */
+int waste_dense_debug_wait(int32_t polls, int32_t arrive, waste_stream_t stream);
+
 /* ---- gated feed-forward block ---------------------------------------------------------
  * d % 8 == 0, f % 8 == 0, both positive; dtype WASTE_ACT_BF16 or WASTE_ACT_F16: the type of x,
  * the weights, g, u, dy and dx.  Sums are held in fp32; a, dg and du are rounded once to dtype

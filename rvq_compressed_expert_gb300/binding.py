@@ -40,7 +40,7 @@ EXPORTED = ["waste_moe_record_layout", "waste_moe_pack_records", "waste_moe_crea
             "waste_moe_create_banked", "waste_rvq_train", "waste_rvq_encode", "waste_moe_debug_wait"]
 
 # include/waste_dense.h
-EXPORTED_DENSE = ["waste_dense_status", "waste_ffn_workspace", "waste_ffn_forward", "waste_ffn_backward", "waste_mx4_layout",
+EXPORTED_DENSE = ["waste_dense_status", "waste_dense_debug_wait", "waste_ffn_workspace", "waste_ffn_forward", "waste_ffn_backward", "waste_mx4_layout",
                   "waste_mx4_quantize", "waste_mx4_dequantize", "waste_mx4_matmul", "waste_mx4_ffn_workspace",
                   "waste_mx4_ffn_forward"]
 
@@ -139,6 +139,7 @@ def load(path: str = LIB_PATH):
     i64 = ctypes.c_int64
     ffn, mx4 = ctypes.POINTER(waste_ffn_config), ctypes.POINTER(waste_mx4_ffn_config)
     lib.waste_dense_status.argtypes = []
+    lib.waste_dense_debug_wait.argtypes = [i32, i32, vp]
     lib.waste_ffn_workspace.argtypes = [ffn, i32, i32, ctypes.POINTER(sz)]
     lib.waste_ffn_forward.argtypes = [ffn, vp, i32, vp, vp, vp, vp, i32, i32, vp, vp, vp, sz, vp]
     lib.waste_ffn_backward.argtypes = [ffn, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, vp, sz, vp]
@@ -357,6 +358,11 @@ def waste_rvq_encode(w, codebooks, codes, err, stream=None):
 def waste_dense_status():
     """Raises WasteError (WASTE_ETIMEOUT) if a device wait of a dense operator gave up (synchronous)."""
     return _check(load().waste_dense_status())
+
+
+def waste_dense_debug_wait(polls=0, arrive=0, stream=None):
+    """Test aid: one bounded device wait that nobody ends (the library never calls it)."""
+    return _check(load().waste_dense_debug_wait(polls, arrive, _stream(stream)))
 
 
 def waste_ffn_workspace(cfg, T, backward=0) -> int:

@@ -86,6 +86,8 @@ cudaError_t launch_mx4_matmul(const Mx4Mat &a, const Mx4Mat &b, void *out, int o
 // of the product behind it.
 cudaError_t launch_mx4_gated(const Mx4Mat &x, const Mx4Mat &gate, const Mx4Mat &up, const Mx4Mat &next,
                              uint8_t *codes, uint8_t *scales, cudaStream_t s);
+// One CTA that waits on a barrier of its own (see waste_dense_debug_wait).
+cudaError_t launch_debug_wait(int polls, int arrive, cudaStream_t s);
 // *out |= whether a device wait of these kernels gave up since the last call (cleared).
 cudaError_t ffn_timeout(uint32_t *out);
 cudaError_t mx4_timeout(uint32_t *out);

@@ -3,6 +3,7 @@
 #include <cstdio>
 
 #include "dense.cuh"
+#include "tc_dev.cuh"
 
 using namespace wm;
 using namespace wm::dense;
@@ -137,6 +138,13 @@ int waste_dense_status(void) {
     if (e != cudaSuccess) return done(e, "reading the status");
     if (timeout) return fail(WASTE_ETIMEOUT, "a device wait of a dense operator gave up");
     return ok();
+}
+
+int waste_dense_debug_wait(int32_t polls, int32_t arrive, waste_stream_t stream) {
+    const NvtxRange nvtx_range(__func__);
+    if (polls < 0 || polls > tc::kWaitPolls) return fail(WASTE_EINVAL, "polls = %d outside [0, 2^18]", polls);
+    if (arrive != 0 && arrive != 1) return fail(WASTE_EINVAL, "arrive = %d", arrive);
+    return done(launch_debug_wait(polls ? polls : tc::kWaitPolls, arrive, reinterpret_cast<cudaStream_t>(stream)), "wait kernel");
 }
 
 int waste_ffn_workspace(const waste_ffn_config *cfg, int32_t T, int32_t backward, size_t *bytes) {

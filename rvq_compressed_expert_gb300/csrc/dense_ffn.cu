@@ -210,6 +210,24 @@ cudaError_t launch_ffn_backward(const FfnBwd &P, cudaStream_t s) {
                  : launch_gemm<kHalf, kOne, true, true>(G, L, st, sms, s);
 }
 
+namespace {
+__global__ void __launch_bounds__(32) debug_wait_kernel(int polls, int arrive) {
+    __shared__ __align__(8) uint64_t bar;
+    const uint32_t at = tc::smem_u32(&bar);
+    if (threadIdx.x == 0) {
+        tc::mbar_init(at, 1);
+        tc::mbar_init_fence();
+        if (arrive) tc::mbar_arrive(at);
+    }
+    __syncwarp();
+    if (!all(tc::mbar_wait(at, 0, polls)) && threadIdx.x == 0) atomicOr(&g_dense_timeout, 1u);
+}
+} // namespace
+cudaError_t launch_debug_wait(int polls, int arrive, cudaStream_t s) {
+    debug_wait_kernel<<<1, 32, 0, s>>>(polls, arrive);
+    return cudaGetLastError();
+}
+
 cudaError_t ffn_timeout(uint32_t *out) { return read_and_clear_timeout(out); }
 
 } // namespace dense

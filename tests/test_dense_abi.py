@@ -181,3 +181,8 @@ def test_reference_codes_by_hand():
     assert codes.shape == (130, 80) and scales.numel() == 2 * 2 * 512
     # row 129, block 4 (its one at column 129): second row tile, second tile of blocks; 1 = 4 x 2^-2
     assert scales[3 * 512 + 1 * 16 + 0 * 4 + 0] == 125 and codes[129, 64] == 6 << 4
+
+
+def test_debug_wait_refusals():
+    for a in ((-1, 0), ((1 << 18) + 1, 0), (1, 2), (1, -1)):
+        refused(B.waste_dense_debug_wait, *a, stream=0)
