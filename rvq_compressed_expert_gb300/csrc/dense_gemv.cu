@@ -24,10 +24,11 @@ namespace {
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kDownRows = 2;
 
-// streamed once: no place in L1, which keeps x (or a)
+// streamed once: no place in L1, which keeps x (or a).  Not a read-only load, here or below: these kernels begin
+// while the one before them ends, which may write what they read.
 __device__ __forceinline__ uint4 load_stream(const void *p) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
     return v;
@@ -83,9 +84,8 @@ constexpr int kRowPieces = 6; // the same of each row in down
 // warps and 7 pieces each 17.1, one column with 4 warps of 7 16.0, 8 warps of 4 15.3; d 2048, f 768:
 // 8 warps 5.6, 4 warps 4.9.
 template <class T, int Q>
-__global__ void __launch_bounds__(Q * 32) gate_up_kernel(const T *__restrict__ x, const T *__restrict__ wg,
-                                                                     const T *__restrict__ wu, float *__restrict__ a,
-                                                                     T *__restrict__ g, T *__restrict__ u, int d, int f) {
+__global__ void __launch_bounds__(Q * 32) gate_up_kernel(const T *x, const T *wg, const T *wu, float *a, T *g, T *u,
+                                                         int d, int f) {
     __shared__ float2 sums[Q];
     const int lane = threadIdx.x & 31, part = threadIdx.x >> 5, col = blockIdx.x;
     tc::grid_wait();
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(Q * 32) gate_up_kernel(const T *__restrict__ x
             float vg[8], vu[8], vx[8];
             widen8<T>(qg[i], vg);
             widen8<T>(qu[i], vu);
-            widen8<T>(__ldg(reinterpret_cast<const uint4 *>(x + k)), vx);
+            widen8<T>(*reinterpret_cast<const uint4 *>(x + k), vx);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 sg = fmaf(vg[j], vx[j], sg);
@@ -136,8 +136,8 @@ __global__ void __launch_bounds__(Q * 32) gate_up_kernel(const T *__restrict__ x
 }
 
 template <class T>
-__global__ void __launch_bounds__(kThreads) down_kernel(const float *__restrict__ a, const T *__restrict__ wd, void *out,
-                                                        int out_dtype, int add, int d, int f) {
+__global__ void __launch_bounds__(kThreads) down_kernel(const float *a, const T *wd, void *out, int out_dtype, int add,
+                                                        int d, int f) {
     const int lane = threadIdx.x & 31, row = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * kDownRows;
     float s[kDownRows] = {};
     uint4 q[kDownRows][kRowPieces];
@@ -221,7 +221,7 @@ constexpr int kMxWarps = 8, kMxThreads = kMxWarps * 32;
 template <class T> __device__ __forceinline__ void block_of(const T *p, float (&v)[32]) {
 #pragma unroll
     for (int i = 0; i < 32 * (int)sizeof(T) / 16; ++i) {
-        const uint4 q = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+        const uint4 q = reinterpret_cast<const uint4 *>(p)[i];
         if constexpr (sizeof(T) == 4) {
             v[4 * i] = __uint_as_float(q.x), v[4 * i + 1] = __uint_as_float(q.y);
             v[4 * i + 2] = __uint_as_float(q.z), v[4 * i + 3] = __uint_as_float(q.w);
@@ -257,9 +257,9 @@ __device__ __forceinline__ void stage_codes(const Mx4Mat &x, uint8_t *smem) {
     for (int i = threadIdx.x; i < x.rows * nb; i += kMxThreads) {
         const int t = i / nb, b = i - t * nb;
         uint8_t *base = smem + t * mx_gemv_smem(x.cols, 1);
-        const uint4 q = __ldg(reinterpret_cast<const uint4 *>(x.codes + (size_t)t * (x.cols / 2)) + b);
+        const uint4 q = reinterpret_cast<const uint4 *>(x.codes + (size_t)t * (x.cols / 2))[b];
         const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-        base[x.cols * 2 + b] = __ldg(x.scales + mx_scale_at(t, b, kb));
+        base[x.cols * 2 + b] = x.scales[mx_scale_at(t, b, kb)];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             uint32_t h[4];
@@ -301,8 +301,7 @@ __device__ __forceinline__ float scaled(float v, uint32_t a, uint32_t b) {
 }
 
 template <class T, int NT>
-__global__ void __launch_bounds__(kMxThreads) mx_gate_up_kernel(const T *__restrict__ x, Mx4Mat wg, Mx4Mat wu,
-                                                              float *__restrict__ a, int T_) {
+__global__ void __launch_bounds__(kMxThreads) mx_gate_up_kernel(const T *x, Mx4Mat wg, Mx4Mat wu, float *a, int T_) {
     extern __shared__ __align__(16) uint8_t smem[];
     constexpr int U = 4;
     const int d = wg.cols, f = wg.rows, nb = d / 32, kb = (d + 127) / 128;
@@ -320,7 +319,7 @@ __global__ void __launch_bounds__(kMxThreads) mx_gate_up_kernel(const T *__restr
                 const Mx4Mat &W = m ? wu : wg;
                 const bool in = b < nb && col < f;
                 q[m][i] = in ? load_stream(W.codes + (size_t)col * (d / 2) + b * 16) : make_uint4(0, 0, 0, 0);
-                sc[m][i] = in ? __ldg(W.scales + mx_scale_at(col, b, kb)) : 0;
+                sc[m][i] = in ? W.scales[mx_scale_at(col, b, kb)] : 0;
             }
         }
     };
@@ -355,7 +354,7 @@ __global__ void __launch_bounds__(kMxThreads) mx_gate_up_kernel(const T *__restr
 // out = x W^T for one or two rows x: fp32 (down: a, quantised here), or 4-bit already.  R rows of W a
 // warp, U blocks of each on the way at once in a lane.
 template <int NT, int R, int U, bool kQuantised>
-__global__ void __launch_bounds__(kMxThreads) mx_rows_kernel(const float *__restrict__ a, Mx4Mat x, Mx4Mat w, void *out,
+__global__ void __launch_bounds__(kMxThreads) mx_rows_kernel(const float *a, Mx4Mat x, Mx4Mat w, void *out,
                                                              int out_dtype, int add, int T_) {
     static_assert(R * NT <= 32, "a lane for each sum");
     extern __shared__ __align__(16) uint8_t smem[];
@@ -371,7 +370,7 @@ __global__ void __launch_bounds__(kMxThreads) mx_rows_kernel(const float *__rest
                 const int b = b0 + 32 * i;
                 const bool in = b < nb && row + r < rows;
                 q[r][i] = in ? load_stream(w.codes + (size_t)(row + r) * (n / 2) + b * 16) : make_uint4(0, 0, 0, 0);
-                sc[r][i] = in ? __ldg(w.scales + mx_scale_at(row + r, b, kb)) : 0;
+                sc[r][i] = in ? w.scales[mx_scale_at(row + r, b, kb)] : 0;
             }
     };
     if constexpr (!kQuantised) fetch(lane); // the kernel before this one made a, not W

@@ -11,7 +11,8 @@
 // the lanes: 66.4 us against 46.6 us (6.4 TB/s) for 16383 x 7168 bf16.
 // dequantize: a lane makes 16 bytes of output, so that every store instruction of a warp is
 // contiguous: 48.8 us for the same matrix (6.1 TB/s), 59.4 us with 32 bytes a lane.
-// The roundings are the hardware's e2m1 conversions.
+// The roundings are the hardware's e2m1 conversions.  Loads are ordinary ones, not read-only: the kernel before may
+// still write what is read here when this one begins.
 #include "dense.cuh"
 #include "dense_tc.cuh"
 
@@ -30,7 +31,7 @@ template <class T> struct Held {
     uint4 q[kPieces];
     __device__ __forceinline__ void load(const T *p) {
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) q[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+        for (int i = 0; i < kPieces; ++i) q[i] = reinterpret_cast<const uint4 *>(p)[i];
     }
     __device__ __forceinline__ void store(T *p) const {
 #pragma unroll
@@ -135,8 +136,8 @@ template <int kLane> __device__ __forceinline__ Walk walk(int cols) {
 }
 
 template <class T>
-__global__ void __launch_bounds__(kThreads) quantize_kernel(const T *__restrict__ x, int rows, int cols, int64_t ld,
-                                                            uint8_t *__restrict__ codes, uint8_t *__restrict__ scales) {
+__global__ void __launch_bounds__(kThreads) quantize_kernel(const T *x, int rows, int cols, int64_t ld, uint8_t *codes,
+                                                            uint8_t *scales) {
     const int lane = threadIdx.x & 31, kb = (cols + 127) / 128;
     const Walk K = walk<kPer>(cols);
     const bool in = K.col < cols;
@@ -185,9 +186,8 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const T *__restrict_
 }
 
 template <class T>
-__global__ void __launch_bounds__(kThreads) dequantize_kernel(const uint8_t *__restrict__ codes,
-                                                              const uint8_t *__restrict__ scales, int rows, int cols,
-                                                              T *__restrict__ out, int64_t ld) {
+__global__ void __launch_bounds__(kThreads) dequantize_kernel(const uint8_t *codes, const uint8_t *scales, int rows,
+                                                              int cols, T *out, int64_t ld) {
     constexpr int kLane = Out<T>::kPer, kDeep = Out<T>::kRows;
     using Codes = typename Out<T>::Codes;
     const int kb = (cols + 127) / 128;
@@ -202,8 +202,8 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const uint8_t *__r
         for (int i = 0; i < kDeep; ++i) {
             const int64_t r = r0 + (int64_t)i * K.step;
             if (r < rows) {
-                w[i] = __ldg(reinterpret_cast<const Codes *>(codes + (size_t)r * (cols / 2) + K.col / 2));
-                s[i] = __ldg(scales + mx_scale_at((int)r, K.col / kMxBlock, kb));
+                w[i] = *reinterpret_cast<const Codes *>(codes + (size_t)r * (cols / 2) + K.col / 2);
+                s[i] = scales[mx_scale_at((int)r, K.col / kMxBlock, kb)];
             }
         }
 #pragma unroll
