@@ -63,10 +63,6 @@ struct GemmArgs {
     // early_b: B does not come from the kernel before this one, so its first pieces are asked for
     // before waiting for that kernel
     int early_b;
-    // late_wait: nothing here comes from the kernel before this one, and that kernel (one of these
-    // operators') itself waited for what does, so this one runs beside it and waits for it only to
-    // end after it (work behind this kernel may rely on both)
-    int late_wait;
     // bytes that the next kernel reads and L2 can hold, asked for behind the own loads (or 0)
     const uint8_t *ahead;
     size_t ahead_bytes;
@@ -279,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     tc::fence_after_sync();
     constexpr uint32_t tmem = 0; // all columns are this CTA's, so they start at the first
     if (*tmem_slot != tmem && tid == 0) *abort_flag = 1;
-    if (warp != 0 && !P.late_wait) tc::grid_wait(); // warp 0's loader may have B's first pieces to ask for before
+    if (warp != 0) tc::grid_wait(); // warp 0's loader may have B's first pieces to ask for before
 
     const int kb0 = S > 1 ? (int)((long long)P.kb * rank / S) : 0;
     const int kb1 = S > 1 ? (int)((long long)P.kb * (rank + 1) / S) : P.kb;
@@ -344,8 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 for (int i = 0; i < early; ++i) load_b(T, kb0 + i, i);
             __syncwarp();
         }
-        if (!P.late_wait) tc::grid_wait();
-        tc::grid_release();
+        tc::grid_wait_release();
         for (int t = tile0; t < P.tiles && ok; t += step) {
             const Tile T = tile_at<kForm, kCG>(P, t, rank);
             for (int kb = kb0; kb < kb1; ++kb) {
@@ -578,7 +573,6 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     if (kCG == 2) tc::cluster_sync(); // nor while its memory takes part in the other's MMAs or barriers
     tc::fence_after_sync();
     if (tid == 0 && *abort_flag) atomicOr(&g_dense_timeout, 1u);
-    if (P.late_wait) tc::grid_wait();
     if (warp == 2) {
         if (kCG == 2)
             tc::tmem_dealloc_pair(tmem, kTmemCols);

@@ -88,8 +88,7 @@ __global__ void __launch_bounds__(Q * 32) gate_up_kernel(const T *x, const T *wg
                                                          int d, int f) {
     __shared__ float2 sums[Q];
     const int lane = threadIdx.x & 31, part = threadIdx.x >> 5, col = blockIdx.x;
-    tc::grid_wait();
-    tc::grid_release();
+    tc::grid_wait_release();
     const int all = (d + 255) / 256, first = all * part / Q, last = all * (part + 1) / Q;
     float sg = 0.f, su = 0.f;
     const T *pg = wg + (size_t)col * d, *pu = wu + (size_t)col * d;
@@ -151,8 +150,7 @@ __global__ void __launch_bounds__(kThreads) down_kernel(const float *a, const T 
             }
     };
     fetch(lane * 8);
-    tc::grid_wait();
-    tc::grid_release();
+    tc::grid_wait_release();
     for (int k0 = lane * 8; k0 - lane * 8 < f;) {
 #pragma unroll
         for (int i = 0; i < kRowPieces; ++i) {
@@ -306,8 +304,7 @@ __global__ void __launch_bounds__(kMxThreads) mx_gate_up_kernel(const T *x, Mx4M
     constexpr int U = 4;
     const int d = wg.cols, f = wg.rows, nb = d / 32, kb = (d + 127) / 128;
     const int lane = threadIdx.x & 31, col = blockIdx.x * kMxWarps + (threadIdx.x >> 5);
-    tc::grid_wait();
-    tc::grid_release();
+    tc::grid_wait_release();
     uint4 q[2][U];
     uint32_t sc[2][U];
     const auto fetch = [&](int b0) {
@@ -374,8 +371,7 @@ __global__ void __launch_bounds__(kMxThreads) mx_rows_kernel(const float *a, Mx4
             }
     };
     if constexpr (!kQuantised) fetch(lane); // the kernel before this one made a, not W
-    tc::grid_wait();
-    tc::grid_release();
+    tc::grid_wait_release();
     if constexpr (kQuantised) {
         fetch(lane);
         stage_codes(x, smem);

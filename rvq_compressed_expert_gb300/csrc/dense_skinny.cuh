@@ -125,8 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1) skinny_kernel(const __grid_consta
         if (tc::elect_one())
             for (int i = 0; i < early; ++i) load_w(kb0 + i, i);
         __syncwarp();
-        tc::grid_wait();
-        tc::grid_release();
+        tc::grid_wait_release();
         for (int kb = kb0; kb < kb1; ++kb) {
             if (issued >= early && !all(tc::mbar_wait(bar_empty + 8 * st, ph ^ 1))) {
                 ok = false;

@@ -174,10 +174,15 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
 }
 
 // ---- dependent launches ------------------------------------------------------------------
-// Wait until the kernels this launch depends on are complete and their writes visible; let the
-// kernel launched behind this one begin its own setup.
+// grid_wait: until the kernel before this one is complete and its writes visible.  grid_wait_release also lets
+// the kernel behind this one begin.  In every CTA of every kernel launched so, one warp or all call it, once, and
+// there is no other release: so when a kernel begins, all kernels but the one before it are complete.  That is what
+// a kernel may rely on before its own wait (weights that the kernel before it does not write are asked for there).
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait_release() {
+    grid_wait();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
 
 // Ask L2 for bytes (a multiple of 16, from a 16-byte aligned address).
 __device__ __forceinline__ void prefetch_l2(const void *p, uint32_t bytes) {

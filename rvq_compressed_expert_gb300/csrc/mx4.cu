@@ -141,8 +141,7 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const T *x, int rows
     const int lane = threadIdx.x & 31, kb = (cols + 127) / 128;
     const Walk K = walk<kPer>(cols);
     const bool in = K.col < cols;
-    tc::grid_wait();
-    tc::grid_release();
+    tc::grid_wait_release();
     for (int64_t r0 = K.row; r0 < rows; r0 += (int64_t)kRows * K.step) {
         Held<T> a[kRows];
 #pragma unroll
@@ -192,8 +191,7 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const uint8_t *cod
     using Codes = typename Out<T>::Codes;
     const int kb = (cols + 127) / 128;
     const Walk K = walk<kLane>(cols);
-    tc::grid_wait();
-    tc::grid_release();
+    tc::grid_wait_release();
     if (K.col >= cols) return;
     for (int64_t r0 = K.row; r0 < rows; r0 += (int64_t)kDeep * K.step) {
         Codes w[kDeep];
