@@ -250,7 +250,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     const int rank = kCG == 2 ? (int)(blockIdx.x & 1) : S > 1 ? (int)(blockIdx.x % S) : 0; // in the cluster
     const bool leads = kCG == 1 || rank == 0; // issues the MMAs
 
-    if (tid == 0) {
+    if (warp == 0 && P.early_b) tc::see_complete(); // while the others set up
+    if (tid == 32) {
         for (int i = 0; i < P.stages; ++i) {
             tc::mbar_init(bar_full + 8 * i, 1);
             tc::mbar_init(bar_empty + 8 * i, 1);

@@ -24,13 +24,19 @@ namespace {
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kDownRows = 2;
 
-// streamed once: no place in L1, which keeps x (or a).  Not a read-only load, here or below: these kernels begin
-// while the one before them ends, which may write what they read.
+// Weights, streamed once: no place in L1, which keeps x (or a), and from L2 (relaxed at the GPU's scope), where what
+// complete kernels wrote is: some are asked for before the kernel's own wait.  Nothing is read by read-only
+// loads: these kernels begin while the one before them ends, which may write what they read.
 __device__ __forceinline__ uint4 load_stream(const void *p) {
     uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.relaxed.gpu.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint32_t load_stream8(const uint8_t *p) {
+    uint32_t v;
+    asm volatile("ld.relaxed.gpu.global.u8 %0, [%1];" : "=r"(v) : "l"(p));
     return v;
 }
 __device__ __forceinline__ void widen(uint32_t w, float &lo, float &hi, __nv_bfloat16) {
@@ -149,7 +155,7 @@ __global__ void __launch_bounds__(kThreads) down_kernel(const float *a, const T 
                 q[r][i] = k < f && row + r < d ? load_stream(wd + (size_t)(row + r) * f + k) : make_uint4(0, 0, 0, 0);
             }
     };
-    fetch(lane * 8);
+    fetch(lane * 8); // the kernel before this one made a, not Wd
     tc::grid_wait_release();
     for (int k0 = lane * 8; k0 - lane * 8 < f;) {
 #pragma unroll
@@ -316,7 +322,7 @@ __global__ void __launch_bounds__(kMxThreads) mx_gate_up_kernel(const T *x, Mx4M
                 const Mx4Mat &W = m ? wu : wg;
                 const bool in = b < nb && col < f;
                 q[m][i] = in ? load_stream(W.codes + (size_t)col * (d / 2) + b * 16) : make_uint4(0, 0, 0, 0);
-                sc[m][i] = in ? W.scales[mx_scale_at(col, b, kb)] : 0;
+                sc[m][i] = in ? load_stream8(W.scales + mx_scale_at(col, b, kb)) : 0;
             }
         }
     };
@@ -367,7 +373,7 @@ __global__ void __launch_bounds__(kMxThreads) mx_rows_kernel(const float *a, Mx4
                 const int b = b0 + 32 * i;
                 const bool in = b < nb && row + r < rows;
                 q[r][i] = in ? load_stream(w.codes + (size_t)(row + r) * (n / 2) + b * 16) : make_uint4(0, 0, 0, 0);
-                sc[r][i] = in ? w.scales[mx_scale_at(row + r, b, kb)] : 0;
+                sc[r][i] = in ? load_stream8(w.scales + mx_scale_at(row + r, b, kb)) : 0;
             }
     };
     if constexpr (!kQuantised) fetch(lane); // the kernel before this one made a, not W

@@ -76,7 +76,8 @@ __global__ void __launch_bounds__(kThreads, 1) skinny_kernel(const __grid_consta
     const int n0 = tile * kCols;
     const int kb0 = (int)((long long)P.kb * rank / S), kb1 = (int)((long long)P.kb * (rank + 1) / S);
 
-    if (tid == 0) {
+    if (warp == 0 && P.early_w) tc::see_complete(); // while the others set up
+    if (tid == 32) {
         for (int i = 0; i < P.stages; ++i) {
             tc::mbar_init(bar_full + 8 * i, 1);
             tc::mbar_init(bar_empty + 8 * i, 1);

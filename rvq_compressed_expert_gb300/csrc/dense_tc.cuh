@@ -183,6 +183,11 @@ __device__ __forceinline__ void grid_wait_release() {
     grid_wait();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
+// Before loads or copies ahead of the own wait: what is complete (all but the kernel before this one) is seen by
+// this thread's loads, and by the copies that it starts (another proxy), as after a wait.
+__device__ __forceinline__ void see_complete() {
+    asm volatile("fence.acq_rel.gpu;\n\tfence.proxy.async.global;" ::: "memory");
+}
 
 // Ask L2 for bytes (a multiple of 16, from a 16-byte aligned address).
 __device__ __forceinline__ void prefetch_l2(const void *p, uint32_t bytes) {

@@ -50,3 +50,31 @@ def test_kernels_release_behind_their_own_wait():
             assert len(lines) == 1 and lines[0].strip() == f"tc::{name}();", (p, lines)
             assert "return;" not in kernel[:kernel.index(lines[0])], p
     assert launched == 8
+
+
+def test_loads_ahead_of_the_wait_see_what_is_complete():
+    """Weights that a kernel asks for before its own wait: copies stand behind the fence that makes complete kernels'
+    writes visible to them, loads are answered by L2 (relaxed at the GPU's scope), not by an SM's cache."""
+    copies = loads = 0
+    for p in FILES:
+        text = code(p)
+        for part in re.split(r"__global__ void", text)[1:]:
+            if "tc::grid_wait_release()" not in part:
+                continue
+            before = part[:part.index("tc::grid_wait_release()")]
+            fetch = re.search(r"const auto fetch = \[&\]\(.*?\n    \};", before, flags=re.S)
+            run = re.sub(r"const auto \w+ = \[&?\]\(.*?\n\s*\};", "", before, flags=re.S)  # not what is only defined there
+            at = [m.start() for m in re.finditer(r"\b(?:load_\w+|tc::tma_load\w*)\(", run)]
+            if at:
+                copies += 1
+                assert "tc::see_complete();" in run and run.index("tc::see_complete();") < min(at), p
+            if re.search(r"\bfetch\(", run):
+                loads += 1
+                assert "load_stream(" in fetch.group(0), p
+                bare = re.sub(r"load_stream8?\([^:]*", "", fetch.group(0))
+                assert not re.search(r"\.(?:codes|scales)\b|\bwd\b", bare), (p, bare)
+    assert (copies, loads) == (2, 2)
+    text = code(os.path.join(CSRC, "dense_gemv.cu"))
+    for name in ("load_stream", "load_stream8"):
+        body = re.search(name + r"\(const \w+ \*p\) \{.*?\n\}", text, flags=re.S).group(0)
+        assert "ld.relaxed.gpu.global" in body
