@@ -18,7 +18,8 @@
  * waste_moe_last_error().  Matrices are row-major without padding unless a row stride is an
  * argument, and no size is past 2^30.  Pointers are 16-byte aligned, workspaces 256-byte aligned.  A workspace holds
  * nothing between calls; two calls that may run at the same time (two streams, two captured
- * graphs) need one each.  Inputs and outputs do not overlap, unless a call says so.  The same
+ * graphs) need one each.  What a call writes (its workspace too) overlaps nothing else of the call, unless
+ * the call says so: WASTE_EINVAL where it does.  The same
  * inputs give the same bits: no sum depends on the order in which blocks run.
  */
 #ifndef WASTE_DENSE_H
@@ -63,6 +64,7 @@ int waste_ffn_workspace(const waste_ffn_config *cfg, int32_t T, int32_t backward
 /* y into d_out [T][d] of type out_dtype (cfg->dtype or WASTE_ACT_F32).
  *   mode 0: out = y;  mode 1: out += y (the sum is rounded once to out_dtype)
  *   d_g, d_u  [T][f] of cfg->dtype: receive g and u for waste_ffn_backward, or both NULL
+ * d_out may overlap d_x (x is read before anything is written there).
  * T >= 0; T == 0 does nothing. */
 int waste_ffn_forward(const waste_ffn_config *cfg, const void *d_x, int32_t T, const void *d_w_gate,
                       const void *d_w_up, const void *d_w_down, void *d_out, int32_t out_dtype, int32_t mode,
@@ -116,7 +118,7 @@ int waste_mx4_matmul(int32_t M, int32_t N, int32_t K, const uint8_t *d_a_codes, 
 /* The gated feed-forward block with MXFP4 weights: x is quantised as by waste_mx4_quantize, g
  * and u are fp32 sums, a = silu(g) * u in fp32 is quantised by the same rules, y = a Wd^T.
  * d % 32 == 0, f % 32 == 0; x [T][d] of type x_dtype (WASTE_ACT_F32, _BF16 or _F16); out [T][d]
- * and mode as in waste_mx4_matmul. */
+ * and mode as in waste_mx4_matmul; d_out may overlap d_x. */
 typedef struct {
     uint32_t abi_version; /* must equal WASTE_MOE_ABI_VERSION */
     int32_t d;

@@ -42,6 +42,30 @@ int check_ptrs(const void *const *p, const char *const *name, int n) {
     return WASTE_OK;
 }
 
+// Memory of a call: rows of row_bytes, pitch bytes apart.
+struct Span {
+    const void *p;
+    size_t row_bytes;
+    const char *name;
+    size_t rows = 1, pitch = 0;
+};
+// Whether a (one row) and b share a byte.
+bool meet(const Span &a, const Span &b) {
+    if (!a.p || !b.p || !a.row_bytes || !b.row_bytes || !b.rows) return false;
+    const uintptr_t a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p;
+    // the first row of b that ends behind a's start
+    const size_t past = a0 < b0 + b.row_bytes ? 0 : a0 - b0 - b.row_bytes;
+    const size_t i = a0 < b0 + b.row_bytes ? 0 : b.pitch ? past / b.pitch + 1 : b.rows;
+    return i < b.rows && b0 + i * b.pitch < a0 + a.row_bytes;
+}
+// Every one of the first n spans, which a call writes, lies apart from all others.
+int check_apart(const Span *s, int n, int all) {
+    for (int i = 0; i < n; ++i)
+        for (int j = i + 1; j < all; ++j)
+            if (meet(s[i], s[j])) return fail(WASTE_EINVAL, "%s overlaps %s", s[i].name, s[j].name);
+    return WASTE_OK;
+}
+
 int check_workspace(const void *ws, size_t have, size_t need) {
     if (need == 0) return WASTE_OK;
     if (!ws || !aligned(ws, 256)) return fail(WASTE_EINVAL, "workspace is NULL or not 256-byte aligned");
@@ -169,8 +193,15 @@ int waste_ffn_forward(const waste_ffn_config *cfg, const void *d_x, int32_t T, c
     const void *p[] = {d_x, d_w_gate, d_w_up, d_w_down, d_out, d_g, d_u};
     const char *n[] = {"x", "w_gate", "w_up", "w_down", "out", "g", "u"};
     rc = check_ptrs(p, n, d_g ? 7 : 5);
-    if (!rc) rc = check_workspace(d_workspace, workspace_bytes, ffn_bytes(cfg, T, false));
+    const size_t need = ffn_bytes(cfg, T, false), w = (size_t)cfg->d * cfg->f * 2, tf = (size_t)T * cfg->f * 2;
+    if (!rc) rc = check_workspace(d_workspace, workspace_bytes, need);
     if (rc) return rc;
+    // x is read by the first launch alone, out written by the last: the two may overlap
+    const Span x{d_x, (size_t)T * cfg->d * 2, "x"}, out{d_out, (size_t)T * cfg->d * type_size(out_dtype), "out"};
+    const Span ws{d_workspace, need, "workspace"}, g{d_g, tf, "g"}, u{d_u, tf, "u"};
+    const Span wg{d_w_gate, w, "w_gate"}, wu{d_w_up, w, "w_up"}, wd{d_w_down, w, "w_down"};
+    const Span kept[] = {ws, g, u, out, x, wg, wu, wd}, last[] = {out, wg, wu, wd};
+    if ((rc = check_apart(kept, 3, 8)) || (rc = check_apart(last, 1, 4))) return rc;
     FfnFwd P{cfg->d, cfg->f, T, cfg->dtype, out_dtype, mode, d_x, d_w_gate, d_w_up, d_w_down, d_out, d_g, d_u,
              d_workspace, reinterpret_cast<float *>(static_cast<char *>(d_workspace) + ffn_part(cfg, T))};
     return done(launch_ffn_forward(P, reinterpret_cast<cudaStream_t>(stream)), "gated feed-forward");
@@ -208,9 +239,15 @@ int waste_ffn_backward(const waste_ffn_config *cfg, const void *d_dy, int32_t T,
     const void *p[] = {d_dy, d_x, d_g, d_u, d_w_gate, d_w_up, d_w_down, d_dx};
     const char *n[] = {"dy", "x", "g", "u", "w_gate", "w_up", "w_down", "dx"};
     rc = check_ptrs(p, n, d_dx ? 8 : 7);
-    const size_t part = ffn_part(cfg, T);
-    if (!rc) rc = check_workspace(d_workspace, workspace_bytes, ffn_bytes(cfg, T, true));
+    const size_t part = ffn_part(cfg, T), need = ffn_bytes(cfg, T, true), wn = (size_t)cfg->d * cfg->f;
+    if (!rc) rc = check_workspace(d_workspace, workspace_bytes, need);
     if (rc) return rc;
+    const size_t td = (size_t)T * cfg->d * 2, tf = (size_t)T * cfg->f * 2, gn = wn * type_size(grad_dtype);
+    const Span spans[] = {{d_workspace, need, "workspace"}, {d_dx, td, "dx"}, {d_dw_gate, gn, "dw_gate"},
+                          {d_dw_up, gn, "dw_up"}, {d_dw_down, gn, "dw_down"}, {d_dy, td, "dy"}, {d_x, td, "x"},
+                          {d_g, tf, "g"}, {d_u, tf, "u"}, {d_w_gate, wn * 2, "w_gate"}, {d_w_up, wn * 2, "w_up"},
+                          {d_w_down, wn * 2, "w_down"}};
+    if ((rc = check_apart(spans, 5, 12))) return rc;
     char *w = static_cast<char *>(d_workspace);
     FfnBwd P{cfg->d, cfg->f,  T,      cfg->dtype, grad_dtype, accumulate, d_dy, d_x,      d_g,         d_u, d_w_gate,
              d_w_up, d_w_down, d_dx, d_dw_gate,  d_dw_up,    d_dw_down,  w,    w + part, w + 2 * part,
@@ -236,6 +273,10 @@ int waste_mx4_quantize(const void *d_x, int32_t dtype, int32_t rows, int32_t col
     const char *n[] = {"codes", "scales"};
     if (!rc) rc = check_ptrs(p, n, 2);
     if (rc) return rc;
+    const size_t size = type_size(dtype);
+    const Span spans[] = {{d_codes, mx_code_bytes(rows, cols), "codes"}, {d_scales, mx_scale_bytes(rows, cols), "scales"},
+                          {d_x, cols * size, "x", (size_t)rows, ld * size}};
+    if ((rc = check_apart(spans, 2, 3))) return rc;
     return done(launch_mx4_quantize(d_x, dtype, rows, cols, ld, d_codes, d_scales,
                                     reinterpret_cast<cudaStream_t>(stream)),
                 "4-bit quantisation");
@@ -251,6 +292,10 @@ int waste_mx4_dequantize(const uint8_t *d_codes, const uint8_t *d_scales, int32_
     const char *n[] = {"codes", "scales"};
     if (!rc) rc = check_ptrs(p, n, 2);
     if (rc) return rc;
+    const size_t size = type_size(dtype);
+    const Span out{d_out, cols * size, "out", (size_t)rows, ld * size};
+    if (meet({d_codes, mx_code_bytes(rows, cols), "codes"}, out)) return fail(WASTE_EINVAL, "out overlaps codes");
+    if (meet({d_scales, mx_scale_bytes(rows, cols), "scales"}, out)) return fail(WASTE_EINVAL, "out overlaps scales");
     return done(launch_mx4_dequantize(Mx4Mat{d_codes, d_scales, rows, cols}, d_out, dtype, ld,
                                       reinterpret_cast<cudaStream_t>(stream)),
                 "4-bit dequantisation");
@@ -270,6 +315,12 @@ int waste_mx4_matmul(int32_t M, int32_t N, int32_t K, const uint8_t *d_a_codes, 
     const char *n[] = {"a_codes", "a_scales", "b_codes", "b_scales", "out"};
     rc = check_ptrs(p, n, 5);
     if (rc) return rc;
+    const Span spans[] = {{d_out, (size_t)M * N * type_size(out_dtype), "out"},
+                          {d_a_codes, mx_code_bytes(M, K), "a_codes"},
+                          {d_a_scales, mx_scale_bytes(M, K), "a_scales"},
+                          {d_b_codes, mx_code_bytes(N, K), "b_codes"},
+                          {d_b_scales, mx_scale_bytes(N, K), "b_scales"}};
+    if ((rc = check_apart(spans, 1, 5))) return rc;
     return done(launch_mx4_matmul(Mx4Mat{d_a_codes, d_a_scales, M, K}, Mx4Mat{d_b_codes, d_b_scales, N, K}, d_out,
                                   out_dtype, mode, false, reinterpret_cast<cudaStream_t>(stream)),
                 "4-bit product");
@@ -309,6 +360,18 @@ int waste_mx4_ffn_forward(const waste_mx4_ffn_config *cfg, const void *d_x, int3
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     uint8_t *w = static_cast<uint8_t *>(d_workspace);
     const int d = cfg->d, f = cfg->f;
+    // x is read by the first launch alone, out written by the last: the two may overlap
+    const size_t wide = mx_code_bytes(f, d), tall = mx_code_bytes(d, f), ws = mx_scale_bytes(f, d), ds = mx_scale_bytes(d, f);
+    const Span spans[] = {{d_workspace, W.total, "workspace"},
+                          {d_out, (size_t)T * d * type_size(out_dtype), "out"},
+                          {cfg->d_gate_codes, wide, "gate_codes"},
+                          {cfg->d_gate_scales, ws, "gate_scales"},
+                          {cfg->d_up_codes, wide, "up_codes"},
+                          {cfg->d_up_scales, ws, "up_scales"},
+                          {cfg->d_down_codes, tall, "down_codes"},
+                          {cfg->d_down_scales, ds, "down_scales"}};
+    if ((rc = check_apart(spans, 2, 8))) return rc;
+    if (meet(spans[0], {d_x, (size_t)T * d * type_size(x_dtype), "x"})) return fail(WASTE_EINVAL, "workspace overlaps x");
     const Mx4Mat gate{cfg->d_gate_codes, cfg->d_gate_scales, f, d}, up{cfg->d_up_codes, cfg->d_up_scales, f, d},
         down{cfg->d_down_codes, cfg->d_down_scales, d, f};
     if (T <= kMxGemvTokens && mx_gemv_smem(d, T) <= kMxGemvSmem && mx_gemv_smem(f, T) <= kMxGemvSmem)

@@ -99,7 +99,8 @@ class DenseExpert:
 
     def forward(self, x, out=None, mode: int = 0, save_g=None, save_u=None, stream=None):
         """out [T, d] (fp32 or the weights' type; made if None) = (mode 0) or += (mode 1) the
-        block's output for x [T, d].  save_g, save_u [T, f] receive what backward needs."""
+        block's output for x [T, d].  save_g, save_u [T, f] receive what backward needs.  out may be
+        x; nothing else that is written may overlap anything of the call."""
         index = self.index
         if B.device_now() != index:
             with torch.cuda.device(index):
@@ -121,7 +122,8 @@ class DenseExpert:
                  stream=None):
         """Gradients for dy [T, d], given forward's x, g and u: into dx [T, d] (None: not computed)
         and the three weights' gradients (all or none; fp32 or the weights' type), added to
-        what is there with accumulate."""
+        what is there with accumulate.  No output may overlap anything else of the call (dx
+        over dy, say): refused."""
         index = self.index
         if B.device_now() != index:
             with torch.cuda.device(index):

@@ -119,7 +119,7 @@ class Mx4Expert:
 
     def forward(self, x, out=None, mode: int = 0, stream=None):
         """out [T, d] (fp32, bf16 or fp16; made as x if None) = (mode 0) or += (mode 1) the block's
-        output for x [T, d]."""
+        output for x [T, d].  out may be x."""
         index = self.index
         if B.device_now() != index:
             with torch.cuda.device(index):

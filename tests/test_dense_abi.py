@@ -186,3 +186,84 @@ def test_reference_codes_by_hand():
 def test_debug_wait_refusals():
     for a in ((-1, 0), ((1 << 18) + 1, 0), (1, 2), (1, -1)):
         refused(B.waste_dense_debug_wait, *a, stream=0)
+
+
+# ---------------------------------------------------------------- memory that a call writes and something else of it
+
+A = 1 << 40  # far from anything; never read
+
+
+def overlap(f, *a):
+    with pytest.raises(B.WasteError) as ei:
+        f(*a, stream=0)
+    assert ei.value.status == -1 and "overlaps" in ei.value.message, ei.value.message
+
+
+def test_backward_overlaps():
+    """dx over dy, over x, a gradient over its weight or another gradient, by their first and last 16 bytes."""
+    T, d, f = 6, 64, 32
+    size = dict(dy=T * d * 2, x=T * d * 2, g=T * f * 2, u=T * f * 2, wg=d * f * 2, wu=d * f * 2, wd=d * f * 2, dx=T * d * 2,
+                dwg=d * f * 4, dwu=d * f * 4, dwd=d * f * 4)
+    need = B.waste_ffn_workspace(cfg(d, f), T, 1)
+    names = list(size)
+    place = {n: A + (i << 20) for i, n in enumerate(names)}
+
+    def call(p, ws):
+        B.waste_ffn_backward(cfg(d, f), p["dy"], T, *(p[k] for k in names[1:]), B.ACT_F32, 0, Bytes(need, ws), stream=0)
+
+    for out in ("dx", "dwg", "dwu", "dwd"):
+        for other in names:
+            if other == out:
+                continue
+            for at in (place[other], place[other] + size[other] - 16, place[other] - size[out] + 16):
+                with pytest.raises(B.WasteError) as ei:
+                    call({**place, out: at}, A - (1 << 30))
+                assert ei.value.status == -1 and "overlaps" in ei.value.message
+    for other in names:
+        with pytest.raises(B.WasteError) as ei:
+            call(place, (place[other] + size[other] - 1) // 256 * 256)
+        assert "workspace overlaps" in ei.value.message
+
+
+def test_forward_overlaps():
+    T, d, f = 5, 64, 32
+    c, need = cfg(d, f), B.waste_ffn_workspace(cfg(d, f), 5)
+    w = [A + (i << 20) for i in range(8)]  # x wg wu wd out g u ws
+
+    def call(**k):
+        x, wg, wu, wd, out, g, u, ws = (k.get(n, v) for n, v in zip(("x", "wg", "wu", "wd", "out", "g", "u", "ws"), w))
+        overlap(B.waste_ffn_forward, c, x, T, wg, wu, wd, out, B.ACT_F32, 0, g, u, Bytes(need, ws))
+
+    for n in range(1, 4):
+        call(out=w[n] + d * f * 2 - 16)
+        call(g=w[n])
+        call(ws=w[n])
+    call(g=w[0])
+    call(u=w[0] + 16)
+    call(g=w[4] + T * d * 4 - 16)
+    call(u=w[5] + 16)
+    call(ws=w[0])
+    call(ws=w[4])
+
+
+def test_mx4_overlaps():
+    M, N, K = 3, 5, 64
+    ns = 512
+    p = [A + (i << 20) for i in range(5)]
+    for i, n in ((0, M * K // 2), (1, ns), (2, N * K // 2), (3, ns)):
+        for at in (p[i], p[i] + (n - 1) // 16 * 16, p[i] - M * N * 4 // 16 * 16):
+            overlap(B.waste_mx4_matmul, M, N, K, *p[:4], at, B.ACT_F32, 0)
+    # strided rows: the gaps between them are the caller's
+    rows, cols, ld = 4, 32, 96
+    for at in (p[0], p[0] + 16, p[0] + 3 * ld * 4, p[0] + 3 * ld * 4 + 112):
+        overlap(B.waste_mx4_quantize, p[0], B.ACT_F32, rows, cols, ld, at, p[1])
+        overlap(B.waste_mx4_dequantize, at, p[1], rows, cols, p[0], B.ACT_F32, ld)
+    overlap(B.waste_mx4_quantize, p[0], B.ACT_F32, rows, cols, ld, p[1], p[1] + 16)
+    overlap(B.waste_mx4_dequantize, p[2], p[0] + 2 * ld * 4, rows, cols, p[0], B.ACT_F32, ld)
+    m = B.waste_mx4_ffn_config(B.ABI_VERSION, 64, 32, *(A + (i << 20) for i in range(6)))
+    need = B.waste_mx4_ffn_workspace(m, 2)
+    for i in range(6):
+        overlap(B.waste_mx4_ffn_forward, m, A - (1 << 20), 0, 2, A + (i << 20), 0, 0, Bytes(need, A - (1 << 24)))
+        overlap(B.waste_mx4_ffn_forward, m, A - (1 << 20), 0, 2, A - (2 << 20), 0, 0, Bytes(need, A + (i << 20)))
+    overlap(B.waste_mx4_ffn_forward, m, A - (1 << 20), 0, 2, A - (2 << 20), 0, 0, Bytes(need, A - (1 << 20)))
+    overlap(B.waste_mx4_ffn_forward, m, A - (1 << 20), 0, 2, A - (2 << 20), 0, 0, Bytes(need, A - (2 << 20)))

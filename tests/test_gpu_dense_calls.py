@@ -1,0 +1,99 @@
+"""How the dense operators may be called: on memory that overlaps."""
+import pytest
+import torch
+
+from rvq_compressed_expert_gb300 import binding as B
+from rvq_compressed_expert_gb300.dense import DenseExpert
+from rvq_compressed_expert_gb300.mx4 import Mx4Expert, Mx4Matrix
+
+pytestmark = pytest.mark.gpu
+BF, HF, FP = torch.bfloat16, torch.float16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from rvq_compressed_expert_gb300 import _build
+    _build.build()
+    B.load()
+
+
+def gen(seed):
+    return torch.Generator("cuda").manual_seed(seed)
+
+
+def randn(g, *shape, scale=1.0, t=FP):
+    return (torch.randn(*shape, generator=g, device="cuda") * scale).to(t)
+
+
+def weights(g, d, f, t):
+    return randn(g, f, d, scale=d ** -0.5, t=t), randn(g, f, d, scale=d ** -0.5, t=t), randn(g, d, f, scale=f ** -0.5, t=t)
+
+
+# ---------------------------------------------------------------- overlapping memory
+
+@pytest.mark.parametrize("T,d,f", [(1, 2048, 264), (2, 2048, 264), (7, 1032, 136), (32, 4104, 520), (64, 1032, 264), (131, 2056, 520),
+                                   (300, 520, 264), (1000, 1032, 392)])
+def test_forward_in_place(T, d, f):
+    """out = x, and x += block(x): the bits of a call with memory of its own."""
+    g = gen(T + d)
+    e = DenseExpert(*weights(g, d, f, BF), max_tokens=T)
+    x = randn(g, T, d, t=BF)
+    want = e.forward(x)
+    added = e.forward(x, x.clone(), mode=1)
+    for mode, ref in ((0, want), (1, added)):
+        y = x.clone()
+        e.forward(y, y, mode=mode)
+        assert torch.equal(y, ref)
+    d, f = d // 32 * 32, f // 32 * 32
+    q = Mx4Expert.from_dense(*weights(g, d, f, BF), max_tokens=T)
+    x = randn(g, T, d)
+    want, added = q.forward(x), q.forward(x, x.clone(), mode=1)
+    for mode, ref in ((0, want), (1, added)):
+        y = x.clone()
+        q.forward(y, y, mode=mode)
+        assert torch.equal(y, ref)
+
+
+def test_overlaps_are_refused():
+    g = gen(1)
+    T, d, f = 20, 64, 32
+    W = weights(g, d, f, BF)
+    e = DenseExpert(*W, max_tokens=T)
+    x, dy, sg, su = (randn(g, T, n, t=BF) for n in (d, d, f, f))
+    dw = [torch.empty_like(w) for w in W]
+    keep = [v.clone() for v in (x, dy, sg, su, *W)]
+    both = torch.empty(2 * f, d, dtype=BF, device="cuda")
+    for call in (lambda: e.backward(dy, x, sg, su, dy, *dw), lambda: e.backward(dy, x, sg, su, x, *dw),
+                 lambda: e.backward(dy, x, sg, su, None, W[0], *dw[1:]),
+                 lambda: e.backward(dy, x, sg, su, None, both[:f], both[8:f + 8], dw[2]),
+                 lambda: e.forward(x, save_g=sg, save_u=sg), lambda: e.forward(x, W[0].view(-1)[:T * d].view(T, d))):
+        with pytest.raises(B.WasteError) as ei:
+            call()
+        assert ei.value.status == -1
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(keep, (x, dy, sg, su, *W)))
+    # inputs may be one tensor, gradients neighbours in one buffer
+    dx = torch.empty_like(x)
+    e.backward(dy, dy, sg, sg, dx, both[:f], both[f:], dw[2])
+    dw2 = [torch.empty_like(w) for w in W]
+    e.backward(dy, dy.clone(), sg, sg.clone(), None, *dw2)
+    assert torch.equal(both[:f], dw2[0]) and torch.equal(both[f:], dw2[1]) and torch.equal(dw[2], dw2[2])
+
+
+def test_codes_between_strided_rows():
+    """Codes and scales in the gaps between x's rows (and then out's) overlap nothing."""
+    rows, cols, ld = 5, 96, 512
+    g = gen(2)
+    buf = torch.zeros(rows + 1, ld, device="cuda")
+    x = buf[:rows, :cols]
+    x.copy_(randn(g, rows, cols))
+    want = Mx4Matrix.from_dense(x.clone())
+    codes, scales = buf[0, cols:cols + rows * cols // 8], buf[1, cols:cols + want.scales.numel() // 4]
+    values = x.clone()
+    B.waste_mx4_quantize(x, B.ACT_F32, rows, cols, ld, codes, scales)
+    assert torch.equal(codes.view(torch.uint8), want.codes.view(-1)) and torch.equal(scales.view(torch.uint8), want.scales)
+    assert torch.equal(x, values)
+    B.waste_mx4_dequantize(codes, scales, rows, cols, x, B.ACT_F32, ld)
+    assert torch.equal(x, want.dequantize())
