@@ -23,46 +23,44 @@ EncodeFn encoder() {
     }();
     return fn;
 }
+// A two-dimensional map.  In a host thread that has not used CUDA yet no context is current, and the driver
+// refuses (the runtime would make the device's own current by itself): it is made current, once a thread.
+cudaError_t encode(CUtensorMap *m, CUtensorMapDataType type, const void *p, const cuuint64_t (&dims)[2], cuuint64_t stride,
+                   const cuuint32_t (&box)[2], CUtensorMapSwizzle swizzle, CUtensorMapL2promotion l2) {
+    const EncodeFn fn = encoder();
+    if (!fn) return cudaErrorNotSupported;
+    const cuuint32_t one[2] = {1, 1};
+    const auto call = [&] {
+        return fn(m, type, 2, const_cast<void *>(p), dims, &stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, l2,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    CUresult r = call();
+    if (r != CUDA_SUCCESS) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e == cudaSuccess) e = cudaSetDevice(dev);
+        if (e != cudaSuccess) return e;
+        r = call();
+    }
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
 } // namespace
 
 cudaError_t make_map(CUtensorMap *m, const void *p, int unit, int rows, size_t row_bytes, int box_rows) {
-    const EncodeFn fn = encoder();
-    if (!fn) return cudaErrorNotSupported;
-    const cuuint64_t dims[2] = {row_bytes / unit, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {row_bytes};
-    const cuuint32_t box[2] = {(cuuint32_t)(kRowBytes / unit), (cuuint32_t)box_rows};
-    const cuuint32_t one[2] = {1, 1};
-    const CUresult r = fn(m, unit == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
-                          const_cast<void *>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+    return encode(m, unit == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, p,
+                  {row_bytes / unit, (cuuint64_t)rows}, row_bytes, {(cuuint32_t)(kRowBytes / unit), (cuuint32_t)box_rows},
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 cudaError_t store_map(CUtensorMap *m, void *p, int bytes, int rows, int cols) {
-    const EncodeFn fn = encoder();
-    if (!fn) return cudaErrorNotSupported;
-    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)cols * bytes};
-    const cuuint32_t box[2] = {(cuuint32_t)(64 / bytes), 32};
-    const cuuint32_t one[2] = {1, 1};
-    const CUresult r = fn(m, bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, p, dims, strides,
-                          box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
-                          CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+    return encode(m, bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT32, p,
+                  {(cuuint64_t)cols, (cuuint64_t)rows}, (cuuint64_t)cols * bytes, {(cuuint32_t)(64 / bytes), 32},
+                  CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
 }
 
 cudaError_t make_scale_map(CUtensorMap *m, const void *p, size_t tiles) {
-    const EncodeFn fn = encoder();
-    if (!fn) return cudaErrorNotSupported;
-    const cuuint64_t dims[2] = {kMxTileBytes / 4, (cuuint64_t)tiles};
-    const cuuint64_t strides[1] = {kMxTileBytes};
-    const cuuint32_t box[2] = {kMxTileBytes / 4, 2};
-    const cuuint32_t one[2] = {1, 1};
-    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void *>(p), dims, strides, box, one,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, p, {kMxTileBytes / 4, (cuuint64_t)tiles}, kMxTileBytes,
+                  {kMxTileBytes / 4, 2}, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 namespace {

@@ -1,10 +1,12 @@
-"""How the dense operators may be called: on memory that overlaps."""
+"""How the dense operators may be called: on memory that overlaps, from several host threads."""
+import threading
+
 import pytest
 import torch
 
 from rvq_compressed_expert_gb300 import binding as B
 from rvq_compressed_expert_gb300.dense import DenseExpert
-from rvq_compressed_expert_gb300.mx4 import Mx4Expert, Mx4Matrix
+from rvq_compressed_expert_gb300.mx4 import Mx4Expert, Mx4Matrix, matmul
 
 pytestmark = pytest.mark.gpu
 BF, HF, FP = torch.bfloat16, torch.float16, torch.float32
@@ -97,3 +99,53 @@ def test_codes_between_strided_rows():
     assert torch.equal(x, values)
     B.waste_mx4_dequantize(codes, scales, rows, cols, x, B.ACT_F32, ld)
     assert torch.equal(x, want.dequantize())
+
+
+# ---------------------------------------------------------------- several host threads
+
+def in_threads(*work):
+    """Every function in a thread of its own, begun together; the first error is raised here."""
+    gate, errors = threading.Barrier(len(work)), []
+
+    def run(f):
+        try:
+            gate.wait()
+            f()
+        except BaseException as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(f,)) for f in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    if errors:
+        raise errors[0]
+
+
+@pytest.mark.parametrize("T", [1, 2, 20, 150, 600])
+def test_first_calls_of_a_thread(T):
+    """A host thread whose first use of CUDA is a call of these operators (no context is current in it yet)."""
+    d, f = 320, 160
+    g = gen(T)
+    W = weights(g, d, f, BF)
+    e, q = DenseExpert(*W, max_tokens=T), Mx4Expert.from_dense(*W, max_tokens=T)
+    e.reserve_backward()
+    x, dy, sg, su = (randn(g, T, n, t=BF) for n in (d, d, f, f))
+    a, s = Mx4Matrix.from_dense(x), torch.cuda.Stream()
+    y, dx, y4, back = (torch.empty_like(x) for _ in range(4))
+    dw, c = [torch.empty_like(w) for w in W], torch.empty(T, f, device="cuda")
+    m = Mx4Matrix.empty(T, d)
+    calls = {"forward": (lambda: e.forward(x, y, stream=s), [y]), "backward": (lambda: e.backward(dy, x, sg, su, dx, *dw, stream=s), [dx, *dw]),
+             "quantize": (lambda: m.quantize(x, stream=s), [m.codes, m.scales]), "dequantize": (lambda: a.dequantize(back, stream=s), [back]),
+             "matmul": (lambda: matmul(a, q.gate, c, stream=s), [c]), "block": (lambda: q.forward(x, y4, stream=s), [y4])}
+    for name, (call, out) in calls.items():
+        call()
+        torch.cuda.synchronize()
+        want = [v.clone() for v in out]
+        for v in out:
+            v.zero_()
+        torch.cuda.synchronize()
+        in_threads(call)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want)), name
