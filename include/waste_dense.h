@@ -16,11 +16,11 @@
  * captured into a CUDA graph; arguments are checked on the host before anything is launched;
  * the return value is WASTE_OK or a negative waste_status whose message is
  * waste_moe_last_error().  Matrices are row-major without padding unless a row stride is an
- * argument, and no size is past 2^30.  Pointers are 16-byte aligned, workspaces 256-byte aligned.  A workspace holds
- * nothing between calls; two calls that may run at the same time (two streams, two captured
- * graphs) need one each.  What a call writes (its workspace too) overlaps nothing else of the call, unless
- * the call says so: WASTE_EINVAL where it does.  The same
- * inputs give the same bits: no sum depends on the order in which blocks run.
+ * argument, and no size is past 2^30.  Pointers are 16-byte aligned, workspaces 256-byte aligned.
+ * A workspace holds nothing between calls; two calls that may run at the same time (two streams, two
+ * captured graphs), or are made at the same time by two host threads, need one each.  What a call
+ * writes (its workspace too) overlaps nothing else of the call, unless the call says so: WASTE_EINVAL
+ * where it does.  The same inputs give the same bits: no sum depends on the order in which blocks run.
  */
 #ifndef WASTE_DENSE_H
 #define WASTE_DENSE_H

@@ -7,6 +7,8 @@ is in the library's kernels.
 """
 from __future__ import annotations
 
+import threading
+
 import torch
 
 from . import binding as B
@@ -51,9 +53,10 @@ class Workspace:
 class DenseExpert:
     """w_gate, w_up [f, d] and w_down [d, f], bf16 or fp16, contiguous on one GPU (borrowed, not
     copied).  max_tokens bounds T and sizes the workspace, which belongs to this object: calls
-    of one object must not run at the same time on two streams, two captured graphs that may
+    of one object must not run at the same time on two streams (from several host threads on one
+    stream they may: a lock keeps a call's launches together), two captured graphs that may
     replay at the same time need an object each, and an object outlives the graphs that hold its
-    calls.  stream: a torch.cuda.Stream, an integer handle (then the object must outlive the
+    calls.  A device wait that gave up shows in ``binding.waste_dense_status``.  stream: a torch.cuda.Stream, an integer handle (then the object must outlive the
     call) or None for the current stream; ordering the tensors' use between streams is the
     caller's."""
 
@@ -71,6 +74,7 @@ class DenseExpert:
         self._own, self._out = (t,), (t, torch.float32)  # types of inputs, and of outputs
         self.cfg = B.waste_ffn_config(B.ABI_VERSION, d, f, ACT[t])
         self._ws = {}
+        self._one = threading.Lock()
         self._workspace(0)
 
     def _workspace(self, backward: int) -> Workspace:
@@ -86,7 +90,8 @@ class DenseExpert:
 
     def reserve_backward(self):
         """Makes the backward's workspace (three [max_tokens, f] buffers, and partial sums of few tokens) now."""
-        self._workspace(1)
+        with self._one:
+            self._workspace(1)
 
     def _tokens(self, x, name):
         if not isinstance(x, torch.Tensor) or x.dim() != 2:
@@ -114,8 +119,9 @@ class DenseExpert:
             if t is not None:
                 check(t, n, (T, self.f), self._own, self.device)
         h = B.stream_on(index, stream)
-        B.waste_ffn_forward(self.cfg, x, T, self.w_gate, self.w_up, self.w_down, out, ACT[out.dtype], mode, save_g,
-                            save_u, self._ws[0].lend(stream, h), h)
+        with self._one:
+            B.waste_ffn_forward(self.cfg, x, T, self.w_gate, self.w_up, self.w_down, out, ACT[out.dtype], mode, save_g,
+                                save_u, self._ws[0].lend(stream, h), h)
         return out
 
     def backward(self, dy, x, g, u, dx=None, dw_gate=None, dw_up=None, dw_down=None, accumulate: bool = False,
@@ -140,5 +146,6 @@ class DenseExpert:
             if t is not None:
                 check(t, n, w.shape, (gt,) if gt in self._out else self._out, self.device)
         h = B.stream_on(index, stream)
-        B.waste_ffn_backward(self.cfg, dy, T, x, g, u, self.w_gate, self.w_up, self.w_down, dx, dw_gate, dw_up, dw_down,
-                             ACT[gt], int(accumulate), self._workspace(1).lend(stream, h), h)
+        with self._one:
+            B.waste_ffn_backward(self.cfg, dy, T, x, g, u, self.w_gate, self.w_up, self.w_down, dx, dw_gate, dw_up,
+                                 dw_down, ACT[gt], int(accumulate), self._workspace(1).lend(stream, h), h)

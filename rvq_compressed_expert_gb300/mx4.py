@@ -7,6 +7,8 @@ without decoding.  All computation is in the library's kernels.
 """
 from __future__ import annotations
 
+import threading
+
 import torch
 
 from . import binding as B
@@ -99,7 +101,7 @@ class Mx4Expert:
     max_tokens bounds T and sizes the workspace, which belongs to this object: calls of one
     object must not run at the same time on two streams, two captured graphs that may replay at the
     same time need an object each, and an object outlives the graphs that hold its calls.  stream
-    as for ``dense.DenseExpert``."""
+    and host threads as for ``dense.DenseExpert``."""
 
     def __init__(self, gate: Mx4Matrix, up: Mx4Matrix, down: Mx4Matrix, max_tokens: int):
         f, d = gate.rows, gate.cols
@@ -111,6 +113,7 @@ class Mx4Expert:
         self.d, self.f, self.device, self.index, self.max_tokens = d, f, gate.device, gate.index, int(max_tokens)
         self.cfg = B.waste_mx4_ffn_config(B.ABI_VERSION, d, f, *(t.data_ptr() for m in (gate, up, down)
                                                                  for t in (m.codes, m.scales)))
+        self._one = threading.Lock()
         self._ws = Workspace(B.waste_mx4_ffn_workspace(self.cfg, self.max_tokens), self.device)
 
     @classmethod
@@ -134,5 +137,6 @@ class Mx4Expert:
             out = make((T, self.d), x.dtype, self.device, stream)
         check(out, "out", (T, self.d), _FLOATS, self.device)
         h = B.stream_on(index, stream)
-        B.waste_mx4_ffn_forward(self.cfg, x, ACT[x.dtype], T, out, ACT[out.dtype], mode, self._ws.lend(stream, h), h)
+        with self._one:
+            B.waste_mx4_ffn_forward(self.cfg, x, ACT[x.dtype], T, out, ACT[out.dtype], mode, self._ws.lend(stream, h), h)
         return out

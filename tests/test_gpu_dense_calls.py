@@ -149,3 +149,65 @@ def test_first_calls_of_a_thread(T):
         in_threads(call)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want)), name
+
+
+@pytest.mark.parametrize("T,d,f", [(3, 1032, 264), (40, 1032, 264), (150, 520, 392)])
+def test_one_expert_in_two_threads(T, d, f):
+    """Calls of one object from two host threads on one stream, the first backward (which makes its workspace)
+    among them: each thread gets the bits of its own inputs."""
+    g = gen(T)
+    W = weights(g, d, f, BF)
+    sets = [[randn(g, T, n, t=BF) for n in (d, d, f, f)] for _ in range(2)]
+    alone = DenseExpert(*W, max_tokens=T)
+    q = Mx4Expert.from_dense(*(w[:, : w.shape[1] // 32 * 32][: w.shape[0] // 32 * 32].contiguous() for w in W), max_tokens=T)
+    xq = [s[0][:, :q.d].contiguous() for s in sets]
+    want = []
+    for s, xs in zip(sets, xq):
+        out = [torch.empty(T, d, dtype=BF, device="cuda") for _ in range(2)] + [torch.empty_like(w) for w in W]
+        alone.forward(s[0], out[0])
+        alone.backward(*s, *out[1:])
+        want.append(out + [q.forward(xs)])
+    torch.cuda.synchronize()
+    for again in range(3):
+        e = DenseExpert(*W, max_tokens=T)
+        n = 150
+        got = [[[torch.empty_like(v) for v in w] for _ in range(n)] for w in want]
+        torch.cuda.synchronize()
+
+        def calls(i):
+            def run():
+                for out in got[i]:
+                    e.backward(*sets[i], *out[1:5])
+                    e.forward(sets[i][0], out[0])
+                    q.forward(xq[i], out[5])
+            return run
+
+        in_threads(calls(0), calls(1))
+        torch.cuda.synchronize()
+        for i in range(2):
+            wrong = sum(not torch.equal(a, b) for out in got[i] for a, b in zip(out, want[i]))
+            assert wrong == 0, (again, i, wrong)
+
+
+def test_two_experts_in_two_threads():
+    """Experts of their own on streams of their own, of sizes that need different shared memory of the same kernels."""
+    sizes = [(17, 2056, 1032), (170, 520, 136)]
+    work, checks = [], []
+    for T, d, f in sizes:
+        g = gen(T)
+        e = DenseExpert(*weights(g, d, f, HF), max_tokens=T)
+        x, s = randn(g, T, d, t=HF), torch.cuda.Stream()
+        want = e.forward(x).clone()
+        outs = [torch.empty_like(want) for _ in range(100)]
+        torch.cuda.synchronize()
+
+        def run(e=e, x=x, s=s, outs=outs):
+            for out in outs:
+                e.forward(x, out, stream=s)
+
+        work.append(run)
+        checks.append((want, outs))
+    in_threads(*work)
+    torch.cuda.synchronize()
+    for want, outs in checks:
+        assert all(torch.equal(want, o) for o in outs)
