@@ -1,12 +1,17 @@
-"""How the dense operators may be called: on memory that overlaps, from several host threads."""
+"""How the dense operators may be called: on memory that overlaps, from several host threads, in decode stacks
+of every kind."""
 import threading
 
 import pytest
 import torch
 
 from rvq_compressed_expert_gb300 import binding as B
+from rvq_compressed_expert_gb300 import synth
+from rvq_compressed_expert_gb300.bank import TieredStack
 from rvq_compressed_expert_gb300.dense import DenseExpert
+from rvq_compressed_expert_gb300.layer import MoELayer
 from rvq_compressed_expert_gb300.mx4 import Mx4Expert, Mx4Matrix, matmul
+from rvq_compressed_expert_gb300.stack import DecodeStack
 
 pytestmark = pytest.mark.gpu
 BF, HF, FP = torch.bfloat16, torch.float16, torch.float32
@@ -211,3 +216,88 @@ def test_two_experts_in_two_threads():
     torch.cuda.synchronize()
     for want, outs in checks:
         assert all(torch.equal(want, o) for o in outs)
+
+
+# ---------------------------------------------------------------- shared experts of decode stacks
+
+def workload(tokens):
+    return synth.Workload("shared-calls", 512, 256, 16, 4, tokens, "f32", "offsets", n_layers=4, lookahead=3)
+
+
+def shared_experts(tokens):
+    g = gen(60)
+    return [DenseExpert(*weights(g, 512, 256, BF), max_tokens=tokens), Mx4Expert.from_dense(*weights(g, 512, 160, BF), max_tokens=tokens),
+            None, DenseExpert(*weights(g, 512, 264, HF), max_tokens=tokens + 5)]
+
+
+def eager(stack, hidden, lookahead):
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    main.wait_stream(torch.cuda.current_stream())
+    outs = []
+    for h in hidden:
+        out = stack.run(h, lookahead, main, side)
+        with torch.cuda.stream(main):
+            outs.append(out.clone())
+    torch.cuda.synchronize()
+    return outs
+
+
+@pytest.mark.parametrize("lookahead", [0, 3])
+@pytest.mark.parametrize("tokens", [1, 3])
+def test_stack_of_shared_experts_captured(tokens, lookahead):
+    """A pass through layers with dense (bf16, fp16) and 4-bit shared experts, recorded into a graph and replayed
+    on other tokens, gives the bits of eager passes, and each layer's residual is the layer's parts one by one."""
+    w = workload(tokens)
+    layers = [MoELayer(w, 0, L, "cuda") for L in range(w.n_layers)]
+    try:
+        shared = shared_experts(tokens)
+        stack = DecodeStack(layers, tokens, shared=shared)
+        hidden = [synth.hidden(70 + i, tokens, w.d, "f32", "cuda") for i in range(3)]
+        want = eager(stack, hidden, lookahead)
+        h, x = hidden[0].clone(), torch.empty_like(hidden[0])
+        idx, gate, logits, _ = layers[0].alloc_outputs(tokens)
+        for L, e in enumerate(shared):
+            B.waste_moe_rmsnorm(h, x, tokens, w.d)
+            layers[L].route(x, tokens, idx, gate, logits)
+            layers[L].forward(x, tokens, idx, gate, h, 1)
+            if e is not None:
+                e.forward(x.to(e.dtype) if isinstance(e, DenseExpert) else x, h, mode=1)
+        torch.cuda.synchronize()
+        assert torch.equal(want[0], h)
+        h0, main, side = hidden[0].clone(), torch.cuda.Stream(), torch.cuda.Stream()
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr, stream=main):
+            out = stack.run(h0, lookahead, main, side)
+        for i in (2, 0, 1):
+            h0.copy_(hidden[i])
+            gr.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want[i])
+        del gr
+        B.waste_dense_status()
+    finally:
+        for m in layers:
+            m.close()
+
+
+@pytest.mark.parametrize("lookahead", [0, 3])
+def test_banked_stack_with_shared_experts(lookahead):
+    """Layers whose records come through an HBM cache that evicts, with shared experts: the resident stack's bits."""
+    w = workload(1)
+    hidden = [synth.hidden(80 + i, 1, w.d, "f32", "cuda") for i in range(4)]
+    layers = [MoELayer(w, 0, L, "cuda") for L in range(w.n_layers)]
+    try:
+        want = eager(DecodeStack(layers, 1, shared=shared_experts(1)), hidden, lookahead)
+        plain = eager(DecodeStack(layers, 1), hidden, lookahead)
+    finally:
+        for m in layers:
+            m.close()
+    ts = TieredStack(w, 0, w.n_layers, 6)
+    try:
+        got = eager(DecodeStack(ts.layers, 1, banked=True, shared=shared_experts(1)), hidden, lookahead)
+        for a, b, c in zip(got, want, plain):
+            assert torch.equal(a, b) and not torch.equal(a, c)
+        for m in ts.layers:
+            m.stats()
+    finally:
+        ts.close()
