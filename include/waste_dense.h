@@ -47,9 +47,10 @@ int waste_dense_debug_wait(int32_t polls, int32_t arrive, waste_stream_t stream)
 /* ---- gated feed-forward block ---------------------------------------------------------
  * d % 8 == 0, f % 8 == 0, both positive; dtype WASTE_ACT_BF16 or WASTE_ACT_F16: the type of x,
  * the weights, g, u, dy and dx.  Sums are held in fp32; a, dg and du are rounded once to dtype
- * on their way into the next product (calls of at most 32 tokens keep what that rounding leaves as
- * well, to about 2^-16 of the value in bf16 and 2^-22 in fp16; an infinite weight or dy may then give NaN
- * where one product would give an infinity). */
+ * on their way into the next product.  Calls of at most 32 tokens keep what that rounding leaves as
+ * well, rounded to dtype too: a value v is then off by at most 2^-16 |v| in bf16, and in fp16, whose
+ * rests become subnormal for |v| < 2^-3, by the larger of 2^-22 |v| and 2^-25; an infinite x, weight or dy
+ * may then give NaN where one product would give an infinity.  (A forward of one token keeps a in fp32.) */
 typedef struct {
     uint32_t abi_version; /* must equal WASTE_MOE_ABI_VERSION */
     int32_t d;            /* hidden size */

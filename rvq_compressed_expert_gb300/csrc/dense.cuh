@@ -94,7 +94,8 @@ cudaError_t mx4_timeout(uint32_t *out);
 
 #ifdef __CUDACC__
 // By the approximate exponential and quotient: relative errors of 2^-22 and of the argument's rounding,
-// |g| 2^-23, far below what the 16-bit or 4-bit rounding behind it leaves.  Below 2^-126 (g < -87.3) the
+// |g| 2^-23: far below what one rounding to 16 or 4 bits behind it leaves, and below the rounding of bf16's two
+// parts; in fp32 (one token) and beside fp16's two parts (2^-22) it is the larger error of a.  Below 2^-126 (g < -87.3) the
 // quotient is 0, by definition for divisors past 2^126, and so is what is multiplied with it.
 __device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
 

@@ -658,7 +658,8 @@ __device__ __forceinline__ void put_as(int dtype, void *out, size_t at, int n, i
     else
         put(static_cast<__half *>(out) + at, n, N, vec, add, v);
 }
-// What rounding v to the 16-bit type leaves, rounded to it; nothing where it leaves the type's range.
+// What rounding v to the 16-bit type leaves, rounded to it (in fp16 below 2^-14, so for |v| < 2^-3, to
+// multiples of 2^-24); nothing where it leaves the type's range.
 template <int W>
 __device__ __forceinline__ void put_rest(int dtype, void *out, size_t at, int n, int N, const float (&v)[W]) {
     float r[W];

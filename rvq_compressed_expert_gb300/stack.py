@@ -21,7 +21,8 @@ stream can still read x_L while x_{L+1} is written; layer L+1 routes only after
 its prefetch has finished (an event), which also keeps the next write of x_L's
 buffer behind the read.
 A layer may also have a dense expert that serves every token beside the routed ones
-(``shared``): its output for x_L joins the residual after the routed experts' combine.
+(``shared``): its output for x_L joins the residual after the routed experts' combine.  For an expert
+of 16-bit weights x_L is cast by a torch copy.
 """
 from __future__ import annotations
 

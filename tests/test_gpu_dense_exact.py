@@ -203,3 +203,37 @@ def test_mx4_expert_exact(T, d, f, tx):
         o16 = torch.full((T, d), float("nan"), dtype=BF, device="cuda")
         e.forward(x.to(tx), o16)
         same(o16, y, "bf16 y")
+
+
+@pytest.mark.parametrize("T", [2, 16, 17, 32])
+@pytest.mark.parametrize("t", [BF, HF])
+def test_what_two_parts_leave(T, t):
+    """The stated bound on a value kept in two parts, seen through a unit matrix: 2^-16 of it in bf16; in fp16 2^-22,
+    but 2^-25 in all where the rest is subnormal.  a = 40 u with u the sum of a value and a small multiple of another, over
+    20 binades; one fp32 rounding of a, none of y (one product a column)."""
+    d, f = 136, 64
+    g = gen(T)
+    x = torch.zeros(T, d, dtype=t, device="cuda")
+    x[:, 0] = 1
+    x[:, 8:] = (torch.randn(T, 128, generator=g, device="cuda") * torch.exp2(torch.randint(-20, 1, (T, 64), generator=g, device="cuda")
+                                                                            .float()).repeat(1, 2)).to(t)
+    wg, wu, wd = (torch.zeros(s, dtype=t, device="cuda") for s in ((f, d), (f, d), (d, f)))
+    wg[:, 0] = 40
+    i = torch.arange(f, device="cuda")
+    wu[i, 8 + i], wu[i, 72 + i], wd[i, i] = 1, 2.0 ** -9, 1
+    e = DenseExpert(wg, wu, wd, max_tokens=T)
+    y = torch.empty(T, d, device="cuda")
+    e.forward(x, y)
+    u = x[:, 8:72].double() + x[:, 72:].double() * 2.0 ** -9
+    a = (40 * u.float()).double()
+    off = (y[:, :f].double() - a).abs()
+    small = a.abs() < 2.0 ** -3
+    assert small.any() and (~small).any()
+    if t == BF:  # and its least subnormal is far below
+        assert (off <= 2.0 ** -16 * a.abs()).all()
+    else:
+        assert (off <= torch.clamp(2.0 ** -22 * a.abs(), min=2.0 ** -25)).all()
+        assert (off > 2.0 ** -22 * a.abs()).any()  # the relative part alone would not hold
+    assert (y[:, f:] == 0).all()
+    # one part alone is off by far more
+    assert ((a.to(t).double() - a).abs() > 8 * off.clamp(min=2.0 ** -30)).any()
