@@ -237,3 +237,22 @@ def test_what_two_parts_leave(T, t):
     assert (y[:, f:] == 0).all()
     # one part alone is off by far more
     assert ((a.to(t).double() - a).abs() > 8 * off.clamp(min=2.0 ** -30)).any()
+
+
+@pytest.mark.parametrize("M", [1, 2, 3, 40, 200, 700])
+@pytest.mark.parametrize("K", [64, 1056])
+def test_matmul_of_extreme_scales(M, K):
+    """Ones with every kind of power of two, 2^-127 and 2^127 among them, down to subnormal sums and up past fp32."""
+    def ones(rows, byte):
+        m = Mx4Matrix.from_dense(torch.ones(rows, K, device="cuda"))  # code 6 is 1 at 2^-2
+        real = m.scales == 125
+        m.codes.fill_(0x22)
+        m.scales[real] = byte
+        return m
+
+    for sa, sb in ((0, 127), (0, 240), (1, 250), (0, 254), (254, 0), (100, 20), (60, 60), (57, 57), (53, 53), (50, 58), (254, 254),
+                   (190, 190), (189, 189)):
+        out = torch.full((M, 200), float("nan"), device="cuda")
+        matmul(ones(M, sa), ones(200, sb), out)
+        want = torch.tensor(float(K), dtype=torch.float64) * 2.0 ** (sa + sb - 254)
+        assert (out == want.float().item()).all(), (sa, sb, out[0, 0].item(), want.item())
