@@ -1,3 +1,4 @@
+import gc
 import os
 import sys
 
@@ -10,6 +11,18 @@ if ROOT not in sys.path:
 
 def pytest_configure(config):
     config.addinivalue_line("markers", "gpu: needs a CUDA GPU (GB300, sm_103a)")
+
+
+def pytest_collection_finish(session):
+    gc.freeze()  # what is imported by now stays: collections between tests are short
+
+
+@pytest.fixture(autouse=True)
+def _garbage_ends_with_its_test():
+    """A test's cycles (a caught error and its frames, say) may hold CUDA graphs, and one destroyed by the collector while a
+    later test records another makes that recording fail."""
+    yield
+    gc.collect()
 
 
 @pytest.fixture(scope="session")
