@@ -74,15 +74,30 @@ class waste_bank_stats_t(ctypes.Structure):
         "demand_hits", "demand_misses", "prefetch_copies", "prefetch_present", "copied_bytes")]
 
 
+def _far(*sizes):
+    """Sizes that ctypes would cut to 32 bits without a word."""
+    raise WasteError(-1, f"sizes {sizes}: at most 2^30")
+
+
 class waste_ffn_config(ctypes.Structure):
     _fields_ = [("abi_version", ctypes.c_uint32), ("d", ctypes.c_int32), ("f", ctypes.c_int32),
                 ("dtype", ctypes.c_int32)]
+
+    def __init__(self, abi_version=ABI_VERSION, d=0, f=0, dtype=0):
+        if not -1 <= (d | f) >> 31 <= 0:
+            _far(d, f)
+        super().__init__(abi_version, d, f, dtype)
 
 
 class waste_mx4_ffn_config(ctypes.Structure):
     _fields_ = [("abi_version", ctypes.c_uint32), ("d", ctypes.c_int32), ("f", ctypes.c_int32)] + [
         (n, ctypes.c_void_p) for n in ("d_gate_codes", "d_gate_scales", "d_up_codes", "d_up_scales",
                                        "d_down_codes", "d_down_scales")]
+
+    def __init__(self, abi_version=ABI_VERSION, d=0, f=0, *pointers):
+        if not -1 <= (d | f) >> 31 <= 0:
+            _far(d, f)
+        super().__init__(abi_version, d, f, *pointers)
 
 
 class WasteError(RuntimeError):
@@ -366,6 +381,8 @@ def waste_dense_debug_wait(polls=0, arrive=0, stream=None):
 
 
 def waste_ffn_workspace(cfg, T, backward=0) -> int:
+    if not -1 <= T >> 31 <= 0:
+        _far(T)
     n = ctypes.c_size_t()
     _check(load().waste_ffn_workspace(ctypes.byref(cfg), T, backward, ctypes.byref(n)))
     return n.value
@@ -374,6 +391,8 @@ def waste_ffn_workspace(cfg, T, backward=0) -> int:
 def waste_ffn_forward(cfg, d_x, T, d_w_gate, d_w_up, d_w_down, d_out, out_dtype, mode, d_g, d_u, workspace,
                       stream=None):
     """workspace: a uint8 tensor (its size is passed on)."""
+    if not -1 <= T >> 31 <= 0:
+        _far(T)
     rc = (_lib or load()).waste_ffn_forward(
         ctypes.byref(cfg), _ptr(d_x), T, _ptr(d_w_gate), _ptr(d_w_up), _ptr(d_w_down), _ptr(d_out), out_dtype, mode,
         _ptr(d_g), _ptr(d_u), workspace.data_ptr(), workspace.numel(), _stream(stream))
@@ -382,6 +401,8 @@ def waste_ffn_forward(cfg, d_x, T, d_w_gate, d_w_up, d_w_down, d_out, out_dtype,
 
 def waste_ffn_backward(cfg, d_dy, T, d_x, d_g, d_u, d_w_gate, d_w_up, d_w_down, d_dx, d_dw_gate, d_dw_up, d_dw_down,
                        grad_dtype, accumulate, workspace, stream=None):
+    if not -1 <= T >> 31 <= 0:
+        _far(T)
     rc = (_lib or load()).waste_ffn_backward(
         ctypes.byref(cfg), _ptr(d_dy), T, _ptr(d_x), _ptr(d_g), _ptr(d_u), _ptr(d_w_gate), _ptr(d_w_up),
         _ptr(d_w_down), _ptr(d_dx), _ptr(d_dw_gate), _ptr(d_dw_up), _ptr(d_dw_down), grad_dtype, accumulate,
@@ -391,36 +412,48 @@ def waste_ffn_backward(cfg, d_dy, T, d_x, d_g, d_u, d_w_gate, d_w_up, d_w_down, 
 
 def waste_mx4_layout(rows, cols):
     """(bytes of codes, bytes of scales)."""
+    if not -1 <= (rows | cols) >> 31 <= 0:
+        _far(rows, cols)
     c, s = ctypes.c_size_t(), ctypes.c_size_t()
     _check(load().waste_mx4_layout(rows, cols, ctypes.byref(c), ctypes.byref(s)))
     return c.value, s.value
 
 
 def waste_mx4_quantize(d_x, dtype, rows, cols, ld, d_codes, d_scales, stream=None):
+    if not -1 <= (rows | cols) >> 31 <= 0:
+        _far(rows, cols)
     rc = (_lib or load()).waste_mx4_quantize(_ptr(d_x), dtype, rows, cols, ld, _ptr(d_codes), _ptr(d_scales),
                                              _stream(stream))
     return rc and _check(rc)
 
 
 def waste_mx4_dequantize(d_codes, d_scales, rows, cols, d_out, dtype, ld, stream=None):
+    if not -1 <= (rows | cols) >> 31 <= 0:
+        _far(rows, cols)
     rc = (_lib or load()).waste_mx4_dequantize(_ptr(d_codes), _ptr(d_scales), rows, cols, _ptr(d_out), dtype, ld,
                                                _stream(stream))
     return rc and _check(rc)
 
 
 def waste_mx4_matmul(M, N, K, d_a_codes, d_a_scales, d_b_codes, d_b_scales, d_out, out_dtype, mode=0, stream=None):
+    if not -1 <= (M | N | K) >> 31 <= 0:
+        _far(M, N, K)
     rc = (_lib or load()).waste_mx4_matmul(M, N, K, _ptr(d_a_codes), _ptr(d_a_scales), _ptr(d_b_codes),
                                            _ptr(d_b_scales), _ptr(d_out), out_dtype, mode, _stream(stream))
     return rc and _check(rc)
 
 
 def waste_mx4_ffn_workspace(cfg, T) -> int:
+    if not -1 <= T >> 31 <= 0:
+        _far(T)
     n = ctypes.c_size_t()
     _check(load().waste_mx4_ffn_workspace(ctypes.byref(cfg), T, ctypes.byref(n)))
     return n.value
 
 
 def waste_mx4_ffn_forward(cfg, d_x, x_dtype, T, d_out, out_dtype, mode, workspace, stream=None):
+    if not -1 <= T >> 31 <= 0:
+        _far(T)
     rc = (_lib or load()).waste_mx4_ffn_forward(ctypes.byref(cfg), _ptr(d_x), x_dtype, T, _ptr(d_out), out_dtype, mode,
                                                 workspace.data_ptr(), workspace.numel(), _stream(stream))
     return rc and _check(rc)

@@ -267,3 +267,24 @@ def test_mx4_overlaps():
         overlap(B.waste_mx4_ffn_forward, m, A - (1 << 20), 0, 2, A - (2 << 20), 0, 0, Bytes(need, A + (i << 20)))
     overlap(B.waste_mx4_ffn_forward, m, A - (1 << 20), 0, 2, A - (2 << 20), 0, 0, Bytes(need, A - (1 << 20)))
     overlap(B.waste_mx4_ffn_forward, m, A - (1 << 20), 0, 2, A - (2 << 20), 0, 0, Bytes(need, A - (2 << 20)))
+
+
+@pytest.mark.parametrize("far", [(1 << 32) + 32, 1 << 31, (1 << 40) + 64, -(1 << 32) + 32])
+def test_sizes_past_32_bits(far):
+    """Sizes that would be other, valid ones once cut to 32 bits."""
+    refused(B.waste_ffn_config, B.ABI_VERSION, far, 32, B.ACT_BF16)
+    refused(B.waste_ffn_config, B.ABI_VERSION, 64, far, B.ACT_BF16)
+    refused(B.waste_mx4_ffn_config, B.ABI_VERSION, far, 32, P, P, P, P, P, P)
+    refused(B.waste_mx4_ffn_config, B.ABI_VERSION, 32, far, P, P, P, P, P, P)
+    m, w = B.waste_mx4_ffn_config(B.ABI_VERSION, 64, 32, P, P, P, P, P, P), Bytes(1 << 40)
+    refused(B.waste_ffn_workspace, cfg(), far)
+    refused(B.waste_ffn_forward, cfg(), P, far, P, P, P, P, B.ACT_F32, 0, None, None, w, stream=0)
+    refused(B.waste_ffn_backward, cfg(), P, far, P, P, P, P, P, P, P, P, P, P, B.ACT_F32, 0, w, stream=0)
+    refused(B.waste_mx4_ffn_workspace, m, far)
+    refused(B.waste_mx4_ffn_forward, m, P, 0, far, P, 0, 0, w, stream=0)
+    for r, c in ((far, 32), (32, far)):
+        refused(B.waste_mx4_layout, r, c)
+        refused(B.waste_mx4_quantize, P, 0, r, c, max(far, 32), P, P, stream=0)
+        refused(B.waste_mx4_dequantize, P, P, r, c, P, 0, max(far, 32), stream=0)
+    for s in ((far, 32, 32), (32, far, 32), (32, 32, far)):
+        refused(B.waste_mx4_matmul, *s, P, P, P, P, P, 0, stream=0)

@@ -1,5 +1,5 @@
-"""How the dense operators may be called: on memory that overlaps, from several host threads, in decode stacks
-of every kind."""
+"""How the dense operators may be called: on memory that overlaps, with sizes past 32 bits, from several
+host threads, in decode stacks of every kind."""
 import threading
 
 import pytest
@@ -104,6 +104,36 @@ def test_codes_between_strided_rows():
     assert torch.equal(x, values)
     B.waste_mx4_dequantize(codes, scales, rows, cols, x, B.ACT_F32, ld)
     assert torch.equal(x, want.dequantize())
+
+
+# ---------------------------------------------------------------- sizes past 2^30
+
+def test_sizes_past_32_bits_are_refused():
+    """Sizes that are other, small ones in 32 bits (one token, f = 8, one row tile): refused, not taken for those."""
+    W = weights(gen(3), 64, 32, BF)
+    far = 1 << 32
+    q = [Mx4Matrix.from_dense(w) for w in W]
+    for n in (far + 1, far + 300, (1 << 30) + 1):
+        for make in (lambda: DenseExpert(*W, max_tokens=n), lambda: Mx4Expert(*q, max_tokens=n)):
+            with pytest.raises(B.WasteError) as ei:
+                make()
+            assert ei.value.status == -1
+    room = torch.empty(8 * (far + 32), dtype=BF, device="cuda")  # 69 GB, not touched
+    w = codes = None
+    try:
+        w = room.view(far + 32, 8)
+        with pytest.raises(B.WasteError):
+            DenseExpert(w, w, room.view(8, far + 32), max_tokens=1)
+        with pytest.raises(B.WasteError):
+            DenseExpert(room.view(8, far + 32), room.view(8, far + 32), w, max_tokens=1)
+        codes = room.view(torch.uint8)[:(far + 32) * 16].view(far + 32, 16)
+        with pytest.raises(B.WasteError):
+            Mx4Matrix(far + 32, 32, codes, torch.empty(512, dtype=torch.uint8, device="cuda"))
+        with pytest.raises(B.WasteError):
+            Mx4Matrix(1, far + 32, codes.view(-1)[:(far + 32) // 2].view(1, -1), torch.empty(512, dtype=torch.uint8, device="cuda"))
+    finally:
+        del room, w, codes
+        torch.cuda.empty_cache()
 
 
 # ---------------------------------------------------------------- several host threads
