@@ -53,6 +53,7 @@ struct Span {
 bool meet(const Span &a, const Span &b) {
     if (!a.p || !b.p || !a.row_bytes || !b.row_bytes || !b.rows) return false;
     const uintptr_t a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p;
+    if (b.rows == 1) return a0 < b0 + b.row_bytes && b0 < a0 + a.row_bytes;
     // the first row of b that ends behind a's start
     const size_t past = a0 < b0 + b.row_bytes ? 0 : a0 - b0 - b.row_bytes;
     const size_t i = a0 < b0 + b.row_bytes ? 0 : b.pitch ? past / b.pitch + 1 : b.rows;
