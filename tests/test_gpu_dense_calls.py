@@ -1,5 +1,8 @@
-"""How the dense operators may be called: on memory that overlaps, with sizes past 32 bits, from several
-host threads, in decode stacks of every kind."""
+"""How the dense operators may be called: on memory that overlaps, with sizes past 32 bits, right behind
+what writes their weights, first in a process, from several host threads, in decode stacks of every kind."""
+import os
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -134,6 +137,94 @@ def test_sizes_past_32_bits_are_refused():
     finally:
         del room, w, codes
         torch.cuda.empty_cache()
+
+
+# ---------------------------------------------------------------- what stands right before a call
+
+@pytest.mark.parametrize("T", [1, 2, 3, 20, 64, 131, 600])
+def test_weights_written_just_before(T):
+    """Weights that the operators' own kernels write right before the calls that read them, the down matrix last (its
+    first rows are asked for ahead of a wait): each call sees the newest."""
+    d, f, n = 2048, 768, 40
+    g = gen(T)
+    sets = [weights(g, d, f, FP) for _ in range(2)]
+    fours = [[Mx4Matrix.from_dense(w) for w in ws] for ws in sets]
+    x, dy, sg, su = (randn(g, T, k, t=BF) for k in (d, d, f, f))
+    W = [torch.empty_like(w, dtype=BF) for w in sets[0]]
+    e = DenseExpert(*W, max_tokens=T)
+    m = [Mx4Matrix.empty(*w.shape) for w in W]
+    q = Mx4Expert(*m, max_tokens=T)
+    want = []
+    for four in fours:
+        for a, w in zip(four, W):
+            a.dequantize(w)
+        torch.cuda.synchronize()
+        y, dx = e.forward(x), torch.empty_like(x)
+        e.backward(dy, x, sg, su, dx)
+        want.append((y, dx, Mx4Expert(*four, max_tokens=T).forward(x)))
+        torch.cuda.synchronize()
+    assert not any(torch.equal(a, b) for a, b in zip(*want))
+    got = [[torch.empty_like(x) for _ in range(3)] for _ in range(n)]
+    for i, (y, dx, y4) in enumerate(got):
+        for a, w in zip(fours[i & 1], W):
+            a.dequantize(w)
+        e.forward(x, y)
+        fours[1 - (i & 1)][1].dequantize(W[1])  # and the order of the backward's
+        for j in (2, 0, 1):
+            fours[i & 1][j].dequantize(W[j])
+        e.backward(dy, x, sg, su, dx)
+        for a, w in zip(m, sets[i & 1]):
+            a.quantize(w)
+        q.forward(x, y4)
+    torch.cuda.synchronize()
+    for i, out in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(out, want[i & 1])), i
+
+
+FIRST = """
+import sys, torch
+from rvq_compressed_expert_gb300 import binding as B
+from rvq_compressed_expert_gb300.dense import DenseExpert
+from rvq_compressed_expert_gb300.mx4 import Mx4Expert, Mx4Matrix, matmul
+T, d, f = int(sys.argv[1]), 512, 256
+torch.manual_seed(1)
+rn = lambda *s: torch.randn(*s, device="cuda").bfloat16()
+W = [rn(f, d) / 20, rn(f, d) / 20, rn(d, f) / 16]
+x, dy, g, u = rn(T, d), rn(T, d), rn(T, f), rn(T, f)
+e, m, M4 = DenseExpert(*W, max_tokens=T), Mx4Matrix.empty(T, d), [Mx4Matrix.empty(*w.shape) for w in W]
+e.reserve_backward()
+q = Mx4Expert(*M4, max_tokens=T)
+out = [torch.empty_like(x) for _ in range(3)] + [torch.empty_like(w) for w in W] + [torch.empty(T, f, device="cuda"), x.float()]
+def calls():
+    e.forward(x, out[0])
+    e.backward(dy, x, g, u, out[1], *out[3:6])
+    m.quantize(x)
+    for a, b in zip(M4, W):
+        a.quantize(b)
+    matmul(m, M4[0], out[6])
+    q.forward(x, out[2])
+    m.dequantize(out[7])
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    calls()
+graph.replay()
+torch.cuda.synchronize()
+first = [o.clone() for o in out]
+calls()
+torch.cuda.synchronize()
+B.waste_dense_status()
+assert all(torch.equal(a, b) and torch.isfinite(a.float()).all() for a, b in zip(first, out))
+print("same")
+"""
+
+
+@pytest.mark.parametrize("T", [1, 20, 300])
+def test_first_calls_of_a_process_are_captured(T):
+    """A process whose first calls of every operator are recorded into a graph: its replay gives an eager call's bits."""
+    r = subprocess.run([sys.executable, "-c", FIRST, str(T)], capture_output=True, text=True, timeout=120,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr[-2000:]
 
 
 # ---------------------------------------------------------------- several host threads
