@@ -181,6 +181,62 @@ def test_weights_written_just_before(T):
         assert all(torch.equal(a, b) for a, b in zip(out, want[i & 1])), i
 
 
+@pytest.mark.parametrize("T", [1, 3, 40, 300])
+def test_captured_behind_memsets_copies_and_joins(T):
+    """Calls recorded right behind a memset, a copy, and the join of two streams (nodes that are no kernels, or several
+    of them), and calls with such nodes behind them: the replay gives eager bits."""
+    d, f = 512, 256
+    g = gen(T)
+    W = weights(g, d, f, BF)
+    e, q = DenseExpert(*W, max_tokens=T), Mx4Expert.from_dense(*W, max_tokens=T)
+    e.reserve_backward()
+    src, x, x2, dy, sg, su = (randn(g, T, n, t=BF) for n in (d, d, d, d, f, f))
+    y, y4, dx, back = (torch.empty(T, d, dtype=BF, device="cuda") for _ in range(4))
+    dw, m, c = [torch.empty_like(w) for w in W], Mx4Matrix.empty(T, d), torch.empty(T, f, device="cuda")
+    side = torch.cuda.Stream()
+    now = torch.cuda.current_stream
+
+    def calls():
+        for v in (y, y4, dx):
+            v.zero_()
+        x.copy_(src)                       # a copy, then the call that reads it
+        e.forward(x, y, mode=1)
+        side.wait_stream(now())
+        with torch.cuda.stream(side):
+            x2.copy_(y)                    # a copy behind a call
+            q.forward(x2, y4, mode=1)
+        c.zero_()
+        m.quantize(x)
+        matmul(m, q.gate, c, mode=1)
+        now().wait_stream(side)             # two predecessors
+        e.backward(dy, y4, sg, su, dx, *dw)
+        dy.copy_(dx)
+        e.backward(dy, x, sg, su, dx, *dw, accumulate=True)
+        back.copy_(dx)
+        m.dequantize(dx)
+
+    out = [y, y4, dx, back, c, *dw]
+    keep = dy.clone()
+    warm = torch.cuda.Stream()
+    warm.wait_stream(now())
+    with torch.cuda.stream(warm):
+        calls()
+    torch.cuda.synchronize()
+    want = [v.clone() for v in out]
+    dy.copy_(keep)
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        calls()
+    for _ in range(3):
+        dy.copy_(keep)
+        for v in out:
+            v.fill_(float("nan"))
+        gr.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+    assert all(torch.isfinite(v.float()).all() for v in want)
+
+
 FIRST = """
 import sys, torch
 from rvq_compressed_expert_gb300 import binding as B
