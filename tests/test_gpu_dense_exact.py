@@ -256,3 +256,81 @@ def test_matmul_of_extreme_scales(M, K):
         matmul(ones(M, sa), ones(200, sb), out)
         want = torch.tensor(float(K), dtype=torch.float64) * 2.0 ** (sa + sb - 254)
         assert (out == want.float().item()).all(), (sa, sb, out[0, 0].item(), want.item())
+
+
+# ---------------------------------------------------------------- values that one 16-bit part holds
+
+ONE_PART = [(1, 1032, 1544), (1, 7168, 1536), (33, 136, 264), (48, 2056, 520), (49, 2056, 520), (127, 1032, 136), (128, 512, 520),
+            (129, 72, 1544), (131, 7168, 1536), (150, 2056, 1032), (200, 1032, 264), (208, 4104, 136), (209, 4104, 136),
+            (257, 264, 1032), (333, 1032, 264), (511, 648, 392), (1000, 1544, 776), (2049, 2056, 1032), (4097, 1032, 1544)]
+
+
+@pytest.mark.parametrize("t", [BF, HF])
+@pytest.mark.parametrize("T,d,f", ONE_PART)
+def test_forward_of_whole_numbers(T, d, f, t):
+    """Every other column of a has g a sum over all of d (128 and up to 64 ones) and u a power of two, the rest the other
+    way round: a has at most 8 bits, so its one rounding is exact, and so is y over all of f."""
+    g = gen(T * 13 + d + f)
+    x = whole(g, -1, 1, T, d)
+    x[:, :2] = 1
+    odd = torch.arange(f, device="cuda") % 2 == 1
+    wg, wu = (sparse(g, f, d, 64, [1, -1]) for _ in range(2))
+    wg[odd], wu[~odd] = 0, 0
+    wg[:, :2], wu[:, :2] = 0, 0
+    wg[:, 0] = torch.where(odd, 32.0, 128.0)
+    wu[~odd, 1] = torch.exp2(whole(g, 0, 4, f))[~odd]
+    wd = whole(g, -1, 1, d, f)
+    G, U = exact_sums(x, wg), exact_sums(x, wu)
+    a = G * U
+    assert G.min() >= 32 and torch.equal(a.to(t).double(), a)
+    y = exact_sums(a, wd)
+    e = DenseExpert(*(w.to(t) for w in (wg, wu, wd)), max_tokens=T)
+    out, sg, su = (torch.full((T, n), float("nan"), dtype=o, device="cuda") for n, o in ((d, FP), (f, t), (f, t)))
+    e.forward(x.to(t), out, save_g=sg, save_u=su)
+    same(out, y, "y")
+    same(sg, G, "g")
+    same(su, U, "u")
+    scaled = wd * 2.0 ** -9  # into fp16's range
+    o16 = torch.full((T, d), float("nan"), dtype=t, device="cuda")
+    e = DenseExpert(*(w.to(t) for w in (wg, wu, scaled)), max_tokens=T)
+    e.forward(x.to(t), o16)
+    same(o16, y * 2.0 ** -9, "16-bit y")
+    base = whole(g, -1000, 1000, T, d) * 2.0 ** -9
+    acc = base.float()
+    e.forward(x.to(t), acc, mode=1)
+    if float(y.abs().max()) < 2 ** 23:
+        same(acc, base + y * 2.0 ** -9, "base + y")
+
+
+@pytest.mark.parametrize("t", [BF, HF])
+@pytest.mark.parametrize("T,d,f", ONE_PART)
+def test_backward_of_whole_numbers(T, d, f, t):
+    """g and u powers of two, da a sum over all of d of at most 64 ones: a, dg and du have at most 7 bits, and dx and the
+    weights' gradients are exact sums over all of f and of the tokens."""
+    g = gen(T * 11 + d + f)
+    x, dy = whole(g, -1, 1, T, d) * 0.25, whole(g, -1, 1, T, d)
+    sg, su = torch.exp2(whole(g, 5, 6, T, f)), torch.exp2(whole(g, 0, 2, T, f)) * (2 * whole(g, 0, 1, T, f) - 1)
+    wd = sparse(g, f, d, 64, [1, -1]).T.contiguous()
+    wg, wu = (whole(g, -1, 1, f, d) * 2.0 ** -9 for _ in range(2))
+    da = exact_sums(dy, wd.T)
+    a, dg, du = sg * su, da * su, da * sg
+    assert all(torch.equal(v.to(t).double(), v) for v in (a, dg, du))
+    assert float(((dg.abs() @ wg.abs()) + (du.abs() @ wu.abs())).max()) < 2 ** 24 * 2.0 ** -9
+    dx = dg @ wg + du @ wu
+    dw = [exact_sums(dg.T, x.T, 0.25), exact_sums(du.T, x.T, 0.25), exact_sums(dy.T, a.T)]
+    e = DenseExpert(*(w.to(t) for w in (wg, wu, wd)), max_tokens=T)
+    got = torch.full((T, d), float("nan"), dtype=t, device="cuda")
+    gw = [torch.full(v.shape, float("nan"), device="cuda") for v in dw]
+    call = [v.to(t) for v in (dy, x, sg, su)]
+    e.backward(*call, got, *gw)
+    same(got, dx, "dx")
+    for n, v, r in zip(("dw_gate", "dw_up", "dw_down"), gw, dw):
+        same(v, r, n)
+    assert all(v.abs().max() < 65504 for v in dw)
+    g16 = [torch.full(v.shape, float("nan"), dtype=t, device="cuda") for v in dw]
+    e.backward(*call, None, *g16)
+    for n, v, r in zip(("dw_gate", "dw_up", "dw_down"), g16, dw):
+        same(v, r, n + " in 16 bits")
+    e.backward(*call, None, *gw, accumulate=True)
+    for n, v, r in zip(("dw_gate", "dw_up", "dw_down"), gw, dw):
+        same(v, 2 * r, n + " added")
