@@ -17,11 +17,11 @@
 //
 // What bounds it: at 256 x 256 a stage brings 32 KB into an SM for 512 cycles of MMAs, and an SM takes
 // in about 100 B/ns, so loads and MMAs are near balance, and long 16-bit products run at the power
-// limit.  Measured: block of 4096 tokens (d 7168, f 1536, bf16, g and u kept) 168 us = 1.61 PFLOP/s,
-// its gradients 347 us = 1.56 PFLOP/s (cuBLAS sustains 1.71 on a square product); 4-bit
-// 4096 x 7168 x 7168 68 us = 6.2 PFLOP/s, tensor pipe 63 % active.
+// limit.  Measured, calls one behind another, range over GPUs: block of 4096 tokens (d 7168, f 1536, bf16, g and u
+// kept) 168 to 175 us = 1.54 to 1.61 PFLOP/s, its gradients 347 to 358 us = 1.51 to 1.56 PFLOP/s (cuBLAS sustains
+// 1.71 on a square product); 4-bit 4096 x 7168 x 7168 68 to 71 us = 5.9 to 6.2 PFLOP/s, tensor pipe 63 % active.
 //
-// Waits are bounded: one that gives up (about a second) latches g_dense_timeout, which
+// Waits are bounded: one that gives up (1.1 s) latches g_dense_timeout, which
 // waste_dense_status reports, and the CTA winds up.
 #pragma once
 
@@ -102,7 +102,7 @@ template <int kForm, int kCG> __device__ __forceinline__ Tile tile_at(const Gemm
 // A warp's common answer, which the compiler knows to be common.
 __device__ __forceinline__ bool all(bool v) { return __all_sync(0xffffffffu, v); }
 
-// A wait for a whole tile's product: about a second, and one more for every million pieces of k (a
+// A wait for a whole tile's product: 1.1 s, and as much again for every million pieces of k (a
 // piece takes well under a microsecond).
 __device__ __forceinline__ bool wait_tile(uint32_t bar, uint32_t parity, int pieces) {
     for (int i = 0; i <= pieces >> 20; ++i)

@@ -9,9 +9,9 @@
 // depend on gate_up for its weights: it is launched while gate_up runs and asks for its first rows
 // before it waits for a.  a never leaves fp32, so only the output is rounded.
 //
-// Against the tensor cores, d 7168, f 1536, weights from memory: one token of 16 bits 15.4 us here and
-// 20.5 there (dense_skinny.cuh), two 25.7 here and 20.5 there; 4-bit weights, one token 10.5 us here
-// and 16.8 there, two 16.4, three 20.6, four 22.8 (there 16.8 for all): the multiplications grow with the
+// Against the tensor cores, d 7168, f 1536, weights from memory: one token of 16 bits 14.8 us here and
+// 20.4 there (dense_skinny.cuh), two 25.7 here and 20.4 there; 4-bit weights, one token 9.8 us here
+// and 17.0 there, two 15.6, three 20.6, four 22.8 (there 17.0 for all): the multiplications grow with the
 // tokens.
 #include "dense.cuh"
 #include "dense_tc.cuh"

@@ -6,7 +6,8 @@
 // in is bound too (about 100 B/ns): in 128-row tiles of tokens (dense_gemm.cuh) most of a stage
 // would be the tokens' rows, loaded again for every tile.  Here a stage is 128 rows of each weight
 // matrix and only as many columns as there are tokens, so nearly all of it is weights that are read
-// once.  Every tile is split over k by a cluster, so that all SMs take part.
+// once.  Where there are fewer tiles than SMs a tile is split over k by a cluster (S CTAs, 1 where no more run at
+// once or k is short), so that more of the SMs take part.
 //
 // The sums leave tensor memory transposed (a lane is a weight row) into rows per token, each CTA of a
 // cluster adds up its share of them in rank order, and they go through the same epilogues as
