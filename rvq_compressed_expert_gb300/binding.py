@@ -79,14 +79,20 @@ def _far(*sizes):
     raise WasteError(-1, f"sizes {sizes}: at most 2^30")
 
 
+def _near(fields, named):
+    """Refuses a configuration whose d or f (its second and third field) do not fit 32 bits."""
+    d, f = (fields[i] if len(fields) > i else named.get(n, 0) for i, n in ((1, "d"), (2, "f")))
+    if not -1 <= (d | f) >> 31 <= 0:
+        _far(d, f)
+
+
 class waste_ffn_config(ctypes.Structure):
     _fields_ = [("abi_version", ctypes.c_uint32), ("d", ctypes.c_int32), ("f", ctypes.c_int32),
                 ("dtype", ctypes.c_int32)]
 
-    def __init__(self, abi_version=ABI_VERSION, d=0, f=0, dtype=0):
-        if not -1 <= (d | f) >> 31 <= 0:
-            _far(d, f)
-        super().__init__(abi_version, d, f, dtype)
+    def __init__(self, *fields, **named):
+        _near(fields, named)
+        super().__init__(*fields, **named)
 
 
 class waste_mx4_ffn_config(ctypes.Structure):
@@ -94,10 +100,9 @@ class waste_mx4_ffn_config(ctypes.Structure):
         (n, ctypes.c_void_p) for n in ("d_gate_codes", "d_gate_scales", "d_up_codes", "d_up_scales",
                                        "d_down_codes", "d_down_scales")]
 
-    def __init__(self, abi_version=ABI_VERSION, d=0, f=0, *pointers):
-        if not -1 <= (d | f) >> 31 <= 0:
-            _far(d, f)
-        super().__init__(abi_version, d, f, *pointers)
+    def __init__(self, *fields, **named):
+        _near(fields, named)
+        super().__init__(*fields, **named)
 
 
 class WasteError(RuntimeError):

@@ -288,3 +288,12 @@ def test_sizes_past_32_bits(far):
         refused(B.waste_mx4_dequantize, P, P, r, c, P, 0, max(far, 32), stream=0)
     for s in ((far, 32, 32), (32, far, 32), (32, 32, far)):
         refused(B.waste_mx4_matmul, *s, P, P, P, P, P, 0, stream=0)
+
+
+def test_configs_take_fields_by_name():
+    c = B.waste_ffn_config(abi_version=B.ABI_VERSION, d=64, f=32, dtype=B.ACT_F16)
+    assert (c.d, c.f, c.dtype) == (64, 32, B.ACT_F16) and B.waste_ffn_config().d == 0
+    m = B.waste_mx4_ffn_config(B.ABI_VERSION, 64, d_up_codes=P, f=32)
+    assert (m.d, m.f, m.d_up_codes, m.d_gate_codes) == (64, 32, P, None)
+    refused(lambda: B.waste_ffn_config(d=1 << 32))
+    refused(lambda: B.waste_mx4_ffn_config(B.ABI_VERSION, 64, f=1 << 33))
