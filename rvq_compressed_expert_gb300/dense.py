@@ -37,11 +37,20 @@ def make(shape, dtype, device, stream) -> torch.Tensor:
 
 class Workspace:
     """A buffer made on one stream and lent to calls on any: the allocator is told of the others, so
-    that its memory is not given away while a call there still runs."""
+    that its memory is not given away while a call there still runs.  one: held while a call is
+    enqueued, so that the launches of two host threads' calls do not mix."""
 
     def __init__(self, nbytes: int, device):
         self.bytes = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
         self.home = B.stream_on(device.index, None)
+        self.one = threading.Lock()
+
+    def __getstate__(self):
+        return self.bytes, self.home
+
+    def __setstate__(self, state):
+        self.bytes, self.home = state
+        self.one = threading.Lock()
 
     def lend(self, stream, handle: int) -> torch.Tensor:
         """For a call on `stream`, whose handle is given."""
@@ -74,7 +83,6 @@ class DenseExpert:
         self._own, self._out = (t,), (t, torch.float32)  # types of inputs, and of outputs
         self.cfg = B.waste_ffn_config(B.ABI_VERSION, d, f, ACT[t])
         self._ws = {}
-        self._one = threading.Lock()
         self._workspace(0)
 
     def _workspace(self, backward: int) -> Workspace:
@@ -85,13 +93,14 @@ class DenseExpert:
         if ws is None:
             require(not torch.cuda.is_current_stream_capturing(),
                     "reserve the workspace before the capture (reserve_backward)")
-            ws = self._ws[backward] = Workspace(B.waste_ffn_workspace(self.cfg, self.max_tokens, backward), self.device)
+            # of two host threads that come first, both take one's
+            ws = self._ws.setdefault(backward, Workspace(B.waste_ffn_workspace(self.cfg, self.max_tokens, backward),
+                                                         self.device))
         return ws
 
     def reserve_backward(self):
         """Makes the backward's workspace (three [max_tokens, f] buffers, and partial sums of few tokens) now."""
-        with self._one:
-            self._workspace(1)
+        self._workspace(1)
 
     def _tokens(self, x, name):
         if not isinstance(x, torch.Tensor) or x.dim() != 2:
@@ -119,9 +128,10 @@ class DenseExpert:
             if t is not None:
                 check(t, n, (T, self.f), self._own, self.device)
         h = B.stream_on(index, stream)
-        with self._one:
+        ws = self._ws[0]
+        with ws.one:
             B.waste_ffn_forward(self.cfg, x, T, self.w_gate, self.w_up, self.w_down, out, ACT[out.dtype], mode, save_g,
-                                save_u, self._ws[0].lend(stream, h), h)
+                                save_u, ws.lend(stream, h), h)
         return out
 
     def backward(self, dy, x, g, u, dx=None, dw_gate=None, dw_up=None, dw_down=None, accumulate: bool = False,
@@ -146,6 +156,7 @@ class DenseExpert:
             if t is not None:
                 check(t, n, w.shape, (gt,) if gt in self._out else self._out, self.device)
         h = B.stream_on(index, stream)
-        with self._one:
+        ws = self._workspace(1)
+        with ws.one:
             B.waste_ffn_backward(self.cfg, dy, T, x, g, u, self.w_gate, self.w_up, self.w_down, dx, dw_gate, dw_up,
-                                 dw_down, ACT[gt], int(accumulate), self._workspace(1).lend(stream, h), h)
+                                 dw_down, ACT[gt], int(accumulate), ws.lend(stream, h), h)

@@ -7,8 +7,6 @@ without decoding.  All computation is in the library's kernels.
 """
 from __future__ import annotations
 
-import threading
-
 import torch
 
 from . import binding as B
@@ -113,7 +111,6 @@ class Mx4Expert:
         self.d, self.f, self.device, self.index, self.max_tokens = d, f, gate.device, gate.index, int(max_tokens)
         self.cfg = B.waste_mx4_ffn_config(B.ABI_VERSION, d, f, *(t.data_ptr() for m in (gate, up, down)
                                                                  for t in (m.codes, m.scales)))
-        self._one = threading.Lock()
         self._ws = Workspace(B.waste_mx4_ffn_workspace(self.cfg, self.max_tokens), self.device)
 
     @classmethod
@@ -137,6 +134,7 @@ class Mx4Expert:
             out = make((T, self.d), x.dtype, self.device, stream)
         check(out, "out", (T, self.d), _FLOATS, self.device)
         h = B.stream_on(index, stream)
-        with self._one:
-            B.waste_mx4_ffn_forward(self.cfg, x, ACT[x.dtype], T, out, ACT[out.dtype], mode, self._ws.lend(stream, h), h)
+        ws = self._ws
+        with ws.one:
+            B.waste_mx4_ffn_forward(self.cfg, x, ACT[x.dtype], T, out, ACT[out.dtype], mode, ws.lend(stream, h), h)
         return out

@@ -1,6 +1,9 @@
 """How the dense operators may be called: on memory that overlaps, with sizes past 32 bits, right behind
-what writes their weights, first in a process, from several host threads, in decode stacks of every kind."""
+what writes their weights, first in a process, from several host threads, in decode stacks of every kind, on copies
+of an expert."""
+import copy
 import os
+import pickle
 import subprocess
 import sys
 import threading
@@ -478,3 +481,23 @@ def test_banked_stack_with_shared_experts(lookahead):
             m.stats()
     finally:
         ts.close()
+
+
+# ---------------------------------------------------------------- copies of an expert
+
+def test_copies_of_an_expert():
+    """A shallow copy (it shares the workspace, and what keeps two threads' calls apart in it), a deep one and one
+    through pickle give the same bits, forward and backward."""
+    T, d, f = 40, 64, 32
+    g = gen(9)
+    e = DenseExpert(*weights(g, d, f, BF), max_tokens=T)
+    x, dy, sg, su = (randn(g, T, n, t=BF) for n in (d, d, f, f))
+    want, dx = e.forward(x), torch.empty_like(x)
+    e.backward(dy, x, sg, su, dx)
+    for twin in (copy.copy(e), copy.deepcopy(e), pickle.loads(pickle.dumps(e))):
+        got = torch.empty_like(dx)
+        twin.backward(dy, x, sg, su, got)
+        assert torch.equal(twin.forward(x), want) and torch.equal(got, dx)
+        assert (twin._ws[0].one is e._ws[0].one) == (twin._ws[0].bytes.data_ptr() == e._ws[0].bytes.data_ptr())
+    q = Mx4Expert.from_dense(*weights(g, d, f, BF), max_tokens=T)
+    assert torch.equal(copy.copy(q).forward(x), q.forward(x))
