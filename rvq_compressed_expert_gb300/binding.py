@@ -40,8 +40,8 @@ EXPORTED = ["waste_moe_record_layout", "waste_moe_pack_records", "waste_moe_crea
             "waste_moe_create_banked", "waste_rvq_train", "waste_rvq_encode", "waste_moe_debug_wait"]
 
 # include/waste_dense.h
-EXPORTED_DENSE = ["waste_dense_status", "waste_dense_debug_wait", "waste_ffn_workspace", "waste_ffn_forward", "waste_ffn_backward", "waste_mx4_layout",
-                  "waste_mx4_quantize", "waste_mx4_dequantize", "waste_mx4_matmul", "waste_mx4_ffn_workspace",
+EXPORTED_DENSE = ["waste_dense_status", "waste_dense_debug_wait", "waste_ffn_workspace", "waste_ffn_forward",
+                  "waste_ffn_backward", "waste_mx4_layout", "waste_mx4_quantize", "waste_mx4_dequantize", "waste_mx4_matmul", "waste_mx4_ffn_workspace",
                   "waste_mx4_ffn_forward"]
 
 

@@ -35,7 +35,7 @@ cudaError_t encode(CUtensorMap *m, CUtensorMapDataType type, const void *p, cons
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     };
     CUresult r = call();
-    if (r != CUDA_SUCCESS) {
+    if (r == CUDA_ERROR_INVALID_CONTEXT) {
         int dev = 0;
         cudaError_t e = cudaGetDevice(&dev);
         if (e == cudaSuccess) e = cudaSetDevice(dev);
