@@ -35,7 +35,8 @@ enum { WASTE_ACT_F16 = 2 }; /* beside WASTE_ACT_F32 and WASTE_ACT_BF16 */
 
 /* Synchronises the device; WASTE_ETIMEOUT if a bounded device wait of one of these operators
  * gave up on the current device since the last call of this (outputs since then are not to be
- * used, and the context is to be treated as unusable, as after waste_moe_stats), else WASTE_OK. */
+ * used, and the context is to be treated as unusable, as after waste_moe_stats), WASTE_EINVAL if one of
+ * waste_train.h found offsets that fall or leave the rows, else WASTE_OK. */
 int waste_dense_status(void);
 
 /* Test aid for that report: one CTA on `stream` waits, by the operators' own wait, on a barrier that

@@ -1,4 +1,4 @@
-"""ctypes binding of libwaste_moe (include/waste_moe.h, include/waste_dense.h): same names, argument marshalling only.
+"""ctypes binding of libwaste_moe (include/waste_moe.h, waste_dense.h, waste_train.h): same names, argument marshalling only.
 
 Tensors are passed as torch tensors (their data pointers are handed to the
 library) or as raw integer addresses; streams as ``torch.cuda.Stream``, an
@@ -17,7 +17,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libwaste_moe.so")
 
 ABI_VERSION = 1
-ACT_F32, ACT_BF16, ACT_F16 = 0, 1, 2  # ACT_F16: the dense operators only
+ACT_F32, ACT_BF16, ACT_F16 = 0, 1, 2  # ACT_F16: the dense and training operators only
 FLAG_VERIFY_CRC = 1 << 0
 FLAG_FORCE_GEMV = 1 << 2
 FLAG_FORCE_MMA = 1 << 3
@@ -43,6 +43,10 @@ EXPORTED = ["waste_moe_record_layout", "waste_moe_pack_records", "waste_moe_crea
 EXPORTED_DENSE = ["waste_dense_status", "waste_dense_debug_wait", "waste_ffn_workspace", "waste_ffn_forward",
                   "waste_ffn_backward", "waste_mx4_layout", "waste_mx4_quantize", "waste_mx4_dequantize", "waste_mx4_matmul", "waste_mx4_ffn_workspace",
                   "waste_mx4_ffn_forward"]
+
+# include/waste_train.h
+EXPORTED_TRAIN = ["waste_norm_forward", "waste_norm_workspace", "waste_norm_backward", "waste_group_forward",
+                  "waste_group_backward", "waste_ortho_workspace", "waste_ortho_update"]
 
 
 class waste_moe_config(ctypes.Structure):
@@ -103,6 +107,31 @@ class waste_mx4_ffn_config(ctypes.Structure):
     def __init__(self, *fields, **named):
         _near(fields, named)
         super().__init__(*fields, **named)
+
+
+class _SizedConfig(ctypes.Structure):
+    """A configuration whose 32-bit integers are refused where they do not fit, not cut."""
+
+    def __init__(self, *fields, **named):
+        values = dict(zip((n for n, _ in self._fields_), fields), **named)
+        for n, c in self._fields_:
+            if c is ctypes.c_int32 and not -1 <= values.get(n, 0) >> 31 <= 0:
+                _far(values[n])
+        super().__init__(*fields, **named)
+
+
+class waste_norm_config(_SizedConfig):
+    _fields_ = [("abi_version", ctypes.c_uint32)] + [(n, ctypes.c_int32) for n in (
+        "d", "x_dtype", "y_dtype", "w_dtype")] + [("eps", ctypes.c_float)]
+
+
+class waste_group_config(_SizedConfig):
+    _fields_ = [("abi_version", ctypes.c_uint32)] + [(n, ctypes.c_int32) for n in ("n_experts", "k", "n", "dtype")]
+
+
+class waste_ortho_config(_SizedConfig):
+    _fields_ = [("abi_version", ctypes.c_uint32)] + [(n, ctypes.c_int32) for n in ("count", "rows", "cols", "steps")] + [
+        (n, ctypes.c_float) for n in "abc"]
 
 
 class WasteError(RuntimeError):
@@ -169,7 +198,15 @@ def load(path: str = LIB_PATH):
     lib.waste_mx4_matmul.argtypes = [i32, i32, i32, vp, vp, vp, vp, vp, i32, i32, vp]
     lib.waste_mx4_ffn_workspace.argtypes = [mx4, i32, ctypes.POINTER(sz)]
     lib.waste_mx4_ffn_forward.argtypes = [mx4, vp, i32, i32, vp, i32, i32, vp, sz, vp]
-    for name in EXPORTED + EXPORTED_DENSE:
+    norm, group, ortho = (ctypes.POINTER(c) for c in (waste_norm_config, waste_group_config, waste_ortho_config))
+    lib.waste_norm_forward.argtypes = [norm, vp, i64, i32, vp, vp, vp, i64, vp, vp, vp]
+    lib.waste_norm_workspace.argtypes = [norm, i32, ctypes.POINTER(sz)]
+    lib.waste_norm_backward.argtypes = [norm, vp, i64, vp, i64, i32, vp, vp, vp, vp, i64, vp, vp, i32, i32, vp, sz, vp]
+    lib.waste_group_forward.argtypes = [group, vp, i32, vp, vp, vp, i32, i32, vp]
+    lib.waste_group_backward.argtypes = [group, vp, vp, i32, vp, vp, vp, vp, i32, i32, vp]
+    lib.waste_ortho_workspace.argtypes = [ortho, ctypes.POINTER(sz)]
+    lib.waste_ortho_update.argtypes = [ortho, vp, i32, vp, i32, ctypes.c_float, i32, vp, sz, vp]
+    for name in EXPORTED + EXPORTED_DENSE + EXPORTED_TRAIN:
         if name not in ("waste_moe_destroy", "waste_moe_last_error", "waste_bank_destroy"):
             getattr(lib, name).restype = ctypes.c_int
     _lib = lib
@@ -461,4 +498,60 @@ def waste_mx4_ffn_forward(cfg, d_x, x_dtype, T, d_out, out_dtype, mode, workspac
         _far(T)
     rc = (_lib or load()).waste_mx4_ffn_forward(ctypes.byref(cfg), _ptr(d_x), x_dtype, T, _ptr(d_out), out_dtype, mode,
                                                 workspace.data_ptr(), workspace.numel(), _stream(stream))
+    return rc and _check(rc)
+
+
+def waste_norm_forward(cfg, d_x, ld_x, T, d_w, d_b, d_y, ld_y, d_mean=None, d_rstd=None, stream=None):
+    if not -1 <= T >> 31 <= 0:
+        _far(T)
+    rc = (_lib or load()).waste_norm_forward(ctypes.byref(cfg), _ptr(d_x), ld_x, T, _ptr(d_w), _ptr(d_b), _ptr(d_y), ld_y,
+                                             _ptr(d_mean), _ptr(d_rstd), _stream(stream))
+    return rc and _check(rc)
+
+
+def waste_norm_workspace(cfg, T) -> int:
+    if not -1 <= T >> 31 <= 0:
+        _far(T)
+    n = ctypes.c_size_t()
+    _check(load().waste_norm_workspace(ctypes.byref(cfg), T, ctypes.byref(n)))
+    return n.value
+
+
+def waste_norm_backward(cfg, d_dy, ld_dy, d_x, ld_x, T, d_mean, d_rstd, d_w, d_dx, ld_dx, d_dw, d_db, grad_dtype,
+                        accumulate, workspace, stream=None):
+    """workspace: a uint8 tensor (its size is passed on), or None."""
+    if not -1 <= T >> 31 <= 0:
+        _far(T)
+    rc = (_lib or load()).waste_norm_backward(
+        ctypes.byref(cfg), _ptr(d_dy), ld_dy, _ptr(d_x), ld_x, T, _ptr(d_mean), _ptr(d_rstd), _ptr(d_w), _ptr(d_dx), ld_dx,
+        _ptr(d_dw), _ptr(d_db), grad_dtype, accumulate, _ptr(workspace), 0 if workspace is None else workspace.numel(),
+        _stream(stream))
+    return rc and _check(rc)
+
+
+def waste_group_forward(cfg, d_x, rows, d_offsets, d_w, d_out, out_dtype, mode=0, stream=None):
+    if not -1 <= rows >> 31 <= 0:
+        _far(rows)
+    rc = (_lib or load()).waste_group_forward(ctypes.byref(cfg), _ptr(d_x), rows, _ptr(d_offsets), _ptr(d_w), _ptr(d_out),
+                                              out_dtype, mode, _stream(stream))
+    return rc and _check(rc)
+
+
+def waste_group_backward(cfg, d_dy, d_x, rows, d_offsets, d_w, d_dx, d_dw, grad_dtype, accumulate=0, stream=None):
+    if not -1 <= rows >> 31 <= 0:
+        _far(rows)
+    rc = (_lib or load()).waste_group_backward(ctypes.byref(cfg), _ptr(d_dy), _ptr(d_x), rows, _ptr(d_offsets), _ptr(d_w),
+                                               _ptr(d_dx), _ptr(d_dw), grad_dtype, accumulate, _stream(stream))
+    return rc and _check(rc)
+
+
+def waste_ortho_workspace(cfg) -> int:
+    n = ctypes.c_size_t()
+    _check(load().waste_ortho_workspace(ctypes.byref(cfg), ctypes.byref(n)))
+    return n.value
+
+
+def waste_ortho_update(cfg, d_g, g_dtype, d_out, out_dtype, scale, mode, workspace, stream=None):
+    rc = (_lib or load()).waste_ortho_update(ctypes.byref(cfg), _ptr(d_g), g_dtype, _ptr(d_out), out_dtype, scale, mode,
+                                             _ptr(workspace), workspace.numel(), _stream(stream))
     return rc and _check(rc)

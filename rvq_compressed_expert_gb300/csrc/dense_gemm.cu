@@ -23,15 +23,17 @@ EncodeFn encoder() {
     }();
     return fn;
 }
-// A two-dimensional map.  In a host thread that has not used CUDA yet no context is current, and the driver
+} // namespace
+
+// In a host thread that has not used CUDA yet no context is current, and the driver
 // refuses (the runtime would make the device's own current by itself): it is made current, once a thread.
-cudaError_t encode(CUtensorMap *m, CUtensorMapDataType type, const void *p, const cuuint64_t (&dims)[2], cuuint64_t stride,
-                   const cuuint32_t (&box)[2], CUtensorMapSwizzle swizzle, CUtensorMapL2promotion l2) {
+cudaError_t encode_map(CUtensorMap *m, CUtensorMapDataType type, int rank, const void *p, const cuuint64_t *dims,
+                       const cuuint64_t *strides, const cuuint32_t *box, CUtensorMapSwizzle swizzle, CUtensorMapL2promotion l2) {
     const EncodeFn fn = encoder();
     if (!fn) return cudaErrorNotSupported;
-    const cuuint32_t one[2] = {1, 1};
+    const cuuint32_t one[3] = {1, 1, 1};
     const auto call = [&] {
-        return fn(m, type, 2, const_cast<void *>(p), dims, &stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, l2,
+        return fn(m, type, rank, const_cast<void *>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, l2,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     };
     CUresult r = call();
@@ -43,6 +45,13 @@ cudaError_t encode(CUtensorMap *m, CUtensorMapDataType type, const void *p, cons
         r = call();
     }
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+namespace {
+// A two-dimensional map.
+cudaError_t encode(CUtensorMap *m, CUtensorMapDataType type, const void *p, const cuuint64_t (&dims)[2], cuuint64_t stride,
+                   const cuuint32_t (&box)[2], CUtensorMapSwizzle swizzle, CUtensorMapL2promotion l2) {
+    return encode_map(m, type, 2, p, dims, &stride, box, swizzle, l2);
 }
 } // namespace
 

@@ -584,6 +584,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
 
 // ---- tensor maps (host) --------------------------------------------------------------------
 
+// A tiled tensor map of rank 2 or 3 (strides in bytes, of all dimensions but the first).
+cudaError_t encode_map(CUtensorMap *m, CUtensorMapDataType type, int rank, const void *p, const cuuint64_t *dims,
+                       const cuuint64_t *strides, const cuuint32_t *box, CUtensorMapSwizzle swizzle, CUtensorMapL2promotion l2);
+
 // A tensor map over rows x row_bytes bytes (contiguous rows): boxes of box_rows rows x 128 bytes,
 // 128-byte swizzle, zeros past the ends.  unit: bytes of one coordinate step (2 or 1).
 cudaError_t make_map(CUtensorMap *m, const void *p, int unit, int rows, size_t row_bytes, int box_rows);

@@ -1,0 +1,304 @@
+// Updates made orthogonal by Newton-Schulz products (waste_train.h).
+//
+// X holds 2^10 times its value in two fp16 parts, hi + lo; products take hi and sum in fp32.  The factor keeps what is
+// small (A starts with entries of 1e-5 and less) above fp16's subnormals and what is large (at most 8) in its range.
+// With hi alone the error of one rounding stays in X: for a gradient of low rank it lies outside the rank's space, where
+// every step makes it 3.4 times larger (4 % for rank 8, 15 % for rank 1).  B = b A + c A^2 keeps its diagonal apart
+// in fp32: near the end it is the largest part of B, and its rounding would be the largest error (1.7e-3 with
+// it in fp16, 0.9e-3 without, G Gaussian).  The diagonal multiplies hi while noise can still grow, so that
+// B X stays in X's space, and hi + lo in the last two steps.
+#include "tile_mma.cuh"
+
+namespace wm {
+namespace train {
+
+namespace {
+
+constexpr float kUp = 1024.f, kDown = 1.f / 1024.f;
+constexpr int kFlat = 256; // threads of the kernels that are not products
+
+__device__ __forceinline__ float value(const void *p, int dtype, size_t i) {
+    if (dtype == WASTE_ACT_F32) return static_cast<const float *>(p)[i];
+    if (dtype == WASTE_ACT_BF16) return (float)static_cast<const __nv_bfloat16 *>(p)[i];
+    return (float)static_cast<const __half *>(p)[i];
+}
+
+// Sums of squares of each matrix, in three ranges so that none leaves fp32: below 2^-45 times 2^80, past 2^45 times
+// 2^-80, and the rest (NaN among it).  sums [count][kOrthoParts][3].
+__global__ void __launch_bounds__(kFlat) squares_kernel(const void *g, int dtype, int64_t size, float *sums) {
+    __shared__ float part[3][kFlat / 32];
+    tc::grid_wait_release();
+    const int64_t i0 = size * blockIdx.x / kOrthoParts, i1 = size * (blockIdx.x + 1) / kOrthoParts;
+    const size_t at = (size_t)blockIdx.y * size;
+    float s[3] = {0.f, 0.f, 0.f};
+    for (int64_t i = i0 + threadIdx.x; i < i1; i += kFlat) {
+        const float v = value(g, dtype, at + i), m = fabsf(v);
+        const float up = v * 0x1p80f, down = v * 0x1p-80f;
+        if (m < 0x1p-45f)
+            s[0] = fmaf(up, up, s[0]);
+        else if (m > 0x1p45f)
+            s[1] = fmaf(down, down, s[1]);
+        else
+            s[2] = fmaf(v, v, s[2]);
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
+        if ((threadIdx.x & 31) == 0) part[k][threadIdx.x >> 5] = s[k];
+    }
+    __syncthreads();
+    if (threadIdx.x < 3) {
+        float v = 0.f;
+        for (int w = 0; w < kFlat / 32; ++w) v += part[threadIdx.x][w];
+        sums[((size_t)blockIdx.y * kOrthoParts + blockIdx.x) * 3 + threadIdx.x] = v;
+    }
+}
+
+// 2^10 G / |G| in two parts.
+__global__ void __launch_bounds__(kFlat)
+    start_kernel(const void *g, int dtype, int rows, int cols, int ldx, const float *sums, __half *hi, __half *lo) {
+    __shared__ double part[kOrthoParts];
+    __shared__ float factor, two_a, two_b;
+    tc::grid_wait_release();
+    const float *mine = sums + (size_t)blockIdx.y * kOrthoParts * 3;
+    if (threadIdx.x < kOrthoParts) {
+        const float *p = mine + threadIdx.x * 3;
+        part[threadIdx.x] = (double)p[0] * 0x1p-160 + (double)p[1] * 0x1p160 + (double)p[2];
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double s = 0.;
+        for (int i = 0; i < kOrthoParts; ++i) s += part[i];
+        s = sqrt(s);
+        // |G| = f 2^e, 0.5 <= f < 1: G 2^-e by two exact powers of two, then 1 / f
+        int e = 0;
+        const double f = frexp(s, &e);
+        const bool bad = isnan(s) || isinf(s);
+        factor = bad ? __int_as_float(0x7fc00000) : s == 0. ? 0.f : (float)((double)kUp / f);
+        const int h = bad ? 0 : -e / 2;
+        two_a = (float)ldexp(1., h);
+        two_b = (float)ldexp(1., (bad ? 0 : -e) - h);
+    }
+    __syncthreads();
+    const float f = factor, ta = two_a, tb = two_b;
+    const int64_t n = (int64_t)rows * ldx;
+    for (int64_t i = (int64_t)blockIdx.x * kFlat + threadIdx.x; i < n; i += (int64_t)gridDim.x * kFlat) {
+        const int r = (int)(i / ldx), c = (int)(i - (int64_t)r * ldx);
+        float v = c < cols ? value(g, dtype, (size_t)blockIdx.y * rows * cols + (size_t)r * cols + c) * ta * tb * f : 0.f;
+        const __half h = __float2half_rn(v);
+        const size_t to = (size_t)blockIdx.y * n + i;
+        hi[to] = h;
+        lo[to] = __float2half_rn(v - __half2float(h));
+    }
+}
+
+// What the three products of a step have in common: `count` matrices of M x N results, tiles of 128 * cg x BN.
+struct Stack {
+    int BN, high, tm, tn, count, M, K;
+    cudaError_t set(int cg, int bn, int n, int m, int cols, int k) {
+        BN = bn, high = kBM * cg, M = m, K = k, count = n;
+        tm = (m + high - 1) / high;
+        tn = (cols + bn - 1) / bn;
+        return cudaSuccess;
+    }
+    __device__ __forceinline__ int tiles() const { return count * tm * tn; }
+    __device__ __forceinline__ Spot spot(int t) const {
+        const int z = t / (tm * tn), r = t - z * tm * tn;
+        // groups of rows of tiles, columns moving slowest inside a group
+        const int group = 2048 / high, per = group * tn, g = r / per, top = g * group, gm = min(group, tm - top), i = r - g * per;
+        Spot T;
+        T.am = (top + i % gm) * high;
+        T.bm = T.n = i / gm * BN;
+        T.az = T.bz = z;
+        T.ak = T.bk = 0;
+        T.pieces = (K + 63) >> 6;
+        T.left = 64;
+        T.m = z * M + T.am;
+        T.rows = M - T.am;
+        return T;
+    }
+};
+// 32 rows x W columns of fp16 (rows of `ld`, a multiple of 8) as floats.
+template <int W> __device__ __forceinline__ void halves(Out32 &o, const void *p, int ld, int n, float (&v)[W]) {
+    uint4 q[W / 8];
+    dense::get32<W>(o, p, ld, n, ld, q);
+#pragma unroll
+    for (int i = 0; i < W / 8; ++i) dense::widen8(false, q[i], *reinterpret_cast<float(*)[8]>(&v[8 * i]));
+}
+template <int W>
+__device__ __forceinline__ void put_halves(Out32 &o, const CUtensorMap *map, void *p, int ld, int n, const float (&v)[W]) {
+    dense::put32_as(WASTE_ACT_F16, o, o.rows >= 32 ? map : nullptr, p, ld, n, ld, true, false, v);
+}
+
+// A = X X^T (kMn: X^T X)
+template <bool kMn> struct GramJob {
+    static constexpr bool kAmn = kMn, kBmn = kMn, kMask = false;
+    CUtensorMap ta, tb, to;
+    Stack s;
+    void *a;
+    int ldm;
+    __device__ void begin(uint8_t *) const {}
+    __device__ __forceinline__ int tiles(const uint8_t *) const { return s.tiles(); }
+    __device__ __forceinline__ Spot spot(const uint8_t *, int t) const { return s.spot(t); }
+    template <int W> __device__ __forceinline__ void tile(Out32 &o, const Spot &, int n, const float (&v)[W]) const {
+        float x[W];
+#pragma unroll
+        for (int i = 0; i < W; ++i) x[i] = v[i] * kDown;
+        put_halves(o, &to, a, ldm, n, x);
+    }
+};
+// B = b A + c A^2, its diagonal apart
+struct SquareJob {
+    static constexpr bool kAmn = false, kBmn = false, kMask = false;
+    CUtensorMap ta, tb, to;
+    Stack s;
+    const void *a;
+    void *out;
+    float *diag;
+    int ldm;
+    float b, c;
+    __device__ void begin(uint8_t *) const {}
+    __device__ __forceinline__ int tiles(const uint8_t *) const { return s.tiles(); }
+    __device__ __forceinline__ Spot spot(const uint8_t *, int t) const { return s.spot(t); }
+    template <int W> __device__ __forceinline__ void tile(Out32 &o, const Spot &T, int n, const float (&v)[W]) const {
+        float x[W];
+        halves(o, a, ldm, n, x);
+        const int row = o.m - T.az * s.M + o.lane; // of its matrix
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            x[i] = fmaf(c, v[i] * kDown, b * x[i]);
+            if (n + i == row) {
+                if (o.lane < o.rows) diag[(size_t)o.m + o.lane] = x[i] * kDown;
+                x[i] = 0.f;
+            }
+        }
+        put_halves(o, &to, out, ldm, n, x);
+    }
+};
+// X <- a X + B X (kTall: a X + X B), the last one to the caller's memory
+template <bool kTall> struct StepJob {
+    static constexpr bool kAmn = false, kBmn = !kTall, kMask = false;
+    CUtensorMap ta, tb, thi, tlo;
+    Stack s;
+    const void *hi;
+    void *lo, *hi_next;
+    const float *diag;
+    int ldx, cols;
+    float a;
+    int full; // the diagonal multiplies both parts
+    // last step
+    CUtensorMap tout;
+    void *out;
+    int out_dtype, add, by_map;
+    float scale;
+    __device__ void begin(uint8_t *) const {}
+    __device__ __forceinline__ int tiles(const uint8_t *) const { return s.tiles(); }
+    __device__ __forceinline__ Spot spot(const uint8_t *, int t) const { return s.spot(t); }
+    template <int W> __device__ __forceinline__ void tile(Out32 &o, const Spot &T, int n, const float (&v)[W]) const {
+        float x[W], l[W];
+        halves(o, hi, ldx, n, x);
+        halves(o, lo, ldx, n, l);
+        const float *d = diag + (size_t)T.az * (kTall ? cols : s.M);
+        float dr = 0.f;
+        if (!kTall && o.lane < o.rows) dr = d[o.m - T.az * s.M + o.lane];
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            const float w = x[i] + l[i], dd = kTall ? (n + i < cols ? d[n + i] : 0.f) : dr;
+            x[i] = fmaf(a, w, fmaf(dd, full ? w : x[i], v[i] * kDown));
+        }
+        if (out) {
+#pragma unroll
+            for (int i = 0; i < W; ++i) x[i] *= scale;
+            dense::put32_as(out_dtype, o, by_map && o.rows >= 32 ? &tout : nullptr, out, cols, n, cols, cols % 4 == 0, add, x);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < W; ++i) l[i] = x[i] - __half2float(__float2half_rn(x[i]));
+        put_halves(o, &thi, hi_next, ldx, n, x);
+        put_halves(o, &tlo, lo, ldx, n, l);
+    }
+};
+
+int width(int n) { return n >= 256 ? 256 : n <= 64 ? 64 : (n + 31) / 32 * 32; }
+
+template <bool kTall> cudaError_t steps(const Ortho &P, const OrthoParts &W, cudaStream_t s) {
+    const int m = kTall ? P.cols : P.rows, n = kTall ? P.rows : P.cols, sms = device_sm_count();
+    uint8_t *hi[2] = {P.ws + W.hi[0], P.ws + W.hi[1]}, *lo = P.ws + W.lo, *A = P.ws + W.a, *B = P.ws + W.b;
+    float *diag = reinterpret_cast<float *>(P.ws + W.diag);
+    const size_t xs = (size_t)P.rows * W.ldx, ss = (size_t)m * W.ldm;
+    const int wide = width(m), step_wide = width(P.cols);
+    cudaError_t e = cudaSuccess;
+    const auto x_map = [&](CUtensorMap *t, int i, int box) {
+        if (e == cudaSuccess) e = stack_map(t, hi[i], P.cols, P.rows, P.count, W.ldx, xs, box);
+    };
+    const auto s_map = [&](CUtensorMap *t, const void *p, int box) {
+        if (e == cudaSuccess) e = stack_map(t, p, m, m, P.count, W.ldm, ss, box);
+    };
+    const auto o_map = [&](CUtensorMap *t, void *p, int rows, int ld) {
+        if (e == cudaSuccess) e = dense::store_map(t, p, 2, rows, ld);
+    };
+    GramJob<kTall> G = {};
+    SquareJob Q = {};
+    StepJob<kTall> S = {};
+    G.s.set(1, wide, P.count, m, m, n);
+    o_map(&G.to, A, P.count * m, W.ldm);
+    G.a = A;
+    G.ldm = W.ldm;
+    Q.s.set(1, wide, P.count, m, m, m);
+    s_map(&Q.ta, A, kBM);
+    s_map(&Q.tb, A, wide);
+    o_map(&Q.to, B, P.count * m, W.ldm);
+    Q.a = A, Q.out = B, Q.diag = diag, Q.ldm = W.ldm, Q.b = P.b, Q.c = P.c;
+    S.s.set(1, step_wide, P.count, P.rows, P.cols, m);
+    s_map(kTall ? &S.tb : &S.ta, B, kTall ? step_wide : kBM);
+    o_map(&S.tlo, lo, P.count * P.rows, W.ldx);
+    S.lo = lo, S.diag = diag, S.ldx = W.ldx, S.cols = P.cols, S.a = P.a;
+    S.out_dtype = P.out_dtype, S.add = P.add, S.scale = P.scale * kDown;
+    const size_t size = dense::type_size(P.out_dtype);
+    S.by_map = !P.add && (size_t)P.cols * size % 16 == 0;
+    if (S.by_map && e == cudaSuccess) e = dense::store_map(&S.tout, P.out, (int)size, P.count * P.rows, P.cols);
+    CUtensorMap ga[2], gb[2], sx[2], st[2];
+    for (int i = 0; i < 2; ++i) {
+        x_map(&ga[i], i, kTall ? 64 : kBM);
+        x_map(&gb[i], i, kTall ? 64 : wide);
+        x_map(&sx[i], i, kTall ? kBM : 64);
+        o_map(&st[i], hi[i], P.count * P.rows, W.ldx);
+    }
+    for (int i = 0; i < P.steps && e == cudaSuccess; ++i) {
+        const int from = i & 1;
+        TileArgs T = {};
+        T.BN = wide;
+        G.ta = ga[from], G.tb = gb[from];
+        e = launch_tiles_as<1>(T, G, false, 0, (long long)P.count * G.s.tm * G.s.tn, sms, s);
+        if (e == cudaSuccess) e = launch_tiles_as<1>(T, Q, false, 0, (long long)P.count * Q.s.tm * Q.s.tn, sms, s);
+        if (e != cudaSuccess) break;
+        T.BN = step_wide;
+        (kTall ? S.ta : S.tb) = sx[from];
+        S.thi = st[from ^ 1];
+        S.hi = hi[from], S.hi_next = hi[from ^ 1];
+        S.full = i + 2 >= P.steps;
+        S.out = i + 1 == P.steps ? P.out : nullptr;
+        e = launch_tiles_as<1>(T, S, false, 0, (long long)P.count * S.s.tm * S.s.tn, sms, s);
+    }
+    return e;
+}
+
+} // namespace
+
+cudaError_t launch_ortho(const Ortho &P, cudaStream_t s) {
+    const OrthoParts W = ortho_parts(P.count, P.rows, P.cols);
+    float *sums = reinterpret_cast<float *>(P.ws + W.sums);
+    cudaError_t e = launch_behind(squares_kernel, dim3(kOrthoParts, P.count), dim3(kFlat), 0, s, P.g, P.g_dtype,
+                                  (int64_t)P.rows * P.cols, sums);
+    if (e != cudaSuccess) return e;
+    const int64_t blocks = ((int64_t)P.rows * W.ldx + 4 * kFlat - 1) / (4 * kFlat), most = 8 * device_sm_count();
+    e = launch_behind(start_kernel, dim3((unsigned)(blocks < most ? blocks : most), P.count), dim3(kFlat), 0, s, P.g, P.g_dtype, P.rows,
+                      P.cols, W.ldx, sums, reinterpret_cast<__half *>(P.ws + W.hi[0]), reinterpret_cast<__half *>(P.ws + W.lo));
+    if (e != cudaSuccess) return e;
+    return P.rows > P.cols ? steps<true>(P, W, s) : steps<false>(P, W, s);
+}
+cudaError_t ortho_timeout(uint32_t *out) { return dense::read_and_clear_timeout(out); }
+
+} // namespace train
+} // namespace wm

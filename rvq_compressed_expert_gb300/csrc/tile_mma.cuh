@@ -1,0 +1,353 @@
+// The tensor-core product of the training operators: tiles of D = A B^T in fp32 on tcgen05.mma, where a job says
+// which tiles there are, where a tile's operands lie and what becomes of its sums.  Built from dense_gemm.cuh's parts.
+//
+// A persistent grid, one CTA per SM: one warp moves 128-byte-wide pieces of A and B (64 16-bit values of k) into a
+// ring of shared-memory stages by TMA, one issues the MMAs on full stages into one of two TMEM accumulators, eight
+// take the other one out through the job's epilogue.  Operands are three-dimensional maps (matrix, row, column), so
+// that a matrix of a stack ends where it ends; parts past its ends arrive as zeros.
+//
+// A job J (a kernel argument, with its tensor maps ta and tb) has
+//   kAmn, kBmn   operands that lie with m (or n) contiguous (MN-major) rather than k
+//   kMask        tiles whose k ends inside a piece that holds other values: those are cleared in shared memory
+//   begin(smem)  by all threads, once what the kernel before wrote is visible; smem: P.job_bytes of its own
+//   tiles(smem), spot(smem, t): how many, and which
+//   tile<W>(out, spot, n, v): W sums of 32 rows from column n on (lane = row, all lanes together)
+// Waits are bounded, as dense_gemm.cuh's.
+#pragma once
+
+#include "dense_gemm.cuh"
+#include "train.cuh"
+
+namespace wm {
+namespace train {
+
+using dense::all;
+using dense::kBarBytes;
+using dense::kBM;
+using dense::kMaxStages;
+using dense::kPieceBytes;
+using dense::kRowBytes;
+using dense::kSmemBudget;
+using dense::kTmemCols;
+using dense::Out32;
+constexpr int kTileThreads = dense::kThreads;
+
+struct Spot {
+    int am, az, bm, bz; // A's and B's first row (m, n) and matrix
+    int ak, bk;         // their first k
+    int pieces, left;   // pieces of k; how many k of the last one count (kMask)
+    int m, n, rows;     // place in the result: first row, first column, rows that are the tile's
+};
+struct TileArgs {
+    int BN, stages;
+    uint32_t idesc, smem, job_bytes;
+};
+
+// One box of one matrix of a stack; the second form from either CTA of a pair, its bytes counting on an mbarrier of
+// either (a shared::cluster address).
+__device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap *m, int x, int y, int z, uint32_t mbar) {
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+                 "[%2];" ::"r"(dst),
+                 "l"(m), "r"(mbar), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_load3_pair(uint32_t dst, const CUtensorMap *m, int x, int y, int z, uint32_t mbar) {
+    asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+                 "[%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+                 "l"(m), "r"(mbar), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+
+// Bytes of a stage in one CTA of cg.
+inline uint32_t tile_stage(int BN, int cg, bool b_mn) { return dense::stage_size(BN, cg, b_mn, false); }
+
+template <int kCG, class J>
+__global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_constant__ TileArgs P, const __grid_constant__ J job) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[]; // stages, pieces on their way out, the job's, barriers
+    const uint32_t base = tc::smem_u32(smem_raw);
+    const uint32_t bars_at = P.smem - kBarBytes;
+    const uint32_t bars = base + bars_at;
+    const uint32_t bar_full = bars, bar_empty = bars + 64, bar_accf = bars + 128, bar_acce = bars + 144;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem_raw + bars_at + 160);
+    volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem_raw + bars_at + 164);
+    const uint32_t drain = bars + 168;
+
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    const int BN = P.BN;
+    constexpr uint32_t a_bytes = kBM * kRowBytes;
+    const uint32_t b_bytes = dense::stage_b_bytes(BN, kCG, J::kBmn);
+    const uint32_t stage_bytes = dense::stage_size(BN, kCG, J::kBmn, false);
+    const int rank = kCG == 2 ? (int)(blockIdx.x & 1) : 0;
+    const bool leads = kCG == 1 || rank == 0;
+    uint8_t *turns = smem_raw + P.stages * stage_bytes, *mine = turns + 8 * 2 * kPieceBytes;
+
+    if (tid == 32) {
+        for (int i = 0; i < P.stages; ++i) {
+            tc::mbar_init(bar_full + 8 * i, 1);
+            tc::mbar_init(bar_empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(bar_accf + 8 * i, 1);
+            tc::mbar_init(bar_acce + 8 * i, 8 * kCG);
+        }
+        tc::mbar_init(drain, 1);
+        *abort_flag = 0;
+        tc::mbar_init_fence();
+    }
+    if (warp == 2) {
+        if (kCG == 2)
+            tc::tmem_alloc_pair(tc::smem_u32(tmem_slot), kTmemCols);
+        else
+            tc::tmem_alloc(tc::smem_u32(tmem_slot), kTmemCols);
+    }
+    tc::grid_wait_release();
+    job.begin(mine);
+    tc::fence_before_sync();
+    __syncthreads();
+    if (kCG == 2) tc::cluster_sync(); // the other CTA's barriers are up
+    tc::fence_after_sync();
+    constexpr uint32_t tmem = 0; // all columns are this CTA's, so they start at the first
+    if (*tmem_slot != tmem && tid == 0) *abort_flag = 1;
+
+    const int tiles = job.tiles(mine), tile0 = (int)blockIdx.x / kCG, step = (int)gridDim.x / kCG;
+
+    if (warp == 0) {
+        // ---- loader (the warp walks the loop, an elected lane issues)
+        int st = 0, issued = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        const uint32_t full0 = kCG == 2 ? tc::map_rank(bar_full, 0) : bar_full;
+        for (int t = tile0; t < tiles && ok; t += step) {
+            const Spot T = job.spot(mine, t);
+            const int am = T.am + rank * kBM, bm = T.bm + (kCG == 2 ? rank * (BN / 2) : 0);
+            for (int kb = 0; kb < T.pieces; ++kb) {
+                if (!all(tc::mbar_wait(bar_empty + 8 * st, ph ^ 1))) {
+                    ok = false;
+                    break;
+                }
+                if (tc::elect_one()) {
+                    const uint32_t sa = base + st * stage_bytes, sb = sa + a_bytes, full = full0 + 8 * st;
+                    if (leads) tc::mbar_arrive_expect_tx(bar_full + 8 * st, kCG * (a_bytes + b_bytes));
+                    const auto load = [&](uint32_t dst, const CUtensorMap *m, int x, int y, int z) {
+                        if (kCG == 2)
+                            tma_load3_pair(dst, m, x, y, z, full);
+                        else
+                            tma_load3(dst, m, x, y, z, full);
+                    };
+                    const int ka = T.ak + kb * 64, kk = T.bk + kb * 64;
+                    if (J::kAmn) {
+                        for (int i = 0; i < kBM / 64; ++i) load(sa + i * 8192, &job.ta, am + 64 * i, ka, T.az);
+                    } else {
+                        load(sa, &job.ta, ka, am, T.az);
+                    }
+                    if (J::kBmn) {
+                        for (uint32_t i = 0; i * 8192 < b_bytes; ++i) load(sb + i * 8192, &job.tb, bm + 64 * i, kk, T.bz);
+                    } else {
+                        load(sb, &job.tb, kk, bm, T.bz);
+                    }
+                }
+                __syncwarp();
+                ++issued;
+                if (++st == P.stages) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+        }
+        if (!ok) { // copies in flight land before the CTA goes
+            if (lane == 0) *abort_flag = 1;
+            const int n = min(issued, P.stages);
+            for (int i = 0; i < n && leads; ++i) {
+                const int j = issued - n + i;
+                tc::mbar_wait(bar_full + 8 * (j % P.stages), (j / P.stages) & 1);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (leads) {
+            // ---- MMA issuer
+            const auto commit = [](uint32_t bar) {
+                if (kCG == 2)
+                    tc::mma_commit_pair(bar);
+                else
+                    tc::mma_commit(bar);
+            };
+            int st = 0, it = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            const uint64_t desc0 = tc::desc_sw128(base, 8192);
+            for (int t = tile0; t < tiles && ok; t += step) {
+                const Spot T = job.spot(mine, t);
+                if (T.pieces == 0) continue;
+                const int buf = it & 1, use = it >> 1;
+                ++it;
+                if (!all(tc::mbar_wait(bar_acce + 8 * buf, (use & 1) ^ 1))) {
+                    ok = false;
+                    break;
+                }
+                tc::fence_after_sync();
+                const uint32_t d = tmem + buf * 256;
+                for (int kb = 0; kb < T.pieces; ++kb) {
+                    if (!all(tc::mbar_wait(bar_full + 8 * st, ph))) {
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after_sync();
+                    const uint64_t da = desc0 + (uint64_t)((st * stage_bytes) >> 4), db = da + (uint64_t)(a_bytes >> 4);
+                    int steps = 4;
+                    if (J::kMask && kb + 1 == T.pieces && T.left < 64) {
+                        // rows of k behind the tile's last, up to the MMA's 16: zeros (others' values, a NaN
+                        // among them maybe, must not meet zeros of the other operand)
+                        static_assert(!J::kMask || (kCG == 1 && J::kAmn && J::kBmn), "a row of a stage is one k");
+                        steps = (T.left + 15) >> 4;
+                        const int first = T.left, n = 16 * steps - first, slabs = (int)((a_bytes + b_bytes) >> 13);
+                        for (int i = lane; i < n * 8 * slabs; i += 32) {
+                            const int s = i / (n * 8), j = i - s * n * 8;
+                            *reinterpret_cast<uint4 *>(smem_raw + st * stage_bytes + s * 8192 + first * 128 + j * 16) = uint4{};
+                        }
+                        tc::fence_proxy_async();
+                        __syncwarp();
+                    }
+                    if (tc::elect_one()) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            if (J::kMask && j >= steps) break;
+                            const uint64_t dj = da + (uint64_t)(j * ((J::kAmn ? 2048 : 32) >> 4));
+                            const uint64_t ej = db + (uint64_t)(j * ((J::kBmn ? 2048 : 32) >> 4));
+                            if (kCG == 2)
+                                tc::mma_f16_pair(d, dj, ej, P.idesc, j > 0 || kb > 0);
+                            else
+                                tc::mma_f16(d, dj, ej, P.idesc, j > 0 || kb > 0);
+                        }
+                        commit(bar_empty + 8 * st);
+                        if (kb + 1 == T.pieces) commit(bar_accf + 8 * buf);
+                    }
+                    __syncwarp();
+                    if (++st == P.stages) {
+                        st = 0;
+                        ph ^= 1;
+                    }
+                }
+            }
+            if (!ok) {
+                if (lane == 0) *abort_flag = 1;
+                if (tc::elect_one()) commit(drain);
+                tc::mbar_wait(drain, 0);
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 3) {
+        // ---- epilogue: two warps for each quarter of the lanes (rows); they take its pieces of 32 columns in turn
+        const int q = warp & 3, half = (warp - 3) >> 2;
+        Out32 out{reinterpret_cast<uint4 *>(turns) + (warp - 3) * (2 * kPieceBytes / 16), 0, 0, lane, 0};
+        int it = 0;
+        for (int t = tile0; t < tiles; t += step) {
+            Spot T = job.spot(mine, t);
+            T.m += rank * kBM;
+            T.rows -= rank * kBM;
+            const bool any = 32 * q < T.rows, empty = T.pieces == 0;
+            out.m = T.m + 32 * q;
+            out.rows = T.rows - 32 * q;
+            const int buf = it & 1, use = it >> 1;
+            if (!empty) {
+                ++it;
+                bool ok = true;
+                if (lane == 0) ok = dense::wait_tile(bar_accf + 8 * buf, use & 1, T.pieces);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) {
+                    *abort_flag = 1;
+                    break;
+                }
+                tc::fence_after_sync();
+            }
+            const uint32_t src = tmem + buf * 256 + ((uint32_t)(32 * q) << 16);
+            if (any) {
+                const auto take = [&](auto width, int c) {
+                    constexpr int W = decltype(width)::value;
+                    alignas(16) uint32_t v[W];
+                    if (empty) {
+#pragma unroll
+                        for (int i = 0; i < W; ++i) v[i] = 0;
+                    } else if constexpr (W == 32) {
+                        tc::tmem_ld32(src + c, v);
+                        tc::tmem_wait_ld(v);
+                    } else {
+                        tc::tmem_ld16n(src + c, v);
+                        tc::tmem_wait_ld(v);
+                    }
+                    job.template tile<W>(out, T, T.n + c, *reinterpret_cast<const float(*)[W]>(v));
+                };
+                for (int c = 32 * half; c < BN; c += 64) {
+                    if (c + 32 <= BN)
+                        take(std::integral_constant<int, 32>(), c);
+                    else
+                        take(std::integral_constant<int, 16>(), c);
+                }
+            }
+            if (!empty) {
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    if (leads)
+                        tc::mbar_arrive(bar_acce + 8 * buf);
+                    else
+                        tc::mbar_arrive_cluster(tc::map_rank(bar_acce + 8 * buf, 0));
+                }
+            }
+        }
+        if (lane == 0) {
+            tc::close_stores();
+            tc::stores_done();
+        }
+        __syncwarp();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (kCG == 2) tc::cluster_sync(); // no CTA leaves while its memory takes part in the other's MMAs or barriers
+    tc::fence_after_sync();
+    if (tid == 0 && *abort_flag) atomicOr(&dense::g_dense_timeout, 1u);
+    if (warp == 2) {
+        if (kCG == 2)
+            tc::tmem_dealloc_pair(tmem, kTmemCols);
+        else
+            tc::tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// A map over `mats` matrices of rows x cols 16-bit values, ld values from row to row and `step` from matrix to
+// matrix: boxes of box_rows rows x 64 values of one of them, 128-byte swizzle, zeros past its ends.
+cudaError_t stack_map(CUtensorMap *m, const void *p, int cols, int rows, int mats, size_t ld, size_t step, int box_rows);
+
+// Fills in the rest of P (BN set) and launches: at most `tiles` tiles (an upper bound).
+template <int kCG, class J>
+cudaError_t launch_tiles_as(TileArgs &P, const J &job, bool bf16, size_t job_bytes, long long tiles, int sms, cudaStream_t s) {
+    static SmemAttr attr;
+    const auto kernel = tile_kernel<kCG, J>;
+    const uint32_t stage = tile_stage(P.BN, kCG, J::kBmn), turn = 8 * 2 * kPieceBytes;
+    P.job_bytes = (uint32_t)round_up(job_bytes, 16);
+    P.stages = (int)((kSmemBudget - kBarBytes - turn - P.job_bytes) / stage);
+    if (P.stages > kMaxStages) P.stages = kMaxStages;
+    if (P.stages < 2) return cudaErrorInvalidValue;
+    P.smem = P.stages * stage + turn + P.job_bytes + kBarBytes;
+    P.idesc = tc::idesc_half(kBM * kCG, P.BN, bf16, J::kAmn, J::kBmn);
+    cudaError_t e = ensure_smem(attr, reinterpret_cast<const void *>(kernel), (int)P.smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = kCG;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    const int most = sms / kCG;
+    cfg.gridDim = dim3((tiles < most ? (int)tiles : most) * kCG);
+    cfg.blockDim = dim3(kTileThreads);
+    cfg.dynamicSmemBytes = P.smem;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = kCG == 2 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P, job);
+}
+
+} // namespace train
+} // namespace wm

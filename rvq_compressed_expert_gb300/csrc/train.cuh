@@ -1,0 +1,107 @@
+// Internal declarations of the training operators (waste_train.h).
+#pragma once
+
+#include "dense.cuh"
+#include "dense_tc.cuh"
+#include "waste_train.h"
+
+namespace wm {
+namespace train {
+
+// Rows of memory, ld elements apart.
+struct Rows {
+    void *p;
+    int64_t ld;
+};
+struct NormFwd {
+    int d, T, x_dtype, y_dtype, w_dtype;
+    float eps;
+    const void *w, *b; // or null
+    Rows x, y;
+    float *mean, *rstd; // or null
+};
+struct NormBwd {
+    int d, T, x_dtype, y_dtype, w_dtype, grad_dtype, accumulate;
+    const void *w; // or null
+    Rows x, dy, dx; // dx.p may be null
+    const float *mean, *rstd;
+    void *dw, *db; // or null
+    float *parts;  // workspace: [norm_parts][2][d]
+};
+// Partial sums of dw and db: so many rows of them at most.
+constexpr int kNormParts = 304;
+inline size_t norm_bytes(int d, int T) { return round_up((size_t)(T < kNormParts ? T : kNormParts) * 2 * d * 4, 256); }
+
+struct Group {
+    int E, k, n, dtype, rows;
+    const int32_t *offsets;
+};
+// y = x W^T by expert, dx = dy W, dW = dy^T x.
+cudaError_t launch_group_forward(const Group &G, const void *x, const void *w, void *y, int out_dtype, int add, cudaStream_t s);
+cudaError_t launch_group_dx(const Group &G, const void *dy, const void *w, void *dx, cudaStream_t s);
+cudaError_t launch_group_dw(const Group &G, const void *dy, const void *x, void *dw, int grad_dtype, int add, cudaStream_t s);
+// *timeout |= whether a wait gave up, *offsets |= whether offsets were out of order, since the last call (cleared).
+cudaError_t group_status(uint32_t *timeout, uint32_t *offsets);
+
+// Newton-Schulz: the matrices of a call and its workspace.
+struct Ortho {
+    int count, rows, cols, steps;
+    float a, b, c;
+    const void *g;
+    int g_dtype;
+    void *out;
+    int out_dtype, add;
+    float scale;
+    uint8_t *ws;
+};
+// What stands in the workspace, from its start: X in two halves (the first of them twice, taken in turn), A and
+// b A + c A^2 without its diagonal, that diagonal, and partial sums of squares.
+constexpr int kOrthoParts = 128; // of a matrix
+struct OrthoParts {
+    size_t hi[2], lo, a, b, diag, sums, total;
+    int ldx, ldm;
+};
+inline OrthoParts ortho_parts(int count, int rows, int cols) {
+    const int m = rows < cols ? rows : cols;
+    OrthoParts p;
+    p.ldx = (cols + 7) / 8 * 8;
+    p.ldm = (m + 7) / 8 * 8;
+    size_t at = 0;
+    const auto take = [&](size_t bytes) {
+        const size_t o = at;
+        at += round_up(bytes, 256);
+        return o;
+    };
+    const size_t x = (size_t)count * rows * p.ldx * 2, s = (size_t)count * m * p.ldm * 2;
+    p.hi[0] = take(x), p.hi[1] = take(x), p.lo = take(x);
+    p.a = take(s), p.b = take(s);
+    p.diag = take((size_t)count * m * 4);
+    p.sums = take((size_t)count * kOrthoParts * 3 * 4);
+    p.total = at;
+    return p;
+}
+cudaError_t launch_ortho(const Ortho &P, cudaStream_t s);
+cudaError_t ortho_timeout(uint32_t *out);
+
+cudaError_t launch_norm_forward(const NormFwd &P, cudaStream_t s);
+cudaError_t launch_norm_backward(const NormBwd &P, cudaStream_t s);
+
+// A launch that may begin while the kernel before it in the stream ends; the kernel waits for that one itself
+// (tc::grid_wait_release) before it touches memory.
+template <class... P, class... A>
+cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A &&...args) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
+} // namespace train
+} // namespace wm
