@@ -235,8 +235,8 @@ int waste_group_backward(const waste_group_config *cfg, const void *d_dy, const 
     if (!d_dx && !d_dw) return ok();
     if ((rc = check_ptrs(p, n, d_dx ? 3 : 1))) return rc;
     const Span spans[] = {{d_dx, (size_t)rows * cfg->k * 2, "dx"}, {d_dw, wn * type_size(grad_dtype), "dw"},
-                          {d_dy, (size_t)rows * cfg->n * 2, "dy"}, {d_dw ? d_x : nullptr, (size_t)rows * cfg->k * 2, "x"},
-                          {d_dx ? d_w : nullptr, wn * 2, "w"}, {d_offsets, (size_t)(E + 1) * 4, "offsets"}};
+                          {d_dy, (size_t)rows * cfg->n * 2, "dy"}, {d_x, (size_t)rows * cfg->k * 2, "x"},
+                          {d_w, wn * 2, "w"}, {d_offsets, (size_t)(E + 1) * 4, "offsets"}};
     if ((rc = check_apart(spans, 2, 6))) return rc;
     const Group G{E, cfg->k, cfg->n, cfg->dtype, rows, d_offsets};
     cudaError_t e = d_dx ? launch_group_dx(G, d_dy, d_w, d_dx, s) : cudaSuccess;
