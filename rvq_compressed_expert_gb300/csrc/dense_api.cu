@@ -96,6 +96,7 @@ int waste_dense_status(void) {
     if (e == cudaSuccess) e = mx4_timeout(&timeout);
     if (e == cudaSuccess) e = train::group_status(&timeout, &offsets);
     if (e == cudaSuccess) e = train::ortho_timeout(&timeout);
+    if (e == cudaSuccess) e = train::norm_timeout(&timeout);
     if (e != cudaSuccess) return done(e, "reading the status");
     if (timeout) return fail(WASTE_ETIMEOUT, "a device wait of a dense operator gave up");
     if (offsets) return fail(WASTE_EINVAL, "offsets of a product grouped by expert fall or leave the rows");

@@ -10,6 +10,8 @@ namespace {
 
 constexpr int kThreads = 512;
 
+__device__ uint32_t g_norm_timeout;
+
 template <class T> __device__ __forceinline__ float widen(T v) { return (float)v; }
 template <class T> __device__ __forceinline__ T round_to(float v);
 template <> __device__ __forceinline__ float round_to<float>(float v) { return v; }
@@ -23,55 +25,79 @@ template <class T, int V> struct alignas(V == 8 ? 16 : sizeof(T)) Piece {
 template <class T, int V> __device__ __forceinline__ Piece<T, V> load(const T *p) {
     return *reinterpret_cast<const Piece<T, V> *>(p);
 }
-// Sum over the warps of a group (gw of them, group `g` of the CTA), in every thread.  slot alternates between
-// two halves of part, so one barrier a sum is enough.
+// All warps of group g, 16 groups at most.
+__device__ __forceinline__ void group_meet(int gw, int g) {
+    if (gw == 1)
+        __syncwarp();
+    else
+        asm volatile("bar.sync %0, %1;" ::"r"(g), "r"(gw * 32) : "memory");
+}
+
+// Sum over the warps of a group (gw of them, 16 at most; group `g` of the CTA), in every thread.  slot alternates
+// between two halves of part (32 floats each), so one barrier a sum is enough.
 __device__ __forceinline__ float group_sum(float v, int gw, int g, float *part, int &slot) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     if (gw == 1) return v;
     const int lane = threadIdx.x & 31, warp = (int)(threadIdx.x >> 5) - g * gw;
-    float *p = part + slot * 16 + g * gw;
-    slot ^= 1;
-    if (lane == 0) p[warp] = v;
-    asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "r"(gw * 32) : "memory");
-    v = lane < gw ? p[lane] : 0.f;
-#pragma unroll
-    for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return __shfl_sync(0xffffffffu, v, 0);
-}
-
-// Two sums at once; part: 64 floats.
-__device__ __forceinline__ void group_sum2(float &a, float &b, int gw, int g, float *part, int &slot) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        a += __shfl_xor_sync(0xffffffffu, a, o);
-        b += __shfl_xor_sync(0xffffffffu, b, o);
-    }
-    if (gw == 1) return;
-    const int lane = threadIdx.x & 31, warp = (int)(threadIdx.x >> 5) - g * gw;
     float *p = part + slot * 32 + g * gw;
     slot ^= 1;
-    if (lane == 0) p[warp] = a, p[16 + warp] = b;
-    asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "r"(gw * 32) : "memory");
-    a = lane < gw ? p[lane] : 0.f;
-    b = lane < gw ? p[16 + lane] : 0.f;
+    if (lane == 0) p[warp] = v;
+    group_meet(gw, g);
+    v = (lane & 15) < gw ? p[lane & 15] : 0.f;
 #pragma unroll
-    for (int o = 8; o; o >>= 1) {
-        a += __shfl_xor_sync(0xffffffffu, a, o);
-        b += __shfl_xor_sync(0xffffffffu, b, o);
-    }
-    a = __shfl_sync(0xffffffffu, a, 0);
-    b = __shfl_sync(0xffffffffu, b, 0);
+    for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
 }
 
-// The kernels that read a row once hold it in registers: so many values a lane, of rows up to kHeldMost.  The work is
-// bound by the instructions per value before memory is (29 of them took 126 us for 16384 x 7168 bf16, where memory
-// needs 70), so values are held and computed in pairs (one instruction for both), a reduction is spread over many
-// values a lane, and rows that fill all lanes go without masks.
-constexpr int kFwdHeld = 32, kFwdThreads = 256;
-constexpr int kBwdHeld = 16, kBwdThreads = 512;
-constexpr int kHeldMost = 8192;
-static_assert(kFwdHeld * kFwdThreads == kHeldMost && kBwdHeld * kBwdThreads == kHeldMost, "one row a CTA at most");
+// n sums at once (1, 2 or 4), in every thread; part: 64 n floats.  The lanes share the values out between them in the first
+// steps, so that 2 sums take 5 + 4 exchanges instead of 18, and 4 take 6 + 3 instead of 36.
+template <int n> __device__ __forceinline__ void group_sums(float (&v)[n], int gw, int g, float *part, int &slot) {
+    static_assert(n == 1 || n == 2 || n == 4, "a warp, its halves or quarters");
+    if constexpr (n == 1) {
+        v[0] = group_sum(v[0], gw, g, part, slot);
+        return;
+    }
+    constexpr int kLanes = 32 / n;
+    const int lane = threadIdx.x & 31, warp = (int)(threadIdx.x >> 5) - g * gw, mine = lane / kLanes;
+    float k = 0.f;
+    if constexpr (n == 2) {
+        const bool up = lane & 16;
+        k = (up ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, up ? v[0] : v[1], 16);
+    } else if constexpr (n == 4) {
+        const bool up = lane & 16, odd = lane & 8;
+        const float a = (up ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 16);
+        const float b = (up ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, up ? v[1] : v[3], 16);
+        k = (odd ? b : a) + __shfl_xor_sync(0xffffffffu, odd ? a : b, 8);
+    }
+#pragma unroll
+    for (int o = kLanes / 2; o; o >>= 1) k += __shfl_xor_sync(0xffffffffu, k, o);
+    if (gw > 1) {
+        float *p = part + slot * 32 * n + mine * 32 + g * gw;
+        slot ^= 1;
+        const int i = lane % kLanes;
+        if (i == 0) p[warp] = k;
+        group_meet(gw, g);
+        k = i < gw ? p[i] : 0.f;
+        if (kLanes < 16 && i + kLanes < gw) k += p[i + kLanes];
+#pragma unroll
+        for (int o = kLanes / 2; o; o >>= 1) k += __shfl_xor_sync(0xffffffffu, k, o);
+    }
+#pragma unroll
+    for (int j = 0; j < n; ++j) v[j] = __shfl_sync(0xffffffffu, k, j * kLanes);
+}
+
+// The kernels that read a row once hold it in registers, kHeld values a lane, for rows of up to kHeldMost.  They are
+// bound by instructions, by shared memory's pipe (reads and the lanes' exchanges) and by the chain of steps of a row
+// before they are bound by memory, so: a group of warps works on several rows at once, which share their reads of w and
+// b (in shared memory, in fp32) and their exchanges; values are held and computed in pairs; rows that fill all lanes
+// go without masks; and rows come by bulk copies, one instruction each.
+constexpr int kHeld = 16;
+template <int V> constexpr int rows_at_once() { return V == 8 ? 2 : 1; }
+constexpr int kHeldThreads = 512;
+constexpr int kHeldMost = kHeld * kHeldThreads;
+constexpr int kHeldSmem = 220 << 10;
+constexpr int kDeepMost = 8;
 
 // Two values at a time.
 __device__ __forceinline__ uint64_t bits(float2 v) { return *reinterpret_cast<uint64_t *>(&v); }
@@ -102,87 +128,13 @@ __device__ __forceinline__ void round2(float *p, float2 v) { p[0] = v.x, p[1] = 
 __device__ __forceinline__ void round2(__nv_bfloat16 *p, float2 v) { *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(v.x, v.y); }
 __device__ __forceinline__ void round2(__half *p, float2 v) { *reinterpret_cast<__half2 *>(p) = __floats2half2_rn(v.x, v.y); }
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void close_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void copies_left() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-// A lane's H values of a row, in H / V pieces a group's width apart.  Whole pieces come through shared memory, each
-// lane's own (asynchronous copies need no registers while they are on their way, and no barrier: nobody else
-// reads them); single values straight from memory.  kFull: the row fills all lanes.
-template <class X, int V, int H, bool kFull> struct Lane {
-    static constexpr int kPieces = H / V, kParts = V == 8 ? V * (int)sizeof(X) / 16 : 0;
-    static constexpr uint32_t kSlot = kPieces * kParts * 16; // bytes a lane and row
-    int t, gt, d;
-    uint32_t ring, wide; // this lane's, and 16 bytes for every thread of the CTA
-    __device__ Lane(int t_, int gt_, int d_, uint32_t smem) : t(t_), gt(gt_), d(d_), ring(smem + threadIdx.x * 16), wide(blockDim.x * 16) {}
-    __device__ __forceinline__ int column(int i) const { return (i * gt + t) * V; }
-    __device__ __forceinline__ bool in(int i) const { return kFull || column(i) < d; }
-    __device__ __forceinline__ void ask(const X *row, int slot) const {
-        if constexpr (V == 8) {
-#pragma unroll
-            for (int i = 0; i < kPieces; ++i)
-                if (in(i))
-#pragma unroll
-                    for (int j = 0; j < kParts; ++j)
-                        copy16(ring + ((slot * kPieces + i) * kParts + j) * wide,
-                               reinterpret_cast<const char *>(row + column(i)) + 16 * j);
-        }
-    }
-    // zeros past the row's end
-    __device__ __forceinline__ void take(const X *row, int slot, float2 (&x)[H / 2]) const {
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            if constexpr (V == 8) {
-                Piece<X, V> q;
-#pragma unroll
-                for (int j = 0; j < kParts; ++j) {
-                    uint4 u = {};
-                    if (in(i))
-                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
-                                     : "r"(ring + ((slot * kPieces + i) * kParts + j) * wide)
-                                     : "memory");
-                    reinterpret_cast<uint4 *>(&q)[j] = u;
-                }
-#pragma unroll
-                for (int k = 0; k < V / 2; ++k) x[V / 2 * i + k] = widen2(&q.v[2 * k]);
-            } else {
-                const float v = in(i) ? widen(row[column(i)]) : 0.f;
-                if (i & 1)
-                    x[i / 2].y = v;
-                else
-                    x[i / 2].x = v;
-            }
-        }
-    }
-    // rounded to their places
-    template <class Y> __device__ __forceinline__ void give(Y *row, const float2 (&y)[H / 2]) const {
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            if (!in(i)) continue;
-            if constexpr (V == 8) {
-                Piece<Y, V> o;
-#pragma unroll
-                for (int k = 0; k < V / 2; ++k) round2(&o.v[2 * k], y[V / 2 * i + k]);
-                *reinterpret_cast<Piece<Y, V> *>(row + column(i)) = o;
-            } else {
-                row[column(i)] = round_to<Y>(i & 1 ? y[i / 2].y : y[i / 2].x);
-            }
-        }
-    }
-    // Whether the two values of pair j are the row's.
-    __device__ __forceinline__ bool first(int j) const { return in(2 * j / V); }
-    __device__ __forceinline__ bool second(int j) const { return in((2 * j + 1) / V); }
-};
 // V values of w or b from column c on.
 template <class T, int V> __device__ __forceinline__ void widen_all(const void *p, int c, float (&o)[V]) {
     const Piece<T, V> q = load<T, V>(static_cast<const T *>(p) + c);
 #pragma unroll
     for (int k = 0; k < V; ++k) o[k] = widen(q.v[k]);
 }
-template <int V> __device__ __forceinline__ void params(const void *p, int dtype, int c, float none, float (&o)[V]) {
+template <int V> __device__ __forceinline__ void widen_params(const void *p, int dtype, int c, float none, float (&o)[V]) {
     if (!p) {
 #pragma unroll
         for (int k = 0; k < V; ++k) o[k] = none;
@@ -194,179 +146,387 @@ template <int V> __device__ __forceinline__ void params(const void *p, int dtype
         widen_all<__half>(p, c, o);
     }
 }
-// A lane's values of w or b, `none` past the row's end too.
-template <class T, class L, int H> __device__ __forceinline__ void widen_row(const L &l, const void *p, float none, float2 (&o)[H]) {
-    constexpr int n = L::kPieces, V = 2 * H / n;
+// A lane's values of a row, in kHeld / V pieces a group's width apart: whole pieces from a copy of the row in shared
+// memory, single values straight from memory.  kFull: the row fills all lanes.
+template <class X, int V, bool kFull> struct Lane {
+    static constexpr int H = kHeld, kPieces = H / V;
+    int t, gt, d;
+    __device__ __forceinline__ int column(int i) const { return (i * gt + t) * V; }
+    __device__ __forceinline__ bool in(int i) const { return kFull || column(i) < d; }
+    // zeros past the row's end
+    __device__ __forceinline__ void take(const X *row, float2 (&x)[H / 2]) const {
 #pragma unroll
-    for (int i = 0; i < n; ++i) {
-        if constexpr (V == 8) {
-            if (l.in(i)) {
-                const Piece<T, V> q = load<T, V>(static_cast<const T *>(p) + l.column(i));
+        for (int i = 0; i < kPieces; ++i) {
+            if constexpr (V == 8) {
+                Piece<X, V> q = {};
+                if (in(i)) q = load<X, V>(row + column(i));
 #pragma unroll
-                for (int k = 0; k < V / 2; ++k) o[V / 2 * i + k] = widen2(&q.v[2 * k]);
+                for (int k = 0; k < V / 2; ++k) x[V / 2 * i + k] = widen2(&q.v[2 * k]);
             } else {
-#pragma unroll
-                for (int k = 0; k < V / 2; ++k) o[V / 2 * i + k] = both(none);
+                const float v = in(i) ? widen(row[column(i)]) : 0.f;
+                if (i & 1)
+                    x[i / 2].y = v;
+                else
+                    x[i / 2].x = v;
             }
-        } else {
-            const float v = l.in(i) ? widen(static_cast<const T *>(p)[l.column(i)]) : none;
-            if (i & 1)
-                o[i / 2].y = v;
-            else
-                o[i / 2].x = v;
         }
     }
-}
-template <class L, int H> __device__ __forceinline__ void param_row(const L &l, const void *p, int dtype, float none, float2 (&o)[H]) {
-    if (!p) {
+    // w or b at the same places, `none` past the row's end
+    __device__ __forceinline__ void params(const void *p, int dtype, float none, float2 (&o)[H / 2]) const {
 #pragma unroll
-        for (int k = 0; k < H; ++k) o[k] = both(none);
-    } else if (dtype == WASTE_ACT_F32) {
-        widen_row<float>(l, p, none, o);
-    } else if (dtype == WASTE_ACT_BF16) {
-        widen_row<__nv_bfloat16>(l, p, none, o);
-    } else {
-        widen_row<__half>(l, p, none, o);
+        for (int i = 0; i < kPieces; ++i) {
+            float v[V];
+#pragma unroll
+            for (int k = 0; k < V; ++k) v[k] = none;
+            if (in(i)) widen_params<V>(p, dtype, column(i), none, v);
+#pragma unroll
+            for (int k = 0; k < V; ++k) ((V * i + k) & 1 ? o[(V * i + k) / 2].y : o[(V * i + k) / 2].x) = v[k];
+        }
+    }
+    // Whether the two values of pair j are the row's.
+    __device__ __forceinline__ bool first(int j) const { return in(2 * j / V); }
+    __device__ __forceinline__ bool second(int j) const { return in((2 * j + 1) / V); }
+};
+// w or b, in fp32, into shared memory, by all threads: of every eight the first four in one half and the last four in the
+// other, so that the lanes of a warp, eight columns apart, read neighbouring 16 bytes.
+__device__ __forceinline__ void stage(float *to, const void *p, int dtype, int d, float none) {
+    for (int i = threadIdx.x; i < d; i += blockDim.x) {
+        float v[1];
+        widen_params<1>(p, dtype, i, none, v);
+        to[(i & 4 ? d / 2 : 0) + (i >> 3) * 4 + (i & 3)] = v[0];
+    }
+}
+// Four of them from column c on (a multiple of 4).
+__device__ __forceinline__ void four(const float *p, int d, int c, float2 &a, float2 &b) {
+    const float4 q = *reinterpret_cast<const float4 *>(p + (c & 4 ? d / 2 : 0) + (c >> 3) * 4);
+    a = make_float2(q.x, q.y), b = make_float2(q.z, q.w);
+}
+
+// The rows of one operand on their way to a group of warps: `deep` places in shared memory, filled in order by bulk
+// copies of one thread.  A place is free again once the group has met (in a sum) behind its reading.
+template <class X> struct Ring {
+    const X *p;
+    int64_t ld;
+    uint8_t *at;      // this group's places
+    uint32_t bytes, pitch, bars, deep;
+    __device__ __forceinline__ const X *place(uint32_t i) const { return reinterpret_cast<const X *>(at + i * pitch); }
+    __device__ __forceinline__ void ask(int64_t row, uint32_t i) const { // by one thread
+        const uint32_t bar = bars + 8 * i;
+        tc::mbar_arrive_expect_tx(bar, bytes);
+        tc::bulk_g2s(tc::smem_u32(at + i * pitch), p + row * ld, bytes, bar);
+    }
+};
+// A wait gives up after 1.1 s: then none is waited for any more, and waste_dense_status reports it.
+__device__ __forceinline__ void wait_row(uint32_t bar, uint32_t parity, volatile uint32_t *gave_up) {
+    if (*gave_up) return;
+    if (!tc::mbar_wait(bar, parity)) {
+        *gave_up = 1;
+        atomicOr(&g_norm_timeout, 1u);
     }
 }
 
-// Rows on their way to a CTA whose lanes hold so many bytes of one: as many as shared memory has room for.
-constexpr int deep(uint32_t bytes, uint32_t most) { return bytes * 4 <= most ? 4 : 3; }
-template <class L> constexpr int forward_deep() { return deep(L::kSlot * kFwdThreads, 72 << 10); } // three CTAs an SM, or two
-template <class LX, class LY> constexpr int backward_deep() { return deep((LX::kSlot + LY::kSlot) * kBwdThreads, 200 << 10); }
-
-// One pass: a group holds its row in registers, the next rows are on their way.
-template <class X, class Y, int V, bool kFull>
-__global__ void __launch_bounds__(kFwdThreads, 3) forward_held_kernel(const NormFwd P, int gw) {
-    using L = Lane<X, V, kFwdHeld, kFull>;
-    constexpr int kDeep = forward_deep<L>(), N = kFwdHeld / 2;
+// One pass.  kFew: a row a group, straight from memory, w and b held too, for all loads to be on their way at once;
+// otherwise (V == 8) kRowsAtOnce rows at a time.
+constexpr int kRowsAtOnce = 4;
+template <class X, class Y, int V, bool kFull, bool kFew>
+__global__ void __launch_bounds__(kHeldThreads) forward_held_kernel(const NormFwd P, int gw, int deep) {
+    using L = Lane<X, V, kFull>;
+    constexpr int N = kHeld / 2, R = kFew ? 1 : kRowsAtOnce;
+    static_assert(kFew || V == 8, "copies take whole pieces");
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float part[32];
+    __shared__ float part[64 * R];
+    __shared__ __align__(8) uint64_t bars[kHeldThreads / 32 * kDeepMost];
+    __shared__ uint32_t gave_up;
     tc::grid_wait_release();
     const int gt = gw * 32, g = threadIdx.x / gt, t = threadIdx.x % gt, groups = blockDim.x / gt;
     const float inv = 1.f / (float)P.d;
     const int64_t step = (int64_t)gridDim.x * groups, row0 = (int64_t)blockIdx.x * groups + g;
-    const L lane(t, gt, P.d, tc::smem_u32(smem));
-    const auto x_at = [&](int64_t row) { return static_cast<const X *>(P.x.p) + row * P.x.ld; };
-#pragma unroll
-    for (int i = 0; i < kDeep - 1; ++i) {
-        if (row0 + i * step < P.T) lane.ask(x_at(row0 + i * step), i);
-        close_copies();
-    }
-    int slot = 0, turn = 0;
-    for (int64_t row = row0; row < P.T; row += step) {
-        const int last = turn == 0 ? kDeep - 1 : turn - 1;
-        if (row + (kDeep - 1) * step < P.T) lane.ask(x_at(row + (kDeep - 1) * step), last);
-        close_copies();
-        copies_left<kDeep - 1>();
-        float2 x[N], s = both(0.f);
-        lane.take(x_at(row), turn, x);
-        turn = turn + 1 == kDeep ? 0 : turn + 1;
-#pragma unroll
-        for (int i = 0; i < N; ++i) s = add2(s, x[i]);
-        const float mu = group_sum(s.x + s.y, gw, g, part, slot) * inv;
-        s = both(0.f);
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            x[i] = add2(x[i], both(-mu));
-            if (!kFull && !lane.first(i)) x[i].x = 0.f;
-            if (!kFull && !lane.second(i)) x[i].y = 0.f;
-            s = fma2(x[i], x[i], s);
+    const L lane{t, gt, P.d};
+    const uint32_t bytes = P.d * (uint32_t)sizeof(X);
+    const Ring<X> ring{static_cast<const X *>(P.x.p), P.x.ld, smem + (size_t)g * deep * bytes, bytes, bytes,
+                       tc::smem_u32(bars + g * deep), (uint32_t)deep};
+    float *w = reinterpret_cast<float *>(smem + (size_t)groups * deep * bytes), *b = w + P.d;
+    if constexpr (!kFew) {
+        if (threadIdx.x == 0) gave_up = 0;
+        if (t == 0) {
+            for (int i = 0; i < deep; ++i) tc::mbar_init(ring.bars + 8 * i, 1);
+            tc::mbar_init_fence();
+            for (int i = 0; i < deep && row0 + i * step < P.T; ++i) ring.ask(row0 + i * step, i);
         }
-        const float r = 1.f / sqrtf(group_sum(s.x + s.y, gw, g, part, slot) * inv + P.eps);
-        Y *y = static_cast<Y *>(P.y.p) + row * P.y.ld;
+        stage(w, P.w, P.w_dtype, P.d, 1.f);
+        stage(b, P.b, P.w_dtype, P.d, 0.f);
+        __syncthreads();
+    }
+    int slot = 0;
+    uint32_t turn = 0, phase = 0;
+    for (int64_t row = row0; row < P.T; row += R * step) {
+        // rows of this turn; past the last row the first one takes its place, and is not written again
+        int there = 1;
 #pragma unroll
-        for (int i = 0; i < L::kPieces; ++i) { // w and b piece by piece: they would not fit beside the row
-            if (!lane.in(i)) continue;
-            const int c = lane.column(i);
-            float w[V], b[V];
-            params<V>(P.w, P.w_dtype, c, 1.f, w);
-            params<V>(P.b, P.w_dtype, c, 0.f, b);
-            if constexpr (V == 8) {
-                Piece<Y, V> o;
+        for (int q = 1; q < R; ++q) there += row + q * step < P.T;
+        float2 x[R][N], wv[kFew ? N : 1], bv[kFew ? N : 1];
+        float s[R];
+        uint32_t used[R];
 #pragma unroll
-                for (int k = 0; k < V; k += 2)
-                    round2(&o.v[k], fma2(mul2(x[(V * i + k) / 2], both(r)), make_float2(w[k], w[k + 1]), make_float2(b[k], b[k + 1])));
-                *reinterpret_cast<Piece<Y, V> *>(y + c) = o;
+        for (int q = 0; q < R; ++q) {
+            if constexpr (kFew) {
+                lane.take(ring.p + row * ring.ld, x[q]);
+                lane.params(P.w, P.w_dtype, 1.f, wv);
+                lane.params(P.b, P.w_dtype, 0.f, bv);
             } else {
-                y[c] = round_to<Y>(fmaf((i & 1 ? x[i / 2].y : x[i / 2].x) * r, w[0], b[0]));
+                used[q] = q < there ? turn : used[0];
+                if (q < there) {
+                    wait_row(ring.bars + 8 * turn, phase, &gave_up);
+                    if (++turn == (uint32_t)deep) turn = 0, phase ^= 1;
+                }
+                lane.take(ring.place(used[q]), x[q]);
+            }
+            float2 a = both(0.f);
+#pragma unroll
+            for (int i = 0; i < N; ++i) a = add2(a, x[q][i]);
+            s[q] = a.x + a.y;
+        }
+        group_sums(s, gw, g, part, slot);
+        if constexpr (!kFew)
+            if (t == 0)
+#pragma unroll
+                for (int q = 0; q < R; ++q)
+                    if (row + (q + deep) * step < P.T) ring.ask(row + (q + deep) * step, used[q]);
+        float mu[R];
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            mu[q] = s[q] * inv;
+            float2 a = both(0.f);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                x[q][i] = add2(x[q][i], both(-mu[q]));
+                if (!kFull && !lane.first(i)) x[q][i].x = 0.f;
+                if (!kFull && !lane.second(i)) x[q][i].y = 0.f;
+                a = fma2(x[q][i], x[q][i], a);
+            }
+            s[q] = a.x + a.y;
+        }
+        group_sums(s, gw, g, part, slot);
+        Y *y[R];
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            y[q] = static_cast<Y *>(P.y.p) + (row + q * step) * P.y.ld;
+            s[q] = 1.f / sqrtf(s[q] * inv + P.eps);
+            if (P.mean && t == 0 && q < there) {
+                P.mean[row + q * step] = mu[q];
+                P.rstd[row + q * step] = s[q];
             }
         }
-        if (P.mean && t == 0) {
-            P.mean[row] = mu;
-            P.rstd[row] = r;
+#pragma unroll
+        for (int i = 0; i < L::kPieces; ++i) {
+            if (!lane.in(i)) continue;
+            const int c = lane.column(i);
+            if constexpr (V == 8) {
+                Piece<Y, V> o[R];
+#pragma unroll
+                for (int k = 0; k < V; k += 4) {
+                    const int j = (V * i + k) / 2;
+                    float2 w0, w1, b0, b1;
+                    if constexpr (kFew) {
+                        w0 = wv[j], w1 = wv[j + 1], b0 = bv[j], b1 = bv[j + 1];
+                    } else {
+                        four(w, P.d, c + k, w0, w1);
+                        four(b, P.d, c + k, b0, b1);
+                    }
+#pragma unroll
+                    for (int q = 0; q < R; ++q) {
+                        round2(&o[q].v[k], fma2(mul2(x[q][j], both(s[q])), w0, b0));
+                        round2(&o[q].v[k + 2], fma2(mul2(x[q][j + 1], both(s[q])), w1, b1));
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < R; ++q)
+                    if (q < there) *reinterpret_cast<Piece<Y, V> *>(y[q] + c) = o[q];
+            } else {
+                const int j = i / 2;
+                y[0][c] = round_to<Y>(i & 1 ? fmaf(x[0][j].y * s[0], wv[j].y, bv[j].y) : fmaf(x[0][j].x * s[0], wv[j].x, bv[j].x));
+            }
         }
     }
 }
 
 // dx, and a CTA's share of dw and db, in one pass.
 template <class X, class Y, int V, bool kFull>
-__global__ void __launch_bounds__(kBwdThreads) backward_held_kernel(const NormBwd P, int gw) {
-    using LX = Lane<X, V, kBwdHeld, kFull>;
-    using LY = Lane<Y, V, kBwdHeld, kFull>;
-    constexpr int kDeep = backward_deep<LX, LY>(), N = kBwdHeld / 2;
+__global__ void __launch_bounds__(kHeldThreads) backward_held_kernel(const NormBwd P, int gw, int deep) {
+    using L = Lane<X, V, kFull>;
+    constexpr int N = kHeld / 2, R = rows_at_once<V>();
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float part[64];
+    __shared__ float part[128 * R];
+    __shared__ __align__(8) uint64_t bars[kHeldThreads / 32 * kDeepMost];
+    __shared__ uint32_t gave_up;
     tc::grid_wait_release();
     const int gt = gw * 32, g = threadIdx.x / gt, t = threadIdx.x % gt, groups = blockDim.x / gt;
     const float inv = 1.f / (float)P.d;
     const int64_t step = (int64_t)gridDim.x * groups, row0 = (int64_t)blockIdx.x * groups + g;
-    const LX lx(t, gt, P.d, tc::smem_u32(smem));
-    const LY ly(t, gt, P.d, tc::smem_u32(smem) + kDeep * LX::kSlot * blockDim.x);
+    const L lx{t, gt, P.d};
+    // x and dy of a row stand behind each other and share a barrier
+    const uint32_t xb = P.d * (uint32_t)sizeof(X), yb = P.d * (uint32_t)sizeof(Y), pitch = xb + yb;
+    uint8_t *places = smem + (size_t)g * deep * pitch;
+    const uint32_t bar0 = tc::smem_u32(bars + g * deep);
+    const float *w = reinterpret_cast<const float *>(smem + (size_t)groups * deep * pitch);
     const auto x_at = [&](int64_t row) { return static_cast<const X *>(P.x.p) + row * P.x.ld; };
     const auto y_at = [&](int64_t row) { return static_cast<const Y *>(P.dy.p) + row * P.dy.ld; };
-    const auto ask = [&](int64_t row, int slot) {
-        if (row < P.T) {
-            lx.ask(x_at(row), slot);
-            ly.ask(y_at(row), slot);
-        }
-        close_copies();
+    const auto ask = [&](int64_t row, uint32_t i) {
+        tc::mbar_arrive_expect_tx(bar0 + 8 * i, pitch);
+        tc::bulk_g2s(tc::smem_u32(places + i * pitch), x_at(row), xb, bar0 + 8 * i);
+        tc::bulk_g2s(tc::smem_u32(places + i * pitch + xb), y_at(row), yb, bar0 + 8 * i);
     };
+    if constexpr (V == 8) {
+        if (threadIdx.x == 0) gave_up = 0;
+        if (t == 0) {
+            for (int i = 0; i < deep; ++i) tc::mbar_init(bar0 + 8 * i, 1);
+            tc::mbar_init_fence();
+            for (int i = 0; i < deep && row0 + i * step < P.T; ++i) ask(row0 + i * step, i);
+        }
+        stage(const_cast<float *>(w), P.w, P.w_dtype, P.d, 1.f);
+        __syncthreads();
+    }
     float2 dw[N], db[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) dw[i] = db[i] = both(0.f);
+    float mu_next[R], r_next[R];
+    const auto stats = [&](int64_t row) {
 #pragma unroll
-    for (int i = 0; i < kDeep - 1; ++i) ask(row0 + i * step, i);
-    float mu_next = 0.f, r_next = 0.f;
-    if (row0 < P.T) mu_next = P.mean[row0], r_next = P.rstd[row0];
-    int slot = 0, turn = 0;
-    for (int64_t row = row0; row < P.T; row += step) {
-        const float mu = mu_next, r = r_next;
-        if (row + step < P.T) mu_next = P.mean[row + step], r_next = P.rstd[row + step];
-        ask(row + (kDeep - 1) * step, turn == 0 ? kDeep - 1 : turn - 1);
-        copies_left<kDeep - 1>();
-        float2 x[N], e[N], w[N], s1 = both(0.f), s2 = both(0.f);
-        param_row(lx, P.w, P.w_dtype, 0.f, w);
-        lx.take(x_at(row), turn, x);
-        ly.take(y_at(row), turn, e);
-        turn = turn + 1 == kDeep ? 0 : turn + 1;
-#pragma unroll
-        for (int i = 0; i < N; ++i) { // past the row's end dy is zero, so all of these are
-            x[i] = mul2(add2(x[i], both(-mu)), both(r));
-            dw[i] = fma2(e[i], x[i], dw[i]);
-            db[i] = add2(db[i], e[i]);
-            if (P.w) e[i] = mul2(e[i], w[i]);
-            s1 = add2(s1, e[i]);
-            s2 = fma2(e[i], x[i], s2);
+        for (int q = 0; q < R; ++q) {
+            const bool in = row + q * step < P.T;
+            mu_next[q] = in ? P.mean[row + q * step] : 0.f;
+            r_next[q] = in ? P.rstd[row + q * step] : 0.f;
         }
-        if (P.dx.p) {
-            float a = s1.x + s1.y, b = s2.x + s2.y;
-            group_sum2(a, b, gw, g, part, slot);
-            const float2 c1 = both(-a * inv), c2 = both(-b * inv), rr = both(r);
+    };
+    stats(row0);
+    int slot = 0;
+    uint32_t turn = 0, phase = 0;
+    for (int64_t row = row0; row < P.T; row += R * step) {
+        float mu[R], r[R];
 #pragma unroll
-            for (int i = 0; i < N; ++i) e[i] = mul2(fma2(x[i], c2, add2(e[i], c1)), rr);
-            lx.give(static_cast<X *>(P.dx.p) + row * P.dx.ld, e);
+        for (int q = 0; q < R; ++q) mu[q] = mu_next[q], r[q] = r_next[q];
+        stats(row + R * step);
+        const uint32_t first = turn;
+        if constexpr (V == 8) {
+#pragma unroll
+            for (int q = 0; q < R; ++q) {
+                if (row + q * step < P.T) wait_row(bar0 + 8 * turn, phase, &gave_up);
+                if (++turn == (uint32_t)deep) turn = 0, phase ^= 1;
+            }
+        }
+        // (x - mu) r and dy w of piece i of row q, from shared memory (V == 1: from memory, an eighth of a piece)
+        const auto piece = [&](int q, int i, float2(&xh)[4], float2(&e)[4]) {
+            uint32_t at = first + q;
+            if (at >= (uint32_t)deep) at -= deep;
+            const uint8_t *p = places + at * pitch;
+            Piece<X, 8> u = {};
+            Piece<Y, 8> v = {};
+            if constexpr (V == 8) {
+                if (lx.in(i) && row + q * step < P.T) {
+                    u = load<X, 8>(reinterpret_cast<const X *>(p) + lx.column(i));
+                    v = load<Y, 8>(reinterpret_cast<const Y *>(p + xb) + lx.column(i));
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (lx.in(8 * i + k)) {
+                        u.v[k] = x_at(row)[lx.column(8 * i + k)];
+                        v.v[k] = y_at(row)[lx.column(8 * i + k)];
+                    }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                xh[k] = mul2(add2(widen2(&u.v[2 * k]), both(-mu[q])), both(r[q]));
+                e[k] = widen2(&v.v[2 * k]);
+            }
+        };
+        const auto weights = [&](int i, float2(&o)[4]) {
+            if constexpr (V == 8) {
+                if (!lx.in(i)) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) o[k] = both(0.f);
+                    return;
+                }
+                four(w, P.d, lx.column(i), o[0], o[1]);
+                four(w, P.d, lx.column(i) + 4, o[2], o[3]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    float one[1] = {0.f};
+                    if (lx.in(8 * i + k)) widen_params<1>(P.w, P.w_dtype, lx.column(8 * i + k), 1.f, one);
+                    (k & 1 ? o[k / 2].y : o[k / 2].x) = one[0];
+                }
+            }
+        };
+        float2 s1[R], s2[R];
+#pragma unroll
+        for (int q = 0; q < R; ++q) s1[q] = s2[q] = both(0.f);
+#pragma unroll
+        for (int i = 0; i < kHeld / 8; ++i) { // past the row's end dy is zero, so all of these are
+            float2 wv[4];
+            weights(i, wv);
+#pragma unroll
+            for (int q = 0; q < R; ++q) {
+                float2 xh[4], e[4];
+                piece(q, i, xh, e);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    dw[4 * i + k] = fma2(e[k], xh[k], dw[4 * i + k]);
+                    db[4 * i + k] = add2(db[4 * i + k], e[k]);
+                    e[k] = mul2(e[k], wv[k]);
+                    s1[q] = add2(s1[q], e[k]);
+                    s2[q] = fma2(e[k], xh[k], s2[q]);
+                }
+            }
+        }
+        float s[2 * R];
+#pragma unroll
+        for (int q = 0; q < R; ++q) s[2 * q] = s1[q].x + s1[q].y, s[2 * q + 1] = s2[q].x + s2[q].y;
+        group_sums(s, gw, g, part, slot);
+        if constexpr (V == 8) // the rows before these have been read by all: into their places
+            if (t == 0 && row > row0 && deep >= 2 * R)
+                for (int q = 0; q < R; ++q)
+                    if (row + (q + deep - R) * step < P.T) ask(row + (q + deep - R) * step, (first + deep - R + q) % deep);
+#pragma unroll
+        for (int i = 0; i < kHeld / 8 && P.dx.p; ++i) {
+            float2 wv[4];
+            weights(i, wv);
+#pragma unroll
+            for (int q = 0; q < R; ++q) {
+                float2 xh[4], e[4];
+                piece(q, i, xh, e);
+                const float2 c1 = both(-s[2 * q] * inv), c2 = both(-s[2 * q + 1] * inv), rr = both(r[q]);
+                X *dx = static_cast<X *>(P.dx.p) + (row + q * step) * P.dx.ld;
+                Piece<X, 8> o;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    round2(&o.v[2 * k], mul2(fma2(xh[k], c2, add2(mul2(e[k], wv[k]), c1)), rr));
+                if (row + q * step >= P.T) continue;
+                if constexpr (V == 8) {
+                    if (lx.in(i)) *reinterpret_cast<Piece<X, 8> *>(dx + lx.column(i)) = o;
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (lx.in(8 * i + k)) dx[lx.column(8 * i + k)] = o.v[k];
+                }
+            }
+        }
+        if (V == 8 && deep < 2 * R) { // long rows of 32 bits: no place but these rows' own
+            group_meet(gw, g);
+            if (t == 0)
+#pragma unroll
+                for (int q = 0; q < R; ++q)
+                    if (row + (q + deep) * step < P.T) ask(row + (q + deep) * step, (first + q) % deep);
         }
     }
     if (!P.dw && !P.db) return;
-    // the groups' sums, one behind another
-    copies_left<0>();
-    __syncthreads();
+    // the groups' sums, one behind another (barrier 0 is the first group's own until here)
+    asm volatile("bar.sync 15;" ::: "memory");
     float *sum = reinterpret_cast<float *>(smem);
     for (int j = 0; j < groups; ++j) {
         if (g == j)
 #pragma unroll
-            for (int i = 0; i < kBwdHeld; ++i) {
+            for (int i = 0; i < kHeld; ++i) {
                 const int c = lx.column(i / V) + i % V;
                 if (lx.in(i / V)) {
                     float &vw = i & 1 ? dw[i / 2].y : dw[i / 2].x, &vb = i & 1 ? db[i / 2].y : db[i / 2].x;
@@ -388,7 +548,7 @@ __global__ void __launch_bounds__(kBwdThreads) backward_held_kernel(const NormBw
 // Rows longer than that: read again for each step.
 template <class X, class Y, int V>
 __global__ void __launch_bounds__(kThreads) forward_kernel(const NormFwd P, int gw) {
-    __shared__ float part[32];
+    __shared__ float part[64];
     tc::grid_wait_release();
     const int gt = gw * 32, g = threadIdx.x / gt, t = threadIdx.x % gt, groups = blockDim.x / gt;
     const float inv = 1.f / (float)P.d;
@@ -417,8 +577,8 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const NormFwd P, int 
             const auto q = load<X, V>(x + c);
             Piece<Y, V> o;
             float w[V], b[V];
-            params<V>(P.w, P.w_dtype, c, 1.f, w);
-            params<V>(P.b, P.w_dtype, c, 0.f, b);
+            widen_params<V>(P.w, P.w_dtype, c, 1.f, w);
+            widen_params<V>(P.b, P.w_dtype, c, 0.f, b);
 #pragma unroll
             for (int i = 0; i < V; ++i) o.v[i] = round_to<Y>(fmaf((widen(q.v[i]) - mu) * r, w[i], b[i]));
             *reinterpret_cast<Piece<Y, V> *>(y + c) = o;
@@ -432,7 +592,7 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const NormFwd P, int 
 
 template <class X, class Y, int V>
 __global__ void __launch_bounds__(kThreads) dx_kernel(const NormBwd P, int gw) {
-    __shared__ float part[32];
+    __shared__ float part[64];
     tc::grid_wait_release();
     const int gt = gw * 32, g = threadIdx.x / gt, t = threadIdx.x % gt, groups = blockDim.x / gt;
     const float inv = 1.f / (float)P.d;
@@ -447,7 +607,7 @@ __global__ void __launch_bounds__(kThreads) dx_kernel(const NormBwd P, int gw) {
             const auto q = load<X, V>(x + c);
             const auto e = load<Y, V>(dy + c);
             float w[V];
-            params<V>(P.w, P.w_dtype, c, 1.f, w);
+            widen_params<V>(P.w, P.w_dtype, c, 1.f, w);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const float gv = widen(e.v[i]) * w[i];
@@ -462,7 +622,7 @@ __global__ void __launch_bounds__(kThreads) dx_kernel(const NormBwd P, int gw) {
             const auto e = load<Y, V>(dy + c);
             Piece<X, V> o;
             float w[V];
-            params<V>(P.w, P.w_dtype, c, 1.f, w);
+            widen_params<V>(P.w, P.w_dtype, c, 1.f, w);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const float xh = (widen(q.v[i]) - mu) * r, gv = widen(e.v[i]) * w[i];
@@ -558,10 +718,14 @@ bool whole_rows(const Rows &r, int dtype, int T) {
     return aligned16(r.p) && (T < 2 || r.ld * (int64_t)dense::type_size(dtype) % 16 == 0);
 }
 
+// Rows of `bytes` a group keeps on their way beside `rest` bytes in shared memory: at least the two in work.
+int rows_ahead(size_t bytes, size_t rest, int groups) {
+    const size_t n = (kHeldSmem - rest) / (bytes * groups);
+    return n > kDeepMost ? kDeepMost : (int)n;
+}
+constexpr int kFewRows = 4; // an SM
 // Warps of a group for a row of `pieces` pieces.
 int group_warps(int pieces, int per_lane) { return (pieces + 32 * per_lane - 1) / (32 * per_lane); }
-// CTAs of the forward an SM holds, by shared memory.
-int held_ctas(int smem) { return smem > 75 << 10 ? 2 : 3; }
 cudaError_t reduce(const NormBwd &P, int n, cudaStream_t s) {
     return launch_behind(reduce_kernel, dim3((unsigned)((2ll * P.d + 31) / 32)), dim3(256), 0, s, P, n);
 }
@@ -577,20 +741,28 @@ cudaError_t launch_norm_forward(const NormFwd &P, cudaStream_t s) {
         constexpr int V = decltype(v)::value;
         const int pieces = P.d / V + (P.d % V != 0), sms = device_sm_count();
         if (P.d <= kHeldMost) {
-            const int gw = group_warps(pieces, kFwdHeld / V), groups = kFwdThreads / 32 / gw, threads = groups * gw * 32;
-            const auto launch = [&](auto full) {
-                using L = Lane<X, V, kFwdHeld, decltype(full)::value>;
+            const int gw = group_warps(pieces, kHeld / V), most = kHeldThreads / 32 / gw;
+            const auto launch = [&](auto full, auto few) {
+                constexpr bool kFull = decltype(full)::value, kFew = decltype(few)::value;
                 static SmemAttr attr;
-                const auto kernel = forward_held_kernel<X, Y, V, decltype(full)::value>;
-                const int blocks = (P.T + groups - 1) / groups, smem = forward_deep<L>() * L::kSlot * threads;
+                const auto kernel = forward_held_kernel<X, Y, V, kFull, kFew>;
+                const size_t row = sizeof(X) * P.d, rest = (size_t)P.d * 8;
+                // few rows: as many CTAs as there are SMs before several groups a CTA
+                int groups = (P.T + sms - 1) / sms;
+                if (groups > most) groups = most;
+                const int deep = kFew ? 1 : rows_ahead(row, rest, groups), smem = kFew ? 0 : (int)(deep * groups * row + rest);
                 cudaError_t e = ensure_smem(attr, reinterpret_cast<const void *>(kernel), smem);
                 if (e != cudaSuccess) return e;
-                const int most = held_ctas(smem) * sms;
-                return launch_behind(kernel, dim3(blocks < most ? blocks : most), dim3(threads), smem, s, P, gw);
+                const int blocks = (P.T + groups - 1) / groups, all = kFew ? 4 * sms : sms;
+                return launch_behind(kernel, dim3(blocks < all ? blocks : all), dim3(groups * gw * 32), smem, s, P, gw, deep);
             };
-            if constexpr (V == 8)
-                if (P.d == gw * 32 * kFwdHeld) return launch(std::true_type());
-            return launch(std::false_type());
+            if constexpr (V == 8) {
+                // copies and staged parameters pay from some rows a group on, whose places fit
+                if (P.T > kFewRows * sms && rows_ahead(sizeof(X) * P.d, (size_t)P.d * 8, most) >= kRowsAtOnce)
+                    return P.d == gw * 32 * kHeld ? launch(std::true_type(), std::false_type())
+                                                  : launch(std::false_type(), std::false_type());
+            }
+            return launch(std::false_type(), std::true_type());
         }
         return launch_behind(forward_kernel<X, Y, V>, dim3(P.T < 4 * sms ? P.T : 4 * sms), dim3(kThreads), 0, s, P, kThreads / 32);
     });
@@ -607,21 +779,22 @@ cudaError_t launch_norm_backward(const NormBwd &P, cudaStream_t s) {
         const bool sums = P.dw || P.db;
         cudaError_t e = cudaSuccess;
         if (P.d <= kHeldMost) {
-            const int gw = group_warps(pieces, kBwdHeld / V), groups = kBwdThreads / 32 / gw, threads = groups * gw * 32;
-            const int most = sms < kNormParts ? sms : kNormParts, need = (P.T + groups - 1) / groups;
-            const int blocks = need < most ? need : most;
+            const int gw = group_warps(pieces, kHeld / V);
+            int groups = kHeldThreads / 32 / gw, need = (P.T + sms - 1) / sms;
+            if (groups > need) groups = need; // 8 at most where a group has barriers
+            const int threads = groups * gw * 32, most = sms < kNormParts ? sms : kNormParts, all = (P.T + groups - 1) / groups;
+            const int blocks = all < most ? all : most;
             const auto launch = [&](auto full) {
                 constexpr bool kFull = decltype(full)::value;
-                using LX = Lane<X, V, kBwdHeld, kFull>;
-                using LY = Lane<Y, V, kBwdHeld, kFull>;
                 static SmemAttr attr;
                 const auto kernel = backward_held_kernel<X, Y, V, kFull>;
-                const int ring = backward_deep<LX, LY>() * (LX::kSlot + LY::kSlot) * threads, last = groups > 1 ? P.d * 8 : 0;
-                const int smem = ring > last ? ring : last;
+                const size_t row = (sizeof(X) + sizeof(Y)) * P.d, rest = (size_t)P.d * 4;
+                const int deep = V == 8 ? rows_ahead(row, rest, groups) : 2, last = groups > 1 ? P.d * 8 : 0;
+                const int ring = V == 8 ? (int)(deep * groups * row + rest) : 0, smem = ring > last ? ring : last;
                 const cudaError_t f = ensure_smem(attr, reinterpret_cast<const void *>(kernel), smem);
-                return f == cudaSuccess ? launch_behind(kernel, dim3(blocks), dim3(threads), smem, s, P, gw) : f;
+                return f == cudaSuccess ? launch_behind(kernel, dim3(blocks), dim3(threads), smem, s, P, gw, deep) : f;
             };
-            if (V == 8 && P.d == gw * 32 * kBwdHeld) {
+            if (V == 8 && P.d == gw * 32 * kHeld) {
                 if constexpr (V == 8) e = launch(std::true_type());
             } else {
                 e = launch(std::false_type());
@@ -639,6 +812,15 @@ cudaError_t launch_norm_backward(const NormBwd &P, cudaStream_t s) {
         if (e != cudaSuccess || !P.dx.p) return e;
         return launch_behind(dx_kernel<X, Y, V>, dim3(P.T < 4 * sms ? P.T : 4 * sms), dim3(kThreads), 0, s, P, kThreads / 32);
     });
+}
+
+cudaError_t norm_timeout(uint32_t *out) {
+    uint32_t v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_norm_timeout, sizeof v);
+    const uint32_t zero = 0;
+    if (e == cudaSuccess && v) e = cudaMemcpyToSymbol(g_norm_timeout, &zero, sizeof zero);
+    *out |= v;
+    return e;
 }
 
 } // namespace train

@@ -85,6 +85,7 @@ cudaError_t ortho_timeout(uint32_t *out);
 
 cudaError_t launch_norm_forward(const NormFwd &P, cudaStream_t s);
 cudaError_t launch_norm_backward(const NormBwd &P, cudaStream_t s);
+cudaError_t norm_timeout(uint32_t *out);
 
 // A launch that may begin while the kernel before it in the stream ends; the kernel waits for that one itself
 // (tc::grid_wait_release) before it touches memory.
