@@ -158,6 +158,9 @@ struct WeightsJob {
 // Whole widths of 32 columns, 256 at most.
 int width(int n) { return n >= 256 ? 256 : n <= 64 ? 64 : (n + 31) / 32 * 32; }
 
+// Pairs of CTAs, with tiles of 256 rows, from so many rows an expert on (their mean: the offsets are on the device).
+bool pairs(const Group &G) { return G.rows / G.E >= 160; }
+
 template <int kCG, bool kWmn>
 cudaError_t rows_product(const Group &G, const void *a, int K, const void *w, int N, void *out, int out_dtype, int add, cudaStream_t s) {
     RowsJob<kCG, kWmn> J = {};
@@ -177,10 +180,12 @@ cudaError_t rows_product(const Group &G, const void *a, int K, const void *w, in
 } // namespace
 
 cudaError_t launch_group_forward(const Group &G, const void *x, const void *w, void *y, int out_dtype, int add, cudaStream_t s) {
-    return rows_product<1, false>(G, x, G.k, w, G.n, y, out_dtype, add, s);
+    return pairs(G) ? rows_product<2, false>(G, x, G.k, w, G.n, y, out_dtype, add, s)
+                    : rows_product<1, false>(G, x, G.k, w, G.n, y, out_dtype, add, s);
 }
 cudaError_t launch_group_dx(const Group &G, const void *dy, const void *w, void *dx, cudaStream_t s) {
-    return rows_product<1, true>(G, dy, G.n, w, G.k, dx, G.dtype, 0, s);
+    return pairs(G) ? rows_product<2, true>(G, dy, G.n, w, G.k, dx, G.dtype, 0, s)
+                    : rows_product<1, true>(G, dy, G.n, w, G.k, dx, G.dtype, 0, s);
 }
 cudaError_t launch_group_dw(const Group &G, const void *dy, const void *x, void *dw, int grad_dtype, int add, cudaStream_t s) {
     WeightsJob J = {};

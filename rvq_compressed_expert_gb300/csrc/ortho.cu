@@ -96,11 +96,10 @@ __global__ void __launch_bounds__(kFlat)
 // What the three products of a step have in common: `count` matrices of M x N results, tiles of 128 * cg x BN.
 struct Stack {
     int BN, high, tm, tn, count, M, K;
-    cudaError_t set(int cg, int bn, int n, int m, int cols, int k) {
+    void set(int cg, int bn, int n, int m, int cols, int k) {
         BN = bn, high = kBM * cg, M = m, K = k, count = n;
         tm = (m + high - 1) / high;
         tn = (cols + bn - 1) / bn;
-        return cudaSuccess;
     }
     __device__ __forceinline__ int tiles() const { return count * tm * tn; }
     __device__ __forceinline__ Spot spot(int t) const {
@@ -131,23 +130,82 @@ __device__ __forceinline__ void put_halves(Out32 &o, const CUtensorMap *map, voi
     dense::put32_as(WASTE_ACT_F16, o, o.rows >= 32 ? map : nullptr, p, ld, n, ld, true, false, v);
 }
 
-// A = X X^T (kMn: X^T X)
+// Tile t of those on and below a diagonal, row by row.
+__host__ __device__ __forceinline__ void triangle(int t, int &i, int &j) {
+    i = (int)((sqrtf(8.f * t + 1.f) - 1.f) * 0.5f);
+    while (i * (i + 1) / 2 > t) --i;
+    while ((i + 1) * (i + 2) / 2 <= t) ++i;
+    j = t - i * (i + 1) / 2;
+}
+// Partial sums of A = X X^T (kMn: X^T X): [matrix][share of k][tile][side][side], fp32.
 template <bool kMn> struct GramJob {
     static constexpr bool kAmn = kMn, kBmn = kMn, kMask = false;
     CUtensorMap ta, tb, to;
-    Stack s;
-    void *a;
-    int ldm;
+    void *out;
+    int side, tri, slices, count, pieces;
     __device__ void begin(uint8_t *) const {}
-    __device__ __forceinline__ int tiles(const uint8_t *) const { return s.tiles(); }
-    __device__ __forceinline__ Spot spot(const uint8_t *, int t) const { return s.spot(t); }
+    __device__ __forceinline__ int tiles(const uint8_t *) const { return count * slices * tri; }
+    __device__ __forceinline__ Spot spot(const uint8_t *, int t) const {
+        const int s = t / tri, z = s / slices, share = s - z * slices;
+        int i, j;
+        triangle(t - s * tri, i, j);
+        const int k0 = (int)((long long)pieces * share / slices), k1 = (int)((long long)pieces * (share + 1) / slices);
+        Spot T;
+        T.am = i * side;
+        T.bm = j * side;
+        T.az = T.bz = z;
+        T.ak = T.bk = k0 * 64;
+        T.pieces = k1 - k0;
+        T.left = 64;
+        T.m = t * side;
+        T.n = 0;
+        T.rows = side;
+        return T;
+    }
     template <int W> __device__ __forceinline__ void tile(Out32 &o, const Spot &, int n, const float (&v)[W]) const {
-        float x[W];
-#pragma unroll
-        for (int i = 0; i < W; ++i) x[i] = v[i] * kDown;
-        put_halves(o, &to, a, ldm, n, x);
+        dense::put32_as(WASTE_ACT_F32, o, &to, out, side, n, side, true, false, v);
     }
 };
+// A from its partial sums, both halves: a CTA takes 64 x 64 values of a tile.
+__global__ void __launch_bounds__(kFlat) gram_kernel(const float *parts, int side, int tri, int slices, int m, int ldm, __half *a) {
+    __shared__ __half turn[64][66];
+    tc::grid_wait_release();
+    const int per = side / 64, z = blockIdx.y, tile = blockIdx.x / (per * per), sub = blockIdx.x % (per * per);
+    int i, j;
+    triangle(tile, i, j);
+    const int r0 = i * side + sub / per * 64, c0 = j * side + sub % per * 64; // of the matrix
+    if (r0 < c0 || r0 >= m || c0 >= m) return; // above the diagonal, or past the end
+    const size_t step = (size_t)tri * side * side;
+    const float *p = parts + ((size_t)z * slices * tri + tile) * side * side + (size_t)(sub / per * 64) * side + sub % per * 64;
+    __half *to = a + (size_t)z * m * ldm;
+    for (int e = threadIdx.x; e < 64 * 16; e += kFlat) {
+        const int r = e / 16, c = e % 16 * 4;
+        float4 v = {};
+#pragma unroll 4
+        for (int s = 0; s < slices; ++s) {
+            const float4 q = *reinterpret_cast<const float4 *>(p + s * step + (size_t)r * side + c);
+            v.x += q.x, v.y += q.y, v.z += q.z, v.w += q.w;
+        }
+        const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) turn[r][c + k] = __float2half_rn(x[k] * kDown);
+    }
+    __syncthreads();
+    const bool cross = r0 == c0;
+    for (int e = threadIdx.x; e < 64 * 32; e += kFlat) { // the block, and turned round
+        const int r = e / 32, c = e % 32 * 2;
+#pragma unroll
+        for (int side2 = 0; side2 < 2; ++side2) {
+            if (side2 && cross) break;
+            const int row = (side2 ? c0 : r0) + r, col = (side2 ? r0 : c0) + c;
+            if (row >= m || col >= ldm) continue;
+            __half x[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) x[k] = side2 || (cross && c + k > r) ? turn[c + k][r] : turn[r][c + k];
+            *reinterpret_cast<__half2 *>(to + (size_t)row * ldm + col) = __halves2half2(x[0], x[1]);
+        }
+    }
+}
 // B = b A + c A^2, its diagonal apart
 struct SquareJob {
     static constexpr bool kAmn = false, kBmn = false, kMask = false;
@@ -220,14 +278,38 @@ template <bool kTall> struct StepJob {
     }
 };
 
-int width(int n) { return n >= 256 ? 256 : n <= 64 ? 64 : (n + 31) / 32 * 32; }
+// Tiles of 128 * cg x BN for `count` results of M x N: the quickest by whole waves of tiles, each as long as its bytes
+// need into an SM (80 B/ns) or its MMAs take.
+struct Shape {
+    int cg, BN;
+};
+Shape shape(int count, int M, int N, int sms) {
+    Shape best{1, 64};
+    double least = 1e30;
+    for (int cg = 1; cg <= 2; ++cg)
+        for (int BN = 64; BN <= 256; BN += 32) {
+            if (cg == 2 && M <= kBM) continue;
+            if (BN > 64 && BN - 32 >= N) break;
+            const long long tiles = (long long)count * ((M + kBM * cg - 1) / (kBM * cg)) * ((N + BN - 1) / BN), slots = sms / cg;
+            const double load = (kBM + BN / cg) * kRowBytes / 80., mma = BN * 1.31;
+            const double t = (double)((tiles + slots - 1) / slots) * (load > mma ? load : mma);
+            if (t < least) least = t, best = Shape{cg, BN};
+        }
+    return best;
+}
+template <class J> cudaError_t launch(int cg, int BN, const J &job, long long tiles, int sms, cudaStream_t s) {
+    TileArgs T = {};
+    T.BN = BN;
+    return cg == 2 ? launch_tiles_as<2>(T, job, false, 0, tiles, sms, s) : launch_tiles_as<1>(T, job, false, 0, tiles, sms, s);
+}
 
 template <bool kTall> cudaError_t steps(const Ortho &P, const OrthoParts &W, cudaStream_t s) {
     const int m = kTall ? P.cols : P.rows, n = kTall ? P.rows : P.cols, sms = device_sm_count();
     uint8_t *hi[2] = {P.ws + W.hi[0], P.ws + W.hi[1]}, *lo = P.ws + W.lo, *A = P.ws + W.a, *B = P.ws + W.b;
-    float *diag = reinterpret_cast<float *>(P.ws + W.diag);
+    float *diag = reinterpret_cast<float *>(P.ws + W.diag), *parts = reinterpret_cast<float *>(P.ws + W.gram);
     const size_t xs = (size_t)P.rows * W.ldx, ss = (size_t)m * W.ldm;
-    const int wide = width(m), step_wide = width(P.cols);
+    const Shape qs = shape(P.count, m, m, sms), xx = shape(P.count, P.rows, P.cols, sms);
+    const int gcg = W.side == 256 ? 2 : 1;
     cudaError_t e = cudaSuccess;
     const auto x_map = [&](CUtensorMap *t, int i, int box) {
         if (e == cudaSuccess) e = stack_map(t, hi[i], P.cols, P.rows, P.count, W.ldx, xs, box);
@@ -235,51 +317,52 @@ template <bool kTall> cudaError_t steps(const Ortho &P, const OrthoParts &W, cud
     const auto s_map = [&](CUtensorMap *t, const void *p, int box) {
         if (e == cudaSuccess) e = stack_map(t, p, m, m, P.count, W.ldm, ss, box);
     };
-    const auto o_map = [&](CUtensorMap *t, void *p, int rows, int ld) {
-        if (e == cudaSuccess) e = dense::store_map(t, p, 2, rows, ld);
+    const auto o_map = [&](CUtensorMap *t, void *p, int bytes, int rows, int ld) {
+        if (e == cudaSuccess) e = dense::store_map(t, p, bytes, rows, ld);
     };
     GramJob<kTall> G = {};
     SquareJob Q = {};
     StepJob<kTall> S = {};
-    G.s.set(1, wide, P.count, m, m, n);
-    o_map(&G.to, A, P.count * m, W.ldm);
-    G.a = A;
-    G.ldm = W.ldm;
-    Q.s.set(1, wide, P.count, m, m, m);
+    G.out = parts;
+    G.side = W.side, G.tri = W.tri, G.slices = W.slices, G.count = P.count, G.pieces = (n + 63) / 64;
+    const long long items = (long long)P.count * W.tri * W.slices;
+    o_map(&G.to, parts, 4, (int)(items * W.side), W.side);
+    Q.s.set(qs.cg, qs.BN, P.count, m, m, m);
     s_map(&Q.ta, A, kBM);
-    s_map(&Q.tb, A, wide);
-    o_map(&Q.to, B, P.count * m, W.ldm);
+    s_map(&Q.tb, A, qs.BN / qs.cg);
+    o_map(&Q.to, B, 2, P.count * m, W.ldm);
     Q.a = A, Q.out = B, Q.diag = diag, Q.ldm = W.ldm, Q.b = P.b, Q.c = P.c;
-    S.s.set(1, step_wide, P.count, P.rows, P.cols, m);
-    s_map(kTall ? &S.tb : &S.ta, B, kTall ? step_wide : kBM);
-    o_map(&S.tlo, lo, P.count * P.rows, W.ldx);
+    S.s.set(xx.cg, xx.BN, P.count, P.rows, P.cols, m);
+    s_map(kTall ? &S.tb : &S.ta, B, kTall ? xx.BN / xx.cg : kBM);
+    o_map(&S.tlo, lo, 2, P.count * P.rows, W.ldx);
     S.lo = lo, S.diag = diag, S.ldx = W.ldx, S.cols = P.cols, S.a = P.a;
     S.out_dtype = P.out_dtype, S.add = P.add, S.scale = P.scale * kDown;
     const size_t size = dense::type_size(P.out_dtype);
     S.by_map = !P.add && (size_t)P.cols * size % 16 == 0;
-    if (S.by_map && e == cudaSuccess) e = dense::store_map(&S.tout, P.out, (int)size, P.count * P.rows, P.cols);
+    if (S.by_map) o_map(&S.tout, P.out, (int)size, P.count * P.rows, P.cols);
     CUtensorMap ga[2], gb[2], sx[2], st[2];
     for (int i = 0; i < 2; ++i) {
         x_map(&ga[i], i, kTall ? 64 : kBM);
-        x_map(&gb[i], i, kTall ? 64 : wide);
+        x_map(&gb[i], i, kTall ? 64 : W.side / gcg);
         x_map(&sx[i], i, kTall ? kBM : 64);
-        o_map(&st[i], hi[i], P.count * P.rows, W.ldx);
+        o_map(&st[i], hi[i], 2, P.count * P.rows, W.ldx);
     }
+    const int per = W.side / 64;
     for (int i = 0; i < P.steps && e == cudaSuccess; ++i) {
         const int from = i & 1;
-        TileArgs T = {};
-        T.BN = wide;
         G.ta = ga[from], G.tb = gb[from];
-        e = launch_tiles_as<1>(T, G, false, 0, (long long)P.count * G.s.tm * G.s.tn, sms, s);
-        if (e == cudaSuccess) e = launch_tiles_as<1>(T, Q, false, 0, (long long)P.count * Q.s.tm * Q.s.tn, sms, s);
+        e = launch(gcg, W.side, G, items, sms, s);
+        if (e == cudaSuccess)
+            e = launch_behind(gram_kernel, dim3(W.tri * per * per, P.count), dim3(kFlat), 0, s, parts, W.side, W.tri, W.slices, m, W.ldm,
+                              reinterpret_cast<__half *>(A));
+        if (e == cudaSuccess) e = launch(qs.cg, qs.BN, Q, (long long)P.count * Q.s.tm * Q.s.tn, sms, s);
         if (e != cudaSuccess) break;
-        T.BN = step_wide;
         (kTall ? S.ta : S.tb) = sx[from];
         S.thi = st[from ^ 1];
         S.hi = hi[from], S.hi_next = hi[from ^ 1];
         S.full = i + 2 >= P.steps;
         S.out = i + 1 == P.steps ? P.out : nullptr;
-        e = launch_tiles_as<1>(T, S, false, 0, (long long)P.count * S.s.tm * S.s.tn, sms, s);
+        e = launch(xx.cg, xx.BN, S, (long long)P.count * S.s.tm * S.s.tn, sms, s);
     }
     return e;
 }

@@ -55,15 +55,35 @@ struct Ortho {
     uint8_t *ws;
 };
 // What stands in the workspace, from its start: X in two halves (the first of them twice, taken in turn), A and
-// b A + c A^2 without its diagonal, that diagonal, and partial sums of squares.
+// b A + c A^2 without its diagonal, that diagonal, partial sums of squares, and A's partial sums.
 constexpr int kOrthoParts = 128; // of a matrix
 struct OrthoParts {
-    size_t hi[2], lo, a, b, diag, sums, total;
+    size_t hi[2], lo, a, b, diag, sums, gram, total;
     int ldx, ldm;
+    int side, tri, slices; // of A: tiles of side x side, those on and below its diagonal, in so many shares of k
 };
+// A is made in tiles of 256 x 256 by pairs of CTAs (of 128 x 128 by one where it is no larger), on and below its
+// diagonal, the long side split into shares: as many as shorten the waves of tiles (a piece of k takes about
+// 370 ns) by more than their fp32 partial sums, written and read again, cost.  The workspace has to have one size
+// everywhere, so this counts with the SMs of the one device the library is for.
+inline int gram_slices(long long tiles, int pieces, int side) {
+    const int slots = side == 256 ? 76 : 152;
+    int best = 1;
+    double least = 1e30;
+    for (int s = 1; s <= 16 && s <= pieces; ++s) {
+        const double waves = (double)((tiles * s + slots - 1) / slots);
+        const double t = waves * ((pieces + s - 1) / s) * 370. + (double)(tiles * s) * side * side * 8. / 5000.;
+        if (t < least) least = t, best = s;
+    }
+    return best;
+}
 inline OrthoParts ortho_parts(int count, int rows, int cols) {
-    const int m = rows < cols ? rows : cols;
+    const int m = rows < cols ? rows : cols, n = rows < cols ? cols : rows;
     OrthoParts p;
+    p.side = m > 128 ? 256 : 128;
+    const int across = (m + p.side - 1) / p.side;
+    p.tri = across * (across + 1) / 2;
+    p.slices = gram_slices((long long)count * p.tri, (n + 63) / 64, p.side);
     p.ldx = (cols + 7) / 8 * 8;
     p.ldm = (m + 7) / 8 * 8;
     size_t at = 0;
@@ -77,6 +97,7 @@ inline OrthoParts ortho_parts(int count, int rows, int cols) {
     p.a = take(s), p.b = take(s);
     p.diag = take((size_t)count * m * 4);
     p.sums = take((size_t)count * kOrthoParts * 3 * 4);
+    p.gram = take((size_t)count * p.tri * p.slices * p.side * p.side * 4);
     p.total = at;
     return p;
 }
