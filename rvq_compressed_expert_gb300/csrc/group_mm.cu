@@ -72,20 +72,6 @@ struct Offsets {
     }
 };
 
-struct Out {
-    CUtensorMap map; // over the whole result
-    void *p;
-    int N, dtype, add;
-    cudaError_t set(void *out, int rows, int cols, int type, int accumulate) {
-        p = out, N = cols, dtype = type, add = accumulate;
-        return dense::store_map(&map, out, (int)dense::type_size(type), rows, cols);
-    }
-    // a copy writes 32 whole rows: others would be another expert's
-    template <int W> __device__ __forceinline__ void put(Out32 &o, int n, const float (&v)[W]) const {
-        dense::put32_as(dtype, o, !add && o.rows >= 32 ? &map : nullptr, p, N, n, N, true, add, v);
-    }
-};
-
 // Results by row: y (W K-major) and dx (W MN-major).
 template <int kCG, bool kWmn> struct RowsJob {
     static constexpr bool kAmn = false, kBmn = kWmn, kMask = false;
@@ -120,8 +106,12 @@ template <int kCG, bool kWmn> struct RowsJob {
         T.rows = n - mi * kHigh;
         return T;
     }
-    template <int W> __device__ __forceinline__ void tile(Out32 &o, const Spot &, int n, const float (&v)[W]) const {
-        out.put(o, n, v);
+    using Held = Out::Held;
+    using In = float[32];
+    __device__ __forceinline__ void fetch(const Out32 &o, const Spot &, int n, Held &h) const { out.fetch(o, n, h); }
+    __device__ __forceinline__ void turn(Out32 &o, const Held &h, In &in) const { out.turn(o, h, in); }
+    __device__ __forceinline__ void tile(Out32 &o, const Spot &, int n, const float (&v)[32], const In &in) const {
+        out.put(o, n, v, in);
     }
 };
 
@@ -149,9 +139,12 @@ struct WeightsJob {
         T.rows = M - mi * kBM;
         return T;
     }
-    template <int W> __device__ __forceinline__ void tile(Out32 &o, const Spot &T, int n, const float (&v)[W]) const {
-        if (T.pieces == 0 && out.add) return;
-        out.put(o, n, v);
+    using Held = Out::Held;
+    using In = float[32];
+    __device__ __forceinline__ void fetch(const Out32 &o, const Spot &, int n, Held &h) const { out.fetch(o, n, h); }
+    __device__ __forceinline__ void turn(Out32 &o, const Held &h, In &in) const { out.turn(o, h, in); }
+    __device__ __forceinline__ void tile(Out32 &o, const Spot &T, int n, const float (&v)[32], const In &in) const {
+        if (T.pieces || !out.add) out.put(o, n, v, in);
     }
 };
 

@@ -7,6 +7,8 @@
 // in fp32: near the end it is the largest part of B, and its rounding would be the largest error (1.7e-3 with
 // it in fp16, 0.9e-3 without, G Gaussian).  The diagonal multiplies hi while noise can still grow, so that
 // B X stays in X's space, and hi + lo in the last two steps.
+#include <type_traits>
+
 #include "tile_mma.cuh"
 
 namespace wm {
@@ -17,34 +19,40 @@ namespace {
 constexpr float kUp = 1024.f, kDown = 1.f / 1024.f;
 constexpr int kFlat = 256; // threads of the kernels that are not products
 
-__device__ __forceinline__ float value(const void *p, int dtype, size_t i) {
-    if (dtype == WASTE_ACT_F32) return static_cast<const float *>(p)[i];
-    if (dtype == WASTE_ACT_BF16) return (float)static_cast<const __nv_bfloat16 *>(p)[i];
-    return (float)static_cast<const __half *>(p)[i];
+template <class T, int V> struct alignas(V == 8 ? 16 : sizeof(T)) Piece {
+    T v[V];
+};
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
 }
 
-// Sums of squares of each matrix, in three ranges so that none leaves fp32: below 2^-45 times 2^80, past 2^45 times
-// 2^-80, and the rest (NaN among it).  sums [count][kOrthoParts][3].
-__global__ void __launch_bounds__(kFlat) squares_kernel(const void *g, int dtype, int64_t size, float *sums) {
+// Sums of squares of each matrix (`size` values, in pieces of V), in three ranges so that none leaves fp32: below 2^-45
+// times 2^80, past 2^45 times 2^-80, and the rest (NaN among it).  sums [count][kOrthoParts][3].
+template <class T, int V>
+__global__ void __launch_bounds__(kFlat) squares_kernel(const T *g, int64_t size, float *sums) {
     __shared__ float part[3][kFlat / 32];
     tc::grid_wait_release();
-    const int64_t i0 = size * blockIdx.x / kOrthoParts, i1 = size * (blockIdx.x + 1) / kOrthoParts;
-    const size_t at = (size_t)blockIdx.y * size;
+    const int64_t n = size / V, i0 = n * blockIdx.x / kOrthoParts, i1 = n * (blockIdx.x + 1) / kOrthoParts;
+    const Piece<T, V> *p = reinterpret_cast<const Piece<T, V> *>(g + (size_t)blockIdx.y * size);
     float s[3] = {0.f, 0.f, 0.f};
+#pragma unroll 4
     for (int64_t i = i0 + threadIdx.x; i < i1; i += kFlat) {
-        const float v = value(g, dtype, at + i), m = fabsf(v);
-        const float up = v * 0x1p80f, down = v * 0x1p-80f;
-        if (m < 0x1p-45f)
-            s[0] = fmaf(up, up, s[0]);
-        else if (m > 0x1p45f)
-            s[1] = fmaf(down, down, s[1]);
-        else
-            s[2] = fmaf(v, v, s[2]);
+        const Piece<T, V> q = p[i];
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const float v = (float)q.v[k], m = fabsf(v);
+            const bool low = m < 0x1p-45f, high = m > 0x1p45f;
+            const float x = low ? v * 0x1p80f : high ? v * 0x1p-80f : v;
+            s[0] = fmaf(low ? x : 0.f, x, s[0]);
+            s[1] = fmaf(high ? x : 0.f, x, s[1]);
+            s[2] = fmaf(low || high ? 0.f : x, low || high ? 0.f : x, s[2]);
+        }
     }
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-#pragma unroll
-        for (int o = 16; o; o >>= 1) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
+        s[k] = warp_sum(s[k]);
         if ((threadIdx.x & 31) == 0) part[k][threadIdx.x >> 5] = s[k];
     }
     __syncthreads();
@@ -55,41 +63,58 @@ __global__ void __launch_bounds__(kFlat) squares_kernel(const void *g, int dtype
     }
 }
 
-// 2^10 G / |G| in two parts.
+// What G is multiplied with: |G| = f 2^e with 0.5 <= f < 1, so by two exact powers of two, then by 2^10 / f.
+struct Factor {
+    float a, b, f;
+    __device__ __forceinline__ float operator()(float v) const { return v * a * b * f; }
+};
+// From sums[0 .. kOrthoParts][3]; by one warp.
+__device__ __forceinline__ Factor factor_of(const float *sums) {
+    double s = 0.;
+    for (int i = threadIdx.x & 31; i < kOrthoParts; i += 32)
+        s += (double)sums[3 * i] * 0x1p-160 + (double)sums[3 * i + 1] * 0x1p160 + (double)sums[3 * i + 2];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    s = sqrt(s);
+    int e = 0;
+    const double f = frexp(s, &e);
+    const bool bad = isnan(s) || isinf(s);
+    if (bad) e = 0;
+    const int h = -e / 2;
+    return Factor{(float)ldexp(1., h), (float)ldexp(1., -e - h),
+                  bad ? __int_as_float(0x7fc00000) : s == 0. ? 0.f : (float)((double)kUp / f)};
+}
+
+// 2^10 G / |G| in two parts, V columns at a time.
+template <class T, int V>
 __global__ void __launch_bounds__(kFlat)
-    start_kernel(const void *g, int dtype, int rows, int cols, int ldx, const float *sums, __half *hi, __half *lo) {
-    __shared__ double part[kOrthoParts];
-    __shared__ float factor, two_a, two_b;
+    start_kernel(const T *g, int rows, int cols, int ldx, const float *sums, __half *hi, __half *lo) {
+    __shared__ Factor shared;
     tc::grid_wait_release();
-    const float *mine = sums + (size_t)blockIdx.y * kOrthoParts * 3;
-    if (threadIdx.x < kOrthoParts) {
-        const float *p = mine + threadIdx.x * 3;
-        part[threadIdx.x] = (double)p[0] * 0x1p-160 + (double)p[1] * 0x1p160 + (double)p[2];
+    if (threadIdx.x < 32) {
+        const Factor f = factor_of(sums + (size_t)blockIdx.y * kOrthoParts * 3);
+        if (threadIdx.x == 0) shared = f;
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-        double s = 0.;
-        for (int i = 0; i < kOrthoParts; ++i) s += part[i];
-        s = sqrt(s);
-        // |G| = f 2^e, 0.5 <= f < 1: G 2^-e by two exact powers of two, then 1 / f
-        int e = 0;
-        const double f = frexp(s, &e);
-        const bool bad = isnan(s) || isinf(s);
-        factor = bad ? __int_as_float(0x7fc00000) : s == 0. ? 0.f : (float)((double)kUp / f);
-        const int h = bad ? 0 : -e / 2;
-        two_a = (float)ldexp(1., h);
-        two_b = (float)ldexp(1., (bad ? 0 : -e) - h);
-    }
-    __syncthreads();
-    const float f = factor, ta = two_a, tb = two_b;
-    const int64_t n = (int64_t)rows * ldx;
+    const Factor f = shared;
+    const int per = ldx / V;
+    const int64_t n = (int64_t)rows * per;
+    g += (size_t)blockIdx.y * rows * cols;
+#pragma unroll 2
     for (int64_t i = (int64_t)blockIdx.x * kFlat + threadIdx.x; i < n; i += (int64_t)gridDim.x * kFlat) {
-        const int r = (int)(i / ldx), c = (int)(i - (int64_t)r * ldx);
-        float v = c < cols ? value(g, dtype, (size_t)blockIdx.y * rows * cols + (size_t)r * cols + c) * ta * tb * f : 0.f;
-        const __half h = __float2half_rn(v);
+        const int r = (int)(i / per), c = (int)(i - (int64_t)r * per) * V;
+        Piece<T, V> q = {};
+        if (V > 1 || c < cols) q = *reinterpret_cast<const Piece<T, V> *>(g + (size_t)r * cols + c);
+        Piece<__half, V> h, l;
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const float v = f((float)q.v[k]);
+            h.v[k] = __float2half_rn(v);
+            l.v[k] = __float2half_rn(v - __half2float(h.v[k]));
+        }
         const size_t to = (size_t)blockIdx.y * n + i;
-        hi[to] = h;
-        lo[to] = __float2half_rn(v - __half2float(h));
+        reinterpret_cast<Piece<__half, V> *>(hi)[to] = h;
+        reinterpret_cast<Piece<__half, V> *>(lo)[to] = l;
     }
 }
 
@@ -118,17 +143,10 @@ struct Stack {
         return T;
     }
 };
-// 32 rows x W columns of fp16 (rows of `ld`, a multiple of 8) as floats.
-template <int W> __device__ __forceinline__ void halves(Out32 &o, const void *p, int ld, int n, float (&v)[W]) {
-    uint4 q[W / 8];
-    dense::get32<W>(o, p, ld, n, ld, q);
-#pragma unroll
-    for (int i = 0; i < W / 8; ++i) dense::widen8(false, q[i], *reinterpret_cast<float(*)[8]>(&v[8 * i]));
-}
-template <int W>
-__device__ __forceinline__ void put_halves(Out32 &o, const CUtensorMap *map, void *p, int ld, int n, const float (&v)[W]) {
+__device__ __forceinline__ void put_halves(Out32 &o, const CUtensorMap *map, void *p, int ld, int n, const float (&v)[32]) {
     dense::put32_as(WASTE_ACT_F16, o, o.rows >= 32 ? map : nullptr, p, ld, n, ld, true, false, v);
 }
+struct Nothing {};
 
 // Tile t of those on and below a diagonal, row by row.
 __host__ __device__ __forceinline__ void triangle(int t, int &i, int &j) {
@@ -162,7 +180,11 @@ template <bool kMn> struct GramJob {
         T.rows = side;
         return T;
     }
-    template <int W> __device__ __forceinline__ void tile(Out32 &o, const Spot &, int n, const float (&v)[W]) const {
+    using Held = Nothing;
+    using In = Nothing;
+    __device__ __forceinline__ void fetch(const Out32 &, const Spot &, int, Held &) const {}
+    __device__ __forceinline__ void turn(Out32 &, const Held &, In &) const {}
+    __device__ __forceinline__ void tile(Out32 &o, const Spot &, int n, const float (&v)[32], const In &) const {
         dense::put32_as(WASTE_ACT_F32, o, &to, out, side, n, side, true, false, v);
     }
 };
@@ -219,12 +241,18 @@ struct SquareJob {
     __device__ void begin(uint8_t *) const {}
     __device__ __forceinline__ int tiles(const uint8_t *) const { return s.tiles(); }
     __device__ __forceinline__ Spot spot(const uint8_t *, int t) const { return s.spot(t); }
-    template <int W> __device__ __forceinline__ void tile(Out32 &o, const Spot &T, int n, const float (&v)[W]) const {
-        float x[W];
-        halves(o, a, ldm, n, x);
+    using Held = Block<2>;
+    struct In {
+        uint4 q[4];
+    };
+    __device__ __forceinline__ void fetch(const Out32 &o, const Spot &, int n, Held &h) const { h.fetch(o, a, ldm, n, ldm); }
+    __device__ __forceinline__ void turn(Out32 &o, const Held &h, In &in) const { h.turn(o, in.q); }
+    __device__ __forceinline__ void tile(Out32 &o, const Spot &T, int n, const float (&v)[32], const In &in) const {
+        float x[32];
+        halves(in.q, false, x);
         const int row = o.m - T.az * s.M + o.lane; // of its matrix
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
+        for (int i = 0; i < 32; ++i) {
             x[i] = fmaf(c, v[i] * kDown, b * x[i]);
             if (n + i == row) {
                 if (o.lane < o.rows) diag[(size_t)o.m + o.lane] = x[i] * kDown;
@@ -235,7 +263,7 @@ struct SquareJob {
     }
 };
 // X <- a X + B X (kTall: a X + X B), the last one to the caller's memory
-template <bool kTall> struct StepJob {
+template <bool kTall, bool kLast> struct StepJob {
     static constexpr bool kAmn = false, kBmn = !kTall, kMask = false;
     CUtensorMap ta, tb, thi, tlo;
     Stack s;
@@ -245,36 +273,51 @@ template <bool kTall> struct StepJob {
     int ldx, cols;
     float a;
     int full; // the diagonal multiplies both parts
-    // last step
-    CUtensorMap tout;
-    void *out;
-    int out_dtype, add, by_map;
+    Out out; // of the last step
     float scale;
     __device__ void begin(uint8_t *) const {}
     __device__ __forceinline__ int tiles(const uint8_t *) const { return s.tiles(); }
     __device__ __forceinline__ Spot spot(const uint8_t *, int t) const { return s.spot(t); }
-    template <int W> __device__ __forceinline__ void tile(Out32 &o, const Spot &T, int n, const float (&v)[W]) const {
-        float x[W], l[W];
-        halves(o, hi, ldx, n, x);
-        halves(o, lo, ldx, n, l);
+    struct Held {
+        Block<2> hi, lo;
+        std::conditional_t<kLast, Out::Held, Nothing> base;
+    };
+    struct In {
+        uint4 hi[4], lo[4];
+        float base[kLast ? 32 : 1];
+    };
+    __device__ __forceinline__ void fetch(const Out32 &o, const Spot &, int n, Held &h) const {
+        h.hi.fetch(o, hi, ldx, n, ldx);
+        h.lo.fetch(o, lo, ldx, n, ldx);
+        if constexpr (kLast) out.fetch(o, n, h.base);
+    }
+    __device__ __forceinline__ void turn(Out32 &o, const Held &h, In &in) const {
+        h.hi.turn(o, in.hi);
+        h.lo.turn(o, in.lo);
+        if constexpr (kLast) out.turn(o, h.base, in.base);
+    }
+    __device__ __forceinline__ void tile(Out32 &o, const Spot &T, int n, const float (&v)[32], const In &in) const {
+        float x[32], l[32];
+        halves(in.hi, false, x);
+        halves(in.lo, false, l);
         const float *d = diag + (size_t)T.az * (kTall ? cols : s.M);
         float dr = 0.f;
         if (!kTall && o.lane < o.rows) dr = d[o.m - T.az * s.M + o.lane];
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
+        for (int i = 0; i < 32; ++i) {
             const float w = x[i] + l[i], dd = kTall ? (n + i < cols ? d[n + i] : 0.f) : dr;
             x[i] = fmaf(a, w, fmaf(dd, full ? w : x[i], v[i] * kDown));
         }
-        if (out) {
+        if constexpr (kLast) {
 #pragma unroll
-            for (int i = 0; i < W; ++i) x[i] *= scale;
-            dense::put32_as(out_dtype, o, by_map && o.rows >= 32 ? &tout : nullptr, out, cols, n, cols, cols % 4 == 0, add, x);
-            return;
+            for (int i = 0; i < 32; ++i) x[i] *= scale;
+            out.put(o, n, x, in.base);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) l[i] = x[i] - __half2float(__float2half_rn(x[i]));
+            put_halves(o, &thi, hi_next, ldx, n, x);
+            put_halves(o, &tlo, lo, ldx, n, l);
         }
-#pragma unroll
-        for (int i = 0; i < W; ++i) l[i] = x[i] - __half2float(__float2half_rn(x[i]));
-        put_halves(o, &thi, hi_next, ldx, n, x);
-        put_halves(o, &tlo, lo, ldx, n, l);
     }
 };
 
@@ -322,7 +365,8 @@ template <bool kTall> cudaError_t steps(const Ortho &P, const OrthoParts &W, cud
     };
     GramJob<kTall> G = {};
     SquareJob Q = {};
-    StepJob<kTall> S = {};
+    StepJob<kTall, false> S = {};
+    StepJob<kTall, true> L = {};
     G.out = parts;
     G.side = W.side, G.tri = W.tri, G.slices = W.slices, G.count = P.count, G.pieces = (n + 63) / 64;
     const long long items = (long long)P.count * W.tri * W.slices;
@@ -336,10 +380,7 @@ template <bool kTall> cudaError_t steps(const Ortho &P, const OrthoParts &W, cud
     s_map(kTall ? &S.tb : &S.ta, B, kTall ? xx.BN / xx.cg : kBM);
     o_map(&S.tlo, lo, 2, P.count * P.rows, W.ldx);
     S.lo = lo, S.diag = diag, S.ldx = W.ldx, S.cols = P.cols, S.a = P.a;
-    S.out_dtype = P.out_dtype, S.add = P.add, S.scale = P.scale * kDown;
-    const size_t size = dense::type_size(P.out_dtype);
-    S.by_map = !P.add && (size_t)P.cols * size % 16 == 0;
-    if (S.by_map) o_map(&S.tout, P.out, (int)size, P.count * P.rows, P.cols);
+    if (e == cudaSuccess) e = L.out.set(P.out, P.count * P.rows, P.cols, P.out_dtype, P.add);
     CUtensorMap ga[2], gb[2], sx[2], st[2];
     for (int i = 0; i < 2; ++i) {
         x_map(&ga[i], i, kTall ? 64 : kBM);
@@ -357,27 +398,42 @@ template <bool kTall> cudaError_t steps(const Ortho &P, const OrthoParts &W, cud
                               reinterpret_cast<__half *>(A));
         if (e == cudaSuccess) e = launch(qs.cg, qs.BN, Q, (long long)P.count * Q.s.tm * Q.s.tn, sms, s);
         if (e != cudaSuccess) break;
+        const long long tiles = (long long)P.count * S.s.tm * S.s.tn;
         (kTall ? S.ta : S.tb) = sx[from];
-        S.thi = st[from ^ 1];
-        S.hi = hi[from], S.hi_next = hi[from ^ 1];
+        S.hi = hi[from];
         S.full = i + 2 >= P.steps;
-        S.out = i + 1 == P.steps ? P.out : nullptr;
-        e = launch(xx.cg, xx.BN, S, (long long)P.count * S.s.tm * S.s.tn, sms, s);
+        if (i + 1 < P.steps) {
+            S.thi = st[from ^ 1];
+            S.hi_next = hi[from ^ 1];
+            e = launch(xx.cg, xx.BN, S, tiles, sms, s);
+        } else {
+            L.ta = S.ta, L.tb = S.tb, L.s = S.s, L.hi = S.hi, L.lo = S.lo, L.diag = S.diag, L.ldx = S.ldx, L.cols = S.cols, L.a = S.a;
+            L.full = S.full, L.scale = P.scale * kDown;
+            e = launch(xx.cg, xx.BN, L, tiles, sms, s);
+        }
     }
     return e;
+}
+
+template <class T, int V> cudaError_t start(const Ortho &P, const OrthoParts &W, cudaStream_t s) {
+    float *sums = reinterpret_cast<float *>(P.ws + W.sums);
+    const T *g = static_cast<const T *>(P.g);
+    cudaError_t e = launch_behind(squares_kernel<T, V>, dim3(kOrthoParts, P.count), dim3(kFlat), 0, s, g, (int64_t)P.rows * P.cols, sums);
+    if (e != cudaSuccess) return e;
+    const int64_t blocks = ((int64_t)P.rows * (W.ldx / V) + 2 * kFlat - 1) / (2 * kFlat), most = 16 * device_sm_count();
+    return launch_behind(start_kernel<T, V>, dim3((unsigned)(blocks < most ? blocks : most), P.count), dim3(kFlat), 0, s, g, P.rows, P.cols,
+                         W.ldx, sums, reinterpret_cast<__half *>(P.ws + W.hi[0]), reinterpret_cast<__half *>(P.ws + W.lo));
 }
 
 } // namespace
 
 cudaError_t launch_ortho(const Ortho &P, cudaStream_t s) {
     const OrthoParts W = ortho_parts(P.count, P.rows, P.cols);
-    float *sums = reinterpret_cast<float *>(P.ws + W.sums);
-    cudaError_t e = launch_behind(squares_kernel, dim3(kOrthoParts, P.count), dim3(kFlat), 0, s, P.g, P.g_dtype,
-                                  (int64_t)P.rows * P.cols, sums);
-    if (e != cudaSuccess) return e;
-    const int64_t blocks = ((int64_t)P.rows * W.ldx + 4 * kFlat - 1) / (4 * kFlat), most = 8 * device_sm_count();
-    e = launch_behind(start_kernel, dim3((unsigned)(blocks < most ? blocks : most), P.count), dim3(kFlat), 0, s, P.g, P.g_dtype, P.rows,
-                      P.cols, W.ldx, sums, reinterpret_cast<__half *>(P.ws + W.hi[0]), reinterpret_cast<__half *>(P.ws + W.lo));
+    const auto go = [&](auto t) {
+        using T = decltype(t);
+        return P.cols % 8 ? start<T, 1>(P, W, s) : start<T, 8>(P, W, s);
+    };
+    const cudaError_t e = P.g_dtype == WASTE_ACT_F32 ? go(float()) : P.g_dtype == WASTE_ACT_BF16 ? go(__nv_bfloat16()) : go(__half());
     if (e != cudaSuccess) return e;
     return P.rows > P.cols ? steps<true>(P, W, s) : steps<false>(P, W, s);
 }

@@ -11,7 +11,9 @@
 //   kMask        tiles whose k ends inside a piece that holds other values: those are cleared in shared memory
 //   begin(smem)  by all threads, once what the kernel before wrote is visible; smem: P.job_bytes of its own
 //   tiles(smem), spot(smem, t): how many, and which
-//   tile<W>(out, spot, n, v): W sums of 32 rows from column n on (lane = row, all lanes together)
+//   fetch(out, spot, n, held), turn(out, held, in), tile(out, spot, n, v, in): the sums v of 32 rows and 32 columns
+//                from n on (lane = row, all lanes together), with what the epilogue reads besides: asked for ahead of
+//                the sums (held), then brought to the lanes' rows (in)
 // Waits are bounded, as dense_gemm.cuh's.
 #pragma once
 
@@ -57,6 +59,88 @@ __device__ __forceinline__ void tma_load3_pair(uint32_t dst, const CUtensorMap *
                  "l"(m), "r"(mbar), "r"(x), "r"(y), "r"(z)
                  : "memory");
 }
+
+// 32 rows x 32 columns of a matrix of 2 or 4 byte values, on their way: consecutive lanes hold consecutive 16 bytes of a
+// row (rows of whole 16-byte pieces; zeros past the ends), to be turned round in shared memory.
+template <int kBytes> struct Block {
+    static constexpr int kPieces = 2 * kBytes, kPer = 16 / kBytes;
+    uint4 q[kPieces];
+    __device__ __forceinline__ void fetch(const Out32 &o, const void *src, size_t ld, int n, int N) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const int at = 32 * i + o.lane, row = at / kPieces, c = n + kPer * (at % kPieces);
+            const uint8_t *p = static_cast<const uint8_t *>(src) + ((size_t)(o.m + row) * ld + c) * kBytes;
+            q[i] = row < o.rows && c < N ? *reinterpret_cast<const uint4 *>(p) : uint4{};
+        }
+    }
+    // this lane's row: its 16-byte pieces, in order
+    __device__ __forceinline__ void turn(Out32 &o, uint4 (&out)[kPieces]) const {
+#pragma unroll
+        for (int h = 0; h < kPieces; h += 4) { // four pieces a row at a time
+            uint4 *t = o.next();
+            if constexpr (kPieces == 4) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int at = 32 * i + o.lane;
+                    t[dense::turned(at / 4, at % 4, 4)] = q[i];
+                }
+            } else {
+                // pieces h .. h + 3 of each row: of 8 lanes those 4 that hold them
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int at = 32 * i + o.lane;
+                    if (at % 8 / 4 == h / 4) t[dense::turned(at / 8, at % 4, 4)] = q[i];
+                }
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) out[h + i] = t[dense::turned(o.lane, i, 4)];
+        }
+    }
+};
+__device__ __forceinline__ void halves(const uint4 (&q)[4], bool bf16, float (&v)[32]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dense::widen8(bf16, q[i], *reinterpret_cast<float(*)[8]>(&v[8 * i]));
+}
+
+// A result in memory: written, or added to what is there.
+struct Out {
+    CUtensorMap map; // over all of it; copies write 32 whole rows
+    void *p;
+    int N, dtype, add, vec; // vec: rows of whole 16-byte pieces, for copies and blocks
+    cudaError_t set(void *out, int rows, int cols, int type, int accumulate) {
+        p = out, N = cols, dtype = type, add = accumulate;
+        vec = (size_t)cols * dense::type_size(type) % 16 == 0;
+        return vec ? dense::store_map(&map, out, (int)dense::type_size(type), rows, cols) : cudaSuccess;
+    }
+    // what is there, if it is to be added to
+    struct Held {
+        Block<4> wide;
+    };
+    __device__ __forceinline__ void fetch(const Out32 &o, int n, Held &h) const {
+        if (!add || !vec) return;
+        if (dtype == WASTE_ACT_F32)
+            h.wide.fetch(o, p, N, n, N);
+        else
+            reinterpret_cast<Block<2> &>(h.wide).fetch(o, p, N, n, N);
+    }
+    __device__ __forceinline__ void turn(Out32 &o, const Held &h, float (&base)[32]) const {
+        if (!add || !vec) return;
+        if (dtype == WASTE_ACT_F32) {
+            h.wide.turn(o, reinterpret_cast<uint4(&)[8]>(base));
+        } else {
+            uint4 q[4];
+            reinterpret_cast<const Block<2> &>(h.wide).turn(o, q);
+            halves(q, dtype == WASTE_ACT_BF16, base);
+        }
+    }
+    __device__ __forceinline__ void put(Out32 &o, int n, const float (&v)[32], const float (&base)[32]) const {
+        float x[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = add && vec ? base[i] + v[i] : v[i];
+        dense::put32_as(dtype, o, vec && o.rows >= 32 ? &map : nullptr, p, N, n, N, vec || N % 4 == 0, add && !vec, x);
+    }
+};
 
 // Bytes of a stage in one CTA of cg.
 inline uint32_t tile_stage(int BN, int cg, bool b_mn) { return dense::stage_size(BN, cg, b_mn, false); }
@@ -249,6 +333,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
             out.m = T.m + 32 * q;
             out.rows = T.rows - 32 * q;
             const int buf = it & 1, use = it >> 1;
+            typename J::Held held;
+            if (any) job.fetch(out, T, T.n + 32 * half, held);
             if (!empty) {
                 ++it;
                 bool ok = true;
@@ -262,26 +348,19 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
             }
             const uint32_t src = tmem + buf * 256 + ((uint32_t)(32 * q) << 16);
             if (any) {
-                const auto take = [&](auto width, int c) {
-                    constexpr int W = decltype(width)::value;
-                    alignas(16) uint32_t v[W];
+                for (int c = 32 * half; c < BN; c += 64) { // BN is a multiple of 32
+                    alignas(16) uint32_t v[32];
                     if (empty) {
 #pragma unroll
-                        for (int i = 0; i < W; ++i) v[i] = 0;
-                    } else if constexpr (W == 32) {
+                        for (int i = 0; i < 32; ++i) v[i] = 0;
+                    } else {
                         tc::tmem_ld32(src + c, v);
                         tc::tmem_wait_ld(v);
-                    } else {
-                        tc::tmem_ld16n(src + c, v);
-                        tc::tmem_wait_ld(v);
                     }
-                    job.template tile<W>(out, T, T.n + c, *reinterpret_cast<const float(*)[W]>(v));
-                };
-                for (int c = 32 * half; c < BN; c += 64) {
-                    if (c + 32 <= BN)
-                        take(std::integral_constant<int, 32>(), c);
-                    else
-                        take(std::integral_constant<int, 16>(), c);
+                    typename J::In in;
+                    job.turn(out, held, in);
+                    if (c + 64 < BN) job.fetch(out, T, T.n + c + 64, held);
+                    job.tile(out, T, T.n + c, *reinterpret_cast<const float(*)[32]>(v), in);
                 }
             }
             if (!empty) {
