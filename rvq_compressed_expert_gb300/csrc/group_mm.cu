@@ -108,6 +108,9 @@ template <int kCG, bool kWmn> struct RowsJob {
     }
     using Held = Out::Held;
     using In = float[32];
+    __device__ __forceinline__ void ahead(const Spot &T, int r, int half, int BN) const {
+        if (r < T.rows) out.ahead(T.m + r, T.n, half, BN);
+    }
     __device__ __forceinline__ void fetch(const Out32 &o, const Spot &, int n, Held &h) const { out.fetch(o, n, h); }
     __device__ __forceinline__ void turn(Out32 &o, const Held &h, In &in) const { out.turn(o, h, in); }
     __device__ __forceinline__ void tile(Out32 &o, const Spot &, int n, const float (&v)[32], const In &in) const {
@@ -141,6 +144,9 @@ struct WeightsJob {
     }
     using Held = Out::Held;
     using In = float[32];
+    __device__ __forceinline__ void ahead(const Spot &T, int r, int half, int BN) const {
+        if (r < T.rows) out.ahead(T.m + r, T.n, half, BN);
+    }
     __device__ __forceinline__ void fetch(const Out32 &o, const Spot &, int n, Held &h) const { out.fetch(o, n, h); }
     __device__ __forceinline__ void turn(Out32 &o, const Held &h, In &in) const { out.turn(o, h, in); }
     __device__ __forceinline__ void tile(Out32 &o, const Spot &T, int n, const float (&v)[32], const In &in) const {

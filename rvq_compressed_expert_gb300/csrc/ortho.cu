@@ -6,7 +6,8 @@
 // every step makes it 3.4 times larger (4 % for rank 8, 15 % for rank 1).  B = b A + c A^2 keeps its diagonal apart
 // in fp32: near the end it is the largest part of B, and its rounding would be the largest error (1.7e-3 with
 // it in fp16, 0.9e-3 without, G Gaussian).  The diagonal multiplies hi while noise can still grow, so that
-// B X stays in X's space, and hi + lo in the last two steps.
+// B X stays in X's space, and hi + lo in the last step but one.  The last step takes hi alone: what its rounding leaves
+// is not multiplied by a step any more.
 #include <type_traits>
 
 #include "tile_mma.cuh"
@@ -28,61 +29,85 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
+// A sum over the CTA, in thread 0.
+__device__ __forceinline__ float block_sum(float v, float *part) {
+    v = warp_sum(v);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    if (threadIdx.x == 0)
+        for (int w = 1; w < kFlat / 32; ++w) v += part[w];
+    return v;
+}
+
 // Sums of squares of each matrix (`size` values, in pieces of V), in three ranges so that none leaves fp32: below 2^-45
-// times 2^80, past 2^45 times 2^-80, and the rest (NaN among it).  sums [count][kOrthoParts][3].
+// times 2^80, past 2^45 times 2^-80, and the rest (NaN among it).  sums [count][kOrthoParts][3].  A share whose
+// largest magnitude is in the middle range takes one sum of all: what underflows there is nothing beside it.
 template <class T, int V>
 __global__ void __launch_bounds__(kFlat) squares_kernel(const T *g, int64_t size, float *sums) {
-    __shared__ float part[3][kFlat / 32];
+    __shared__ float part[kFlat / 32];
+    __shared__ int rare;
     tc::grid_wait_release();
     const int64_t n = size / V, i0 = n * blockIdx.x / kOrthoParts, i1 = n * (blockIdx.x + 1) / kOrthoParts;
     const Piece<T, V> *p = reinterpret_cast<const Piece<T, V> *>(g + (size_t)blockIdx.y * size);
-    float s[3] = {0.f, 0.f, 0.f};
+    float s[3] = {0.f, 0.f, 0.f}, most = 0.f;
 #pragma unroll 4
     for (int64_t i = i0 + threadIdx.x; i < i1; i += kFlat) {
         const Piece<T, V> q = p[i];
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-            const float v = (float)q.v[k], m = fabsf(v);
-            const bool low = m < 0x1p-45f, high = m > 0x1p45f;
-            const float x = low ? v * 0x1p80f : high ? v * 0x1p-80f : v;
-            s[0] = fmaf(low ? x : 0.f, x, s[0]);
-            s[1] = fmaf(high ? x : 0.f, x, s[1]);
-            s[2] = fmaf(low || high ? 0.f : x, low || high ? 0.f : x, s[2]);
+            const float v = (float)q.v[k];
+            most = fmaxf(most, fabsf(v));
+            s[2] = fmaf(v, v, s[2]);
+        }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    if (threadIdx.x == 0) rare = 0;
+    __syncthreads();
+    if (most > 0x1p45f) rare = 1;
+    if (!__syncthreads_or(most >= 0x1p-45f) && threadIdx.x == 0) rare = 1;
+    __syncthreads();
+    if (rare) {
+        s[2] = 0.f;
+        for (int64_t i = i0 + threadIdx.x; i < i1; i += kFlat) {
+            const Piece<T, V> q = p[i];
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                const float v = (float)q.v[k], m = fabsf(v), up = v * 0x1p80f, down = v * 0x1p-80f;
+                if (m < 0x1p-45f)
+                    s[0] = fmaf(up, up, s[0]);
+                else if (m > 0x1p45f)
+                    s[1] = fmaf(down, down, s[1]);
+                else
+                    s[2] = fmaf(v, v, s[2]);
+            }
         }
     }
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-        s[k] = warp_sum(s[k]);
-        if ((threadIdx.x & 31) == 0) part[k][threadIdx.x >> 5] = s[k];
-    }
-    __syncthreads();
-    if (threadIdx.x < 3) {
-        float v = 0.f;
-        for (int w = 0; w < kFlat / 32; ++w) v += part[threadIdx.x][w];
-        sums[((size_t)blockIdx.y * kOrthoParts + blockIdx.x) * 3 + threadIdx.x] = v;
+        const float v = block_sum(s[k], part);
+        if (threadIdx.x == 0) sums[((size_t)blockIdx.y * kOrthoParts + blockIdx.x) * 3 + k] = v;
     }
 }
 
-// What G is multiplied with: |G| = f 2^e with 0.5 <= f < 1, so by two exact powers of two, then by 2^10 / f.
+// What G is multiplied with: |G| = f 2^e, 1/2 <= f < 2, so by two exact powers of two, then by 2^10 / f.
 struct Factor {
     float a, b, f;
     __device__ __forceinline__ float operator()(float v) const { return v * a * b * f; }
 };
-// From sums[0 .. kOrthoParts][3]; by one warp.
-__device__ __forceinline__ Factor factor_of(const float *sums) {
-    double s = 0.;
-    for (int i = threadIdx.x & 31; i < kOrthoParts; i += 32)
-        s += (double)sums[3 * i] * 0x1p-160 + (double)sums[3 * i + 1] * 0x1p160 + (double)sums[3 * i + 2];
-#pragma unroll
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    s = sqrt(s);
-    int e = 0;
-    const double f = frexp(s, &e);
-    const bool bad = isnan(s) || isinf(s);
-    if (bad) e = 0;
-    const int h = -e / 2;
-    return Factor{(float)ldexp(1., h), (float)ldexp(1., -e - h),
-                  bad ? __int_as_float(0x7fc00000) : s == 0. ? 0.f : (float)((double)kUp / f)};
+__device__ __forceinline__ float power(int e) { return __int_as_float((e + 127) << 23); } // -126 .. 127
+// From the sum in the three ranges.
+__device__ __forceinline__ Factor factor_of(float low, float high, float rest) {
+    // |G|^2 = s 2^(2 shift)
+    const int shift = high > 0.f ? 80 : rest > 0.f ? 0 : -80;
+    const float s = high > 0.f ? high + rest * 0x1p-80f * 0x1p-80f : rest > 0.f ? rest + low * 0x1p-80f * 0x1p-80f : low;
+    if (!isfinite(s + rest)) return Factor{1.f, 1.f, __int_as_float(0x7fc00000)};
+    if (s == 0.f) return Factor{1.f, 1.f, 0.f};
+    const float r = sqrtf(s); // 2^-75 .. 2^64: a normal number
+    const int e = ((__float_as_int(r) >> 23) & 255) - 127;
+    const int down = -e - shift, half = down / 2; // within -144 .. 155
+    return Factor{power(half), power(down - half), kUp / (r * power(-e))};
 }
 
 // 2^10 G / |G| in two parts, V columns at a time.
@@ -90,19 +115,26 @@ template <class T, int V>
 __global__ void __launch_bounds__(kFlat)
     start_kernel(const T *g, int rows, int cols, int ldx, const float *sums, __half *hi, __half *lo) {
     __shared__ Factor shared;
+    __shared__ float part[kFlat / 32];
     tc::grid_wait_release();
-    if (threadIdx.x < 32) {
-        const Factor f = factor_of(sums + (size_t)blockIdx.y * kOrthoParts * 3);
-        if (threadIdx.x == 0) shared = f;
-    }
+    float all[3] = {0.f, 0.f, 0.f};
+    sums += (size_t)blockIdx.y * kOrthoParts * 3;
+#pragma unroll
+    for (int i = threadIdx.x; i < kOrthoParts; i += kFlat)
+#pragma unroll
+        for (int k = 0; k < 3; ++k) all[k] += sums[3 * i + k];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) all[k] = block_sum(all[k], part);
+    if (threadIdx.x == 0) shared = factor_of(all[0], all[1], all[2]);
     __syncthreads();
     const Factor f = shared;
-    const int per = ldx / V;
+    const uint32_t per = ldx / V;
     const int64_t n = (int64_t)rows * per;
     g += (size_t)blockIdx.y * rows * cols;
 #pragma unroll 2
     for (int64_t i = (int64_t)blockIdx.x * kFlat + threadIdx.x; i < n; i += (int64_t)gridDim.x * kFlat) {
-        const int r = (int)(i / per), c = (int)(i - (int64_t)r * per) * V;
+        const uint32_t r = n >> 32 ? (uint32_t)(i / per) : (uint32_t)i / per;
+        const int c = (int)(i - (int64_t)r * per) * V;
         Piece<T, V> q = {};
         if (V > 1 || c < cols) q = *reinterpret_cast<const Piece<T, V> *>(g + (size_t)r * cols + c);
         Piece<__half, V> h, l;
@@ -182,6 +214,7 @@ template <bool kMn> struct GramJob {
     }
     using Held = Nothing;
     using In = Nothing;
+    __device__ __forceinline__ void ahead(const Spot &, int, int, int) const {}
     __device__ __forceinline__ void fetch(const Out32 &, const Spot &, int, Held &) const {}
     __device__ __forceinline__ void turn(Out32 &, const Held &, In &) const {}
     __device__ __forceinline__ void tile(Out32 &o, const Spot &, int n, const float (&v)[32], const In &) const {
@@ -245,6 +278,7 @@ struct SquareJob {
     struct In {
         uint4 q[4];
     };
+    __device__ __forceinline__ void ahead(const Spot &, int, int, int) const {}
     __device__ __forceinline__ void fetch(const Out32 &o, const Spot &, int n, Held &h) const { h.fetch(o, a, ldm, n, ldm); }
     __device__ __forceinline__ void turn(Out32 &o, const Held &h, In &in) const { h.turn(o, in.q); }
     __device__ __forceinline__ void tile(Out32 &o, const Spot &T, int n, const float (&v)[32], const In &in) const {
@@ -272,12 +306,20 @@ template <bool kTall, bool kLast> struct StepJob {
     const float *diag;
     int ldx, cols;
     float a;
-    int full; // the diagonal multiplies both parts
+    int full;    // the diagonal multiplies both parts
+    int keep_lo; // the next step takes both
     Out out; // of the last step
     float scale;
     __device__ void begin(uint8_t *) const {}
     __device__ __forceinline__ int tiles(const uint8_t *) const { return s.tiles(); }
     __device__ __forceinline__ Spot spot(const uint8_t *, int t) const { return s.spot(t); }
+    __device__ __forceinline__ void ahead(const Spot &T, int r, int half, int BN) const {
+        if (r >= T.rows) return;
+        const int w = min(BN, ldx - T.n);
+        if (w > 0 && !(kLast && half))
+            ask_l2(static_cast<const __half *>(half ? static_cast<const void *>(lo) : hi) + (size_t)(T.m + r) * ldx + T.n, w * 2);
+        if constexpr (kLast) out.ahead(T.m + r, T.n, half, BN);
+    }
     struct Held {
         Block<2> hi, lo;
         std::conditional_t<kLast, Out::Held, Nothing> base;
@@ -288,24 +330,24 @@ template <bool kTall, bool kLast> struct StepJob {
     };
     __device__ __forceinline__ void fetch(const Out32 &o, const Spot &, int n, Held &h) const {
         h.hi.fetch(o, hi, ldx, n, ldx);
-        h.lo.fetch(o, lo, ldx, n, ldx);
+        if constexpr (!kLast) h.lo.fetch(o, lo, ldx, n, ldx);
         if constexpr (kLast) out.fetch(o, n, h.base);
     }
     __device__ __forceinline__ void turn(Out32 &o, const Held &h, In &in) const {
         h.hi.turn(o, in.hi);
-        h.lo.turn(o, in.lo);
+        if constexpr (!kLast) h.lo.turn(o, in.lo);
         if constexpr (kLast) out.turn(o, h.base, in.base);
     }
     __device__ __forceinline__ void tile(Out32 &o, const Spot &T, int n, const float (&v)[32], const In &in) const {
         float x[32], l[32];
         halves(in.hi, false, x);
-        halves(in.lo, false, l);
+        if constexpr (!kLast) halves(in.lo, false, l);
         const float *d = diag + (size_t)T.az * (kTall ? cols : s.M);
         float dr = 0.f;
         if (!kTall && o.lane < o.rows) dr = d[o.m - T.az * s.M + o.lane];
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-            const float w = x[i] + l[i], dd = kTall ? (n + i < cols ? d[n + i] : 0.f) : dr;
+            const float w = kLast ? x[i] : x[i] + l[i], dd = kTall ? (n + i < cols ? d[n + i] : 0.f) : dr;
             x[i] = fmaf(a, w, fmaf(dd, full ? w : x[i], v[i] * kDown));
         }
         if constexpr (kLast) {
@@ -316,17 +358,18 @@ template <bool kTall, bool kLast> struct StepJob {
 #pragma unroll
             for (int i = 0; i < 32; ++i) l[i] = x[i] - __half2float(__float2half_rn(x[i]));
             put_halves(o, &thi, hi_next, ldx, n, x);
-            put_halves(o, &tlo, lo, ldx, n, l);
+            if (keep_lo) put_halves(o, &tlo, lo, ldx, n, l);
         }
     }
 };
 
-// Tiles of 128 * cg x BN for `count` results of M x N: the quickest by whole waves of tiles, each as long as its bytes
-// need into an SM (80 B/ns) or its MMAs take.
+// Tiles of 128 * cg x BN for `count` results of M x N over `pieces` of k: the quickest by whole waves of tiles, each as
+// long as its operands and what its epilogue reads (`extra` bytes a value) need into an SM (100 B/ns) or as its
+// MMAs take.  An MN-major B comes in columns of 64.
 struct Shape {
     int cg, BN;
 };
-Shape shape(int count, int M, int N, int sms) {
+Shape shape(int count, int M, int N, int pieces, bool b_mn, int extra, int sms) {
     Shape best{1, 64};
     double least = 1e30;
     for (int cg = 1; cg <= 2; ++cg)
@@ -334,8 +377,9 @@ Shape shape(int count, int M, int N, int sms) {
             if (cg == 2 && M <= kBM) continue;
             if (BN > 64 && BN - 32 >= N) break;
             const long long tiles = (long long)count * ((M + kBM * cg - 1) / (kBM * cg)) * ((N + BN - 1) / BN), slots = sms / cg;
-            const double load = (kBM + BN / cg) * kRowBytes / 80., mma = BN * 1.31;
-            const double t = (double)((tiles + slots - 1) / slots) * (load > mma ? load : mma);
+            const double in = pieces * (kBM * kRowBytes + (double)dense::stage_b_bytes(BN, cg, b_mn)) + kBM * BN * extra;
+            const double load = in / 100., mma = pieces * BN * 1.31, out = kBM * BN * 0.1; // the last tile's epilogue
+            const double t = (double)((tiles + slots - 1) / slots) * (load > mma ? load : mma) + out;
             if (t < least) least = t, best = Shape{cg, BN};
         }
     return best;
@@ -351,7 +395,8 @@ template <bool kTall> cudaError_t steps(const Ortho &P, const OrthoParts &W, cud
     uint8_t *hi[2] = {P.ws + W.hi[0], P.ws + W.hi[1]}, *lo = P.ws + W.lo, *A = P.ws + W.a, *B = P.ws + W.b;
     float *diag = reinterpret_cast<float *>(P.ws + W.diag), *parts = reinterpret_cast<float *>(P.ws + W.gram);
     const size_t xs = (size_t)P.rows * W.ldx, ss = (size_t)m * W.ldm;
-    const Shape qs = shape(P.count, m, m, sms), xx = shape(P.count, P.rows, P.cols, sms);
+    const int pieces = (m + 63) / 64;
+    const Shape qs = shape(P.count, m, m, pieces, false, 2, sms), xx = shape(P.count, P.rows, P.cols, pieces, !kTall, 4, sms);
     const int gcg = W.side == 256 ? 2 : 1;
     cudaError_t e = cudaSuccess;
     const auto x_map = [&](CUtensorMap *t, int i, int box) {
@@ -404,6 +449,7 @@ template <bool kTall> cudaError_t steps(const Ortho &P, const OrthoParts &W, cud
         S.full = i + 2 >= P.steps;
         if (i + 1 < P.steps) {
             S.thi = st[from ^ 1];
+            S.keep_lo = i + 2 < P.steps;
             S.hi_next = hi[from ^ 1];
             e = launch(xx.cg, xx.BN, S, tiles, sms, s);
         } else {

@@ -11,6 +11,7 @@
 //   kMask        tiles whose k ends inside a piece that holds other values: those are cleared in shared memory
 //   begin(smem)  by all threads, once what the kernel before wrote is visible; smem: P.job_bytes of its own
 //   tiles(smem), spot(smem, t): how many, and which
+//   ahead(spot, r, half, BN): row r of a later tile will be read besides: may be asked of L2 (two lanes a row)
 //   fetch(out, spot, n, held), turn(out, held, in), tile(out, spot, n, v, in): the sums v of 32 rows and 32 columns
 //                from n on (lane = row, all lanes together), with what the epilogue reads besides: asked for ahead of
 //                the sums (held), then brought to the lanes' rows (in)
@@ -103,6 +104,11 @@ __device__ __forceinline__ void halves(const uint4 (&q)[4], bool bf16, float (&v
     for (int i = 0; i < 4; ++i) dense::widen8(bf16, q[i], *reinterpret_cast<float(*)[8]>(&v[8 * i]));
 }
 
+// Ask L2 for `bytes` bytes from p on.
+__device__ __forceinline__ void ask_l2(const void *p, int bytes) {
+    for (int i = 0; i < bytes; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char *>(p) + i));
+}
+
 // A result in memory: written, or added to what is there.
 struct Out {
     CUtensorMap map; // over all of it; copies write 32 whole rows
@@ -117,6 +123,12 @@ struct Out {
     struct Held {
         Block<4> wide;
     };
+    // half a row of BN columns from n on
+    __device__ __forceinline__ void ahead(size_t m, int n, int half, int BN) const {
+        if (!add) return;
+        const int size = dtype == WASTE_ACT_F32 ? 4 : 2, c = n + half * (BN / 2), cols = min(BN / 2, N - c);
+        if (cols > 0) ask_l2(static_cast<const char *>(p) + (m * N + c) * size, cols * size);
+    }
     __device__ __forceinline__ void fetch(const Out32 &o, int n, Held &h) const {
         if (!add || !vec) return;
         if (dtype == WASTE_ACT_F32)
@@ -333,6 +345,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
             out.m = T.m + 32 * q;
             out.rows = T.rows - 32 * q;
             const int buf = it & 1, use = it >> 1;
+            if (t + step < tiles) job.ahead(job.spot(mine, t + step), 32 * q + rank * kBM + lane, half, BN);
             typename J::Held held;
             if (any) job.fetch(out, T, T.n + 32 * half, held);
             if (!empty) {

@@ -56,7 +56,7 @@ struct Ortho {
 };
 // What stands in the workspace, from its start: X in two halves (the first of them twice, taken in turn), A and
 // b A + c A^2 without its diagonal, that diagonal, partial sums of squares, and A's partial sums.
-constexpr int kOrthoParts = 256; // of a matrix
+constexpr int kOrthoParts = 512; // of a matrix
 struct OrthoParts {
     size_t hi[2], lo, a, b, diag, sums, gram, total;
     int ldx, ldm;

@@ -110,7 +110,7 @@ def orthogonal_rounded(g, steps=5, coefficients=MUON):
     x = x / n if n > 0 else x
     for i in range(steps):
         h = r(x)
-        x = h + r(x - h)
+        x = h + r(x - h) if i + 1 < steps else h
         p = r(h @ h.T)
         q = b * p + c * (p @ p)
         d = torch.diagonal(q).clone()
