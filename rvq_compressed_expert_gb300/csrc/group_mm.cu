@@ -74,7 +74,7 @@ struct Offsets {
 
 // Results by row: y (W K-major) and dx (W MN-major).
 template <int kCG, bool kWmn> struct RowsJob {
-    static constexpr bool kAmn = false, kBmn = kWmn, kMask = false;
+    static constexpr bool kAmn = false, kBmn = kWmn, kMask = false, kReads = true;
     CUtensorMap ta, tb;
     Out out;
     Offsets off;
@@ -112,7 +112,7 @@ template <int kCG, bool kWmn> struct RowsJob {
         if (r < T.rows) out.ahead(T.m + r, T.n, half, BN);
     }
     __device__ __forceinline__ void fetch(const Out32 &o, const Spot &, int n, Held &h) const { out.fetch(o, n, h); }
-    __device__ __forceinline__ void turn(Out32 &o, const Held &h, In &in) const { out.turn(o, h, in); }
+    __device__ __forceinline__ void turn(const Out32 &o, uint4 *t, const Held &h, In &in) const { out.turn(o, t, h, in); }
     __device__ __forceinline__ void tile(Out32 &o, const Spot &, int n, const float (&v)[32], const In &in) const {
         out.put(o, n, v, in);
     }
@@ -120,7 +120,7 @@ template <int kCG, bool kWmn> struct RowsJob {
 
 // dW: the rows are what is summed over.
 struct WeightsJob {
-    static constexpr bool kAmn = true, kBmn = true, kMask = true;
+    static constexpr bool kAmn = true, kBmn = true, kMask = true, kReads = true;
     CUtensorMap ta, tb;
     Out out;
     Offsets off;
@@ -148,7 +148,7 @@ struct WeightsJob {
         if (r < T.rows) out.ahead(T.m + r, T.n, half, BN);
     }
     __device__ __forceinline__ void fetch(const Out32 &o, const Spot &, int n, Held &h) const { out.fetch(o, n, h); }
-    __device__ __forceinline__ void turn(Out32 &o, const Held &h, In &in) const { out.turn(o, h, in); }
+    __device__ __forceinline__ void turn(const Out32 &o, uint4 *t, const Held &h, In &in) const { out.turn(o, t, h, in); }
     __device__ __forceinline__ void tile(Out32 &o, const Spot &T, int n, const float (&v)[32], const In &in) const {
         if (T.pieces || !out.add) out.put(o, n, v, in);
     }

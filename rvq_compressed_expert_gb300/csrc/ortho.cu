@@ -189,7 +189,7 @@ __host__ __device__ __forceinline__ void triangle(int t, int &i, int &j) {
 }
 // Partial sums of A = X X^T (kMn: X^T X): [matrix][share of k][tile][side][side], fp32.
 template <bool kMn> struct GramJob {
-    static constexpr bool kAmn = kMn, kBmn = kMn, kMask = false;
+    static constexpr bool kAmn = kMn, kBmn = kMn, kMask = false, kReads = false;
     CUtensorMap ta, tb, to;
     void *out;
     int side, tri, slices, count, pieces;
@@ -216,7 +216,7 @@ template <bool kMn> struct GramJob {
     using In = Nothing;
     __device__ __forceinline__ void ahead(const Spot &, int, int, int) const {}
     __device__ __forceinline__ void fetch(const Out32 &, const Spot &, int, Held &) const {}
-    __device__ __forceinline__ void turn(Out32 &, const Held &, In &) const {}
+    __device__ __forceinline__ void turn(const Out32 &, uint4 *, const Held &, In &) const {}
     __device__ __forceinline__ void tile(Out32 &o, const Spot &, int n, const float (&v)[32], const In &) const {
         dense::put32_as(WASTE_ACT_F32, o, &to, out, side, n, side, true, false, v);
     }
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kFlat) gram_kernel(const float *parts, int sid
 }
 // B = b A + c A^2, its diagonal apart
 struct SquareJob {
-    static constexpr bool kAmn = false, kBmn = false, kMask = false;
+    static constexpr bool kAmn = false, kBmn = false, kMask = false, kReads = true;
     CUtensorMap ta, tb, to;
     Stack s;
     const void *a;
@@ -280,7 +280,7 @@ struct SquareJob {
     };
     __device__ __forceinline__ void ahead(const Spot &, int, int, int) const {}
     __device__ __forceinline__ void fetch(const Out32 &o, const Spot &, int n, Held &h) const { h.fetch(o, a, ldm, n, ldm); }
-    __device__ __forceinline__ void turn(Out32 &o, const Held &h, In &in) const { h.turn(o, in.q); }
+    __device__ __forceinline__ void turn(const Out32 &o, uint4 *t, const Held &h, In &in) const { h.turn(o, t, in.q); }
     __device__ __forceinline__ void tile(Out32 &o, const Spot &T, int n, const float (&v)[32], const In &in) const {
         float x[32];
         halves(in.q, false, x);
@@ -289,7 +289,7 @@ struct SquareJob {
         for (int i = 0; i < 32; ++i) {
             x[i] = fmaf(c, v[i] * kDown, b * x[i]);
             if (n + i == row) {
-                if (o.lane < o.rows) diag[(size_t)o.m + o.lane] = x[i] * kDown;
+                if (o.lane < o.rows) diag[(size_t)T.az * ldm + row] = x[i] * kDown;
                 x[i] = 0.f;
             }
         }
@@ -298,13 +298,13 @@ struct SquareJob {
 };
 // X <- a X + B X (kTall: a X + X B), the last one to the caller's memory
 template <bool kTall, bool kLast> struct StepJob {
-    static constexpr bool kAmn = false, kBmn = !kTall, kMask = false;
+    static constexpr bool kAmn = false, kBmn = !kTall, kMask = false, kReads = true;
     CUtensorMap ta, tb, thi, tlo;
     Stack s;
     const void *hi;
     void *lo, *hi_next;
     const float *diag;
-    int ldx, cols;
+    int ldx, ldm;
     float a;
     int full;    // the diagonal multiplies both parts
     int keep_lo; // the next step takes both
@@ -333,22 +333,29 @@ template <bool kTall, bool kLast> struct StepJob {
         if constexpr (!kLast) h.lo.fetch(o, lo, ldx, n, ldx);
         if constexpr (kLast) out.fetch(o, n, h.base);
     }
-    __device__ __forceinline__ void turn(Out32 &o, const Held &h, In &in) const {
-        h.hi.turn(o, in.hi);
-        if constexpr (!kLast) h.lo.turn(o, in.lo);
-        if constexpr (kLast) out.turn(o, h.base, in.base);
+    __device__ __forceinline__ void turn(const Out32 &o, uint4 *t, const Held &h, In &in) const {
+        h.hi.turn(o, t, in.hi);
+        if constexpr (!kLast) h.lo.turn(o, t, in.lo);
+        if constexpr (kLast) out.turn(o, t, h.base, in.base);
     }
     __device__ __forceinline__ void tile(Out32 &o, const Spot &T, int n, const float (&v)[32], const In &in) const {
         float x[32], l[32];
         halves(in.hi, false, x);
         if constexpr (!kLast) halves(in.lo, false, l);
-        const float *d = diag + (size_t)T.az * (kTall ? cols : s.M);
+        const float *d = diag + (size_t)T.az * ldm;
         float dr = 0.f;
         if (!kTall && o.lane < o.rows) dr = d[o.m - T.az * s.M + o.lane];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const float w = kLast ? x[i] : x[i] + l[i], dd = kTall ? (n + i < cols ? d[n + i] : 0.f) : dr;
-            x[i] = fmaf(a, w, fmaf(dd, full ? w : x[i], v[i] * kDown));
+        for (int j = 0; j < 32; j += 4) {
+            float4 dc = {dr, dr, dr, dr};
+            if (kTall) dc = n + j < ldm ? *reinterpret_cast<const float4 *>(d + n + j) : float4{};
+            const float dd[4] = {dc.x, dc.y, dc.z, dc.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int i = j + k;
+                const float w = kLast ? x[i] : x[i] + l[i];
+                x[i] = fmaf(a, w, fmaf(dd[k], full ? w : x[i], v[i] * kDown));
+            }
         }
         if constexpr (kLast) {
 #pragma unroll
@@ -424,7 +431,7 @@ template <bool kTall> cudaError_t steps(const Ortho &P, const OrthoParts &W, cud
     S.s.set(xx.cg, xx.BN, P.count, P.rows, P.cols, m);
     s_map(kTall ? &S.tb : &S.ta, B, kTall ? xx.BN / xx.cg : kBM);
     o_map(&S.tlo, lo, 2, P.count * P.rows, W.ldx);
-    S.lo = lo, S.diag = diag, S.ldx = W.ldx, S.cols = P.cols, S.a = P.a;
+    S.lo = lo, S.diag = diag, S.ldx = W.ldx, S.ldm = W.ldm, S.a = P.a;
     if (e == cudaSuccess) e = L.out.set(P.out, P.count * P.rows, P.cols, P.out_dtype, P.add);
     CUtensorMap ga[2], gb[2], sx[2], st[2];
     for (int i = 0; i < 2; ++i) {
@@ -453,7 +460,7 @@ template <bool kTall> cudaError_t steps(const Ortho &P, const OrthoParts &W, cud
             S.hi_next = hi[from ^ 1];
             e = launch(xx.cg, xx.BN, S, tiles, sms, s);
         } else {
-            L.ta = S.ta, L.tb = S.tb, L.s = S.s, L.hi = S.hi, L.lo = S.lo, L.diag = S.diag, L.ldx = S.ldx, L.cols = S.cols, L.a = S.a;
+            L.ta = S.ta, L.tb = S.tb, L.s = S.s, L.hi = S.hi, L.lo = S.lo, L.diag = S.diag, L.ldx = S.ldx, L.ldm = S.ldm, L.a = S.a;
             L.full = S.full, L.scale = P.scale * kDown;
             e = launch(xx.cg, xx.BN, L, tiles, sms, s);
         }

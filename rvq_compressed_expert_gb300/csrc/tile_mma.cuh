@@ -8,11 +8,12 @@
 //
 // A job J (a kernel argument, with its tensor maps ta and tb) has
 //   kAmn, kBmn   operands that lie with m (or n) contiguous (MN-major) rather than k
+//   kReads       an epilogue that reads
 //   kMask        tiles whose k ends inside a piece that holds other values: those are cleared in shared memory
 //   begin(smem)  by all threads, once what the kernel before wrote is visible; smem: P.job_bytes of its own
 //   tiles(smem), spot(smem, t): how many, and which
 //   ahead(spot, r, half, BN): row r of a later tile will be read besides: may be asked of L2 (two lanes a row)
-//   fetch(out, spot, n, held), turn(out, held, in), tile(out, spot, n, v, in): the sums v of 32 rows and 32 columns
+//   fetch(out, spot, n, held), turn(out, shared, held, in), tile(out, spot, n, v, in): the sums v of 32 rows and 32 columns
 //                from n on (lane = row, all lanes together), with what the epilogue reads besides: asked for ahead of
 //                the sums (held), then brought to the lanes' rows (in)
 // Waits are bounded, as dense_gemm.cuh's.
@@ -74,11 +75,12 @@ template <int kBytes> struct Block {
             q[i] = row < o.rows && c < N ? *reinterpret_cast<const uint4 *>(p) : uint4{};
         }
     }
-    // this lane's row: its 16-byte pieces, in order
-    __device__ __forceinline__ void turn(Out32 &o, uint4 (&out)[kPieces]) const {
+    // this lane's row: its 16-byte pieces, in order.  t: the warp's own kPieceBytes (not those that copies leave from,
+    // which would have to have left)
+    __device__ __forceinline__ void turn(const Out32 &o, uint4 *t, uint4 (&out)[kPieces]) const {
 #pragma unroll
         for (int h = 0; h < kPieces; h += 4) { // four pieces a row at a time
-            uint4 *t = o.next();
+            __syncwarp();
             if constexpr (kPieces == 4) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -136,13 +138,13 @@ struct Out {
         else
             reinterpret_cast<Block<2> &>(h.wide).fetch(o, p, N, n, N);
     }
-    __device__ __forceinline__ void turn(Out32 &o, const Held &h, float (&base)[32]) const {
+    __device__ __forceinline__ void turn(const Out32 &o, uint4 *t, const Held &h, float (&base)[32]) const {
         if (!add || !vec) return;
         if (dtype == WASTE_ACT_F32) {
-            h.wide.turn(o, reinterpret_cast<uint4(&)[8]>(base));
+            h.wide.turn(o, t, reinterpret_cast<uint4(&)[8]>(base));
         } else {
             uint4 q[4];
-            reinterpret_cast<const Block<2> &>(h.wide).turn(o, q);
+            reinterpret_cast<const Block<2> &>(h.wide).turn(o, t, q);
             halves(q, dtype == WASTE_ACT_BF16, base);
         }
     }
@@ -156,6 +158,9 @@ struct Out {
 
 // Bytes of a stage in one CTA of cg.
 inline uint32_t tile_stage(int BN, int cg, bool b_mn) { return dense::stage_size(BN, cg, b_mn, false); }
+
+// Shared memory of the eight epilogue warps: two pieces each on their way out, one on its way in.
+template <class J> constexpr uint32_t kTurnBytes = 8 * (J::kReads ? 3 : 2) * kPieceBytes;
 
 template <int kCG, class J>
 __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_constant__ TileArgs P, const __grid_constant__ J job) {
@@ -175,7 +180,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
     const uint32_t stage_bytes = dense::stage_size(BN, kCG, J::kBmn, false);
     const int rank = kCG == 2 ? (int)(blockIdx.x & 1) : 0;
     const bool leads = kCG == 1 || rank == 0;
-    uint8_t *turns = smem_raw + P.stages * stage_bytes, *mine = turns + 8 * 2 * kPieceBytes;
+    uint8_t *turns = smem_raw + P.stages * stage_bytes, *mine = turns + kTurnBytes<J>;
 
     if (tid == 32) {
         for (int i = 0; i < P.stages; ++i) {
@@ -336,6 +341,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
         // ---- epilogue: two warps for each quarter of the lanes (rows); they take its pieces of 32 columns in turn
         const int q = warp & 3, half = (warp - 3) >> 2;
         Out32 out{reinterpret_cast<uint4 *>(turns) + (warp - 3) * (2 * kPieceBytes / 16), 0, 0, lane, 0};
+        uint4 *turned = reinterpret_cast<uint4 *>(turns + 8 * 2 * kPieceBytes) + (warp - 3) * (kPieceBytes / 16);
         int it = 0;
         for (int t = tile0; t < tiles; t += step) {
             Spot T = job.spot(mine, t);
@@ -371,7 +377,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
                         tc::tmem_wait_ld(v);
                     }
                     typename J::In in;
-                    job.turn(out, held, in);
+                    job.turn(out, turned, held, in);
                     if (c + 64 < BN) job.fetch(out, T, T.n + c + 64, held);
                     job.tile(out, T, T.n + c, *reinterpret_cast<const float(*)[32]>(v), in);
                 }
@@ -415,7 +421,7 @@ template <int kCG, class J>
 cudaError_t launch_tiles_as(TileArgs &P, const J &job, bool bf16, size_t job_bytes, long long tiles, int sms, cudaStream_t s) {
     static SmemAttr attr;
     const auto kernel = tile_kernel<kCG, J>;
-    const uint32_t stage = tile_stage(P.BN, kCG, J::kBmn), turn = 8 * 2 * kPieceBytes;
+    const uint32_t stage = tile_stage(P.BN, kCG, J::kBmn), turn = kTurnBytes<J>;
     P.job_bytes = (uint32_t)round_up(job_bytes, 16);
     P.stages = (int)((kSmemBudget - kBarBytes - turn - P.job_bytes) / stage);
     if (P.stages > kMaxStages) P.stages = kMaxStages;

@@ -95,7 +95,7 @@ inline OrthoParts ortho_parts(int count, int rows, int cols) {
     const size_t x = (size_t)count * rows * p.ldx * 2, s = (size_t)count * m * p.ldm * 2;
     p.hi[0] = take(x), p.hi[1] = take(x), p.lo = take(x);
     p.a = take(s), p.b = take(s);
-    p.diag = take((size_t)count * m * 4);
+    p.diag = take((size_t)count * p.ldm * 4);
     p.sums = take((size_t)count * kOrthoParts * 3 * 4);
     p.gram = take((size_t)count * p.tri * p.slices * p.side * p.side * 4);
     p.total = at;
