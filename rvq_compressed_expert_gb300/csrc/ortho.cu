@@ -40,55 +40,55 @@ __device__ __forceinline__ float block_sum(float v, float *part) {
     return v;
 }
 
-// Sums of squares of each matrix (`size` values, in pieces of V), in three ranges so that none leaves fp32: below 2^-45
-// times 2^80, past 2^45 times 2^-80, and the rest (NaN among it).  sums [count][kOrthoParts][3].  A share whose
-// largest magnitude is in the middle range takes one sum of all: what underflows there is nothing beside it.
+// Sum of squares of the values that each(f) hands to f (every thread its own, the same each time), in three ranges so
+// that none leaves fp32: below 2^-45 times 2^80, past 2^45 times 2^-80, and the rest (NaN among it); in thread 0.  Where
+// the CTA's largest magnitude is in the middle range one sum of all is enough: what underflows there is nothing
+// beside it.
+template <class F> __device__ __forceinline__ void squares_of(const F &each, float *part, float (&s)[3]) {
+    float most = 0.f;
+    s[0] = s[1] = s[2] = 0.f;
+    each([&](float v) {
+        most = fmaxf(most, fabsf(v));
+        s[2] = fmaf(v, v, s[2]);
+    });
+    const bool far = __syncthreads_or(most > 0x1p45f), some = __syncthreads_or(most >= 0x1p-45f);
+    if (far || !some) {
+        s[2] = 0.f;
+        each([&](float v) {
+            const float m = fabsf(v), up = v * 0x1p80f, down = v * 0x1p-80f;
+            if (m < 0x1p-45f)
+                s[0] = fmaf(up, up, s[0]);
+            else if (m > 0x1p45f)
+                s[1] = fmaf(down, down, s[1]);
+            else
+                s[2] = fmaf(v, v, s[2]);
+        });
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) s[k] = block_sum(s[k], part);
+}
+
+// Of each matrix (`size` values, in pieces of V): sums [count][kOrthoParts][3].
 template <class T, int V>
 __global__ void __launch_bounds__(kFlat) squares_kernel(const T *g, int64_t size, float *sums) {
     __shared__ float part[kFlat / 32];
-    __shared__ int rare;
     tc::grid_wait_release();
     const int64_t n = size / V, i0 = n * blockIdx.x / kOrthoParts, i1 = n * (blockIdx.x + 1) / kOrthoParts;
     const Piece<T, V> *p = reinterpret_cast<const Piece<T, V> *>(g + (size_t)blockIdx.y * size);
-    float s[3] = {0.f, 0.f, 0.f}, most = 0.f;
+    float s[3];
+    squares_of(
+        [&](auto f) {
 #pragma unroll 4
-    for (int64_t i = i0 + threadIdx.x; i < i1; i += kFlat) {
-        const Piece<T, V> q = p[i];
+            for (int64_t i = i0 + threadIdx.x; i < i1; i += kFlat) {
+                const Piece<T, V> q = p[i];
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-            const float v = (float)q.v[k];
-            most = fmaxf(most, fabsf(v));
-            s[2] = fmaf(v, v, s[2]);
-        }
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-    if (threadIdx.x == 0) rare = 0;
-    __syncthreads();
-    if (most > 0x1p45f) rare = 1;
-    if (!__syncthreads_or(most >= 0x1p-45f) && threadIdx.x == 0) rare = 1;
-    __syncthreads();
-    if (rare) {
-        s[2] = 0.f;
-        for (int64_t i = i0 + threadIdx.x; i < i1; i += kFlat) {
-            const Piece<T, V> q = p[i];
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                const float v = (float)q.v[k], m = fabsf(v), up = v * 0x1p80f, down = v * 0x1p-80f;
-                if (m < 0x1p-45f)
-                    s[0] = fmaf(up, up, s[0]);
-                else if (m > 0x1p45f)
-                    s[1] = fmaf(down, down, s[1]);
-                else
-                    s[2] = fmaf(v, v, s[2]);
+                for (int k = 0; k < V; ++k) f((float)q.v[k]);
             }
-        }
-    }
+        },
+        part, s);
+    if (threadIdx.x < 1)
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-        const float v = block_sum(s[k], part);
-        if (threadIdx.x == 0) sums[((size_t)blockIdx.y * kOrthoParts + blockIdx.x) * 3 + k] = v;
-    }
+        for (int k = 0; k < 3; ++k) sums[((size_t)blockIdx.y * kOrthoParts + blockIdx.x) * 3 + k] = s[k];
 }
 
 // What G is multiplied with: |G| = f 2^e, 1/2 <= f < 2, so by two exact powers of two, then by 2^10 / f.
@@ -370,6 +370,238 @@ template <bool kTall, bool kLast> struct StepJob {
     }
 };
 
+// ---- small matrices: all steps in one launch, one CTA a matrix
+//
+// X (short side first, 128 rows) stays in shared memory: hi in the layout of an MMA operand with 128-byte swizzle, which
+// serves A = X X^T with the long side as k and B X with the rows as k alike, lo in the same layout beside it.  A, and
+// B in its place, have 32 KB more.  A step is three products of a few hundred nanoseconds, each followed by its epilogue
+// and a barrier.
+constexpr int kSmallRows = 128, kSmallCols = 320;
+constexpr int kSlab = 16384; // 128 rows x 64 columns
+
+// Byte of row r, columns 8 i .. 8 i + 7 in slabs of 64 columns.
+__device__ __forceinline__ uint32_t place(int r, int i) { return (i >> 3) * kSlab + r * 128 + (((i & 7) ^ (r & 7)) << 4); }
+__device__ __forceinline__ uint4 pack_halves(const float (&v)[8]) { return dense::piece_of(v, __half()); }
+
+template <class O> __device__ __forceinline__ void put_one(O *p, float v, int add) { *p = dense::round_to<O>(add ? (float)*p + v : v); }
+__device__ __forceinline__ void put_value(void *p, int dtype, size_t i, float v, int add) {
+    if (dtype == WASTE_ACT_F32)
+        put_one(static_cast<float *>(p) + i, v, add);
+    else if (dtype == WASTE_ACT_BF16)
+        put_one(static_cast<__nv_bfloat16 *>(p) + i, v, add);
+    else
+        put_one(static_cast<__half *>(p) + i, v, add);
+}
+
+template <class T, bool kTall>
+__global__ void __launch_bounds__(kFlat)
+    small_kernel(const T *g, int m, int n, int steps, float ca, float cb, float cc, void *out, int out_dtype, int add, float scale) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
+    __shared__ float part[kFlat / 32], diag[kSmallRows];
+    __shared__ Factor shared;
+    __shared__ __align__(8) uint64_t bar_word;
+    __shared__ uint32_t tmem_slot;
+    const int slabs = (n + 63) / 64, tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    uint8_t *hi = smem, *lo = smem + slabs * kSlab, *mat = lo + slabs * kSlab;
+    const uint32_t hi_at = tc::smem_u32(hi), mat_at = tc::smem_u32(mat), bar = tc::smem_u32(&bar_word);
+    if (tid == 0) {
+        tc::mbar_init(bar, 1);
+        tc::mbar_init_fence();
+    }
+    const uint32_t columns = slabs <= 2 ? 256 : kTmemCols; // two CTAs an SM where they fit
+    if (warp == 0) tc::tmem_alloc(tc::smem_u32(&tmem_slot), columns);
+    tc::grid_wait_release();
+
+    // ---- G, by pieces of 8 of X's columns: i = tid, tid + 256, ..
+    g += (size_t)blockIdx.x * m * n;
+    const int per = slabs * 8;
+    const auto values = [&](int i, float (&v)[8]) -> uint32_t { // where they go; neighbours read neighbouring values
+        const int r = kTall ? i % kSmallRows : i / per, c = (kTall ? i / kSmallRows : i % per) * 8;
+        if (!kTall && sizeof(T) == 2 && n % 8 == 0) {
+            Piece<T, 8> q = {};
+            if (r < m && c < n) q = *reinterpret_cast<const Piece<T, 8> *>(g + r * n + c);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = (float)q.v[k];
+        } else if (!kTall && n % 4 == 0 && sizeof(T) == 4) {
+            float4 q[2] = {};
+            if (r < m && c < n) q[0] = *reinterpret_cast<const float4 *>(g + r * n + c);
+            if (r < m && c + 4 < n) q[1] = *reinterpret_cast<const float4 *>(g + r * n + c + 4);
+            v[0] = q[0].x, v[1] = q[0].y, v[2] = q[0].z, v[3] = q[0].w, v[4] = q[1].x, v[5] = q[1].y, v[6] = q[1].z, v[7] = q[1].w;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = r < m && c + k < n ? (float)g[kTall ? (c + k) * m + r : r * n + c + k] : 0.f;
+        }
+        return place(r, c / 8);
+    };
+    float s[3];
+    squares_of(
+        [&](auto f) {
+#pragma unroll 2
+            for (int i = tid; i < kSmallRows * per; i += kFlat) {
+                float v[8];
+                values(i, v);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) f(v[k]);
+            }
+        },
+        part, s);
+    if (tid == 0) shared = factor_of(s[0], s[1], s[2]);
+    __syncthreads();
+    const Factor f = shared;
+#pragma unroll 2
+    for (int i = tid; i < kSmallRows * per; i += kFlat) {
+        float v[8], l[8];
+        const uint32_t at = values(i, v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            v[k] = f(v[k]);
+            l[k] = v[k] - __half2float(__float2half_rn(v[k]));
+        }
+        *reinterpret_cast<uint4 *>(hi + at) = pack_halves(v);
+        *reinterpret_cast<uint4 *>(lo + at) = pack_halves(l);
+    }
+
+    // ---- steps
+    const int q = warp & 3, side = warp >> 2, r = 32 * q + lane; // this thread's row, and every other 32 columns of it
+    uint32_t phase = 0;
+    bool ok = true;
+    // one product: what the threads wrote is there for it, and its sums are there for them
+    const auto product = [&](auto issue) {
+        tc::fence_proxy_async();
+        tc::fence_before_sync();
+        __syncthreads();
+        tc::fence_after_sync();
+        if (warp == 0) {
+            if (tc::elect_one()) {
+                issue();
+                tc::mma_commit(bar);
+            }
+            __syncwarp();
+        }
+        const bool mine = tc::mbar_wait(bar, phase);
+        phase ^= 1;
+        ok = !__syncthreads_or(!mine);
+        tc::fence_after_sync();
+    };
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0), wide = 128; // A's and B's sums in the first 128, X's behind them
+    const uint64_t hi_desc = tc::desc_sw128(hi_at, kSlab), mat_desc = tc::desc_sw128(mat_at, kSlab);
+    constexpr uint32_t square = tc::idesc_half(kSmallRows, kSmallRows, false, false, false);
+    const auto sums = [&](uint32_t col, uint32_t (&v)[32]) {
+        tc::tmem_ld32(tmem + col + ((uint32_t)(32 * q) << 16), v);
+        tc::tmem_wait_ld(v);
+    };
+    for (int i = 0; i < steps && ok; ++i) {
+        product([&] {
+            for (int k = 0; k < 4 * slabs; ++k) {
+                const uint64_t d = hi_desc + (uint64_t)((k / 4 * kSlab + k % 4 * 32) >> 4);
+                tc::mma_f16(tmem, d, d, square, k > 0);
+            }
+        });
+        if (!ok) break;
+        for (int c = 32 * side; c < kSmallRows; c += 64) {
+            uint32_t v[32];
+            sums(c, v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float x[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(v[8 * j + k]) * kDown;
+                *reinterpret_cast<uint4 *>(mat + place(r, c / 8 + j)) = pack_halves(x);
+            }
+        }
+        product([&] {
+            for (int k = 0; k < 8; ++k) {
+                const uint64_t d = mat_desc + (uint64_t)((k / 4 * kSlab + k % 4 * 32) >> 4);
+                tc::mma_f16(tmem, d, d, square, k > 0);
+            }
+        });
+        if (!ok) break;
+        for (int c = 32 * side; c < kSmallRows; c += 64) {
+            uint32_t v[32];
+            sums(c, v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint4 *at = reinterpret_cast<uint4 *>(mat + place(r, c / 8 + j));
+                float x[8];
+                dense::widen8(false, *at, x);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    x[k] = fmaf(cc, __uint_as_float(v[8 * j + k]) * kDown, cb * x[k]);
+                    if (c + 8 * j + k == r) {
+                        diag[r] = x[k] * kDown;
+                        x[k] = 0.f;
+                    }
+                }
+                *at = pack_halves(x);
+            }
+        }
+        product([&] {
+            for (int h = 0; h < slabs; h += 4) { // 256 columns at most in one MMA
+                const int cols = 64 * (slabs - h < 4 ? slabs - h : 4);
+                const uint32_t id = tc::idesc_half(kSmallRows, cols, false, false, true);
+                for (int k = 0; k < 8; ++k)
+                    tc::mma_f16(tmem + wide + 64 * h, mat_desc + (uint64_t)((k / 4 * kSlab + k % 4 * 32) >> 4),
+                                hi_desc + (uint64_t)((h * kSlab + k * 2048) >> 4), id, k > 0);
+            }
+        });
+        if (!ok) break;
+        const bool last = i + 1 == steps, full = i + 2 >= steps;
+        const float d = diag[r];
+        for (int c = 32 * side; c < 64 * slabs; c += 64) {
+            uint32_t v[32];
+            sums(wide + c, v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t at = place(r, c / 8 + j);
+                float x[8], l[8];
+                dense::widen8(false, *reinterpret_cast<const uint4 *>(hi + at), x);
+                dense::widen8(false, *reinterpret_cast<const uint4 *>(lo + at), l);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float w = x[k] + l[k];
+                    x[k] = fmaf(ca, w, fmaf(d, full ? w : x[k], __uint_as_float(v[8 * j + k]) * kDown));
+                }
+                if (!last) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) l[k] = x[k] - __half2float(__float2half_rn(x[k]));
+                    *reinterpret_cast<uint4 *>(hi + at) = pack_halves(x);
+                    *reinterpret_cast<uint4 *>(lo + at) = pack_halves(l);
+                    continue;
+                }
+                if (r >= m) continue;
+                const int c0 = c + 8 * j;
+                const size_t mat0 = (size_t)blockIdx.x * m * n;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k] *= scale;
+                if (kTall) { // neighbouring lanes, neighbouring values
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (c0 + k < n) put_value(out, out_dtype, mat0 + (size_t)(c0 + k) * m + r, x[k], add);
+                } else {
+                    dense::put_as(out_dtype, out, mat0 + (size_t)r * n + c0, c0, n, n % 8 == 0, add, x);
+                }
+            }
+        }
+    }
+    if (!ok && tid == 0) atomicOr(&dense::g_dense_timeout, 1u);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == 0) tc::tmem_dealloc(tmem, columns);
+}
+
+template <class T, bool kTall> cudaError_t small(const Ortho &P, cudaStream_t s) {
+    static SmemAttr attr;
+    const auto kernel = small_kernel<T, kTall>;
+    const int m = kTall ? P.cols : P.rows, n = kTall ? P.rows : P.cols;
+    const int smem = (2 * ((n + 63) / 64) + 2) * kSlab + 1024;
+    const cudaError_t e = ensure_smem(attr, reinterpret_cast<const void *>(kernel), smem);
+    if (e != cudaSuccess) return e;
+    return launch_behind(kernel, dim3(P.count), dim3(kFlat), smem, s, static_cast<const T *>(P.g), m, n, P.steps, P.a, P.b, P.c, P.out,
+                         P.out_dtype, P.add, P.scale * kDown);
+}
+
 // Tiles of 128 * cg x BN for `count` results of M x N over `pieces` of k: the quickest by whole waves of tiles, each as
 // long as its operands and what its epilogue reads (`extra` bytes a value) need into an SM (100 B/ns) or as its
 // MMAs take.  An MN-major B comes in columns of 64.
@@ -482,13 +714,22 @@ template <class T, int V> cudaError_t start(const Ortho &P, const OrthoParts &W,
 
 cudaError_t launch_ortho(const Ortho &P, cudaStream_t s) {
     const OrthoParts W = ortho_parts(P.count, P.rows, P.cols);
+    const bool tall = P.rows > P.cols;
+    const int m = tall ? P.cols : P.rows, n = tall ? P.rows : P.cols;
+    if (m <= kSmallRows && n <= kSmallCols) {
+        const auto go = [&](auto t) {
+            using T = decltype(t);
+            return tall ? small<T, true>(P, s) : small<T, false>(P, s);
+        };
+        return P.g_dtype == WASTE_ACT_F32 ? go(float()) : P.g_dtype == WASTE_ACT_BF16 ? go(__nv_bfloat16()) : go(__half());
+    }
     const auto go = [&](auto t) {
         using T = decltype(t);
         return P.cols % 8 ? start<T, 1>(P, W, s) : start<T, 8>(P, W, s);
     };
     const cudaError_t e = P.g_dtype == WASTE_ACT_F32 ? go(float()) : P.g_dtype == WASTE_ACT_BF16 ? go(__nv_bfloat16()) : go(__half());
     if (e != cudaSuccess) return e;
-    return P.rows > P.cols ? steps<true>(P, W, s) : steps<false>(P, W, s);
+    return tall ? steps<true>(P, W, s) : steps<false>(P, W, s);
 }
 cudaError_t ortho_timeout(uint32_t *out) { return dense::read_and_clear_timeout(out); }
 

@@ -438,7 +438,7 @@ def distance(a, b):
     return float((a.double() - b).norm() / n) if n > 0 else float(a.double().norm())
 
 
-ORTHOS = [(1, 1, 1), (1, 1, 40), (2, 40, 1), (3, 8, 8), (1, 33, 70), (2, 70, 33), (8, 128, 256), (2, 256, 128), (1, 129, 513), (1, 513, 129),
+ORTHOS = [(1, 1, 1), (1, 1, 40), (3, 128, 320), (2, 320, 100), (2, 128, 321), (2, 65, 64), (2, 40, 1), (3, 8, 8), (1, 33, 70), (2, 70, 33), (8, 128, 256), (2, 256, 128), (1, 129, 513), (1, 513, 129),
           (1, 264, 1032), (2, 1000, 328), (1, 520, 520), (1, 301, 2007)]
 
 
@@ -508,20 +508,23 @@ def test_orthogonalize_added():
     assert torch.equal(a, (2.0 * ns.orthogonalize(G).double()).to(BF))
 
 
-def test_orthogonalize_zero_and_not_finite():
-    G = gradient(gen(4), 4, 64, 96)
-    good = NewtonSchulz(4, 64, 96).orthogonalize(G)
+@pytest.mark.parametrize("rows,cols", [(64, 96), (96, 64), (136, 200), (330, 96), (130, 131)])
+def test_orthogonalize_zero_and_not_finite(rows, cols):
+    G = gradient(gen(4), 4, rows, cols)
+    ns = NewtonSchulz(4, rows, cols)
+    good = ns.orthogonalize(G)
     G[1] = 0.0
     G[2, 5, 5] = float("nan")
     G[3, 1, 2] = float("inf")
-    out = NewtonSchulz(4, 64, 96).orthogonalize(G)
+    out = ns.orthogonalize(G)
     assert torch.equal(out[0], good[0]) and (out[1] == 0).all() and out[2].isnan().all() and out[3].isnan().all()
 
 
-def test_orthogonalize_scales():
+@pytest.mark.parametrize("rows,cols", [(48, 80), (140, 88), (90, 400)])
+def test_orthogonalize_scales(rows, cols):
     """A power of two times G gives the same bits, however large or small."""
-    G = gradient(gen(6), 1, 48, 80)
-    ns = NewtonSchulz(1, 48, 80)
+    G = gradient(gen(6), 1, rows, cols)
+    ns = NewtonSchulz(1, rows, cols)
     want = ns.orthogonalize(G * 1024)
     for p in (-100, -70, -40, 0, 40, 90, 120):
         assert torch.equal(ns.orthogonalize(G * 1024 * 2.0 ** p), want), p
