@@ -29,14 +29,14 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// A sum over the CTA, in thread 0.
+// A sum over the CTA, in thread 0; part: a float a warp.
 __device__ __forceinline__ float block_sum(float v, float *part) {
     v = warp_sum(v);
     __syncthreads();
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
     if (threadIdx.x == 0)
-        for (int w = 1; w < kFlat / 32; ++w) v += part[w];
+        for (int w = 1; w < (int)blockDim.x / 32; ++w) v += part[w];
     return v;
 }
 
@@ -376,7 +376,7 @@ template <bool kTall, bool kLast> struct StepJob {
 // serves A = X X^T with the long side as k and B X with the rows as k alike, lo in the same layout beside it.  A, and
 // B in its place, have 32 KB more.  A step is three products of a few hundred nanoseconds, each followed by its epilogue
 // and a barrier.
-constexpr int kSmallRows = 128, kSmallCols = 320;
+constexpr int kSmallRows = 128, kSmallCols = 320, kSmallThreads = 512;
 constexpr int kSlab = 16384; // 128 rows x 64 columns
 
 // Byte of row r, columns 8 i .. 8 i + 7 in slabs of 64 columns.
@@ -394,11 +394,11 @@ __device__ __forceinline__ void put_value(void *p, int dtype, size_t i, float v,
 }
 
 template <class T, bool kTall>
-__global__ void __launch_bounds__(kFlat)
+__global__ void __launch_bounds__(kSmallThreads)
     small_kernel(const T *g, int m, int n, int steps, float ca, float cb, float cc, void *out, int out_dtype, int add, float scale) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
-    __shared__ float part[kFlat / 32], diag[kSmallRows];
+    __shared__ float part[kSmallThreads / 32], diag[kSmallRows];
     __shared__ Factor shared;
     __shared__ __align__(8) uint64_t bar_word;
     __shared__ uint32_t tmem_slot;
@@ -413,57 +413,62 @@ __global__ void __launch_bounds__(kFlat)
     if (warp == 0) tc::tmem_alloc(tc::smem_u32(&tmem_slot), columns);
     tc::grid_wait_release();
 
-    // ---- G, by pieces of 8 of X's columns: i = tid, tid + 256, ..
+    // ---- G, by pieces of 8 of X's columns: thread t holds t, t + 512, .. in registers, all asked for at once
     g += (size_t)blockIdx.x * m * n;
     const int per = slabs * 8;
-    const auto values = [&](int i, float (&v)[8]) -> uint32_t { // where they go; neighbours read neighbouring values
-        const int r = kTall ? i % kSmallRows : i / per, c = (kTall ? i / kSmallRows : i % per) * 8;
+    constexpr int kMost = kSmallRows * kSmallCols / 8 / kSmallThreads;
+    float x0[kMost][8];
+    const auto row = [&](int i) { return kTall ? i % kSmallRows : i / per; }; // neighbours read neighbouring values
+    const auto col = [&](int i) { return kTall ? i / kSmallRows : i % per; };
+#pragma unroll
+    for (int p = 0; p < kMost; ++p) {
+        float(&v)[8] = x0[p];
+        const int i = p * kSmallThreads + tid, r = row(i), c = col(i) * 8;
+        const bool in = i < kSmallRows * per && r < m;
         if (!kTall && sizeof(T) == 2 && n % 8 == 0) {
             Piece<T, 8> q = {};
-            if (r < m && c < n) q = *reinterpret_cast<const Piece<T, 8> *>(g + r * n + c);
+            if (in && c < n) q = *reinterpret_cast<const Piece<T, 8> *>(g + r * n + c);
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] = (float)q.v[k];
         } else if (!kTall && n % 4 == 0 && sizeof(T) == 4) {
             float4 q[2] = {};
-            if (r < m && c < n) q[0] = *reinterpret_cast<const float4 *>(g + r * n + c);
-            if (r < m && c + 4 < n) q[1] = *reinterpret_cast<const float4 *>(g + r * n + c + 4);
+            if (in && c < n) q[0] = *reinterpret_cast<const float4 *>(g + r * n + c);
+            if (in && c + 4 < n) q[1] = *reinterpret_cast<const float4 *>(g + r * n + c + 4);
             v[0] = q[0].x, v[1] = q[0].y, v[2] = q[0].z, v[3] = q[0].w, v[4] = q[1].x, v[5] = q[1].y, v[6] = q[1].z, v[7] = q[1].w;
         } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = r < m && c + k < n ? (float)g[kTall ? (c + k) * m + r : r * n + c + k] : 0.f;
+            for (int k = 0; k < 8; ++k) v[k] = in && c + k < n ? (float)g[kTall ? (c + k) * m + r : r * n + c + k] : 0.f;
         }
-        return place(r, c / 8);
-    };
+    }
     float s[3];
     squares_of(
         [&](auto f) {
-#pragma unroll 2
-            for (int i = tid; i < kSmallRows * per; i += kFlat) {
-                float v[8];
-                values(i, v);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) f(v[k]);
-            }
+            for (int p = 0; p < kMost; ++p)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) f(x0[p][k]);
         },
         part, s);
     if (tid == 0) shared = factor_of(s[0], s[1], s[2]);
     __syncthreads();
     const Factor f = shared;
-#pragma unroll 2
-    for (int i = tid; i < kSmallRows * per; i += kFlat) {
-        float v[8], l[8];
-        const uint32_t at = values(i, v);
+#pragma unroll
+    for (int p = 0; p < kMost; ++p) {
+        const int i = p * kSmallThreads + tid;
+        if (i >= kSmallRows * per) break;
+        float(&v)[8] = x0[p], l[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             v[k] = f(v[k]);
             l[k] = v[k] - __half2float(__float2half_rn(v[k]));
         }
+        const uint32_t at = place(row(i), col(i));
         *reinterpret_cast<uint4 *>(hi + at) = pack_halves(v);
         *reinterpret_cast<uint4 *>(lo + at) = pack_halves(l);
     }
 
     // ---- steps
-    const int q = warp & 3, side = warp >> 2, r = 32 * q + lane; // this thread's row, and every other 32 columns of it
+    const int q = warp & 3, r = 32 * q + lane, first = 32 * (warp >> 2), step = kSmallThreads / 4; // this thread's row and columns
     uint32_t phase = 0;
     bool ok = true;
     // one product: what the threads wrote is there for it, and its sums are there for them
@@ -499,7 +504,7 @@ __global__ void __launch_bounds__(kFlat)
             }
         });
         if (!ok) break;
-        for (int c = 32 * side; c < kSmallRows; c += 64) {
+        for (int c = first; c < kSmallRows; c += step) {
             uint32_t v[32];
             sums(c, v);
 #pragma unroll
@@ -517,7 +522,7 @@ __global__ void __launch_bounds__(kFlat)
             }
         });
         if (!ok) break;
-        for (int c = 32 * side; c < kSmallRows; c += 64) {
+        for (int c = first; c < kSmallRows; c += step) {
             uint32_t v[32];
             sums(c, v);
 #pragma unroll
@@ -548,7 +553,7 @@ __global__ void __launch_bounds__(kFlat)
         if (!ok) break;
         const bool last = i + 1 == steps, full = i + 2 >= steps;
         const float d = diag[r];
-        for (int c = 32 * side; c < 64 * slabs; c += 64) {
+        for (int c = first; c < 64 * slabs; c += step) {
             uint32_t v[32];
             sums(wide + c, v);
 #pragma unroll
@@ -598,7 +603,7 @@ template <class T, bool kTall> cudaError_t small(const Ortho &P, cudaStream_t s)
     const int smem = (2 * ((n + 63) / 64) + 2) * kSlab + 1024;
     const cudaError_t e = ensure_smem(attr, reinterpret_cast<const void *>(kernel), smem);
     if (e != cudaSuccess) return e;
-    return launch_behind(kernel, dim3(P.count), dim3(kFlat), smem, s, static_cast<const T *>(P.g), m, n, P.steps, P.a, P.b, P.c, P.out,
+    return launch_behind(kernel, dim3(P.count), dim3(kSmallThreads), smem, s, static_cast<const T *>(P.g), m, n, P.steps, P.a, P.b, P.c, P.out,
                          P.out_dtype, P.add, P.scale * kDown);
 }
 
