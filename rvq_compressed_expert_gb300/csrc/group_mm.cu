@@ -119,7 +119,8 @@ template <int kCG, bool kWmn> struct RowsJob {
 };
 
 // dW: the rows are what is summed over.
-struct WeightsJob {
+template <int kCG> struct WeightsJob {
+    static constexpr int kHigh = kBM * kCG;
     static constexpr bool kAmn = true, kBmn = true, kMask = true, kReads = true;
     CUtensorMap ta, tb;
     Out out;
@@ -132,14 +133,14 @@ struct WeightsJob {
         const int e = t / (tm * tn), r = t - e * tm * tn, mi = r % tm, ni = r / tm;
         const int r0 = first[e], n = first[e + 1] - r0;
         Spot T;
-        T.am = mi * kBM;
+        T.am = mi * kHigh;
         T.bm = T.n = ni * BN;
         T.az = T.bz = 0;
         T.ak = T.bk = r0;
         T.pieces = (n + 63) >> 6;
         T.left = n - ((T.pieces - 1) << 6);
-        T.m = e * M + mi * kBM;
-        T.rows = M - mi * kBM;
+        T.m = e * M + mi * kHigh;
+        T.rows = M - mi * kHigh;
         return T;
     }
     using Held = Out::Held;
@@ -176,6 +177,23 @@ cudaError_t rows_product(const Group &G, const void *a, int K, const void *w, in
     return launch_tiles_as<kCG>(P, J, G.dtype == WASTE_ACT_BF16, (size_t)(G.E + 1) * 8, most, device_sm_count(), s);
 }
 
+template <int kCG>
+cudaError_t weights_product(const Group &G, const void *dy, const void *x, void *dw, int grad_dtype, int add, cudaStream_t s) {
+    WeightsJob<kCG> J = {};
+    TileArgs P = {};
+    P.BN = J.BN = width(G.k);
+    J.off = {G.offsets, G.E, G.rows};
+    J.M = G.n;
+    J.tm = (G.n + J.kHigh - 1) / J.kHigh;
+    J.tn = (G.k + J.BN - 1) / J.BN;
+    cudaError_t e = stack_map(&J.ta, dy, G.n, G.rows, 1, G.n, (size_t)G.n * G.rows, 64);
+    if (e == cudaSuccess) e = stack_map(&J.tb, x, G.k, G.rows, 1, G.k, (size_t)G.k * G.rows, 64);
+    if (e == cudaSuccess) e = J.out.set(dw, G.E * G.n, G.k, grad_dtype, add);
+    if (e != cudaSuccess) return e;
+    return launch_tiles_as<kCG>(P, J, G.dtype == WASTE_ACT_BF16, (size_t)(G.E + 1) * 4, (long long)G.E * J.tm * J.tn,
+                                device_sm_count(), s);
+}
+
 } // namespace
 
 cudaError_t launch_group_forward(const Group &G, const void *x, const void *w, void *y, int out_dtype, int add, cudaStream_t s) {
@@ -187,19 +205,8 @@ cudaError_t launch_group_dx(const Group &G, const void *dy, const void *w, void 
                     : rows_product<1, true>(G, dy, G.n, w, G.k, dx, G.dtype, 0, s);
 }
 cudaError_t launch_group_dw(const Group &G, const void *dy, const void *x, void *dw, int grad_dtype, int add, cudaStream_t s) {
-    WeightsJob J = {};
-    TileArgs P = {};
-    P.BN = J.BN = width(G.k);
-    J.off = {G.offsets, G.E, G.rows};
-    J.M = G.n;
-    J.tm = (G.n + kBM - 1) / kBM;
-    J.tn = (G.k + J.BN - 1) / J.BN;
-    cudaError_t e = stack_map(&J.ta, dy, G.n, G.rows, 1, G.n, (size_t)G.n * G.rows, 64);
-    if (e == cudaSuccess) e = stack_map(&J.tb, x, G.k, G.rows, 1, G.k, (size_t)G.k * G.rows, 64);
-    if (e == cudaSuccess) e = J.out.set(dw, G.E * G.n, G.k, grad_dtype, add);
-    if (e != cudaSuccess) return e;
-    return launch_tiles_as<1>(P, J, G.dtype == WASTE_ACT_BF16, (size_t)(G.E + 1) * 4, (long long)G.E * J.tm * J.tn, device_sm_count(),
-                              s);
+    return pairs(G) && G.n > kBM ? weights_product<2>(G, dy, x, dw, grad_dtype, add, s)
+                                 : weights_product<1>(G, dy, x, dw, grad_dtype, add, s);
 }
 
 cudaError_t group_status(uint32_t *timeout, uint32_t *offsets) {

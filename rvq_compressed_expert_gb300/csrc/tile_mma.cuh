@@ -159,6 +159,34 @@ struct Out {
 // Bytes of a stage in one CTA of cg.
 inline uint32_t tile_stage(int BN, int cg, bool b_mn) { return dense::stage_size(BN, cg, b_mn, false); }
 
+// tc::mbar_wait for an arrival from the pair's other CTA, which is to be seen to have written its shared memory.
+__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity) {
+    for (int it = 0; it < tc::kWaitPolls; ++it) {
+        uint32_t ok;
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(ok)
+                     : "r"(bar), "r"(parity)
+                     : "memory");
+        if (ok) return true;
+        if (it > 64) __nanosleep(128);
+    }
+    return false;
+}
+
+// Zeros in rows first .. end - 1 of a stage's slabs (64 rows of 128 bytes each, a row one k), by one warp, seen by MMAs
+// behind it: others' values, a NaN among them maybe, must not meet zeros of the other operand.
+__device__ __forceinline__ void mask_rows(uint8_t *stage, int first, int end, int slabs, int lane) {
+    const int n = (end - first) * 8;
+    for (int i = lane; i < n * slabs; i += 32) {
+        const int s = i / n, j = i - s * n;
+        *reinterpret_cast<uint4 *>(stage + s * 8192 + first * 128 + j * 16) = uint4{};
+    }
+    tc::fence_proxy_async();
+    __syncwarp();
+}
+
 // Shared memory of the eight epilogue warps: two pieces each on their way out, one on its way in.
 template <class J> constexpr uint32_t kTurnBytes = 8 * (J::kReads ? 3 : 2) * kPieceBytes;
 
@@ -171,7 +199,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
     const uint32_t bar_full = bars, bar_empty = bars + 64, bar_accf = bars + 128, bar_acce = bars + 144;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem_raw + bars_at + 160);
     volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem_raw + bars_at + 164);
-    const uint32_t drain = bars + 168;
+    const uint32_t drain = bars + 168, bar_mask = bars + 176;
 
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int BN = P.BN;
@@ -186,13 +214,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
         for (int i = 0; i < P.stages; ++i) {
             tc::mbar_init(bar_full + 8 * i, 1);
             tc::mbar_init(bar_empty + 8 * i, 1);
+            tc::mbar_init(bar_mask + 8 * i, 1); // one a stage: the other CTA may be further along than this one
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(bar_accf + 8 * i, 1);
             tc::mbar_init(bar_acce + 8 * i, 8 * kCG);
         }
         tc::mbar_init(drain, 1);
-        *abort_flag = 0;
+                *abort_flag = 0;
         tc::mbar_init_fence();
     }
     if (warp == 2) {
@@ -227,10 +256,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
                     break;
                 }
                 if (tc::elect_one()) {
-                    const uint32_t sa = base + st * stage_bytes, sb = sa + a_bytes, full = full0 + 8 * st;
-                    if (leads) tc::mbar_arrive_expect_tx(bar_full + 8 * st, kCG * (a_bytes + b_bytes));
+                    const uint32_t sa = base + st * stage_bytes, sb = sa + a_bytes;
+                    // a piece to be masked counts on each CTA's own barrier
+                    const bool own = kCG == 1 || (J::kMask && kb + 1 == T.pieces && T.left < 64);
+                    const uint32_t full = own ? bar_full + 8 * st : full0 + 8 * st;
+                    if (leads || own) tc::mbar_arrive_expect_tx(bar_full + 8 * st, (own ? 1 : kCG) * (a_bytes + b_bytes));
                     const auto load = [&](uint32_t dst, const CUtensorMap *m, int x, int y, int z) {
-                        if (kCG == 2)
+                        if (kCG == 2 && !(J::kMask && own))
                             tma_load3_pair(dst, m, x, y, z, full);
                         else
                             tma_load3(dst, m, x, y, z, full);
@@ -274,8 +306,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
                     tc::mma_commit(bar);
             };
             int st = 0, it = 0;
-            uint32_t ph = 0;
+            uint32_t ph = 0, masked = 0;
             bool ok = true;
+            static_assert(!J::kMask || (J::kAmn && J::kBmn), "a row of a stage is one k");
             const uint64_t desc0 = tc::desc_sw128(base, 8192);
             for (int t = tile0; t < tiles && ok; t += step) {
                 const Spot T = job.spot(mine, t);
@@ -297,17 +330,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
                     const uint64_t da = desc0 + (uint64_t)((st * stage_bytes) >> 4), db = da + (uint64_t)(a_bytes >> 4);
                     int steps = 4;
                     if (J::kMask && kb + 1 == T.pieces && T.left < 64) {
-                        // rows of k behind the tile's last, up to the MMA's 16: zeros (others' values, a NaN
-                        // among them maybe, must not meet zeros of the other operand)
-                        static_assert(!J::kMask || (kCG == 1 && J::kAmn && J::kBmn), "a row of a stage is one k");
                         steps = (T.left + 15) >> 4;
-                        const int first = T.left, n = 16 * steps - first, slabs = (int)((a_bytes + b_bytes) >> 13);
-                        for (int i = lane; i < n * 8 * slabs; i += 32) {
-                            const int s = i / (n * 8), j = i - s * n * 8;
-                            *reinterpret_cast<uint4 *>(smem_raw + st * stage_bytes + s * 8192 + first * 128 + j * 16) = uint4{};
+                        mask_rows(smem_raw + st * stage_bytes, T.left, 16 * steps, (int)((a_bytes + b_bytes) >> 13), lane);
+                        if (kCG == 2) { // and the other CTA its own
+                            if (!all(wait_cluster(bar_mask + 8 * st, masked >> st & 1))) {
+                                ok = false;
+                                break;
+                            }
+                            masked ^= 1u << st;
+                            tc::fence_after_sync();
                         }
-                        tc::fence_proxy_async();
-                        __syncwarp();
                     }
                     if (tc::elect_one()) {
 #pragma unroll
@@ -334,6 +366,24 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
                 if (lane == 0) *abort_flag = 1;
                 if (tc::elect_one()) commit(drain);
                 tc::mbar_wait(drain, 0);
+            }
+        } else if (J::kMask) {
+            // ---- the pair's other CTA clears what is not the tile's in its own shared memory, and says so
+            int st = 0;
+            uint32_t used = 0; // a bit a stage: its own barrier's parity
+            for (int t = tile0; t < tiles; t += step) {
+                const Spot T = job.spot(mine, t);
+                if (T.pieces == 0) continue;
+                const int last = (st + T.pieces - 1) % P.stages;
+                st = (st + T.pieces) % P.stages;
+                if (T.left == 64) continue;
+                if (!all(tc::mbar_wait(bar_full + 8 * last, used >> last & 1))) {
+                    if (lane == 0) *abort_flag = 1;
+                    break;
+                }
+                used ^= 1u << last;
+                mask_rows(smem_raw + last * stage_bytes, T.left, (T.left + 15) & ~15, (int)((a_bytes + b_bytes) >> 13), lane);
+                if (lane == 0) tc::mbar_arrive_cluster(tc::map_rank(bar_mask + 8 * last, 0));
             }
         }
         __syncwarp();

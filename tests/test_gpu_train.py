@@ -311,9 +311,10 @@ def test_grouped(sizes, k, n, t, before, behind):
 
 
 @pytest.mark.parametrize("t", [BF, HF])
-def test_grouped_exact(t):
+@pytest.mark.parametrize("sizes,k,n", [([37, 0, 130, 1, 16, 300, 63], 456, 328), ([257, 1, 640, 0, 319, 95], 328, 456),
+                                       ([1029], 520, 136), ([160] * 40, 72, 1000)])
+def test_grouped_exact(t, sizes, k, n):
     """Small whole numbers: every sum is exact, so a lost or a foreign k, row or column shows in the bits."""
-    sizes, k, n = [37, 0, 130, 1, 16, 300, 63], 456, 328
     g = gen(1)
     rows = sum(sizes)
 
@@ -347,20 +348,21 @@ def test_grouped_many_experts():
     R.close(dw, v, e + R.rnd(v.abs() + e, BF), "dw")
 
 
-def test_grouped_not_finite():
+@pytest.mark.parametrize("sizes,k,n", [([5, 70, 9], 64, 40), ([333, 470, 131], 264, 200)])
+def test_grouped_not_finite(sizes, k, n):
     """An infinity or a NaN in a row or a matrix stays with its expert, in the sums over rows too."""
-    sizes, k, n = [5, 70, 9], 64, 40
     g, x, dy, w, off = group_inputs(sizes, k, n, BF)
     m = GroupedLinear(w)
     y, dx, dw = m.forward(x, off), torch.empty_like(x), torch.empty_like(w)
     m.backward(dy, x, off, dx, dw)
     x2, dy2 = x.clone(), dy.clone()
-    x2[7, 3], dy2[20, 1] = float("nan"), float("inf")  # rows of expert 1
+    i, j = sizes[0] + 2, sizes[0] + 15  # rows of expert 1
+    x2[i, 3], dy2[j, 1] = float("nan"), float("inf")
     y2, dx2, dw2 = m.forward(x2, off), torch.empty_like(x), torch.empty_like(w)
     m.backward(dy2, x2, off, dx2, dw2)
-    assert y2[7].isnan().all() and not dx2[20].isfinite().any()
-    rows = torch.arange(84, device="cuda")
-    assert torch.equal(y2[rows != 7], y[rows != 7]) and torch.equal(dx2[rows != 20], dx[rows != 20])
+    assert y2[i].isnan().all() and not dx2[j].isfinite().any()
+    rows = torch.arange(sum(sizes), device="cuda")
+    assert torch.equal(y2[rows != i], y[rows != i]) and torch.equal(dx2[rows != j], dx[rows != j])
     assert torch.equal(dw2[0], dw[0]) and torch.equal(dw2[2], dw[2]) and dw2[1, :, 3].isnan().all()
 
 
