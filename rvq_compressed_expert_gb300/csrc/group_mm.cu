@@ -5,6 +5,8 @@
 // its tiles by bisection.  A tile has rows of one expert alone: TMA loads start at any row, what the last tile of an
 // expert loads of the next one's rows is never stored, and in dW, where rows are summed over, the rows
 // behind the expert's last are cleared in shared memory.
+#include <type_traits>
+
 #include "tile_mma.cuh"
 
 namespace wm {
@@ -73,10 +75,10 @@ struct Offsets {
 };
 
 // Results by row: y (W K-major) and dx (W MN-major).
-template <int kCG, bool kWmn> struct RowsJob {
-    static constexpr bool kAmn = false, kBmn = kWmn, kMask = false, kReads = true;
+template <int kCG, bool kWmn, bool kAdd> struct RowsJob {
+    static constexpr bool kAmn = false, kBmn = kWmn, kMask = false, kReads = kAdd;
     CUtensorMap ta, tb;
-    Out out;
+    Out<kAdd> out;
     Offsets off;
     int BN, tn, pieces;
     static constexpr int kHigh = kBM * kCG;
@@ -106,8 +108,8 @@ template <int kCG, bool kWmn> struct RowsJob {
         T.rows = n - mi * kHigh;
         return T;
     }
-    using Held = Out::Held;
-    using In = float[32];
+    using Held = typename Out<kAdd>::Held;
+    using In = typename Out<kAdd>::In;
     __device__ __forceinline__ void ahead(const Spot &T, int r, int half, int BN) const {
         if (r < T.rows) out.ahead(T.m + r, T.n, half, BN);
     }
@@ -119,11 +121,11 @@ template <int kCG, bool kWmn> struct RowsJob {
 };
 
 // dW: the rows are what is summed over.
-template <int kCG> struct WeightsJob {
+template <int kCG, bool kAdd> struct WeightsJob {
     static constexpr int kHigh = kBM * kCG;
-    static constexpr bool kAmn = true, kBmn = true, kMask = true, kReads = true;
+    static constexpr bool kAmn = true, kBmn = true, kMask = true, kReads = kAdd;
     CUtensorMap ta, tb;
-    Out out;
+    Out<kAdd> out;
     Offsets off;
     int BN, tm, tn, M;
     __device__ void begin(uint8_t *smem) const { off.read(reinterpret_cast<int *>(smem), nullptr, 0, 0); }
@@ -143,17 +145,22 @@ template <int kCG> struct WeightsJob {
         T.rows = M - mi * kHigh;
         return T;
     }
-    using Held = Out::Held;
-    using In = float[32];
+    using Held = typename Out<kAdd>::Held;
+    using In = typename Out<kAdd>::In;
     __device__ __forceinline__ void ahead(const Spot &T, int r, int half, int BN) const {
         if (r < T.rows) out.ahead(T.m + r, T.n, half, BN);
     }
     __device__ __forceinline__ void fetch(const Out32 &o, const Spot &, int n, Held &h) const { out.fetch(o, n, h); }
     __device__ __forceinline__ void turn(const Out32 &o, uint4 *t, const Held &h, In &in) const { out.turn(o, t, h, in); }
     __device__ __forceinline__ void tile(Out32 &o, const Spot &T, int n, const float (&v)[32], const In &in) const {
-        if (T.pieces || !out.add) out.put(o, n, v, in);
+        if (T.pieces || !kAdd) out.put(o, n, v, in);
     }
 };
+
+constexpr std::integral_constant<int, 1> kOne;
+constexpr std::integral_constant<int, 2> kTwo;
+constexpr std::true_type kYes;
+constexpr std::false_type kNo;
 
 // Whole widths of 32 columns, 256 at most.
 int width(int n) { return n >= 256 ? 256 : n <= 64 ? 64 : (n + 31) / 32 * 32; }
@@ -161,9 +168,9 @@ int width(int n) { return n >= 256 ? 256 : n <= 64 ? 64 : (n + 31) / 32 * 32; }
 // Pairs of CTAs, with tiles of 256 rows, from so many rows an expert on (their mean: the offsets are on the device).
 bool pairs(const Group &G) { return G.rows / G.E >= 160; }
 
-template <int kCG, bool kWmn>
-cudaError_t rows_product(const Group &G, const void *a, int K, const void *w, int N, void *out, int out_dtype, int add, cudaStream_t s) {
-    RowsJob<kCG, kWmn> J = {};
+template <int kCG, bool kWmn, bool kAdd>
+cudaError_t rows_product(const Group &G, const void *a, int K, const void *w, int N, void *out, int out_dtype, cudaStream_t s) {
+    RowsJob<kCG, kWmn, kAdd> J = {};
     TileArgs P = {};
     P.BN = J.BN = width(N);
     J.off = {G.offsets, G.E, G.rows};
@@ -171,15 +178,15 @@ cudaError_t rows_product(const Group &G, const void *a, int K, const void *w, in
     J.pieces = (K + 63) / 64;
     cudaError_t e = stack_map(&J.ta, a, K, G.rows, 1, K, (size_t)K * G.rows, kBM);
     if (e == cudaSuccess) e = stack_map(&J.tb, w, G.k, G.n, G.E, G.k, (size_t)G.k * G.n, kWmn ? 64 : J.BN / kCG);
-    if (e == cudaSuccess) e = J.out.set(out, G.rows, N, out_dtype, add);
+    if (e == cudaSuccess) e = J.out.set(out, G.rows, N, out_dtype);
     if (e != cudaSuccess) return e;
     const long long most = ((long long)G.rows / J.kHigh + (G.E < G.rows ? G.E : G.rows)) * J.tn;
     return launch_tiles_as<kCG>(P, J, G.dtype == WASTE_ACT_BF16, (size_t)(G.E + 1) * 8, most, device_sm_count(), s);
 }
 
-template <int kCG>
-cudaError_t weights_product(const Group &G, const void *dy, const void *x, void *dw, int grad_dtype, int add, cudaStream_t s) {
-    WeightsJob<kCG> J = {};
+template <int kCG, bool kAdd>
+cudaError_t weights_product(const Group &G, const void *dy, const void *x, void *dw, int grad_dtype, cudaStream_t s) {
+    WeightsJob<kCG, kAdd> J = {};
     TileArgs P = {};
     P.BN = J.BN = width(G.k);
     J.off = {G.offsets, G.E, G.rows};
@@ -188,7 +195,7 @@ cudaError_t weights_product(const Group &G, const void *dy, const void *x, void 
     J.tn = (G.k + J.BN - 1) / J.BN;
     cudaError_t e = stack_map(&J.ta, dy, G.n, G.rows, 1, G.n, (size_t)G.n * G.rows, 64);
     if (e == cudaSuccess) e = stack_map(&J.tb, x, G.k, G.rows, 1, G.k, (size_t)G.k * G.rows, 64);
-    if (e == cudaSuccess) e = J.out.set(dw, G.E * G.n, G.k, grad_dtype, add);
+    if (e == cudaSuccess) e = J.out.set(dw, G.E * G.n, G.k, grad_dtype);
     if (e != cudaSuccess) return e;
     return launch_tiles_as<kCG>(P, J, G.dtype == WASTE_ACT_BF16, (size_t)(G.E + 1) * 4, (long long)G.E * J.tm * J.tn,
                                 device_sm_count(), s);
@@ -197,16 +204,20 @@ cudaError_t weights_product(const Group &G, const void *dy, const void *x, void 
 } // namespace
 
 cudaError_t launch_group_forward(const Group &G, const void *x, const void *w, void *y, int out_dtype, int add, cudaStream_t s) {
-    return pairs(G) ? rows_product<2, false>(G, x, G.k, w, G.n, y, out_dtype, add, s)
-                    : rows_product<1, false>(G, x, G.k, w, G.n, y, out_dtype, add, s);
+    const auto go = [&](auto cg, auto adds) {
+        return rows_product<decltype(cg)::value, false, decltype(adds)::value>(G, x, G.k, w, G.n, y, out_dtype, s);
+    };
+    return pairs(G) ? (add ? go(kTwo, kYes) : go(kTwo, kNo)) : add ? go(kOne, kYes) : go(kOne, kNo);
 }
 cudaError_t launch_group_dx(const Group &G, const void *dy, const void *w, void *dx, cudaStream_t s) {
-    return pairs(G) ? rows_product<2, true>(G, dy, G.n, w, G.k, dx, G.dtype, 0, s)
-                    : rows_product<1, true>(G, dy, G.n, w, G.k, dx, G.dtype, 0, s);
+    return pairs(G) ? rows_product<2, true, false>(G, dy, G.n, w, G.k, dx, G.dtype, s)
+                    : rows_product<1, true, false>(G, dy, G.n, w, G.k, dx, G.dtype, s);
 }
 cudaError_t launch_group_dw(const Group &G, const void *dy, const void *x, void *dw, int grad_dtype, int add, cudaStream_t s) {
-    return pairs(G) && G.n > kBM ? weights_product<2>(G, dy, x, dw, grad_dtype, add, s)
-                                 : weights_product<1>(G, dy, x, dw, grad_dtype, add, s);
+    const auto go = [&](auto cg, auto adds) {
+        return weights_product<decltype(cg)::value, decltype(adds)::value>(G, dy, x, dw, grad_dtype, s);
+    };
+    return pairs(G) && G.n > kBM ? (add ? go(kTwo, kYes) : go(kTwo, kNo)) : add ? go(kOne, kYes) : go(kOne, kNo);
 }
 
 cudaError_t group_status(uint32_t *timeout, uint32_t *offsets) {

@@ -178,8 +178,6 @@ struct Stack {
 __device__ __forceinline__ void put_halves(Out32 &o, const CUtensorMap *map, void *p, int ld, int n, const float (&v)[32]) {
     dense::put32_as(WASTE_ACT_F16, o, o.rows >= 32 ? map : nullptr, p, ld, n, ld, true, false, v);
 }
-struct Nothing {};
-
 // Tile t of those on and below a diagonal, row by row.
 __host__ __device__ __forceinline__ void triangle(int t, int &i, int &j) {
     i = (int)((sqrtf(8.f * t + 1.f) - 1.f) * 0.5f);
@@ -297,7 +295,8 @@ struct SquareJob {
     }
 };
 // X <- a X + B X (kTall: a X + X B), the last one to the caller's memory
-template <bool kTall, bool kLast> struct StepJob {
+// kAdd: the last one added to what is there
+template <bool kTall, bool kLast, bool kAdd> struct StepJob {
     static constexpr bool kAmn = false, kBmn = !kTall, kMask = false, kReads = true;
     CUtensorMap ta, tb, thi, tlo;
     Stack s;
@@ -308,7 +307,7 @@ template <bool kTall, bool kLast> struct StepJob {
     float a;
     int full;    // the diagonal multiplies both parts
     int keep_lo; // the next step takes both
-    Out out; // of the last step
+    Out<kAdd> out; // of the last step
     float scale;
     __device__ void begin(uint8_t *) const {}
     __device__ __forceinline__ int tiles(const uint8_t *) const { return s.tiles(); }
@@ -318,25 +317,25 @@ template <bool kTall, bool kLast> struct StepJob {
         const int w = min(BN, ldx - T.n);
         if (w > 0 && !(kLast && half))
             ask_l2(static_cast<const __half *>(half ? static_cast<const void *>(lo) : hi) + (size_t)(T.m + r) * ldx + T.n, w * 2);
-        if constexpr (kLast) out.ahead(T.m + r, T.n, half, BN);
+        if constexpr (kAdd) out.ahead(T.m + r, T.n, half, BN);
     }
     struct Held {
         Block<2> hi, lo;
-        std::conditional_t<kLast, Out::Held, Nothing> base;
+        std::conditional_t<kAdd, typename Out<kAdd>::Held, Nothing> base;
     };
     struct In {
         uint4 hi[4], lo[4];
-        float base[kLast ? 32 : 1];
+        typename Out<kAdd>::In base;
     };
     __device__ __forceinline__ void fetch(const Out32 &o, const Spot &, int n, Held &h) const {
         h.hi.fetch(o, hi, ldx, n, ldx);
         if constexpr (!kLast) h.lo.fetch(o, lo, ldx, n, ldx);
-        if constexpr (kLast) out.fetch(o, n, h.base);
+        if constexpr (kAdd) out.fetch(o, n, h.base);
     }
     __device__ __forceinline__ void turn(const Out32 &o, uint4 *t, const Held &h, In &in) const {
         h.hi.turn(o, t, in.hi);
         if constexpr (!kLast) h.lo.turn(o, t, in.lo);
-        if constexpr (kLast) out.turn(o, t, h.base, in.base);
+        if constexpr (kAdd) out.turn(o, t, h.base, in.base);
     }
     __device__ __forceinline__ void tile(Out32 &o, const Spot &T, int n, const float (&v)[32], const In &in) const {
         float x[32], l[32];
@@ -634,7 +633,7 @@ template <class J> cudaError_t launch(int cg, int BN, const J &job, long long ti
     return cg == 2 ? launch_tiles_as<2>(T, job, false, 0, tiles, sms, s) : launch_tiles_as<1>(T, job, false, 0, tiles, sms, s);
 }
 
-template <bool kTall> cudaError_t steps(const Ortho &P, const OrthoParts &W, cudaStream_t s) {
+template <bool kTall, bool kAdd> cudaError_t steps(const Ortho &P, const OrthoParts &W, cudaStream_t s) {
     const int m = kTall ? P.cols : P.rows, n = kTall ? P.rows : P.cols, sms = device_sm_count();
     uint8_t *hi[2] = {P.ws + W.hi[0], P.ws + W.hi[1]}, *lo = P.ws + W.lo, *A = P.ws + W.a, *B = P.ws + W.b;
     float *diag = reinterpret_cast<float *>(P.ws + W.diag), *parts = reinterpret_cast<float *>(P.ws + W.gram);
@@ -654,8 +653,8 @@ template <bool kTall> cudaError_t steps(const Ortho &P, const OrthoParts &W, cud
     };
     GramJob<kTall> G = {};
     SquareJob Q = {};
-    StepJob<kTall, false> S = {};
-    StepJob<kTall, true> L = {};
+    StepJob<kTall, false, false> S = {};
+    StepJob<kTall, true, kAdd> L = {};
     G.out = parts;
     G.side = W.side, G.tri = W.tri, G.slices = W.slices, G.count = P.count, G.pieces = (n + 63) / 64;
     const long long items = (long long)P.count * W.tri * W.slices;
@@ -669,7 +668,7 @@ template <bool kTall> cudaError_t steps(const Ortho &P, const OrthoParts &W, cud
     s_map(kTall ? &S.tb : &S.ta, B, kTall ? xx.BN / xx.cg : kBM);
     o_map(&S.tlo, lo, 2, P.count * P.rows, W.ldx);
     S.lo = lo, S.diag = diag, S.ldx = W.ldx, S.ldm = W.ldm, S.a = P.a;
-    if (e == cudaSuccess) e = L.out.set(P.out, P.count * P.rows, P.cols, P.out_dtype, P.add);
+    if (e == cudaSuccess) e = L.out.set(P.out, P.count * P.rows, P.cols, P.out_dtype);
     CUtensorMap ga[2], gb[2], sx[2], st[2];
     for (int i = 0; i < 2; ++i) {
         x_map(&ga[i], i, kTall ? 64 : kBM);
@@ -734,7 +733,8 @@ cudaError_t launch_ortho(const Ortho &P, cudaStream_t s) {
     };
     const cudaError_t e = P.g_dtype == WASTE_ACT_F32 ? go(float()) : P.g_dtype == WASTE_ACT_BF16 ? go(__nv_bfloat16()) : go(__half());
     if (e != cudaSuccess) return e;
-    return tall ? steps<true>(P, W, s) : steps<false>(P, W, s);
+    if (P.add) return tall ? steps<true, true>(P, W, s) : steps<false, true>(P, W, s);
+    return tall ? steps<true, false>(P, W, s) : steps<false, false>(P, W, s);
 }
 cudaError_t ortho_timeout(uint32_t *out) { return dense::read_and_clear_timeout(out); }
 

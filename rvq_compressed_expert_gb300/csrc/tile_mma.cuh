@@ -111,35 +111,37 @@ __device__ __forceinline__ void ask_l2(const void *p, int bytes) {
     for (int i = 0; i < bytes; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char *>(p) + i));
 }
 
-// A result in memory: written, or added to what is there.
-struct Out {
+struct Nothing {};
+
+// A result in memory: written, or (kAdd) added to what is there.
+template <bool kAdd> struct Out {
     CUtensorMap map; // over all of it; copies write 32 whole rows
     void *p;
-    int N, dtype, add, vec; // vec: rows of whole 16-byte pieces, for copies and blocks
-    cudaError_t set(void *out, int rows, int cols, int type, int accumulate) {
-        p = out, N = cols, dtype = type, add = accumulate;
+    int N, dtype, vec; // vec: rows of whole 16-byte pieces, for copies and blocks
+    cudaError_t set(void *out, int rows, int cols, int type) {
+        p = out, N = cols, dtype = type;
         vec = (size_t)cols * dense::type_size(type) % 16 == 0;
         return vec ? dense::store_map(&map, out, (int)dense::type_size(type), rows, cols) : cudaSuccess;
     }
-    // what is there, if it is to be added to
+    // what is there, to be added to
     struct Held {
         Block<4> wide;
     };
+    using In = std::conditional_t<kAdd, float[32], Nothing>;
     // half a row of BN columns from n on
     __device__ __forceinline__ void ahead(size_t m, int n, int half, int BN) const {
-        if (!add) return;
         const int size = dtype == WASTE_ACT_F32 ? 4 : 2, c = n + half * (BN / 2), cols = min(BN / 2, N - c);
         if (cols > 0) ask_l2(static_cast<const char *>(p) + (m * N + c) * size, cols * size);
     }
     __device__ __forceinline__ void fetch(const Out32 &o, int n, Held &h) const {
-        if (!add || !vec) return;
+        if (!vec) return;
         if (dtype == WASTE_ACT_F32)
             h.wide.fetch(o, p, N, n, N);
         else
             reinterpret_cast<Block<2> &>(h.wide).fetch(o, p, N, n, N);
     }
     __device__ __forceinline__ void turn(const Out32 &o, uint4 *t, const Held &h, float (&base)[32]) const {
-        if (!add || !vec) return;
+        if (!vec) return;
         if (dtype == WASTE_ACT_F32) {
             h.wide.turn(o, t, reinterpret_cast<uint4(&)[8]>(base));
         } else {
@@ -148,11 +150,16 @@ struct Out {
             halves(q, dtype == WASTE_ACT_BF16, base);
         }
     }
-    __device__ __forceinline__ void put(Out32 &o, int n, const float (&v)[32], const float (&base)[32]) const {
-        float x[32];
+    __device__ __forceinline__ void put(Out32 &o, int n, const float (&v)[32], const In &base) const {
+        const CUtensorMap *by = vec && o.rows >= 32 ? &map : nullptr;
+        if constexpr (kAdd) {
+            float x[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = add && vec ? base[i] + v[i] : v[i];
-        dense::put32_as(dtype, o, vec && o.rows >= 32 ? &map : nullptr, p, N, n, N, vec || N % 4 == 0, add && !vec, x);
+            for (int i = 0; i < 32; ++i) x[i] = vec ? base[i] + v[i] : v[i];
+            dense::put32_as(dtype, o, by, p, N, n, N, vec || N % 4 == 0, !vec, x);
+        } else {
+            dense::put32_as(dtype, o, by, p, N, n, N, vec || N % 4 == 0, false, v);
+        }
     }
 };
 
@@ -401,23 +408,65 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
             out.m = T.m + 32 * q;
             out.rows = T.rows - 32 * q;
             const int buf = it & 1, use = it >> 1;
-            if (t + step < tiles) job.ahead(job.spot(mine, t + step), 32 * q + rank * kBM + lane, half, BN);
-            typename J::Held held;
-            if (any) job.fetch(out, T, T.n + 32 * half, held);
-            if (!empty) {
+            if constexpr (J::kReads)
+                if (t + step < tiles) job.ahead(job.spot(mine, t + step), 32 * q + rank * kBM + lane, half, BN);
+            const uint32_t src = tmem + buf * 256 + ((uint32_t)(32 * q) << 16);
+            const auto ready = [&] { // the tile's sums
+                if (empty) return true;
                 ++it;
                 bool ok = true;
                 if (lane == 0) ok = dense::wait_tile(bar_accf + 8 * buf, use & 1, T.pieces);
                 ok = __shfl_sync(0xffffffffu, ok, 0);
-                if (!ok) {
-                    *abort_flag = 1;
-                    break;
-                }
+                if (!ok) *abort_flag = 1;
                 tc::fence_after_sync();
-            }
-            const uint32_t src = tmem + buf * 256 + ((uint32_t)(32 * q) << 16);
-            if (any) {
-                for (int c = 32 * half; c < BN; c += 64) { // BN is a multiple of 32
+                return ok;
+            };
+            const auto free_acc = [&] {
+                if (empty) return;
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    if (leads)
+                        tc::mbar_arrive(bar_acce + 8 * buf);
+                    else
+                        tc::mbar_arrive_cluster(tc::map_rank(bar_acce + 8 * buf, 0));
+                }
+            };
+            if constexpr (!J::kReads) {
+                // nothing but the sums: two pieces to registers at once, so that the next tile's MMAs may follow while
+                // the last two are on their way out
+                if (!ready()) break;
+                alignas(16) uint32_t v[32], w[32];
+                const auto take = [&](int c) {
+                    if (any && !empty) {
+                        if (c < BN) tc::tmem_ld32(src + c, v);
+                        if (c + 64 < BN) tc::tmem_ld32(src + c + 64, w);
+                        if (c < BN) tc::tmem_wait_ld(v);
+                        if (c + 64 < BN) tc::tmem_wait_ld(w);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) v[k] = w[k] = 0;
+                    }
+                };
+                const auto give = [&](int c) {
+                    if (any && c < BN) job.tile(out, T, T.n + c, reinterpret_cast<const float(&)[32]>(v), {});
+                    if (any && c + 64 < BN) job.tile(out, T, T.n + c + 64, reinterpret_cast<const float(&)[32]>(w), {});
+                };
+                take(32 * half);
+                if (BN <= 128) {
+                    free_acc();
+                    give(32 * half);
+                } else {
+                    give(32 * half);
+                    take(128 + 32 * half);
+                    free_acc();
+                    give(128 + 32 * half);
+                }
+            } else {
+                typename J::Held held;
+                if (any) job.fetch(out, T, T.n + 32 * half, held);
+                if (!ready()) break;
+                for (int c = 32 * half; any && c < BN; c += 64) { // BN is a multiple of 32
                     alignas(16) uint32_t v[32];
                     if (empty) {
 #pragma unroll
@@ -429,18 +478,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
                     typename J::In in;
                     job.turn(out, turned, held, in);
                     if (c + 64 < BN) job.fetch(out, T, T.n + c + 64, held);
-                    job.tile(out, T, T.n + c, *reinterpret_cast<const float(*)[32]>(v), in);
+                    job.tile(out, T, T.n + c, reinterpret_cast<const float(&)[32]>(v), in);
                 }
-            }
-            if (!empty) {
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) {
-                    if (leads)
-                        tc::mbar_arrive(bar_acce + 8 * buf);
-                    else
-                        tc::mbar_arrive_cluster(tc::map_rank(bar_acce + 8 * buf, 0));
-                }
+                free_acc();
             }
         }
         if (lane == 0) {
