@@ -2,9 +2,14 @@
 // by expert, as tiles of tile_mma.cuh.
 //
 // The offsets stay on the device: every CTA reads them, adds up the experts' tiles in shared memory, and finds each of
-// its tiles by bisection.  A tile has rows of one expert alone: TMA loads start at any row, what the last tile of an
-// expert loads of the next one's rows is never stored, and in dW, where rows are summed over, the rows
-// behind the expert's last are cleared in shared memory.
+// its tiles by bisection.
+//
+// y and dx: the matrices are on the MMA's row side (128 rows, 256 for a pair of CTAs) and the expert's rows on its column
+// side, whose width is a multiple of 16 (32), so that little is computed for rows that are not there: an expert's
+// rows are cut into equal shares of at most 256 (64).  With the rows on the row side, in tiles of 256, a batch of uneven
+// popularity (126 to 2048 rows an expert) wastes 20 %.  The sums are turned round in shared memory on their way out.
+// Loads start at any row; what the last share of an expert loads of the next one's rows is never stored.
+// dW: its rows are what is summed over; those behind the expert's last are cleared in shared memory.
 #include <type_traits>
 
 #include "tile_mma.cuh"
@@ -24,13 +29,13 @@ namespace {
 
 __device__ uint32_t g_bad_offsets;
 
+
 // Offsets as the kernels use them: what does not ascend within 0 .. rows is replaced by the nearest that does.
 struct Offsets {
     const int32_t *p;
-    int E, rows;
-    // Into first[0 .. E]; with tn > 0 also the tiles of all experts before each, of `high` rows and tn
-    // columns of tiles, into before[0 .. E].
-    __device__ void read(int *first, int *before, int high, int tn) const {
+    int E, rows, share; // share: rows of an expert in one tile, at most
+    // Into first[0 .. E]; and the shares (of at most `share` rows) of all experts before each into before[0 .. E], if not null.
+    __device__ void read(int *first, int *before) const {
         for (int e = threadIdx.x; e <= E; e += kTileThreads) first[e] = p[e];
         __syncthreads();
         if (threadIdx.x < 32) {
@@ -54,10 +59,10 @@ struct Offsets {
             int last = up;
             for (int e = e0; e < e1; ++e) first[e] = last = max(last, min(first[e], rows));
             __syncwarp();
-            if (tn > 0) {
+            if (before) {
                 int sum = 0;
                 for (int e = e0; e < e1; ++e)
-                    if (e > 0) sum += (first[e] - first[e - 1] + high - 1) / high * tn;
+                    if (e > 0) sum += (first[e] - first[e - 1] + share - 1) / share;
                 int at = sum;
                 for (int o = 1; o < 32; o <<= 1) {
                     const int v = __shfl_up_sync(0xffffffffu, at, o);
@@ -65,7 +70,7 @@ struct Offsets {
                 }
                 at -= sum;
                 for (int e = e0; e < e1; ++e) {
-                    if (e > 0) at += (first[e] - first[e - 1] + high - 1) / high * tn;
+                    if (e > 0) at += (first[e] - first[e - 1] + share - 1) / share;
                     before[e] = at;
                 }
             }
@@ -76,59 +81,126 @@ struct Offsets {
 
 // Results by row: y (W K-major) and dx (W MN-major).
 template <int kCG, bool kWmn, bool kAdd> struct RowsJob {
-    static constexpr bool kAmn = false, kBmn = kWmn, kMask = false, kReads = kAdd;
-    CUtensorMap ta, tb;
-    Out<kAdd> out;
+    static constexpr bool kAmn = kWmn, kBmn = false, kMask = false, kReads = false, kTwoPieces = true, kRagged = true;
+    static constexpr int kUnit = 16 * kCG, kTall = kBM * kCG;
+    CUtensorMap ta, ta_low, tb, tb_low, to;
     Offsets off;
-    int BN, tn, pieces;
-    static constexpr int kHigh = kBM * kCG;
+    int N, pieces;
+    void *out;
+    int dtype;
+    // shared memory: first[E + 1], before[E + 1], height of a tile, tiles down
     __device__ void begin(uint8_t *smem) const {
-        int *first = reinterpret_cast<int *>(smem);
-        off.read(first, first + off.E + 1, kHigh, tn);
+        int *first = reinterpret_cast<int *>(smem), *before = first + off.E + 1;
+        off.read(first, before);
+        if (threadIdx.x == 0) {
+            // few tiles: lower ones where they fill the GPU's rounds better (each costs what its rows of W need, and a
+            // bit); 16 experts of 1536 rows on 152 SMs: 192 tiles of 128 make two rounds, 256 of 96 two shorter ones
+            int best = kTall;
+            if (kCG == 1) {
+                int least = 0x7fffffff;
+                for (int h = kBM; h >= (kWmn ? 64 : 32); h -= kWmn ? 64 : 32) {
+                    const long long tiles = (long long)before[off.E] * ((N + h - 1) / h);
+                    if (tiles > 16 * (int)gridDim.x) break; // many rounds: as they are
+                    const int t = (int)((tiles + gridDim.x - 1) / gridDim.x) * (h + 16);
+                    if (t < least) least = t, best = h;
+                }
+            }
+            before[off.E + 1] = best;
+            before[off.E + 2] = (N + best - 1) / best;
+        }
+        __syncthreads();
     }
-    __device__ __forceinline__ int tiles(const uint8_t *smem) const { return reinterpret_cast<const int *>(smem)[2 * off.E + 1]; }
+    __device__ __forceinline__ int tiles(const uint8_t *smem) const {
+        const int *before = reinterpret_cast<const int *>(smem) + off.E + 1;
+        return before[off.E] * before[off.E + 2];
+    }
     __device__ __forceinline__ Spot spot(const uint8_t *smem, int t) const {
         const int *first = reinterpret_cast<const int *>(smem), *before = first + off.E + 1;
-        int e = 0; // the last with before[e] <= t
+        const int high = before[off.E + 1], tm = before[off.E + 2], u = t / tm;
+        int e = 0; // the last with before[e] <= u
         for (int b = 1 << (31 - __clz(off.E)); b; b >>= 1)
-            if (e + b <= off.E && before[e + b] <= t) e += b;
-        const int r = t - before[e], r0 = first[e], n = first[e + 1] - r0, tm = (n + kHigh - 1) / kHigh;
-        // groups of 16 row tiles (of 128), columns moving slowest inside a group
-        constexpr int kGroup = 16 / kCG;
-        const int per = kGroup * tn, g = r / per, top = g * kGroup, gm = min(kGroup, tm - top), i = r - g * per;
-        const int mi = top + i % gm, ni = i / gm;
+            if (e + b <= off.E && before[e + b] <= u) e += b;
+        const int r = t - before[e] * tm, r0 = first[e], n = first[e + 1] - r0, shares = before[e + 1] - before[e];
+        // groups of 8 shares, W's rows moving slowest inside a group: the tiles in flight share their operands in L2
+        const int per = 8 * tm, g = r / per, top = g * 8, gm = min(8, shares - top), i = r - g * per;
+        const int share = top + i % gm, mi = i / gm;
+        const int each = ((n + shares - 1) / shares + kUnit - 1) / kUnit * kUnit, left = n - share * each;
         Spot T;
-        T.am = T.m = r0 + mi * kHigh;
-        T.az = 0;
-        T.bm = T.n = ni * BN;
-        T.bz = e;
+        T.am = T.m = mi * high;
+        T.az = e;
+        T.bm = T.n = r0 + share * each;
+        T.bz = 0;
         T.ak = T.bk = 0;
         T.pieces = pieces;
-        T.left = 64;
-        T.rows = n - mi * kHigh;
+        T.left = min(each, left); // rows that are there
+        T.rows = min(high, N - mi * high);
+        T.cols = min(each, (left + kUnit - 1) / kUnit * kUnit);
+        T.high = high / kCG;
         return T;
     }
-    using Held = typename Out<kAdd>::Held;
-    using In = typename Out<kAdd>::In;
-    __device__ __forceinline__ void ahead(const Spot &T, int r, int half, int BN) const {
-        if (r < T.rows) out.ahead(T.m + r, T.n, half, BN);
+    using Held = Nothing;
+    using In = Nothing;
+    // 32 columns of y (lane = column, o.rows of them there) of 32 rows from n on
+    __device__ __forceinline__ void tile(Out32 &o, const Spot &T, int n, const float (&v)[32], const In &) const {
+        const int rows = T.n + T.left - n;
+        if (rows <= 0) return;
+        if (!kAdd && rows >= 32) {
+            if (dtype == WASTE_ACT_F32) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t *t = reinterpret_cast<uint32_t *>(o.next());
+                    if (o.lane / 16 == h)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) t[dense::turned(i, o.lane % 16 / 4, 4) * 4 + o.lane % 4] = __float_as_uint(v[i]);
+                    send(o, t, o.m + 16 * h, n, 16 * h < o.rows);
+                }
+            } else {
+                uint16_t *t = reinterpret_cast<uint16_t *>(o.next());
+                // two rows at a time: their values of a column, rounded together
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                    const uint32_t w = dtype == WASTE_ACT_BF16 ? dense::two(v[i], v[i + 1], __nv_bfloat16()) : dense::two(v[i], v[i + 1], __half());
+                    t[dense::turned(i, o.lane / 8, 4) * 8 + o.lane % 8] = (uint16_t)w;
+                    t[dense::turned(i + 1, o.lane / 8, 4) * 8 + o.lane % 8] = (uint16_t)(w >> 16);
+                }
+                send(o, t, o.m, n, true);
+            }
+            return;
+        }
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+            uint4 *t = o.next();
+            float *f = reinterpret_cast<float *>(t);
+            if (o.lane / 16 == h)
+#pragma unroll
+                for (int i = 0; i < 32; ++i) f[dense::turned(i, o.lane % 16 / 4, 4) * 4 + o.lane % 4] = v[i];
+            __syncwarp();
+            const size_t at = (size_t)n * N + o.m + 16 * h;
+            const int cols = N - o.m - 16 * h;
+            if (dtype == WASTE_ACT_F32)
+                dense::drain(t, static_cast<float *>(out) + at, N, rows, cols, true, kAdd, o.lane);
+            else if (dtype == WASTE_ACT_BF16)
+                dense::drain(t, static_cast<__nv_bfloat16 *>(out) + at, N, rows, cols, true, kAdd, o.lane);
+            else
+                dense::drain(t, static_cast<__half *>(out) + at, N, rows, cols, true, kAdd, o.lane);
+        }
     }
-    __device__ __forceinline__ void fetch(const Out32 &o, const Spot &, int n, Held &h) const { out.fetch(o, n, h); }
-    __device__ __forceinline__ void turn(const Out32 &o, uint4 *t, const Held &h, In &in) const { out.turn(o, t, h, in); }
-    __device__ __forceinline__ void tile(Out32 &o, const Spot &, int n, const float (&v)[32], const In &in) const {
-        out.put(o, n, v, in);
+    __device__ __forceinline__ void send(Out32 &o, const void *t, int x, int y, bool any) const {
+        tc::fence_proxy_async();
+        __syncwarp();
+        if (o.lane == 0 && any) tc::tma_store(&to, x, y, tc::smem_u32(t));
     }
 };
 
 // dW: the rows are what is summed over.
 template <int kCG, bool kAdd> struct WeightsJob {
     static constexpr int kHigh = kBM * kCG;
-    static constexpr bool kAmn = true, kBmn = true, kMask = true, kReads = kAdd;
+    static constexpr bool kAmn = true, kBmn = true, kMask = true, kReads = kAdd, kTwoPieces = !kAdd, kRagged = false;
     CUtensorMap ta, tb;
     Out<kAdd> out;
     Offsets off;
     int BN, tm, tn, M;
-    __device__ void begin(uint8_t *smem) const { off.read(reinterpret_cast<int *>(smem), nullptr, 0, 0); }
+    __device__ void begin(uint8_t *smem) const { off.read(reinterpret_cast<int *>(smem), nullptr); }
     __device__ __forceinline__ int tiles(const uint8_t *) const { return off.E * tm * tn; }
     __device__ __forceinline__ Spot spot(const uint8_t *smem, int t) const {
         const int *first = reinterpret_cast<const int *>(smem);
@@ -165,23 +237,34 @@ constexpr std::false_type kNo;
 // Whole widths of 32 columns, 256 at most.
 int width(int n) { return n >= 256 ? 256 : n <= 64 ? 64 : (n + 31) / 32 * 32; }
 
-// Pairs of CTAs, with tiles of 256 rows, from so many rows an expert on (their mean: the offsets are on the device).
+// Pairs of CTAs from so many rows an expert on (their mean: the offsets are on the device): they halve the bytes of W
+// an SM takes in for its columns, which counts once W is not what memory is read for.
 bool pairs(const Group &G) { return G.rows / G.E >= 160; }
+
+// Rows of an expert in one tile: few where there are few, so that the stages, which have room for as many, hold more of
+// W on its way (one token, 16 rows of 16 experts: 73 us with 256, 59 with 64).
+int share_rows(const Group &G) { return G.rows / G.E < 32 ? 64 : 256; }
 
 template <int kCG, bool kWmn, bool kAdd>
 cudaError_t rows_product(const Group &G, const void *a, int K, const void *w, int N, void *out, int out_dtype, cudaStream_t s) {
     RowsJob<kCG, kWmn, kAdd> J = {};
     TileArgs P = {};
-    P.BN = J.BN = width(N);
-    J.off = {G.offsets, G.E, G.rows};
-    J.tn = (N + J.BN - 1) / J.BN;
+    P.BN = J.off.share = share_rows(G);
+    J.off.p = G.offsets, J.off.E = G.E, J.off.rows = G.rows;
+    J.N = N;
     J.pieces = (K + 63) / 64;
-    cudaError_t e = stack_map(&J.ta, a, K, G.rows, 1, K, (size_t)K * G.rows, kBM);
-    if (e == cudaSuccess) e = stack_map(&J.tb, w, G.k, G.n, G.E, G.k, (size_t)G.k * G.n, kWmn ? 64 : J.BN / kCG);
-    if (e == cudaSuccess) e = J.out.set(out, G.rows, N, out_dtype);
+    J.out = out;
+    J.dtype = out_dtype;
+    cudaError_t e = stack_map(&J.ta, w, G.k, G.n, G.E, G.k, (size_t)G.k * G.n, kWmn ? 64 : kBM);
+    if (e == cudaSuccess) e = stack_map(&J.ta_low, w, G.k, G.n, G.E, G.k, (size_t)G.k * G.n, 32);
+    if (e == cudaSuccess) e = stack_map(&J.tb, a, K, G.rows, 1, K, (size_t)K * G.rows, 64);
+    if (e == cudaSuccess) e = stack_map(&J.tb_low, a, K, G.rows, 1, K, (size_t)K * G.rows, 16);
+    if (e == cudaSuccess) e = dense::store_map(&J.to, out, (int)dense::type_size(out_dtype), G.rows, N);
     if (e != cudaSuccess) return e;
-    const long long most = ((long long)G.rows / J.kHigh + (G.E < G.rows ? G.E : G.rows)) * J.tn;
-    return launch_tiles_as<kCG>(P, J, G.dtype == WASTE_ACT_BF16, (size_t)(G.E + 1) * 8, most, device_sm_count(), s);
+    const long long shares = (long long)G.rows / P.BN + (G.E < G.rows ? G.E : G.rows);
+    const int low = kCG == 2 ? J.kTall : kWmn ? 64 : 32;
+    return launch_tiles_as<kCG>(P, J, G.dtype == WASTE_ACT_BF16, (size_t)(G.E + 2) * 8, shares * ((N + low - 1) / low),
+                                device_sm_count(), s);
 }
 
 template <int kCG, bool kAdd>
@@ -189,7 +272,7 @@ cudaError_t weights_product(const Group &G, const void *dy, const void *x, void 
     WeightsJob<kCG, kAdd> J = {};
     TileArgs P = {};
     P.BN = J.BN = width(G.k);
-    J.off = {G.offsets, G.E, G.rows};
+    J.off = {G.offsets, G.E, G.rows, 0};
     J.M = G.n;
     J.tm = (G.n + J.kHigh - 1) / J.kHigh;
     J.tn = (G.k + J.BN - 1) / J.BN;

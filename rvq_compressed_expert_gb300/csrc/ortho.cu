@@ -187,7 +187,7 @@ __host__ __device__ __forceinline__ void triangle(int t, int &i, int &j) {
 }
 // Partial sums of A = X X^T (kMn: X^T X): [matrix][share of k][tile][side][side], fp32.
 template <bool kMn> struct GramJob {
-    static constexpr bool kAmn = kMn, kBmn = kMn, kMask = false, kReads = false;
+    static constexpr bool kAmn = kMn, kBmn = kMn, kMask = false, kReads = false, kTwoPieces = false, kRagged = false;
     CUtensorMap ta, tb, to;
     void *out;
     int side, tri, slices, count, pieces;
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kFlat) gram_kernel(const float *parts, int sid
 }
 // B = b A + c A^2, its diagonal apart
 struct SquareJob {
-    static constexpr bool kAmn = false, kBmn = false, kMask = false, kReads = true;
+    static constexpr bool kAmn = false, kBmn = false, kMask = false, kReads = true, kTwoPieces = false, kRagged = false;
     CUtensorMap ta, tb, to;
     Stack s;
     const void *a;
@@ -297,7 +297,7 @@ struct SquareJob {
 // X <- a X + B X (kTall: a X + X B), the last one to the caller's memory
 // kAdd: the last one added to what is there
 template <bool kTall, bool kLast, bool kAdd> struct StepJob {
-    static constexpr bool kAmn = false, kBmn = !kTall, kMask = false, kReads = true;
+    static constexpr bool kAmn = false, kBmn = !kTall, kMask = false, kReads = true, kTwoPieces = false, kRagged = false;
     CUtensorMap ta, tb, thi, tlo;
     Stack s;
     const void *hi;

@@ -9,6 +9,9 @@
 // A job J (a kernel argument, with its tensor maps ta and tb) has
 //   kAmn, kBmn   operands that lie with m (or n) contiguous (MN-major) rather than k
 //   kReads       an epilogue that reads
+//   kTwoPieces   an epilogue that reads nothing and has registers for two pieces of 32 columns at once
+//   kRagged      tiles of their own heights and widths: A also comes in boxes of 32 rows (ta_low), B (K-major) in boxes
+//                of 64 and 16 (tb, tb_low)
 //   kMask        tiles whose k ends inside a piece that holds other values: those are cleared in shared memory
 //   begin(smem)  by all threads, once what the kernel before wrote is visible; smem: P.job_bytes of its own
 //   tiles(smem), spot(smem, t): how many, and which
@@ -41,6 +44,8 @@ struct Spot {
     int ak, bk;         // their first k
     int pieces, left;   // pieces of k; how many k of the last one count (kMask)
     int m, n, rows;     // place in the result: first row, first column, rows that are the tile's
+    // kRagged: columns of the tile (a multiple of 16 a CTA), and the rows of A that each CTA loads (of 32, MN-major 64)
+    int cols = 0, high = 0;
 };
 struct TileArgs {
     int BN, stages;
@@ -228,7 +233,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
             tc::mbar_init(bar_acce + 8 * i, 8 * kCG);
         }
         tc::mbar_init(drain, 1);
-                *abort_flag = 0;
+        *abort_flag = 0;
         tc::mbar_init_fence();
     }
     if (warp == 2) {
@@ -256,7 +261,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
         const uint32_t full0 = kCG == 2 ? tc::map_rank(bar_full, 0) : bar_full;
         for (int t = tile0; t < tiles && ok; t += step) {
             const Spot T = job.spot(mine, t);
-            const int am = T.am + rank * kBM, bm = T.bm + (kCG == 2 ? rank * (BN / 2) : 0);
+            const int am = T.am + rank * kBM, bm = T.bm + (kCG == 2 ? rank * ((J::kRagged ? T.cols : BN) / 2) : 0);
             for (int kb = 0; kb < T.pieces; ++kb) {
                 if (!all(tc::mbar_wait(bar_empty + 8 * st, ph ^ 1))) {
                     ok = false;
@@ -267,7 +272,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
                     // a piece to be masked counts on each CTA's own barrier
                     const bool own = kCG == 1 || (J::kMask && kb + 1 == T.pieces && T.left < 64);
                     const uint32_t full = own ? bar_full + 8 * st : full0 + 8 * st;
-                    if (leads || own) tc::mbar_arrive_expect_tx(bar_full + 8 * st, (own ? 1 : kCG) * (a_bytes + b_bytes));
+                    const uint32_t bytes = J::kRagged ? (uint32_t)(T.high + T.cols / kCG) * kRowBytes : a_bytes + b_bytes;
+                    if (leads || own) tc::mbar_arrive_expect_tx(bar_full + 8 * st, (own ? 1 : kCG) * bytes);
                     const auto load = [&](uint32_t dst, const CUtensorMap *m, int x, int y, int z) {
                         if (kCG == 2 && !(J::kMask && own))
                             tma_load3_pair(dst, m, x, y, z, full);
@@ -276,12 +282,20 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
                     };
                     const int ka = T.ak + kb * 64, kk = T.bk + kb * 64;
                     if (J::kAmn) {
-                        for (int i = 0; i < kBM / 64; ++i) load(sa + i * 8192, &job.ta, am + 64 * i, ka, T.az);
+                        for (int i = 0; i < (J::kRagged ? T.high : kBM) / 64; ++i) load(sa + i * 8192, &job.ta, am + 64 * i, ka, T.az);
+                    } else if (J::kRagged && T.high < kBM) {
+                        if constexpr (J::kRagged)
+                            for (int i = 0; i < T.high; i += 32) load(sa + i * kRowBytes, &job.ta_low, ka, am + i, T.az);
                     } else {
                         load(sa, &job.ta, ka, am, T.az);
                     }
                     if (J::kBmn) {
                         for (uint32_t i = 0; i * 8192 < b_bytes; ++i) load(sb + i * 8192, &job.tb, bm + 64 * i, kk, T.bz);
+                    } else if constexpr (J::kRagged) {
+                        const int n = T.cols / kCG;
+                        int i = 0;
+                        for (; i + 64 <= n; i += 64) load(sb + i * kRowBytes, &job.tb, kk, bm + i, T.bz);
+                        for (; i < n; i += 16) load(sb + i * kRowBytes, &job.tb_low, kk, bm + i, T.bz);
                     } else {
                         load(sb, &job.tb, kk, bm, T.bz);
                     }
@@ -328,6 +342,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
                 }
                 tc::fence_after_sync();
                 const uint32_t d = tmem + buf * 256;
+                const uint32_t idesc = J::kRagged ? (P.idesc & ~(63u << 17)) | (uint32_t)(T.cols >> 3) << 17 : P.idesc;
                 for (int kb = 0; kb < T.pieces; ++kb) {
                     if (!all(tc::mbar_wait(bar_full + 8 * st, ph))) {
                         ok = false;
@@ -355,9 +370,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
                             const uint64_t dj = da + (uint64_t)(j * ((J::kAmn ? 2048 : 32) >> 4));
                             const uint64_t ej = db + (uint64_t)(j * ((J::kBmn ? 2048 : 32) >> 4));
                             if (kCG == 2)
-                                tc::mma_f16_pair(d, dj, ej, P.idesc, j > 0 || kb > 0);
+                                tc::mma_f16_pair(d, dj, ej, idesc, j > 0 || kb > 0);
                             else
-                                tc::mma_f16(d, dj, ej, P.idesc, j > 0 || kb > 0);
+                                tc::mma_f16(d, dj, ej, idesc, j > 0 || kb > 0);
                         }
                         commit(bar_empty + 8 * st);
                         if (kb + 1 == T.pieces) commit(bar_accf + 8 * buf);
@@ -411,6 +426,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
             if constexpr (J::kReads)
                 if (t + step < tiles) job.ahead(job.spot(mine, t + step), 32 * q + rank * kBM + lane, half, BN);
             const uint32_t src = tmem + buf * 256 + ((uint32_t)(32 * q) << 16);
+            const int width = J::kRagged ? T.cols : BN;
             const auto ready = [&] { // the tile's sums
                 if (empty) return true;
                 ++it;
@@ -432,28 +448,28 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
                         tc::mbar_arrive_cluster(tc::map_rank(bar_acce + 8 * buf, 0));
                 }
             };
-            if constexpr (!J::kReads) {
+            if constexpr (J::kTwoPieces) {
                 // nothing but the sums: two pieces to registers at once, so that the next tile's MMAs may follow while
                 // the last two are on their way out
                 if (!ready()) break;
                 alignas(16) uint32_t v[32], w[32];
                 const auto take = [&](int c) {
                     if (any && !empty) {
-                        if (c < BN) tc::tmem_ld32(src + c, v);
-                        if (c + 64 < BN) tc::tmem_ld32(src + c + 64, w);
-                        if (c < BN) tc::tmem_wait_ld(v);
-                        if (c + 64 < BN) tc::tmem_wait_ld(w);
+                        if (c < width) tc::tmem_ld32(src + c, v);
+                        if (c + 64 < width) tc::tmem_ld32(src + c + 64, w);
+                        if (c < width) tc::tmem_wait_ld(v);
+                        if (c + 64 < width) tc::tmem_wait_ld(w);
                     } else {
 #pragma unroll
                         for (int k = 0; k < 32; ++k) v[k] = w[k] = 0;
                     }
                 };
                 const auto give = [&](int c) {
-                    if (any && c < BN) job.tile(out, T, T.n + c, reinterpret_cast<const float(&)[32]>(v), {});
-                    if (any && c + 64 < BN) job.tile(out, T, T.n + c + 64, reinterpret_cast<const float(&)[32]>(w), {});
+                    if (any && c < width) job.tile(out, T, T.n + c, reinterpret_cast<const float(&)[32]>(v), {});
+                    if (any && c + 64 < width) job.tile(out, T, T.n + c + 64, reinterpret_cast<const float(&)[32]>(w), {});
                 };
                 take(32 * half);
-                if (BN <= 128) {
+                if (width <= 128) {
                     free_acc();
                     give(32 * half);
                 } else {
