@@ -4,7 +4,8 @@ Per layer L, for one batch of tokens with residual h_L (page "Exécuter Kimi K3
 avec 29 Go de RAM à 0,50 tok/s", section "Lecture anticipée et prédiction du
 routeur"):
   - x_L = rmsnorm(h_L)  (stand-in for the trunk's normalisation of the MoE
-    input; without it the chain h <- h + MoE(h) diverges at these scales),
+    input; without it the chain h <- h + MoE(h) diverges at these scales), or the layer's own
+    layer norm where it has one (``norm``),
   - on the main stream layer L routes x_L (waste_moe_route),
   - on a side stream, once that route is done, layer L+1's router runs on x_L and
     its top-P experts are prefetched into L2 (waste_moe_prefetch),
@@ -30,11 +31,13 @@ import torch
 
 from . import binding as B
 from .dense import DenseExpert
+from .norm import LayerNorm
 
 
 class DecodeStack:
-    def __init__(self, layers, tokens: int, device="cuda", banked: bool = False, shared=None):
-        """shared: None, or per layer None, a ``dense.DenseExpert`` or an ``mx4.Mx4Expert`` with
+    def __init__(self, layers, tokens: int, device="cuda", banked: bool = False, shared=None, norm=None):
+        """norm: None, or per layer None (rmsnorm with unit weight) or a ``norm.LayerNorm`` of the hidden size.
+        shared: None, or per layer None, a ``dense.DenseExpert`` or an ``mx4.Mx4Expert`` with
         max_tokens >= tokens, applied to the layer's input and added to the residual.
         banked: the layers' records live in a tiered bank (TieredStack); each layer's
         forward is then issued before the lookahead into the next layer, whose copies into
@@ -54,6 +57,12 @@ class DecodeStack:
         for e in self.shared:
             if e is not None and (e.d != w.d or e.max_tokens < tokens):
                 raise ValueError("a shared expert has another hidden size or too small a max_tokens")
+        self.norm = list(norm) if norm is not None else [None] * len(layers)
+        if len(self.norm) != len(layers):
+            raise ValueError(f"{len(self.norm)} norms for {len(layers)} layers")
+        for n in self.norm:
+            if n is not None and not (isinstance(n, LayerNorm) and n.d == w.d):
+                raise ValueError("a norm is no LayerNorm or has another hidden size")
         # 16-bit copies of x_L, for the shared experts whose weights are of that type
         self.x16 = {t: torch.empty(tokens, w.d, dtype=t, device=device)
                     for t in {e.dtype for e in self.shared if isinstance(e, DenseExpert)}}
@@ -73,7 +82,7 @@ class DecodeStack:
             return self._run_one_token(lookahead, main, on_layer)
         for L in range(n):
             x = self.x[L & 1]
-            B.waste_moe_rmsnorm(self.h, x, T, self.d, main)
+            self._normalize(L, x, main)
             if pending is not None:
                 main.wait_event(pending)  # layer L's prediction is in place before it routes
             self.layers[L].route(x, T, self.idx, self.gate, stream=main)
@@ -92,6 +101,13 @@ class DecodeStack:
         if pending is not None:
             main.wait_event(pending)
         return self.h
+
+    def _normalize(self, L, x, main):
+        """x = layer L's norm of the residual."""
+        if self.norm[L] is None:
+            B.waste_moe_rmsnorm(self.h, x, self.T, self.d, main)
+        else:
+            self.norm[L].forward(self.h, x, stream=main)
 
     def _add_shared(self, L, x, main):
         """h += shared expert of layer L applied to x_L, if the layer has one."""
@@ -114,7 +130,7 @@ class DecodeStack:
             B.waste_moe_set_lookahead(self.layers[L].handle, nxt, lookahead if nxt is not None else 0)
         for L in range(n):
             x = self.x[L & 1]
-            B.waste_moe_rmsnorm(self.h, x, 1, self.d, main)
+            self._normalize(L, x, main)
             self.layers[L].step(x, 1, self.idx, self.gate, self.h, 1, stream=main)
             self._add_shared(L, x, main)
             if on_layer is not None:
@@ -127,7 +143,7 @@ class DecodeStack:
         pending = None
         for L in range(n):
             x = self.x[L & 1]
-            B.waste_moe_rmsnorm(self.h, x, T, self.d, main)
+            self._normalize(L, x, main)
             x_ready = torch.cuda.Event()
             x_ready.record(main)
             if pending is not None:

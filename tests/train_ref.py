@@ -116,3 +116,9 @@ def orthogonal_rounded(g, steps=5, coefficients=MUON):
         d = torch.diagonal(q).clone()
         x = a * x + d[:, None] * (x if i + 2 >= steps else h) + r(q - torch.diag(d)) @ h
     return x.T if tall else x
+
+
+def dense_distance(a, b):
+    """Norm of the difference over the norm of b (of a where b is zero)."""
+    n = b.norm()
+    return float((a.double() - b).norm() / n) if n > 0 else float(a.double().norm())
