@@ -149,7 +149,7 @@ template <int V> __device__ __forceinline__ void widen_params(const void *p, int
 // A lane's values of a row, in kHeld / V pieces a group's width apart: whole pieces from a copy of the row in shared
 // memory, single values straight from memory.  kFull: the row fills all lanes.
 template <class X, int V, bool kFull> struct Lane {
-    static constexpr int H = kHeld, kPieces = H / V;
+    enum { H = kHeld, kPieces = H / V };
     int t, gt, d;
     __device__ __forceinline__ int column(int i) const { return (i * gt + t) * V; }
     __device__ __forceinline__ bool in(int i) const { return kFull || column(i) < d; }
@@ -168,6 +168,21 @@ template <class X, int V, bool kFull> struct Lane {
                     x[i / 2].y = v;
                 else
                     x[i / 2].x = v;
+            }
+        }
+    }
+    // rounded to their places
+    template <class Y> __device__ __forceinline__ void give(Y *row, const float2 (&y)[H / 2]) const {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            if (!in(i)) continue;
+            if constexpr (V == 8) {
+                Piece<Y, V> o;
+#pragma unroll
+                for (int k = 0; k < V / 2; ++k) round2(&o.v[2 * k], y[V / 2 * i + k]);
+                *reinterpret_cast<Piece<Y, V> *>(row + column(i)) = o;
+            } else {
+                row[column(i)] = round_to<Y>(i & 1 ? y[i / 2].y : y[i / 2].x);
             }
         }
     }
@@ -196,10 +211,23 @@ __device__ __forceinline__ void stage(float *to, const void *p, int dtype, int d
         to[(i & 4 ? d / 2 : 0) + (i >> 3) * 4 + (i & 3)] = v[0];
     }
 }
+// A piece in shared memory, said to be there (an address that the compiler has lost track of goes the long way).
+__device__ __forceinline__ uint4 shared16(uint32_t at) {
+    uint4 u;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(at) : "memory");
+    return u;
+}
+template <class X> __device__ __forceinline__ Piece<X, 8> load_shared(uint32_t at) {
+    Piece<X, 8> q;
+    reinterpret_cast<uint4 *>(&q)[0] = shared16(at);
+    if constexpr (sizeof(X) == 4) reinterpret_cast<uint4 *>(&q)[1] = shared16(at + 16);
+    return q;
+}
+
 // Four of them from column c on (a multiple of 4).
-__device__ __forceinline__ void four(const float *p, int d, int c, float2 &a, float2 &b) {
-    const float4 q = *reinterpret_cast<const float4 *>(p + (c & 4 ? d / 2 : 0) + (c >> 3) * 4);
-    a = make_float2(q.x, q.y), b = make_float2(q.z, q.w);
+__device__ __forceinline__ void four(uint32_t p, int d, int c, float2 &a, float2 &b) {
+    const uint4 q = shared16(p + ((c & 4 ? d / 2 : 0) + (c >> 3) * 4) * 4);
+    a = make_float2(__uint_as_float(q.x), __uint_as_float(q.y)), b = make_float2(__uint_as_float(q.z), __uint_as_float(q.w));
 }
 
 // The rows of one operand on their way to a group of warps: `deep` places in shared memory, filled in order by bulk
@@ -207,13 +235,13 @@ __device__ __forceinline__ void four(const float *p, int d, int c, float2 &a, fl
 template <class X> struct Ring {
     const X *p;
     int64_t ld;
-    uint8_t *at;      // this group's places
-    uint32_t bytes, pitch, bars, deep;
-    __device__ __forceinline__ const X *place(uint32_t i) const { return reinterpret_cast<const X *>(at + i * pitch); }
+    uint32_t at;      // this group's places
+    uint32_t bytes, bars;
+    __device__ __forceinline__ uint32_t place(uint32_t i) const { return at + i * bytes; }
     __device__ __forceinline__ void ask(int64_t row, uint32_t i) const { // by one thread
         const uint32_t bar = bars + 8 * i;
         tc::mbar_arrive_expect_tx(bar, bytes);
-        tc::bulk_g2s(tc::smem_u32(at + i * pitch), p + row * ld, bytes, bar);
+        tc::bulk_g2s(place(i), p + row * ld, bytes, bar);
     }
 };
 // A wait gives up after 1.1 s: then none is waited for any more, and waste_dense_status reports it.
@@ -225,128 +253,122 @@ __device__ __forceinline__ void wait_row(uint32_t bar, uint32_t parity, volatile
     }
 }
 
-// One pass.  kFew: a row a group, straight from memory, w and b held too, for all loads to be on their way at once;
-// otherwise (V == 8) kRowsAtOnce rows at a time.
-constexpr int kRowsAtOnce = 4;
-template <class X, class Y, int V, bool kFull, bool kFew>
-__global__ void __launch_bounds__(kHeldThreads) forward_held_kernel(const NormFwd P, int gw, int deep) {
-    using L = Lane<X, V, kFull>;
-    constexpr int N = kHeld / 2, R = kFew ? 1 : kRowsAtOnce;
-    static_assert(kFew || V == 8, "copies take whole pieces");
+// Few rows: a row a group, straight from memory, w and b held too, for all loads to be on their way at once.
+template <class X, class Y, int V>
+__global__ void __launch_bounds__(kHeldThreads) forward_few_kernel(const NormFwd P, int gw) {
+    using L = Lane<X, V, false>;
+    constexpr int N = kHeld / 2;
+    __shared__ float part[64];
+    tc::grid_wait_release();
+    const int gt = gw * 32, g = threadIdx.x / gt, t = threadIdx.x % gt, groups = blockDim.x / gt;
+    const float inv = 1.f / (float)P.d;
+    const L lane{t, gt, P.d};
+    int slot = 0;
+    for (int64_t row = (int64_t)blockIdx.x * groups + g; row < P.T; row += (int64_t)gridDim.x * groups) {
+        float2 x[N], w[N], b[N], s = both(0.f);
+        lane.take(static_cast<const X *>(P.x.p) + row * P.x.ld, x);
+        lane.params(P.w, P.w_dtype, 1.f, w);
+        lane.params(P.b, P.w_dtype, 0.f, b);
+#pragma unroll
+        for (int i = 0; i < N; ++i) s = add2(s, x[i]);
+        const float mu = group_sum(s.x + s.y, gw, g, part, slot) * inv;
+        s = both(0.f);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            x[i] = add2(x[i], both(-mu));
+            if (!lane.first(i)) x[i].x = 0.f;
+            if (!lane.second(i)) x[i].y = 0.f;
+            s = fma2(x[i], x[i], s);
+        }
+        const float r = 1.f / sqrtf(group_sum(s.x + s.y, gw, g, part, slot) * inv + P.eps);
+        if (P.mean && t == 0) {
+            P.mean[row] = mu;
+            P.rstd[row] = r;
+        }
+        Y *y = static_cast<Y *>(P.y.p) + row * P.y.ld;
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = fma2(mul2(x[i], both(r)), w[i], b[i]);
+        lane.give(y, x);
+    }
+}
+
+// Many rows: kStreamHeld values a lane, so that a row takes eight warps at most and an SM works on four rows or more at
+// once, each group at a step of its own.
+constexpr int kStreamHeld = 32, kStreamPieces = kStreamHeld / 8, kStreamThreads = 768;
+template <class X, class Y>
+__global__ void __launch_bounds__(kStreamThreads) forward_stream_kernel(const NormFwd P, int gw, int deep) {
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float part[64 * R];
-    __shared__ __align__(8) uint64_t bars[kHeldThreads / 32 * kDeepMost];
+    __shared__ float part[64];
+    __shared__ __align__(8) uint64_t bars[32 * kDeepMost];
     __shared__ uint32_t gave_up;
     tc::grid_wait_release();
     const int gt = gw * 32, g = threadIdx.x / gt, t = threadIdx.x % gt, groups = blockDim.x / gt;
     const float inv = 1.f / (float)P.d;
-    const int64_t step = (int64_t)gridDim.x * groups, row0 = (int64_t)blockIdx.x * groups + g;
-    const L lane{t, gt, P.d};
+    const int step = gridDim.x * groups, row0 = blockIdx.x * groups + g; // rows are 2^30 at most
     const uint32_t bytes = P.d * (uint32_t)sizeof(X);
-    const Ring<X> ring{static_cast<const X *>(P.x.p), P.x.ld, smem + (size_t)g * deep * bytes, bytes, bytes,
-                       tc::smem_u32(bars + g * deep), (uint32_t)deep};
+    const Ring<X> ring{static_cast<const X *>(P.x.p), P.x.ld, tc::smem_u32(smem) + g * deep * bytes, bytes,
+                       tc::smem_u32(bars + g * deep)};
     float *w = reinterpret_cast<float *>(smem + (size_t)groups * deep * bytes), *b = w + P.d;
-    if constexpr (!kFew) {
-        if (threadIdx.x == 0) gave_up = 0;
-        if (t == 0) {
-            for (int i = 0; i < deep; ++i) tc::mbar_init(ring.bars + 8 * i, 1);
-            tc::mbar_init_fence();
-            for (int i = 0; i < deep && row0 + i * step < P.T; ++i) ring.ask(row0 + i * step, i);
-        }
-        stage(w, P.w, P.w_dtype, P.d, 1.f);
-        stage(b, P.b, P.w_dtype, P.d, 0.f);
-        __syncthreads();
+    const uint32_t w_at = tc::smem_u32(w), b_at = tc::smem_u32(b);
+    if (threadIdx.x == 0) gave_up = 0;
+    if (t == 0) {
+        for (int i = 0; i < deep; ++i) tc::mbar_init(ring.bars + 8 * i, 1);
+        tc::mbar_init_fence();
+        for (int i = 0; i < deep && row0 + i * step < P.T; ++i) ring.ask(row0 + i * step, i);
     }
+    stage(w, P.w, P.w_dtype, P.d, 1.f);
+    stage(b, P.b, P.w_dtype, P.d, 0.f);
+    __syncthreads();
     int slot = 0;
     uint32_t turn = 0, phase = 0;
-    for (int64_t row = row0; row < P.T; row += R * step) {
-        // rows of this turn; past the last row the first one takes its place, and is not written again
-        int there = 1;
+    const auto column = [&](int i) { return (i * gt + t) * 8; };
+    for (int row = row0; row < P.T; row += step) {
+        float2 x[kStreamHeld / 2], s = both(0.f);
+        wait_row(ring.bars + 8 * turn, phase, &gave_up);
+        const uint32_t from = ring.place(turn);
 #pragma unroll
-        for (int q = 1; q < R; ++q) there += row + q * step < P.T;
-        float2 x[R][N], wv[kFew ? N : 1], bv[kFew ? N : 1];
-        float s[R];
-        uint32_t used[R];
+        for (int i = 0; i < kStreamPieces; ++i)
+            if (column(i) < P.d) {
+                const Piece<X, 8> q = load_shared<X>(from + column(i) * (uint32_t)sizeof(X));
 #pragma unroll
-        for (int q = 0; q < R; ++q) {
-            if constexpr (kFew) {
-                lane.take(ring.p + row * ring.ld, x[q]);
-                lane.params(P.w, P.w_dtype, 1.f, wv);
-                lane.params(P.b, P.w_dtype, 0.f, bv);
-            } else {
-                used[q] = q < there ? turn : used[0];
-                if (q < there) {
-                    wait_row(ring.bars + 8 * turn, phase, &gave_up);
-                    if (++turn == (uint32_t)deep) turn = 0, phase ^= 1;
+                for (int k = 0; k < 4; ++k) {
+                    x[4 * i + k] = widen2(&q.v[2 * k]);
+                    s = add2(s, x[4 * i + k]);
                 }
-                lane.take(ring.place(used[q]), x[q]);
             }
-            float2 a = both(0.f);
+        const float mu = group_sum(s.x + s.y, gw, g, part, slot) * inv;
+        if (t == 0 && row + deep * step < P.T) ring.ask(row + deep * step, turn); // the group has read this one
+        if (++turn == (uint32_t)deep) turn = 0, phase ^= 1;
+        s = both(0.f);
 #pragma unroll
-            for (int i = 0; i < N; ++i) a = add2(a, x[q][i]);
-            s[q] = a.x + a.y;
-        }
-        group_sums(s, gw, g, part, slot);
-        if constexpr (!kFew)
-            if (t == 0)
+        for (int i = 0; i < kStreamPieces; ++i)
+            if (column(i) < P.d) {
 #pragma unroll
-                for (int q = 0; q < R; ++q)
-                    if (row + (q + deep) * step < P.T) ring.ask(row + (q + deep) * step, used[q]);
-        float mu[R];
-#pragma unroll
-        for (int q = 0; q < R; ++q) {
-            mu[q] = s[q] * inv;
-            float2 a = both(0.f);
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                x[q][i] = add2(x[q][i], both(-mu[q]));
-                if (!kFull && !lane.first(i)) x[q][i].x = 0.f;
-                if (!kFull && !lane.second(i)) x[q][i].y = 0.f;
-                a = fma2(x[q][i], x[q][i], a);
+                for (int k = 0; k < 4; ++k) {
+                    x[4 * i + k] = add2(x[4 * i + k], both(-mu));
+                    s = fma2(x[4 * i + k], x[4 * i + k], s);
+                }
             }
-            s[q] = a.x + a.y;
+        const float r = 1.f / sqrtf(group_sum(s.x + s.y, gw, g, part, slot) * inv + P.eps);
+        if (P.mean && t == 0) {
+            P.mean[row] = mu;
+            P.rstd[row] = r;
         }
-        group_sums(s, gw, g, part, slot);
-        Y *y[R];
+        Y *y = static_cast<Y *>(P.y.p) + (int64_t)row * P.y.ld;
 #pragma unroll
-        for (int q = 0; q < R; ++q) {
-            y[q] = static_cast<Y *>(P.y.p) + (row + q * step) * P.y.ld;
-            s[q] = 1.f / sqrtf(s[q] * inv + P.eps);
-            if (P.mean && t == 0 && q < there) {
-                P.mean[row + q * step] = mu[q];
-                P.rstd[row + q * step] = s[q];
-            }
-        }
+        for (int i = 0; i < kStreamPieces; ++i)
+            if (column(i) < P.d) {
+                Piece<Y, 8> o;
 #pragma unroll
-        for (int i = 0; i < L::kPieces; ++i) {
-            if (!lane.in(i)) continue;
-            const int c = lane.column(i);
-            if constexpr (V == 8) {
-                Piece<Y, V> o[R];
-#pragma unroll
-                for (int k = 0; k < V; k += 4) {
-                    const int j = (V * i + k) / 2;
+                for (int k = 0; k < 8; k += 4) {
                     float2 w0, w1, b0, b1;
-                    if constexpr (kFew) {
-                        w0 = wv[j], w1 = wv[j + 1], b0 = bv[j], b1 = bv[j + 1];
-                    } else {
-                        four(w, P.d, c + k, w0, w1);
-                        four(b, P.d, c + k, b0, b1);
-                    }
-#pragma unroll
-                    for (int q = 0; q < R; ++q) {
-                        round2(&o[q].v[k], fma2(mul2(x[q][j], both(s[q])), w0, b0));
-                        round2(&o[q].v[k + 2], fma2(mul2(x[q][j + 1], both(s[q])), w1, b1));
-                    }
+                    four(w_at, P.d, column(i) + k, w0, w1);
+                    four(b_at, P.d, column(i) + k, b0, b1);
+                    round2(&o.v[k], fma2(mul2(x[4 * i + k / 2], both(r)), w0, b0));
+                    round2(&o.v[k + 2], fma2(mul2(x[4 * i + k / 2 + 1], both(r)), w1, b1));
                 }
-#pragma unroll
-                for (int q = 0; q < R; ++q)
-                    if (q < there) *reinterpret_cast<Piece<Y, V> *>(y[q] + c) = o[q];
-            } else {
-                const int j = i / 2;
-                y[0][c] = round_to<Y>(i & 1 ? fmaf(x[0][j].y * s[0], wv[j].y, bv[j].y) : fmaf(x[0][j].x * s[0], wv[j].x, bv[j].x));
+                *reinterpret_cast<Piece<Y, 8> *>(y + column(i)) = o;
             }
-        }
     }
 }
 
@@ -368,7 +390,8 @@ __global__ void __launch_bounds__(kHeldThreads) backward_held_kernel(const NormB
     const uint32_t xb = P.d * (uint32_t)sizeof(X), yb = P.d * (uint32_t)sizeof(Y), pitch = xb + yb;
     uint8_t *places = smem + (size_t)g * deep * pitch;
     const uint32_t bar0 = tc::smem_u32(bars + g * deep);
-    const float *w = reinterpret_cast<const float *>(smem + (size_t)groups * deep * pitch);
+    float *w = reinterpret_cast<float *>(smem + (size_t)groups * deep * pitch);
+    const uint32_t w_at = tc::smem_u32(w), places_at = tc::smem_u32(places);
     const auto x_at = [&](int64_t row) { return static_cast<const X *>(P.x.p) + row * P.x.ld; };
     const auto y_at = [&](int64_t row) { return static_cast<const Y *>(P.dy.p) + row * P.dy.ld; };
     const auto ask = [&](int64_t row, uint32_t i) {
@@ -383,7 +406,7 @@ __global__ void __launch_bounds__(kHeldThreads) backward_held_kernel(const NormB
             tc::mbar_init_fence();
             for (int i = 0; i < deep && row0 + i * step < P.T; ++i) ask(row0 + i * step, i);
         }
-        stage(const_cast<float *>(w), P.w, P.w_dtype, P.d, 1.f);
+        stage(w, P.w, P.w_dtype, P.d, 1.f);
         __syncthreads();
     }
     float2 dw[N], db[N];
@@ -414,17 +437,17 @@ __global__ void __launch_bounds__(kHeldThreads) backward_held_kernel(const NormB
                 if (++turn == (uint32_t)deep) turn = 0, phase ^= 1;
             }
         }
-        // (x - mu) r and dy w of piece i of row q, from shared memory (V == 1: from memory, an eighth of a piece)
-        const auto piece = [&](int q, int i, float2(&xh)[4], float2(&e)[4]) {
+        // x - mu and dy of piece i of row q, from shared memory (V == 1: from memory, eight single values)
+        const auto piece = [&](int q, int i, float2(&c)[4], float2(&e)[4]) {
             uint32_t at = first + q;
             if (at >= (uint32_t)deep) at -= deep;
-            const uint8_t *p = places + at * pitch;
+            const uint32_t p = places_at + at * pitch;
             Piece<X, 8> u = {};
             Piece<Y, 8> v = {};
             if constexpr (V == 8) {
                 if (lx.in(i) && row + q * step < P.T) {
-                    u = load<X, 8>(reinterpret_cast<const X *>(p) + lx.column(i));
-                    v = load<Y, 8>(reinterpret_cast<const Y *>(p + xb) + lx.column(i));
+                    u = load_shared<X>(p + lx.column(i) * (uint32_t)sizeof(X));
+                    v = load_shared<Y>(p + xb + lx.column(i) * (uint32_t)sizeof(Y));
                 }
             } else {
 #pragma unroll
@@ -436,7 +459,7 @@ __global__ void __launch_bounds__(kHeldThreads) backward_held_kernel(const NormB
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                xh[k] = mul2(add2(widen2(&u.v[2 * k]), both(-mu[q])), both(r[q]));
+                c[k] = add2(widen2(&u.v[2 * k]), both(-mu[q]));
                 e[k] = widen2(&v.v[2 * k]);
             }
         };
@@ -447,8 +470,8 @@ __global__ void __launch_bounds__(kHeldThreads) backward_held_kernel(const NormB
                     for (int k = 0; k < 4; ++k) o[k] = both(0.f);
                     return;
                 }
-                four(w, P.d, lx.column(i), o[0], o[1]);
-                four(w, P.d, lx.column(i) + 4, o[2], o[3]);
+                four(w_at, P.d, lx.column(i), o[0], o[1]);
+                four(w_at, P.d, lx.column(i) + 4, o[2], o[3]);
             } else {
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
@@ -467,15 +490,15 @@ __global__ void __launch_bounds__(kHeldThreads) backward_held_kernel(const NormB
             weights(i, wv);
 #pragma unroll
             for (int q = 0; q < R; ++q) {
-                float2 xh[4], e[4];
-                piece(q, i, xh, e);
+                float2 c[4], e[4];
+                piece(q, i, c, e);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    dw[4 * i + k] = fma2(e[k], xh[k], dw[4 * i + k]);
+                    const float2 xh = mul2(c[k], both(r[q])), gv = mul2(e[k], wv[k]);
+                    dw[4 * i + k] = fma2(e[k], xh, dw[4 * i + k]);
                     db[4 * i + k] = add2(db[4 * i + k], e[k]);
-                    e[k] = mul2(e[k], wv[k]);
-                    s1[q] = add2(s1[q], e[k]);
-                    s2[q] = fma2(e[k], xh[k], s2[q]);
+                    s1[q] = add2(s1[q], gv);
+                    s2[q] = fma2(gv, xh, s2[q]);
                 }
             }
         }
@@ -493,14 +516,15 @@ __global__ void __launch_bounds__(kHeldThreads) backward_held_kernel(const NormB
             weights(i, wv);
 #pragma unroll
             for (int q = 0; q < R; ++q) {
-                float2 xh[4], e[4];
-                piece(q, i, xh, e);
-                const float2 c1 = both(-s[2 * q] * inv), c2 = both(-s[2 * q + 1] * inv), rr = both(r[q]);
+                float2 c[4], e[4];
+                piece(q, i, c, e);
+                // r (g - m1 - (x - mu) r m2), its factors of the row put together first
+                const float2 rr = both(r[q]), c1 = both(-r[q] * (s[2 * q] * inv)), c2 = both(-r[q] * (r[q] * (s[2 * q + 1] * inv)));
                 X *dx = static_cast<X *>(P.dx.p) + (row + q * step) * P.dx.ld;
                 Piece<X, 8> o;
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    round2(&o.v[2 * k], mul2(fma2(xh[k], c2, add2(mul2(e[k], wv[k]), c1)), rr));
+                    round2(&o.v[2 * k], fma2(mul2(e[k], wv[k]), rr, fma2(c[k], c2, c1)));
                 if (row + q * step >= P.T) continue;
                 if constexpr (V == 8) {
                     if (lx.in(i)) *reinterpret_cast<Piece<X, 8> *>(dx + lx.column(i)) = o;
@@ -741,28 +765,24 @@ cudaError_t launch_norm_forward(const NormFwd &P, cudaStream_t s) {
         constexpr int V = decltype(v)::value;
         const int pieces = P.d / V + (P.d % V != 0), sms = device_sm_count();
         if (P.d <= kHeldMost) {
-            const int gw = group_warps(pieces, kHeld / V), most = kHeldThreads / 32 / gw;
-            const auto launch = [&](auto full, auto few) {
-                constexpr bool kFull = decltype(full)::value, kFew = decltype(few)::value;
-                static SmemAttr attr;
-                const auto kernel = forward_held_kernel<X, Y, V, kFull, kFew>;
-                const size_t row = sizeof(X) * P.d, rest = (size_t)P.d * 8;
-                // few rows: as many CTAs as there are SMs before several groups a CTA
-                int groups = (P.T + sms - 1) / sms;
-                if (groups > most) groups = most;
-                const int deep = kFew ? 1 : rows_ahead(row, rest, groups), smem = kFew ? 0 : (int)(deep * groups * row + rest);
-                cudaError_t e = ensure_smem(attr, reinterpret_cast<const void *>(kernel), smem);
-                if (e != cudaSuccess) return e;
-                const int blocks = (P.T + groups - 1) / groups, all = kFew ? 4 * sms : sms;
-                return launch_behind(kernel, dim3(blocks < all ? blocks : all), dim3(groups * gw * 32), smem, s, P, gw, deep);
-            };
             if constexpr (V == 8) {
-                // copies and staged parameters pay from some rows a group on, whose places fit
-                if (P.T > kFewRows * sms && rows_ahead(sizeof(X) * P.d, (size_t)P.d * 8, most) >= kRowsAtOnce)
-                    return P.d == gw * 32 * kHeld ? launch(std::true_type(), std::false_type())
-                                                  : launch(std::false_type(), std::false_type());
+                const int gw = group_warps(pieces, kStreamPieces), groups = kStreamThreads / 32 / gw;
+                const size_t row = sizeof(X) * P.d, rest = (size_t)P.d * 8;
+                if (P.T > kFewRows * sms) {
+                    static SmemAttr attr;
+                    const auto kernel = forward_stream_kernel<X, Y>;
+                    const int deep = rows_ahead(row, rest, groups), smem = (int)(deep * groups * row + rest);
+                    const cudaError_t e = ensure_smem(attr, reinterpret_cast<const void *>(kernel), smem);
+                    if (e != cudaSuccess) return e;
+                    const int blocks = (P.T + groups - 1) / groups;
+                    return launch_behind(kernel, dim3(blocks < sms ? blocks : sms), dim3(groups * gw * 32), smem, s, P, gw, deep);
+                }
             }
-            return launch(std::false_type(), std::true_type());
+            const int gw = group_warps(pieces, kHeld / V), most = kHeldThreads / 32 / gw;
+            int groups = (P.T + sms - 1) / sms; // as many CTAs as there are SMs before several groups a CTA
+            if (groups > most) groups = most;
+            const int blocks = (P.T + groups - 1) / groups;
+            return launch_behind(forward_few_kernel<X, Y, V>, dim3(blocks < 4 * sms ? blocks : 4 * sms), dim3(groups * gw * 32), 0, s, P, gw);
         }
         return launch_behind(forward_kernel<X, Y, V>, dim3(P.T < 4 * sms ? P.T : 4 * sms), dim3(kThreads), 0, s, P, kThreads / 32);
     });
