@@ -93,7 +93,7 @@ template <int n> __device__ __forceinline__ void group_sums(float (&v)[n], int g
 // b (in shared memory, in fp32) and their exchanges; values are held and computed in pairs; rows that fill all lanes
 // go without masks; and rows come by bulk copies, one instruction each.
 constexpr int kHeld = 16;
-template <int V> constexpr int rows_at_once() { return V == 8 ? 2 : 1; }
+template <int V> constexpr int kRowsAtOnce = V == 8 ? 2 : 1; // of a group in the backward
 constexpr int kHeldThreads = 512;
 constexpr int kHeldMost = kHeld * kHeldThreads;
 constexpr int kHeldSmem = 220 << 10;
@@ -202,13 +202,13 @@ template <class X, int V, bool kFull> struct Lane {
     __device__ __forceinline__ bool first(int j) const { return in(2 * j / V); }
     __device__ __forceinline__ bool second(int j) const { return in((2 * j + 1) / V); }
 };
-// w or b, in fp32, into shared memory, by all threads: of every eight the first four in one half and the last four in the
-// other, so that the lanes of a warp, eight columns apart, read neighbouring 16 bytes.
-__device__ __forceinline__ void stage(float *to, const void *p, int dtype, int d, float none) {
+// w or b, in fp32, into shared memory, by all threads.  V == 8: of every eight the first four in one half and the last
+// four in the other, so that the lanes of a warp, eight columns apart, read neighbouring 16 bytes.
+template <int V> __device__ __forceinline__ void stage(float *to, const void *p, int dtype, int d, float none) {
     for (int i = threadIdx.x; i < d; i += blockDim.x) {
         float v[1];
         widen_params<1>(p, dtype, i, none, v);
-        to[(i & 4 ? d / 2 : 0) + (i >> 3) * 4 + (i & 3)] = v[0];
+        to[V == 8 ? (i & 4 ? d / 2 : 0) + (i >> 3) * 4 + (i & 3) : i] = v[0];
     }
 }
 // A piece in shared memory, said to be there (an address that the compiler has lost track of goes the long way).
@@ -216,6 +216,19 @@ __device__ __forceinline__ uint4 shared16(uint32_t at) {
     uint4 u;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(at) : "memory");
     return u;
+}
+template <class X> __device__ __forceinline__ float shared_value(uint32_t at) {
+    if constexpr (sizeof(X) == 4) {
+        float v;
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+        return v;
+    } else {
+        uint16_t u;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(u) : "r"(at) : "memory");
+        X x;
+        *reinterpret_cast<uint16_t *>(&x) = u;
+        return widen(x);
+    }
 }
 template <class X> __device__ __forceinline__ Piece<X, 8> load_shared(uint32_t at) {
     Piece<X, 8> q;
@@ -230,20 +243,27 @@ __device__ __forceinline__ void four(uint32_t p, int d, int c, float2 &a, float2
     a = make_float2(__uint_as_float(q.x), __uint_as_float(q.y)), b = make_float2(__uint_as_float(q.z), __uint_as_float(q.w));
 }
 
-// The rows of one operand on their way to a group of warps: `deep` places in shared memory, filled in order by bulk
-// copies of one thread.  A place is free again once the group has met (in a sum) behind its reading.
-template <class X> struct Ring {
+// The rows of one operand on their way to a group of warps: places in shared memory, filled in order by bulk
+// copies of one thread.  A place is free again once the group has met (in a sum) behind its reading.  Copies take whole
+// 16-byte pieces: of a row that begins or ends inside one, its neighbours in that piece come too (nothing lies
+// between them and the row that could be out of memory: allocations begin and end on such pieces), and are not used.
+template <class X, bool kWhole> struct Ring {
     const X *p;
     int64_t ld;
-    uint32_t at;      // this group's places
-    uint32_t bytes, bars;
-    __device__ __forceinline__ uint32_t place(uint32_t i) const { return at + i * bytes; }
-    __device__ __forceinline__ void ask(int64_t row, uint32_t i) const { // by one thread
-        const uint32_t bar = bars + 8 * i;
-        tc::mbar_arrive_expect_tx(bar, bytes);
-        tc::bulk_g2s(place(i), p + row * ld, bytes, bar);
+    int d;
+    uint32_t at, pitch; // this group's places
+    __device__ __forceinline__ const X *row_at(int64_t row) const { return p + row * ld; }
+    // bytes between the place's start and the row's
+    __device__ __forceinline__ uint32_t shift(int64_t row) const { return kWhole ? 0 : (uint32_t)(uintptr_t)row_at(row) & 15u; }
+    __device__ __forceinline__ uint32_t bytes(int64_t row) const { return (shift(row) + d * (uint32_t)sizeof(X) + 15) & ~15u; }
+    __device__ __forceinline__ uint32_t place(int64_t row, uint32_t i) const { return at + i * pitch + shift(row); }
+    __device__ __forceinline__ void copy(int64_t row, uint32_t i, uint32_t bar) const {
+        tc::bulk_g2s(at + i * pitch, reinterpret_cast<const uint8_t *>(row_at(row)) - shift(row), bytes(row), bar);
     }
 };
+__host__ __device__ constexpr uint32_t ring_pitch(int d, uint32_t size, bool whole) {
+    return (d * size + 15) / 16 * 16 + (whole ? 0 : 16);
+}
 // A wait gives up after 1.1 s: then none is waited for any more, and waste_dense_status reports it.
 __device__ __forceinline__ void wait_row(uint32_t bar, uint32_t parity, volatile uint32_t *gave_up) {
     if (*gave_up) return;
@@ -294,61 +314,83 @@ __global__ void __launch_bounds__(kHeldThreads) forward_few_kernel(const NormFwd
 
 // Many rows: kStreamHeld values a lane, so that a row takes eight warps at most and an SM works on four rows or more at
 // once, each group at a step of its own.
-constexpr int kStreamHeld = 32, kStreamPieces = kStreamHeld / 8, kStreamThreads = 768;
-template <class X, class Y>
-__global__ void __launch_bounds__(kStreamThreads) forward_stream_kernel(const NormFwd P, int gw, int deep) {
+// (Single values: 16 a lane and more threads, as their addresses take registers too.)
+template <int V> constexpr int kStreamHeld = V == 8 ? 32 : 16;
+template <int V> constexpr int kStreamThreads = V == 8 ? 768 : 896;
+template <class X, class Y, int V>
+__global__ void __launch_bounds__(kStreamThreads<V>) forward_stream_kernel(const NormFwd P, int gw, int deep) {
+    constexpr int kPieces = kStreamHeld<V> / V, kSize = sizeof(X);
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float part[64];
-    __shared__ __align__(8) uint64_t bars[32 * kDeepMost];
+    __shared__ __align__(8) uint64_t bars[kStreamThreads<V> / 32 * kDeepMost];
     __shared__ uint32_t gave_up;
     tc::grid_wait_release();
     const int gt = gw * 32, g = threadIdx.x / gt, t = threadIdx.x % gt, groups = blockDim.x / gt;
     const float inv = 1.f / (float)P.d;
     const int step = gridDim.x * groups, row0 = blockIdx.x * groups + g; // rows are 2^30 at most
-    const uint32_t bytes = P.d * (uint32_t)sizeof(X);
-    const Ring<X> ring{static_cast<const X *>(P.x.p), P.x.ld, tc::smem_u32(smem) + g * deep * bytes, bytes,
-                       tc::smem_u32(bars + g * deep)};
-    float *w = reinterpret_cast<float *>(smem + (size_t)groups * deep * bytes), *b = w + P.d;
+    const uint32_t pitch = ring_pitch(P.d, kSize, V == 8), bar0 = tc::smem_u32(bars + g * deep);
+    const Ring<X, V == 8> ring{static_cast<const X *>(P.x.p), P.x.ld, P.d, tc::smem_u32(smem) + g * deep * pitch, pitch};
+    float *w = reinterpret_cast<float *>(smem + (size_t)groups * deep * pitch), *b = w + P.d;
     const uint32_t w_at = tc::smem_u32(w), b_at = tc::smem_u32(b);
+    const auto ask = [&](int row, uint32_t i) {
+        tc::mbar_arrive_expect_tx(bar0 + 8 * i, ring.bytes(row));
+        ring.copy(row, i, bar0 + 8 * i);
+    };
     if (threadIdx.x == 0) gave_up = 0;
     if (t == 0) {
-        for (int i = 0; i < deep; ++i) tc::mbar_init(ring.bars + 8 * i, 1);
+        for (int i = 0; i < deep; ++i) tc::mbar_init(bar0 + 8 * i, 1);
         tc::mbar_init_fence();
-        for (int i = 0; i < deep && row0 + i * step < P.T; ++i) ring.ask(row0 + i * step, i);
+        for (int i = 0; i < deep && row0 + i * step < P.T; ++i) ask(row0 + i * step, i);
     }
-    stage(w, P.w, P.w_dtype, P.d, 1.f);
-    stage(b, P.b, P.w_dtype, P.d, 0.f);
+    stage<V>(w, P.w, P.w_dtype, P.d, 1.f);
+    stage<V>(b, P.b, P.w_dtype, P.d, 0.f);
     __syncthreads();
     int slot = 0;
     uint32_t turn = 0, phase = 0;
-    const auto column = [&](int i) { return (i * gt + t) * 8; };
+    const auto column = [&](int i) { return (i * gt + t) * V; };
     for (int row = row0; row < P.T; row += step) {
-        float2 x[kStreamHeld / 2], s = both(0.f);
-        wait_row(ring.bars + 8 * turn, phase, &gave_up);
-        const uint32_t from = ring.place(turn);
+        float2 x[kStreamHeld<V> / 2], s = both(0.f);
+        wait_row(bar0 + 8 * turn, phase, &gave_up);
+        const uint32_t from = ring.place(row, turn);
 #pragma unroll
-        for (int i = 0; i < kStreamPieces; ++i)
-            if (column(i) < P.d) {
-                const Piece<X, 8> q = load_shared<X>(from + column(i) * (uint32_t)sizeof(X));
+        for (int i = 0; i < kPieces; ++i) {
+            const bool in = column(i) < P.d;
+            if constexpr (V == 8) {
+                if (in) {
+                    const Piece<X, 8> q = load_shared<X>(from + column(i) * kSize);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    x[4 * i + k] = widen2(&q.v[2 * k]);
-                    s = add2(s, x[4 * i + k]);
+                    for (int k = 0; k < 4; ++k) {
+                        x[4 * i + k] = widen2(&q.v[2 * k]);
+                        s = add2(s, x[4 * i + k]);
+                    }
                 }
+            } else {
+                const float v = in ? shared_value<X>(from + column(i) * kSize) : 0.f;
+                (i & 1 ? x[i / 2].y : x[i / 2].x) = v;
+                if (i & 1) s = add2(s, x[i / 2]);
             }
+        }
         const float mu = group_sum(s.x + s.y, gw, g, part, slot) * inv;
-        if (t == 0 && row + deep * step < P.T) ring.ask(row + deep * step, turn); // the group has read this one
+        if (t == 0 && row + deep * step < P.T) ask(row + deep * step, turn); // the group has read this one
         if (++turn == (uint32_t)deep) turn = 0, phase ^= 1;
         s = both(0.f);
 #pragma unroll
-        for (int i = 0; i < kStreamPieces; ++i)
-            if (column(i) < P.d) {
+        for (int i = 0; i < kPieces; ++i) {
+            const bool in = column(i) < P.d;
+            if constexpr (V == 8) {
+                if (in) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    x[4 * i + k] = add2(x[4 * i + k], both(-mu));
-                    s = fma2(x[4 * i + k], x[4 * i + k], s);
+                    for (int k = 0; k < 4; ++k) {
+                        x[4 * i + k] = add2(x[4 * i + k], both(-mu));
+                        s = fma2(x[4 * i + k], x[4 * i + k], s);
+                    }
                 }
+            } else {
+                float &v = i & 1 ? x[i / 2].y : x[i / 2].x;
+                v = in ? v - mu : 0.f;
+                if (i & 1) s = fma2(x[i / 2], x[i / 2], s);
             }
+        }
         const float r = 1.f / sqrtf(group_sum(s.x + s.y, gw, g, part, slot) * inv + P.eps);
         if (P.mean && t == 0) {
             P.mean[row] = mu;
@@ -356,18 +398,23 @@ __global__ void __launch_bounds__(kStreamThreads) forward_stream_kernel(const No
         }
         Y *y = static_cast<Y *>(P.y.p) + (int64_t)row * P.y.ld;
 #pragma unroll
-        for (int i = 0; i < kStreamPieces; ++i)
+        for (int i = 0; i < kPieces; ++i)
             if (column(i) < P.d) {
-                Piece<Y, 8> o;
+                if constexpr (V == 8) {
+                    Piece<Y, 8> o;
 #pragma unroll
-                for (int k = 0; k < 8; k += 4) {
-                    float2 w0, w1, b0, b1;
-                    four(w_at, P.d, column(i) + k, w0, w1);
-                    four(b_at, P.d, column(i) + k, b0, b1);
-                    round2(&o.v[k], fma2(mul2(x[4 * i + k / 2], both(r)), w0, b0));
-                    round2(&o.v[k + 2], fma2(mul2(x[4 * i + k / 2 + 1], both(r)), w1, b1));
+                    for (int k = 0; k < 8; k += 4) {
+                        float2 w0, w1, b0, b1;
+                        four(w_at, P.d, column(i) + k, w0, w1);
+                        four(b_at, P.d, column(i) + k, b0, b1);
+                        round2(&o.v[k], fma2(mul2(x[4 * i + k / 2], both(r)), w0, b0));
+                        round2(&o.v[k + 2], fma2(mul2(x[4 * i + k / 2 + 1], both(r)), w1, b1));
+                    }
+                    *reinterpret_cast<Piece<Y, 8> *>(y + column(i)) = o;
+                } else {
+                    const float v = i & 1 ? x[i / 2].y : x[i / 2].x;
+                    y[column(i)] = round_to<Y>(fmaf(v * r, shared_value<float>(w_at + column(i) * 4), shared_value<float>(b_at + column(i) * 4)));
                 }
-                *reinterpret_cast<Piece<Y, 8> *>(y + column(i)) = o;
             }
     }
 }
@@ -376,7 +423,7 @@ __global__ void __launch_bounds__(kStreamThreads) forward_stream_kernel(const No
 template <class X, class Y, int V, bool kFull>
 __global__ void __launch_bounds__(kHeldThreads) backward_held_kernel(const NormBwd P, int gw, int deep) {
     using L = Lane<X, V, kFull>;
-    constexpr int N = kHeld / 2, R = rows_at_once<V>();
+    constexpr int N = kHeld / 2, R = kRowsAtOnce<V>;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float part[128 * R];
     __shared__ __align__(8) uint64_t bars[kHeldThreads / 32 * kDeepMost];
@@ -387,28 +434,25 @@ __global__ void __launch_bounds__(kHeldThreads) backward_held_kernel(const NormB
     const int64_t step = (int64_t)gridDim.x * groups, row0 = (int64_t)blockIdx.x * groups + g;
     const L lx{t, gt, P.d};
     // x and dy of a row stand behind each other and share a barrier
-    const uint32_t xb = P.d * (uint32_t)sizeof(X), yb = P.d * (uint32_t)sizeof(Y), pitch = xb + yb;
-    uint8_t *places = smem + (size_t)g * deep * pitch;
-    const uint32_t bar0 = tc::smem_u32(bars + g * deep);
+    const uint32_t xp = ring_pitch(P.d, sizeof(X), V == 8), pitch = xp + ring_pitch(P.d, sizeof(Y), V == 8);
+    const uint32_t bar0 = tc::smem_u32(bars + g * deep), mine = tc::smem_u32(smem) + g * deep * pitch;
+    const Ring<X, V == 8> rx{static_cast<const X *>(P.x.p), P.x.ld, P.d, mine, pitch};
+    const Ring<Y, V == 8> ry{static_cast<const Y *>(P.dy.p), P.dy.ld, P.d, mine + xp, pitch};
     float *w = reinterpret_cast<float *>(smem + (size_t)groups * deep * pitch);
-    const uint32_t w_at = tc::smem_u32(w), places_at = tc::smem_u32(places);
-    const auto x_at = [&](int64_t row) { return static_cast<const X *>(P.x.p) + row * P.x.ld; };
-    const auto y_at = [&](int64_t row) { return static_cast<const Y *>(P.dy.p) + row * P.dy.ld; };
+    const uint32_t w_at = tc::smem_u32(w);
     const auto ask = [&](int64_t row, uint32_t i) {
-        tc::mbar_arrive_expect_tx(bar0 + 8 * i, pitch);
-        tc::bulk_g2s(tc::smem_u32(places + i * pitch), x_at(row), xb, bar0 + 8 * i);
-        tc::bulk_g2s(tc::smem_u32(places + i * pitch + xb), y_at(row), yb, bar0 + 8 * i);
+        tc::mbar_arrive_expect_tx(bar0 + 8 * i, rx.bytes(row) + ry.bytes(row));
+        rx.copy(row, i, bar0 + 8 * i);
+        ry.copy(row, i, bar0 + 8 * i);
     };
-    if constexpr (V == 8) {
-        if (threadIdx.x == 0) gave_up = 0;
-        if (t == 0) {
-            for (int i = 0; i < deep; ++i) tc::mbar_init(bar0 + 8 * i, 1);
-            tc::mbar_init_fence();
-            for (int i = 0; i < deep && row0 + i * step < P.T; ++i) ask(row0 + i * step, i);
-        }
-        stage(w, P.w, P.w_dtype, P.d, 1.f);
-        __syncthreads();
+    if (threadIdx.x == 0) gave_up = 0;
+    if (t == 0) {
+        for (int i = 0; i < deep; ++i) tc::mbar_init(bar0 + 8 * i, 1);
+        tc::mbar_init_fence();
+        for (int i = 0; i < deep && row0 + i * step < P.T; ++i) ask(row0 + i * step, i);
     }
+    stage<V>(w, P.w, P.w_dtype, P.d, 1.f);
+    __syncthreads();
     float2 dw[N], db[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) dw[i] = db[i] = both(0.f);
@@ -430,37 +474,38 @@ __global__ void __launch_bounds__(kHeldThreads) backward_held_kernel(const NormB
         for (int q = 0; q < R; ++q) mu[q] = mu_next[q], r[q] = r_next[q];
         stats(row + R * step);
         const uint32_t first = turn;
-        if constexpr (V == 8) {
 #pragma unroll
-            for (int q = 0; q < R; ++q) {
-                if (row + q * step < P.T) wait_row(bar0 + 8 * turn, phase, &gave_up);
-                if (++turn == (uint32_t)deep) turn = 0, phase ^= 1;
-            }
+        for (int q = 0; q < R; ++q) {
+            if (row + q * step < P.T) wait_row(bar0 + 8 * turn, phase, &gave_up);
+            if (++turn == (uint32_t)deep) turn = 0, phase ^= 1;
         }
-        // x - mu and dy of piece i of row q, from shared memory (V == 1: from memory, eight single values)
+        // x - mu and dy of piece i of row q (V == 1: eight single values), zeros past the rows' ends
         const auto piece = [&](int q, int i, float2(&c)[4], float2(&e)[4]) {
             uint32_t at = first + q;
             if (at >= (uint32_t)deep) at -= deep;
-            const uint32_t p = places_at + at * pitch;
-            Piece<X, 8> u = {};
-            Piece<Y, 8> v = {};
+            const int64_t from = row + q * step;
+            const bool there = from < P.T;
             if constexpr (V == 8) {
-                if (lx.in(i) && row + q * step < P.T) {
-                    u = load_shared<X>(p + lx.column(i) * (uint32_t)sizeof(X));
-                    v = load_shared<Y>(p + xb + lx.column(i) * (uint32_t)sizeof(Y));
+                Piece<X, 8> u = {};
+                Piece<Y, 8> v = {};
+                if (lx.in(i) && there) {
+                    u = load_shared<X>(rx.place(from, at) + lx.column(i) * (uint32_t)sizeof(X));
+                    v = load_shared<Y>(ry.place(from, at) + lx.column(i) * (uint32_t)sizeof(Y));
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    c[k] = add2(widen2(&u.v[2 * k]), both(-mu[q]));
+                    e[k] = widen2(&v.v[2 * k]);
                 }
             } else {
+                const uint32_t px = rx.place(from, at), py = ry.place(from, at);
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (lx.in(8 * i + k)) {
-                        u.v[k] = x_at(row)[lx.column(8 * i + k)];
-                        v.v[k] = y_at(row)[lx.column(8 * i + k)];
-                    }
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                c[k] = add2(widen2(&u.v[2 * k]), both(-mu[q]));
-                e[k] = widen2(&v.v[2 * k]);
+                for (int k = 0; k < 8; ++k) {
+                    const int col = lx.column(8 * i + k);
+                    const bool in = there && lx.in(8 * i + k);
+                    (k & 1 ? c[k / 2].y : c[k / 2].x) = in ? shared_value<X>(px + col * (uint32_t)sizeof(X)) - mu[q] : 0.f;
+                    (k & 1 ? e[k / 2].y : e[k / 2].x) = in ? shared_value<Y>(py + col * (uint32_t)sizeof(Y)) : 0.f;
+                }
             }
         };
         const auto weights = [&](int i, float2(&o)[4]) {
@@ -474,11 +519,8 @@ __global__ void __launch_bounds__(kHeldThreads) backward_held_kernel(const NormB
                 four(w_at, P.d, lx.column(i) + 4, o[2], o[3]);
             } else {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    float one[1] = {0.f};
-                    if (lx.in(8 * i + k)) widen_params<1>(P.w, P.w_dtype, lx.column(8 * i + k), 1.f, one);
-                    (k & 1 ? o[k / 2].y : o[k / 2].x) = one[0];
-                }
+                for (int k = 0; k < 8; ++k)
+                    (k & 1 ? o[k / 2].y : o[k / 2].x) = lx.in(8 * i + k) ? shared_value<float>(w_at + lx.column(8 * i + k) * 4) : 0.f;
             }
         };
         float2 s1[R], s2[R];
@@ -506,10 +548,9 @@ __global__ void __launch_bounds__(kHeldThreads) backward_held_kernel(const NormB
 #pragma unroll
         for (int q = 0; q < R; ++q) s[2 * q] = s1[q].x + s1[q].y, s[2 * q + 1] = s2[q].x + s2[q].y;
         group_sums(s, gw, g, part, slot);
-        if constexpr (V == 8) // the rows before these have been read by all: into their places
-            if (t == 0 && row > row0 && deep >= 2 * R)
-                for (int q = 0; q < R; ++q)
-                    if (row + (q + deep - R) * step < P.T) ask(row + (q + deep - R) * step, (first + deep - R + q) % deep);
+        if (t == 0 && row > row0 && deep >= 2 * R) // the rows before these have been read by all: into their places
+            for (int q = 0; q < R; ++q)
+                if (row + (q + deep - R) * step < P.T) ask(row + (q + deep - R) * step, (first + deep - R + q) % deep);
 #pragma unroll
         for (int i = 0; i < kHeld / 8 && P.dx.p; ++i) {
             float2 wv[4];
@@ -535,7 +576,7 @@ __global__ void __launch_bounds__(kHeldThreads) backward_held_kernel(const NormB
                 }
             }
         }
-        if (V == 8 && deep < 2 * R) { // long rows of 32 bits: no place but these rows' own
+        if (deep < 2 * R) { // long rows of 32 bits: no place but these rows' own
             group_meet(gw, g);
             if (t == 0)
 #pragma unroll
@@ -544,28 +585,23 @@ __global__ void __launch_bounds__(kHeldThreads) backward_held_kernel(const NormB
         }
     }
     if (!P.dw && !P.db) return;
-    // the groups' sums, one behind another (barrier 0 is the first group's own until here)
+    // the groups' sums, added up in their order (barrier 0 is the first group's own until here)
     asm volatile("bar.sync 15;" ::: "memory");
-    float *sum = reinterpret_cast<float *>(smem);
-    for (int j = 0; j < groups; ++j) {
-        if (g == j)
+    float *sum = reinterpret_cast<float *>(smem) + (size_t)g * 2 * P.d, *out = P.parts + (size_t)blockIdx.x * 2 * P.d;
+    if (groups == 1) sum = out;
 #pragma unroll
-            for (int i = 0; i < kHeld; ++i) {
-                const int c = lx.column(i / V) + i % V;
-                if (lx.in(i / V)) {
-                    float &vw = i & 1 ? dw[i / 2].y : dw[i / 2].x, &vb = i & 1 ? db[i / 2].y : db[i / 2].x;
-                    vw += j ? sum[c] : 0.f;
-                    vb += j ? sum[P.d + c] : 0.f;
-                    if (j + 1 < groups) {
-                        sum[c] = vw;
-                        sum[P.d + c] = vb;
-                    } else {
-                        P.parts[(size_t)blockIdx.x * 2 * P.d + c] = vw;
-                        P.parts[((size_t)blockIdx.x * 2 + 1) * P.d + c] = vb;
-                    }
-                }
-            }
-        __syncthreads();
+    for (int i = 0; i < kHeld; ++i) {
+        const int c = lx.column(i / V) + i % V;
+        if (!lx.in(i / V)) continue;
+        sum[c] = i & 1 ? dw[i / 2].y : dw[i / 2].x;
+        sum[P.d + c] = i & 1 ? db[i / 2].y : db[i / 2].x;
+    }
+    if (groups == 1) return;
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * P.d; c += blockDim.x) {
+        float v = 0.f;
+        for (int j = 0; j < groups; ++j) v += reinterpret_cast<const float *>(smem)[(size_t)j * 2 * P.d + c];
+        out[c] = v;
     }
 }
 
@@ -765,18 +801,18 @@ cudaError_t launch_norm_forward(const NormFwd &P, cudaStream_t s) {
         constexpr int V = decltype(v)::value;
         const int pieces = P.d / V + (P.d % V != 0), sms = device_sm_count();
         if (P.d <= kHeldMost) {
-            if constexpr (V == 8) {
-                const int gw = group_warps(pieces, kStreamPieces), groups = kStreamThreads / 32 / gw;
-                const size_t row = sizeof(X) * P.d, rest = (size_t)P.d * 8;
-                if (P.T > kFewRows * sms) {
-                    static SmemAttr attr;
-                    const auto kernel = forward_stream_kernel<X, Y>;
-                    const int deep = rows_ahead(row, rest, groups), smem = (int)(deep * groups * row + rest);
-                    const cudaError_t e = ensure_smem(attr, reinterpret_cast<const void *>(kernel), smem);
-                    if (e != cudaSuccess) return e;
-                    const int blocks = (P.T + groups - 1) / groups;
-                    return launch_behind(kernel, dim3(blocks < sms ? blocks : sms), dim3(groups * gw * 32), smem, s, P, gw, deep);
-                }
+            if (P.T > kFewRows * sms) {
+                static SmemAttr attr;
+                const auto kernel = forward_stream_kernel<X, Y, V>;
+                const int gw = group_warps(pieces, kStreamHeld<V> / V);
+                int groups = kStreamThreads<V> / 32 / gw;
+                if (groups > 16 && gw > 1) groups = 16; // barriers
+                const size_t row = ring_pitch(P.d, sizeof(X), V == 8), rest = (size_t)P.d * 8;
+                const int deep = rows_ahead(row, rest, groups), smem = (int)(deep * groups * row + rest);
+                const cudaError_t e = ensure_smem(attr, reinterpret_cast<const void *>(kernel), smem);
+                if (e != cudaSuccess) return e;
+                const int blocks = (P.T + groups - 1) / groups;
+                return launch_behind(kernel, dim3(blocks < sms ? blocks : sms), dim3(groups * gw * 32), smem, s, P, gw, deep);
             }
             const int gw = group_warps(pieces, kHeld / V), most = kHeldThreads / 32 / gw;
             int groups = (P.T + sms - 1) / sms; // as many CTAs as there are SMs before several groups a CTA
@@ -808,9 +844,9 @@ cudaError_t launch_norm_backward(const NormBwd &P, cudaStream_t s) {
                 constexpr bool kFull = decltype(full)::value;
                 static SmemAttr attr;
                 const auto kernel = backward_held_kernel<X, Y, V, kFull>;
-                const size_t row = (sizeof(X) + sizeof(Y)) * P.d, rest = (size_t)P.d * 4;
-                const int deep = V == 8 ? rows_ahead(row, rest, groups) : 2, last = groups > 1 ? P.d * 8 : 0;
-                const int ring = V == 8 ? (int)(deep * groups * row + rest) : 0, smem = ring > last ? ring : last;
+                const size_t row = ring_pitch(P.d, sizeof(X), V == 8) + ring_pitch(P.d, sizeof(Y), V == 8), rest = (size_t)P.d * 4;
+                const int deep = rows_ahead(row, rest, groups), last = groups > 1 ? groups * P.d * 8 : 0;
+                const int ring = (int)(deep * groups * row + rest), smem = ring > last ? ring : last;
                 const cudaError_t f = ensure_smem(attr, reinterpret_cast<const void *>(kernel), smem);
                 return f == cudaSuccess ? launch_behind(kernel, dim3(blocks), dim3(threads), smem, s, P, gw, deep) : f;
             };
