@@ -19,6 +19,8 @@
 //   fetch(out, spot, n, held), turn(out, shared, held, in), tile(out, spot, n, v, in): the sums v of 32 rows and 32 columns
 //                from n on (lane = row, all lanes together), with what the epilogue reads besides: asked for ahead of
 //                the sums (held), then brought to the lanes' rows (in)
+// What bounds it: a pair's 256 x 256 tile brings 32 KB a piece of k into each SM for 512 cycles of MMAs, about what an SM
+// takes in (100 B/ns), so an epilogue that reads costs nearly its share of bytes; long runs are at the power limit.
 // Waits are bounded, as dense_gemm.cuh's.
 #pragma once
 

@@ -105,13 +105,20 @@ int check_ortho(const waste_ortho_config *c) {
     if (m > 1 << 15) return fail(WASTE_EINVAL, "rows = %d, cols = %d: the shorter side at most 2^15", c->rows, c->cols);
     if ((int64_t)c->count * c->rows > kMostRows) return fail(WASTE_EINVAL, "count = %d, rows = %d: %d rows at most", c->count, c->rows, kMostRows);
     if (c->steps < 1 || c->steps > 32) return fail(WASTE_EINVAL, "steps = %d outside [1, 32]", c->steps);
-    double s = 1.;
+    // singular values s <= most: A's are s^2, B's b s^2 + c s^4, and their entries no larger; 2^10 times them are fp16
+    constexpr double kRange = 62.;
+    double most = 1.;
     for (int i = 0; i < c->steps; ++i) {
-        s = largest(c, s < 1. ? 1. : s); // also for singular values that stay where they are
-        if (!(s <= 8.)) // NaN too
-            return fail(WASTE_EINVAL, "coefficients %g, %g, %g take singular values past 8 in %d steps", (double)c->a, (double)c->b,
-                        (double)c->c, i + 1);
+        const auto q = [&](double t) { return std::fabs(t * (c->b + t * c->c)); };
+        const double top = most * most, bend = c->c != 0.f ? -c->b / (2. * c->c) : 0.;
+        double b = q(top);
+        if (bend > 0. && bend < top) b = std::fmax(b, q(bend));
+        if (!(top <= kRange) || !(b <= kRange)) // NaN too
+            return fail(WASTE_EINVAL, "coefficients %g, %g, %g leave the range of step %d", (double)c->a, (double)c->b, (double)c->c, i + 1);
+        most = std::fmax(1., largest(c, most)); // 1: singular values that stay where they are
     }
+    if (!(most <= kRange))
+        return fail(WASTE_EINVAL, "coefficients %g, %g, %g leave the range of the last step", (double)c->a, (double)c->b, (double)c->c);
     return WASTE_OK;
 }
 
