@@ -31,7 +31,6 @@ namespace wm {
 namespace train {
 
 using dense::all;
-using dense::kBarBytes;
 using dense::kBM;
 using dense::kMaxStages;
 using dense::kPieceBytes;
@@ -40,6 +39,7 @@ using dense::kSmemBudget;
 using dense::kTmemCols;
 using dense::Out32;
 constexpr int kTileThreads = dense::kThreads;
+constexpr uint32_t kTileBars = 320; // bytes of barriers
 
 struct Spot {
     int am, az, bm, bz; // A's and B's first row (m, n) and matrix
@@ -208,12 +208,12 @@ template <int kCG, class J>
 __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_constant__ TileArgs P, const __grid_constant__ J job) {
     extern __shared__ __align__(1024) uint8_t smem_raw[]; // stages, pieces on their way out, the job's, barriers
     const uint32_t base = tc::smem_u32(smem_raw);
-    const uint32_t bars_at = P.smem - kBarBytes;
+    const uint32_t bars_at = P.smem - kTileBars;
     const uint32_t bars = base + bars_at;
     const uint32_t bar_full = bars, bar_empty = bars + 64, bar_accf = bars + 128, bar_acce = bars + 144;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem_raw + bars_at + 160);
     volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem_raw + bars_at + 164);
-    const uint32_t drain = bars + 168, bar_mask = bars + 176;
+    const uint32_t drain = bars + 168, bar_mask = bars + 176, bar_land = bars + 240;
 
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int BN = P.BN;
@@ -228,7 +228,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
         for (int i = 0; i < P.stages; ++i) {
             tc::mbar_init(bar_full + 8 * i, 1);
             tc::mbar_init(bar_empty + 8 * i, 1);
-            tc::mbar_init(bar_mask + 8 * i, 1); // one a stage: the other CTA may be further along than this one
+            tc::mbar_init(bar_mask + 8 * i, kCG); // one a stage: who clears may be further along than the issuer
+            tc::mbar_init(bar_land + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(bar_accf + 8 * i, 1);
@@ -258,7 +259,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
     if (warp == 0) {
         // ---- loader (the warp walks the loop, an elected lane issues)
         int st = 0, issued = 0;
-        uint32_t ph = 0;
+        uint32_t ph = 0, land = 0, there = 0; // a bit a stage: uses of bar_land so far, whether the last load was one
         bool ok = true;
         const uint32_t full0 = kCG == 2 ? tc::map_rank(bar_full, 0) : bar_full;
         for (int t = tile0; t < tiles && ok; t += step) {
@@ -271,11 +272,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
                 }
                 if (tc::elect_one()) {
                     const uint32_t sa = base + st * stage_bytes, sb = sa + a_bytes;
-                    // a piece to be masked counts on each CTA's own barrier
-                    const bool own = kCG == 1 || (J::kMask && kb + 1 == T.pieces && T.left < 64);
-                    const uint32_t full = own ? bar_full + 8 * st : full0 + 8 * st;
+                    // a piece to be masked counts on a barrier of its own in each CTA, for the warp that clears
+                    const bool own = J::kMask && kb + 1 == T.pieces && T.left < 64;
+                    const uint32_t full = own ? bar_land + 8 * st : full0 + 8 * st;
                     const uint32_t bytes = J::kRagged ? (uint32_t)(T.high + T.cols / kCG) * kRowBytes : a_bytes + b_bytes;
-                    if (leads || own) tc::mbar_arrive_expect_tx(bar_full + 8 * st, (own ? 1 : kCG) * bytes);
+                    if (own) {
+                        tc::mbar_arrive_expect_tx(bar_land + 8 * st, bytes);
+                        if (leads) tc::mbar_arrive(bar_full + 8 * st);
+                    } else if (leads) {
+                        tc::mbar_arrive_expect_tx(bar_full + 8 * st, kCG * bytes);
+                    }
                     const auto load = [&](uint32_t dst, const CUtensorMap *m, int x, int y, int z) {
                         if (kCG == 2 && !(J::kMask && own))
                             tma_load3_pair(dst, m, x, y, z, full);
@@ -303,6 +309,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
                     }
                 }
                 __syncwarp();
+                if (J::kMask) {
+                    const uint32_t own = kb + 1 == T.pieces && T.left < 64;
+                    land ^= own << st;
+                    there = (there & ~(1u << st)) | own << st;
+                }
                 ++issued;
                 if (++st == P.stages) {
                     st = 0;
@@ -317,6 +328,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
                 const int j = issued - n + i;
                 tc::mbar_wait(bar_full + 8 * (j % P.stages), (j / P.stages) & 1);
             }
+            for (int i = 0; J::kMask && i < P.stages; ++i)
+                if (there >> i & 1) tc::mbar_wait(bar_land + 8 * i, (land >> i & 1) ^ 1);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -355,15 +368,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
                     int steps = 4;
                     if (J::kMask && kb + 1 == T.pieces && T.left < 64) {
                         steps = (T.left + 15) >> 4;
-                        mask_rows(smem_raw + st * stage_bytes, T.left, 16 * steps, (int)((a_bytes + b_bytes) >> 13), lane);
-                        if (kCG == 2) { // and the other CTA its own
-                            if (!all(wait_cluster(bar_mask + 8 * st, masked >> st & 1))) {
-                                ok = false;
-                                break;
-                            }
-                            masked ^= 1u << st;
-                            tc::fence_after_sync();
+                        if (!all(wait_cluster(bar_mask + 8 * st, masked >> st & 1))) { // cleared, in both CTAs
+                            ok = false;
+                            break;
                         }
+                        masked ^= 1u << st;
+                        tc::fence_after_sync();
                     }
                     if (tc::elect_one()) {
 #pragma unroll
@@ -391,23 +401,32 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
                 if (tc::elect_one()) commit(drain);
                 tc::mbar_wait(drain, 0);
             }
-        } else if (J::kMask) {
-            // ---- the pair's other CTA clears what is not the tile's in its own shared memory, and says so
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        if (J::kMask) {
+            // ---- clears what is not the tile's in this CTA's part of a stage as soon as it is there, often ahead of the MMAs
+            // before it, and says so to the issuer
             int st = 0;
-            uint32_t used = 0; // a bit a stage: its own barrier's parity
+            uint32_t used = 0; // a bit a stage: the parity of the barrier that it lands on
             for (int t = tile0; t < tiles; t += step) {
                 const Spot T = job.spot(mine, t);
                 if (T.pieces == 0) continue;
                 const int last = (st + T.pieces - 1) % P.stages;
                 st = (st + T.pieces) % P.stages;
                 if (T.left == 64) continue;
-                if (!all(tc::mbar_wait(bar_full + 8 * last, used >> last & 1))) {
+                if (!all(tc::mbar_wait(bar_land + 8 * last, used >> last & 1))) {
                     if (lane == 0) *abort_flag = 1;
                     break;
                 }
                 used ^= 1u << last;
                 mask_rows(smem_raw + last * stage_bytes, T.left, (T.left + 15) & ~15, (int)((a_bytes + b_bytes) >> 13), lane);
-                if (lane == 0) tc::mbar_arrive_cluster(tc::map_rank(bar_mask + 8 * last, 0));
+                if (lane == 0) {
+                    if (leads)
+                        tc::mbar_arrive(bar_mask + 8 * last);
+                    else
+                        tc::mbar_arrive_cluster(tc::map_rank(bar_mask + 8 * last, 0));
+                }
             }
         }
         __syncwarp();
@@ -531,10 +550,10 @@ cudaError_t launch_tiles_as(TileArgs &P, const J &job, bool bf16, size_t job_byt
     const auto kernel = tile_kernel<kCG, J>;
     const uint32_t stage = tile_stage(P.BN, kCG, J::kBmn), turn = kTurnBytes<J>;
     P.job_bytes = (uint32_t)round_up(job_bytes, 16);
-    P.stages = (int)((kSmemBudget - kBarBytes - turn - P.job_bytes) / stage);
+    P.stages = (int)((kSmemBudget - kTileBars - turn - P.job_bytes) / stage);
     if (P.stages > kMaxStages) P.stages = kMaxStages;
     if (P.stages < 2) return cudaErrorInvalidValue;
-    P.smem = P.stages * stage + turn + P.job_bytes + kBarBytes;
+    P.smem = P.stages * stage + turn + P.job_bytes + kTileBars;
     P.idesc = tc::idesc_half(kBM * kCG, P.BN, bf16, J::kAmn, J::kBmn);
     cudaError_t e = ensure_smem(attr, reinterpret_cast<const void *>(kernel), (int)P.smem);
     if (e != cudaSuccess) return e;

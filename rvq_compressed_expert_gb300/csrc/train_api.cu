@@ -105,6 +105,8 @@ int check_ortho(const waste_ortho_config *c) {
     if (m > 1 << 15) return fail(WASTE_EINVAL, "rows = %d, cols = %d: the shorter side at most 2^15", c->rows, c->cols);
     if ((int64_t)c->count * c->rows > kMostRows) return fail(WASTE_EINVAL, "count = %d, rows = %d: %d rows at most", c->count, c->rows, kMostRows);
     if (c->steps < 1 || c->steps > 32) return fail(WASTE_EINVAL, "steps = %d outside [1, 32]", c->steps);
+    if (!std::isfinite(c->a) || !std::isfinite(c->b) || !std::isfinite(c->c))
+        return fail(WASTE_EINVAL, "coefficients %g, %g, %g", (double)c->a, (double)c->b, (double)c->c);
     // singular values s <= most: A's are s^2, B's b s^2 + c s^4, and their entries no larger; 2^10 times them are fp16
     constexpr double kRange = 62.;
     double most = 1.;

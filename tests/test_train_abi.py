@@ -186,7 +186,7 @@ def update(c=None, ws=Bytes(1 << 30, A + (1 << 32)), **k):
                                ortho(count=60000, rows=30000, cols=2), ortho(steps=0), ortho(steps=33), ortho(abi=3),
                                ortho(abc=(9.0, 0.0, 0.0)), ortho(abc=(3.4445, 4.775, 2.0315)), ortho(abc=(float("nan"), 0.0, 0.0)),
                                ortho(abc=(2.0, 0.0, 0.0)), ortho(abc=(1.0, float("inf"), 1.0)), ortho(abc=(7.9, 0.0, 0.0), steps=2),
-                               ortho(abc=(1.0, -300.0, 299.0))])
+                               ortho(abc=(1.0, -9.0, 50.0))])
 def test_ortho_bad_config(c):
     refused(B.waste_ortho_workspace, c)
     refused(update, c)

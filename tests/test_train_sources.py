@@ -35,7 +35,7 @@ def test_kernels_wait_and_release_once():
             assert "return" not in before.split("{", 1)[1] and "tma_load" not in before and "P.x" not in before
             line = [l for l in kernel.split("\n") if "grid_wait_release" in l][0]
             assert line == "    tc::grid_wait_release();", (path, line)  # the kernel's own level: under no condition
-    assert kernels == 11
+    assert kernels == 12
     launches = sum(len(re.findall(r"<<<", code(p))) for p in FILES)
     assert launches == 0  # all by launches that may overlap
 
