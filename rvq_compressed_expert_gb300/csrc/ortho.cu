@@ -225,6 +225,25 @@ template <bool kMn> struct GramJob {
         dense::put32_as(WASTE_ACT_F32, o, &to, out, side, n, side, true, false, v);
     }
 };
+// A = X X^T (kMn: X^T X) at once.
+template <bool kMn> struct WholeGramJob {
+    static constexpr bool kAmn = kMn, kBmn = kMn, kMask = false, kReads = false, kTwoPieces = true, kRagged = false;
+    CUtensorMap ta, tb, to;
+    Stack s;
+    void *a;
+    int ldm;
+    __device__ void begin(uint8_t *) const {}
+    __device__ __forceinline__ int tiles(const uint8_t *) const { return s.tiles(); }
+    __device__ __forceinline__ Spot spot(const uint8_t *, int t) const { return s.spot(t); }
+    using Held = Nothing;
+    using In = Nothing;
+    __device__ __forceinline__ void tile(Out32 &o, const Spot &, int n, const float (&v)[32], const In &) const {
+        float x[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = v[i] * kDown;
+        put_halves(o, &to, a, ldm, n, x);
+    }
+};
 // A from its partial sums, both halves: a CTA takes 64 x 64 values of a tile.
 __global__ void __launch_bounds__(kFlat) gram_kernel(const float *parts, int side, int tri, int slices, int m, int ldm, __half *a) {
     __shared__ __half turn[64][66];
@@ -646,7 +665,9 @@ template <bool kTall, bool kAdd> cudaError_t steps(const Ortho &P, const OrthoPa
     const size_t xs = (size_t)P.rows * W.ldx, ss = (size_t)m * W.ldm;
     const int pieces = (m + 63) / 64;
     const Shape qs = shape(P.count, m, m, pieces, false, 2, sms), xx = shape(P.count, P.rows, P.cols, pieces, !kTall, 4, sms);
-    const int gcg = W.side == 256 ? 2 : 1;
+    const int gcg = W.side == 256 ? 2 : 1, long_pieces = (n + 63) / 64;
+    const bool whole = W.slices == 0;
+    const Shape gs = whole ? shape(P.count, m, m, long_pieces, kTall, 0, sms) : Shape{gcg, W.side};
     cudaError_t e = cudaSuccess;
     const auto x_map = [&](CUtensorMap *t, int i, int box) {
         if (e == cudaSuccess) e = stack_map(t, hi[i], P.cols, P.rows, P.count, W.ldx, xs, box);
@@ -664,7 +685,11 @@ template <bool kTall, bool kAdd> cudaError_t steps(const Ortho &P, const OrthoPa
     G.out = parts;
     G.side = W.side, G.tri = W.tri, G.slices = W.slices, G.count = P.count, G.pieces = (n + 63) / 64;
     const long long items = (long long)P.count * W.tri * W.slices;
-    o_map(&G.to, parts, 4, (int)(items * W.side), W.side);
+    if (!whole) o_map(&G.to, parts, 4, (int)(items * W.side), W.side);
+    WholeGramJob<kTall> D = {};
+    D.s.set(gs.cg, gs.BN, P.count, m, m, n);
+    o_map(&D.to, A, 2, P.count * m, W.ldm);
+    D.a = A, D.ldm = W.ldm;
     Q.s.set(qs.cg, qs.BN, P.count, m, m, m);
     s_map(&Q.ta, A, kBM);
     s_map(&Q.tb, A, qs.BN / qs.cg);
@@ -678,16 +703,16 @@ template <bool kTall, bool kAdd> cudaError_t steps(const Ortho &P, const OrthoPa
     CUtensorMap ga[2], gb[2], sx[2], st[2];
     for (int i = 0; i < 2; ++i) {
         x_map(&ga[i], i, kTall ? 64 : kBM);
-        x_map(&gb[i], i, kTall ? 64 : W.side / gcg);
+        x_map(&gb[i], i, kTall ? 64 : gs.BN / gs.cg);
         x_map(&sx[i], i, kTall ? kBM : 64);
         o_map(&st[i], hi[i], 2, P.count * P.rows, W.ldx);
     }
     const int per = W.side / 64;
     for (int i = 0; i < P.steps && e == cudaSuccess; ++i) {
         const int from = i & 1;
-        G.ta = ga[from], G.tb = gb[from];
-        e = launch(gcg, W.side, G, items, sms, s);
-        if (e == cudaSuccess)
+        G.ta = D.ta = ga[from], G.tb = D.tb = gb[from];
+        e = whole ? launch(gs.cg, gs.BN, D, (long long)P.count * D.s.tm * D.s.tn, sms, s) : launch(gcg, W.side, G, items, sms, s);
+        if (e == cudaSuccess && !whole)
             e = launch_behind(gram_kernel, dim3(W.tri * per * per, P.count), dim3(kFlat), 0, s, parts, W.side, W.tri, W.slices, m, W.ldm,
                               reinterpret_cast<__half *>(A));
         if (e == cudaSuccess) e = launch(qs.cg, qs.BN, Q, (long long)P.count * Q.s.tm * Q.s.tn, sms, s);

@@ -62,17 +62,19 @@ struct OrthoParts {
     int ldx, ldm;
     int side, tri, slices; // of A: tiles of side x side, those on and below its diagonal, in so many shares of k
 };
-// A is made in tiles of 256 x 256 by pairs of CTAs (of 128 x 128 by one where it is no larger), on and below its
-// diagonal, the long side split into shares: as many as shorten the waves of tiles (a piece of k takes about
-// 370 ns) by more than their fp32 partial sums, written and read again, cost.  The workspace has to have one size
-// everywhere, so this counts with the SMs of the one device the library is for.
-inline int gram_slices(long long tiles, int pieces, int side) {
+// A is made in tiles of 256 x 256 by pairs of CTAs (of 128 x 128 by one where it is no larger).  Either those on and below its
+// diagonal, the long side split into shares: as many as shorten the waves of tiles (a piece of k takes about 370 ns, 410 in those) by
+// more than their fp32 partial sums, written and read again, cost; these are added up by a launch of their own, about 6
+// us.  Or, where that costs more than it saves (0 shares), all of its tiles at once.  The workspace has to have one
+// size everywhere, so this counts with the SMs of the one device the library is for.
+inline int gram_slices(int count, int across, int pieces, int side) {
     const int slots = side == 256 ? 76 : 152;
-    int best = 1;
-    double least = 1e30;
+    const long long tiles = (long long)count * across * (across + 1) / 2, all = (long long)count * across * across;
+    int best = 0;
+    double least = (double)((all + slots - 1) / slots) * pieces * 410.;
     for (int s = 1; s <= 16 && s <= pieces; ++s) {
         const double waves = (double)((tiles * s + slots - 1) / slots);
-        const double t = waves * ((pieces + s - 1) / s) * 370. + (double)(tiles * s) * side * side * 8. / 5000.;
+        const double t = waves * ((pieces + s - 1) / s) * 370. + (double)(tiles * s) * side * side * 8. / 5000. + 6000.;
         if (t < least) least = t, best = s;
     }
     return best;
@@ -83,7 +85,7 @@ inline OrthoParts ortho_parts(int count, int rows, int cols) {
     p.side = m > 128 ? 256 : 128;
     const int across = (m + p.side - 1) / p.side;
     p.tri = across * (across + 1) / 2;
-    p.slices = gram_slices((long long)count * p.tri, (n + 63) / 64, p.side);
+    p.slices = gram_slices(count, across, (n + 63) / 64, p.side);
     p.ldx = (cols + 7) / 8 * 8;
     p.ldm = (m + 7) / 8 * 8;
     size_t at = 0;
