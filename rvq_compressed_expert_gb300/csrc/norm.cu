@@ -284,6 +284,12 @@ __device__ __forceinline__ void wait_row(uint32_t bar, uint32_t parity, volatile
     }
 }
 
+// Behind a wait that gave up: time for copies on their way to land before the CTA goes.
+__device__ __forceinline__ void settle(volatile uint32_t *gave_up) {
+    if (*gave_up)
+        for (int i = 0; i < 64; ++i) __nanosleep(1 << 14);
+}
+
 // Few rows: a row a group, straight from memory, w and b held too, for all loads to be on their way at once.
 template <class X, class Y, int V>
 __global__ void __launch_bounds__(kHeldThreads) forward_few_kernel(const NormFwd P, int gw) {
@@ -428,6 +434,7 @@ __global__ void __launch_bounds__(kStreamThreads<V>) forward_stream_kernel(const
                 }
             }
     }
+    settle(&gave_up);
 }
 
 // dx, and a CTA's share of dw and db, in one pass.
@@ -595,6 +602,7 @@ __global__ void __launch_bounds__(kHeldThreads) backward_held_kernel(const NormB
                     if (row + (q + deep) * step < P.T) ask(row + (q + deep) * step, (first + q) % deep);
         }
     }
+    settle(&gave_up);
     if (!P.dw && !P.db) return;
     // the groups' sums, added up in their order (barrier 0 is the first group's own until here)
     asm volatile("bar.sync 15;" ::: "memory");
