@@ -3,13 +3,17 @@
 // Both are one pass over the rows, whose floor is memory: 16384 x 7168 bf16 is 470 MB forward and 705 MB backward, 70 and
 // 104 us at the 6.75 TB/s of a plain copy.  The mean comes first and the squares are taken about it (two sums over
 // the row as it is held, no cancellation).
-//   forward_stream_kernel  many rows: 92 us = 5.1 TB/s (rows of 7167 values, which begin anywhere: 215 us)
+//   forward_stream_kernel  many rows: 92 us = 5.1 TB/s (rows of 7167 values, which begin anywhere: 124 us)
 //   forward_few_kernel     up to 4 rows an SM: one row 3 us and the launch
-//   backward_held_kernel   142 us = 5.0 TB/s (rows of 7167: 460 us), with the partial sums of dw and db; reduce_kernel
+//   backward_held_kernel   140 us = 5.0 TB/s (rows of 7167: 270 us; fp32 233 and 282, floor 209), with the partial sums of dw and db; reduce_kernel
 //                          adds those up: one row of them a CTA, 152 at most
 //   forward_kernel, dx_kernel, columns_kernel  rows past 8192 values: read two or three times, from L2 as far as it holds
 // What bounds the forward is the chain of steps of a row (wait, sum, squares, write) on the warps an SM holds; the backward's
-// lanes also hold the sums of their columns, so a row takes 14 of its 16 warps, and two rows are in work at once.
+// lanes also hold the sums of their columns, so a row takes 14 of its 16 warps, and two rows are in work at once (of 16 bits;
+// of fp32, two in work leave too few on their way: 292 us against 233).
+// Rows that begin anywhere: results go out in whole 16-byte pieces, and what does not lie in the same pieces is moved by
+// words and half words in registers (single values through shared memory: 215 and 460 us).  The sums of dw and db are tied
+// to columns, so the backward moves both operands there: that is what it costs.
 // Spilled registers cost more than elsewhere: the rows on their way leave the L1 cache 28 KB, and what does not fit
 // there goes to L2 (1024 threads with 52 bytes spilled 110 us, 896 with 24 bytes 98, 768 with none 92).
 #include <type_traits>
@@ -104,7 +108,8 @@ template <int n> __device__ __forceinline__ void group_sums(float (&v)[n], int g
 // each, some ahead; values are computed in pairs (one instruction for both); w and b stand in shared memory in fp32.
 // kHeld: values a lane where a row is spread over up to 16 warps.
 constexpr int kHeld = 16;
-template <int V> constexpr int kRowsAtOnce = V == 8 ? 2 : 1; // of a group in the backward
+// Rows of a group in work at once in the backward: two of 16 bits, where two more fit on their way behind them.
+template <class X, class Y, int V> constexpr int kRowsAtOnce = V == 8 && sizeof(X) + sizeof(Y) == 4 ? 2 : 1;
 constexpr int kHeldThreads = 512;
 constexpr int kHeldMost = kHeld * kHeldThreads;
 constexpr int kHeldSmem = 220 << 10;
@@ -213,33 +218,48 @@ template <class X, int V, bool kFull> struct Lane {
     __device__ __forceinline__ bool first(int j) const { return in(2 * j / V); }
     __device__ __forceinline__ bool second(int j) const { return in((2 * j + 1) / V); }
 };
-// w or b, in fp32, into shared memory, by all threads.  V == 8: of every eight the first four in one half and the last
-// four in the other, so that the lanes of a warp, eight columns apart, read neighbouring 16 bytes.
-template <int V> __device__ __forceinline__ void stage(float *to, const void *p, int dtype, int d, float none) {
+// Values of w (and b) in shared memory, in fp32, filled by all threads.
+// Whole rows: of every eight the first four in one half and the last four in the other, so that the lanes of a
+// warp, eight columns apart, read neighbouring 16 bytes.
+__device__ __forceinline__ void stage(float *to, const void *p, int dtype, int d, float none) {
     for (int i = threadIdx.x; i < d; i += blockDim.x) {
         float v[1];
         widen_params<1>(p, dtype, i, none, v);
-        to[V == 8 ? (i & 4 ? d / 2 : 0) + (i >> 3) * 4 + (i & 3) : i] = v[0];
+        to[(i & 4 ? d / 2 : 0) + (i >> 3) * 4 + (i & 3)] = v[0];
     }
 }
+// Any rows: columns of the same remainder by eight stand together, so that lanes eight columns apart read neighbours
+// wherever they begin, -7 to d + 7 (zeros past d); n of them beside each other (w alone; w and b).
+__host__ __device__ constexpr int eighths(int d) { return (d + 15) / 8; }
+template <int n> __device__ __forceinline__ void stage_any(float *to, const void *w, const void *b, int dtype, int d) {
+    for (int i = threadIdx.x; i < 8 * eighths(d); i += blockDim.x) {
+        float v[1] = {0.f}, u[1] = {0.f};
+        if (i < d) {
+            widen_params<1>(w, dtype, i, 1.f, v);
+            if (n == 2) widen_params<1>(b, dtype, i, 0.f, u);
+        }
+        const int at = n * ((i & 7) * eighths(d) + (i >> 3));
+        to[at] = v[0];
+        if (n == 2) to[at + 1] = u[0];
+    }
+}
+// Byte of column c there.
+template <int n> __device__ __forceinline__ uint32_t place_any(int d, int c) { return 4 * n * ((c & 7) * eighths(d) + (c >> 3)); }
 // A piece in shared memory, said to be there (an address that the compiler has lost track of goes the long way).
 __device__ __forceinline__ uint4 shared16(uint32_t at) {
     uint4 u;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(at) : "memory");
     return u;
 }
-template <class X> __device__ __forceinline__ float shared_value(uint32_t at) {
-    if constexpr (sizeof(X) == 4) {
-        float v;
-        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-        return v;
-    } else {
-        uint16_t u;
-        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(u) : "r"(at) : "memory");
-        X x;
-        *reinterpret_cast<uint16_t *>(&x) = u;
-        return widen(x);
-    }
+__device__ __forceinline__ float shared_float(uint32_t at) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ float2 shared_float2(uint32_t at) {
+    float2 v;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+    return v;
 }
 template <class X> __device__ __forceinline__ Piece<X, 8> load_shared(uint32_t at) {
     Piece<X, 8> q;
@@ -248,12 +268,57 @@ template <class X> __device__ __forceinline__ Piece<X, 8> load_shared(uint32_t a
     return q;
 }
 
+// Eight values that begin anywhere: the 16-byte pieces around them, moved by words and by half a word.  Reads up to 14
+// bytes before and 30 behind what is asked for.
+template <class X> __device__ __forceinline__ Piece<X, 8> load_any(uint32_t at) {
+    constexpr int W = 2 * sizeof(X); // words
+    if ((at & 15) == 0) return load_shared<X>(at);
+    Piece<X, 8> q;
+    uint32_t u[W + 4], v[W + 2], w[W + 1];
+#pragma unroll
+    for (int i = 0; i < W + 4; i += 4) {
+        const uint4 s = shared16((at & ~15u) + 4 * i);
+        u[i] = s.x, u[i + 1] = s.y, u[i + 2] = s.z, u[i + 3] = s.w;
+    }
+#pragma unroll
+    for (int i = 0; i < W + 2; ++i) v[i] = at & 8 ? u[i + 2] : u[i];
+#pragma unroll
+    for (int i = 0; i < W + 1; ++i) w[i] = at & 4 ? v[i + 1] : v[i];
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+        reinterpret_cast<uint32_t *>(&q)[i] = sizeof(X) == 2 ? __funnelshift_r(w[i], w[i + 1], (at & 2) * 8) : w[i];
+    return q;
+}
+// Zeros in those of eight values from column c on that are not the row's.
+__device__ __forceinline__ void trim(float2 *x, int c, int d) {
+    if (c >= 0 && c + 8 <= d) return;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if (c + 2 * k < 0 || c + 2 * k >= d) x[k].x = 0.f;
+        if (c + 2 * k + 1 < 0 || c + 2 * k + 1 >= d) x[k].y = 0.f;
+    }
+}
+// Eight results to column c on, of which those outside the row are left out; the first on 16 bytes.
+template <class Y> __device__ __forceinline__ void give_any(Y *row, int c, int d, const Piece<Y, 8> &o) {
+    if (c >= 0 && c + 8 <= d) {
+        *reinterpret_cast<Piece<Y, 8> *>(row + c) = o;
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (c + k >= 0 && c + k < d) row[c + k] = o.v[k];
+    }
+}
+// Values between a 16-byte boundary and p.
+template <class Y> __device__ __forceinline__ int before16(const Y *p) { return (int)(((uintptr_t)p & 15) / sizeof(Y)); }
+
 // Four of them from column c on (a multiple of 4).
 __device__ __forceinline__ void four(uint32_t p, int d, int c, float2 &a, float2 &b) {
     const uint4 q = shared16(p + ((c & 4 ? d / 2 : 0) + (c >> 3) * 4) * 4);
     a = make_float2(__uint_as_float(q.x), __uint_as_float(q.y)), b = make_float2(__uint_as_float(q.z), __uint_as_float(q.w));
 }
 
+// Beside rows that begin anywhere there is room for what load_any reads around them, from column -7 to d + 7.
+constexpr uint32_t kRingFront = 32, kRingBack = 64; // the shift, and 48
 // The rows of one operand on their way to a group of warps: places in shared memory, filled in order by bulk
 // copies of one thread.  A place is free again once the group has met (in a sum) behind its reading.  Copies take whole
 // 16-byte pieces: of a row that begins or ends inside one, its neighbours in that piece come too (nothing lies
@@ -263,17 +328,18 @@ template <class X, bool kWhole> struct Ring {
     int64_t ld;
     int d;
     uint32_t at, pitch; // this group's places
+    enum { kFront = kWhole ? 0 : kRingFront };
     __device__ __forceinline__ const X *row_at(int64_t row) const { return p + row * ld; }
     // bytes between the place's start and the row's
     __device__ __forceinline__ uint32_t shift(int64_t row) const { return kWhole ? 0 : (uint32_t)(uintptr_t)row_at(row) & 15u; }
     __device__ __forceinline__ uint32_t bytes(int64_t row) const { return (shift(row) + d * (uint32_t)sizeof(X) + 15) & ~15u; }
-    __device__ __forceinline__ uint32_t place(int64_t row, uint32_t i) const { return at + i * pitch + shift(row); }
+    __device__ __forceinline__ uint32_t place(int64_t row, uint32_t i) const { return at + i * pitch + kFront + shift(row); }
     __device__ __forceinline__ void copy(int64_t row, uint32_t i, uint32_t bar) const {
-        tc::bulk_g2s(at + i * pitch, reinterpret_cast<const uint8_t *>(row_at(row)) - shift(row), bytes(row), bar);
+        tc::bulk_g2s(at + i * pitch + kFront, reinterpret_cast<const uint8_t *>(row_at(row)) - shift(row), bytes(row), bar);
     }
 };
 __host__ __device__ constexpr uint32_t ring_pitch(int d, uint32_t size, bool whole) {
-    return (d * size + 15) / 16 * 16 + (whole ? 0 : 16);
+    return (d * size + 15) / 16 * 16 + (whole ? 0 : kRingFront + kRingBack);
 }
 // A wait gives up after 1.1 s: then none is waited for any more, and waste_dense_status reports it.
 __device__ __forceinline__ void wait_row(uint32_t bar, uint32_t parity, volatile uint32_t *gave_up) {
@@ -331,15 +397,14 @@ __global__ void __launch_bounds__(kHeldThreads) forward_few_kernel(const NormFwd
 
 // Many rows: kStreamHeld values a lane, so that a row takes eight warps at most and an SM works on four rows or more at
 // once, each group at a step of its own.
-// (Single values: 16 a lane and more threads, as their addresses take registers too.)
-template <int V> constexpr int kStreamHeld = V == 8 ? 32 : 16;
-template <int V> constexpr int kStreamThreads = V == 8 ? 768 : 896;
+// Rows that begin anywhere (V = 1): a lane's eight columns are those of a whole 16-byte piece of y.
+constexpr int kStreamHeld = 32, kStreamThreads = 768;
 template <class X, class Y, int V>
-__global__ void __launch_bounds__(kStreamThreads<V>) forward_stream_kernel(const NormFwd P, int gw, int deep) {
-    constexpr int kPieces = kStreamHeld<V> / V, kSize = sizeof(X);
+__global__ void __launch_bounds__(kStreamThreads) forward_stream_kernel(const NormFwd P, int gw, int deep) {
+    constexpr int kPieces = kStreamHeld / 8, kSize = sizeof(X);
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float part[64];
-    __shared__ __align__(8) uint64_t bars[kStreamThreads<V> / 32 * kDeepMost];
+    __shared__ __align__(8) uint64_t bars[kStreamThreads / 32 * kDeepMost];
     __shared__ uint32_t gave_up;
     tc::grid_wait_release();
     const int gt = gw * 32, g = threadIdx.x / gt, t = threadIdx.x % gt, groups = blockDim.x / gt;
@@ -359,14 +424,19 @@ __global__ void __launch_bounds__(kStreamThreads<V>) forward_stream_kernel(const
         tc::mbar_init_fence();
         for (int i = 0; i < deep && row0 + i * step < P.T; ++i) ask(row0 + i * step, i);
     }
-    stage<V>(w, P.w, P.w_dtype, P.d, 1.f);
-    stage<V>(b, P.b, P.w_dtype, P.d, 0.f);
+    if constexpr (V == 8) {
+        stage(w, P.w, P.w_dtype, P.d, 1.f);
+        stage(b, P.b, P.w_dtype, P.d, 0.f);
+    } else {
+        stage_any<2>(w, P.w, P.b, P.w_dtype, P.d);
+    }
     __syncthreads();
     int slot = 0;
     uint32_t turn = 0, phase = 0;
-    const auto column = [&](int i) { return (i * gt + t) * V; };
     for (int row = row0; row < P.T; row += step) {
-        float2 x[kStreamHeld<V> / 2], s = both(0.f);
+        float2 x[kStreamHeld / 2], s = both(0.f);
+        const int before = V == 8 ? 0 : before16(static_cast<Y *>(P.y.p) + (int64_t)row * P.y.ld);
+        const auto column = [&](int i) { return (i * gt + t) * 8 - before; };
         wait_row(bar0 + 8 * turn, phase, &gave_up);
         const uint32_t from = ring.place(row, turn);
 #pragma unroll
@@ -381,10 +451,13 @@ __global__ void __launch_bounds__(kStreamThreads<V>) forward_stream_kernel(const
                         s = add2(s, x[4 * i + k]);
                     }
                 }
-            } else {
-                const float v = in ? shared_value<X>(from + column(i) * kSize) : 0.f;
-                (i & 1 ? x[i / 2].y : x[i / 2].x) = v;
-                if (i & 1) s = add2(s, x[i / 2]);
+            } else if (in) {
+                const Piece<X, 8> q = load_any<X>(from + column(i) * kSize);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x[4 * i + k] = widen2(&q.v[2 * k]);
+                trim(x + 4 * i, column(i), P.d);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) s = add2(s, x[4 * i + k]);
             }
         }
         const float mu = group_sum(s.x + s.y, gw, g, part, slot) * inv;
@@ -402,10 +475,12 @@ __global__ void __launch_bounds__(kStreamThreads<V>) forward_stream_kernel(const
                         s = fma2(x[4 * i + k], x[4 * i + k], s);
                     }
                 }
-            } else {
-                float &v = i & 1 ? x[i / 2].y : x[i / 2].x;
-                v = in ? v - mu : 0.f;
-                if (i & 1) s = fma2(x[i / 2], x[i / 2], s);
+            } else if (in) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x[4 * i + k] = add2(x[4 * i + k], both(-mu));
+                trim(x + 4 * i, column(i), P.d);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) s = fma2(x[4 * i + k], x[4 * i + k], s);
             }
         }
         const float r = 1.f / sqrtf(group_sum(s.x + s.y, gw, g, part, slot) * inv + P.eps);
@@ -417,8 +492,8 @@ __global__ void __launch_bounds__(kStreamThreads<V>) forward_stream_kernel(const
 #pragma unroll
         for (int i = 0; i < kPieces; ++i)
             if (column(i) < P.d) {
+                Piece<Y, 8> o;
                 if constexpr (V == 8) {
-                    Piece<Y, 8> o;
 #pragma unroll
                     for (int k = 0; k < 8; k += 4) {
                         float2 w0, w1, b0, b1;
@@ -429,8 +504,13 @@ __global__ void __launch_bounds__(kStreamThreads<V>) forward_stream_kernel(const
                     }
                     *reinterpret_cast<Piece<Y, 8> *>(y + column(i)) = o;
                 } else {
-                    const float v = i & 1 ? x[i / 2].y : x[i / 2].x;
-                    y[column(i)] = round_to<Y>(fmaf(v * r, shared_value<float>(w_at + column(i) * 4), shared_value<float>(b_at + column(i) * 4)));
+                    const int c = column(i);
+#pragma unroll
+                    for (int k = 0; k < 8; k += 2) {
+                        const float2 u = shared_float2(w_at + place_any<2>(P.d, c + k)), v = shared_float2(w_at + place_any<2>(P.d, c + k + 1));
+                        round2(&o.v[k], fma2(mul2(x[4 * i + k / 2], both(r)), make_float2(u.x, v.x), make_float2(u.y, v.y)));
+                    }
+                    give_any(y, c, P.d, o);
                 }
             }
     }
@@ -440,8 +520,8 @@ __global__ void __launch_bounds__(kStreamThreads<V>) forward_stream_kernel(const
 // dx, and a CTA's share of dw and db, in one pass.
 template <class X, class Y, int V, bool kFull>
 __global__ void __launch_bounds__(kHeldThreads) backward_held_kernel(const NormBwd P, int gw, int deep) {
-    using L = Lane<X, V, kFull>;
-    constexpr int N = kHeld / 2, R = kRowsAtOnce<V>;
+    using L = Lane<X, 8, kFull>; // its columns, for dw and db
+    constexpr int N = kHeld / 2, R = kRowsAtOnce<X, Y, V>;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float part[128 * R];
     __shared__ __align__(8) uint64_t bars[kHeldThreads / 32 * kDeepMost];
@@ -469,7 +549,10 @@ __global__ void __launch_bounds__(kHeldThreads) backward_held_kernel(const NormB
         tc::mbar_init_fence();
         for (int i = 0; i < deep && row0 + i * step < P.T; ++i) ask(row0 + i * step, i);
     }
-    stage<V>(w, P.w, P.w_dtype, P.d, 1.f);
+    if constexpr (V == 8)
+        stage(w, P.w, P.w_dtype, P.d, 1.f);
+    else
+        stage_any<1>(w, P.w, nullptr, P.w_dtype, P.d);
     __syncthreads();
     float2 dw[N], db[N];
 #pragma unroll
@@ -497,48 +580,41 @@ __global__ void __launch_bounds__(kHeldThreads) backward_held_kernel(const NormB
             if (row + q * step < P.T) wait_row(bar0 + 8 * turn, phase, &gave_up);
             if (++turn == (uint32_t)deep) turn = 0, phase ^= 1;
         }
-        // x - mu and dy of piece i of row q (V == 1: eight single values), zeros past the rows' ends
-        const auto piece = [&](int q, int i, float2(&c)[4], float2(&e)[4]) {
+        // x - mu and dy of row q, eight columns from col on, zeros past the row's ends
+        const auto piece = [&](int q, int col, float2(&c)[4], float2(&e)[4]) {
             uint32_t at = first + q;
             if (at >= (uint32_t)deep) at -= deep;
             const int64_t from = row + q * step;
-            const bool there = from < P.T;
-            if constexpr (V == 8) {
-                Piece<X, 8> u = {};
-                Piece<Y, 8> v = {};
-                if (lx.in(i) && there) {
-                    u = load_shared<X>(rx.place(from, at) + lx.column(i) * (uint32_t)sizeof(X));
-                    v = load_shared<Y>(ry.place(from, at) + lx.column(i) * (uint32_t)sizeof(Y));
-                }
+            const bool there = (kFull || col < P.d) && from < P.T;
+            Piece<X, 8> u = {};
+            Piece<Y, 8> v = {};
+            if (there) {
+                const uint32_t ux = rx.place(from, at) + col * (int)sizeof(X), vy = ry.place(from, at) + col * (int)sizeof(Y);
+                u = V == 8 ? load_shared<X>(ux) : load_any<X>(ux);
+                v = V == 8 ? load_shared<Y>(vy) : load_any<Y>(vy);
+            }
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    c[k] = add2(widen2(&u.v[2 * k]), both(-mu[q]));
-                    e[k] = widen2(&v.v[2 * k]);
-                }
-            } else {
-                const uint32_t px = rx.place(from, at), py = ry.place(from, at);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int col = lx.column(8 * i + k);
-                    const bool in = there && lx.in(8 * i + k);
-                    (k & 1 ? c[k / 2].y : c[k / 2].x) = in ? shared_value<X>(px + col * (uint32_t)sizeof(X)) - mu[q] : 0.f;
-                    (k & 1 ? e[k / 2].y : e[k / 2].x) = in ? shared_value<Y>(py + col * (uint32_t)sizeof(Y)) : 0.f;
-                }
+            for (int k = 0; k < 4; ++k) {
+                c[k] = add2(widen2(&u.v[2 * k]), both(-mu[q]));
+                e[k] = widen2(&v.v[2 * k]);
+            }
+            if (V != 8) {
+                trim(c, col, P.d);
+                trim(e, col, P.d);
             }
         };
-        const auto weights = [&](int i, float2(&o)[4]) {
-            if constexpr (V == 8) {
-                if (!lx.in(i)) {
+        const auto weights = [&](int col, float2(&o)[4]) {
+            if (!kFull && col >= P.d) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) o[k] = both(0.f);
-                    return;
-                }
-                four(w_at, P.d, lx.column(i), o[0], o[1]);
-                four(w_at, P.d, lx.column(i) + 4, o[2], o[3]);
+                for (int k = 0; k < 4; ++k) o[k] = both(0.f);
+                return;
+            }
+            if constexpr (V == 8) {
+                four(w_at, P.d, col, o[0], o[1]);
+                four(w_at, P.d, col + 4, o[2], o[3]);
             } else {
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    (k & 1 ? o[k / 2].y : o[k / 2].x) = lx.in(8 * i + k) ? shared_value<float>(w_at + lx.column(8 * i + k) * 4) : 0.f;
+                for (int k = 0; k < 8; ++k) (k & 1 ? o[k / 2].y : o[k / 2].x) = shared_float(w_at + place_any<1>(P.d, col + k));
             }
         };
         float2 s1[R], s2[R];
@@ -547,11 +623,11 @@ __global__ void __launch_bounds__(kHeldThreads) backward_held_kernel(const NormB
 #pragma unroll
         for (int i = 0; i < kHeld / 8; ++i) { // past the row's end dy is zero, so all of these are
             float2 wv[4];
-            weights(i, wv);
+            weights(lx.column(i), wv);
 #pragma unroll
             for (int q = 0; q < R; ++q) {
                 float2 c[4], e[4];
-                piece(q, i, c, e);
+                piece(q, lx.column(i), c, e);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const float2 xh = mul2(c[k], both(r[q])), gv = mul2(e[k], wv[k]);
@@ -566,40 +642,32 @@ __global__ void __launch_bounds__(kHeldThreads) backward_held_kernel(const NormB
 #pragma unroll
         for (int q = 0; q < R; ++q) s[2 * q] = s1[q].x + s1[q].y, s[2 * q + 1] = s2[q].x + s2[q].y;
         group_sums(s, gw, g, part, slot);
-        if (t == 0 && row > row0 && deep >= 2 * R) // the rows before these have been read by all: into their places
+        if (t == 0 && row > row0) // the rows before these have been read by all: into their places
             for (int q = 0; q < R; ++q)
                 if (row + (q + deep - R) * step < P.T) ask(row + (q + deep - R) * step, (first + deep - R + q) % deep);
 #pragma unroll
         for (int i = 0; i < kHeld / 8 && P.dx.p; ++i) {
             float2 wv[4];
-            weights(i, wv);
+            if (V == 8) weights(lx.column(i), wv);
 #pragma unroll
             for (int q = 0; q < R; ++q) {
+                X *dx = static_cast<X *>(P.dx.p) + (row + q * step) * P.dx.ld;
+                const int col = lx.column(i) - (V == 8 ? 0 : before16(dx)); // whole 16-byte pieces of dx
+                if (V != 8) weights(col, wv);
                 float2 c[4], e[4];
-                piece(q, i, c, e);
+                piece(q, col, c, e);
                 // r (g - m1 - (x - mu) r m2), its factors of the row put together first
                 const float2 rr = both(r[q]), c1 = both(-r[q] * (s[2 * q] * inv)), c2 = both(-r[q] * (r[q] * (s[2 * q + 1] * inv)));
-                X *dx = static_cast<X *>(P.dx.p) + (row + q * step) * P.dx.ld;
                 Piece<X, 8> o;
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     round2(&o.v[2 * k], fma2(mul2(e[k], wv[k]), rr, fma2(c[k], c2, c1)));
-                if (row + q * step >= P.T) continue;
-                if constexpr (V == 8) {
-                    if (lx.in(i)) *reinterpret_cast<Piece<X, 8> *>(dx + lx.column(i)) = o;
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        if (lx.in(8 * i + k)) dx[lx.column(8 * i + k)] = o.v[k];
-                }
+                if (row + q * step >= P.T || (!kFull && col >= P.d)) continue;
+                if constexpr (V == 8)
+                    *reinterpret_cast<Piece<X, 8> *>(dx + col) = o;
+                else
+                    give_any(dx, col, P.d, o);
             }
-        }
-        if (deep < 2 * R) { // long rows of 32 bits: no place but these rows' own
-            group_meet(gw, g);
-            if (t == 0)
-#pragma unroll
-                for (int q = 0; q < R; ++q)
-                    if (row + (q + deep) * step < P.T) ask(row + (q + deep) * step, (first + q) % deep);
         }
     }
     settle(&gave_up);
@@ -610,8 +678,8 @@ __global__ void __launch_bounds__(kHeldThreads) backward_held_kernel(const NormB
     if (groups == 1) sum = out;
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
-        const int c = lx.column(i / V) + i % V;
-        if (!lx.in(i / V)) continue;
+        const int c = lx.column(i / 8) + i % 8;
+        if (!kFull && c >= P.d) continue;
         sum[c] = i & 1 ? dw[i / 2].y : dw[i / 2].x;
         sum[P.d + c] = i & 1 ? db[i / 2].y : db[i / 2].x;
     }
@@ -802,6 +870,9 @@ int rows_ahead(size_t bytes, size_t rest, int groups) {
     const size_t n = (kHeldSmem - rest) / (bytes * groups);
     return n > kDeepMost ? kDeepMost : (int)n;
 }
+// Pieces of eight columns of a row, as many as there are where they begin anywhere; whether all lanes hold them.
+int eights(int d, bool whole) { return whole ? d / 8 : (d + 14) / 8; }
+bool at_once(int d, bool whole) { return eights(d, whole) * 8 <= kHeldMost; }
 constexpr int kFewRows = 4; // an SM
 // Warps of a group for a row of `pieces` pieces.
 int group_warps(int pieces, int per_lane) { return (pieces + 32 * per_lane - 1) / (32 * per_lane); }
@@ -820,13 +891,13 @@ cudaError_t launch_norm_forward(const NormFwd &P, cudaStream_t s) {
         constexpr int V = decltype(v)::value;
         const int pieces = P.d / V + (P.d % V != 0), sms = device_sm_count();
         if (P.d <= kHeldMost) {
-            if (P.T > kFewRows * sms) {
+            if (P.T > kFewRows * sms && at_once(P.d, V == 8)) {
                 static SmemAttr attr;
                 const auto kernel = forward_stream_kernel<X, Y, V>;
-                const int gw = group_warps(pieces, kStreamHeld<V> / V);
-                int groups = kStreamThreads<V> / 32 / gw;
+                const int gw = group_warps(eights(P.d, V == 8), kStreamHeld / 8);
+                int groups = kStreamThreads / 32 / gw;
                 if (groups > 16 && gw > 1) groups = 16; // barriers
-                const size_t row = ring_pitch(P.d, sizeof(X), V == 8), rest = (size_t)P.d * 8;
+                const size_t row = ring_pitch(P.d, sizeof(X), V == 8), rest = V == 8 ? (size_t)P.d * 8 : (size_t)eighths(P.d) * 64;
                 const int deep = rows_ahead(row, rest, groups), smem = (int)(deep * groups * row + rest);
                 const cudaError_t e = ensure_smem(attr, reinterpret_cast<const void *>(kernel), smem);
                 if (e != cudaSuccess) return e;
@@ -853,8 +924,8 @@ cudaError_t launch_norm_backward(const NormBwd &P, cudaStream_t s) {
         const int pieces = P.d / V + (P.d % V != 0), sms = device_sm_count();
         const bool sums = P.dw || P.db;
         cudaError_t e = cudaSuccess;
-        if (P.d <= kHeldMost) {
-            const int gw = group_warps(pieces, kHeld / V);
+        if (at_once(P.d, V == 8)) {
+            const int gw = group_warps(eights(P.d, V == 8), kHeld / 8);
             int groups = kHeldThreads / 32 / gw, need = (P.T + sms - 1) / sms;
             if (groups > need) groups = need; // 8 at most where a group has barriers
             const int threads = groups * gw * 32, most = sms < kNormParts ? sms : kNormParts, all = (P.T + groups - 1) / groups;
@@ -863,7 +934,7 @@ cudaError_t launch_norm_backward(const NormBwd &P, cudaStream_t s) {
                 constexpr bool kFull = decltype(full)::value;
                 static SmemAttr attr;
                 const auto kernel = backward_held_kernel<X, Y, V, kFull>;
-                const size_t row = ring_pitch(P.d, sizeof(X), V == 8) + ring_pitch(P.d, sizeof(Y), V == 8), rest = (size_t)P.d * 4;
+                const size_t row = ring_pitch(P.d, sizeof(X), V == 8) + ring_pitch(P.d, sizeof(Y), V == 8), rest = V == 8 ? (size_t)P.d * 4 : (size_t)eighths(P.d) * 32;
                 const int deep = rows_ahead(row, rest, groups), last = groups > 1 ? groups * P.d * 8 : 0;
                 const int ring = (int)(deep * groups * row + rest), smem = ring > last ? ring : last;
                 const cudaError_t f = ensure_smem(attr, reinterpret_cast<const void *>(kernel), smem);

@@ -151,6 +151,47 @@ def test_norm_strided_rows(t, d, ld):
     assert torch.equal(over, dxs) and torch.equal(dw, dw2) and torch.equal(db, db2)
 
 
+@pytest.mark.parametrize("d", [1, 5, 8, 9, 33, 1001, 4090, 8185, 8186, 8192])
+@pytest.mark.parametrize("tx,ty", [(FP, FP), (BF, BF), (HF, FP), (FP, BF), (BF, HF)])
+def test_norm_rows_that_begin_anywhere(tx, ty, d):
+    """Each operand at an offset and a stride of its own, so that a row's 16-byte pieces differ between them and from
+    row to row; many rows and few."""
+    for T, at in ((1301, (1, 3, 6, 5)), (40, (2, 1, 7, 4))):
+        g, x, w, b = norm_inputs(T, d, tx, FP)
+        bufs = []
+
+        def rows(t, i, values=None):
+            ld = d + (1, 2, 5, 3)[i]
+            buf = torch.full((at[i] + T * ld + 64,), 7.0, dtype=t, device="cuda")
+            v = buf[at[i]:at[i] + T * ld].view(T, ld)[:, :d]
+            if values is not None:
+                v.copy_(values)
+            bufs.append((buf, v))
+            return v
+
+        n = LayerNorm(w, b)
+        xs, y = rows(tx, 0, x), rows(ty, 1)
+        mean, rstd = (torch.empty(T, device="cuda") for _ in range(2))
+        n.forward(xs, y, mean, rstd)
+        for k, v in (("y", y), ("mean", mean), ("rstd", rstd)):
+            R.close(v, *R.norm_forward(x, w, b, 1e-5, ty)[k], k)
+        dy = randn(g, T, d, t=ty)
+        dys, dx = rows(ty, 2, dy), rows(tx, 3)
+        dw, db = (torch.empty(d, device="cuda") for _ in range(2))
+        n.backward(dys, xs, mean, rstd, dx, dw, db)
+        for k, v, t in (("dx", dx, tx), ("dw", dw, FP), ("db", db, FP)):
+            r, e = R.norm_backward(dy, x, mean, rstd, w)[k]
+            R.close(v, r, e + R.rnd(r.abs() + e, t), k)
+        if tx == ty:  # in place
+            n.backward(dys, xs, mean, rstd, dys)
+            assert torch.equal(dys, dx)
+            n.forward(xs, xs)
+            R.close(xs, *R.norm_forward(x, w, b, 1e-5, ty)["y"], "y over x")
+        for buf, v in bufs:  # nothing beside the rows
+            v.fill_(7.0)
+            assert (buf == 7.0).all()
+
+
 def test_norm_far_values():
     """A mean a thousand times the spread, large and small values, constant rows, rows with an infinity or a NaN."""
     g = gen(5)
