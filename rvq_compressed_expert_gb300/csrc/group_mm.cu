@@ -245,6 +245,9 @@ int width(int n) { return n >= 256 ? 256 : n <= 64 ? 64 : (n + 31) / 32 * 32; }
 // Pairs of CTAs from so many rows an expert on (their mean: the offsets are on the device): they halve the bytes of W
 // an SM takes in for its columns, which counts once W is not what memory is read for.
 bool pairs(const Group &G) { return G.rows / G.E >= 160; }
+// For dW, whose sums are over an expert's rows, from more on: short sums leave the two CTAs waiting for each other's
+// epilogues (40 x 1536 x 5120: 256 rows 205 us in pairs, 159 apart; 400 rows 253 and 259; 64 experts of 512 rows 540 and 615).
+bool weight_pairs(const Group &G) { return G.rows / G.E >= 384 && G.n > kBM; }
 
 // Rows of an expert in one tile: few where there are few, so that the stages, which have room for as many, hold more of
 // W on its way (one token, 16 rows of 16 experts: 73 us with 256, 59 with 64).
@@ -305,7 +308,7 @@ cudaError_t launch_group_dw(const Group &G, const void *dy, const void *x, void 
     const auto go = [&](auto cg, auto adds) {
         return weights_product<decltype(cg)::value, decltype(adds)::value>(G, dy, x, dw, grad_dtype, s);
     };
-    return pairs(G) && G.n > kBM ? (add ? go(kTwo, kYes) : go(kTwo, kNo)) : add ? go(kOne, kYes) : go(kOne, kNo);
+    return weight_pairs(G) ? (add ? go(kTwo, kYes) : go(kTwo, kNo)) : add ? go(kOne, kYes) : go(kOne, kNo);
 }
 
 cudaError_t group_status(uint32_t *timeout, uint32_t *offsets) {
