@@ -249,15 +249,40 @@ bool pairs(const Group &G) { return G.rows / G.E >= 160; }
 // epilogues (40 x 1536 x 5120: 256 rows 205 us in pairs, 159 apart; 400 rows 253 and 259; 64 experts of 512 rows 540 and 615).
 bool weight_pairs(const Group &G) { return G.rows / G.E >= 384 && G.n > kBM; }
 
-// Rows of an expert in one tile: few where there are few, so that the stages, which have room for as many, hold more of
-// W on its way (one token, 16 rows of 16 experts: 73 us with 256, 59 with 64).
-int share_rows(const Group &G) { return G.rows / G.E < 32 ? 64 : 256; }
+// What the tiles of y or dx (N columns) take into an SM for a piece of k, by rounds of tiles, were the rows spread evenly:
+// single CTAs take the best of the heights that begin() has.
+long long rows_cost(const Group &G, int N, int share, bool pair, bool mn, int sms) {
+    const long long experts = G.E < G.rows ? G.E : G.rows, n = (G.rows + experts - 1) / experts, cuts = (n + share - 1) / share;
+    const long long unit = pair ? 32 : 16, cols = ((n + cuts - 1) / cuts + unit - 1) / unit * unit, shares = experts * cuts;
+    const auto rounds = [&](int high, int slots) { return (shares * ((N + high - 1) / high) + slots - 1) / slots; };
+    if (pair) return rounds(2 * kBM, sms / 2) * (kBM + cols / 2);
+    long long best = rounds(kBM, sms) * (kBM + cols);
+    for (int h = kBM; h > 0; h -= mn ? 64 : 32) {
+        const long long c = rounds(h, sms) * (h + cols);
+        if (c < best) best = c;
+    }
+    return best;
+}
+
+// Rows of an expert in one tile, and whether a pair of CTAs takes it.  64 where there are few, so that the stages, which
+// have room for as many, hold more of W on its way (one token, 16 rows of 16 experts: 73 us with 256, 59 with 64); and where
+// wide tiles leave SMs without work (229 rows of one expert, 1912 to 104: 17.8 us and 12.7; 4 x 1150 rows, 184 to 216: 9.5 and 8.0).
+struct RowsPlan {
+    int share;
+    bool pair;
+};
+RowsPlan rows_plan(const Group &G, int N, bool mn) {
+    const RowsPlan P{G.rows / G.E < 32 ? 64 : 256, pairs(G)};
+    const int sms = device_sm_count();
+    const bool narrow = P.share > 64 && 5 * rows_cost(G, N, 64, false, mn, sms) < 4 * rows_cost(G, N, P.share, P.pair, mn, sms);
+    return narrow ? RowsPlan{64, false} : P;
+}
 
 template <int kCG, bool kWmn, bool kAdd>
-cudaError_t rows_product(const Group &G, const void *a, int K, const void *w, int N, void *out, int out_dtype, cudaStream_t s) {
+cudaError_t rows_product(const Group &G, int share, const void *a, int K, const void *w, int N, void *out, int out_dtype, cudaStream_t s) {
     RowsJob<kCG, kWmn, kAdd> J = {};
     TileArgs P = {};
-    P.BN = J.off.share = share_rows(G);
+    P.BN = J.off.share = share;
     J.off.p = G.offsets, J.off.E = G.E, J.off.rows = G.rows;
     J.N = N;
     J.pieces = (K + 63) / 64;
@@ -295,14 +320,16 @@ cudaError_t weights_product(const Group &G, const void *dy, const void *x, void 
 } // namespace
 
 cudaError_t launch_group_forward(const Group &G, const void *x, const void *w, void *y, int out_dtype, int add, cudaStream_t s) {
+    const RowsPlan R = rows_plan(G, G.n, false);
     const auto go = [&](auto cg, auto adds) {
-        return rows_product<decltype(cg)::value, false, decltype(adds)::value>(G, x, G.k, w, G.n, y, out_dtype, s);
+        return rows_product<decltype(cg)::value, false, decltype(adds)::value>(G, R.share, x, G.k, w, G.n, y, out_dtype, s);
     };
-    return pairs(G) ? (add ? go(kTwo, kYes) : go(kTwo, kNo)) : add ? go(kOne, kYes) : go(kOne, kNo);
+    return R.pair ? (add ? go(kTwo, kYes) : go(kTwo, kNo)) : add ? go(kOne, kYes) : go(kOne, kNo);
 }
 cudaError_t launch_group_dx(const Group &G, const void *dy, const void *w, void *dx, cudaStream_t s) {
-    return pairs(G) ? rows_product<2, true, false>(G, dy, G.n, w, G.k, dx, G.dtype, s)
-                    : rows_product<1, true, false>(G, dy, G.n, w, G.k, dx, G.dtype, s);
+    const RowsPlan R = rows_plan(G, G.k, true);
+    return R.pair ? rows_product<2, true, false>(G, R.share, dy, G.n, w, G.k, dx, G.dtype, s)
+                  : rows_product<1, true, false>(G, R.share, dy, G.n, w, G.k, dx, G.dtype, s);
 }
 cudaError_t launch_group_dw(const Group &G, const void *dy, const void *x, void *dw, int grad_dtype, int add, cudaStream_t s) {
     const auto go = [&](auto cg, auto adds) {
