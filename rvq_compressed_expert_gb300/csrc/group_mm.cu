@@ -249,6 +249,24 @@ bool pairs(const Group &G) { return G.rows / G.E >= 160; }
 // epilogues (40 x 1536 x 5120: 256 rows 205 us in pairs, 159 apart; 400 rows 253 and 259; 64 experts of 512 rows 540 and 615).
 bool weight_pairs(const Group &G) { return G.rows / G.E >= 384 && G.n > kBM; }
 
+// Columns of dW's tiles: as many as there are, 256 at most, or 64 by single CTAs where those leave SMs without work, by what
+// the rounds of tiles take into an SM for a piece of the rows (dx and dW of 684 rows of one expert, 1192 x 152: 21.7 us and
+// 16.1; two of 2985 rows, 1592 x 136: 43.8 and 36.9).
+struct WeightsPlan {
+    int BN;
+    bool pair;
+};
+WeightsPlan weights_plan(const Group &G) {
+    const int sms = device_sm_count();
+    const auto cost = [&](const WeightsPlan &P) {
+        const int high = P.pair ? 2 * kBM : kBM, slots = P.pair ? sms / 2 : sms;
+        const long long tiles = (long long)G.E * ((G.n + high - 1) / high) * ((G.k + P.BN - 1) / P.BN);
+        return (tiles + slots - 1) / slots * (kBM + P.BN / (P.pair ? 2 : 1));
+    };
+    const WeightsPlan wide{width(G.k), weight_pairs(G)}, narrow{64, false};
+    return 5 * cost(narrow) < 4 * cost(wide) ? narrow : wide;
+}
+
 // What the tiles of y or dx (N columns) take into an SM for a piece of k, by rounds of tiles, were the rows spread evenly:
 // single CTAs take the best of the heights that begin() has.
 long long rows_cost(const Group &G, int N, int share, bool pair, bool mn, int sms) {
@@ -301,10 +319,10 @@ cudaError_t rows_product(const Group &G, int share, const void *a, int K, const 
 }
 
 template <int kCG, bool kAdd>
-cudaError_t weights_product(const Group &G, const void *dy, const void *x, void *dw, int grad_dtype, cudaStream_t s) {
+cudaError_t weights_product(const Group &G, int BN, const void *dy, const void *x, void *dw, int grad_dtype, cudaStream_t s) {
     WeightsJob<kCG, kAdd> J = {};
     TileArgs P = {};
-    P.BN = J.BN = width(G.k);
+    P.BN = J.BN = BN;
     J.off = {G.offsets, G.E, G.rows, 0};
     J.M = G.n;
     J.tm = (G.n + J.kHigh - 1) / J.kHigh;
@@ -332,10 +350,11 @@ cudaError_t launch_group_dx(const Group &G, const void *dy, const void *w, void 
                   : rows_product<1, true, false>(G, R.share, dy, G.n, w, G.k, dx, G.dtype, s);
 }
 cudaError_t launch_group_dw(const Group &G, const void *dy, const void *x, void *dw, int grad_dtype, int add, cudaStream_t s) {
+    const WeightsPlan W = weights_plan(G);
     const auto go = [&](auto cg, auto adds) {
-        return weights_product<decltype(cg)::value, decltype(adds)::value>(G, dy, x, dw, grad_dtype, s);
+        return weights_product<decltype(cg)::value, decltype(adds)::value>(G, W.BN, dy, x, dw, grad_dtype, s);
     };
-    return weight_pairs(G) ? (add ? go(kTwo, kYes) : go(kTwo, kNo)) : add ? go(kOne, kYes) : go(kOne, kNo);
+    return W.pair ? (add ? go(kTwo, kYes) : go(kTwo, kNo)) : add ? go(kOne, kYes) : go(kOne, kNo);
 }
 
 cudaError_t group_status(uint32_t *timeout, uint32_t *offsets) {
