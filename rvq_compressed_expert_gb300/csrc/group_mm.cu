@@ -31,6 +31,15 @@ cudaError_t stack_map(CUtensorMap *m, const void *p, int cols, int rows, int mat
                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
+cudaError_t store_map3(CUtensorMap *m, void *p, int dtype, int mats, int rows, int cols) {
+    const size_t size = dense::type_size(dtype);
+    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)mats};
+    const cuuint64_t strides[2] = {cols * size, cols * size * rows};
+    const cuuint32_t box[3] = {(cuuint32_t)(64 / size), 32, 1};
+    return dense::encode_map(m, size == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, p, dims, strides, box,
+                             CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
+}
+
 namespace {
 
 __device__ uint32_t g_bad_offsets;
@@ -219,6 +228,7 @@ template <int kCG, bool kAdd> struct WeightsJob {
         T.pieces = (n + 63) >> 6;
         T.left = n - ((T.pieces - 1) << 6);
         T.m = e * M + mi * kHigh;
+        T.z = e;
         T.rows = M - mi * kHigh;
         return T;
     }
@@ -230,7 +240,7 @@ template <int kCG, bool kAdd> struct WeightsJob {
     __device__ __forceinline__ void fetch(const Out32 &o, const Spot &, int n, Held &h) const { out.fetch(o, n, h); }
     __device__ __forceinline__ void turn(const Out32 &o, uint4 *t, const Held &h, In &in) const { out.turn(o, t, h, in); }
     __device__ __forceinline__ void tile(Out32 &o, const Spot &T, int n, const float (&v)[32], const In &in) const {
-        if (T.pieces || !kAdd) out.put(o, n, v, in);
+        if (T.pieces || !kAdd) out.put(o, T, n, v, in);
     }
 };
 
@@ -329,7 +339,7 @@ cudaError_t weights_product(const Group &G, int BN, const void *dy, const void *
     J.tn = (G.k + J.BN - 1) / J.BN;
     cudaError_t e = stack_map(&J.ta, dy, G.n, G.rows, 1, G.n, (size_t)G.n * G.rows, 64);
     if (e == cudaSuccess) e = stack_map(&J.tb, x, G.k, G.rows, 1, G.k, (size_t)G.k * G.rows, 64);
-    if (e == cudaSuccess) e = J.out.set(dw, G.E * G.n, G.k, grad_dtype);
+    if (e == cudaSuccess) e = J.out.set(dw, G.E, G.n, G.k, grad_dtype);
     if (e != cudaSuccess) return e;
     return launch_tiles_as<kCG>(P, J, G.dtype == WASTE_ACT_BF16, (size_t)(G.E + 1) * 4, (long long)G.E * J.tm * J.tn,
                                 device_sm_count(), s);

@@ -177,12 +177,14 @@ struct Stack {
         T.pieces = (K + 63) >> 6;
         T.left = 64;
         T.m = z * M + T.am;
+        T.z = z;
         T.rows = M - T.am;
         return T;
     }
 };
-__device__ __forceinline__ void put_halves(Out32 &o, const CUtensorMap *map, void *p, int ld, int n, const float (&v)[32]) {
-    dense::put32_as(WASTE_ACT_F16, o, o.rows >= 32 ? map : nullptr, p, ld, n, ld, true, false, v);
+// 32 columns of rows of a matrix of M x ld halves
+__device__ __forceinline__ void put_halves(Out32 &o, const Spot &T, const CUtensorMap *map, int M, int ld, int n, const float (&v)[32]) {
+    put3_as(WASTE_ACT_F16, o, map, n, ld, o.m - T.z * M, T.z, v);
 }
 // Tile t of those on and below a diagonal, row by row.
 __host__ __device__ __forceinline__ void triangle(int t, int &i, int &j) {
@@ -230,18 +232,17 @@ template <bool kMn> struct WholeGramJob {
     static constexpr bool kAmn = kMn, kBmn = kMn, kMask = false, kReads = false, kTwoPieces = true, kRagged = false;
     CUtensorMap ta, tb, to;
     Stack s;
-    void *a;
     int ldm;
     __device__ void begin(uint8_t *) const {}
     __device__ __forceinline__ int tiles(const uint8_t *) const { return s.tiles(); }
     __device__ __forceinline__ Spot spot(const uint8_t *, int t) const { return s.spot(t); }
     using Held = Nothing;
     using In = Nothing;
-    __device__ __forceinline__ void tile(Out32 &o, const Spot &, int n, const float (&v)[32], const In &) const {
+    __device__ __forceinline__ void tile(Out32 &o, const Spot &T, int n, const float (&v)[32], const In &) const {
         float x[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) x[i] = v[i] * kDown;
-        put_halves(o, &to, a, ldm, n, x);
+        put_halves(o, T, &to, s.M, ldm, n, x);
     }
 };
 // A from its partial sums, both halves: a CTA takes 64 x 64 values of a tile.
@@ -290,7 +291,6 @@ struct SquareJob {
     CUtensorMap ta, tb, to;
     Stack s;
     const void *a;
-    void *out;
     float *diag;
     int ldm;
     float b, c;
@@ -316,7 +316,7 @@ struct SquareJob {
                 x[i] = 0.f;
             }
         }
-        put_halves(o, &to, out, ldm, n, x);
+        put_halves(o, T, &to, s.M, ldm, n, x);
     }
 };
 // X <- a X + B X (kTall: a X + X B), the last one to the caller's memory
@@ -325,8 +325,7 @@ template <bool kTall, bool kLast, bool kAdd> struct StepJob {
     static constexpr bool kAmn = false, kBmn = !kTall, kMask = false, kReads = true, kTwoPieces = false, kRagged = false;
     CUtensorMap ta, tb, thi, tlo;
     Stack s;
-    const void *hi;
-    void *lo, *hi_next;
+    const void *hi, *lo;
     const float *diag;
     int ldx, ldm;
     float a;
@@ -341,7 +340,7 @@ template <bool kTall, bool kLast, bool kAdd> struct StepJob {
         if (r >= T.rows) return;
         const int w = min(BN, ldx - T.n);
         if (w > 0 && !(kLast && half))
-            ask_l2(static_cast<const __half *>(half ? static_cast<const void *>(lo) : hi) + (size_t)(T.m + r) * ldx + T.n, w * 2);
+            ask_l2(static_cast<const __half *>(half ? lo : hi) + (size_t)(T.m + r) * ldx + T.n, w * 2);
         if constexpr (kAdd) out.ahead(T.m + r, T.n, half, BN);
     }
     struct Held {
@@ -384,12 +383,12 @@ template <bool kTall, bool kLast, bool kAdd> struct StepJob {
         if constexpr (kLast) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) x[i] *= scale;
-            out.put(o, n, x, in.base);
+            out.put(o, T, n, x, in.base);
         } else {
 #pragma unroll
             for (int i = 0; i < 32; ++i) l[i] = x[i] - __half2float(__float2half_rn(x[i]));
-            put_halves(o, &thi, hi_next, ldx, n, x);
-            if (keep_lo) put_halves(o, &tlo, lo, ldx, n, l);
+            put_halves(o, T, &thi, s.M, ldx, n, x);
+            if (keep_lo) put_halves(o, T, &tlo, s.M, ldx, n, l);
         }
     }
 };
@@ -675,8 +674,8 @@ template <bool kTall, bool kAdd> cudaError_t steps(const Ortho &P, const OrthoPa
     const auto s_map = [&](CUtensorMap *t, const void *p, int box) {
         if (e == cudaSuccess) e = stack_map(t, p, m, m, P.count, W.ldm, ss, box);
     };
-    const auto o_map = [&](CUtensorMap *t, void *p, int bytes, int rows, int ld) {
-        if (e == cudaSuccess) e = dense::store_map(t, p, bytes, rows, ld);
+    const auto o_map = [&](CUtensorMap *t, void *p, int rows, int ld) { // a stack of halves
+        if (e == cudaSuccess) e = store_map3(t, p, WASTE_ACT_F16, P.count, rows, ld);
     };
     GramJob<kTall> G = {};
     SquareJob Q = {};
@@ -685,27 +684,27 @@ template <bool kTall, bool kAdd> cudaError_t steps(const Ortho &P, const OrthoPa
     G.out = parts;
     G.side = W.side, G.tri = W.tri, G.slices = W.slices, G.count = P.count, G.pieces = (n + 63) / 64;
     const long long items = (long long)P.count * W.tri * W.slices;
-    if (!whole) o_map(&G.to, parts, 4, (int)(items * W.side), W.side);
+    if (!whole) e = dense::store_map(&G.to, parts, 4, (int)(items * W.side), W.side);
     WholeGramJob<kTall> D = {};
     D.s.set(gs.cg, gs.BN, P.count, m, m, n);
-    o_map(&D.to, A, 2, P.count * m, W.ldm);
-    D.a = A, D.ldm = W.ldm;
+    o_map(&D.to, A, m, W.ldm);
+    D.ldm = W.ldm;
     Q.s.set(qs.cg, qs.BN, P.count, m, m, m);
     s_map(&Q.ta, A, kBM);
     s_map(&Q.tb, A, qs.BN / qs.cg);
-    o_map(&Q.to, B, 2, P.count * m, W.ldm);
-    Q.a = A, Q.out = B, Q.diag = diag, Q.ldm = W.ldm, Q.b = P.b, Q.c = P.c;
+    o_map(&Q.to, B, m, W.ldm);
+    Q.a = A, Q.diag = diag, Q.ldm = W.ldm, Q.b = P.b, Q.c = P.c;
     S.s.set(xx.cg, xx.BN, P.count, P.rows, P.cols, m);
     s_map(kTall ? &S.tb : &S.ta, B, kTall ? xx.BN / xx.cg : kBM);
-    o_map(&S.tlo, lo, 2, P.count * P.rows, W.ldx);
+    o_map(&S.tlo, lo, P.rows, W.ldx);
     S.lo = lo, S.diag = diag, S.ldx = W.ldx, S.ldm = W.ldm, S.a = P.a;
-    if (e == cudaSuccess) e = L.out.set(P.out, P.count * P.rows, P.cols, P.out_dtype);
+    if (e == cudaSuccess) e = L.out.set(P.out, P.count, P.rows, P.cols, P.out_dtype);
     CUtensorMap ga[2], gb[2], sx[2], st[2];
     for (int i = 0; i < 2; ++i) {
         x_map(&ga[i], i, kTall ? 64 : kBM);
         x_map(&gb[i], i, kTall ? 64 : gs.BN / gs.cg);
         x_map(&sx[i], i, kTall ? kBM : 64);
-        o_map(&st[i], hi[i], 2, P.count * P.rows, W.ldx);
+        o_map(&st[i], hi[i], P.rows, W.ldx);
     }
     const int per = W.side / 64;
     for (int i = 0; i < P.steps && e == cudaSuccess; ++i) {
@@ -724,7 +723,6 @@ template <bool kTall, bool kAdd> cudaError_t steps(const Ortho &P, const OrthoPa
         if (i + 1 < P.steps) {
             S.thi = st[from ^ 1];
             S.keep_lo = i + 2 < P.steps;
-            S.hi_next = hi[from ^ 1];
             e = launch(xx.cg, xx.BN, S, tiles, sms, s);
         } else {
             L.ta = S.ta, L.tb = S.tb, L.s = S.s, L.hi = S.hi, L.lo = S.lo, L.diag = S.diag, L.ldx = S.ldx, L.ldm = S.ldm, L.a = S.a;

@@ -45,7 +45,8 @@ struct Spot {
     int am, az, bm, bz; // A's and B's first row (m, n) and matrix
     int ak, bk;         // their first k
     int pieces, left;   // pieces of k; how many k of the last one count (kMask)
-    int m, n, rows;     // place in the result: first row, first column, rows that are the tile's
+    int m, n, rows;     // place in the result: first row (of all matrices'), first column, rows that are the tile's
+    int z;              // matrix of the result
     // kRagged: columns of the tile (a multiple of 16 a CTA), and the rows of A that each CTA loads (of 32, MN-major 64)
     int cols = 0, high = 0;
 };
@@ -120,15 +121,47 @@ __device__ __forceinline__ void ask_l2(const void *p, int bytes) {
 
 struct Nothing {};
 
+// The copy out for a stack of matrices, a box of 32 rows and 64 bytes ending where its matrix ends: a tile's last
+// rows go the same way as all others (lane by lane they take longer than the rest of the tile: 63 matrices of 240 x 5376
+// zeros 65 us, 256 rows 37).
+__device__ __forceinline__ void tma_store3(const CUtensorMap *m, int x, int y, int z, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(m), "r"(src),
+                 "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+// A map for it: rows of cols values (whole 16-byte pieces).
+cudaError_t store_map3(CUtensorMap *m, void *p, int dtype, int mats, int rows, int cols);
+template <class O>
+__device__ __forceinline__ void send3(Out32 &o, const CUtensorMap *map, int n, int N, int row, int z, const float *v) {
+    constexpr int kPer = 16 / (int)sizeof(O);
+    uint4 *turn = o.next();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) turn[dense::turned(o.lane, i, 4)] = dense::piece_of(v + kPer * i, O());
+    tc::fence_proxy_async();
+    __syncwarp();
+    if (o.lane == 0 && n < N) tma_store3(map, n, row, z, tc::smem_u32(turn));
+}
+// 32 columns from n on of up to 32 rows from `row` on, lane = row.
+__device__ __forceinline__ void put3_as(int dtype, Out32 &o, const CUtensorMap *map, int n, int N, int row, int z, const float (&v)[32]) {
+    if (dtype == WASTE_ACT_BF16) {
+        send3<__nv_bfloat16>(o, map, n, N, row, z, v);
+    } else if (dtype == WASTE_ACT_F16) {
+        send3<__half>(o, map, n, N, row, z, v);
+    } else {
+        send3<float>(o, map, n, N, row, z, v);
+        send3<float>(o, map, n + 16, N, row, z, v + 16);
+    }
+}
+
 // A result in memory: written, or (kAdd) added to what is there.
 template <bool kAdd> struct Out {
-    CUtensorMap map; // over all of it; copies write 32 whole rows
+    CUtensorMap map;
     void *p;
-    int N, dtype, vec; // vec: rows of whole 16-byte pieces, for copies and blocks
-    cudaError_t set(void *out, int rows, int cols, int type) {
-        p = out, N = cols, dtype = type;
+    int M, N, dtype, vec; // M x N: a matrix; vec: rows of whole 16-byte pieces, for copies and blocks
+    cudaError_t set(void *out, int mats, int rows, int cols, int type) {
+        p = out, M = rows, N = cols, dtype = type;
         vec = (size_t)cols * dense::type_size(type) % 16 == 0;
-        return vec ? dense::store_map(&map, out, (int)dense::type_size(type), rows, cols) : cudaSuccess;
+        return vec ? store_map3(&map, out, type, mats, rows, cols) : cudaSuccess;
     }
     // what is there, to be added to
     struct Held {
@@ -157,15 +190,17 @@ template <bool kAdd> struct Out {
             halves(q, dtype == WASTE_ACT_BF16, base);
         }
     }
-    __device__ __forceinline__ void put(Out32 &o, int n, const float (&v)[32], const In &base) const {
-        const CUtensorMap *by = vec && o.rows >= 32 ? &map : nullptr;
-        if constexpr (kAdd) {
+    __device__ __forceinline__ void put(Out32 &o, const Spot &T, int n, const float (&v)[32], const In &base) const {
+        const int row = o.m - T.z * M; // of its matrix
+        if (!vec) {
+            dense::put32_as(dtype, o, nullptr, p, N, n, N, N % 4 == 0, kAdd, v);
+        } else if constexpr (kAdd) {
             float x[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = vec ? base[i] + v[i] : v[i];
-            dense::put32_as(dtype, o, by, p, N, n, N, vec || N % 4 == 0, !vec, x);
+            for (int i = 0; i < 32; ++i) x[i] = base[i] + v[i];
+            put3_as(dtype, o, &map, n, N, row, T.z, x);
         } else {
-            dense::put32_as(dtype, o, by, p, N, n, N, vec || N % 4 == 0, false, v);
+            put3_as(dtype, o, &map, n, N, row, T.z, v);
         }
     }
 };
