@@ -107,15 +107,17 @@ template <int kCG, bool kWmn, bool kAdd> struct RowsJob {
         int *first = reinterpret_cast<int *>(smem), *before = first + off.E + 1;
         off.read(first, before);
         if (threadIdx.x == 0) {
-            // few tiles: lower ones where they fill the GPU's rounds better (each costs what its rows of W need, and a
-            // bit); 16 experts of 1536 rows on 152 SMs: 192 tiles of 128 make two rounds, 256 of 96 two shorter ones
+            // few tiles: lower ones where they fill the GPU's rounds better (each costs what its rows of W and of x need);
+            // 16 experts of 1536 rows on 152 SMs: 192 tiles of 128 make two rounds, 256 of 96 two shorter ones.
+            // (Without x's rows in the cost, dx of 40 experts of 100 rows, 5120 to 1536, took 64: 196 us against 139.)
             int best = kTall;
             if (kCG == 1) {
                 int least = 0x7fffffff;
+                const int cols = max(16, (first[off.E] - first[0]) / max(1, before[off.E]));
                 for (int h = kBM; h >= (kWmn ? 64 : 32); h -= kWmn ? 64 : 32) {
                     const long long tiles = (long long)before[off.E] * ((N + h - 1) / h);
                     if (tiles > 16 * (int)gridDim.x) break; // many rounds: as they are
-                    const int t = (int)((tiles + gridDim.x - 1) / gridDim.x) * (h + 16);
+                    const int t = (int)((tiles + gridDim.x - 1) / gridDim.x) * (h + cols);
                     if (t < least) least = t, best = h;
                 }
             }
