@@ -6,16 +6,18 @@
 //
 // y and dx: the matrices are on the MMA's row side (128 rows, 256 for a pair of CTAs) and the expert's rows on its column
 // side, whose width is a multiple of 16 (32), so that little is computed for rows that are not there: an expert's
-// rows are cut into equal shares of at most 256 (64 where experts have fewer than 32 rows on average: deeper stages).  With the rows on the row side, in tiles of 256, a batch of uneven
-// popularity (126 to 2048 rows an expert) wastes 20 %.  The sums are turned round in shared memory on their way out.
+// rows are cut into equal shares of at most 256, or 64 (rows_plan).  With the rows on the row side, in tiles of 256, a
+// batch of uneven popularity (126 to 2048 rows an expert) wastes 20 %.  The sums are turned round in shared memory on
+// their way out.
 // Loads start at any row; what the last share of an expert loads of the next one's rows is never stored.
 // dW: its rows are what is summed over; those behind the expert's last are cleared in shared memory.
 //
 // Measured (bf16, k 7168, n 1536; popularity falling as 1 / rank^1.1; floors at 6.75 TB/s and 1.90 PFLOP/s): 16 rows of 16
 // experts 63 us (floor 52: W's 352 MB; 256 tiles of 96 x 16 on 152 SMs make two rounds, the second not full); 2048
-// rows over 384 experts 978 us = 7.1 TB/s of W; 32768 rows over 64 experts, back through down, 478 us cold and 531 in long
-// runs at 1.65 GHz (floor 379; cuBLAS takes 408 for one matrix of as many rows), their gradients 1143 to 1176 us (floor
-// 758; dx 500, the rest dW: 1.4 GB of it are written).
+// rows over 384 experts 975 us = 7.1 TB/s of W; 32768 rows over 64 experts, back through down, 478 us cold and 531 to 550 in long
+// runs at 1.65 GHz (floor 379; cuBLAS takes 408 for one matrix of as many rows), their gradients 1130 to 1190 us (floor
+// 758; dx 500, the rest dW: 1.4 GB of it are written).  40 matrices of 1536 x 5120 from 128 rows each are written at
+// 4.6 TB/s (137 us): the epilogue's chain (neither more places on the way out nor fewer rows change it).
 #include <type_traits>
 
 #include "tile_mma.cuh"

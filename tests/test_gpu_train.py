@@ -351,9 +351,11 @@ def test_grouped(sizes, k, n, t, before, behind):
     assert torch.equal(only, dx)
 
 
+# sizes whose tiles are wide, by pairs of CTAs ([700, ..]) and by single ones ([100, ..]), and narrow
 @pytest.mark.parametrize("t", [BF, HF])
 @pytest.mark.parametrize("sizes,k,n", [([37, 0, 130, 1, 16, 300, 63], 456, 328), ([257, 1, 640, 0, 319, 95], 328, 456),
-                                       ([1029], 520, 136), ([160] * 40, 72, 1000)])
+                                       ([1029], 520, 136), ([160] * 40, 72, 1000), ([700, 0, 1, 555, 944], 3336, 4008),
+                                       ([100] * 30 + [0, 37], 1304, 2008)])
 def test_grouped_exact(t, sizes, k, n):
     """Small whole numbers: every sum is exact, so a lost or a foreign k, row or column shows in the bits."""
     g = gen(1)
@@ -389,7 +391,7 @@ def test_grouped_many_experts():
     R.close(dw, v, e + R.rnd(v.abs() + e, BF), "dw")
 
 
-@pytest.mark.parametrize("sizes,k,n", [([5, 70, 9], 64, 40), ([333, 470, 131], 264, 200)])
+@pytest.mark.parametrize("sizes,k,n", [([5, 70, 9], 64, 40), ([333, 470, 131], 264, 200), ([500, 470, 431], 2600, 1000)])
 def test_grouped_not_finite(sizes, k, n):
     """An infinity or a NaN in a row or a matrix stays with its expert, in the sums over rows too."""
     g, x, dy, w, off = group_inputs(sizes, k, n, BF)
@@ -482,7 +484,7 @@ def distance(a, b):
 
 
 ORTHOS = [(1, 1, 1), (1, 1, 40), (3, 128, 320), (2, 320, 100), (2, 128, 321), (2, 65, 64), (2, 40, 1), (3, 8, 8), (1, 33, 70), (2, 70, 33), (8, 128, 256), (2, 256, 128), (1, 129, 513), (1, 513, 129),
-          (1, 264, 1032), (2, 1000, 328), (1, 520, 520), (1, 301, 2007)]
+          (1, 264, 1032), (2, 1000, 328), (1, 520, 520), (1, 301, 2007), (3, 201, 1004), (3, 1001, 200)]
 
 
 @pytest.mark.parametrize("count,rows,cols", ORTHOS)
