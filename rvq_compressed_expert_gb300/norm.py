@@ -32,7 +32,7 @@ class LayerNorm:
         self.weight, self.bias, self.eps = weight, bias, float(eps)
         self.d, self.dtype, self.device, self.index = d, t, dev, dev.index
         self._cfg = {}
-        self._ws = None
+        self._ws = {}  # the backward's workspace, once it is made
         B.waste_norm_workspace(self._config(t, t), 1)  # refuses a bad d or eps here
 
     def _config(self, x, y):
@@ -43,7 +43,7 @@ class LayerNorm:
         return c
 
     def __getstate__(self):  # configurations are made anew, a copy's workspace too
-        return {**self.__dict__, "_cfg": {}, "_ws": None}
+        return {**self.__dict__, "_cfg": {}, "_ws": {}}
 
     def _rows(self, t, name, T=None) -> int:
         """The row stride of a [T, d] tensor whose rows are contiguous."""
@@ -55,12 +55,14 @@ class LayerNorm:
 
     def reserve_backward(self):
         """Makes the backward's workspace (partial sums of the weight's and bias's gradients) now."""
-        if self._ws is None:
+        ws = self._ws.get("backward")
+        if ws is None:
             require(not torch.cuda.is_current_stream_capturing(),
                     "reserve the workspace before the capture (reserve_backward)")
             t = self.dtype  # its size does not grow past some rows
-            self._ws = Workspace(B.waste_norm_workspace(self._config(t, t), 1 << 30), self.device)
-        return self._ws
+            # of two host threads that come first, both take one's
+            ws = self._ws.setdefault("backward", Workspace(B.waste_norm_workspace(self._config(t, t), 1 << 30), self.device))
+        return ws
 
     def forward(self, x, y=None, mean=None, rstd=None, stream=None):
         """y [T, d] (fp32, bf16 or fp16; made as x if None) from x [T, d] of any of these types; rows may be strided.
@@ -109,6 +111,6 @@ class LayerNorm:
         if dw is None and db is None:
             B.waste_norm_backward(*args, None, h)
             return
-        ws = self._ws or self.reserve_backward()
+        ws = self._ws.get("backward") or self.reserve_backward()
         with ws.one:
             B.waste_norm_backward(*args, ws.lend(stream, h), h)

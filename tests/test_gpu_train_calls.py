@@ -423,3 +423,34 @@ def test_training_step():
         assert (wg[e].double() - want).norm() <= R.half(t) * want.norm() + 0.02 * far * o.norm()
     # the moved matrices serve the next step
     near(gate.forward(xs, off), R.grouped(xs, off, wg), t)
+
+
+def test_first_backwards_of_two_threads():
+    """The first backwards of an object, from two host threads at once on one stream given by its handle, which is not the
+    one that the workspace is made on: both take the same, and it stays."""
+    T, d = 300, 520
+    g = gen(7)
+    w, b, x, dy = randn(g, d), randn(g, d), randn(g, T, d), randn(g, T, d)
+    mean, rstd = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    n = LayerNorm(w, b)
+    n.forward(x, None, mean, rstd)
+    want = [torch.empty_like(x), torch.empty(d, device="cuda"), torch.empty(d, device="cuda")]
+    n.backward(dy, x, mean, rstd, *want)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(20):
+        n = LayerNorm(w, b)
+        got = [[torch.empty_like(t) for t in want] for _ in range(2)]
+        beside, gate = [None, None], threading.Barrier(2)
+        torch.cuda.synchronize()
+
+        def work(i):
+            gate.wait()
+            n.backward(dy, x, mean, rstd, *got[i], stream=s.cuda_stream)
+            beside[i] = torch.full((2432 * d,), 255, dtype=torch.uint8, device="cuda")  # what a dropped workspace left free
+
+        threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+        [t.start() for t in threads]
+        [t.join() for t in threads]
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for out in got for p, q in zip(out, want)) and all((t == 255).all() for t in beside)
