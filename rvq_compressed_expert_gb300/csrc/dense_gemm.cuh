@@ -21,8 +21,8 @@
 // kept) 168 to 175 us = 1.54 to 1.61 PFLOP/s, its gradients 347 to 358 us = 1.51 to 1.56 PFLOP/s (cuBLAS sustains
 // 1.71 on a square product); 4-bit 4096 x 7168 x 7168 68 to 71 us = 5.9 to 6.2 PFLOP/s, tensor pipe 63 % active.
 //
-// Waits are bounded: one that gives up (1.1 s) latches g_dense_timeout, which
-// waste_dense_status reports, and the CTA winds up.
+// Waits are bounded: one that gives up (a second or so; for a tile's product longer, by its k) latches
+// g_dense_timeout, which waste_dense_status reports, and the CTA winds up.
 #pragma once
 
 #include "dense.cuh"
@@ -102,11 +102,16 @@ template <int kForm, int kCG> __device__ __forceinline__ Tile tile_at(const Gemm
 // A warp's common answer, which the compiler knows to be common.
 __device__ __forceinline__ bool all(bool v) { return __all_sync(0xffffffffu, v); }
 
-// A wait for a whole tile's product: 1.1 s, and as much again for every million pieces of k (a
-// piece takes well under a microsecond).
+// A wait for a whole tile's product, by the clock: 1.1 s, and 2 us for each piece of k (one takes 0.2 to 0.4).  Polls do
+// not tell the time: one returns when another wait of the CTA ends, so beside the loop over k 2^18 of them were over
+// in 60 ms.
 __device__ __forceinline__ bool wait_tile(uint32_t bar, uint32_t parity, int pieces) {
-    for (int i = 0; i <= pieces >> 20; ++i)
-        if (tc::mbar_wait(bar, parity)) return true;
+    constexpr int kPolls = 1024;
+    if (tc::mbar_wait(bar, parity, kPolls)) return true;
+    const uint64_t end = tc::clock_ns() + 1100000000ull + 2000ull * (uint32_t)pieces;
+    do {
+        if (tc::mbar_wait(bar, parity, kPolls)) return true;
+    } while (tc::clock_ns() < end);
     return false;
 }
 

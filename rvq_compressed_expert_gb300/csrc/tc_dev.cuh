@@ -25,8 +25,10 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t addr, uint32_t parity) {
                  : "memory");
     return ok != 0;
 }
-// Bounded wait for the phase of the given parity: false after `polls` failed ones (the default: 1.1 s; a
-// poll suspends the thread for up to 4.0 us, measured on a barrier that nobody arrives at).
+// Bounded wait for the phase of the given parity: false after `polls` failed ones.  A poll suspends the thread for up
+// to 4.0 us (measured on a barrier that nobody arrives at), and returns earlier when another wait of the CTA ends: the
+// default is 1.1 s in a CTA where nothing else happens, 60 ms beside one that ends every 0.2 us.  So it is for what
+// takes microseconds (one copy, one piece of k).
 constexpr int kWaitPolls = 1 << 18;
 __device__ __forceinline__ bool mbar_wait(uint32_t addr, uint32_t parity, int polls = kWaitPolls) {
     for (int it = 0; it < polls; ++it) {
@@ -34,6 +36,12 @@ __device__ __forceinline__ bool mbar_wait(uint32_t addr, uint32_t parity, int po
         if (it > 64) __nanosleep(128);
     }
     return false;
+}
+
+__device__ __forceinline__ uint64_t clock_ns() {
+    uint64_t t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
 }
 
 __device__ __forceinline__ void mbar_arrive(uint32_t addr) {

@@ -78,3 +78,10 @@ def test_loads_ahead_of_the_wait_see_what_is_complete():
     for name in ("load_stream", "load_stream8"):
         body = re.search(name + r"\(const \w+ \*p\) \{.*?\n\}", text, flags=re.S).group(0)
         assert "ld.relaxed.gpu.global" in body
+
+
+def test_a_wait_for_a_tile_goes_by_the_clock():
+    """Polls return early beside other waits of the CTA: a product over many pieces of k is waited for by time."""
+    body = re.search(r"bool wait_tile\(.*?\n\}", code(os.path.join(CSRC, "dense_gemm.cuh")), flags=re.S).group(0)
+    assert re.search(r"end = tc::clock_ns\(\) \+ \d+ull \+ 2000ull \* \(uint32_t\)pieces;", body)
+    assert re.search(r"do \{\s*if \(tc::mbar_wait\([^;]*\)\) return true;\s*\} while \(tc::clock_ns\(\) < end\);\s*return false;", body)
