@@ -403,7 +403,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
                     int steps = 4;
                     if (J::kMask && kb + 1 == T.pieces && T.left < 64) {
                         steps = (T.left + 15) >> 4;
-                        if (!all(wait_cluster(bar_mask + 8 * st, masked >> st & 1))) { // cleared, in both CTAs
+                        // cleared, in both CTAs: these are a piece behind at most, the pieces before have come from both
+                        if (!all(wait_cluster(bar_mask + 8 * st, masked >> st & 1))) {
                             ok = false;
                             break;
                         }
@@ -442,18 +443,20 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
         if (J::kMask) {
             // ---- clears what is not the tile's in this CTA's part of a stage as soon as it is there, often ahead of the MMAs
             // before it, and says so to the issuer
-            int st = 0;
-            uint32_t used = 0; // a bit a stage: the parity of the barrier that it lands on
+            int st = 0, pieces = 0; // since the last wait: it takes as long as all of them
+            uint32_t used = 0;      // a bit a stage: the parity of the barrier that it lands on
             for (int t = tile0; t < tiles; t += step) {
                 const Spot T = job.spot(mine, t);
                 if (T.pieces == 0) continue;
                 const int last = (st + T.pieces - 1) % P.stages;
                 st = (st + T.pieces) % P.stages;
+                pieces += T.pieces;
                 if (T.left == 64) continue;
-                if (!all(tc::mbar_wait(bar_land + 8 * last, used >> last & 1))) {
+                if (!all(dense::wait_tile(bar_land + 8 * last, used >> last & 1, pieces))) {
                     if (lane == 0) *abort_flag = 1;
                     break;
                 }
+                pieces = 0;
                 used ^= 1u << last;
                 mask_rows(smem_raw + last * stage_bytes, T.left, (T.left + 15) & ~15, (int)((a_bytes + b_bytes) >> 13), lane);
                 if (lane == 0) {

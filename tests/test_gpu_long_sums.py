@@ -69,3 +69,45 @@ def test_dense_gradients_of_many_tokens():
     assert torch.equal(dw[0].double(), (p * r).T @ q)
     assert torch.equal(dw[1].double(), (64 * p).T @ q)
     assert torch.equal(dw[2].double(), p.T @ (64 * r))
+
+
+@pytest.mark.parametrize("rows", [(1 << 25) - 37, (1 << 30) - 37])
+def test_grouped_gradient_of_many_rows(rows):
+    """One expert's dW: a tile of a tenth of a second, and of four, whose last piece ends inside rows of no expert."""
+    c, behind = 8, 37
+    g = gen(3)
+    x, dy = (torch.zeros(rows + behind, c, dtype=BF, device="cuda") for _ in range(2))
+    at = places(g, rows)
+    for v in (x, dy):
+        v[at] = whole(g, len(at), c)
+        v[rows:] = 3.0  # nobody's
+    off = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    w = whole(g, 1, c, c)
+    m, dw = GroupedLinear(w), torch.empty(1, c, c, device="cuda")
+    m.backward(dy, x, off, None, dw)
+    B.waste_dense_status()
+    assert torch.equal(dw[0].double(), dy[at].double().T @ x[at].double())
+    y = torch.full((rows + behind, c), 7.0, dtype=BF, device="cuda")
+    m.forward(x, off, y)
+    assert torch.equal(y[at].double(), x[at].double() @ w[0].double().T) and (y[rows:] == 7).all()
+
+
+def test_grouped_gradient_behind_whole_pieces():
+    """Experts of whole pieces of 64 rows, which need no clearing, before one that does, on the same SMs."""
+    c, many = 8, (1 << 18) * 64
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    sizes = [many] + [0] * (sms - 1) + [100] + [64] * (sms - 1) + [99]
+    off = torch.tensor([0] + sizes, device="cuda").cumsum(0).to(torch.int32)
+    rows = int(off[-1])
+    g = gen(4)
+    x, dy = (torch.zeros(rows, c, dtype=BF, device="cuda") for _ in range(2))
+    at = torch.cat([places(g, many), torch.arange(many, rows, device="cuda")])
+    for v in (x, dy):
+        v[at] = whole(g, len(at), c)
+    dw = torch.empty(len(sizes), c, c, device="cuda")
+    GroupedLinear(whole(g, len(sizes), c, c)).backward(dy, x, off, None, dw)
+    B.waste_dense_status()
+    ends = off.tolist()
+    for e in range(len(sizes)):
+        in_e = at[(at >= ends[e]) & (at < ends[e + 1])] if sizes[e] == many else torch.arange(ends[e], ends[e + 1], device="cuda")
+        assert torch.equal(dw[e].double(), dy[in_e].double().T @ x[in_e].double()), e

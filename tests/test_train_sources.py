@@ -48,3 +48,15 @@ def test_waits_are_bounded():
             around = text[max(0, m.start() - 400):m.start()]
             assert "kWaitPolls" in around, path
         assert not re.search(r"while\s*\(\s*(?:!|true|1)", text), path
+
+
+def test_waits_for_many_pieces_scale_with_them():
+    """A tile's sum may be over 2^24 pieces of k, seconds of work: who waits from its start for its last piece, or for its
+    sums, waits as much longer (wait_tile); the plain wait is for what one piece takes."""
+    text = code(os.path.join(CSRC, "tile_mma.cuh"))
+    waits = re.findall(r"(mbar_wait|wait_tile|wait_cluster)\((bar_\w+)([^;{]*)", text)
+    long = {b for f, b, _ in waits if f == "wait_tile"}
+    assert long == {"bar_accf", "bar_land"}
+    for f, b, rest in waits:  # the loader's last waits, once it gave up, are for copies on their way
+        assert f == "wait_tile" or b not in long or "land >> i" in rest, (f, b)
+    (clearing,) = re.findall(r"pieces \+= T\.pieces;\s*if \(T\.left == 64\) continue;\s*if \(!all\(dense::wait_tile\(bar_land[^;]*, pieces\)\)\)", text)
