@@ -13,11 +13,11 @@ _FLOATS = (torch.float32, torch.bfloat16, torch.float16)
 
 class NewtonSchulz:
     """For stacks of `count` matrices [rows, cols]: X = G / |G|, then `steps` times X <- a X + (b A + c A^2) X with
-    A = X X^T on the short side; coefficients are a, b and c.  The workspace belongs to this object: calls of one object must not run at
-    the same time on two streams (from several host threads on one stream they may), two captured graphs that may
-    replay at the same time need an object each, and an object outlives the graphs that hold its calls.  stream: a
-    torch.cuda.Stream, an integer handle (then the object must outlive the call) or None for the current stream;
-    ordering the tensors' use between streams is the caller's."""
+    A = X X^T on the short side; coefficients are a, b and c.  The workspace belongs to this object, which is not made
+    during a capture: calls of one object must not run at the same time on two streams (from several host threads on one
+    stream they may), two captured graphs that may replay at the same time need an object each, and an object outlives
+    the graphs that hold its calls.  stream: a torch.cuda.Stream, an integer handle (then the object must outlive the
+    call) or None for the current stream; ordering the tensors' use between streams is the caller's."""
 
     def __init__(self, count: int, rows: int, cols: int, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), device="cuda"):
         dev = torch.device(device)
@@ -28,7 +28,9 @@ class NewtonSchulz:
         self.count, self.rows, self.cols, self.steps = int(count), int(rows), int(cols), int(steps)
         self.coefficients, self.device, self.index = tuple(map(float, coefficients)), dev, dev.index
         self.cfg = B.waste_ortho_config(B.ABI_VERSION, self.count, self.rows, self.cols, self.steps, *self.coefficients)
-        self._ws = Workspace(B.waste_ortho_workspace(self.cfg), dev)
+        need = B.waste_ortho_workspace(self.cfg)
+        require(not torch.cuda.is_current_stream_capturing(), "make the object, and its workspace with it, before the capture")
+        self._ws = Workspace(need, dev)
 
     def orthogonalize(self, g, out=None, scale: float = 1.0, mode: int = 0, stream=None):
         """out [count, rows, cols] = (mode 0; bf16, made if None) or += (mode 1; fp32, bf16 or fp16: a weight and its

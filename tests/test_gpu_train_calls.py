@@ -454,3 +454,16 @@ def test_first_backwards_of_two_threads():
         [t.join() for t in threads]
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for out in got for p, q in zip(out, want)) and all((t == 255).all() for t in beside)
+
+
+def test_newton_schulz_is_not_made_in_a_capture():
+    x, refusal = torch.ones(4, device="cuda"), None
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        try:
+            NewtonSchulz(1, 200, 300)
+        except B.WasteError as e:
+            refusal = e
+        x.add_(1)
+    assert refusal is not None and refusal.status == -1
+    del gr

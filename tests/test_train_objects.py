@@ -8,7 +8,7 @@ import torch
 
 from rvq_compressed_expert_gb300 import _build
 from rvq_compressed_expert_gb300 import binding as B
-from rvq_compressed_expert_gb300 import norm
+from rvq_compressed_expert_gb300 import norm, ortho
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -46,3 +46,16 @@ def test_first_backwards_of_two_threads_share_a_workspace(monkeypatch):
     [t.join() for t in threads]
     assert len(got) == 2 and got[0] is got[1] is n.reserve_backward()
     assert got[0].nbytes == B.waste_norm_workspace(n._config(torch.float32, torch.float32), 1 << 30)
+
+
+def test_newton_schulz_is_not_made_in_a_capture(monkeypatch):
+    """Its workspace would belong to the graph."""
+    made = []
+    monkeypatch.setattr(ortho, "Workspace", lambda *a: made.append(a))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    with pytest.raises(B.WasteError) as ei:
+        ortho.NewtonSchulz(1, 200, 300, device="cuda:0")
+    assert ei.value.status == -1 and "capture" in ei.value.message and not made
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    ortho.NewtonSchulz(1, 200, 300, device="cuda:0")
+    assert len(made) == 1
