@@ -7,6 +7,7 @@ import pytest
 
 from rvq_compressed_expert_gb300 import _build
 from rvq_compressed_expert_gb300 import binding as B
+from tests import train_ref as R
 
 HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "waste_train.h")
 A = 1 << 40  # an address that a refused call never reads
@@ -225,3 +226,13 @@ def test_sizes_past_32_bits(far):
     refused(B.waste_norm_workspace, norm(), far)
     refused(gforward, rows=far)
     refused(gbackward, rows=far)
+
+
+def test_ortho_ways():
+    """Which way each of the GPU tests' stacks takes: its workspace's size tells.  Wide and tall, one matrix and several,
+    both sizes of tiles, shares and all at once are among them."""
+    for (count, rows, cols), (side, slices) in R.ORTHO_WAYS.items():
+        assert B.waste_ortho_workspace(ortho(count, rows, cols)) == R.ortho_workspace(count, rows, cols, side, slices), (count, rows, cols)
+    ways = {(rows > cols, count > 1, side, slices > 0) for (count, rows, cols), (side, slices) in R.ORTHO_WAYS.items()}
+    assert {(tall, many, side, True) for tall in (False, True) for many in (False, True) for side in (128, 256)} <= ways
+    assert {(tall, True, 256, False) for tall in (False, True)} <= ways

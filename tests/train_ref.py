@@ -122,3 +122,25 @@ def dense_distance(a, b):
     """Norm of the difference over the norm of b (of a where b is zero)."""
     n = b.norm()
     return float((a.double() - b).norm() / n) if n > 0 else float(a.double().norm())
+
+
+# Stacks (count, rows, cols) past the small kernel, and the way that A is made on: tiles of side x side, and shares of the long
+# side whose sums are added up by a launch of their own (0: all tiles at once).  test_train_abi holds this against the
+# library's workspaces, so that a change of the rule cannot take a way's cases away unseen.
+ORTHO_WAYS = {(1, 301, 2007): (256, 8), (1, 2007, 301): (256, 8), (2, 301, 2007): (256, 4), (2, 2007, 301): (256, 4),
+              (3, 301, 3007): (256, 4), (3, 3001, 304): (256, 4), (1, 520, 5000): (256, 8), (1, 5003, 520): (256, 8),
+              (1, 16, 7168): (128, 16), (1, 7168, 16): (128, 16), (1, 4000, 100): (128, 16), (3, 100, 4001): (128, 16),
+              (4, 4000, 100): (128, 16), (2, 64, 1500): (128, 12), (2, 1500, 65): (128, 12), (2, 520, 136): (256, 0),
+              (2, 200, 520): (256, 0), (2, 330, 131): (256, 0), (1, 513, 129): (256, 0), (4, 2007, 301): (256, 0)}
+
+
+def ortho_workspace(count, rows, cols, side, slices):
+    """Bytes of a call's workspace, made that way: X in three parts, A and B, B's diagonal, sums of squares, A's partial
+    sums."""
+    def take(n):
+        return (n + 255) // 256 * 256
+
+    m = min(rows, cols)
+    ldx, ldm, across = (cols + 7) // 8 * 8, (m + 7) // 8 * 8, (m + side - 1) // side
+    return (3 * take(count * rows * ldx * 2) + 2 * take(count * m * ldm * 2) + take(count * ldm * 4) + take(count * 512 * 3 * 4)
+            + take(count * (across * (across + 1) // 2) * slices * side * side * 4))
