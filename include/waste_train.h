@@ -19,6 +19,10 @@
 extern "C" {
 #endif
 
+/* Test aid, as waste_dense_debug_wait: the wait is latched as one of the layer norm's (unit 0), of the products grouped by
+ * expert (1) or of the orthogonalised updates (2). */
+int waste_train_debug_wait(int32_t unit, int32_t polls, int32_t arrive, waste_stream_t stream);
+
 /* ---- layer norm -------------------------------------------------------------------------
  * Over each row of d >= 1 values: mu = mean(x), r = 1 / sqrt(mean((x - mu)^2) + eps),
  *   y = (x - mu) r w + b

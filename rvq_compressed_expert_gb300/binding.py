@@ -45,7 +45,7 @@ EXPORTED_DENSE = ["waste_dense_status", "waste_dense_debug_wait", "waste_ffn_wor
                   "waste_mx4_ffn_forward"]
 
 # include/waste_train.h
-EXPORTED_TRAIN = ["waste_norm_forward", "waste_norm_workspace", "waste_norm_backward", "waste_group_forward",
+EXPORTED_TRAIN = ["waste_train_debug_wait", "waste_norm_forward", "waste_norm_workspace", "waste_norm_backward", "waste_group_forward",
                   "waste_group_backward", "waste_ortho_workspace", "waste_ortho_update"]
 
 
@@ -199,6 +199,7 @@ def load(path: str = LIB_PATH):
     lib.waste_mx4_ffn_workspace.argtypes = [mx4, i32, ctypes.POINTER(sz)]
     lib.waste_mx4_ffn_forward.argtypes = [mx4, vp, i32, i32, vp, i32, i32, vp, sz, vp]
     norm, group, ortho = (ctypes.POINTER(c) for c in (waste_norm_config, waste_group_config, waste_ortho_config))
+    lib.waste_train_debug_wait.argtypes = [i32, i32, i32, vp]
     lib.waste_norm_forward.argtypes = [norm, vp, i64, i32, vp, vp, vp, i64, vp, vp, vp]
     lib.waste_norm_workspace.argtypes = [norm, i32, ctypes.POINTER(sz)]
     lib.waste_norm_backward.argtypes = [norm, vp, i64, vp, i64, i32, vp, vp, vp, vp, i64, vp, vp, i32, i32, vp, sz, vp]
@@ -499,6 +500,11 @@ def waste_mx4_ffn_forward(cfg, d_x, x_dtype, T, d_out, out_dtype, mode, workspac
     rc = (_lib or load()).waste_mx4_ffn_forward(ctypes.byref(cfg), _ptr(d_x), x_dtype, T, _ptr(d_out), out_dtype, mode,
                                                 workspace.data_ptr(), workspace.numel(), _stream(stream))
     return rc and _check(rc)
+
+
+def waste_train_debug_wait(unit, polls=0, arrive=0, stream=None):
+    """Test aid for waste_dense_status: a wait of unit 0 (norm), 1 (grouped) or 2 (ortho) that gives up after `polls` polls."""
+    return _check(load().waste_train_debug_wait(unit, polls, arrive, _stream(stream)))
 
 
 def waste_norm_forward(cfg, d_x, ld_x, T, d_w, d_b, d_y, ld_y, d_mean=None, d_rstd=None, stream=None):

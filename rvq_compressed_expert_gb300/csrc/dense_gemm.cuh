@@ -118,6 +118,10 @@ __device__ __forceinline__ bool wait_tile(uint32_t bar, uint32_t parity, int pie
 // One word in each translation unit that has kernels; read_and_clear_timeout reads its own.
 static __device__ uint32_t g_dense_timeout;
 
+// Its address, for the test aids.
+static inline cudaError_t timeout_word(uint32_t **word) {
+    return cudaGetSymbolAddress(reinterpret_cast<void **>(word), g_dense_timeout);
+}
 static inline cudaError_t read_and_clear_timeout(uint32_t *out) {
     uint32_t v = 0;
     cudaError_t e = cudaMemcpyFromSymbol(&v, g_dense_timeout, sizeof v);

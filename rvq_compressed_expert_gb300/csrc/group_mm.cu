@@ -371,6 +371,7 @@ cudaError_t launch_group_dw(const Group &G, const void *dy, const void *x, void 
     return W.pair ? (add ? go(kTwo, kYes) : go(kTwo, kNo)) : add ? go(kOne, kYes) : go(kOne, kNo);
 }
 
+cudaError_t group_word(uint32_t **word) { return dense::timeout_word(word); }
 cudaError_t group_status(uint32_t *timeout, uint32_t *offsets) {
     cudaError_t e = dense::read_and_clear_timeout(timeout);
     uint32_t v = 0;

@@ -341,21 +341,6 @@ template <class X, bool kWhole> struct Ring {
 __host__ __device__ constexpr uint32_t ring_pitch(int d, uint32_t size, bool whole) {
     return (d * size + 15) / 16 * 16 + (whole ? 0 : kRingFront + kRingBack);
 }
-// A wait gives up after 1.1 s: then none is waited for any more, and waste_dense_status reports it.
-__device__ __forceinline__ void wait_row(uint32_t bar, uint32_t parity, volatile uint32_t *gave_up) {
-    if (*gave_up) return;
-    if (!tc::mbar_wait(bar, parity)) {
-        *gave_up = 1;
-        atomicOr(&g_norm_timeout, 1u);
-    }
-}
-
-// Behind a wait that gave up: time for copies on their way to land before the CTA goes.
-__device__ __forceinline__ void settle(volatile uint32_t *gave_up) {
-    if (*gave_up)
-        for (int i = 0; i < 64; ++i) __nanosleep(1 << 14);
-}
-
 // Few rows: a row a group, straight from memory, w and b held too, for all loads to be on their way at once.
 template <class X, class Y, int V>
 __global__ void __launch_bounds__(kHeldThreads) forward_few_kernel(const NormFwd P, int gw) {
@@ -437,7 +422,7 @@ __global__ void __launch_bounds__(kStreamThreads) forward_stream_kernel(const No
         float2 x[kStreamHeld / 2], s = both(0.f);
         const int before = V == 8 ? 0 : before16(static_cast<Y *>(P.y.p) + (int64_t)row * P.y.ld);
         const auto column = [&](int i) { return (i * gt + t) * 8 - before; };
-        wait_row(bar0 + 8 * turn, phase, &gave_up);
+        wait_row(bar0 + 8 * turn, phase, &gave_up, &g_norm_timeout);
         const uint32_t from = ring.place(row, turn);
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
@@ -577,7 +562,7 @@ __global__ void __launch_bounds__(kHeldThreads) backward_held_kernel(const NormB
         const uint32_t first = turn;
 #pragma unroll
         for (int q = 0; q < R; ++q) {
-            if (row + q * step < P.T) wait_row(bar0 + 8 * turn, phase, &gave_up);
+            if (row + q * step < P.T) wait_row(bar0 + 8 * turn, phase, &gave_up, &g_norm_timeout);
             if (++turn == (uint32_t)deep) turn = 0, phase ^= 1;
         }
         // x - mu and dy of row q, eight columns from col on, zeros past the row's ends
@@ -960,6 +945,7 @@ cudaError_t launch_norm_backward(const NormBwd &P, cudaStream_t s) {
     });
 }
 
+cudaError_t norm_word(uint32_t **word) { return cudaGetSymbolAddress(reinterpret_cast<void **>(word), g_norm_timeout); }
 cudaError_t norm_timeout(uint32_t *out) {
     uint32_t v = 0;
     cudaError_t e = cudaMemcpyFromSymbol(&v, g_norm_timeout, sizeof v);

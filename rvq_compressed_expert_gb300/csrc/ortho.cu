@@ -765,6 +765,7 @@ cudaError_t launch_ortho(const Ortho &P, cudaStream_t s) {
     if (P.add) return tall ? steps<true, true>(P, W, s) : steps<false, true>(P, W, s);
     return tall ? steps<true, false>(P, W, s) : steps<false, false>(P, W, s);
 }
+cudaError_t ortho_word(uint32_t **word) { return dense::timeout_word(word); }
 cudaError_t ortho_timeout(uint32_t *out) { return dense::read_and_clear_timeout(out); }
 
 } // namespace train

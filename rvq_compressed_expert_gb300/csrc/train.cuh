@@ -110,6 +110,31 @@ cudaError_t launch_norm_forward(const NormFwd &P, cudaStream_t s);
 cudaError_t launch_norm_backward(const NormBwd &P, cudaStream_t s);
 cudaError_t norm_timeout(uint32_t *out);
 
+// Where each unit's kernels say that a wait gave up; and a CTA that lets one do so, by the unit's own wait (the norm's:
+// wait_row, three of them and settle), for waste_train_debug_wait.
+cudaError_t norm_word(uint32_t **word);
+cudaError_t group_word(uint32_t **word);
+cudaError_t ortho_word(uint32_t **word);
+cudaError_t launch_debug_wait(uint32_t *word, bool rows, int polls, int arrive, cudaStream_t s);
+
+#ifdef __CUDACC__
+// The norm's wait for a row: one that gives up (1.1 s at most) says so in *word, and then none of the CTA's is waited for
+// any more.
+__device__ __forceinline__ void wait_row(uint32_t bar, uint32_t parity, volatile uint32_t *gave_up, uint32_t *word,
+                                         int polls = tc::kWaitPolls) {
+    if (*gave_up) return;
+    if (!tc::mbar_wait(bar, parity, polls)) {
+        *gave_up = 1;
+        atomicOr(word, 1u);
+    }
+}
+// Behind a wait that gave up: time for copies on their way to land before the CTA goes.
+__device__ __forceinline__ void settle(volatile uint32_t *gave_up) {
+    if (*gave_up)
+        for (int i = 0; i < 64; ++i) __nanosleep(1 << 14);
+}
+#endif
+
 // A launch that may begin while the kernel before it in the stream ends; the kernel waits for that one itself
 // (tc::grid_wait_release) before it touches memory.
 template <class... P, class... A>

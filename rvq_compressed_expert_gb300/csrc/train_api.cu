@@ -285,4 +285,16 @@ int waste_ortho_update(const waste_ortho_config *cfg, const void *d_g, int32_t g
     return done(launch_ortho(P, reinterpret_cast<cudaStream_t>(stream)), "orthogonalised update");
 }
 
+int waste_train_debug_wait(int32_t unit, int32_t polls, int32_t arrive, waste_stream_t stream) {
+    const NvtxRange nvtx_range(__func__);
+    if (unit < 0 || unit > 2) return fail(WASTE_EINVAL, "unit = %d outside [0, 2]", unit);
+    if (polls < 0 || polls > tc::kWaitPolls) return fail(WASTE_EINVAL, "polls = %d outside [0, 2^18]", polls);
+    if (int rc = check_flag(arrive, "arrive")) return rc;
+    uint32_t *word = nullptr;
+    cudaError_t e = unit == 0 ? norm_word(&word) : unit == 1 ? group_word(&word) : ortho_word(&word);
+    if (e == cudaSuccess)
+        e = train::launch_debug_wait(word, unit == 0, polls ? polls : tc::kWaitPolls, arrive, reinterpret_cast<cudaStream_t>(stream));
+    return done(e, "wait kernel");
+}
+
 } // extern "C"

@@ -236,3 +236,8 @@ def test_ortho_ways():
     ways = {(rows > cols, count > 1, side, slices > 0) for (count, rows, cols), (side, slices) in R.ORTHO_WAYS.items()}
     assert {(tall, many, side, True) for tall in (False, True) for many in (False, True) for side in (128, 256)} <= ways
     assert {(tall, True, 256, False) for tall in (False, True)} <= ways
+
+
+def test_debug_wait_refusals():
+    for a in ((-1, 64, 0), (3, 64, 0), (0, -1, 0), (1, (1 << 18) + 1, 0), (2, 64, 2), (2, 64, -1)):
+        refused(B.waste_train_debug_wait, *a, stream=0)
