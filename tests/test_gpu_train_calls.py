@@ -9,6 +9,7 @@ import torch
 
 from rvq_compressed_expert_gb300 import binding as B
 from rvq_compressed_expert_gb300 import synth
+from rvq_compressed_expert_gb300.bank import TieredStack
 from rvq_compressed_expert_gb300.grouped import GroupedLinear
 from rvq_compressed_expert_gb300.layer import MoELayer
 from rvq_compressed_expert_gb300.norm import LayerNorm
@@ -467,3 +468,38 @@ def test_newton_schulz_is_not_made_in_a_capture():
         x.add_(1)
     assert refusal is not None and refusal.status == -1
     del gr
+
+
+@pytest.mark.parametrize("lookahead", [0, 2])
+@pytest.mark.parametrize("tokens", [1, 3])
+def test_banked_stack_with_norms(tokens, lookahead):
+    """Layers whose records come through an HBM cache that evicts, with norms of their own: the resident stack's bits."""
+    w = workload(tokens)
+    g = gen(51)
+    norms = [LayerNorm(1 + randn(g, 256, scale=0.2), randn(g, 256, scale=0.1)), None, LayerNorm((1 + randn(g, 256, scale=0.2)).to(BF))]
+    hidden = [randn(g, tokens, 256) for _ in range(3)]
+
+    def run(layers, **k):
+        main, side, outs = torch.cuda.Stream(), torch.cuda.Stream(), []
+        stack = DecodeStack(layers, tokens, **k)
+        torch.cuda.synchronize()
+        for h in hidden:
+            out = stack.run(h, lookahead, main, side)
+            torch.cuda.synchronize()
+            outs.append(out.clone())
+        return outs
+
+    layers = [MoELayer(w, 1, L, "cuda") for L in range(3)]
+    try:
+        want, plain = run(layers, norm=norms), run(layers)
+    finally:
+        for m in layers:
+            m.close()
+    ts = TieredStack(w, 1, 3, 7)
+    try:
+        got = run(ts.layers, banked=True, norm=norms)
+        assert all(torch.equal(a, b) and not torch.equal(a, c) for a, b, c in zip(got, want, plain))
+        for m in ts.layers:
+            m.stats()
+    finally:
+        ts.close()
