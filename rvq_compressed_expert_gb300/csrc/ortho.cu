@@ -432,8 +432,7 @@ __global__ void __launch_bounds__(kSmallThreads)
         tc::mbar_init(bar, 1);
         tc::mbar_init_fence();
     }
-    const uint32_t columns = slabs <= 2 ? 256 : kTmemCols; // two CTAs an SM where they fit
-    if (warp == 0) tc::tmem_alloc(tc::smem_u32(&tmem_slot), columns);
+    if (warp == 0) tc::tmem_alloc(tc::smem_u32(&tmem_slot), kTmemCols); // one CTA an SM: by its registers, too
     tc::grid_wait_release();
 
     // ---- G, by pieces of 8 of X's columns: thread t holds t, t + 512, .. in registers, all asked for at once
@@ -616,7 +615,7 @@ __global__ void __launch_bounds__(kSmallThreads)
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (warp == 0) tc::tmem_dealloc(tmem, columns);
+    if (warp == 0) tc::tmem_dealloc(tmem, kTmemCols);
 }
 
 template <class T, bool kTall> cudaError_t small(const Ortho &P, cudaStream_t s) {
