@@ -850,7 +850,10 @@ bool whole_rows(const Rows &r, int dtype, int T) {
     return aligned16(r.p) && (T < 2 || r.ld * (int64_t)dense::type_size(dtype) % 16 == 0);
 }
 
-// Rows of `bytes` a group keeps on their way beside `rest` bytes in shared memory: at least the two in work.
+// Rows of `bytes` a group keeps on their way beside `rest` bytes in shared memory, those in work among them.  In the backward
+// twice kRowsAtOnce and more, which the order of its places needs (fp32: rows of x and dy are 64 KB for 16 warps, beside 32 KB
+// of w).  In the forward one and more, read to registers before its place takes the next (fp32: 24 warps' rows are up to
+// 96 KB beside up to 64 KB of w and b, so rows of 4024 to 4096, 5640 to 6144 and 7048 values on have none ahead).
 int rows_ahead(size_t bytes, size_t rest, int groups) {
     const size_t n = (kHeldSmem - rest) / (bytes * groups);
     return n > kDeepMost ? kDeepMost : (int)n;
@@ -880,8 +883,7 @@ cudaError_t launch_norm_forward(const NormFwd &P, cudaStream_t s) {
                 static SmemAttr attr;
                 const auto kernel = forward_stream_kernel<X, Y, V>;
                 const int gw = group_warps(eights(P.d, V == 8), kStreamHeld / 8);
-                int groups = kStreamThreads / 32 / gw;
-                if (groups > 16 && gw > 1) groups = 16; // barriers
+                const int groups = kStreamThreads / 32 / gw; // 12 at most where a group has barriers
                 const size_t row = ring_pitch(P.d, sizeof(X), V == 8), rest = V == 8 ? (size_t)P.d * 8 : (size_t)eighths(P.d) * 64;
                 const int deep = rows_ahead(row, rest, groups), smem = (int)(deep * groups * row + rest);
                 const cudaError_t e = ensure_smem(attr, reinterpret_cast<const void *>(kernel), smem);
