@@ -83,32 +83,6 @@ def _far(*sizes):
     raise WasteError(-1, f"sizes {sizes}: at most 2^30")
 
 
-def _near(fields, named):
-    """Refuses a configuration whose d or f (its second and third field) do not fit 32 bits."""
-    d, f = (fields[i] if len(fields) > i else named.get(n, 0) for i, n in ((1, "d"), (2, "f")))
-    if not -1 <= (d | f) >> 31 <= 0:
-        _far(d, f)
-
-
-class waste_ffn_config(ctypes.Structure):
-    _fields_ = [("abi_version", ctypes.c_uint32), ("d", ctypes.c_int32), ("f", ctypes.c_int32),
-                ("dtype", ctypes.c_int32)]
-
-    def __init__(self, *fields, **named):
-        _near(fields, named)
-        super().__init__(*fields, **named)
-
-
-class waste_mx4_ffn_config(ctypes.Structure):
-    _fields_ = [("abi_version", ctypes.c_uint32), ("d", ctypes.c_int32), ("f", ctypes.c_int32)] + [
-        (n, ctypes.c_void_p) for n in ("d_gate_codes", "d_gate_scales", "d_up_codes", "d_up_scales",
-                                       "d_down_codes", "d_down_scales")]
-
-    def __init__(self, *fields, **named):
-        _near(fields, named)
-        super().__init__(*fields, **named)
-
-
 class _SizedConfig(ctypes.Structure):
     """A configuration whose 32-bit integers are refused where they do not fit, not cut."""
 
@@ -118,6 +92,17 @@ class _SizedConfig(ctypes.Structure):
             if c is ctypes.c_int32 and not -1 <= values.get(n, 0) >> 31 <= 0:
                 _far(values[n])
         super().__init__(*fields, **named)
+
+
+class waste_ffn_config(_SizedConfig):
+    _fields_ = [("abi_version", ctypes.c_uint32), ("d", ctypes.c_int32), ("f", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+class waste_mx4_ffn_config(_SizedConfig):
+    _fields_ = [("abi_version", ctypes.c_uint32), ("d", ctypes.c_int32), ("f", ctypes.c_int32)] + [
+        (n, ctypes.c_void_p) for n in ("d_gate_codes", "d_gate_scales", "d_up_codes", "d_up_scales",
+                                       "d_down_codes", "d_down_scales")]
 
 
 class waste_norm_config(_SizedConfig):
