@@ -28,8 +28,10 @@ int waste_train_debug_wait(int32_t unit, int32_t polls, int32_t arrive, waste_st
  *   y = (x - mu) r w + b
  * and, with xh = (x - mu) r and g = dy w,
  *   dx = r (g - mean(g) - xh mean(g xh)),  dw = sum over rows of dy xh,  db = sum over rows of dy.
- * Statistics and sums are fp32; y, dx, dw and db are rounded once.  Rows are contiguous, ld elements apart
- * (ld >= d), pointers aligned to their type: 16-byte aligned rows of d % 8 == 0 values take the quick way. */
+ * Statistics and sums are fp32; y, dx, dw and db are rounded once.  So a row's sum and its sum of squares about the
+ * mean have to lie in fp32's range: where the squares leave it (distances of 1.8e19 / sqrt(d) and more) r is 0 and y is b.
+ * Rows are contiguous, ld elements apart (ld >= d), pointers aligned to their type: 16-byte aligned rows of d % 8 == 0
+ * values take the quick way. */
 typedef struct {
     uint32_t abi_version; /* must equal WASTE_MOE_ABI_VERSION */
     int32_t d;
@@ -93,8 +95,10 @@ int waste_group_backward(const waste_group_config *cfg, const void *d_dy, const 
  * which moves every singular value of G towards 1 and keeps its singular vectors.  A zero matrix gives
  * zeros; one with an infinity or a NaN gives NaN throughout, the others are not touched by it.
  * Products take fp16 operands scaled by 2^10 and sum in fp32; X is held in two fp16 parts (22 bits) and the
- * diagonal of b A + c A^2 in fp32.  Off the exact result by 1e-3 of its norm or so, below bf16's rounding
- * of it, for full and for low rank. */
+ * diagonal of b A + c A^2 in fp32.  Five steps of 3.4445, -4.7750, 2.0315 are off the exact result by 1e-3 of its norm
+ * or so, below bf16's rounding of it, for full and for low rank; eight by 2e-3, and what converges by less.  A step
+ * multiplies by a what rounding leaves outside the space of a G of low rank, in any arithmetic: with a^steps past
+ * 1e5 (ten steps of 3.4445; fp32 products are no better) the result for such a G is not near the exact one. */
 typedef struct {
     uint32_t abi_version; /* must equal WASTE_MOE_ABI_VERSION */
     int32_t count;        /* matrices, >= 0 */
@@ -109,7 +113,8 @@ int waste_ortho_workspace(const waste_ortho_config *cfg, size_t *bytes);
 
 /* out [count][rows][cols] of out_dtype from d_g of g_dtype:
  *   mode 0: out = scale X (out_dtype WASTE_ACT_BF16);
- *   mode 1: out += scale X (any type, one rounding: a weight and its update)
+ *   mode 1: out += scale X (any type, one rounding: a weight and its update).  fp32 weights too receive X as it is held:
+ *           off by 1e-3 of the update's norm or so, not by fp32's rounding
  * out may not be G. */
 int waste_ortho_update(const waste_ortho_config *cfg, const void *d_g, int32_t g_dtype, void *d_out, int32_t out_dtype,
                        float scale, int32_t mode, void *d_workspace, size_t workspace_bytes, waste_stream_t stream);

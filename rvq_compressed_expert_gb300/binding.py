@@ -399,7 +399,8 @@ def waste_rvq_encode(w, codebooks, codes, err, stream=None):
 
 
 def waste_dense_status():
-    """Raises WasteError (WASTE_ETIMEOUT) if a device wait of a dense operator gave up (synchronous)."""
+    """Raises WasteError if a device wait of a dense or training operator gave up (WASTE_ETIMEOUT), or if offsets of a product
+    grouped by expert fell or left the rows (WASTE_EINVAL), since the last call (synchronous)."""
     return _check(load().waste_dense_status())
 
 

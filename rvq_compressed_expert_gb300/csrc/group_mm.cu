@@ -16,8 +16,12 @@
 // experts 63 us (floor 52: W's 352 MB; 256 tiles of 96 x 16 on 152 SMs make two rounds, the second not full); 2048
 // rows over 384 experts 975 us = 7.1 TB/s of W; 32768 rows over 64 experts, back through down, 478 us cold and 531 to 550 in long
 // runs at 1.65 GHz (floor 379; cuBLAS takes 408 for one matrix of as many rows), their gradients 1130 to 1190 us (floor
-// 758; dx 500, the rest dW: 1.4 GB of it are written).  40 matrices of 1536 x 5120 from 128 rows each are written at
-// 4.6 TB/s (137 us): the epilogue's chain (neither more places on the way out nor fewer rows change it).
+// 758; dx 470, the rest dW).  dW is bound by its epilogue, not by memory or MMAs (8192 rows over 16 experts: DRAM 39 %,
+// tensor pipe 56 %, 142 us; dx, the same operations, 77 % and 112): a tile's sums go out in boxes of 32 rows x 64 bytes, one
+// behind another, 2.1 us for an SM's 128 x 256 values in bf16 however few rows they sum (64 matrices of 1536 x 7168 from 64,
+// 128 and 256 rows each: 312, 302, 361 us), which MMAs hide only where sums are long (512 rows 527 us, MMAs 379; 1024 832
+// and 758; 2048 1545 and 1516).  In fp32 3.5 us, added to bf16 3.7, added to fp32 7.8 (2.8 GB read and written: 5.9).
+// Added y (mode 1) goes out lane by lane: 1536 to 7168, 32768 rows 1038 us against 463.
 #include <type_traits>
 
 #include "tile_mma.cuh"

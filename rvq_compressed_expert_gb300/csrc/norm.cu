@@ -8,6 +8,9 @@
 //   backward_held_kernel   140 us = 5.0 TB/s (rows of 7167: 270 us; fp32 233 and 282, floor 209), with the partial sums of dw and db; reduce_kernel
 //                          adds those up: one row of them a CTA, 152 at most
 //   forward_kernel, dx_kernel, columns_kernel  rows past 8192 values: read two or three times, from L2 as far as it holds
+//                          (4096 x 16384 bf16: 82 us forward, 175 backward, floors 40 and 60; of 16391 values 205 and 499)
+// Short rows cost their steps: 65536 x 256 bf16 31 us forward and 47 backward, floors 10 and 15 (16384 x 1000: 23 and 35, 10
+// and 15).
 // What bounds the forward is the chain of steps of a row (wait, sum, squares, write) on the warps an SM holds; the backward's
 // lanes also hold the sums of their columns, so a row takes 14 of its 16 warps, and two rows are in work at once (of 16 bits;
 // of fp32, two in work leave too few on their way: 292 us against 233).

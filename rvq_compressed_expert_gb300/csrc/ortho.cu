@@ -11,9 +11,11 @@
 //
 // A step is three products: A = X X^T (its tiles on and below the diagonal, the long side in shares, partial sums added by
 // gram_kernel, or a tile at once where shares would cost more than they save), B from A^2, and X from B X, whose epilogue reads and writes both parts of X.  Small matrices do all steps in
-// one launch (the last step included, with both parts of X).  Measured: 1536 x 7168 bf16 382 to 391 us (floor 143 us of MMAs: 272 GFLOP; a step: A 20 us, its sum 6, B 14, X 27
-// to 32; G's norm and start 25), four 7168 x 1536 fp32 added to bf16 weights 1.20 to 1.25 ms (floor 571: a step's X 110 us,
-// of which the epilogue's 350 MB, past what L2 holds, cost 40), eight 128 x 256 33 us in one launch of 15 products.
+// one launch (the last step included, with both parts of X).  Measured: 1536 x 7168 bf16 382 to 391 us (floor 143 us of MMAs: 272 GFLOP; by launch, cold and one
+// by one, a step: A 21 us, its sum 10, B 14, X 30 to 35; G's norm and start 23), four 7168 x 1536 fp32 added to bf16 weights
+// 1.17 to 1.25 ms (floor 571: a step's A 62 us, its sum 14, B 27, X 102 to 130, whose floor is 70: its epilogue's 350 MB go past
+// what L2 holds; A is 168 items on 76 pairs, three waves, for a floor of 36; norm and start 87), eight 128 x 256 33 us in one
+// launch of 15 products.
 #include <type_traits>
 
 #include "tile_mma.cuh"

@@ -219,6 +219,22 @@ def test_norm_far_values():
     assert torch.isnan(z[rows]).all() and torch.equal(z[keep], y[keep])
 
 
+@pytest.mark.parametrize("T,d", [(5, 1024), (700, 1024), (700, 1001), (3, 16384)])
+def test_norm_squares_out_of_range(T, d):
+    """Squares about the mean past fp32's range: r is 0 and y is b, as the header says; other rows as ever."""
+    g = gen(8)
+    x = randn(g, T, d)
+    w, b = 1 + randn(g, d, scale=0.1), randn(g, d)
+    n = LayerNorm(w, b)
+    y, z, mean, rstd = torch.empty_like(x), torch.empty_like(x), torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    n.forward(x, y)
+    far = x.clone()
+    far[1] *= 1e25
+    n.forward(far, z, mean, rstd)
+    keep = torch.arange(T, device="cuda") != 1
+    assert torch.equal(z[1], b) and rstd[1] == 0 and mean[1].isfinite() and torch.equal(z[keep], y[keep])
+
+
 def test_norm_gradients_are_slopes():
     """Against central differences of the definition in fp64, along random directions."""
     T, d = 6, 40
