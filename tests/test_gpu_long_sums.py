@@ -6,6 +6,8 @@ import torch
 from rvq_compressed_expert_gb300 import binding as B
 from rvq_compressed_expert_gb300.dense import DenseExpert
 from rvq_compressed_expert_gb300.grouped import GroupedLinear
+from rvq_compressed_expert_gb300.ortho import NewtonSchulz
+from tests import train_ref as R
 
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
@@ -111,3 +113,28 @@ def test_grouped_gradient_behind_whole_pieces():
     for e in range(len(sizes)):
         in_e = at[(at >= ends[e]) & (at < ends[e + 1])] if sizes[e] == many else torch.arange(ends[e], ends[e + 1], device="cuda")
         assert torch.equal(dw[e].double(), dy[in_e].double().T @ x[in_e].double()), e
+
+
+@pytest.mark.parametrize("rows,cols", [(8, 1 << 28), (1 << 28, 8), (1, 1 << 24), (1 << 24, 1), (3, 5000), (5003, 1)])
+def test_orthogonalize_a_long_side(rows, cols):
+    """One value on each of the short side's rows, the first and the last place of the long side among them: the steps of one
+    number at the same places, zeros elsewhere."""
+    m, n = min(rows, cols), max(rows, cols)
+    g = gen(5)
+    at = places(g, n)
+    at = torch.cat([at[:1] * 0, at[torch.randperm(len(at) - 1, generator=g, device="cuda")[:m]], at[-1:]]).unique()
+    at = torch.cat([at[:m - 1], at[-1:]]) if m > 1 else at[-1:]
+    G = torch.zeros(1, rows, cols, dtype=BF, device="cuda")
+    sign = torch.where(torch.arange(m, device="cuda") % 2 == 0, 1.0, -1.0).to(BF)
+    i = torch.arange(m, device="cuda")
+    G[(0, i, at) if rows <= cols else (0, at, i)] = sign
+    out = NewtonSchulz(1, rows, cols).orthogonalize(G)
+    B.waste_dense_status()
+    small = torch.diag(sign.double())  # the same without the empty places
+    e = R.orthogonal(small)
+    got = out[0][(i, at) if rows <= cols else (at, i)].double()
+    s = float(e.abs().max())
+    # as for the shuffled places of a smaller matrix: the last rounding, one and a half times what the documented ones leave
+    bound = (R.half(BF) + 1.5 * R.dense_distance(R.orthogonal_rounded(small), e) + 1e-4) * s
+    assert (got - torch.diagonal(e)).abs().max() <= bound
+    assert int((out != 0).sum()) == m
