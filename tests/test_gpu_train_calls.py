@@ -503,3 +503,25 @@ def test_banked_stack_with_norms(tokens, lookahead):
             m.stats()
     finally:
         ts.close()
+
+
+def test_streams_at_once():
+    """Every operator on three streams at the same time, each with objects of its own: the bits of calls alone."""
+    calls = [Calls(*s) for s in (SHAPES[1], SHAPES[2], SHAPES[1])]
+    want = []
+    for i, c in enumerate(calls):
+        c.fill(i)
+        c.run()
+        want.append(c.kept())
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for c in calls:
+            for t in c.out.values():
+                t.fill_(3.0)
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for c, s in zip(calls, streams):
+                c.run(s)
+        torch.cuda.synchronize()
+        assert all(same(c.kept(), w) for c, w in zip(calls, want))
